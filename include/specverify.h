@@ -64,7 +64,9 @@ typedef enum {
   SV_ERR_OVERFLOW = 6     /* a candidate set outgrew its buffer (top-k ties)  */
 } sv_status;
 
-typedef enum { SV_BF16 = 0, SV_F32 = 1 } sv_dtype;
+/* SV_E4M3 (8-bit float, 4 exponent and 3 mantissa bits, largest value 448) is
+ * a type of paged caches only. */
+typedef enum { SV_BF16 = 0, SV_F32 = 1, SV_E4M3 = 2 } sv_dtype;
 
 /* Sampling settings applied identically to the target and the draft rows
  * ("Speculative decoding and MTP on Apple silicon", Facts: the draft and
@@ -226,6 +228,117 @@ SV_API sv_status verify_attn_noalloc(const void *q, const void *k_cache,
                                      int Hkv, int D, int64_t kv_len,
                                      int64_t kv_stride_tokens, float scale,
                                      sv_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* Rows, rotations and the paged cache                                      */
+/* ---------------------------------------------------------------------- */
+/* The rows of a layer's q/k/v projection become rotated queries and cache
+ * entries (qk_norm_rope, paged_kv_append), the cache of many sequences lives
+ * in pages that block tables name (paged_attn reads it for the newest rows of
+ * each sequence), and whole prompts attend to themselves (window_attn).  (The
+ * pages this library follows take rotated queries and a filled cache as
+ * given; these calls are what stands before and around verify_attn.) */
+
+/* Rows [token][head][D], D contiguous: strides in elements, non-negative
+ * multiples of 8; ptr device, 16-byte aligned (bf16). */
+typedef struct {
+  void *ptr;
+  int64_t token_stride, head_stride;
+} sv_rows;
+
+/* RMS norm of each head's row: x * rsqrt(mean(x^2) + eps) * (w + weight_offset).
+ * q_weight, k_weight: device bf16 [D], 16-byte aligned; NULL: rows of that
+ * kind are not normed.  eps >= 0. */
+typedef struct {
+  const void *q_weight, *k_weight;
+  float eps, weight_offset;
+} sv_head_norm;
+
+/* Position rotation of the first rot_dim elements of a row: pair p turns by
+ * positions[token] * inv_freq[p]; pairs are (p, p + rot_dim/2), or
+ * (2p, 2p+1) if interleaved.  phases: device uint64 [rot_dim/2], 8-byte
+ * aligned, from rope_phases; NULL: no rotation.  positions: device int32
+ * [T].  rot_dim % 8 == 0, 8 <= rot_dim <= D. */
+typedef struct {
+  const uint64_t *phases;
+  const int32_t *positions;
+  int32_t rot_dim, interleaved;
+} sv_rotation;
+
+/* phases_out[i] (host) = inv_freq[i] / (2 pi) turns per position as a fraction
+ * of 2^64, so that positions times it wraps at whole turns exactly: a
+ * rotation at position 2^31 is off by less than 2^-20 turns, the error of
+ * inv_freq's own 53 bits.  inv_freq: host [n], finite.  Host code only. */
+SV_API sv_status rope_phases(const double *inv_freq, int n, uint64_t *phases_out);
+
+/* Norm and rotation of every query and key row of T tokens in one pass
+ * (arithmetic fp32, one rounding to bf16 at the end).  q_out, k_out may be q,
+ * k themselves (same pointer and strides); other overlaps are undefined.  Rows
+ * of k_out with head_stride = kv_stride_tokens*D and token_stride = D write
+ * straight into a verify_attn cache.
+ * Supported: D in {64, 128, 256}; 0 <= T, T*(Hq+Hkv) < 2^31; Hq, Hkv <= 4096. */
+SV_API sv_status qk_norm_rope(const sv_rows *q, const sv_rows *k, const sv_rows *q_out,
+                              const sv_rows *k_out, const sv_head_norm *norm,
+                              const sv_rotation *rot, int T, int Hq, int Hkv, int D,
+                              sv_stream_t stream);
+
+/* A cache in pages of page_size slots: head h of slot s of page p starts at
+ * element p*page_stride + s*slot_stride + h*head_stride of k and of v (any
+ * order of the three; D contiguous).  dtype SV_BF16, or SV_E4M3: the stored
+ * value times k_scale[h] (v_scale[h]) is the key (value); scales: device fp32
+ * [Hkv], > 0, NULL for 1 (and NULL at bf16).  k, v: device, 16-byte aligned;
+ * strides positive multiples of 16 bytes.  page_size a multiple of 16, at
+ * most 2^16; 1 <= num_pages < 2^31. */
+typedef struct {
+  void *k, *v;
+  const float *k_scale, *v_scale;
+  int64_t page_stride, slot_stride, head_stride;
+  int64_t num_pages;
+  int32_t page_size, dtype;
+} sv_paged_kv;
+
+/* Writes T tokens' keys (normed and rotated on the way, as asked) and values
+ * into the cache, and their queries (normed and rotated) to q_out in the same
+ * launch when q is not NULL.  slots: device int64 [T]: token t goes to slot
+ * slots[t] % page_size of page slots[t] / page_size; a negative slot: that
+ * token's keys and values are not written.  A slot past the last page is not
+ * written and reported by sv_last_device_error() as SV_ERR_INVALID_ARG.  Two
+ * tokens of one call with the same slot: either may remain.  e4m3 rounds to
+ * nearest and saturates at 448 (NaN stays NaN).
+ * norm, rot: NULL for none.  Limits as qk_norm_rope, with T*(Hq+2*Hkv) < 2^31
+ * (Hq counted if q is given); e4m3 needs D in {128, 256}. */
+SV_API sv_status paged_kv_append(const sv_rows *q, const sv_rows *q_out, const sv_rows *k,
+                                 const sv_rows *v, const sv_paged_kv *cache, const int64_t *slots,
+                                 const sv_head_norm *norm, const sv_rotation *rot, int T, int Hq,
+                                 int Hkv, int D, sv_stream_t stream);
+
+/* Attention of the newest M rows of each of B sequences over a paged cache
+ * that already holds them (M = 1: one new token; M = K+1: the verify rows).
+ * Row i of sequence b is q row b*M + i, stands at position
+ * p = kv_lens[b] - M + i and sees position j >= 0 iff j <= p and (window == 0,
+ * or j > p - window, or j < sinks):
+ *   o = softmax_j(scale * <q, k_j>) . v_j, zeros for a row that sees nothing
+ * (kv_lens[b] == 0, or rows before position 0 where kv_lens[b] < M).
+ * block_table: device int32 [B] rows of table_width page indexes,
+ *   table_stride elements apart: position j of sequence b is slot
+ *   j % page_size of page block_table[b][j / page_size].  Entries of pages
+ *   without a slot that some row sees are not read.
+ * kv_lens: device int32 [B].  A length outside 0..table_width*page_size (it
+ *   counts as the nearest of them), and a needed page outside the cache (it
+ *   counts as zeros), are reported by sv_last_device_error() as
+ *   SV_ERR_INVALID_ARG.
+ * Slots that no row of the sequence sees may hold anything, NaN included;
+ * those that some row sees hold finite values.
+ * Supported: D in {128, 256}; Hq % Hkv == 0; M*(Hq/Hkv) <= 128; 0 <= B <= 4096;
+ *   table_width*page_size <= 2^30, B times that <= 2^35; scale > 0 and finite.
+ * Two launches; lengths and tables are read on the device, so a captured call
+ * follows their contents. */
+SV_API size_t paged_attn_workspace_bytes(int B, int M, int Hq, int Hkv, int D);
+SV_API sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const int32_t *block_table,
+                            int64_t table_stride, int table_width, const int32_t *kv_lens,
+                            const sv_rows *o, int B, int M, int Hq, int Hkv, int D, float scale,
+                            int window, int sinks, void *workspace, size_t ws_bytes,
+                            sv_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* Exact acceptance                                                         */

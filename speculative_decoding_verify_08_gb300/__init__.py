@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -32,11 +33,13 @@ __all__ = [
     "sv_status_string", "sv_last_device_error", "sv_set_launch_flags", "sv_get_launch_flags",
     "sv_kernel_launch_count", "prepack", "workspace", "library_path", "spec_pick_depth",
     "gdn_verify",
+    "SV_E4M3", "rope_phases", "qk_norm_rope", "PagedKV", "paged_kv_append",
+    "paged_attn_workspace_bytes", "paged_attn",
 ]
 
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_CUDA = 0, 1, 2, 3
 SV_ERR_TIMEOUT, SV_ERR_WORKSPACE, SV_ERR_OVERFLOW = 4, 5, 6
-SV_BF16, SV_F32 = 0, 1
+SV_BF16, SV_F32, SV_E4M3 = 0, 1, 2
 SV_LAUNCH_PDL = 1
 SV_LAUNCH_QMM_CUDA_CORES = 2  # measurement aid: qmm on CUDA-core FFMA at M = 1 and 4
 SV_LAUNCH_ATTN_MMA_SYNC = 4  # verify_attn on the mma.sync kernel
@@ -103,6 +106,11 @@ def load():
             "sv_kernel_launch_count": (ctypes.c_uint64, []),
             "spec_pick_depth": (I, [P, P, P, I, P]),
             "gdn_verify": (I, [P, P, P, P, P, I, P, P, P, P, P, P, I, I, I, I, I, I, P]),
+            "rope_phases": (I, [P, I, P]),
+            "qk_norm_rope": (I, [P, P, P, P, P, P, I, I, I, I, P]),
+            "paged_kv_append": (I, [P, P, P, P, P, P, P, P, I, I, I, I, P]),
+            "paged_attn_workspace_bytes": (Z, [I, I, I, I, I]),
+            "paged_attn": (I, [P, P, P, L, I, P, P, I, I, I, I, I, ctypes.c_float, I, I, P, Z, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -341,3 +349,148 @@ def gdn_verify(state, q, k, v, g, beta, o, tape=None, n_replay=0, stream=None):
                              _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(o), odt, M, Hk, Hv,
                              dk, dv, _stream(stream)),
            "gdn_verify")
+
+
+# --------------------------------------------- rows, rotations, paged cache ----
+# C structs passed by address, packed per call: a pack() is a fraction of a
+# microsecond, where filling a ctypes.Structure takes several.
+_ROWS = struct.Struct("Pqq")            # sv_rows
+_NORM = struct.Struct("PPff")           # sv_head_norm
+_ROTATION = struct.Struct("PPii")       # sv_rotation
+_PAGED_KV = struct.Struct("PPPPqqqqii")  # sv_paged_kv
+
+
+def _bad(where: str, status: int = SV_ERR_INVALID_ARG):
+    raise SvError(status, where)
+
+
+def _rows(t, tokens, heads, D, where):
+    """sv_rows of a CUDA bf16 tensor [tokens, heads, D] (any strides, D contiguous)."""
+    ts, hs, ds = t.stride()
+    if t.dtype is not torch.bfloat16 or t.shape != (tokens, heads, D) or ds != 1 or not t.is_cuda:
+        _bad(where)
+    # a dimension of one may carry any stride
+    return _ROWS.pack(t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0)
+
+
+def _vector(t, dtype, n, where):
+    """Address of a contiguous CUDA tensor [n]."""
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
+        _bad(where)
+    return t.data_ptr()
+
+
+def _launch_stream(t, stream):
+    """The given stream, or the current one of the tensor's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream(stream)
+
+
+def rope_phases(inv_freq, device=None):
+    """Device table of a rotation (int64 [rot_dim/2], the bits of fractions of
+    a turn in 2^-64) from its inverse frequencies in radians per position."""
+    import numpy as np
+    if isinstance(inv_freq, torch.Tensor):
+        inv_freq = inv_freq.detach().cpu().double().numpy()
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64).ravel()
+    out = np.empty(f.shape[0], dtype=np.uint64)
+    _check(load().rope_phases(f.ctypes.data, f.shape[0], out.ctypes.data), "rope_phases")
+    return torch.from_numpy(out.view(np.int64)).to(device if device is not None else torch.device("cuda"))
+
+
+def _norm_rotation(q_weight, k_weight, eps, weight_offset, positions, phases, interleaved, T, D, where):
+    norm = rot = None
+    if q_weight is not None or k_weight is not None:
+        norm = _NORM.pack(0 if q_weight is None else _vector(q_weight, torch.bfloat16, D, where),
+                          0 if k_weight is None else _vector(k_weight, torch.bfloat16, D, where),
+                          eps, weight_offset)
+    if phases is not None:
+        if positions is None:
+            _bad(where)
+        rot = _ROTATION.pack(_vector(phases, torch.int64, phases.numel(), where),
+                             _vector(positions, torch.int32, T, where),
+                             2 * phases.numel(), 1 if interleaved else 0)
+    return norm, rot
+
+
+def qk_norm_rope(q, k, q_out, k_out, positions=None, phases=None, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, weight_offset: float = 0.0, interleaved: bool = False, stream=None):
+    """RMS norm (where a weight is given) and position rotation (where phases
+    are) of query and key rows [T, heads, D] in one pass; q_out and k_out may
+    be q and k themselves.  rot_dim = 2 * phases.numel()."""
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    w = "qk_norm_rope"
+    norm, rot = _norm_rotation(q_weight, k_weight, eps, weight_offset, positions, phases, interleaved, T, D, w)
+    _check(load().qk_norm_rope(_rows(q, T, Hq, D, w), _rows(k, T, Hkv, D, w), _rows(q_out, T, Hq, D, w),
+                               _rows(k_out, T, Hkv, D, w), norm, rot, T, Hq, Hkv, D,
+                               _launch_stream(q, stream)), w)
+
+
+class PagedKV:
+    """A paged cache: k and v are CUDA tensors of one shape and one set of
+    strides, [pages, slots, heads, D] ("NHD") or [pages, heads, slots, D]
+    ("HND"), bf16 or float8_e4m3fn; with the latter, the stored value times
+    k_scale[head] (v_scale[head], fp32 [heads], None for 1) counts."""
+
+    def __init__(self, k, v, layout: str = "NHD", k_scale=None, v_scale=None):
+        w = "PagedKV"
+        if layout not in ("NHD", "HND") or k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+            _bad(w)
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype is not k.dtype:
+            _bad(w)
+        if not k.is_cuda or v.get_device() != k.get_device() or k.stride(3) != 1:
+            _bad(w)
+        slot, head = (1, 2) if layout == "NHD" else (2, 1)
+        self.k, self.v, self.k_scale, self.v_scale, self.layout = k, v, k_scale, v_scale, layout
+        self.page_size, self.heads, self.D = k.shape[slot], k.shape[head], k.shape[3]
+        self.packed = _PAGED_KV.pack(
+            k.data_ptr(), v.data_ptr(),
+            0 if k_scale is None else _vector(k_scale, torch.float32, self.heads, w),
+            0 if v_scale is None else _vector(v_scale, torch.float32, self.heads, w),
+            k.stride(0), k.stride(slot), k.stride(head), k.shape[0], self.page_size,
+            SV_BF16 if k.dtype is torch.bfloat16 else SV_E4M3)
+
+
+def paged_kv_append(k, v, cache: PagedKV, slots, q=None, q_out=None, positions=None, phases=None,
+                    q_weight=None, k_weight=None, eps: float = 1e-6, weight_offset: float = 0.0,
+                    interleaved: bool = False, stream=None):
+    """Write the keys [T, heads, D] (normed and rotated as in qk_norm_rope) and
+    values of T tokens to slots int64 [T] of the cache (negative: skipped),
+    and in the same launch the queries' rows to q_out when q is given."""
+    T, Hkv, D = k.shape
+    w = "paged_kv_append"
+    if Hkv != cache.heads or D != cache.D or (q is None) != (q_out is None):
+        _bad(w)
+    Hq = 0 if q is None else q.shape[1]
+    norm, rot = _norm_rotation(q_weight if q is not None else None, k_weight, eps, weight_offset, positions,
+                               phases, interleaved, T, D, w)
+    _check(load().paged_kv_append(None if q is None else _rows(q, T, Hq, D, w),
+                                  None if q is None else _rows(q_out, T, Hq, D, w), _rows(k, T, Hkv, D, w),
+                                  _rows(v, T, Hkv, D, w), cache.packed, _vector(slots, torch.int64, T, w), norm,
+                                  rot, T, Hq, Hkv, D, _launch_stream(k, stream)), w)
+
+
+def paged_attn_workspace_bytes(B: int, M: int, Hq: int, Hkv: int, D: int) -> int:
+    return load().paged_attn_workspace_bytes(B, M, Hq, Hkv, D)
+
+
+def paged_attn(q, cache: PagedKV, block_table, kv_lens, o, M: int, scale: float, window: int = 0,
+               sinks: int = 0, workspace=None, stream=None):
+    """Attention of the newest M rows of each sequence over the cache: q and o
+    [B*M, Hq, D], block_table int32 [B, width], kv_lens int32 [B]; window 0:
+    none; sinks: first positions that stay visible under a window."""
+    rows, Hq, D = q.shape
+    w = "paged_attn"
+    B = kv_lens.shape[0]
+    if (D != cache.D or rows != B * M or block_table.dtype is not torch.int32 or block_table.dim() != 2
+            or block_table.shape[0] != B or not block_table.is_cuda):
+        _bad(w)
+    ts, es = block_table.stride()
+    if es != 1 and block_table.shape[1] != 1:
+        _bad(w)
+    _check(load().paged_attn(_rows(q, rows, Hq, D, w), cache.packed, block_table.data_ptr(), ts,
+                             block_table.shape[1], _vector(kv_lens, torch.int32, B, w),
+                             _rows(o, rows, Hq, D, w), B, M, Hq, cache.heads, D, scale, window, sinks,
+                             _ptr(workspace), _nbytes(workspace), _launch_stream(q, stream)), w)

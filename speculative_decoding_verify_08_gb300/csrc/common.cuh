@@ -24,6 +24,7 @@ namespace sv {
 constexpr unsigned ERR_TIMEOUT = 1u;
 constexpr unsigned ERR_OVERFLOW = 2u;
 constexpr unsigned ERR_LISTS = 4u;  // candidate lists made for other rows or a smaller top-k
+constexpr unsigned ERR_INDEX = 8u;  // a slot, page, length or offset in device memory out of range
 
 // A bounded wait gives up after this many SM clock cycles (~1-2 s).
 constexpr long long WAIT_LIMIT_CYCLES = 3000000000LL;
@@ -49,9 +50,12 @@ inline sv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV
 // memory limit to `smem` first, whatever its size: the default limit covers
 // static and dynamic shared memory together, so a kernel with static arrays
 // can exceed it with less than 48 KB of dynamic memory.
+// `after_own`: the kernel follows another of this library's in the same call
+// and waits for it with griddepcontrol.wait, so it may always be launched
+// while that one drains.
 template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                   cudaStream_t stream, Args &&...args) {
+cudaError_t launch_after(bool after_own, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t stream, Args &&...args) {
   if (smem > 0) {
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess) return e;
@@ -63,7 +67,7 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   cfg.numAttrs = 0;
-  if (launch_flags() & SV_LAUNCH_PDL) {
+  if (after_own || (launch_flags() & SV_LAUNCH_PDL)) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
@@ -72,6 +76,12 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
   if (e == cudaSuccess) count_launch();
   return e;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                   cudaStream_t stream, Args &&...args) {
+  return launch_after(false, kern, grid, block, smem, stream, std::forward<Args>(args)...);
 }
 
 // The same launch with thread-block clusters of `cl` CTAs along x (cl >= 2;
@@ -275,6 +285,16 @@ __device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *m
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(smem_dst)),
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// 5-D tiled tensor copy global -> shared.
+__device__ __forceinline__ void tma_load_5d(void *smem_dst, const CUtensorMap *map, int c0, int c1,
+                                            int c2, int c3, int c4, uint64_t *bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(smem_dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
 

@@ -1,0 +1,800 @@
+// paged_attn.cu -- attention of the newest M rows of each of B sequences over
+// a paged cache (M = 1: one new token), with an optional sliding window and a
+// few first tokens that stay visible.
+//
+// Row i of sequence b stands at position p = len_b - M + i and sees position
+// j iff j <= p and (no window, or j > p - window, or j < sinks):
+//   O = softmax_j(scale <Q, K_j>) V,   zeros where nothing is seen.
+//
+// What bounds it: every visible slot of K and V is read once and meets
+// M*Hq/Hkv query rows, so HBM (and, for short sequences, latency).  Hence:
+//  * The work of a call is a line of units, one unit a 16-slot chunk of one
+//    (sequence, KV head); only chunks that some row sees are on it.  Every
+//    CTA (one per SM) finds the line's length from the device's lengths and
+//    takes an equal, contiguous piece, so ragged batches and long single
+//    sequences load all SMs alike and the host needs no lengths.
+//  * One producer warp streams chunks into a shared-memory ring by TMA, one
+//    5-D copy for K and one for V (page, head, 64-column group, slot, column),
+//    looking pages up 32 chunks ahead.  A chunk never crosses a page.
+//  * Each of eight consumer warps takes every (8/MT)-th chunk for one 16-row
+//    tile of query rows and keeps its own running maximum, sum and O in
+//    registers: the scores' accumulator layout is the next product's operand
+//    layout, so nothing but the ring is shared and no barrier stands in the
+//    loop.  The warps' results are joined once per (sequence, head).
+//  * A piece that does not hold all of its (sequence, head) leaves its O,
+//    maximum and sum in the workspace; a second kernel joins them.
+//  * The maximum is raised only when a chunk exceeds it by more than 2^8
+//    (probabilities up to 256 against the old maximum are exact in the same
+//    sense), so the accumulators are rarely rescaled.
+// Probabilities are rounded to the operand type of the second product (bf16;
+// fp16 beside an e4m3 cache): relative 2^-8 or less each, averaging out over
+// the slots, below the output's own rounding.
+// An e4m3 cache is converted in registers to fp16, which holds every e4m3
+// value exactly; the queries are scaled by a power of two per row to fit fp16.
+#include "paged.cuh"
+
+namespace sv {
+namespace attn {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // attn.cu
+}
+namespace paged {
+
+constexpr int CHUNK = 16;  // slots per unit
+constexpr int NCW = 8;     // consumer warps
+constexpr int THREADS = (NCW + 1) * 32;
+constexpr int MAX_B = 4096;
+constexpr int MAX_R = 128;           // query rows per KV head: eight 16-row tiles
+constexpr int MAX_STAGES = 24;
+constexpr float RESCALE = 8.f;       // log2 of the largest probability against an old maximum
+constexpr size_t SMEM_LIMIT = 227 * 1024;
+
+struct Params {
+  sv_rows q, o;
+  const int *table;
+  long long table_stride;
+  int width;  // pages per table row
+  const int *lens;
+  const float *ks, *vs;
+  float *opart;  // [2 * ctas][R][D] unnormalised O
+  float *ml;     // [2 * ctas][R][2] maximum (log2 domain) and sum
+  int4 *desc;    // [ctas] split heads: (b * Hkv + h, first CTA, CTAs, -)
+  unsigned *err;
+  int B, M, Hkv, G, R;
+  float sl2e;  // scale * log2(e)
+  int window, sinks;
+  int page_size, num_pages;
+  int stages;
+  int min_units;  // least units per CTA
+  int by_head;    // desc is indexed by b * Hkv + h (else by CTA)
+};
+
+// Chunks of one sequence that some row sees: the first `ns` chunks, then
+// chunks w0..ce-1.
+struct Span {
+  int L, ns, w0, ce;
+  __device__ __forceinline__ int count() const { return ns + ce - w0; }
+  __device__ __forceinline__ int chunk(int k) const { return k < ns ? k : k - ns + w0; }
+};
+
+__device__ __forceinline__ int first_seen(const Params &P, int L) {
+  return P.window > 0 ? imax(0, L - P.M - P.window + 1) : 0;
+}
+
+__device__ __forceinline__ Span span_of(const Params &P, int L) {
+  Span s;
+  s.L = L;
+  s.ce = (L + CHUNK - 1) / CHUNK;
+  s.w0 = first_seen(P, L) / CHUNK;
+  s.ns = (imin(P.sinks, L) + CHUNK - 1) / CHUNK;
+  if (s.w0 <= s.ns) s.w0 = s.ns = 0;
+  return s;
+}
+
+__device__ __forceinline__ int length_of(const Params &P, int b) {
+  const long long cap = (long long)P.width * P.page_size;
+  const int l = P.lens[b];
+  if (l < 0 || l > cap) {
+    if (blockIdx.x == 0) atomicOr(P.err, ERR_INDEX);
+    return l < 0 ? 0 : (int)cap;
+  }
+  return l;
+}
+
+// Byte offset of 16-byte group c in row r of a 16-row tile stored as
+// 128-byte-wide swizzled boxes.
+__device__ __forceinline__ uint32_t swz16(int r, int c) {
+  return (uint32_t)((c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {  // low 16 bits
+  uint32_t d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}\n" : "=r"(d) : "r"(v));
+  return d;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2_hi(uint32_t v) {  // high 16 bits
+  uint32_t d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}\n" : "=r"(d) : "r"(v));
+  return d;
+}
+
+template <bool F8>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F8)
+    mma_f16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+  else
+    mma_bf16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+}
+
+template <int D, bool F8, int MT>
+struct Layout {
+  static constexpr int TILE = CHUNK * D * (F8 ? 1 : 2);  // bytes of a chunk of K (or V)
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int QS = 1024;                         // after the barriers
+  static constexpr int QBYTES = MT * 16 * D * 2;
+  static constexpr int RS = D + 8;                        // scratch row stride, floats
+  static constexpr int SCRATCH = QS + QBYTES;
+  static constexpr int SBYTES = NCW * 8 * RS * 4;
+  static constexpr int ML = SCRATCH + SBYTES;             // [NCW][16][2] floats
+  static constexpr int FIN = ML + NCW * 16 * 8;           // [MT*16][2] floats
+  static constexpr int QSC = FIN + MT * 16 * 8;           // [MT*16] floats
+  static constexpr int RING = (QSC + MT * 16 * 4 + 1023) / 1024 * 1024;
+  // the prefix sums (B + 1 ints) follow the ring
+};
+
+template <int D, bool F8, int MT>
+__global__ void __launch_bounds__(THREADS, 1)
+    paged_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                 const Params P) {
+  using LY = Layout<D, F8, MT>;
+  constexpr int NL = NCW / MT;  // chunks in flight among the consumer warps
+  constexpr int NKS = D / 16;
+  constexpr int NT = D / 8;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem);
+  uint64_t *empty = full + MAX_STAGES;
+  int *wsum = reinterpret_cast<int *>(smem + 512);  // scan: warp totals
+  uint8_t *qs = smem + LY::QS;
+  float *scratch = reinterpret_cast<float *>(smem + LY::SCRATCH);
+  float *sml = reinterpret_cast<float *>(smem + LY::ML);
+  float *fin = reinterpret_cast<float *>(smem + LY::FIN);
+  float *qsc = reinterpret_cast<float *>(smem + LY::QSC);
+  uint8_t *ring = smem + LY::RING;
+  const int NST = P.stages;
+  int *pre = reinterpret_cast<int *>(ring + NST * LY::STAGE);  // pre[b]: chunks before sequence b
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], MT);
+    }
+    fence_barrier_init();
+  }
+  pdl_wait();
+
+  // ---- the line of units: prefix sums of the sequences' chunk counts ----
+  int total = 0;
+  for (int b0 = 0; b0 < P.B; b0 += THREADS) {
+    const int b = b0 + tid;
+    const int n = b < P.B ? span_of(P, length_of(P, b)).count() : 0;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w <= NCW; ++w) {
+      if (w < warp) before += wsum[w];
+      all += wsum[w];
+    }
+    if (b < P.B) pre[b] = total + before + x - n;
+    total += all;
+    __syncthreads();
+  }
+  if (tid == 0) pre[P.B] = total;
+  __syncthreads();
+
+  const long long units = (long long)total * P.Hkv;
+  const int ctas = gridDim.x;
+  long long per = (units + ctas - 1) / ctas;
+  if (per < P.min_units) per = P.min_units;
+  const long long u0 = lmin(units, per * blockIdx.x), u1 = lmin(units, u0 + per);
+
+  // sequence of unit u < units
+  auto seq_of = [&](long long u) {
+    const int c = (int)(u / P.Hkv);  // chunk-line position rounded down: same sequence as u
+    int lo = 0, hi = P.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= c) lo = mid; else hi = mid - 1;
+    }
+    return lo;  // the last sequence that starts at or before c, so it is not empty
+  };
+
+  if (warp == NCW) {
+    // ------------------------------------------------------- producer --
+    const uint64_t pol = l2_evict_first_policy();
+    const int cpp = P.page_size / CHUNK;
+    bool ok = true;
+    uint32_t q = 0;
+    int b = u0 < u1 ? seq_of(u0) : 0;
+    for (long long u = u0; u < u1 && ok;) {
+      while (pre[b + 1] == pre[b]) ++b;  // (a unit follows: a non-empty sequence exists)
+      const int n = pre[b + 1] - pre[b];
+      const long long in = u - (long long)pre[b] * P.Hkv;
+      const int h = (int)(in / n), ka = (int)(in - (long long)h * n);
+      const int kb = (int)lmin(n, ka + (u1 - u));
+      const Span s = span_of(P, length_of(P, b));
+      const int *row = P.table + (long long)b * P.table_stride;
+      auto page_at = [&](int k) {
+        if (k >= kb) return 0;
+        const int pg = row[s.chunk(k) / cpp];
+        if ((unsigned)pg >= (unsigned)P.num_pages) atomicOr(P.err, ERR_INDEX);
+        return pg;
+      };
+      int next = page_at(ka + lane);
+      for (int k0 = ka; k0 < kb && ok; k0 += 32) {
+        const int cur = next;
+        next = page_at(k0 + 32 + lane);
+        const int m = imin(32, kb - k0);
+        for (int i = 0; i < m; ++i, ++q) {
+          const int page = __shfl_sync(0xffffffffu, cur, i);
+          const int slot = (int)(q % (uint32_t)NST);
+          if (lane == 0) {
+            ok = mbar_wait(&empty[slot], ((q / (uint32_t)NST) & 1) ^ 1, P.err);
+            if (ok) {
+              const int c = s.chunk(k0 + i);
+              uint8_t *dst = ring + slot * LY::STAGE;
+              mbar_arrive_expect_tx(&full[slot], LY::STAGE);
+              // a page out of range reads zeros (the copy is clipped to the cache)
+              tma_load_5d(dst, &mapK, 0, (c % cpp) * CHUNK, 0, h, page, &full[slot], pol);
+              tma_load_5d(dst + LY::TILE, &mapV, 0, (c % cpp) * CHUNK, 0, h, page, &full[slot], pol);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+        }
+      }
+      u += kb - ka;
+      if (h == P.Hkv - 1 && kb == n) ++b;
+    }
+    if (!ok && lane == 0) {  // a wait ran out: no copy may outlive the CTA
+      const uint32_t first = q > (uint32_t)NST ? q - NST : 0u;
+      for (uint32_t qq = first; qq < q; ++qq) mbar_wait(&full[qq % NST], (qq / NST) & 1, P.err);
+    }
+    return;
+  }
+
+  // --------------------------------------------------------- consumers --
+  const int mt = warp % MT, cl = warp / MT;  // query tile; which of every NL chunks
+  const int gq = lane >> 2, tq = lane & 3;
+  const int row0 = 16 * mt + gq, row1 = row0 + 8;
+  const int i0 = row0 / P.G, i1 = row1 / P.G;
+  bool ok = true;
+  uint32_t q0 = 0;  // chunks before this segment
+
+  // outputs and descriptors of empty sequences, shared over the CTAs
+  for (int b = blockIdx.x; b < P.B; b += ctas) {
+    if (pre[b + 1] != pre[b]) continue;
+    const int rows = P.M * P.Hkv * P.G;
+    for (int x = tid; x < rows * (D / 8); x += NCW * 32) {
+      const int r = x / (D / 8), c = x % (D / 8);
+      const int i = r / (P.Hkv * P.G), hq = r % (P.Hkv * P.G);
+      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(P.o.ptr) +
+                                 ((long long)b * P.M + i) * P.o.token_stride + hq * P.o.head_stride + 8 * c) =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (P.by_head)
+      for (int h = tid; h < P.Hkv; h += NCW * 32) P.desc[b * P.Hkv + h] = make_int4(0, 0, 0, 0);
+  }
+  if (!P.by_head && tid == 0) P.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+
+  int b = u0 < u1 ? seq_of(u0) : 0;
+  for (long long u = u0; u < u1;) {
+    while (pre[b + 1] == pre[b]) ++b;
+    const int n = pre[b + 1] - pre[b];
+    const long long head0 = (long long)pre[b] * P.Hkv;
+    const int h = (int)((u - head0) / n), ka = (int)(u - head0 - (long long)h * n);
+    const int kb = (int)lmin(n, ka + (u1 - u));
+    const Span s = span_of(P, length_of(P, b));
+    const int L = s.L, p0 = L - P.M;  // position of row 0
+    const int lo = first_seen(P, L);
+
+    // ---- query rows of this head: r = i*G + j, 128-byte swizzled ----
+    for (int x = tid; x < MT * 16 * (D / 8); x += NCW * 32) {
+      const int r = x / (D / 8), c = x % (D / 8);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (r < P.R) {
+        const int i = r / P.G, j = r % P.G;
+        v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q.ptr) +
+                                             ((long long)b * P.M + i) * P.q.token_stride +
+                                             (long long)(h * P.G + j) * P.q.head_stride + 8 * c);
+      }
+      uint8_t *tile = qs + (r >> 4) * 16 * D * 2;
+      const int rr = r & 15;
+      if (!F8) {
+        *reinterpret_cast<uint4 *>(tile + swz16(rr, c)) = v;
+      } else {
+        // fp16 rows scaled so that the largest element is in [1, 2); within 16
+        // elements, 4t..4t+3 go where an e4m3 word's elements meet them
+        float f[8] = {bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y),
+                      bf16lo(v.z), bf16hi(v.z), bf16lo(v.w), bf16hi(v.w)};
+        float mx = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(f[e]));
+#pragma unroll
+        for (int o = D / 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        int ex = (int)(__float_as_uint(mx) >> 23) - 127;
+        if (ex < -126 || ex > 126) ex = ex < 0 ? (mx > 0.f ? -126 : 0) : (ex > 127 ? 0 : 126);
+        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+        if (c == 0) qsc[r] = __uint_as_float((uint32_t)(127 + ex) << 23);
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(f[2 * e] * down, f[2 * e + 1] * down);
+        // chunk c holds elements 8(c&1).. of its group of 16: t = 2(c&1), 2(c&1)+1
+        const int g16 = c & ~1, t = 2 * (c & 1);
+        uint32_t *lo16 = reinterpret_cast<uint32_t *>(tile + swz16(rr, g16));
+        uint32_t *hi16 = reinterpret_cast<uint32_t *>(tile + swz16(rr, g16 + 1));
+        lo16[t] = w[0], hi16[t] = w[1], lo16[t + 1] = w[2], hi16[t + 1] = w[3];
+      }
+    }
+    named_barrier(1, NCW * 32);
+
+    constexpr bool QREG = D == 128;  // D = 256: O alone takes 128 registers
+    constexpr int NQR = QREG ? NKS : 1;
+    uint32_t qa[NQR][4];
+    const uint32_t qtile = smem_u32(qs + mt * 16 * D * 2);
+    const int qr = (lane & 7) + 8 * ((lane >> 3) & 1);
+    if (QREG) {
+#pragma unroll
+      for (int ks = 0; ks < NQR; ++ks) ldmatrix_x4(qa[ks], qtile + swz16(qr, 2 * ks + (lane >> 4)));
+    }
+    float sc0 = P.sl2e, sc1 = P.sl2e;
+    if (F8) {
+      const float kscale = P.ks ? P.ks[h] : 1.f;
+      sc0 *= kscale * qsc[row0];
+      sc1 *= kscale * qsc[row1];
+    }
+
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float o[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[nt][j] = 0.f;
+
+    const uint32_t q1 = q0 + (uint32_t)(kb - ka);
+    // this warp's first chunk: the least q >= q0 with q % NL == cl
+    for (uint32_t q = q0 + (uint32_t)((cl - (int)(q0 % NL) + NL) % NL); q < q1; q += NL) {
+      const int slot = (int)(q % (uint32_t)NST);
+      if (ok) ok = mbar_wait(&full[slot], (q / (uint32_t)NST) & 1, P.err);
+      if (!ok) continue;
+      const uint32_t kt = smem_u32(ring + slot * LY::STAGE), vt = kt + LY::TILE;
+      // ---- S = Q K^T, 16 rows x 16 slots ----
+      float sa[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sa[nt][j] = 0.f;
+      if (!F8) {
+#pragma unroll
+        for (int ks = 0; ks < NKS; ++ks) {
+          uint32_t kf[4], qf[4];
+          ldmatrix_x4(kf, kt + swz16(8 * (lane >> 4) + (lane & 7), 2 * ks + ((lane >> 3) & 1)));
+          if (QREG) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) qf[t] = qa[QREG ? ks : 0][t];
+          } else {
+            ldmatrix_x4(qf, qtile + swz16(qr, 2 * ks + (lane >> 4)));
+          }
+          mma16<F8>(sa[0], qf, kf[0], kf[1]);
+          mma16<F8>(sa[1], qf, kf[2], kf[3]);
+        }
+      } else {
+#pragma unroll
+        for (int kp = 0; kp < NKS / 2; ++kp) {
+          uint32_t kf[4];
+          ldmatrix_x4(kf, kt + swz16(8 * (lane >> 4) + (lane & 7), 2 * kp + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t qf[4];
+            if (QREG) {
+#pragma unroll
+              for (int t = 0; t < 4; ++t) qf[t] = qa[QREG ? 2 * kp + e : 0][t];
+            } else {
+              ldmatrix_x4(qf, qtile + swz16(qr, 2 * (2 * kp + e) + (lane >> 4)));
+            }
+            mma16<F8>(sa[0], qf, e4m3x2_to_f16x2(kf[e]), e4m3x2_to_f16x2_hi(kf[e]));
+            mma16<F8>(sa[1], qf, e4m3x2_to_f16x2(kf[2 + e]), e4m3x2_to_f16x2_hi(kf[2 + e]));
+          }
+        }
+      }
+      // ---- scale, mask ----
+      const int pos = CHUNK * s.chunk(ka + (int)(q - q0));
+      // every row sees every slot of the chunk
+      const bool whole = pos + CHUNK - 1 <= p0 && (P.window == 0 || pos >= L - P.window || pos + CHUNK <= P.sinks);
+      float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float v = sa[nt][j] * ((j & 2) ? sc1 : sc0);
+          if (!whole) {
+            const int t = pos + 8 * nt + 2 * tq + (j & 1);
+            const int p = p0 + ((j & 2) ? i1 : i0);
+            const bool seen = t <= p && t < L && (P.window == 0 || t > p - P.window || t < P.sinks);
+            v = seen ? v : -INFINITY;
+          }
+          sa[nt][j] = v;
+          if (j & 2) mx1 = fmaxf(mx1, v); else mx0 = fmaxf(mx0, v);
+        }
+      // ---- running maximum, raised only by a chunk far above it ----
+      if (__any_sync(0xffffffffu, mx0 > m0 + RESCALE || mx1 > m1 + RESCALE)) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+        const float a0 = n0 == -INFINITY ? 1.f : ex2_approx(m0 - n0);
+        const float a1 = n1 == -INFINITY ? 1.f : ex2_approx(m1 - n1);
+        l0 *= a0;
+        l1 *= a1;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          o[nt][0] *= a0;
+          o[nt][1] *= a0;
+          o[nt][2] *= a1;
+          o[nt][3] *= a1;
+        }
+        m0 = n0;
+        m1 = n1;
+      }
+      const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+      uint32_t pa[4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const float x0 = ex2_approx(sa[nt][0] - b0), x1 = ex2_approx(sa[nt][1] - b0);
+        const float y0 = ex2_approx(sa[nt][2] - b1), y1 = ex2_approx(sa[nt][3] - b1);
+        l0 += x0 + x1;
+        l1 += y0 + y1;
+        pa[2 * nt] = F8 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
+        pa[2 * nt + 1] = F8 ? pack_f16x2(y0, y1) : pack_bf16x2(y0, y1);
+      }
+      // ---- O += P V; what no row sees may hold anything and counts as zero ----
+      uint32_t vm0 = 0xFFFFFFFFu, vm1 = 0xFFFFFFFFu;
+      if (!whole) {
+        auto seen = [&](int t) { return t < L && (t >= lo || t < P.sinks); };
+        const int t = pos + 2 * tq;
+        vm0 = (seen(t) ? 0xFFFFu : 0u) | (seen(t + 1) ? 0xFFFF0000u : 0u);
+        vm1 = (seen(t + 8) ? 0xFFFFu : 0u) | (seen(t + 9) ? 0xFFFF0000u : 0u);
+      }
+#pragma unroll
+      for (int np = 0; np < (F8 ? NT / 4 : NT / 2); ++np) {
+        uint32_t vf[4];
+        ldmatrix_x4_trans(vf, vt + swz16(8 * ((lane >> 3) & 1) + (lane & 7), 2 * np + (lane >> 4)));
+        if (!whole) {
+          vf[0] &= vm0;
+          vf[1] &= vm1;
+          vf[2] &= vm0;
+          vf[3] &= vm1;
+        }
+        if (!F8) {
+          mma16<F8>(o[2 * np], pa, vf[0], vf[1]);
+          mma16<F8>(o[2 * np + 1], pa, vf[2], vf[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // 16 columns: the even ones, then the odd ones
+            const uint32_t x = __byte_perm(vf[2 * e], 0u, 0x3120), y = __byte_perm(vf[2 * e + 1], 0u, 0x3120);
+            mma16<F8>(o[4 * np + 2 * e], pa, e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
+            mma16<F8>(o[4 * np + 2 * e + 1], pa, e4m3x2_to_f16x2_hi(x), e4m3x2_to_f16x2_hi(y));
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
+    }
+    q0 = q1;
+
+    // ---- join the warps of each query tile ----
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    // every lane of a quad holds the same maximum once it has been raised
+    if (tq == 0) {
+      float *w = sml + warp * 32;
+      w[gq * 2] = m0;
+      w[gq * 2 + 1] = l0;
+      w[(gq + 8) * 2] = m1;
+      w[(gq + 8) * 2 + 1] = l1;
+    }
+    named_barrier(1, NCW * 32);
+    float w0, w1;
+    {
+      float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < NL; ++c) {
+        t0 = fmaxf(t0, sml[(c * MT + mt) * 32 + gq * 2]);
+        t1 = fmaxf(t1, sml[(c * MT + mt) * 32 + (gq + 8) * 2]);
+      }
+      w0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - t0);
+      w1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - t1);
+      if (cl == 0 && tq == 0) {
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < NL; ++c) {
+          const float *w = sml + (c * MT + mt) * 32;
+          const float a = w[gq * 2], d = w[(gq + 8) * 2];
+          s0 += a == -INFINITY ? 0.f : ex2_approx(a - t0) * w[gq * 2 + 1];
+          s1 += d == -INFINITY ? 0.f : ex2_approx(d - t1) * w[(gq + 8) * 2 + 1];
+        }
+        fin[row0 * 2] = t0;
+        fin[row0 * 2 + 1] = s0;
+        fin[row1 * 2] = t1;
+        fin[row1 * 2 + 1] = s1;
+      }
+    }
+    const bool starts = ka == 0, ends = kb == n;
+    const size_t slot = (size_t)blockIdx.x * 2 + (starts ? 1 : 0);  // of a piece
+    const float vscale = F8 && P.vs ? P.vs[h] : 1.f;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (half == 1 && P.R <= 8) break;
+      // rows 8*half .. 8*half+7 of every tile, scaled to the joint maximum
+      float *mine = scratch + (size_t)(warp * 8 + gq) * LY::RS;
+      const float w = half ? w1 : w0;
+      if (!F8) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          *reinterpret_cast<float2 *>(mine + 8 * nt + 2 * tq) =
+              make_float2(o[nt][2 * half] * w, o[nt][2 * half + 1] * w);
+      } else {
+#pragma unroll
+        for (int c = 0; c < NT / 2; ++c)
+          *reinterpret_cast<float4 *>(mine + 16 * c + 4 * tq) =
+              make_float4(o[2 * c][2 * half] * w, o[2 * c + 1][2 * half] * w, o[2 * c][2 * half + 1] * w,
+                          o[2 * c + 1][2 * half + 1] * w);
+      }
+      named_barrier(1, NCW * 32);
+      for (int x = tid; x < MT * 8 * (D / 4); x += NCW * 32) {
+        const int rr = x / (D / 4), d = (x % (D / 4)) * 4;
+        const int r = 16 * (rr >> 3) + 8 * half + (rr & 7);
+        if (r >= P.R) continue;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < NL; ++c) {
+          const float4 v = *reinterpret_cast<const float4 *>(
+              scratch + (size_t)((c * MT + (rr >> 3)) * 8 + (rr & 7)) * LY::RS + d);
+          a.x += v.x;
+          a.y += v.y;
+          a.z += v.z;
+          a.w += v.w;
+        }
+        if (starts && ends) {
+          const float l = fin[r * 2 + 1];
+          const float f = l != 0.f ? vscale / l : 0.f;
+          const int i = r / P.G, j = r % P.G;
+          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(P.o.ptr) +
+                                     ((long long)b * P.M + i) * P.o.token_stride +
+                                     (long long)(h * P.G + j) * P.o.head_stride + d) =
+              make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+        } else {
+          *reinterpret_cast<float4 *>(P.opart + (slot * P.R + r) * D + d) = a;
+          if (d == 0) {
+            P.ml[(slot * P.R + r) * 2] = fin[r * 2];
+            P.ml[(slot * P.R + r) * 2 + 1] = fin[r * 2 + 1];
+          }
+        }
+      }
+      named_barrier(1, NCW * 32);
+    }
+    // the head's first piece names its pieces: CTAs blockIdx.x .. of its last unit
+    if (tid == 0 && starts) {
+      const int hh = b * P.Hkv + h;
+      const long long last = (long long)pre[b] * P.Hkv + (long long)(h + 1) * n - 1;
+      const int4 d = make_int4(hh, (int)blockIdx.x, ends ? 0 : (int)(last / per) - (int)blockIdx.x + 1, 0);
+      if (P.by_head)
+        P.desc[hh] = d;
+      else if (!ends)
+        P.desc[blockIdx.x] = d;
+    }
+    u += kb - ka;
+    if (h == P.Hkv - 1 && ends) ++b;
+  }
+}
+
+// Joins the pieces of the heads that were split: a group of D/4 threads per
+// (row, share of the pieces).  When heads are few (by_head) a block takes one
+// row and its groups share the pieces; else the pieces are few and each
+// group takes a row of its own.
+constexpr int JOIN_THREADS = 256;
+
+template <int D>
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Params P) {
+  constexpr int LPG = D / 4;
+  constexpr int NG = JOIN_THREADS / LPG;
+  __shared__ float4 part[NG][LPG];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int4 d = P.desc[blockIdx.x];
+  const int n = d.z;
+  if (n == 0) return;
+  const int grp = threadIdx.x / LPG, c = threadIdx.x % LPG;
+  const int r = P.by_head ? (int)blockIdx.y : (int)blockIdx.y * NG + grp;
+  const int step = P.by_head ? NG : 1, first = P.by_head ? grp : 0;
+  const bool have = r < P.R;
+  // piece i: the first CTA's second slot, the others' first
+  auto slot_of = [&](int i) { return (size_t)(d.y + i) * 2 + (i == 0 ? 1 : 0); };
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  float top = -INFINITY, l = 0.f;
+  if (have) {
+    for (int i = 0; i < n; ++i) top = fmaxf(top, P.ml[(slot_of(i) * P.R + r) * 2]);
+    for (int i = 0; i < n; ++i) {
+      const float m = P.ml[(slot_of(i) * P.R + r) * 2];
+      l += m == -INFINITY ? 0.f : ex2_approx(m - top) * P.ml[(slot_of(i) * P.R + r) * 2 + 1];
+    }
+#pragma unroll 4
+    for (int i = first; i < n; i += step) {
+      const float m = P.ml[(slot_of(i) * P.R + r) * 2];
+      const float w = m == -INFINITY ? 0.f : ex2_approx(m - top);
+      const float4 v = *reinterpret_cast<const float4 *>(P.opart + (slot_of(i) * P.R + r) * D + 4 * c);
+      a.x = fmaf(w, v.x, a.x);
+      a.y = fmaf(w, v.y, a.y);
+      a.z = fmaf(w, v.z, a.z);
+      a.w = fmaf(w, v.w, a.w);
+    }
+  }
+  if (P.by_head) {
+    part[grp][c] = a;
+    __syncthreads();
+    if (grp != 0) return;
+#pragma unroll
+    for (int g = 1; g < NG; ++g) {
+      const float4 v = part[g][c];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+  }
+  if (!have) return;
+  const int b = d.x / P.Hkv, h = d.x % P.Hkv;
+  const float f = l != 0.f ? (P.vs ? P.vs[h] : 1.f) / l : 0.f;
+  const int i = r / P.G, j = r % P.G;
+  *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(P.o.ptr) +
+                             ((long long)b * P.M + i) * P.o.token_stride +
+                             (long long)(h * P.G + j) * P.o.head_stride + 4 * c) =
+      make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+}
+
+// 5-D map of a cache: (column, slot, 128-byte group, head, page), box 128
+// bytes x 16 slots x all groups, 128-byte swizzle.
+static bool make_map(CUtensorMap *map, void *base, const sv_paged_kv *c, int D, int Hkv) {
+  auto fn = attn::encode_fn();
+  if (!fn) return false;
+  const int es = c->dtype == SV_E4M3 ? 1 : 2;
+  const cuuint32_t cols = 128 / es, groups = (cuuint32_t)(D * es / 128);
+  cuuint64_t dims[5] = {cols, (cuuint64_t)c->page_size, groups, (cuuint64_t)Hkv, (cuuint64_t)c->num_pages};
+  cuuint64_t strides[4] = {(cuuint64_t)c->slot_stride * es, 128, (cuuint64_t)c->head_stride * es,
+                           (cuuint64_t)c->page_stride * es};
+  cuuint32_t box[5] = {cols, (cuuint32_t)CHUNK, groups, 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool F8, int MT>
+static cudaError_t launch_main(const CUtensorMap &mk, const CUtensorMap &mv, Params &P, int ctas,
+                               cudaStream_t s) {
+  using LY = Layout<D, F8, MT>;
+  const size_t fixed = 1024 + LY::RING + ((size_t)P.B + 1) * 4;
+  P.stages = imin(MAX_STAGES, (int)((SMEM_LIMIT - fixed) / LY::STAGE));
+  return launch(paged_kernel<D, F8, MT>, dim3(ctas), dim3(THREADS), fixed + (size_t)P.stages * LY::STAGE, s,
+                mk, mv, P);
+}
+
+template <int D, bool F8>
+static cudaError_t launch_tiles(const CUtensorMap &mk, const CUtensorMap &mv, Params &P, int ctas,
+                                cudaStream_t s) {
+  if (P.R <= 16) return launch_main<D, F8, 1>(mk, mv, P, ctas, s);
+  if (P.R <= 32) return launch_main<D, F8, 2>(mk, mv, P, ctas, s);
+  if (P.R <= 64) return launch_main<D, F8, 4>(mk, mv, P, ctas, s);
+  return launch_main<D, F8, 8>(mk, mv, P, ctas, s);
+}
+
+template <int D>
+static cudaError_t launch_all(bool f8, const CUtensorMap &mk, const CUtensorMap &mv, Params &P, int ctas,
+                              cudaStream_t s) {
+  cudaError_t e = f8 ? launch_tiles<D, true>(mk, mv, P, ctas, s) : launch_tiles<D, false>(mk, mv, P, ctas, s);
+  if (e != cudaSuccess) return e;
+  const int ng = JOIN_THREADS / (D / 4);
+  const dim3 grid(P.by_head ? P.B * P.Hkv : ctas, P.by_head ? P.R : (P.R + ng - 1) / ng);
+  return launch_after(true, join_kernel<D>, grid, dim3(JOIN_THREADS), 0, s, P);
+}
+
+static size_t ws_bytes_for(int sms, int R, int D) {
+  return (size_t)sms * (16 + 2 * (size_t)R * (D + 2) * sizeof(float));
+}
+
+}  // namespace paged
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+size_t paged_attn_workspace_bytes(int B, int M, int Hq, int Hkv, int D) {
+  if (B < 1 || M < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
+  if ((D != 128 && D != 256) || (long long)M * (Hq / Hkv) > paged::MAX_R) return 0;
+  const int sms = device_sm_count();
+  return sms <= 0 ? 0 : paged::ws_bytes_for(sms, M * (Hq / Hkv), D);
+}
+
+sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const int32_t *block_table,
+                     int64_t table_stride, int table_width, const int32_t *kv_lens, const sv_rows *o, int B,
+                     int M, int Hq, int Hkv, int D, float scale, int window, int sinks, void *workspace,
+                     size_t ws_bytes, sv_stream_t stream) {
+  if (B < 0 || M < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv != 0) return SV_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0 || table_width < 1 || table_stride < 0) return SV_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale < INFINITY)) return SV_ERR_INVALID_ARG;
+  if (D != 128 && D != 256) return SV_ERR_UNSUPPORTED;
+  const int G = Hq / Hkv;
+  if ((long long)M * G > paged::MAX_R || B > paged::MAX_B) return SV_ERR_UNSUPPORTED;
+  if ((long long)B * M > 0x7fffffffLL || (long long)B * Hkv > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
+  if (!paged::good_rows(q, (long long)B * M) || !paged::good_rows(o, (long long)B * M)) return SV_ERR_INVALID_ARG;
+  const sv_status cs = paged::check_cache(cache, D);
+  if (cs != SV_OK) return cs;
+  if (B > 0 && (!block_table || !kv_lens)) return SV_ERR_INVALID_ARG;
+  if (!paged::aligned(block_table, 4) || !paged::aligned(kv_lens, 4)) return SV_ERR_INVALID_ARG;
+  // positions are 32-bit (with room for a window), and so is the line of chunks
+  const long long cap = (long long)table_width * cache->page_size;
+  if (cap > 0x40000000LL || window > 0x40000000 || cap / paged::CHUNK * imax(B, 1) > 0x7fffffffLL)
+    return SV_ERR_UNSUPPORTED;
+  if (B == 0) return SV_OK;
+  const int sms = device_sm_count();
+  if (sms <= 0) return SV_ERR_CUDA;
+  const int R = M * G;
+  if (!workspace || ws_bytes < paged::ws_bytes_for(sms, R, D)) return SV_ERR_WORKSPACE;
+  if (!paged::aligned(workspace, 16)) return SV_ERR_INVALID_ARG;
+  CUtensorMap mk, mv;
+  if (!paged::make_map(&mk, cache->k, cache, D, Hkv) || !paged::make_map(&mv, cache->v, cache, D, Hkv))
+    return SV_ERR_CUDA;
+  paged::Params P{};
+  P.q = *q;
+  P.o = *o;
+  P.table = block_table;
+  P.table_stride = table_stride;
+  P.width = table_width;
+  P.lens = kv_lens;
+  P.ks = cache->k_scale;
+  P.vs = cache->v_scale;
+  P.desc = static_cast<int4 *>(workspace);
+  P.opart = reinterpret_cast<float *>(P.desc + sms);
+  P.ml = P.opart + (size_t)2 * sms * R * D;
+  P.err = device_error_word();
+  if (!P.err) return SV_ERR_CUDA;
+  P.B = B;
+  P.M = M;
+  P.Hkv = Hkv;
+  P.G = G;
+  P.R = R;
+  P.sl2e = scale * 1.4426950408889634f;
+  P.window = window;
+  P.sinks = sinks;
+  P.page_size = cache->page_size;
+  P.num_pages = (int)cache->num_pages;
+  P.min_units = 8;
+  P.by_head = (long long)B * Hkv <= sms ? 1 : 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool f8 = cache->dtype == SV_E4M3;
+  return from_cuda(D == 256 ? paged::launch_all<256>(f8, mk, mv, P, sms, s)
+                            : paged::launch_all<128>(f8, mk, mv, P, sms, s));
+}
+
+}  // extern "C"
