@@ -340,6 +340,27 @@ SV_API sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const in
                             int window, int sinks, void *workspace, size_t ws_bytes,
                             sv_stream_t stream);
 
+/* Causal attention of packed prompts: sequence b's queries are rows
+ * cu_q[b]..cu_q[b+1]-1 of q and o, its keys and values rows
+ * cu_k[b]..cu_k[b+1]-1 of k and v.  With nq and nk of them, row i stands at
+ * position p = nk - nq + i (its own key is the last it can see; nk > nq: the
+ * earlier keys precede the prompt) and sees key j >= 0 iff j <= p and
+ * (window == 0, or j > p - window, or j < sinks):
+ *   o = softmax_j(scale * <q, k_j>) . v_j, zeros for a row that sees nothing.
+ * cu_q, cu_k: device int32 [B+1], 0 <= cu[b] <= cu[b+1] <= Tq (Tk).  A sequence
+ *   whose offsets break this is left out and reported by
+ *   sv_last_device_error() as SV_ERR_INVALID_ARG.  Rows of o of no sequence
+ *   are not written.
+ * Keys and values of a sequence hold finite values; rows of others, and rows
+ * of no sequence, may hold anything.
+ * Supported: D in {128, 256}; Hq % Hkv == 0; Hq/Hkv <= 128; 0 <= B <= 4096;
+ *   Tq, Tk <= 2^30; strides of q, k and v above 0; scale > 0 and finite. */
+SV_API size_t window_attn_workspace_bytes(int B, int Hq, int Hkv, int D);
+SV_API sv_status window_attn(const sv_rows *q, const sv_rows *k, const sv_rows *v, const sv_rows *o,
+                             const int32_t *cu_q, const int32_t *cu_k, int B, int Tq, int Tk, int Hq,
+                             int Hkv, int D, float scale, int window, int sinks, void *workspace,
+                             size_t ws_bytes, sv_stream_t stream);
+
 /* ---------------------------------------------------------------------- */
 /* Exact acceptance                                                         */
 /* ---------------------------------------------------------------------- */

@@ -34,7 +34,7 @@ __all__ = [
     "sv_kernel_launch_count", "prepack", "workspace", "library_path", "spec_pick_depth",
     "gdn_verify",
     "SV_E4M3", "rope_phases", "qk_norm_rope", "PagedKV", "paged_kv_append",
-    "paged_attn_workspace_bytes", "paged_attn",
+    "paged_attn_workspace_bytes", "paged_attn", "window_attn_workspace_bytes", "window_attn",
 ]
 
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_CUDA = 0, 1, 2, 3
@@ -111,6 +111,8 @@ def load():
             "paged_kv_append": (I, [P, P, P, P, P, P, P, P, I, I, I, I, P]),
             "paged_attn_workspace_bytes": (Z, [I, I, I, I, I]),
             "paged_attn": (I, [P, P, P, L, I, P, P, I, I, I, I, I, ctypes.c_float, I, I, P, Z, P]),
+            "window_attn_workspace_bytes": (Z, [I, I, I, I]),
+            "window_attn": (I, [P, P, P, P, P, P, I, I, I, I, I, I, ctypes.c_float, I, I, P, Z, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -494,3 +496,22 @@ def paged_attn(q, cache: PagedKV, block_table, kv_lens, o, M: int, scale: float,
                              block_table.shape[1], _vector(kv_lens, torch.int32, B, w),
                              _rows(o, rows, Hq, D, w), B, M, Hq, cache.heads, D, scale, window, sinks,
                              _ptr(workspace), _nbytes(workspace), _launch_stream(q, stream)), w)
+
+
+def window_attn_workspace_bytes(B: int, Hq: int, Hkv: int, D: int) -> int:
+    return load().window_attn_workspace_bytes(B, Hq, Hkv, D)
+
+
+def window_attn(q, k, v, o, cu_q, cu_k, scale: float, window: int = 0, sinks: int = 0, workspace=None,
+                stream=None):
+    """Causal attention of packed prompts: q and o [Tq, Hq, D], k and v [Tk,
+    Hkv, D]; sequence b is rows cu_q[b]..cu_q[b+1] (int32 [B+1]) against keys
+    cu_k[b]..cu_k[b+1], its last row at its last key."""
+    Tq, Hq, D = q.shape
+    Tk, Hkv, _ = k.shape
+    w = "window_attn"
+    n = cu_q.shape[0]
+    _check(load().window_attn(_rows(q, Tq, Hq, D, w), _rows(k, Tk, Hkv, D, w), _rows(v, Tk, Hkv, D, w),
+                              _rows(o, Tq, Hq, D, w), _vector(cu_q, torch.int32, n, w),
+                              _vector(cu_k, torch.int32, n, w), n - 1, Tq, Tk, Hq, Hkv, D, scale, window, sinks,
+                              _ptr(workspace), _nbytes(workspace), _launch_stream(q, stream)), w)

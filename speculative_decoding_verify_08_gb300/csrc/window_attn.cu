@@ -1,0 +1,615 @@
+// window_attn.cu -- causal attention of packed prompts, with an optional
+// sliding window and a few first tokens that stay visible.
+//
+// Row i of a sequence of nq rows and nk keys stands at position
+// p = nk - nq + i and sees key j iff j <= p and (no window, or j > p - window,
+// or j < sinks):   O = softmax_j(scale <Q, K_j>) V, zeros where nothing is seen.
+//
+// What bounds it: 4 * D * Hq products per visible (row, key) pair, so the
+// tensor cores; beside them one exponential per pair and query head.  Hence:
+//  * A tile is 128 query rows of one KV head: 128/G positions times the G query
+//    heads that share it, so short prompts and window edges waste few rows
+//    and the K/V stream of a tile serves all G heads.
+//  * Both products run as tcgen05.mma with fp32 accumulators in tensor memory:
+//    S = Q K^T from shared memory, O += P V with P (bf16) written over S in
+//    tensor memory by the softmax threads, one row a thread.
+//  * D = 128: a CTA carries two tiles (256 rows) with a softmax warpgroup each;
+//    the tensor cores work on one tile's products while the other's softmax
+//    runs, and each K/V block of 128 keys is fetched once for both.
+//    D = 256: O alone takes half of tensor memory, so a CTA carries one tile
+//    with two S buffers over blocks of 64 keys: S of the next block is
+//    computed during the softmax of this one.
+//  * Only blocks that some row of the CTA's tiles sees are visited.  One warp
+//    streams K and V blocks with TMA into a ring of 32 KB slots, another
+//    fetches the next tiles' queries as soon as the last S product is done.
+//  * The maximum that P refers to is raised only when a block exceeds it by
+//    more than 2^8, so O is rarely rescaled; P is rounded to bf16 (relative
+//    2^-8 at most, as the second product's operand), sums are fp32.
+#include "paged.cuh"
+#include "tcgen05.cuh"
+
+namespace sv {
+namespace attn {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // attn.cu
+}
+namespace window {
+
+constexpr int ROWS = 128;           // rows of a tile (TMEM lanes)
+constexpr int MAX_B = 4096;
+constexpr float RESCALE = 8.f;      // log2 of the largest P against an old maximum
+constexpr int SLOT = 32768;         // bytes of a K or V block
+constexpr size_t SMEM_LIMIT = 227 * 1024;
+
+template <int D>
+struct Cfg {
+  static constexpr int NT = D == 128 ? 2 : 1;   // tiles per CTA
+  static constexpr int NSB = D == 128 ? 1 : 2;  // S buffers per tile
+  static constexpr int BN = D == 128 ? 128 : 64;  // keys per block
+  static constexpr int SOFT = 4 * NT;           // softmax warps
+  static constexpr int THREADS = (SOFT + 4) * 32;
+  static constexpr int QBYTES = ROWS * D * 2;
+  static constexpr int QS = 1024;
+  static constexpr int RING = QS + NT * QBYTES;
+  static_assert(BN * D * 2 == SLOT, "block");
+  // tensor memory: O per tile, then the S buffers (P over S)
+  static constexpr uint32_t TO = 0, TS = NT * D;
+  static_assert(NT * D + NT * NSB * BN <= 512, "tensor memory");
+};
+
+struct Params {
+  sv_rows o;
+  const int *cu_q, *cu_k;
+  unsigned *err;
+  int B, Tq, Tk, Hkv, G, PT;  // PT: positions per tile
+  float sl2e;
+  int window, sinks, slots;
+};
+
+struct Item {
+  int h, q0, k0;     // KV head; first row of the packed queries and keys
+  int rows;          // positions of the item
+  int p0, nk;        // position of its first row; keys of the sequence
+  int ns, w0, n;     // blocks: 0..ns-1, then w0.. ; n in all
+  __device__ __forceinline__ int block(int j) const { return j < ns ? j : j - ns + w0; }
+};
+
+// Rows of sequence b, 0 if its offsets are out of order or out of range.
+__device__ __forceinline__ int rows_of(const Params &P, int b) {
+  const int q0 = P.cu_q[b], q1 = P.cu_q[b + 1], k0 = P.cu_k[b], k1 = P.cu_k[b + 1];
+  if (q0 < 0 || q1 < q0 || q1 > P.Tq || k0 < 0 || k1 < k0 || k1 > P.Tk) {
+    if (blockIdx.x == 0) atomicOr(P.err, ERR_INDEX);
+    return 0;
+  }
+  return q1 - q0;
+}
+
+template <int D>
+__device__ __forceinline__ Item item_at(const Params &P, const int *pre, int id) {
+  constexpr int BN = Cfg<D>::BN;
+  const int c = id / P.Hkv;
+  int lo = 0, hi = P.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= c) lo = mid; else hi = mid - 1;
+  }
+  const int b = lo, span = P.PT * Cfg<D>::NT;
+  Item it;
+  it.h = id - c * P.Hkv;
+  // a sequence's last tiles first: they see the most
+  const int tile = pre[b + 1] - 1 - c;
+  const int nq = P.cu_q[b + 1] - P.cu_q[b];
+  it.k0 = P.cu_k[b];
+  it.nk = P.cu_k[b + 1] - it.k0;
+  const int first = tile * span;
+  it.q0 = P.cu_q[b] + first;
+  it.rows = imin(span, nq - first);
+  it.p0 = it.nk - nq + first;
+  const int last = it.p0 + it.rows - 1;
+  const int ce = last < 0 ? 0 : last / BN + 1;
+  it.w0 = P.window > 0 ? imax(0, it.p0 - P.window + 1) / BN : 0;
+  it.ns = (imin(P.sinks, imax(0, last + 1)) + BN - 1) / BN;
+  if (it.w0 <= it.ns) it.w0 = it.ns = 0;
+  it.n = it.ns + ce - it.w0;
+  return it;
+}
+
+// Item of round k for this CTA (-1: none in this round).  Rounds alternate
+// direction, so that the CTA with a round's longest item gets the next one's shortest.
+__device__ __forceinline__ int item_id(int k, int items) {
+  const int g = (int)gridDim.x, at = (k & 1) ? g - 1 - (int)blockIdx.x : (int)blockIdx.x;
+  return k * g + at < items ? k * g + at : -1;
+}
+
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                            int c3, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(smem_dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+    window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                  const __grid_constant__ CUtensorMap mapV, const Params P) {
+  using C = Cfg<D>;
+  constexpr int NT = C::NT, NSB = C::NSB, BN = C::BN;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem);  // ring slots (at most 5)
+  uint64_t *empty = full + 5;
+  uint64_t *s_full = empty + 5;    // [2] per S buffer
+  uint64_t *p_full = s_full + 2;   // [2] per S buffer: P written over it
+  uint64_t *o_done = p_full + 2;   // [2] per S buffer: the second product of its P done
+  uint64_t *o_free = o_done + 2;   // [NT] O read out
+  uint64_t *q_full = o_free + 2;   // queries of the item landed
+  uint64_t *q_free = q_full + 1;   // last S product of the item done
+  uint64_t *idle = q_free + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(idle + 1);
+  int *wsum = reinterpret_cast<int *>(smem + 512);
+  uint8_t *qs = smem + C::QS;
+  uint8_t *ring = smem + C::RING;
+  const int NS = P.slots;
+  int *pre = reinterpret_cast<int *>(ring + (size_t)NS * SLOT);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_done[i], 1);
+      mbar_init(&o_free[i], 4);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_free, 1);
+    mbar_init(idle, 1);
+    fence_barrier_init();
+  }
+  if (warp == C::SOFT) {
+    tc::tmem_alloc(tmem_slot, 512u);
+    tc::tmem_relinquish();
+  }
+  // rows of the query tiles that no load writes stay zero
+  const int used = P.PT * P.G;
+  for (int x = tid; x < NT * (ROWS - used) * (D / 8); x += C::THREADS) {
+    const int t = x / ((ROWS - used) * (D / 8)), y = x % ((ROWS - used) * (D / 8));
+    const int r = used + y / (D / 8), c = y % (D / 8);
+    *reinterpret_cast<uint4 *>(qs + t * C::QBYTES + (c >> 3) * ROWS * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async();
+  pdl_wait();
+
+  // ---- prefix sums of the sequences' items per KV head ----
+  int total = 0;
+  for (int b0 = 0; b0 < P.B; b0 += C::THREADS) {
+    const int b = b0 + tid;
+    const int nt = b < P.B ? (rows_of(P, b) + P.PT * NT - 1) / (P.PT * NT) : 0;
+    int x = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < C::THREADS / 32; ++w) {
+      if (w < warp) before += wsum[w];
+      all += wsum[w];
+    }
+    if (b < P.B) pre[b] = total + before + x - nt;
+    total += all;
+    __syncthreads();
+  }
+  if (tid == 0) pre[P.B] = total;
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = *tmem_slot;
+  const int items = total * P.Hkv;
+  const int rounds = (items + (int)gridDim.x - 1) / (int)gridDim.x;
+
+  if (warp >= C::SOFT) {
+    // 384 threads start with 168 registers each: 128*72 + 256*216 is the same total
+    if (D == 128) setmaxnreg_dec<72>();
+    if (warp == C::SOFT + 1) {
+      // ------------------------------------------- K and V blocks --
+      if (lane == 0) {
+        bool ok = true;
+        uint32_t q = 0;
+        for (int k = 0; k < rounds && ok; ++k) {
+          const int id = item_id(k, items);
+          if (id < 0) continue;
+          const Item it = item_at<D>(P, pre, id);
+          for (int j = 0; j < 2 * it.n && ok; ++j, ++q) {
+            const uint32_t slot = q % (uint32_t)NS;
+            ok = mbar_wait(&empty[slot], ((q / (uint32_t)NS) & 1) ^ 1, P.err);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&full[slot], SLOT);
+            tma_load_4d(ring + slot * SLOT, (j & 1) ? &mapV : &mapK, 0, it.k0 + it.block(j >> 1) * BN, 0, it.h,
+                        &full[slot]);
+          }
+        }
+        if (!ok) {  // no copy may outlive the CTA
+          const uint32_t first = q > (uint32_t)NS ? q - NS : 0u;
+          for (uint32_t qq = first; qq < q; ++qq) mbar_wait(&full[qq % NS], (qq / NS) & 1, P.err);
+        }
+      }
+      __syncwarp();
+    } else if (warp == C::SOFT + 2) {
+      // --------------------------------------------------- queries --
+      if (lane == 0) {
+        bool ok = true;
+        uint32_t c = 0;  // items with work so far
+        for (int k = 0; k < rounds && ok; ++k) {
+          const int id = item_id(k, items);
+          if (id < 0) continue;
+          const Item it = item_at<D>(P, pre, id);
+          if (it.n == 0) continue;
+          if (c > 0) ok = mbar_wait(q_free, (c - 1) & 1, P.err);
+          if (!ok) break;
+          ++c;
+          const int nt = it.rows > P.PT ? NT : 1;
+          mbar_arrive_expect_tx(q_full, (uint32_t)(nt * used * D * 2));
+          for (int t = 0; t < nt; ++t)
+#pragma unroll
+            for (int g = 0; g < D / 64; ++g)
+              tma_load_4d(qs + t * C::QBYTES + g * ROWS * 128, &mapQ, 0, it.h * P.G, it.q0 + t * P.PT, g, q_full);
+        }
+        if (!ok && c > 0) mbar_wait(q_full, (c - 1) & 1, P.err);
+      }
+      __syncwarp();
+    } else if (warp == C::SOFT) {
+      // ------------------------------------------------- MMA issuer --
+      constexpr uint32_t IDS = tc::idesc_bf16_f32(ROWS, BN, false);
+      constexpr uint32_t IDO = tc::idesc_bf16_f32(ROWS, D, true);
+      const uint32_t qs_a = smem_u32(qs), ring_a = smem_u32(ring);
+      bool ok = true;
+      uint32_t q = 0;                 // ring position of the item's first block
+      uint32_t c = 0;                 // items with work so far
+      uint32_t sj[NT] = {}, pj[NT] = {};  // blocks of each tile: S issued, P consumed
+      uint32_t oc[NT] = {};           // items of each tile
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ok) ok = spin_wait(bar, parity, P.err);
+        ok = __all_sync(0xffffffffu, ok);
+      };
+      auto issue_s = [&](int t, uint32_t slot) {  // lane 0
+        const uint32_t sb = NSB == 2 ? (sj[t] & 1) : (uint32_t)t;
+        const uint32_t kb = ring_a + slot * SLOT, qa = qs_a + t * C::QBYTES;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks & 3) * 32;
+          tc::mma_bf16(tbase + C::TS + sb * BN, tc::smem_desc_sw128(qa + (ks >> 2) * ROWS * 128 + off, 16, 1024),
+                       tc::smem_desc_sw128(kb + (ks >> 2) * BN * 128 + off, 16, 1024), IDS, ks > 0);
+        }
+        tc::commit(&s_full[sb]);
+      };
+      for (int k = 0; k < rounds && ok; ++k) {
+        const int id = item_id(k, items);
+        if (id < 0) continue;
+        const Item it = item_at<D>(P, pre, id);
+        if (it.n == 0) continue;
+        const int nt = it.rows > P.PT ? NT : 1;
+        wait(q_full, c & 1);
+        ++c;
+        wait(&full[q % NS], (q / NS) & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (lane == 0) {
+          for (int t = 0; t < nt; ++t) issue_s(t, q % NS);
+          tc::commit(&empty[q % NS]);
+          if (it.n == 1) tc::commit(q_free);
+        }
+        for (int t = 0; t < nt; ++t) ++sj[t];
+        for (int j = 0; j < it.n && ok; ++j) {
+          const uint32_t qv = q + 2 * j + 1, qk = qv + 1;
+          const bool more = j + 1 < it.n;
+          if (NSB == 2 && more) {  // the next S runs during this block's softmax
+            wait(&full[qk % NS], (qk / NS) & 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (lane == 0) {
+              issue_s(0, qk % NS);
+              tc::commit(&empty[qk % NS]);
+              if (j + 2 == it.n) tc::commit(q_free);
+            }
+            ++sj[0];
+          }
+          wait(&full[qv % NS], (qv / NS) & 1);
+          if (!ok) break;
+          // rows past the sequence's keys belong to others: they count as zero
+          const int past = it.block(j) * BN + BN - it.nk;
+          if (past > 0) {
+            uint8_t *vb = ring + (qv % NS) * SLOT;
+            for (int x = lane; x < past * (D / 8); x += 32) {
+              const int r = BN - past + x / (D / 8), y = x % (D / 8);
+              *reinterpret_cast<uint4 *>(vb + (y >> 3) * BN * 128 + r * 128 + (y & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async();
+            __syncwarp();
+          }
+          if (NSB == 1 && more) wait(&full[qk % NS], (qk / NS) & 1);
+          for (int t = 0; t < nt && ok; ++t) {
+            const uint32_t sb = NSB == 2 ? (pj[t] & 1) : (uint32_t)t;
+            if (j == 0 && oc[t] > 0) wait(&o_free[t], (oc[t] - 1) & 1);
+            wait(&p_full[sb], (NSB == 2 ? pj[t] >> 1 : pj[t]) & 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (lane == 0) {
+              const uint32_t vb = ring_a + (qv % NS) * SLOT;
+#pragma unroll
+              for (int ks = 0; ks < BN / 16; ++ks)
+                tc::mma_bf16_ts(tbase + C::TO + t * D, tbase + C::TS + sb * BN + ks * 8,
+                                tc::smem_desc_sw128(vb + ks * 2048, BN * 128, 1024), IDO, j > 0 || ks > 0);
+              tc::commit(&o_done[sb]);
+              if (t == nt - 1) tc::commit(&empty[qv % NS]);
+              if (NSB == 1 && more) {
+                issue_s(t, qk % NS);
+                if (t == nt - 1) {
+                  tc::commit(&empty[qk % NS]);
+                  if (j + 2 == it.n) tc::commit(q_free);
+                }
+              }
+            }
+            ++pj[t];
+            if (NSB == 1 && more) ++sj[t];
+          }
+        }
+        for (int t = 0; t < nt; ++t) ++oc[t];
+        q += 2 * it.n;
+        __syncwarp();
+      }
+      if (lane == 0) {  // every product issued above has completed before TMEM is released
+        tc::commit(idle);
+        spin_wait(idle, 0, P.err);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------ softmax --
+    if (D == 128) setmaxnreg_inc<216>();
+    const int t = warp >> 2;                    // tile
+    const int r = (warp & 3) * 32 + lane;       // row = TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const int ir = r / P.G, jr = r % P.G;       // position and query head in the tile
+    const float sl2e = P.sl2e;
+    const uint32_t tO = tbase + C::TO + t * D + lane_off;
+    bool ok = true;
+    uint32_t cnt = 0;  // blocks of this tile so far
+    // The second product of the latest block.  The barrier's phase before it
+    // is known to be over: its S (one S buffer: S of the latest block) was
+    // issued after that product.
+    auto wait_product = [&]() {
+      const uint32_t at = cnt - 1;
+      if (ok) ok = spin_wait(&o_done[NSB == 2 ? (at & 1) : (uint32_t)t], (NSB == 2 ? at >> 1 : at) & 1, P.err);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    for (int k = 0; k < rounds; ++k) {
+      const int id = item_id(k, items);
+      if (id < 0) continue;
+      const Item it = item_at<D>(P, pre, id);
+      if (t > 0 && it.rows <= P.PT) continue;
+      const bool mine = ir < P.PT && t * P.PT + ir < it.rows;  // a row of the prompt
+      const int pt = it.p0 + t * P.PT, p = pt + ir;            // position of the tile's first row, of this one
+      const int plast = it.p0 + imin(it.rows, (t + 1) * P.PT) - 1;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < it.n; ++j, ++cnt) {
+        const uint32_t sb = NSB == 2 ? (cnt & 1) : (uint32_t)t;
+        const uint32_t tS = tbase + C::TS + sb * BN + lane_off;
+        if (ok) ok = spin_wait(&s_full[sb], (NSB == 2 ? cnt >> 1 : cnt) & 1, P.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc::fence_after_sync();
+        uint32_t raw[BN / 32][32];
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) tc::ld32(tS + 32 * c, raw[c]);
+        tc::wait_ld();
+        const int base = it.block(j) * BN;
+        if (base + BN - 1 > pt || (P.window > 0 && base <= plast - P.window && base + BN > P.sinks)) {
+          const int hi = p - base, lo = P.window > 0 ? hi - P.window : -1, sk = P.sinks - base;
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (c > hi || (c <= lo && c >= sk)) raw[c / 32][c % 32] = 0xFF800000u;  // -inf
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < BN; ++c) mx = fmaxf(mx, __uint_as_float(raw[c / 32][c % 32]));
+        mx *= sl2e;
+        float alpha = 1.f;
+        if (mx > m + RESCALE) {
+          alpha = m == -INFINITY ? 0.f : ex2_approx(m - mx);
+          m = mx;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // the previous block's product is in O before it is rescaled
+          wait_product();
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+            tc::ld32(tO + c0, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tc::st32(tO + c0, o);
+          }
+          tc::wait_st();
+          l *= alpha;
+        }
+        const float nbase = m == -INFINITY ? 0.f : -m;
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x = ex2_approx(fmaf(__uint_as_float(raw[c][2 * e]), sl2e, nbase));
+            const float y = ex2_approx(fmaf(__uint_as_float(raw[c][2 * e + 1]), sl2e, nbase));
+            sum += x + y;
+            pk[e] = pack_bf16x2(x, y);
+          }
+          tc::st16(tS + 16 * c, pk);
+        }
+        l += sum;
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[sb]);
+      }
+      if (it.n > 0) {
+        wait_product();
+        if (!ok) break;
+        tc::fence_after_sync();
+      }
+      const float f = l != 0.f ? 1.f / l : 0.f;
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.o.ptr) +
+                           (long long)(it.q0 + t * P.PT + ir) * P.o.token_stride +
+                           (long long)(it.h * P.G + jr) * P.o.head_stride;
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t o[32];
+        if (it.n > 0) {
+          tc::ld32(tO + c0, o);
+          tc::wait_ld();
+        }
+        if (mine) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 8) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (l != 0.f) {
+              v.x = pack_bf16x2(__uint_as_float(o[c]) * f, __uint_as_float(o[c + 1]) * f);
+              v.y = pack_bf16x2(__uint_as_float(o[c + 2]) * f, __uint_as_float(o[c + 3]) * f);
+              v.z = pack_bf16x2(__uint_as_float(o[c + 4]) * f, __uint_as_float(o[c + 5]) * f);
+              v.w = pack_bf16x2(__uint_as_float(o[c + 6]) * f, __uint_as_float(o[c + 7]) * f);
+            }
+            *reinterpret_cast<uint4 *>(out + c0 + c) = v;
+          }
+        }
+      }
+      if (it.n > 0) {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[t]);
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == C::SOFT) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tbase, 512u);
+  }
+}
+
+// 4-D map of rows [T][H][D]: keys and values (column, token, 64-column group,
+// head) in boxes of 64 x BN x D/64, queries (column, head, token, group) in
+// boxes of 64 x G x PT; 128-byte swizzle, zeros past the last token.
+// `any`: an address to stand in for that of no rows.
+static bool make_map(CUtensorMap *map, const sv_rows *r, int T, int H, int D, bool query, int b1, int b2, void *any) {
+  auto fn = attn::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t t = (cuuint64_t)imax(T, 1), g = (cuuint64_t)(D / 64);
+  // the stride of a dimension of one is never used, but has to be a valid one
+  const cuuint64_t ts = T > 1 ? (cuuint64_t)r->token_stride * 2 : 128, hs = H > 1 ? (cuuint64_t)r->head_stride * 2 : 128;
+  cuuint64_t dk[4] = {64, t, g, (cuuint64_t)H}, sk[3] = {ts, 128, hs};
+  cuuint64_t dq[4] = {64, (cuuint64_t)H, t, g}, sq[3] = {hs, ts, 128};
+  cuuint32_t bk[4] = {64, (cuuint32_t)b1, (cuuint32_t)g, 1}, bq[4] = {64, (cuuint32_t)b1, (cuuint32_t)b2, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, T > 0 ? r->ptr : any, query ? dq : dk, query ? sq : sk, query ? bq : bk, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+static sv_status run(const sv_rows *q, const sv_rows *k, const sv_rows *v, Params &P, int sms, cudaStream_t s) {
+  using C = Cfg<D>;
+  CUtensorMap mq, mk, mv;
+  if (!make_map(&mq, q, P.Tq, P.Hkv * P.G, D, true, P.G, P.PT, q->ptr) ||
+      !make_map(&mk, k, P.Tk, P.Hkv, D, false, C::BN, 0, q->ptr) ||
+      !make_map(&mv, v, P.Tk, P.Hkv, D, false, C::BN, 0, q->ptr))
+    return SV_ERR_CUDA;
+  const size_t fixed = 1024 + C::RING + ((size_t)P.B + 1) * 4;
+  P.slots = imin(5, (int)((SMEM_LIMIT - fixed) / SLOT));
+  // at most one item more per sequence than the rows fill
+  const long long items = ((long long)P.Tq / (P.PT * C::NT) + P.B) * P.Hkv;
+  const int ctas = (int)lmin(items, sms);
+  return from_cuda(launch(window_kernel<D>, dim3(ctas), dim3(C::THREADS), fixed + (size_t)P.slots * SLOT, s, mq, mk,
+                          mv, P));
+}
+
+}  // namespace window
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+size_t window_attn_workspace_bytes(int B, int Hq, int Hkv, int D) {
+  (void)B, (void)Hq, (void)Hkv, (void)D;
+  return 0;
+}
+
+sv_status window_attn(const sv_rows *q, const sv_rows *k, const sv_rows *v, const sv_rows *o,
+                      const int32_t *cu_q, const int32_t *cu_k, int B, int Tq, int Tk, int Hq, int Hkv, int D,
+                      float scale, int window, int sinks, void *workspace, size_t ws_bytes, sv_stream_t stream) {
+  (void)workspace, (void)ws_bytes;
+  if (B < 0 || Tq < 0 || Tk < 0 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv != 0) return SV_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0) return SV_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale < INFINITY)) return SV_ERR_INVALID_ARG;
+  if (D != 128 && D != 256) return SV_ERR_UNSUPPORTED;
+  const int G = Hq / Hkv;
+  if (G > window::ROWS || B > window::MAX_B) return SV_ERR_UNSUPPORTED;
+  if (Tq > 0x40000000 || Tk > 0x40000000 || window > 0x40000000) return SV_ERR_UNSUPPORTED;
+  for (const sv_rows *r : {q, o})
+    if (!paged::good_rows(r, Tq)) return SV_ERR_INVALID_ARG;
+  for (const sv_rows *r : {k, v})
+    if (!paged::good_rows(r, Tk)) return SV_ERR_INVALID_ARG;
+  if (B > 0 && (!cu_q || !cu_k)) return SV_ERR_INVALID_ARG;
+  if (!paged::aligned(cu_q, 4) || !paged::aligned(cu_k, 4)) return SV_ERR_INVALID_ARG;
+  // a tensor map steps by every stride: rows that repeat (stride 0) have none
+  if ((Tq > 1 && !q->token_stride) || (Hq > 1 && !q->head_stride)) return SV_ERR_UNSUPPORTED;
+  for (const sv_rows *r : {k, v})
+    if ((Tk > 1 && !r->token_stride) || (Hkv > 1 && !r->head_stride)) return SV_ERR_UNSUPPORTED;
+  // the items of all KV heads are counted in 31 bits
+  const int pt = window::ROWS / G;
+  if (((long long)Tq / pt + B) * Hkv > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
+  if (B == 0 || Tq == 0) return SV_OK;
+  const int sms = device_sm_count();
+  if (sms <= 0) return SV_ERR_CUDA;
+  window::Params P{};
+  P.o = *o;
+  P.cu_q = cu_q;
+  P.cu_k = cu_k;
+  P.err = device_error_word();
+  if (!P.err) return SV_ERR_CUDA;
+  P.B = B;
+  P.Tq = Tq;
+  P.Tk = Tk;
+  P.Hkv = Hkv;
+  P.G = G;
+  P.PT = pt;
+  P.sl2e = scale * 1.4426950408889634f;
+  P.window = window;
+  P.sinks = sinks;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return D == 256 ? window::run<256>(q, k, v, P, sms, s) : window::run<128>(q, k, v, P, sms, s);
+}
+
+}  // extern "C"

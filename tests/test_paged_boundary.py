@@ -164,3 +164,22 @@ def test_plain_visibility():
     assert plain.visible(10, 7, 3, 2) == [0, 1, 5, 6, 7]
     assert plain.visible(10, 1, 3, 4) == [0, 1]
     assert plain.visible(10, -1, 0, 0) == [] and plain.visible(0, 5, 0, 0) == []
+
+
+def test_window_attn_refusals(sv):
+    f = sv.load().window_attn
+    r = rows(sv)
+
+    def call(q=r, k=r, v=r, o=r, cu_q=A, cu_k=A, B=2, Tq=9, Tk=9, Hq=8, Hkv=4, D=128, scale=0.1, window=0, sinks=0):
+        return f(q, k, v, o, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, scale, window, sinks, None, 0, None)
+
+    assert call(q=None) == 1 and call(v=None) == 1 and call(o=rows(sv, ptr=A + 8)) == 1
+    assert call(cu_q=None) == 1 and call(cu_k=A + 2) == 1
+    assert call(B=-1) == 1 and call(Tq=-1) == 1 and call(Tk=-1) == 1 and call(Hq=6) == 1
+    assert call(scale=0.0) == 1 and call(scale=float("nan")) == 1
+    assert call(window=-1) == 1 and call(sinks=-1) == 1
+    assert call(k=rows(sv, ts=1028)) == 1
+    assert call(D=64) == 2 and call(Hq=129 * 4) == 2 and call(B=5000) == 2
+    assert call(k=rows(sv, ts=0)) == 2 and call(v=rows(sv, hs=0)) == 2   # repeated rows
+    assert call(Tk=(1 << 30) + 1) == 2 and call(window=(1 << 30) + 1) == 2
+    assert call(B=0) == 0 and call(Tq=0) == 0
