@@ -305,6 +305,18 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// Moves registers between the warpgroups of a block (all four warps of a
+// warpgroup execute it); the sum over the block may not pass what it was
+// launched with.
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // 4-byte asynchronous copy global -> shared (completed by cp_async_wait_all).
 __device__ __forceinline__ void cp_async4(void *smem_dst, const void *gmem_src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(gmem_src)

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w <= NCW; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
       if (w < warp) before += wsum[w];
       all += wsum[w];
     }
@@ -218,10 +218,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == NCW) {
     // ------------------------------------------------------- producer --
+    // A lane works out the page and slot of one chunk of the next 32, so that
+    // the chunks' own turns hold little but the wait and the copies.
     const uint64_t pol = l2_evict_first_policy();
     const int cpp = P.page_size / CHUNK;
     bool ok = true;
-    uint32_t q = 0;
+    uint32_t q = 0, parity = 1;
+    int slot = 0;
     int b = u0 < u1 ? seq_of(u0) : 0;
     for (long long u = u0; u < u1 && ok;) {
       while (pre[b + 1] == pre[b]) ++b;  // (a unit follows: a non-empty sequence exists)
@@ -239,25 +242,26 @@ __global__ void __launch_bounds__(THREADS, 1)
       };
       int next = page_at(ka + lane);
       for (int k0 = ka; k0 < kb && ok; k0 += 32) {
-        const int cur = next;
+        const int page = next;
         next = page_at(k0 + 32 + lane);
         const int m = imin(32, kb - k0);
-        for (int i = 0; i < m; ++i, ++q) {
-          const int page = __shfl_sync(0xffffffffu, cur, i);
-          const int slot = (int)(q % (uint32_t)NST);
-          if (lane == 0) {
-            ok = mbar_wait(&empty[slot], ((q / (uint32_t)NST) & 1) ^ 1, P.err);
-            if (ok) {
-              const int c = s.chunk(k0 + i);
-              uint8_t *dst = ring + slot * LY::STAGE;
-              mbar_arrive_expect_tx(&full[slot], LY::STAGE);
-              // a page out of range reads zeros (the copy is clipped to the cache)
-              tma_load_5d(dst, &mapK, 0, (c % cpp) * CHUNK, 0, h, page, &full[slot], pol);
-              tma_load_5d(dst + LY::TILE, &mapV, 0, (c % cpp) * CHUNK, 0, h, page, &full[slot], pol);
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+        const int at = (s.chunk(imin(k0 + lane, kb - 1)) % cpp) * CHUNK;
+        for (int i = 0; i < m; ++i) {
+          const int pg = __shfl_sync(0xffffffffu, page, i), sl = __shfl_sync(0xffffffffu, at, i);
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], parity, P.err));
           if (!ok) break;
+          if (lane == 0) {
+            uint8_t *dst = ring + slot * LY::STAGE;
+            mbar_arrive_expect_tx(&full[slot], LY::STAGE);
+            // a page out of range reads zeros (the copy is clipped to the cache)
+            tma_load_5d(dst, &mapK, 0, sl, 0, h, pg, &full[slot], pol);
+            tma_load_5d(dst + LY::TILE, &mapV, 0, sl, 0, h, pg, &full[slot], pol);
+          }
+          ++q;
+          if (++slot == NST) {
+            slot = 0;
+            parity ^= 1;
+          }
         }
       }
       u += kb - ka;
@@ -265,7 +269,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (!ok && lane == 0) {  // a wait ran out: no copy may outlive the CTA
       const uint32_t first = q > (uint32_t)NST ? q - NST : 0u;
-      for (uint32_t qq = first; qq < q; ++qq) mbar_wait(&full[qq % NST], (qq / NST) & 1, P.err);
+      for (uint32_t qq = first; qq < q && mbar_wait(&full[qq % NST], (qq / NST) & 1, P.err); ++qq) {
+      }
     }
     return;
   }
@@ -694,7 +699,12 @@ static cudaError_t launch_main(const CUtensorMap &mk, const CUtensorMap &mv, Par
                                cudaStream_t s) {
   using LY = Layout<D, F8, MT>;
   const size_t fixed = 1024 + LY::RING + ((size_t)P.B + 1) * 4;
-  P.stages = imin(MAX_STAGES, (int)((SMEM_LIMIT - fixed) / LY::STAGE));
+  // A multiple of the warps that take turns (NCW / MT), so that a ring slot's
+  // chunks all fall to the same warps: a warp that came to a slot's next chunk
+  // while another's was still on its way would take the barrier's phase of two
+  // rounds ago for its own (phases are told apart by parity alone).
+  constexpr int TURNS = NCW / MT;
+  P.stages = imin(MAX_STAGES, (int)((SMEM_LIMIT - fixed) / LY::STAGE)) / TURNS * TURNS;
   return launch(paged_kernel<D, F8, MT>, dim3(ctas), dim3(THREADS), fixed + (size_t)P.stages * LY::STAGE, s,
                 mk, mv, P);
 }
