@@ -13,7 +13,7 @@
 //    CTA (one per SM) finds the line's length from the device's lengths and
 //    takes an equal, contiguous piece, so ragged batches and long single
 //    sequences load all SMs alike and the host needs no lengths.
-//  * One producer warp streams chunks into a shared-memory ring by TMA, one
+//  * Two producer warps stream chunks into a shared-memory ring by TMA, one
 //    5-D copy for K and one for V (page, head, 64-column group, slot, column),
 //    looking pages up 32 chunks ahead.  A chunk never crosses a page.
 //  * Each of eight consumer warps takes every (8/MT)-th chunk for one 16-row
@@ -41,7 +41,8 @@ namespace paged {
 
 constexpr int CHUNK = 16;  // slots per unit
 constexpr int NCW = 8;     // consumer warps
-constexpr int THREADS = (NCW + 1) * 32;
+constexpr int NPW = 4;     // producer warps: K and V of even and odd chunks
+constexpr int THREADS = (NCW + NPW) * 32;
 constexpr int MAX_B = 4096;
 constexpr int MAX_R = 128;           // query rows per KV head: eight 16-row tiles
 constexpr int MAX_STAGES = 24;
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 2);  // K and V
       mbar_init(&empty[i], MT);
     }
     fence_barrier_init();
@@ -216,10 +217,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     return lo;  // the last sequence that starts at or before c, so it is not empty
   };
 
-  if (warp == NCW) {
-    // ------------------------------------------------------- producer --
+  if (warp >= NCW) {
+    // ------------------------------------------------------ producers --
+    // Two warps stream K, two V; the pairs take turns chunk by chunk.
     // A lane works out the page and slot of one chunk of the next 32, so that
     // the chunks' own turns hold little but the wait and the copies.
+    const bool is_v = (warp - NCW) & 1;
+    const int turn = (warp - NCW) >> 1;
     const uint64_t pol = l2_evict_first_policy();
     const int cpp = P.page_size / CHUNK;
     bool ok = true;
@@ -246,18 +250,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         next = page_at(k0 + 32 + lane);
         const int m = imin(32, kb - k0);
         const int at = (s.chunk(imin(k0 + lane, kb - 1)) % cpp) * CHUNK;
-        for (int i = 0; i < m; ++i) {
+        for (int i = 0; i < m; ++i, ++q) {
+          if ((q & 1) == turn) {
           const int pg = __shfl_sync(0xffffffffu, page, i), sl = __shfl_sync(0xffffffffu, at, i);
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], parity, P.err));
           if (!ok) break;
           if (lane == 0) {
-            uint8_t *dst = ring + slot * LY::STAGE;
-            mbar_arrive_expect_tx(&full[slot], LY::STAGE);
+            mbar_arrive_expect_tx(&full[slot], LY::TILE);
             // a page out of range reads zeros (the copy is clipped to the cache)
-            tma_load_5d(dst, &mapK, 0, sl, 0, h, pg, &full[slot], pol);
-            tma_load_5d(dst + LY::TILE, &mapV, 0, sl, 0, h, pg, &full[slot], pol);
+            tma_load_5d(ring + slot * LY::STAGE + (is_v ? LY::TILE : 0), is_v ? &mapV : &mapK, 0, sl, 0, h, pg,
+                        &full[slot], pol);
           }
-          ++q;
+          }
           if (++slot == NST) {
             slot = 0;
             parity ^= 1;
@@ -704,7 +708,7 @@ static cudaError_t launch_main(const CUtensorMap &mk, const CUtensorMap &mv, Par
   // while another's was still on its way would take the barrier's phase of two
   // rounds ago for its own (phases are told apart by parity alone).
   constexpr int TURNS = NCW / MT;
-  P.stages = imin(MAX_STAGES, (int)((SMEM_LIMIT - fixed) / LY::STAGE)) / TURNS * TURNS;
+  P.stages = imin(MAX_STAGES, (int)((SMEM_LIMIT - fixed) / LY::STAGE)) / TURNS * TURNS & ~1;
   return launch(paged_kernel<D, F8, MT>, dim3(ctas), dim3(THREADS), fixed + (size_t)P.stages * LY::STAGE, s,
                 mk, mv, P);
 }
