@@ -330,7 +330,7 @@ SV_API sv_status paged_kv_append(const sv_rows *q, const sv_rows *q_out, const s
  * Slots that no row of the sequence sees may hold anything, NaN included;
  * those that some row sees hold finite values.
  * Supported: D in {128, 256}; Hq % Hkv == 0; M*(Hq/Hkv) <= 128; 0 <= B <= 4096;
- *   table_width*page_size <= 2^30, B times that <= 2^35; scale > 0 and finite.
+ *   table_width*page_size <= 2^30, B*Hkv times that <= 2^35; scale > 0 and finite.
  * Two launches; lengths and tables are read on the device, so a captured call
  * follows their contents. */
 SV_API size_t paged_attn_workspace_bytes(int B, int M, int Hq, int Hkv, int D);

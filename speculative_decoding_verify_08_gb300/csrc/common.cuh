@@ -50,11 +50,11 @@ inline sv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV
 // memory limit to `smem` first, whatever its size: the default limit covers
 // static and dynamic shared memory together, so a kernel with static arrays
 // can exceed it with less than 48 KB of dynamic memory.
-// `after_own`: the kernel follows another of this library's in the same call
-// and waits for it with griddepcontrol.wait, so it may always be launched
-// while that one drains.
+// `early`: the kernel touches no memory of the caller's before its
+// griddepcontrol.wait, so it is launched while its predecessor drains whatever
+// the flags say.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_after(bool after_own, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+cudaError_t launch_as(bool early, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                          cudaStream_t stream, Args &&...args) {
   if (smem > 0) {
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(kern), smem);
@@ -67,7 +67,7 @@ cudaError_t launch_after(bool after_own, void (*kern)(KArgs...), dim3 grid, dim3
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   cfg.numAttrs = 0;
-  if (after_own || (launch_flags() & SV_LAUNCH_PDL)) {
+  if (early || (launch_flags() & SV_LAUNCH_PDL)) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
@@ -81,7 +81,13 @@ cudaError_t launch_after(bool after_own, void (*kern)(KArgs...), dim3 grid, dim3
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                    cudaStream_t stream, Args &&...args) {
-  return launch_after(false, kern, grid, block, smem, stream, std::forward<Args>(args)...);
+  return launch_as(false, kern, grid, block, smem, stream, std::forward<Args>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_early(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t stream, Args &&...args) {
+  return launch_as(true, kern, grid, block, smem, stream, std::forward<Args>(args)...);
 }
 
 // The same launch with thread-block clusters of `cl` CTAs along x (cl >= 2;

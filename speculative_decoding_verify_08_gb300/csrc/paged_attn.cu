@@ -165,11 +165,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   int *pre = reinterpret_cast<int *>(ring + NST * LY::STAGE);  // pre[b]: chunks before sequence b
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], 2);  // K and V
-      mbar_init(&empty[i], MT);
-    }
+  if (tid < NST) {
+    mbar_init(&full[tid], 2);  // K and V
+    mbar_init(&empty[tid], MT);
     fence_barrier_init();
   }
   pdl_wait();
@@ -200,15 +198,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (tid == 0) pre[P.B] = total;
   __syncthreads();
 
-  const long long units = (long long)total * P.Hkv;
-  const int ctas = gridDim.x;
-  long long per = (units + ctas - 1) / ctas;
-  if (per < P.min_units) per = P.min_units;
-  const long long u0 = lmin(units, per * blockIdx.x), u1 = lmin(units, u0 + per);
+  const int units = total * P.Hkv, ctas = (int)gridDim.x;
+  const int per = imax(P.min_units, (int)(((unsigned)units + (unsigned)ctas - 1) / (unsigned)ctas));
+  const int u0 = (int)lmin(units, (long long)per * blockIdx.x), u1 = (int)lmin(units, (long long)u0 + per);
 
   // sequence of unit u < units
-  auto seq_of = [&](long long u) {
-    const int c = (int)(u / P.Hkv);  // chunk-line position rounded down: same sequence as u
+  auto seq_of = [&](int u) {
+    const int c = u / P.Hkv;  // chunk-line position rounded down: same sequence as u
     int lo = 0, hi = P.B - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -230,12 +226,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t q = 0, parity = 1;
     int slot = 0;
     int b = u0 < u1 ? seq_of(u0) : 0;
-    for (long long u = u0; u < u1 && ok;) {
+    for (int u = u0; u < u1 && ok;) {
       while (pre[b + 1] == pre[b]) ++b;  // (a unit follows: a non-empty sequence exists)
       const int n = pre[b + 1] - pre[b];
-      const long long in = u - (long long)pre[b] * P.Hkv;
-      const int h = (int)(in / n), ka = (int)(in - (long long)h * n);
-      const int kb = (int)lmin(n, ka + (u1 - u));
+      const int in = u - pre[b] * P.Hkv, h = in / n, ka = in - h * n;
+      const int kb = imin(n, ka + (u1 - u));
       const Span s = span_of(P, length_of(P, b));
       const int *row = P.table + (long long)b * P.table_stride;
       auto page_at = [&](int k) {
@@ -251,16 +246,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int m = imin(32, kb - k0);
         const int at = (s.chunk(imin(k0 + lane, kb - 1)) % cpp) * CHUNK;
         for (int i = 0; i < m; ++i, ++q) {
-          if ((q & 1) == turn) {
-          const int pg = __shfl_sync(0xffffffffu, page, i), sl = __shfl_sync(0xffffffffu, at, i);
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], parity, P.err));
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&full[slot], LY::TILE);
-            // a page out of range reads zeros (the copy is clipped to the cache)
-            tma_load_5d(ring + slot * LY::STAGE + (is_v ? LY::TILE : 0), is_v ? &mapV : &mapK, 0, sl, 0, h, pg,
-                        &full[slot], pol);
-          }
+          if ((int)(q & 1) == turn) {
+            const int pg = __shfl_sync(0xffffffffu, page, i), sl = __shfl_sync(0xffffffffu, at, i);
+            ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], parity, P.err));
+            if (!ok) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&full[slot], LY::TILE);
+              // a page out of range reads zeros (the copy is clipped to the cache)
+              tma_load_5d(ring + slot * LY::STAGE + (is_v ? LY::TILE : 0), is_v ? &mapV : &mapK, 0, sl, 0, h, pg,
+                          &full[slot], pol);
+            }
           }
           if (++slot == NST) {
             slot = 0;
@@ -304,26 +299,35 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (!P.by_head && tid == 0) P.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
 
   int b = u0 < u1 ? seq_of(u0) : 0;
-  for (long long u = u0; u < u1;) {
+  for (int u = u0; u < u1;) {
     while (pre[b + 1] == pre[b]) ++b;
     const int n = pre[b + 1] - pre[b];
-    const long long head0 = (long long)pre[b] * P.Hkv;
-    const int h = (int)((u - head0) / n), ka = (int)(u - head0 - (long long)h * n);
-    const int kb = (int)lmin(n, ka + (u1 - u));
+    const int in = u - pre[b] * P.Hkv, h = in / n, ka = in - h * n;
+    const int kb = imin(n, ka + (u1 - u));
     const Span s = span_of(P, length_of(P, b));
     const int L = s.L, p0 = L - P.M;  // position of row 0
     const int lo = first_seen(P, L);
 
     // ---- query rows of this head: r = i*G + j, 128-byte swizzled ----
-    for (int x = tid; x < MT * 16 * (D / 8); x += NCW * 32) {
-      const int r = x / (D / 8), c = x % (D / 8);
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (r < P.R) {
-        const int i = r / P.G, j = r % P.G;
-        v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.q.ptr) +
-                                             ((long long)b * P.M + i) * P.q.token_stride +
-                                             (long long)(h * P.G + j) * P.q.head_stride + 8 * c);
+    constexpr int QN = MT * 16 * (D / 8) / (NCW * 32);  // 16-byte groups a thread
+    constexpr int QB = QN < 4 ? QN : 4;                 // with so many loads in flight
+    const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(P.q.ptr) + (long long)b * P.M * P.q.token_stride +
+                              (long long)h * P.G * P.q.head_stride;
+#pragma unroll 1
+    for (int x0 = tid; x0 < MT * 16 * (D / 8); x0 += QB * NCW * 32) {
+      uint4 qv[QB];
+#pragma unroll
+      for (int k = 0; k < QB; ++k) {
+        const int r = (x0 + k * NCW * 32) / (D / 8), c = x0 % (D / 8);
+        const int i = r / P.G, j = r - i * P.G;
+        qv[k] = r < P.R ? *reinterpret_cast<const uint4 *>(qb + (long long)i * P.q.token_stride +
+                                                           (long long)j * P.q.head_stride + 8 * c)
+                        : make_uint4(0u, 0u, 0u, 0u);
       }
+#pragma unroll
+      for (int k = 0; k < QB; ++k) {
+      const int r = (x0 + k * NCW * 32) / (D / 8), c = x0 % (D / 8);
+      const uint4 v = qv[k];
       uint8_t *tile = qs + (r >> 4) * 16 * D * 2;
       const int rr = r & 15;
       if (!F8) {
@@ -350,6 +354,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t *lo16 = reinterpret_cast<uint32_t *>(tile + swz16(rr, g16));
         uint32_t *hi16 = reinterpret_cast<uint32_t *>(tile + swz16(rr, g16 + 1));
         lo16[t] = w[0], hi16[t] = w[1], lo16[t + 1] = w[2], hi16[t + 1] = w[3];
+      }
       }
     }
     named_barrier(1, NCW * 32);
@@ -605,8 +610,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // the head's first piece names its pieces: CTAs blockIdx.x .. of its last unit
     if (tid == 0 && starts) {
       const int hh = b * P.Hkv + h;
-      const long long last = (long long)pre[b] * P.Hkv + (long long)(h + 1) * n - 1;
-      const int4 d = make_int4(hh, (int)blockIdx.x, ends ? 0 : (int)(last / per) - (int)blockIdx.x + 1, 0);
+      const int last = pre[b] * P.Hkv + (h + 1) * n - 1;
+      const int4 d = make_int4(hh, (int)blockIdx.x, ends ? 0 : last / per - (int)blockIdx.x + 1, 0);
       if (P.by_head)
         P.desc[hh] = d;
       else if (!ends)
@@ -615,70 +620,111 @@ __global__ void __launch_bounds__(THREADS, 1)
     u += kb - ka;
     if (h == P.Hkv - 1 && ends) ++b;
   }
+  pdl_launch_dependents();
 }
 
-// Joins the pieces of the heads that were split: a group of D/4 threads per
-// (row, share of the pieces).  When heads are few (by_head) a block takes one
-// row and its groups share the pieces; else the pieces are few and each
-// group takes a row of its own.
+// Join the pieces of the heads that were split.
 constexpr int JOIN_THREADS = 256;
+constexpr int MAX_CTAS = 256;  // pieces a head can have
 
+__device__ __forceinline__ void store_row(const Params &P, int hh, int r, int col, float4 a, float l) {
+  const int b = hh / P.Hkv, h = hh - b * P.Hkv;
+  const float f = l != 0.f ? (P.vs ? P.vs[h] : 1.f) / l : 0.f;
+  const int i = r / P.G, j = r - i * P.G;
+  *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(P.o.ptr) +
+                             ((long long)b * P.M + i) * P.o.token_stride +
+                             (long long)(h * P.G + j) * P.o.head_stride + col) =
+      make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+}
+// slot of piece i of a head that starts in CTA c: the first CTA's second, the others' first
+__device__ __forceinline__ size_t piece(int c, int i) { return (size_t)(c + i) * 2 + (i == 0 ? 1 : 0); }
+
+// Few heads, each in many pieces: a block per (head, row); a thread per piece
+// works out the weights, then groups of D/4 threads share the pieces' rows,
+// the first rows' loads being under way meanwhile.
 template <int D>
-__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Params P) {
-  constexpr int LPG = D / 4;
-  constexpr int NG = JOIN_THREADS / LPG;
+__global__ void __launch_bounds__(JOIN_THREADS) join_few_kernel(const Params P) {
+  constexpr int LPG = D / 4, NG = JOIN_THREADS / LPG, AHEAD = 10;
   __shared__ float4 part[NG][LPG];
+  __shared__ float wts[MAX_CTAS], red[2][JOIN_THREADS / 32];
   pdl_wait();
   pdl_launch_dependents();
   const int4 d = P.desc[blockIdx.x];
-  const int n = d.z;
+  const int n = d.z, r = blockIdx.y, tid = threadIdx.x;
   if (n == 0) return;
-  const int grp = threadIdx.x / LPG, c = threadIdx.x % LPG;
-  const int r = P.by_head ? (int)blockIdx.y : (int)blockIdx.y * NG + grp;
-  const int step = P.by_head ? NG : 1, first = P.by_head ? grp : 0;
-  const bool have = r < P.R;
-  // piece i: the first CTA's second slot, the others' first
-  auto slot_of = [&](int i) { return (size_t)(d.y + i) * 2 + (i == 0 ? 1 : 0); };
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  float top = -INFINITY, l = 0.f;
-  if (have) {
-    for (int i = 0; i < n; ++i) top = fmaxf(top, P.ml[(slot_of(i) * P.R + r) * 2]);
-    for (int i = 0; i < n; ++i) {
-      const float m = P.ml[(slot_of(i) * P.R + r) * 2];
-      l += m == -INFINITY ? 0.f : ex2_approx(m - top) * P.ml[(slot_of(i) * P.R + r) * 2 + 1];
-    }
-#pragma unroll 4
-    for (int i = first; i < n; i += step) {
-      const float m = P.ml[(slot_of(i) * P.R + r) * 2];
-      const float w = m == -INFINITY ? 0.f : ex2_approx(m - top);
-      const float4 v = *reinterpret_cast<const float4 *>(P.opart + (slot_of(i) * P.R + r) * D + 4 * c);
-      a.x = fmaf(w, v.x, a.x);
-      a.y = fmaf(w, v.y, a.y);
-      a.z = fmaf(w, v.z, a.z);
-      a.w = fmaf(w, v.w, a.w);
-    }
-  }
-  if (P.by_head) {
-    part[grp][c] = a;
-    __syncthreads();
-    if (grp != 0) return;
+  const int grp = tid / LPG, c = tid % LPG;
+  auto load = [&](int i) {
+    return *reinterpret_cast<const float4 *>(P.opart + (piece(d.y, i) * P.R + r) * D + 4 * c);
+  };
+  float4 v[AHEAD];
 #pragma unroll
-    for (int g = 1; g < NG; ++g) {
-      const float4 v = part[g][c];
-      a.x += v.x;
-      a.y += v.y;
-      a.z += v.z;
-      a.w += v.w;
-    }
+  for (int k = 0; k < AHEAD; ++k)
+    v[k] = grp + k * NG < n ? load(grp + k * NG) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float2 x = make_float2(-INFINITY, 0.f);
+  if (tid < n) x = *reinterpret_cast<const float2 *>(P.ml + (piece(d.y, tid) * P.R + r) * 2);
+  float top = x.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((tid & 31) == 0) red[0][tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < JOIN_THREADS / 32; ++w) top = fmaxf(top, red[0][w]);
+  const float w = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top);
+  wts[tid] = w;
+  float l = w * x.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if ((tid & 31) == 0) red[1][tid >> 5] = l;
+  __syncthreads();
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float f, float4 y) {
+    a.x = fmaf(f, y.x, a.x);
+    a.y = fmaf(f, y.y, a.y);
+    a.z = fmaf(f, y.z, a.z);
+    a.w = fmaf(f, y.w, a.w);
+  };
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if (grp + k * NG < n) add(wts[grp + k * NG], v[k]);
+#pragma unroll 4
+  for (int i = grp + AHEAD * NG; i < n; i += NG) add(wts[i], load(i));
+  part[grp][c] = a;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int g = 1; g < NG; ++g) add(1.f, part[g][c]);
+  l = 0.f;
+#pragma unroll
+  for (int k = 0; k < JOIN_THREADS / 32; ++k) l += red[1][k];
+  store_row(P, d.x, r, 4 * c, a, l);
+}
+
+// Many heads: at most one per CTA is split, most in two pieces.  A group of
+// D/4 threads takes a row.
+template <int D>
+__global__ void __launch_bounds__(JOIN_THREADS) join_many_kernel(const Params P) {
+  constexpr int LPG = D / 4, NG = JOIN_THREADS / LPG;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int4 d = P.desc[blockIdx.x];
+  const int n = d.z, r = blockIdx.y * NG + threadIdx.x / LPG, c = threadIdx.x % LPG;
+  if (n == 0 || r >= P.R) return;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 2
+  for (int i = 0; i < n; ++i) {
+    const float2 x = *reinterpret_cast<const float2 *>(P.ml + (piece(d.y, i) * P.R + r) * 2);
+    const float4 v = *reinterpret_cast<const float4 *>(P.opart + (piece(d.y, i) * P.R + r) * D + 4 * c);
+    const float top = fmaxf(m, x.x);
+    const float f = m == -INFINITY ? 0.f : ex2_approx(m - top), w = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top);
+    m = top;
+    l = f * l + w * x.y;
+    a.x = f * a.x + w * v.x;
+    a.y = f * a.y + w * v.y;
+    a.z = f * a.z + w * v.z;
+    a.w = f * a.w + w * v.w;
   }
-  if (!have) return;
-  const int b = d.x / P.Hkv, h = d.x % P.Hkv;
-  const float f = l != 0.f ? (P.vs ? P.vs[h] : 1.f) / l : 0.f;
-  const int i = r / P.G, j = r % P.G;
-  *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(P.o.ptr) +
-                             ((long long)b * P.M + i) * P.o.token_stride +
-                             (long long)(h * P.G + j) * P.o.head_stride + 4 * c) =
-      make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+  store_row(P, d.x, r, 4 * c, a, l);
 }
 
 // 5-D map of a cache: (column, slot, 128-byte group, head, page), box 128
@@ -709,7 +755,7 @@ static cudaError_t launch_main(const CUtensorMap &mk, const CUtensorMap &mv, Par
   // rounds ago for its own (phases are told apart by parity alone).
   constexpr int TURNS = NCW / MT;
   P.stages = imin(MAX_STAGES, (int)((SMEM_LIMIT - fixed) / LY::STAGE)) / TURNS * TURNS & ~1;
-  return launch(paged_kernel<D, F8, MT>, dim3(ctas), dim3(THREADS), fixed + (size_t)P.stages * LY::STAGE, s,
+  return launch_early(paged_kernel<D, F8, MT>, dim3(ctas), dim3(THREADS), fixed + (size_t)P.stages * LY::STAGE, s,
                 mk, mv, P);
 }
 
@@ -728,8 +774,8 @@ static cudaError_t launch_all(bool f8, const CUtensorMap &mk, const CUtensorMap 
   cudaError_t e = f8 ? launch_tiles<D, true>(mk, mv, P, ctas, s) : launch_tiles<D, false>(mk, mv, P, ctas, s);
   if (e != cudaSuccess) return e;
   const int ng = JOIN_THREADS / (D / 4);
-  const dim3 grid(P.by_head ? P.B * P.Hkv : ctas, P.by_head ? P.R : (P.R + ng - 1) / ng);
-  return launch_after(true, join_kernel<D>, grid, dim3(JOIN_THREADS), 0, s, P);
+  return P.by_head ? launch_early(join_few_kernel<D>, dim3(P.B * P.Hkv, P.R), dim3(JOIN_THREADS), 0, s, P)
+                   : launch_early(join_many_kernel<D>, dim3(ctas, (P.R + ng - 1) / ng), dim3(JOIN_THREADS), 0, s, P);
 }
 
 static size_t ws_bytes_for(int sms, int R, int D) {
@@ -746,7 +792,7 @@ extern "C" {
 size_t paged_attn_workspace_bytes(int B, int M, int Hq, int Hkv, int D) {
   if (B < 1 || M < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
   if ((D != 128 && D != 256) || (long long)M * (Hq / Hkv) > paged::MAX_R) return 0;
-  const int sms = device_sm_count();
+  const int sms = imin(device_sm_count(), paged::MAX_CTAS);
   return sms <= 0 ? 0 : paged::ws_bytes_for(sms, M * (Hq / Hkv), D);
 }
 
@@ -766,12 +812,12 @@ sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const int32_t *
   if (cs != SV_OK) return cs;
   if (B > 0 && (!block_table || !kv_lens)) return SV_ERR_INVALID_ARG;
   if (!paged::aligned(block_table, 4) || !paged::aligned(kv_lens, 4)) return SV_ERR_INVALID_ARG;
-  // positions are 32-bit (with room for a window), and so is the line of chunks
+  // positions are 32-bit (with room for a window), and so is the line of units
   const long long cap = (long long)table_width * cache->page_size;
-  if (cap > 0x40000000LL || window > 0x40000000 || cap / paged::CHUNK * imax(B, 1) > 0x7fffffffLL)
+  if (cap > 0x40000000LL || window > 0x40000000 || cap / paged::CHUNK * imax(B, 1) > 0x7fffffffLL / Hkv)
     return SV_ERR_UNSUPPORTED;
   if (B == 0) return SV_OK;
-  const int sms = device_sm_count();
+  const int sms = imin(device_sm_count(), paged::MAX_CTAS);
   if (sms <= 0) return SV_ERR_CUDA;
   const int R = M * G;
   if (!workspace || ws_bytes < paged::ws_bytes_for(sms, R, D)) return SV_ERR_WORKSPACE;

@@ -6,16 +6,19 @@
 //   (u, v) <- (u cos a - v sin a, u sin a + v cos a),  a = position * inv_freq[pair]
 // computed in fp32 and rounded once.
 //
-// What bounds it: every row is read once and written once (about 60 fp32
-// instructions per 16 bytes read), so HBM at many tokens and the launch at
-// few.  Hence:
-//  * Rows are taken in (token, head) order, D/8 lanes a row, so a block's
-//    rows are a run of memory and consecutive blocks stream it; each thread
-//    has the loads of its U rows in flight before it computes.
-//  * A lane of a half-split rotation holds four elements of the first half and
-//    their four partners of the second, so a pair never leaves its lane.
-//  * The sines of a block's few tokens are made once, in shared memory, while
-//    the rows' loads are in flight, and serve all heads.
+// What bounds it: every row is read once and written once, so HBM at many
+// tokens (if the instructions per byte stay few) and the launch at few.  Hence:
+//  * A thread keeps one head and takes it at N consecutive tokens: the head's
+//    kind, weights and strides are worked out once, a row costs one address
+//    step, and the N rows' loads are all in flight before anything is computed.
+//    A block holds neighbouring heads, so its loads of a token are one run of
+//    memory.
+//  * D/(2V) lanes share a row.  A lane of a half-split rotation holds V elements of
+//    the first half and their V partners of the second, so that a pair never
+//    leaves its lane; V = 8 (16-byte accesses) unless rot_dim is no multiple
+//    of 16 (V = 4).
+//  * The sines of a block's tokens are made once, in shared memory, while the
+//    rows' loads are in flight, and serve all its heads.
 //  * The angle is an integer: position times a 64-bit fraction of a turn wraps
 //    at whole turns by itself, so a far position loses nothing and no 64-bit
 //    floating-point arithmetic is needed.
@@ -28,7 +31,7 @@
 namespace sv {
 namespace rope {
 
-constexpr int THREADS = 256;
+constexpr int MAX_THREADS = 256;
 
 enum Kind { TO_ROWS = 0, TO_BF16_PAGES = 1, TO_E4M3_PAGES = 2 };
 
@@ -50,8 +53,7 @@ struct Params {
   long long page_stride, slot_stride, head_stride, num_slots;
   int page_size;
   int T, Hq, Hkv, H;  // H: rows per token (queries, keys, values)
-  unsigned magic;     // ceil(2^32 / H)
-  int span;           // tokens that a block's rows can touch
+  int gh;             // heads per block
   unsigned *err;
 };
 
@@ -71,165 +73,185 @@ __device__ __forceinline__ float2 turn(int pos, unsigned long long phase) {
   return make_float2(c, s);
 }
 
-// U rows per thread: 4 when the rows fill the GPU several times over (four
-// 16-byte loads in flight a thread), else 1 (the rows spread over more SMs).
-template <int D, int KIND, int U>
-__global__ void __launch_bounds__(THREADS) rope_kernel(const Params P) {
-  constexpr int LPR = D / 8;           // lanes per row
-  constexpr int RPP = THREADS / LPR;   // rows per pass
-  extern __shared__ __align__(16) uint8_t smem[];
-  float *wt = reinterpret_cast<float *>(smem);                         // [2][D] weights
-  long long *dst = reinterpret_cast<long long *>(smem + 2 * D * 4);    // [span] element, or -1
-  float2 *cs = reinterpret_cast<float2 *>(dst + (P.span + 1) / 2 * 2);  // [span][rot/2]
+__device__ __forceinline__ void unpack(float *y, uint4 v) {
+  y[0] = bf16lo(v.x), y[1] = bf16hi(v.x), y[2] = bf16lo(v.y), y[3] = bf16hi(v.y);
+  y[4] = bf16lo(v.z), y[5] = bf16hi(v.z), y[6] = bf16lo(v.w), y[7] = bf16hi(v.w);
+}
+__device__ __forceinline__ void unpack(float *y, uint2 v) {
+  y[0] = bf16lo(v.x), y[1] = bf16hi(v.x), y[2] = bf16lo(v.y), y[3] = bf16hi(v.y);
+}
+__device__ __forceinline__ void store_bf16(char *p, const float (&y)[8]) {
+  *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                             pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+}
+__device__ __forceinline__ void store_bf16(char *p, const float (&y)[4]) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+}
+__device__ __forceinline__ void store_e4m3(char *p, const float (&y)[8]) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(e4m3x4(y), e4m3x4(y + 4));
+}
+__device__ __forceinline__ void store_e4m3(char *p, const float (&y)[4]) {
+  *reinterpret_cast<uint32_t *>(p) = e4m3x4(y);
+}
+
+template <int V>
+struct Group;
+template <>
+struct Group<8> {
+  using type = uint4;
+};
+template <>
+struct Group<4> {
+  using type = uint2;
+};
+
+template <int D, int KIND, int V, int N>
+__global__ void __launch_bounds__(MAX_THREADS) rope_kernel(const Params P) {
+  using G = typename Group<V>::type;
+  constexpr int LPR = D / (2 * V);  // lanes per row
+  extern __shared__ __align__(16) float2 cs[];  // [N][rot/2] cosine and sine
+  __shared__ long long dst[N];                  // element of the token's slot, or -1
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, lane = tid % LPR;
-  const unsigned total = (unsigned)P.T * (unsigned)P.H;
-  const unsigned r0 = blockIdx.x * (unsigned)(RPP * U);
-  const int tok0 = (int)(r0 / (unsigned)P.H);
-  const int h0 = (int)(r0 - (unsigned)tok0 * (unsigned)P.H);
-  const bool rotates = lane < P.rot / 8;
-  // first elements of this lane's two groups of four
-  const int off0 = (P.split && rotates) ? 4 * lane : 8 * lane;
-  const int off1 = (P.split && rotates) ? P.rot / 2 + 4 * lane : 8 * lane + 4;
+  const int tid = threadIdx.x, lane = tid % LPR, grp = tid / LPR;
+  const int head = blockIdx.y * P.gh + grp;
+  const bool active = grp < P.gh && head < P.H;
+  const int tok0 = blockIdx.x * N;
+  const bool isq = head < P.Hq, isv = head >= P.Hq + P.Hkv;
+  const int h = isq ? head : isv ? head - P.Hq - P.Hkv : head - P.Hq;
+  const bool rotates = lane < P.rot / (2 * V);
+  // first elements of this lane's two groups of V
+  const int off0 = (P.split && rotates) ? V * lane : 2 * V * lane;
+  const int off1 = (P.split && rotates) ? P.rot / 2 + V * lane : 2 * V * lane + V;
 
-  uint2 a[U], b[U];
-  int tl[U], hd[U];
-  bool have[U];
+  G a[N], b[N];
+  {
+    const Rows src = isq ? P.q : isv ? P.v : P.k;
+    const char *x = src.p + 2 * ((long long)tok0 * src.ts + (long long)h * src.hs);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int local = tid / LPR + u * RPP;
-    have[u] = r0 + (unsigned)local < total;
-    tl[u] = (int)__umulhi((unsigned)(h0 + local), P.magic);
-    hd[u] = h0 + local - tl[u] * P.H;
-    a[u] = b[u] = make_uint2(0u, 0u);
-    if (have[u]) {
-      const Rows &src = hd[u] < P.Hq ? P.q : hd[u] < P.Hq + P.Hkv ? P.k : P.v;
-      const int h = hd[u] < P.Hq ? hd[u] : hd[u] < P.Hq + P.Hkv ? hd[u] - P.Hq : hd[u] - P.Hq - P.Hkv;
-      const char *x = src.p + 2 * ((long long)(tok0 + tl[u]) * src.ts + (long long)h * src.hs);
-      if (P.split) {
-        a[u] = *reinterpret_cast<const uint2 *>(x + 2 * off0);
-        b[u] = *reinterpret_cast<const uint2 *>(x + 2 * off1);
-      } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(x + 16 * lane);
-        a[u] = make_uint2(v.x, v.y);
-        b[u] = make_uint2(v.z, v.w);
+    for (int i = 0; i < N; ++i) {
+      a[i] = b[i] = G{};
+      if (active && tok0 + i < P.T) {
+        a[i] = *reinterpret_cast<const G *>(x + 2 * off0);
+        b[i] = *reinterpret_cast<const G *>(x + 2 * off1);
       }
+      x += 2 * src.ts;
     }
+  }
+  const __nv_bfloat16 *weight = isv ? nullptr : isq ? P.qw : P.kw;
+  float w0[V], w1[V];
+  if (active && weight) {
+    unpack(w0, *reinterpret_cast<const G *>(weight + off0));
+    unpack(w1, *reinterpret_cast<const G *>(weight + off1));
+#pragma unroll
+    for (int i = 0; i < V; ++i) w0[i] += P.offset, w1[i] += P.offset;
   }
 
-  const int ntok = imin(P.span, P.T - tok0);
   const int half = P.rot / 2;
-  for (int i = tid; i < ntok * half; i += THREADS) {
-    const int t = i / half;
-    cs[i] = turn(P.positions[tok0 + t], P.phases[i - t * half]);
+#pragma unroll
+  for (int t = 0; t < N; ++t) {
+    if (tok0 + t >= P.T) break;
+    const int pos = half ? P.positions[tok0 + t] : 0;
+    for (int i = tid; i < half; i += blockDim.x) cs[t * half + i] = turn(pos, P.phases[i]);
   }
-  for (int i = tid; i < 2 * D; i += THREADS) {
-    const __nv_bfloat16 *w = i < D ? P.qw : P.kw;
-    wt[i] = w ? __bfloat162float(w[i % D]) + P.offset : 1.f;
-  }
-  if (KIND != TO_ROWS) {
-    for (int i = tid; i < ntok; i += THREADS) {
-      const long long s = P.slots[tok0 + i];
-      long long e = -1;
-      if (s >= P.num_slots) {
-        atomicOr(P.err, ERR_INDEX);
-      } else if (s >= 0) {
-        const long long page = P.num_slots <= 0xFFFFFFFFLL ? (long long)((unsigned)s / (unsigned)P.page_size)
-                                                           : s / P.page_size;
-        e = page * P.page_stride + (s - page * P.page_size) * P.slot_stride;
-      }
-      dst[i] = e;
+  if (KIND != TO_ROWS && tid < N && tok0 + tid < P.T) {
+    const long long s = P.slots[tok0 + tid];
+    long long e = -1;
+    if (s >= P.num_slots) {
+      atomicOr(P.err, ERR_INDEX);
+    } else if (s >= 0) {
+      const long long page = P.num_slots <= 0xFFFFFFFFLL ? (long long)((unsigned)s / (unsigned)P.page_size)
+                                                         : s / P.page_size;
+      e = page * P.page_stride + (s - page * P.page_size) * P.slot_stride;
     }
+    dst[tid] = e;
   }
   __syncthreads();
 
+  const bool to_pages = KIND != TO_ROWS && !isq;
+  const Rows to = isq ? P.qo : P.ko;
+  char *out = to_pages ? (isv ? P.vc : P.kc) + (KIND == TO_E4M3_PAGES ? 1 : 2) * ((long long)h * P.head_stride)
+                       : to.p + 2 * ((long long)tok0 * to.ts + (long long)h * to.hs);
+  float inv = 1.f;
+  if (KIND == TO_E4M3_PAGES && active && to_pages) {
+    const float *sp = isv ? P.vs : P.ks;
+    if (sp) inv = 1.f / sp[h];
+  }
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const bool isq = hd[u] < P.Hq, isv = hd[u] >= P.Hq + P.Hkv;
-    float y[8] = {bf16lo(a[u].x), bf16hi(a[u].x), bf16lo(a[u].y), bf16hi(a[u].y),
-                  bf16lo(b[u].x), bf16hi(b[u].x), bf16lo(b[u].y), bf16hi(b[u].y)};
+  for (int i = 0; i < N; ++i) {
+    float u[V], v[V];
+    unpack(u, a[i]);
+    unpack(v, b[i]);
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+    for (int e = 0; e < V; ++e) ss = fmaf(u[e], u[e], fmaf(v[e], v[e], ss));
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!have[u]) continue;
-    if (!isv) {
-      if (isq ? P.qw != nullptr : P.kw != nullptr) {
-        const float r = rsqrtf(fmaf(ss, 1.f / D, P.eps));
-        const float *w = wt + (isq ? 0 : D);
-        const float4 w0 = *reinterpret_cast<const float4 *>(w + off0);
-        const float4 w1 = *reinterpret_cast<const float4 *>(w + off1);
-        y[0] *= r * w0.x, y[1] *= r * w0.y, y[2] *= r * w0.z, y[3] *= r * w0.w;
-        y[4] *= r * w1.x, y[5] *= r * w1.y, y[6] *= r * w1.z, y[7] *= r * w1.w;
-      }
-      if (rotates) {
-        const float4 *t = reinterpret_cast<const float4 *>(cs + tl[u] * half + 4 * lane);
-        const float4 c01 = t[0], c23 = t[1];  // (cos, sin) of four pairs
-        const float c[4] = {c01.x, c01.z, c23.x, c23.z}, s[4] = {c01.y, c01.w, c23.y, c23.w};
-        float z[8];
+    if (!active || tok0 + i >= P.T) continue;
+    if (weight) {
+      const float r = rsqrtf(fmaf(ss, 1.f / D, P.eps));
+#pragma unroll
+      for (int e = 0; e < V; ++e) u[e] *= r * w0[e], v[e] *= r * w1[e];
+    }
+    if (rotates && !isv) {
+      const float4 *t = reinterpret_cast<const float4 *>(cs + i * half + V * lane);
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {  // (cos, sin) of two pairs
+        const float4 c = t[e];
         if (P.split) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            z[i] = y[i] * c[i] - y[4 + i] * s[i];
-            z[4 + i] = y[i] * s[i] + y[4 + i] * c[i];
-          }
+          const float u0 = u[2 * e], u1 = u[2 * e + 1], v0 = v[2 * e], v1 = v[2 * e + 1];
+          u[2 * e] = u0 * c.x - v0 * c.y;
+          v[2 * e] = u0 * c.y + v0 * c.x;
+          u[2 * e + 1] = u1 * c.z - v1 * c.w;
+          v[2 * e + 1] = u1 * c.w + v1 * c.z;
         } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            z[2 * i] = y[2 * i] * c[i] - y[2 * i + 1] * s[i];
-            z[2 * i + 1] = y[2 * i] * s[i] + y[2 * i + 1] * c[i];
-          }
+          float *y = e < V / 4 ? u : v;
+          const int k = e < V / 4 ? 4 * e : 4 * e - V;
+          const float y0 = y[k], y1 = y[k + 1], y2 = y[k + 2], y3 = y[k + 3];
+          y[k] = y0 * c.x - y1 * c.y;
+          y[k + 1] = y0 * c.y + y1 * c.x;
+          y[k + 2] = y2 * c.z - y3 * c.w;
+          y[k + 3] = y2 * c.w + y3 * c.z;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = z[i];
       }
     }
-    char *out;
-    if (isq || KIND == TO_ROWS) {
-      const Rows &d = isq ? P.qo : P.ko;
-      out = d.p + 2 * ((long long)(tok0 + tl[u]) * d.ts + (long long)(isq ? hd[u] : hd[u] - P.Hq) * d.hs);
-    } else {
-      const long long e = dst[tl[u]];
+    if (to_pages) {
+      const long long e = dst[i];
       if (e < 0) continue;
-      const int h = isv ? hd[u] - P.Hq - P.Hkv : hd[u] - P.Hq;
-      out = (isv ? P.vc : P.kc) + (KIND == TO_E4M3_PAGES ? 1 : 2) * (e + (long long)h * P.head_stride);
       if (KIND == TO_E4M3_PAGES) {
-        const float *sp = isv ? P.vs : P.ks;
-        const float inv = sp ? 1.f / sp[h] : 1.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] *= inv;
-        *reinterpret_cast<uint32_t *>(out + off0) = e4m3x4(y);
-        *reinterpret_cast<uint32_t *>(out + off1) = e4m3x4(y + 4);
-        continue;
+        for (int j = 0; j < V; ++j) u[j] *= inv, v[j] *= inv;
+        store_e4m3(out + e + off0, u);
+        store_e4m3(out + e + off1, v);
+      } else {
+        store_bf16(out + 2 * (e + off0), u);
+        store_bf16(out + 2 * (e + off1), v);
       }
-    }
-    const uint2 z0 = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-    const uint2 z1 = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-    if (P.split) {
-      *reinterpret_cast<uint2 *>(out + 2 * off0) = z0;
-      *reinterpret_cast<uint2 *>(out + 2 * off1) = z1;
     } else {
-      *reinterpret_cast<uint4 *>(out + 16 * lane) = make_uint4(z0.x, z0.y, z1.x, z1.y);
+      store_bf16(out + 2 * (i * to.ts + off0), u);
+      store_bf16(out + 2 * (i * to.ts + off1), v);
     }
   }
 }
 
-template <int D, int KIND, int U>
-static cudaError_t launch_u(Params &P, cudaStream_t s) {
-  constexpr int RB = THREADS / (D / 8) * U;
-  P.span = imin((RB - 1) / P.H + 2, P.T);
-  const unsigned total = (unsigned)P.T * (unsigned)P.H;
-  const size_t smem = 2 * D * 4 + (size_t)(P.span + 1) / 2 * 16 + (size_t)P.span * (P.rot / 2) * 8;
-  return launch(rope_kernel<D, KIND, U>, dim3((total + RB - 1) / RB), dim3(THREADS), smem, s, P);
+template <int D, int KIND, int V, int N>
+static cudaError_t launch_n(Params &P, cudaStream_t s) {
+  constexpr int LPR = D / (2 * V);
+  // heads per block: the rows of about 256 threads, evenly over the blocks of a token
+  const int most = 256 / LPR, blocks = (P.H + most - 1) / most;
+  P.gh = (P.H + blocks - 1) / blocks;
+  const int threads = (P.gh * LPR + 31) / 32 * 32;
+  return launch_early(rope_kernel<D, KIND, V, N>, dim3((P.T + N - 1) / N, blocks), dim3(threads),
+                (size_t)N * (P.rot / 2) * sizeof(float2), s, P);
 }
 
+// Four tokens a thread when the blocks fill the GPU several times over (four
+// rows' loads in flight), else one (rows spread over more SMs).
 template <int D, int KIND>
 static cudaError_t launch_kind(Params &P, int sms, cudaStream_t s) {
-  const long long rows = (long long)P.T * P.H;
-  const long long pass = THREADS / (D / 8);
-  return rows > 8 * pass * sms ? launch_u<D, KIND, 4>(P, s) : launch_u<D, KIND, 1>(P, s);
+  if (P.rot % 16 != 0) return launch_n<D, KIND, 4, 1>(P, s);
+  const long long lanes = (long long)P.T * P.H * (D / 16);
+  return lanes > 4LL * 2048 * sms ? launch_n<D, KIND, 8, 4>(P, s) : launch_n<D, KIND, 8, 1>(P, s);
 }
 
 template <int D>
@@ -277,7 +299,6 @@ static sv_status run(Params &P, int D, int kind, int T, int Hq, int Hkv, int H, 
   P.Hq = Hq;
   P.Hkv = Hkv;
   P.H = H;
-  P.magic = (unsigned)((0x100000000ULL + (unsigned)H - 1) / (unsigned)H);
   return from_cuda(D == 64 ? launch_d<64>(P, kind, sms, s)
                    : D == 128 ? launch_d<128>(P, kind, sms, s)
                               : launch_d<256>(P, kind, sms, s));

@@ -541,7 +541,7 @@ static sv_status run(const sv_rows *q, const sv_rows *k, const sv_rows *v, Param
   // at most one item more per sequence than the rows fill
   const long long items = ((long long)P.Tq / (P.PT * C::NT) + P.B) * P.Hkv;
   const int ctas = (int)lmin(items, sms);
-  return from_cuda(launch(window_kernel<D>, dim3(ctas), dim3(C::THREADS), fixed + (size_t)P.slots * SLOT, s, mq, mk,
+  return from_cuda(launch_early(window_kernel<D>, dim3(ctas), dim3(C::THREADS), fixed + (size_t)P.slots * SLOT, s, mq, mk,
                           mv, P));
 }
 
