@@ -18,7 +18,8 @@
 //    runs, and each K/V block of 128 keys is fetched once for both.
 //    D = 256: O alone takes half of tensor memory, so a CTA carries one tile
 //    with two S buffers over blocks of 64 keys: S of the next block is
-//    computed during the softmax of this one.
+//    computed during the softmax of this one, whose rows two threads share
+//    (half of the keys each; they exchange one maximum a block).
 //  * Only blocks that some row of the CTA's tiles sees are visited.  One warp
 //    streams K and V blocks with TMA into a ring of 32 KB slots, another
 //    fetches the next tiles' queries as soon as the last S product is done.
@@ -38,18 +39,20 @@ constexpr int ROWS = 128;           // rows of a tile (TMEM lanes)
 constexpr int MAX_B = 4096;
 constexpr float RESCALE = 8.f;      // log2 of the largest P against an old maximum
 constexpr int SLOT = 32768;         // bytes of a K or V block
-constexpr size_t SMEM_LIMIT = 227 * 1024;
+// Shared memory: barriers, scan totals (256), halves' exchange (512), prefix
+// sums (2560; after the ring if longer), then the query tiles and the ring.
+constexpr int HEADER = 3072, PREFIX = 2560;
 
 template <int D>
 struct Cfg {
   static constexpr int NT = D == 128 ? 2 : 1;   // tiles per CTA
   static constexpr int NSB = D == 128 ? 1 : 2;  // S buffers per tile
   static constexpr int BN = D == 128 ? 128 : 64;  // keys per block
-  static constexpr int SOFT = 4 * NT;           // softmax warps
+  static constexpr int SOFT = 8;                // softmax warps
+  static constexpr int HALVES = D == 128 ? 1 : 2;  // threads that share a row
   static constexpr int THREADS = (SOFT + 4) * 32;
   static constexpr int QBYTES = ROWS * D * 2;
-  static constexpr int QS = 1024;
-  static constexpr int RING = QS + NT * QBYTES;
+  static constexpr int RING = HEADER + NT * QBYTES;
   static_assert(BN * D * 2 == SLOT, "block");
   // tensor memory: O per tile, then the S buffers (P over S)
   static constexpr uint32_t TO = 0, TS = NT * D;
@@ -136,7 +139,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   using C = Cfg<D>;
   constexpr int NT = C::NT, NSB = C::NSB, BN = C::BN;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *smem = smem_raw;
+  // The swizzled tiles need 1024-byte alignment, which the first dynamic byte
+  // has in a kernel without static shared memory; five slots leave no room to
+  // round up.
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(P.err, ERR_TIMEOUT);
+    return;
+  }
   uint64_t *full = reinterpret_cast<uint64_t *>(smem);  // ring slots (at most 5)
   uint64_t *empty = full + 5;
   uint64_t *s_full = empty + 5;    // [2] per S buffer
@@ -147,11 +157,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   uint64_t *q_free = q_full + 1;   // last S product of the item done
   uint64_t *idle = q_free + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(idle + 1);
-  int *wsum = reinterpret_cast<int *>(smem + 512);
-  uint8_t *qs = smem + C::QS;
+  int *wsum = reinterpret_cast<int *>(smem + 256);
+  float *xchg = reinterpret_cast<float *>(smem + 512);  // [2][2 halves][ROWS] maxima, then sums
+  uint8_t *qs = smem + HEADER;
   uint8_t *ring = smem + C::RING;
   const int NS = P.slots;
-  int *pre = reinterpret_cast<int *>(ring + (size_t)NS * SLOT);
+  int *pre = reinterpret_cast<int *>(NS == 5 ? smem + PREFIX : ring + (size_t)NS * SLOT);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -161,9 +172,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 4 * C::HALVES);
       mbar_init(&o_done[i], 1);
-      mbar_init(&o_free[i], 4);
+      mbar_init(&o_free[i], 4 * C::HALVES);
     }
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
@@ -218,7 +229,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 
   if (warp >= C::SOFT) {
     // 384 threads start with 168 registers each: 128*72 + 256*216 is the same total
-    if (D == 128) setmaxnreg_dec<72>();
+    setmaxnreg_dec<72>();
     if (warp == C::SOFT + 1) {
       // ------------------------------------------- K and V blocks --
       if (lane == 0) {
@@ -270,7 +281,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       // ------------------------------------------------- MMA issuer --
       constexpr uint32_t IDS = tc::idesc_bf16_f32(ROWS, BN, false);
       constexpr uint32_t IDO = tc::idesc_bf16_f32(ROWS, D, true);
-      const uint32_t qs_a = smem_u32(qs), ring_a = smem_u32(ring);
+      // descriptors: queries and keys K-major, values with rows along K
+      const uint64_t dq = tc::smem_desc_sw128(smem_u32(qs), 16, 1024), dk = tc::smem_desc_sw128(smem_u32(ring), 16, 1024);
+      const uint64_t dv = tc::smem_desc_sw128(smem_u32(ring), BN * 128, 1024);
+      const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32), k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32);
+      const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
+      // warp-uniform, so that the products' operands stay in uniform registers
+      const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
+      const bool leader = tc::elect_one();
       bool ok = true;
       uint32_t q = 0;                 // ring position of the item's first block
       uint32_t c = 0;                 // items with work so far
@@ -280,45 +298,47 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (ok) ok = spin_wait(bar, parity, P.err);
         ok = __all_sync(0xffffffffu, ok);
       };
-      auto issue_s = [&](int t, uint32_t slot) {  // lane 0
-        const uint32_t sb = NSB == 2 ? (sj[t] & 1) : (uint32_t)t;
-        const uint32_t kb = ring_a + slot * SLOT, qa = qs_a + t * C::QBYTES;
+      auto issue_s = [&](int t, uint32_t sb, uint32_t slot) {  // the leader
+        const uint32_t ka = k_lo + slot * (SLOT / 16), d = tb + C::TS + sb * BN;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks & 3) * 32;
-          tc::mma_bf16(tbase + C::TS + sb * BN, tc::smem_desc_sw128(qa + (ks >> 2) * ROWS * 128 + off, 16, 1024),
-                       tc::smem_desc_sw128(kb + (ks >> 2) * BN * 128 + off, 16, 1024), IDS, ks > 0);
-        }
+        for (int ks = 0; ks < D / 16; ++ks)
+          tc::mma_bf16(d, q_lo + (t * C::QBYTES + (ks >> 2) * ROWS * 128 + (ks & 3) * 32) / 16, q_hi,
+                       ka + ((ks >> 2) * BN * 128 + (ks & 3) * 32) / 16, k_hi, IDS, ks > 0);
         tc::commit(&s_full[sb]);
       };
       for (int k = 0; k < rounds && ok; ++k) {
         const int id = item_id(k, items);
         if (id < 0) continue;
         const Item it = item_at<D>(P, pre, id);
-        if (it.n == 0) continue;
-        const int nt = it.rows > P.PT ? NT : 1;
+        const int n = __shfl_sync(0xffffffffu, it.n, 0);
+        if (n == 0) continue;
+        const int nt = __shfl_sync(0xffffffffu, it.rows > P.PT ? NT : 1, 0);
         wait(q_full, c & 1);
         ++c;
         wait(&full[q % NS], (q / NS) & 1);
         if (!ok) break;
         tc::fence_after_sync();
-        if (lane == 0) {
-          for (int t = 0; t < nt; ++t) issue_s(t, q % NS);
+        if (leader) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            if (t < nt) issue_s(t, NSB == 2 ? (sj[0] & 1) : (uint32_t)t, q % NS);
           tc::commit(&empty[q % NS]);
-          if (it.n == 1) tc::commit(q_free);
+          if (n == 1) tc::commit(q_free);
         }
-        for (int t = 0; t < nt; ++t) ++sj[t];
-        for (int j = 0; j < it.n && ok; ++j) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          if (t < nt) ++sj[t];
+        for (int j = 0; j < n && ok; ++j) {
           const uint32_t qv = q + 2 * j + 1, qk = qv + 1;
-          const bool more = j + 1 < it.n;
+          const bool more = j + 1 < n;
           if (NSB == 2 && more) {  // the next S runs during this block's softmax
             wait(&full[qk % NS], (qk / NS) & 1);
             if (!ok) break;
             tc::fence_after_sync();
-            if (lane == 0) {
-              issue_s(0, qk % NS);
+            if (leader) {
+              issue_s(0, sj[0] & 1, qk % NS);
               tc::commit(&empty[qk % NS]);
-              if (j + 2 == it.n) tc::commit(q_free);
+              if (j + 2 == n) tc::commit(q_free);
             }
             ++sj[0];
           }
@@ -336,25 +356,27 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             __syncwarp();
           }
           if (NSB == 1 && more) wait(&full[qk % NS], (qk / NS) & 1);
-          for (int t = 0; t < nt && ok; ++t) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (t >= nt || !ok) continue;
             const uint32_t sb = NSB == 2 ? (pj[t] & 1) : (uint32_t)t;
             if (j == 0 && oc[t] > 0) wait(&o_free[t], (oc[t] - 1) & 1);
             wait(&p_full[sb], (NSB == 2 ? pj[t] >> 1 : pj[t]) & 1);
-            if (!ok) break;
+            if (!ok) continue;
             tc::fence_after_sync();
-            if (lane == 0) {
-              const uint32_t vb = ring_a + (qv % NS) * SLOT;
+            if (leader) {
+              const uint32_t va = v_lo + (qv % NS) * (SLOT / 16);
 #pragma unroll
               for (int ks = 0; ks < BN / 16; ++ks)
-                tc::mma_bf16_ts(tbase + C::TO + t * D, tbase + C::TS + sb * BN + ks * 8,
-                                tc::smem_desc_sw128(vb + ks * 2048, BN * 128, 1024), IDO, j > 0 || ks > 0);
+                tc::mma_bf16_ts(tb + C::TO + t * D, tb + C::TS + sb * BN + ks * 8, va + ks * 2048 / 16, v_hi, IDO,
+                                ks > 0 ? 1u : (uint32_t)j);
               tc::commit(&o_done[sb]);
               if (t == nt - 1) tc::commit(&empty[qv % NS]);
               if (NSB == 1 && more) {
-                issue_s(t, qk % NS);
+                issue_s(t, (uint32_t)t, qk % NS);
                 if (t == nt - 1) {
                   tc::commit(&empty[qk % NS]);
-                  if (j + 2 == it.n) tc::commit(q_free);
+                  if (j + 2 == n) tc::commit(q_free);
                 }
               }
             }
@@ -362,11 +384,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             if (NSB == 1 && more) ++sj[t];
           }
         }
-        for (int t = 0; t < nt; ++t) ++oc[t];
-        q += 2 * it.n;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          if (t < nt) ++oc[t];
+        q += 2 * n;
         __syncwarp();
       }
-      if (lane == 0) {  // every product issued above has completed before TMEM is released
+      if (leader) {  // every product issued above has completed before TMEM is released
         tc::commit(idle);
         spin_wait(idle, 0, P.err);
       }
@@ -374,13 +398,17 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     }
   } else {
     // ------------------------------------------------------ softmax --
-    if (D == 128) setmaxnreg_inc<216>();
-    const int t = warp >> 2;                    // tile
+    setmaxnreg_inc<216>();
+    constexpr int HALVES = C::HALVES, COLS = BN / HALVES;  // keys of a block that are this thread's
+    const int t = HALVES == 1 ? warp >> 2 : 0;  // tile
+    const int hf = HALVES == 1 ? 0 : warp >> 2;  // half of a block's keys, and of O's columns
     const int r = (warp & 3) * 32 + lane;       // row = TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const int ir = r / P.G, jr = r % P.G;       // position and query head in the tile
     const float sl2e = P.sl2e;
+    const f2 scale2 = pack2(sl2e, sl2e);
     const uint32_t tO = tbase + C::TO + t * D + lane_off;
+    constexpr int O0 = D / HALVES;
     bool ok = true;
     uint32_t cnt = 0;  // blocks of this tile so far
     // The second product of the latest block.  The barrier's phase before it
@@ -391,6 +419,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       if (ok) ok = spin_wait(&o_done[NSB == 2 ? (at & 1) : (uint32_t)t], (NSB == 2 ? at >> 1 : at) & 1, P.err);
       ok = __all_sync(0xffffffffu, ok);
     };
+    // The two halves of a row trade a value; slots alternate, so that one
+    // barrier a trade is enough.
+    uint32_t trades = 0;
+    auto trade = [&](float x) {
+      float *at = xchg + (trades & 1) * 2 * ROWS;
+      ++trades;
+      at[hf * ROWS + r] = x;
+      named_barrier(2 + (warp & 3), 64);
+      return at[(hf ^ 1) * ROWS + r];
+    };
     for (int k = 0; k < rounds; ++k) {
       const int id = item_id(k, items);
       if (id < 0) continue;
@@ -400,27 +438,46 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const int pt = it.p0 + t * P.PT, p = pt + ir;            // position of the tile's first row, of this one
       const int plast = it.p0 + imin(it.rows, (t + 1) * P.PT) - 1;
       float m = -INFINITY, l = 0.f;
+      // Both halves of a row take part in every trade whatever `ok` says (the
+      // barriers have no time limit); after a wait that ran out only the work
+      // is skipped.
       for (int j = 0; j < it.n; ++j, ++cnt) {
         const uint32_t sb = NSB == 2 ? (cnt & 1) : (uint32_t)t;
-        const uint32_t tS = tbase + C::TS + sb * BN + lane_off;
+        const uint32_t tS = tbase + C::TS + sb * BN + hf * COLS + lane_off;
         if (ok) ok = spin_wait(&s_full[sb], (NSB == 2 ? cnt >> 1 : cnt) & 1, P.err);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
         tc::fence_after_sync();
-        uint32_t raw[BN / 32][32];
+        uint32_t raw[COLS / 32][32];
+        if (ok) {
 #pragma unroll
-        for (int c = 0; c < BN / 32; ++c) tc::ld32(tS + 32 * c, raw[c]);
-        tc::wait_ld();
+          for (int c = 0; c < COLS / 32; ++c) tc::ld32(tS + 32 * c, raw[c]);
+          tc::wait_ld();
+        }
         const int base = it.block(j) * BN;
         if (base + BN - 1 > pt || (P.window > 0 && base <= plast - P.window && base + BN > P.sinks)) {
-          const int hi = p - base, lo = P.window > 0 ? hi - P.window : -1, sk = P.sinks - base;
+          // key c of the block is seen iff c <= hi and (c > lo or c < sk)
+          const int at = base + hf * COLS, hi = p - at, lo = P.window > 0 ? hi - P.window : -1, sk = P.sinks - at;
 #pragma unroll
-          for (int c = 0; c < BN; ++c)
-            if (c > hi || (c <= lo && c >= sk)) raw[c / 32][c % 32] = 0xFF800000u;  // -inf
+          for (int c = 0; c < COLS / 32; ++c) {
+            auto below = [&](int n) {  // bits 0..n-1 of this group of 32
+              const int b = n - 32 * c;
+              return b <= 0 ? 0u : b >= 32 ? 0xFFFFFFFFu : (1u << b) - 1u;
+            };
+            const uint32_t seen = below(hi + 1) & (~below(lo + 1) | below(sk));
+#pragma unroll
+            for (int e = 0; e < 32; ++e) raw[c][e] = (seen >> e & 1u) ? raw[c][e] : 0xFF800000u;  // -inf
+          }
         }
-        float mx = -INFINITY;
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < BN; ++c) mx = fmaxf(mx, __uint_as_float(raw[c / 32][c % 32]));
+        for (int c = 0; c < COLS / 32; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mx4[i] = fmaxf(mx4[i], fmaxf(__uint_as_float(raw[c][e + i]), __uint_as_float(raw[c][e + 4 + i])));
+        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        if (HALVES == 2) mx = fmaxf(mx, trade(mx));
         mx *= sl2e;
         float alpha = 1.f;
         if (mx > m + RESCALE) {
@@ -430,35 +487,43 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           // the previous block's product is in O before it is rescaled
           wait_product();
-          if (!ok) break;
           tc::fence_after_sync();
+          if (ok) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t o[32];
-            tc::ld32(tO + c0, o);
-            tc::wait_ld();
+            for (int c0 = hf * O0; c0 < (hf + 1) * O0; c0 += 32) {
+              uint32_t o[32];
+              tc::ld32(tO + c0, o);
+              tc::wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-            tc::st32(tO + c0, o);
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              tc::st32(tO + c0, o);
+            }
+            tc::wait_st();
           }
-          tc::wait_st();
           l *= alpha;
         }
-        const float nbase = m == -INFINITY ? 0.f : -m;
-        float sum = 0.f;
+        const float nb = m == -INFINITY ? 0.f : -m;
+        const f2 nbase = pack2(nb, nb);
+        f2 sum0 = 0, sum1 = 0;
 #pragma unroll
-        for (int c = 0; c < BN / 32; ++c) {
+        for (int c = 0; c < COLS / 32; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float x = ex2_approx(fmaf(__uint_as_float(raw[c][2 * e]), sl2e, nbase));
-            const float y = ex2_approx(fmaf(__uint_as_float(raw[c][2 * e + 1]), sl2e, nbase));
-            sum += x + y;
-            pk[e] = pack_bf16x2(x, y);
+            const float2 x = unpack2(fma2(pack2(__uint_as_float(raw[c][2 * e]), __uint_as_float(raw[c][2 * e + 1])),
+                                          scale2, nbase));
+            const float y0 = ex2_approx(x.x), y1 = ex2_approx(x.y);
+            if (e & 1)
+              sum1 = add2(sum1, pack2(y0, y1));
+            else
+              sum0 = add2(sum0, pack2(y0, y1));
+            pk[e] = pack_bf16x2(y0, y1);
           }
-          tc::st16(tS + 16 * c, pk);
+          // over S columns that both halves have read: this half's P follows the other's
+          if (ok) tc::st16(tbase + C::TS + sb * BN + (hf * COLS) / 2 + 16 * c + lane_off, pk);
         }
-        l += sum;
+        const float2 s2 = unpack2(add2(sum0, sum1));
+        l += s2.x + s2.y;
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -466,21 +531,21 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
       if (it.n > 0) {
         wait_product();
-        if (!ok) break;
         tc::fence_after_sync();
       }
+      if (HALVES == 2) l += trade(l);
       const float f = l != 0.f ? 1.f / l : 0.f;
       __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.o.ptr) +
                            (long long)(it.q0 + t * P.PT + ir) * P.o.token_stride +
                            (long long)(it.h * P.G + jr) * P.o.head_stride;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
+      for (int c0 = hf * O0; c0 < (hf + 1) * O0; c0 += 32) {
         uint32_t o[32];
-        if (it.n > 0) {
+        if (it.n > 0 && ok) {
           tc::ld32(tO + c0, o);
           tc::wait_ld();
         }
-        if (mine) {
+        if (mine && ok) {
 #pragma unroll
           for (int c = 0; c < 32; c += 8) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -536,12 +601,14 @@ static sv_status run(const sv_rows *q, const sv_rows *k, const sv_rows *v, Param
       !make_map(&mk, k, P.Tk, P.Hkv, D, false, C::BN, 0, q->ptr) ||
       !make_map(&mv, v, P.Tk, P.Hkv, D, false, C::BN, 0, q->ptr))
     return SV_ERR_CUDA;
-  const size_t fixed = 1024 + C::RING + ((size_t)P.B + 1) * 4;
-  P.slots = imin(5, (int)((SMEM_LIMIT - fixed) / SLOT));
+  const size_t prefix = ((size_t)P.B + 1) * 4;
+  P.slots = prefix <= HEADER - PREFIX ? 5 : 4;
+  const size_t smem = C::RING + (size_t)P.slots * SLOT + (P.slots == 5 ? 0 : prefix);
+  static_assert(C::RING + 5 * SLOT <= 227 * 1024 && C::RING + 4 * SLOT + (MAX_B + 1) * 4 <= 227 * 1024, "shared memory");
   // at most one item more per sequence than the rows fill
   const long long items = ((long long)P.Tq / (P.PT * C::NT) + P.B) * P.Hkv;
   const int ctas = (int)lmin(items, sms);
-  return from_cuda(launch_early(window_kernel<D>, dim3(ctas), dim3(C::THREADS), fixed + (size_t)P.slots * SLOT, s, mq, mk,
+  return from_cuda(launch_early(window_kernel<D>, dim3(ctas), dim3(C::THREADS), smem, s, mq, mk,
                           mv, P));
 }
 
