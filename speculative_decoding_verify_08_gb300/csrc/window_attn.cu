@@ -17,9 +17,12 @@
 //    the tensor cores work on one tile's products while the other's softmax
 //    runs, and each K/V block of 128 keys is fetched once for both.
 //    D = 256: O alone takes half of tensor memory, so a CTA carries one tile
-//    with two S buffers over blocks of 64 keys: S of the next block is
-//    computed during the softmax of this one, whose rows two threads share
-//    (half of the keys each; they exchange one maximum a block).
+//    with two S buffers: S of the next block is computed during the softmax of
+//    this one, whose rows two threads share (half of the keys each; they
+//    exchange one maximum a block).  Blocks are 128 keys there too: with 64, S
+//    takes twice the instructions, each as long to issue (about 55 clocks) as
+//    to execute.  A K block comes as two halves of its columns, a V block as
+//    two halves of its keys, 32 KB each.
 //  * Only blocks that some row of the CTA's tiles sees are visited.  One warp
 //    streams K and V blocks with TMA into a ring of 32 KB slots, another
 //    fetches the next tiles' queries as soon as the last S product is done.
@@ -36,9 +39,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // attn.cu
 namespace window {
 
 constexpr int ROWS = 128;           // rows of a tile (TMEM lanes)
+constexpr int BN = 128;             // keys of a block
 constexpr int MAX_B = 4096;
 constexpr float RESCALE = 8.f;      // log2 of the largest P against an old maximum
-constexpr int SLOT = 32768;         // bytes of a K or V block
+constexpr int SLOT = 32768;         // bytes of a ring slot
 // Shared memory: barriers, scan totals (256), halves' exchange (512), prefix
 // sums (2560; after the ring if longer), then the query tiles and the ring.
 constexpr int HEADER = 3072, PREFIX = 2560;
@@ -47,13 +51,14 @@ template <int D>
 struct Cfg {
   static constexpr int NT = D == 128 ? 2 : 1;   // tiles per CTA
   static constexpr int NSB = D == 128 ? 1 : 2;  // S buffers per tile
-  static constexpr int BN = D == 128 ? 128 : 64;  // keys per block
+  static constexpr int PARTS = D / 128;         // ring slots of a K block (of a V block)
+  static constexpr int VK = BN / PARTS;         // keys of a V slot
   static constexpr int SOFT = 8;                // softmax warps
   static constexpr int HALVES = D == 128 ? 1 : 2;  // threads that share a row
   static constexpr int THREADS = (SOFT + 4) * 32;
   static constexpr int QBYTES = ROWS * D * 2;
   static constexpr int RING = HEADER + NT * QBYTES;
-  static_assert(BN * D * 2 == SLOT, "block");
+  static_assert(BN * D * 2 == PARTS * SLOT, "block");
   // tensor memory: O per tile, then the S buffers (P over S)
   static constexpr uint32_t TO = 0, TS = NT * D;
   static_assert(NT * D + NT * NSB * BN <= 512, "tensor memory");
@@ -88,7 +93,6 @@ __device__ __forceinline__ int rows_of(const Params &P, int b) {
 
 template <int D>
 __device__ __forceinline__ Item item_at(const Params &P, const int *pre, int id) {
-  constexpr int BN = Cfg<D>::BN;
   const int c = id / P.Hkv;
   int lo = 0, hi = P.B - 1;
   while (lo < hi) {
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                   const __grid_constant__ CUtensorMap mapV, const Params P) {
   using C = Cfg<D>;
-  constexpr int NT = C::NT, NSB = C::NSB, BN = C::BN;
+  constexpr int NT = C::NT, NSB = C::NSB, PARTS = C::PARTS, VK = C::VK;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw;
   // The swizzled tiles need 1024-byte alignment, which the first dynamic byte
@@ -234,23 +238,35 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       // ------------------------------------------- K and V blocks --
       if (lane == 0) {
         bool ok = true;
-        uint32_t q = 0;
+        uint32_t q = 0, parity = 1;
+        int slot = 0;
         for (int k = 0; k < rounds && ok; ++k) {
           const int id = item_id(k, items);
           if (id < 0) continue;
           const Item it = item_at<D>(P, pre, id);
-          for (int j = 0; j < 2 * it.n && ok; ++j, ++q) {
-            const uint32_t slot = q % (uint32_t)NS;
-            ok = mbar_wait(&empty[slot], ((q / (uint32_t)NS) & 1) ^ 1, P.err);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&full[slot], SLOT);
-            tma_load_4d(ring + slot * SLOT, (j & 1) ? &mapV : &mapK, 0, it.k0 + it.block(j >> 1) * BN, 0, it.h,
-                        &full[slot]);
+          for (int j = 0; j < it.n && ok; ++j) {
+            const int key = it.k0 + it.block(j) * BN;
+#pragma unroll
+            for (int x = 0; x < 2 * PARTS; ++x) {
+              if (ok) ok = mbar_wait(&empty[slot], parity, P.err);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&full[slot], SLOT);
+              if (x < PARTS)
+                tma_load_4d(ring + slot * SLOT, &mapK, 0, key, 2 * x, it.h, &full[slot]);
+              else
+                tma_load_4d(ring + slot * SLOT, &mapV, 0, key + (x - PARTS) * VK, 0, it.h, &full[slot]);
+              ++q;
+              if (++slot == NS) {
+                slot = 0;
+                parity ^= 1;
+              }
+            }
           }
         }
         if (!ok) {  // no copy may outlive the CTA
           const uint32_t first = q > (uint32_t)NS ? q - NS : 0u;
-          for (uint32_t qq = first; qq < q; ++qq) mbar_wait(&full[qq % NS], (qq / NS) & 1, P.err);
+          for (uint32_t qq = first; qq < q && mbar_wait(&full[qq % NS], (qq / NS) & 1, P.err); ++qq) {
+          }
         }
       }
       __syncwarp();
@@ -283,28 +299,40 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       constexpr uint32_t IDO = tc::idesc_bf16_f32(ROWS, D, true);
       // descriptors: queries and keys K-major, values with rows along K
       const uint64_t dq = tc::smem_desc_sw128(smem_u32(qs), 16, 1024), dk = tc::smem_desc_sw128(smem_u32(ring), 16, 1024);
-      const uint64_t dv = tc::smem_desc_sw128(smem_u32(ring), BN * 128, 1024);
+      const uint64_t dv = tc::smem_desc_sw128(smem_u32(ring), VK * 128, 1024);
       const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32), k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32);
       const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
       // warp-uniform, so that the products' operands stay in uniform registers
       const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
       const bool leader = tc::elect_one();
       bool ok = true;
-      uint32_t q = 0;                 // ring position of the item's first block
-      uint32_t c = 0;                 // items with work so far
-      uint32_t sj[NT] = {}, pj[NT] = {};  // blocks of each tile: S issued, P consumed
-      uint32_t oc[NT] = {};           // items of each tile
       auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (ok) ok = spin_wait(bar, parity, P.err);
         ok = __all_sync(0xffffffffu, ok);
       };
-      auto issue_s = [&](int t, uint32_t sb, uint32_t slot) {  // the leader
+      // the next K and the next V slot of the ring
+      struct Cursor {
+        int slot;
+        uint32_t parity;
+        __device__ __forceinline__ void step(int n, int NS) {
+          slot += n;
+          if (slot >= NS) {
+            slot -= NS;
+            parity ^= 1;
+          }
+        }
+      };
+      Cursor ck{0, 0}, cv{PARTS, 0};
+      uint32_t c = 0;                     // items with work so far
+      uint32_t sj[NT] = {}, pj[NT] = {};  // blocks of each tile: S issued, P consumed
+      uint32_t oc[NT] = {};               // items of each tile
+      // S of one block for tile t, the leader's part: columns of K part x
+      auto issue_s = [&](int t, uint32_t sb, int x, int slot) {
         const uint32_t ka = k_lo + slot * (SLOT / 16), d = tb + C::TS + sb * BN;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc::mma_bf16(d, q_lo + (t * C::QBYTES + (ks >> 2) * ROWS * 128 + (ks & 3) * 32) / 16, q_hi,
-                       ka + ((ks >> 2) * BN * 128 + (ks & 3) * 32) / 16, k_hi, IDS, ks > 0);
-        tc::commit(&s_full[sb]);
+        for (int ks = 0; ks < 8; ++ks)
+          tc::mma_bf16(d, q_lo + (t * C::QBYTES + (2 * x + (ks >> 2)) * ROWS * 128 + (ks & 3) * 32) / 16, q_hi,
+                       ka + ((ks >> 2) * BN * 128 + (ks & 3) * 32) / 16, k_hi, IDS, (x > 0 || ks > 0) ? 1u : 0u);
       };
       for (int k = 0; k < rounds && ok; ++k) {
         const int id = item_id(k, items);
@@ -315,79 +343,92 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const int nt = __shfl_sync(0xffffffffu, it.rows > P.PT ? NT : 1, 0);
         wait(q_full, c & 1);
         ++c;
-        wait(&full[q % NS], (q / NS) & 1);
-        if (!ok) break;
-        tc::fence_after_sync();
-        if (leader) {
+        // S of the first block (two S buffers: also of each next one) for all tiles
+        auto all_s = [&](bool last) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            if (t < nt) issue_s(t, NSB == 2 ? (sj[0] & 1) : (uint32_t)t, q % NS);
-          tc::commit(&empty[q % NS]);
-          if (n == 1) tc::commit(q_free);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          if (t < nt) ++sj[t];
-        for (int j = 0; j < n && ok; ++j) {
-          const uint32_t qv = q + 2 * j + 1, qk = qv + 1;
-          const bool more = j + 1 < n;
-          if (NSB == 2 && more) {  // the next S runs during this block's softmax
-            wait(&full[qk % NS], (qk / NS) & 1);
-            if (!ok) break;
+          for (int x = 0; x < PARTS; ++x) {
+            wait(&full[ck.slot], ck.parity);
+            if (!ok) return;
             tc::fence_after_sync();
             if (leader) {
-              issue_s(0, sj[0] & 1, qk % NS);
-              tc::commit(&empty[qk % NS]);
-              if (j + 2 == n) tc::commit(q_free);
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+                if (t < nt) {
+                  const uint32_t sb = NSB == 2 ? (sj[0] & 1) : (uint32_t)t;
+                  issue_s(t, sb, x, ck.slot);
+                  if (x == PARTS - 1) tc::commit(&s_full[sb]);
+                }
+              tc::commit(&empty[ck.slot]);
+              if (last && x == PARTS - 1) tc::commit(q_free);
             }
-            ++sj[0];
+            ck.step(1, NS);
           }
-          wait(&full[qv % NS], (qv / NS) & 1);
-          if (!ok) break;
+          ck.step(PARTS, NS);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            if (t < nt) ++sj[t];
+        };
+        all_s(n == 1);
+        for (int j = 0; j < n && ok; ++j) {
+          const bool more = j + 1 < n;
+          if (NSB == 2 && more) all_s(j + 2 == n);  // runs during this block's softmax
           // rows past the sequence's keys belong to others: they count as zero
           const int past = it.block(j) * BN + BN - it.nk;
-          if (past > 0) {
-            uint8_t *vb = ring + (qv % NS) * SLOT;
-            for (int x = lane; x < past * (D / 8); x += 32) {
-              const int r = BN - past + x / (D / 8), y = x % (D / 8);
-              *reinterpret_cast<uint4 *>(vb + (y >> 3) * BN * 128 + r * 128 + (y & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async();
-            __syncwarp();
+          if (NSB == 1) {  // one slot each for K and V
+            wait(&full[cv.slot], cv.parity);
+            if (more) wait(&full[ck.slot], ck.parity);
           }
-          if (NSB == 1 && more) wait(&full[qk % NS], (qk / NS) & 1);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             if (t >= nt || !ok) continue;
             const uint32_t sb = NSB == 2 ? (pj[t] & 1) : (uint32_t)t;
             if (j == 0 && oc[t] > 0) wait(&o_free[t], (oc[t] - 1) & 1);
             wait(&p_full[sb], (NSB == 2 ? pj[t] >> 1 : pj[t]) & 1);
-            if (!ok) continue;
-            tc::fence_after_sync();
-            if (leader) {
-              const uint32_t va = v_lo + (qv % NS) * (SLOT / 16);
 #pragma unroll
-              for (int ks = 0; ks < BN / 16; ++ks)
-                tc::mma_bf16_ts(tb + C::TO + t * D, tb + C::TS + sb * BN + ks * 8, va + ks * 2048 / 16, v_hi, IDO,
-                                ks > 0 ? 1u : (uint32_t)j);
-              tc::commit(&o_done[sb]);
-              if (t == nt - 1) tc::commit(&empty[qv % NS]);
-              if (NSB == 1 && more) {
-                issue_s(t, (uint32_t)t, qk % NS);
-                if (t == nt - 1) {
-                  tc::commit(&empty[qk % NS]);
-                  if (j + 2 == n) tc::commit(q_free);
+            for (int x = 0; x < PARTS; ++x) {
+              if (NSB == 2) wait(&full[cv.slot], cv.parity);
+              if (!ok) break;
+              // keys of this V slot that are past the end
+              const int gone = imin(VK, past - (PARTS - 1 - x) * VK);
+              if (gone > 0 && t == 0) {
+                uint8_t *vb = ring + cv.slot * SLOT;
+                for (int y = lane; y < gone * (D / 8); y += 32) {
+                  const int r = VK - gone + y / (D / 8), z = y % (D / 8);
+                  *reinterpret_cast<uint4 *>(vb + (z >> 3) * VK * 128 + r * 128 + (z & 7) * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async();
+                __syncwarp();
+              }
+              tc::fence_after_sync();
+              if (leader) {
+                const uint32_t va = v_lo + cv.slot * (SLOT / 16);
+#pragma unroll
+                for (int ks = 0; ks < VK / 16; ++ks)
+                  tc::mma_bf16_ts(tb + C::TO + t * D, tb + C::TS + sb * BN + (x * (VK / 16) + ks) * 8,
+                                  va + ks * 2048 / 16, v_hi, IDO, (x > 0 || ks > 0) ? 1u : (uint32_t)j);
+                if (x == PARTS - 1) tc::commit(&o_done[sb]);
+                if (t == nt - 1) tc::commit(&empty[cv.slot]);
+                if (NSB == 1 && more) {
+                  issue_s(t, (uint32_t)t, 0, ck.slot);
+                  tc::commit(&s_full[t]);
+                  if (t == nt - 1) {
+                    tc::commit(&empty[ck.slot]);
+                    if (j + 2 == n) tc::commit(q_free);
+                  }
                 }
               }
+              if (t == nt - 1) cv.step(1, NS);
             }
             ++pj[t];
             if (NSB == 1 && more) ++sj[t];
           }
+          cv.step(PARTS, NS);
+          if (NSB == 1 && more) ck.step(2, NS);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
           if (t < nt) ++oc[t];
-        q += 2 * n;
         __syncwarp();
       }
       if (leader) {  // every product issued above has completed before TMEM is released
@@ -575,8 +616,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 }
 
 // 4-D map of rows [T][H][D]: keys and values (column, token, 64-column group,
-// head) in boxes of 64 x BN x D/64, queries (column, head, token, group) in
-// boxes of 64 x G x PT; 128-byte swizzle, zeros past the last token.
+// head) in boxes of 64 x b1 x b2, queries (column, head, token, group) in
+// boxes of 64 x b1 x b2; 128-byte swizzle, zeros past the last token.
 // `any`: an address to stand in for that of no rows.
 static bool make_map(CUtensorMap *map, const sv_rows *r, int T, int H, int D, bool query, int b1, int b2, void *any) {
   auto fn = attn::encode_fn();
@@ -586,7 +627,7 @@ static bool make_map(CUtensorMap *map, const sv_rows *r, int T, int H, int D, bo
   const cuuint64_t ts = T > 1 ? (cuuint64_t)r->token_stride * 2 : 128, hs = H > 1 ? (cuuint64_t)r->head_stride * 2 : 128;
   cuuint64_t dk[4] = {64, t, g, (cuuint64_t)H}, sk[3] = {ts, 128, hs};
   cuuint64_t dq[4] = {64, (cuuint64_t)H, t, g}, sq[3] = {hs, ts, 128};
-  cuuint32_t bk[4] = {64, (cuuint32_t)b1, (cuuint32_t)g, 1}, bq[4] = {64, (cuuint32_t)b1, (cuuint32_t)b2, 1};
+  cuuint32_t bk[4] = {64, (cuuint32_t)b1, (cuuint32_t)b2, 1}, bq[4] = {64, (cuuint32_t)b1, (cuuint32_t)b2, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, T > 0 ? r->ptr : any, query ? dq : dk, query ? sq : sk, query ? bq : bk, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -598,8 +639,8 @@ static sv_status run(const sv_rows *q, const sv_rows *k, const sv_rows *v, Param
   using C = Cfg<D>;
   CUtensorMap mq, mk, mv;
   if (!make_map(&mq, q, P.Tq, P.Hkv * P.G, D, true, P.G, P.PT, q->ptr) ||
-      !make_map(&mk, k, P.Tk, P.Hkv, D, false, C::BN, 0, q->ptr) ||
-      !make_map(&mv, v, P.Tk, P.Hkv, D, false, C::BN, 0, q->ptr))
+      !make_map(&mk, k, P.Tk, P.Hkv, D, false, BN, 2, q->ptr) ||
+      !make_map(&mv, v, P.Tk, P.Hkv, D, false, C::VK, D / 64, q->ptr))
     return SV_ERR_CUDA;
   const size_t prefix = ((size_t)P.B + 1) * 4;
   P.slots = prefix <= HEADER - PREFIX ? 5 : 4;
