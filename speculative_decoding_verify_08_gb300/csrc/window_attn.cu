@@ -47,14 +47,15 @@ constexpr int SLOT = 32768;         // bytes of a ring slot
 // sums (2560; after the ring if longer), then the query tiles and the ring.
 constexpr int HEADER = 3072, PREFIX = 2560;
 
-template <int D>
+// Two tiles a CTA (D = 128), or one with two S buffers and two threads a row.
+template <int D, int TILES>
 struct Cfg {
-  static constexpr int NT = D == 128 ? 2 : 1;   // tiles per CTA
-  static constexpr int NSB = D == 128 ? 1 : 2;  // S buffers per tile
+  static constexpr int NT = TILES;
+  static constexpr int NSB = TILES == 2 ? 1 : 2;  // S buffers per tile
+  static constexpr int SOFT = 8;                  // softmax warps
+  static constexpr int HALVES = TILES == 2 ? 1 : 2;  // threads that share a row
   static constexpr int PARTS = D / 128;         // ring slots of a K block (of a V block)
   static constexpr int VK = BN / PARTS;         // keys of a V slot
-  static constexpr int SOFT = 8;                // softmax warps
-  static constexpr int HALVES = D == 128 ? 1 : 2;  // threads that share a row
   static constexpr int THREADS = (SOFT + 4) * 32;
   static constexpr int QBYTES = ROWS * D * 2;
   static constexpr int RING = HEADER + NT * QBYTES;
@@ -91,7 +92,7 @@ __device__ __forceinline__ int rows_of(const Params &P, int b) {
   return q1 - q0;
 }
 
-template <int D>
+template <int NT>
 __device__ __forceinline__ Item item_at(const Params &P, const int *pre, int id) {
   const int c = id / P.Hkv;
   int lo = 0, hi = P.B - 1;
@@ -99,7 +100,7 @@ __device__ __forceinline__ Item item_at(const Params &P, const int *pre, int id)
     const int mid = (lo + hi + 1) >> 1;
     if (pre[mid] <= c) lo = mid; else hi = mid - 1;
   }
-  const int b = lo, span = P.PT * Cfg<D>::NT;
+  const int b = lo, span = P.PT * NT;
   Item it;
   it.h = id - c * P.Hkv;
   // a sequence's last tiles first: they see the most
@@ -136,11 +137,11 @@ __device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *m
       : "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+template <int D, int TILES>
+__global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
     window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                   const __grid_constant__ CUtensorMap mapV, const Params P) {
-  using C = Cfg<D>;
+  using C = Cfg<D, TILES>;
   constexpr int NT = C::NT, NSB = C::NSB, PARTS = C::PARTS, VK = C::VK;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw;
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         for (int k = 0; k < rounds && ok; ++k) {
           const int id = item_id(k, items);
           if (id < 0) continue;
-          const Item it = item_at<D>(P, pre, id);
+          const Item it = item_at<NT>(P, pre, id);
           for (int j = 0; j < it.n && ok; ++j) {
             const int key = it.k0 + it.block(j) * BN;
 #pragma unroll
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         for (int k = 0; k < rounds && ok; ++k) {
           const int id = item_id(k, items);
           if (id < 0) continue;
-          const Item it = item_at<D>(P, pre, id);
+          const Item it = item_at<NT>(P, pre, id);
           if (it.n == 0) continue;
           if (c > 0) ok = mbar_wait(q_free, (c - 1) & 1, P.err);
           if (!ok) break;
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       for (int k = 0; k < rounds && ok; ++k) {
         const int id = item_id(k, items);
         if (id < 0) continue;
-        const Item it = item_at<D>(P, pre, id);
+        const Item it = item_at<NT>(P, pre, id);
         const int n = __shfl_sync(0xffffffffu, it.n, 0);
         if (n == 0) continue;
         const int nt = __shfl_sync(0xffffffffu, it.rows > P.PT ? NT : 1, 0);
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     for (int k = 0; k < rounds; ++k) {
       const int id = item_id(k, items);
       if (id < 0) continue;
-      const Item it = item_at<D>(P, pre, id);
+      const Item it = item_at<NT>(P, pre, id);
       if (t > 0 && it.rows <= P.PT) continue;
       const bool mine = ir < P.PT && t * P.PT + ir < it.rows;  // a row of the prompt
       const int pt = it.p0 + t * P.PT, p = pt + ir;            // position of the tile's first row, of this one
@@ -575,29 +576,50 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         tc::fence_after_sync();
       }
       if (HALVES == 2) l += trade(l);
+      // O / l to bf16.  Read so that the lanes of a quad hold neighbouring
+      // columns of a row; four quad lanes then trade 4-byte pieces for 16
+      // consecutive bytes each, and a store covers eight rows' 64 bytes (one
+      // row a lane took 32 sectors a store: 5 against 1.5 thousand clocks a tile).
       const float f = l != 0.f ? 1.f / l : 0.f;
-      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.o.ptr) +
-                           (long long)(it.q0 + t * P.PT + ir) * P.o.token_stride +
-                           (long long)(it.h * P.G + jr) * P.o.head_stride;
+      const long long at = (mine && ok) ? (long long)(it.q0 + t * P.PT + ir) * P.o.token_stride +
+                                              (long long)(it.h * P.G + jr) * P.o.head_stride
+                                        : -1LL;
+      const int tq = lane & 3;
 #pragma unroll 1
-      for (int c0 = hf * O0; c0 < (hf + 1) * O0; c0 += 32) {
-        uint32_t o[32];
-        if (it.n > 0 && ok) {
-          tc::ld32(tO + c0, o);
-          tc::wait_ld();
-        }
-        if (mine && ok) {
-#pragma unroll
-          for (int c = 0; c < 32; c += 8) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (l != 0.f) {
-              v.x = pack_bf16x2(__uint_as_float(o[c]) * f, __uint_as_float(o[c + 1]) * f);
-              v.y = pack_bf16x2(__uint_as_float(o[c + 2]) * f, __uint_as_float(o[c + 3]) * f);
-              v.z = pack_bf16x2(__uint_as_float(o[c + 4]) * f, __uint_as_float(o[c + 5]) * f);
-              v.w = pack_bf16x2(__uint_as_float(o[c + 6]) * f, __uint_as_float(o[c + 7]) * f);
-            }
-            *reinterpret_cast<uint4 *>(out + c0 + c) = v;
+      for (int lh = 0; lh < 2; ++lh) {
+        const int ra = 16 * lh + (lane >> 2);
+        const float fr[2] = {__shfl_sync(0xffffffffu, f, ra), __shfl_sync(0xffffffffu, f, ra + 8)};
+        const long long to[2] = {__shfl_sync(0xffffffffu, at, ra), __shfl_sync(0xffffffffu, at, ra + 8)};
+#pragma unroll 1
+        for (int c0 = hf * O0; c0 < (hf + 1) * O0; c0 += 64) {
+          uint32_t o[32];
+          if (it.n > 0 && ok) {
+            tc::ld_16x64(tbase + C::TO + t * D + ((uint32_t)((warp & 3) * 32 + 16 * lh) << 16) + c0, o);
+            tc::wait_ld();
           }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              uint32_t x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                x[e] = pack_bf16x2(__uint_as_float(o[16 * g + 4 * e + 2 * i]) * fr[i],
+                                   __uint_as_float(o[16 * g + 4 * e + 2 * i + 1]) * fr[i]);
+              auto trade4 = [&](uint32_t &lo, uint32_t &hi, int bit) {
+                const bool up = tq & bit;
+                const uint32_t y = __shfl_xor_sync(0xffffffffu, up ? lo : hi, bit);
+                if (up) lo = y; else hi = y;
+              };
+              trade4(x[0], x[1], 1);
+              trade4(x[2], x[3], 1);
+              trade4(x[0], x[2], 2);
+              trade4(x[1], x[3], 2);
+              // no key seen: zeros, whatever O holds
+              const uint4 v = fr[i] != 0.f ? make_uint4(x[0], x[1], x[2], x[3]) : make_uint4(0u, 0u, 0u, 0u);
+              if (to[i] >= 0)
+                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(P.o.ptr) + to[i] + c0 + 8 * (4 * g + tq)) = v;
+            }
         }
       }
       if (it.n > 0) {
@@ -634,9 +656,9 @@ static bool make_map(CUtensorMap *map, const sv_rows *r, int T, int H, int D, bo
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, int TILES>
 static sv_status run(const sv_rows *q, const sv_rows *k, const sv_rows *v, Params &P, int sms, cudaStream_t s) {
-  using C = Cfg<D>;
+  using C = Cfg<D, TILES>;
   CUtensorMap mq, mk, mv;
   if (!make_map(&mq, q, P.Tq, P.Hkv * P.G, D, true, P.G, P.PT, q->ptr) ||
       !make_map(&mk, k, P.Tk, P.Hkv, D, false, BN, 2, q->ptr) ||
@@ -649,8 +671,18 @@ static sv_status run(const sv_rows *q, const sv_rows *k, const sv_rows *v, Param
   // at most one item more per sequence than the rows fill
   const long long items = ((long long)P.Tq / (P.PT * C::NT) + P.B) * P.Hkv;
   const int ctas = (int)lmin(items, sms);
-  return from_cuda(launch_early(window_kernel<D>, dim3(ctas), dim3(C::THREADS), smem, s, mq, mk,
-                          mv, P));
+  return from_cuda(launch_early(window_kernel<D, TILES>, dim3(ctas), dim3(C::THREADS), smem, s, mq, mk, mv, P));
+}
+
+static sv_status run_any(const sv_rows *q, const sv_rows *k, const sv_rows *v, Params &P, int D, int sms,
+                         cudaStream_t s) {
+  if (D == 256) return run<256, 1>(q, k, v, P, sms, s);
+  // Two tiles a CTA use the tensor cores best (8192 rows of 32 heads, causal:
+  // 385 us against 458), but their items are twice as long: with fewer than two
+  // for every SM single tiles fill the GPU more evenly (seven prompts of 2 to
+  // 901 rows: 24 us against 28).
+  const long long pairs = ((long long)P.Tq / (P.PT * 2) + P.B) * P.Hkv;
+  return pairs >= 2 * sms ? run<128, 2>(q, k, v, P, sms, s) : run<128, 1>(q, k, v, P, sms, s);
 }
 
 }  // namespace window
@@ -707,8 +739,7 @@ sv_status window_attn(const sv_rows *q, const sv_rows *k, const sv_rows *v, cons
   P.sl2e = scale * 1.4426950408889634f;
   P.window = window;
   P.sinks = sinks;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return D == 256 ? window::run<256>(q, k, v, P, sms, s) : window::run<128>(q, k, v, P, sms, s);
+  return window::run_any(q, k, v, P, D, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
