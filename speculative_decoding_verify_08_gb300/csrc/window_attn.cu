@@ -128,6 +128,12 @@ __device__ __forceinline__ int item_id(int k, int items) {
   return k * g + at < items ? k * g + at : -1;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *map, int c0, int c1, int c2,
                                             int c3, uint64_t *bar) {
   asm volatile(
@@ -161,7 +167,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
   uint64_t *q_full = o_free + 2;   // queries of the item landed
   uint64_t *q_free = q_full + 1;   // last S product of the item done
   uint64_t *idle = q_free + 1;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(idle + 1);
+  uint64_t *p_half = idle + 1;     // [2] one S buffer: P of the first half of a block's keys written
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(p_half + 2);
   int *wsum = reinterpret_cast<int *>(smem + 256);
   float *xchg = reinterpret_cast<float *>(smem + 512);  // [2][2 halves][ROWS] maxima, then sums
   uint8_t *qs = smem + HEADER;
@@ -179,6 +186,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4 * C::HALVES);
       mbar_init(&o_done[i], 1);
+      mbar_init(&p_half[i], 4);
       mbar_init(&o_free[i], 4 * C::HALVES);
     }
     mbar_init(q_full, 1);
@@ -384,7 +392,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
             if (t >= nt || !ok) continue;
             const uint32_t sb = NSB == 2 ? (pj[t] & 1) : (uint32_t)t;
             if (j == 0 && oc[t] > 0) wait(&o_free[t], (oc[t] - 1) & 1);
-            wait(&p_full[sb], (NSB == 2 ? pj[t] >> 1 : pj[t]) & 1);
+            wait(NSB == 2 ? &p_full[sb] : &p_half[sb], (NSB == 2 ? pj[t] >> 1 : pj[t]) & 1);
 #pragma unroll
             for (int x = 0; x < PARTS; ++x) {
               if (NSB == 2) wait(&full[cv.slot], cv.parity);
@@ -402,12 +410,21 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
                 __syncwarp();
               }
               tc::fence_after_sync();
-              if (leader) {
-                const uint32_t va = v_lo + cv.slot * (SLOT / 16);
+              const uint32_t va = v_lo + cv.slot * (SLOT / 16);
+              auto issue_o = [&](int k0, int k1) {
 #pragma unroll
-                for (int ks = 0; ks < VK / 16; ++ks)
+                for (int ks = k0; ks < k1; ++ks)
                   tc::mma_bf16_ts(tb + C::TO + t * D, tb + C::TS + sb * BN + (x * (VK / 16) + ks) * 8,
                                   va + ks * 2048 / 16, v_hi, IDO, (x > 0 || ks > 0) ? 1u : (uint32_t)j);
+              };
+              if (NSB == 1) {  // the first half of the keys while the second's P is made
+                if (leader) issue_o(0, 4);
+                wait(&p_full[sb], pj[t] & 1);
+                if (!ok) break;
+                tc::fence_after_sync();
+              }
+              if (leader) {
+                issue_o(NSB == 1 ? 4 : 0, VK / 16);
                 if (x == PARTS - 1) tc::commit(&o_done[sb]);
                 if (t == nt - 1) tc::commit(&empty[cv.slot]);
                 if (NSB == 1 && more) {
@@ -471,11 +488,17 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
       named_barrier(2 + (warp & 3), 64);
       return at[(hf ^ 1) * ROWS + r];
     };
+    int id = rounds > 0 ? item_id(0, items) : -1;
+    Item it{};
+    if (id >= 0) it = item_at<NT>(P, pre, id);
     for (int k = 0; k < rounds; ++k) {
-      const int id = item_id(k, items);
-      if (id < 0) continue;
-      const Item it = item_at<NT>(P, pre, id);
-      if (t > 0 && it.rows <= P.PT) continue;
+      if (id < 0 || (t > 0 && it.rows <= P.PT)) {  // nothing for this tile
+        if (k + 1 < rounds) {
+          id = item_id(k + 1, items);
+          if (id >= 0) it = item_at<NT>(P, pre, id);
+        }
+        continue;
+      }
       const bool mine = ir < P.PT && t * P.PT + ir < it.rows;  // a row of the prompt
       const int pt = it.p0 + t * P.PT, p = pt + ir;            // position of the tile's first row, of this one
       const int plast = it.p0 + imin(it.rows, (t + 1) * P.PT) - 1;
@@ -517,7 +540,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
           for (int e = 0; e < 32; e += 8)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mx4[i] = fmaxf(mx4[i], fmaxf(__uint_as_float(raw[c][e + i]), __uint_as_float(raw[c][e + 4 + i])));
+              mx4[i] = max3(mx4[i], __uint_as_float(raw[c][e + i]), __uint_as_float(raw[c][e + 4 + i]));
         float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         if (HALVES == 2) mx = fmaxf(mx, trade(mx));
         mx *= sl2e;
@@ -563,6 +586,12 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
           }
           // over S columns that both halves have read: this half's P follows the other's
           if (ok) tc::st16(tbase + C::TS + sb * BN + (hf * COLS) / 2 + 16 * c + lane_off, pk);
+          if (NSB == 1 && c == COLS / 64 - 1) {
+            tc::wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_half[sb]);
+          }
         }
         const float2 s2 = unpack2(add2(sum0, sum1));
         l += s2.x + s2.y;
@@ -571,7 +600,12 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[sb]);
       }
-      if (it.n > 0) {
+      const Item now = it;
+      if (k + 1 < rounds) {  // the next item is looked up while the last product runs
+        id = item_id(k + 1, items);
+        if (id >= 0) it = item_at<NT>(P, pre, id);
+      }
+      if (now.n > 0) {
         wait_product();
         tc::fence_after_sync();
       }
@@ -579,53 +613,58 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
       // O / l to bf16.  Read so that the lanes of a quad hold neighbouring
       // columns of a row; four quad lanes then trade 4-byte pieces for 16
       // consecutive bytes each, and a store covers eight rows' 64 bytes (one
-      // row a lane took 32 sectors a store: 5 against 1.5 thousand clocks a tile).
+      // row a lane would take 32 sectors a store).
+      constexpr int NG = O0 / 64;
       const float f = l != 0.f ? 1.f / l : 0.f;
-      const long long at = (mine && ok) ? (long long)(it.q0 + t * P.PT + ir) * P.o.token_stride +
-                                              (long long)(it.h * P.G + jr) * P.o.head_stride
+      const long long at = (mine && ok) ? (long long)(now.q0 + t * P.PT + ir) * P.o.token_stride +
+                                              (long long)(now.h * P.G + jr) * P.o.head_stride + hf * O0
                                         : -1LL;
       const int tq = lane & 3;
 #pragma unroll 1
-      for (int lh = 0; lh < 2; ++lh) {
-        const int ra = 16 * lh + (lane >> 2);
-        const float fr[2] = {__shfl_sync(0xffffffffu, f, ra), __shfl_sync(0xffffffffu, f, ra + 8)};
-        const long long to[2] = {__shfl_sync(0xffffffffu, at, ra), __shfl_sync(0xffffffffu, at, ra + 8)};
-#pragma unroll 1
-        for (int c0 = hf * O0; c0 < (hf + 1) * O0; c0 += 64) {
-          uint32_t o[32];
-          if (it.n > 0 && ok) {
-            tc::ld_16x64(tbase + C::TO + t * D + ((uint32_t)((warp & 3) * 32 + 16 * lh) << 16) + c0, o);
+      for (int x0 = 0; x0 < 2 * NG; ++x0) {  // 16 rows of 64 columns at a time
+        const int lh = x0 / NG, c = x0 % NG;
+        uint32_t o[32];
+        if (now.n > 0) {
+          if (ok) {
+            tc::ld_16x64(tbase + C::TO + t * D + ((uint32_t)((warp & 3) * 32 + 16 * lh) << 16) + hf * O0 + 64 * c, o);
             tc::wait_ld();
           }
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              uint32_t x[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                x[e] = pack_bf16x2(__uint_as_float(o[16 * g + 4 * e + 2 * i]) * fr[i],
-                                   __uint_as_float(o[16 * g + 4 * e + 2 * i + 1]) * fr[i]);
-              auto trade4 = [&](uint32_t &lo, uint32_t &hi, int bit) {
-                const bool up = tq & bit;
-                const uint32_t y = __shfl_xor_sync(0xffffffffu, up ? lo : hi, bit);
-                if (up) lo = y; else hi = y;
-              };
-              trade4(x[0], x[1], 1);
-              trade4(x[2], x[3], 1);
-              trade4(x[0], x[2], 2);
-              trade4(x[1], x[3], 2);
-              // no key seen: zeros, whatever O holds
-              const uint4 v = fr[i] != 0.f ? make_uint4(x[0], x[1], x[2], x[3]) : make_uint4(0u, 0u, 0u, 0u);
-              if (to[i] >= 0)
-                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(P.o.ptr) + to[i] + c0 + 8 * (4 * g + tq)) = v;
-            }
+          if (x0 == 2 * NG - 1) {  // O is read out
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[t]);
+          }
         }
-      }
-      if (it.n > 0) {
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&o_free[t]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = 16 * lh + 8 * i + (lane >> 2);
+          const float fr = __shfl_sync(0xffffffffu, f, row);
+          const long long to = __shfl_sync(0xffffffffu, at, row);
+          __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.o.ptr) + to + 64 * c + 8 * tq;
+          const f2 fr2 = pack2(fr, fr);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int y = 16 * g + 4 * e + 2 * i;
+              const float2 z = unpack2(mul2(pack2(__uint_as_float(o[y]), __uint_as_float(o[y + 1])), fr2));
+              x[e] = pack_bf16x2(z.x, z.y);
+            }
+            auto trade4 = [&](uint32_t &lo, uint32_t &hi, int bit) {
+              const bool up = tq & bit;
+              const uint32_t y = __shfl_xor_sync(0xffffffffu, up ? lo : hi, bit);
+              if (up) lo = y; else hi = y;
+            };
+            trade4(x[0], x[1], 1);
+            trade4(x[2], x[3], 1);
+            trade4(x[0], x[2], 2);
+            trade4(x[1], x[3], 2);
+            // no key seen: zeros, whatever O holds
+            const uint4 v = fr != 0.f ? make_uint4(x[0], x[1], x[2], x[3]) : make_uint4(0u, 0u, 0u, 0u);
+            if (to >= 0) *reinterpret_cast<uint4 *>(out + 32 * g) = v;
+          }
+        }
       }
     }
   }
