@@ -70,6 +70,8 @@ def library_path() -> str:
 def load():
     """Load libspecverify.so (built by ``__graft_entry__.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -366,10 +368,17 @@ def _bad(where: str, status: int = SV_ERR_INVALID_ARG):
     raise SvError(status, where)
 
 
+# What a call checks here is what the library cannot see (types, shapes, that
+# memory is the GPU's); one attribute of a tensor costs about 0.1 us.
+_BF16 = torch.bfloat16
+
+
 def _rows(t, tokens, heads, D, where):
     """sv_rows of a CUDA bf16 tensor [tokens, heads, D] (any strides, D contiguous)."""
+    if t.dtype is not _BF16 or t.shape != (tokens, heads, D) or not t.is_cuda:
+        _bad(where)
     ts, hs, ds = t.stride()
-    if t.dtype is not torch.bfloat16 or t.shape != (tokens, heads, D) or ds != 1 or not t.is_cuda:
+    if ds != 1:
         _bad(where)
     # a dimension of one may carry any stride
     return _ROWS.pack(t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0)
@@ -377,7 +386,7 @@ def _rows(t, tokens, heads, D, where):
 
 def _vector(t, dtype, n, where):
     """Address of a contiguous CUDA tensor [n]."""
-    if t.dtype is not dtype or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_cuda or (n > 1 and t.stride(0) != 1):
         _bad(where)
     return t.data_ptr()
 
@@ -404,15 +413,15 @@ def rope_phases(inv_freq, device=None):
 def _norm_rotation(q_weight, k_weight, eps, weight_offset, positions, phases, interleaved, T, D, where):
     norm = rot = None
     if q_weight is not None or k_weight is not None:
-        norm = _NORM.pack(0 if q_weight is None else _vector(q_weight, torch.bfloat16, D, where),
-                          0 if k_weight is None else _vector(k_weight, torch.bfloat16, D, where),
+        norm = _NORM.pack(0 if q_weight is None else _vector(q_weight, _BF16, D, where),
+                          0 if k_weight is None else _vector(k_weight, _BF16, D, where),
                           eps, weight_offset)
     if phases is not None:
         if positions is None:
             _bad(where)
-        rot = _ROTATION.pack(_vector(phases, torch.int64, phases.numel(), where),
-                             _vector(positions, torch.int32, T, where),
-                             2 * phases.numel(), 1 if interleaved else 0)
+        half = phases.shape[0]
+        rot = _ROTATION.pack(_vector(phases, torch.int64, half, where), _vector(positions, torch.int32, T, where),
+                             2 * half, 1 if interleaved else 0)
     return norm, rot
 
 
@@ -425,9 +434,10 @@ def qk_norm_rope(q, k, q_out, k_out, positions=None, phases=None, q_weight=None,
     Hkv = k.shape[1]
     w = "qk_norm_rope"
     norm, rot = _norm_rotation(q_weight, k_weight, eps, weight_offset, positions, phases, interleaved, T, D, w)
-    _check(load().qk_norm_rope(_rows(q, T, Hq, D, w), _rows(k, T, Hkv, D, w), _rows(q_out, T, Hq, D, w),
-                               _rows(k_out, T, Hkv, D, w), norm, rot, T, Hq, Hkv, D,
-                               _launch_stream(q, stream)), w)
+    status = load().qk_norm_rope(_rows(q, T, Hq, D, w), _rows(k, T, Hkv, D, w), _rows(q_out, T, Hq, D, w),
+                                 _rows(k_out, T, Hkv, D, w), norm, rot, T, Hq, Hkv, D, _launch_stream(q, stream))
+    if status:
+        _check(status, w)
 
 
 class PagedKV:
@@ -468,10 +478,12 @@ def paged_kv_append(k, v, cache: PagedKV, slots, q=None, q_out=None, positions=N
     Hq = 0 if q is None else q.shape[1]
     norm, rot = _norm_rotation(q_weight if q is not None else None, k_weight, eps, weight_offset, positions,
                                phases, interleaved, T, D, w)
-    _check(load().paged_kv_append(None if q is None else _rows(q, T, Hq, D, w),
-                                  None if q is None else _rows(q_out, T, Hq, D, w), _rows(k, T, Hkv, D, w),
-                                  _rows(v, T, Hkv, D, w), cache.packed, _vector(slots, torch.int64, T, w), norm,
-                                  rot, T, Hq, Hkv, D, _launch_stream(k, stream)), w)
+    status = load().paged_kv_append(None if q is None else _rows(q, T, Hq, D, w),
+                                    None if q is None else _rows(q_out, T, Hq, D, w), _rows(k, T, Hkv, D, w),
+                                    _rows(v, T, Hkv, D, w), cache.packed, _vector(slots, torch.int64, T, w), norm,
+                                    rot, T, Hq, Hkv, D, _launch_stream(k, stream))
+    if status:
+        _check(status, w)
 
 
 def paged_attn_workspace_bytes(B: int, M: int, Hq: int, Hkv: int, D: int) -> int:
