@@ -43,6 +43,8 @@ constexpr int CHUNK = 16;  // slots per unit
 constexpr int NCW = 8;     // consumer warps
 constexpr int NPW = 4;     // producer warps: K and V of even and odd chunks
 constexpr int THREADS = (NCW + NPW) * 32;
+// 384 threads start with 168 registers each; 128 * 72 + 256 * 216 is the same total
+constexpr int REGS_PRODUCER = 72, REGS_CONSUMER = 216;
 constexpr int MAX_B = 4096;
 constexpr int MAX_R = 128;           // query rows per KV head: eight 16-row tiles
 constexpr int MAX_STAGES = 24;
@@ -216,6 +218,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp >= NCW) {
     // ------------------------------------------------------ producers --
     // Two warps stream K, two V; the pairs take turns chunk by chunk.
+    setmaxnreg_dec<REGS_PRODUCER>();
     // A lane works out the page and slot of one chunk of the next 32, so that
     // the chunks' own turns hold little but the wait and the copies.
     const bool is_v = (warp - NCW) & 1;
@@ -275,6 +278,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 
   // --------------------------------------------------------- consumers --
+  setmaxnreg_inc<REGS_CONSUMER>();
   const int mt = warp % MT, cl = warp / MT;  // query tile; which of every NL chunks
   const int gq = lane >> 2, tq = lane & 3;
   const int row0 = 16 * mt + gq, row1 = row0 + 8;
@@ -390,60 +394,74 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) continue;
       const uint32_t kt = smem_u32(ring + slot * LY::STAGE), vt = kt + LY::TILE;
       // ---- S = Q K^T, 16 rows x 16 slots ----
-      float sa[2][4];
+      // (two sums per tile, of the even and the odd steps: a product waits for
+      // the one before it on the same sum)
+      float sa[2][4], sb[2][4];
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sa[nt][j] = 0.f;
+        for (int j = 0; j < 4; ++j) sa[nt][j] = sb[nt][j] = 0.f;
+      auto load_q = [&](int ks, uint32_t (&qf)[4]) {
+        if (QREG) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) qf[t] = qa[QREG ? ks : 0][t];
+        } else {
+          ldmatrix_x4(qf, qtile + swz16(qr, 2 * ks + (lane >> 4)));
+        }
+      };
+      const int kr = 8 * (lane >> 4) + (lane & 7), kc = (lane >> 3) & 1;
       if (!F8) {
 #pragma unroll
-        for (int ks = 0; ks < NKS; ++ks) {
-          uint32_t kf[4], qf[4];
-          ldmatrix_x4(kf, kt + swz16(8 * (lane >> 4) + (lane & 7), 2 * ks + ((lane >> 3) & 1)));
-          if (QREG) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) qf[t] = qa[QREG ? ks : 0][t];
-          } else {
-            ldmatrix_x4(qf, qtile + swz16(qr, 2 * ks + (lane >> 4)));
-          }
-          mma16<F8>(sa[0], qf, kf[0], kf[1]);
-          mma16<F8>(sa[1], qf, kf[2], kf[3]);
+        for (int ks = 0; ks < NKS; ks += 2) {
+          uint32_t ka[4], kb[4], qf[4], qg[4];
+          ldmatrix_x4(ka, kt + swz16(kr, 2 * ks + kc));
+          ldmatrix_x4(kb, kt + swz16(kr, 2 * ks + 2 + kc));
+          load_q(ks, qf);
+          load_q(ks + 1, qg);
+          mma16<F8>(sa[0], qf, ka[0], ka[1]);
+          mma16<F8>(sa[1], qf, ka[2], ka[3]);
+          mma16<F8>(sb[0], qg, kb[0], kb[1]);
+          mma16<F8>(sb[1], qg, kb[2], kb[3]);
         }
       } else {
 #pragma unroll
         for (int kp = 0; kp < NKS / 2; ++kp) {
-          uint32_t kf[4];
-          ldmatrix_x4(kf, kt + swz16(8 * (lane >> 4) + (lane & 7), 2 * kp + ((lane >> 3) & 1)));
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t qf[4];
-            if (QREG) {
-#pragma unroll
-              for (int t = 0; t < 4; ++t) qf[t] = qa[QREG ? 2 * kp + e : 0][t];
-            } else {
-              ldmatrix_x4(qf, qtile + swz16(qr, 2 * (2 * kp + e) + (lane >> 4)));
-            }
-            mma16<F8>(sa[0], qf, e4m3x2_to_f16x2(kf[e]), e4m3x2_to_f16x2_hi(kf[e]));
-            mma16<F8>(sa[1], qf, e4m3x2_to_f16x2(kf[2 + e]), e4m3x2_to_f16x2_hi(kf[2 + e]));
-          }
+          uint32_t kf[4], qf[4], qg[4];
+          ldmatrix_x4(kf, kt + swz16(kr, 2 * kp + kc));
+          load_q(2 * kp, qf);
+          load_q(2 * kp + 1, qg);
+          mma16<F8>(sa[0], qf, e4m3x2_to_f16x2(kf[0]), e4m3x2_to_f16x2_hi(kf[0]));
+          mma16<F8>(sa[1], qf, e4m3x2_to_f16x2(kf[2]), e4m3x2_to_f16x2_hi(kf[2]));
+          mma16<F8>(sb[0], qg, e4m3x2_to_f16x2(kf[1]), e4m3x2_to_f16x2_hi(kf[1]));
+          mma16<F8>(sb[1], qg, e4m3x2_to_f16x2(kf[3]), e4m3x2_to_f16x2_hi(kf[3]));
         }
       }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sa[nt][j] += sb[nt][j];
       // ---- scale, mask ----
       const int pos = CHUNK * s.chunk(ka + (int)(q - q0));
       // every row sees every slot of the chunk
       const bool whole = pos + CHUNK - 1 <= p0 && (P.window == 0 || pos >= L - P.window || pos + CHUNK <= P.sinks);
+      // bits 0..n-1 of a chunk's 16 slots
+      auto below = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xFFFFu : (1u << n) - 1u; };
+      uint32_t seen0 = 0xFFFFu, seen1 = 0xFFFFu, any = 0xFFFFu;  // by this thread's rows; by some row
+      if (!whole) {
+        auto seen_by = [&](int p) {
+          return below(imin(p + 1, L) - pos) & (P.window == 0 ? 0xFFFFu : ~below(p - P.window + 1 - pos) | below(P.sinks - pos));
+        };
+        seen0 = seen_by(p0 + i0);
+        seen1 = seen_by(p0 + i1);
+        any = below(L - pos) & (~below(lo - pos) | below(P.sinks - pos));
+      }
       float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float v = sa[nt][j] * ((j & 2) ? sc1 : sc0);
-          if (!whole) {
-            const int t = pos + 8 * nt + 2 * tq + (j & 1);
-            const int p = p0 + ((j & 2) ? i1 : i0);
-            const bool seen = t <= p && t < L && (P.window == 0 || t > p - P.window || t < P.sinks);
-            v = seen ? v : -INFINITY;
-          }
+          if (!whole) v = (((j & 2) ? seen1 : seen0) >> (8 * nt + 2 * tq + (j & 1)) & 1u) ? v : -INFINITY;
           sa[nt][j] = v;
           if (j & 2) mx1 = fmaxf(mx1, v); else mx0 = fmaxf(mx0, v);
         }
@@ -482,10 +500,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       // ---- O += P V; what no row sees may hold anything and counts as zero ----
       uint32_t vm0 = 0xFFFFFFFFu, vm1 = 0xFFFFFFFFu;
       if (!whole) {
-        auto seen = [&](int t) { return t < L && (t >= lo || t < P.sinks); };
-        const int t = pos + 2 * tq;
-        vm0 = (seen(t) ? 0xFFFFu : 0u) | (seen(t + 1) ? 0xFFFF0000u : 0u);
-        vm1 = (seen(t + 8) ? 0xFFFFu : 0u) | (seen(t + 9) ? 0xFFFF0000u : 0u);
+        const uint32_t x = any >> (2 * tq);
+        vm0 = (x & 1u ? 0xFFFFu : 0u) | (x & 2u ? 0xFFFF0000u : 0u);
+        vm1 = (x & 0x100u ? 0xFFFFu : 0u) | (x & 0x200u ? 0xFFFF0000u : 0u);
       }
 #pragma unroll
       for (int np = 0; np < (F8 ? NT / 4 : NT / 2); ++np) {
