@@ -9,13 +9,19 @@
 // What bounds it: every visible slot of K and V is read once and meets
 // M*Hq/Hkv query rows, so HBM (and, for short sequences, latency).  Hence:
 //  * The work of a call is a line of units, one unit a 16-slot chunk of one
-//    (sequence, KV head); only chunks that some row sees are on it.  Every
-//    CTA (one per SM) finds the line's length from the device's lengths and
-//    takes an equal, contiguous piece, so ragged batches and long single
-//    sequences load all SMs alike and the host needs no lengths.
-//  * Two producer warps stream chunks into a shared-memory ring by TMA, one
+//    (sequence, KV head); only chunks that some row sees are on it, and each
+//    (sequence, head) begins with HEAD_COST more for what it costs beside its
+//    chunks (queries, join, output).  Every CTA (one per SM) finds the line's
+//    length from the device's lengths and takes an equal, contiguous piece, so
+//    ragged batches and long single sequences load all SMs alike and the host
+//    needs no lengths.  Where heads are few, each is cut into equal pieces of
+//    its own instead, so that no CTA has two, if these are no longer than the
+//    line's.
+//  * Four producer warps stream chunks into a shared-memory ring by TMA, one
 //    5-D copy for K and one for V (page, head, 64-column group, slot, column),
-//    looking pages up 32 chunks ahead.  A chunk never crosses a page.
+//    looking pages up 32 chunks ahead.  A chunk never crosses a page.  (A copy
+//    and the wait before it keep a warp for about 250 ns, longer than a chunk's
+//    share of HBM: hence four.)
 //  * Each of eight consumer warps takes every (8/MT)-th chunk for one 16-row
 //    tile of query rows and keeps its own running maximum, sum and O in
 //    registers: the scores' accumulator layout is the next product's operand
@@ -48,6 +54,8 @@ constexpr int REGS_PRODUCER = 72, REGS_CONSUMER = 216;
 constexpr int MAX_B = 4096;
 constexpr int MAX_R = 128;           // query rows per KV head: eight 16-row tiles
 constexpr int MAX_STAGES = 24;
+constexpr int HEAD_COST = 12;        // chunks' time that a (sequence, head) takes beside its chunks
+constexpr int MAX_EVEN_B = 64;       // sequences up to which heads are cut evenly
 constexpr float RESCALE = 8.f;       // log2 of the largest probability against an old maximum
 constexpr size_t SMEM_LIMIT = 227 * 1024;
 
@@ -134,7 +142,7 @@ struct Layout {
   static constexpr int STAGE = 2 * TILE;
   static constexpr int QS = 1024;                         // after the barriers
   static constexpr int QBYTES = MT * 16 * D * 2;
-  static constexpr int RS = D + 8;                        // scratch row stride, floats
+  static constexpr int RS = F8 ? D + 16 : D + 8;          // scratch row stride, floats: no bank met twice
   static constexpr int SCRATCH = QS + QBYTES;
   static constexpr int SBYTES = NCW * 8 * RS * 4;
   static constexpr int ML = SCRATCH + SBYTES;             // [NCW][16][2] floats
@@ -157,6 +165,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t *full = reinterpret_cast<uint64_t *>(smem);
   uint64_t *empty = full + MAX_STAGES;
   int *wsum = reinterpret_cast<int *>(smem + 512);  // scan: warp totals
+  int *cuts = reinterpret_cast<int *>(smem + 640);  // even cuts: pieces before sequence b, per head
   uint8_t *qs = smem + LY::QS;
   float *scratch = reinterpret_cast<float *>(smem + LY::SCRATCH);
   float *sml = reinterpret_cast<float *>(smem + LY::ML);
@@ -164,7 +173,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   float *qsc = reinterpret_cast<float *>(smem + LY::QSC);
   uint8_t *ring = smem + LY::RING;
   const int NST = P.stages;
-  int *pre = reinterpret_cast<int *>(ring + NST * LY::STAGE);  // pre[b]: chunks before sequence b
+  int *pre = reinterpret_cast<int *>(ring + NST * LY::STAGE);  // pre[b]: units before sequence b, per head
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid < NST) {
@@ -174,11 +183,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   pdl_wait();
 
-  // ---- the line of units: prefix sums of the sequences' chunk counts ----
+  // ---- the line of units: prefix sums of the sequences' costs ----
   int total = 0;
   for (int b0 = 0; b0 < P.B; b0 += THREADS) {
     const int b = b0 + tid;
-    const int n = b < P.B ? span_of(P, length_of(P, b)).count() : 0;
+    const int chunks = b < P.B ? span_of(P, length_of(P, b)).count() : 0;
+    const int n = chunks > 0 ? chunks + HEAD_COST : 0;
     int x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -201,8 +211,43 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
 
   const int units = total * P.Hkv, ctas = (int)gridDim.x;
-  const int per = imax(P.min_units, (int)(((unsigned)units + (unsigned)ctas - 1) / (unsigned)ctas));
+  const int per = imax(P.min_units + HEAD_COST, (int)(((unsigned)units + (unsigned)ctas - 1) / (unsigned)ctas));
   const int u0 = (int)lmin(units, (long long)per * blockIdx.x), u1 = (int)lmin(units, (long long)u0 + per);
+
+  // ---- even cuts, where heads are few: the shortest piece length for which
+  // the pieces are no more than the CTAs (every warp works it out) ----
+  bool even = false;
+  if (P.by_head && P.B <= MAX_EVEN_B) {
+    auto chunks_of = [&](int b) { return b < P.B ? imax(0, pre[b + 1] - pre[b] - HEAD_COST) : 0; };
+    const int n0 = chunks_of(lane), n1 = chunks_of(lane + 32);
+    const int all = __reduce_add_sync(0xffffffffu, n0 + n1) * P.Hkv;
+    int len = imax(P.min_units, (all + ctas - 1) / ctas), pieces = 0;
+    auto cut = [&]() {
+      pieces = (n0 + len - 1) / len + (P.B > 32 ? (n1 + len - 1) / len : 0);
+      return __reduce_add_sync(0xffffffffu, pieces) * P.Hkv;
+    };
+    // longer at every step by half the share that the last one overshot
+    int x = cut();
+    while (x > ctas && len <= per) {
+      len += 1 + (int)((float)len * (float)(x - ctas) / (float)(2 * ctas));
+      x = cut();
+    }
+    even = x <= ctas && len <= per;
+    if (even && warp == 0) {
+      int x0 = (n0 + len - 1) / len, x1 = (n1 + len - 1) / len;
+      const int own0 = x0, own1 = x1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y0 = __shfl_up_sync(0xffffffffu, x0, o), y1 = __shfl_up_sync(0xffffffffu, x1, o);
+        if (lane >= o) x0 += y0, x1 += y1;
+      }
+      const int first32 = __shfl_sync(0xffffffffu, x0, 31);
+      cuts[lane] = x0 - own0;
+      cuts[lane + 32] = first32 + x1 - own1;
+      if (lane == 31) cuts[64] = first32 + x1;
+    }
+  }
+  __syncthreads();
 
   // sequence of unit u < units
   auto seq_of = [&](int u) {
@@ -213,6 +258,50 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (pre[mid] <= c) lo = mid; else hi = mid - 1;
     }
     return lo;  // the last sequence that starts at or before c, so it is not empty
+  };
+  // The pieces of this CTA, one after the other: chunks ka..kb-1 of n of (b, h);
+  // `count`: the pieces of the head, which lie in consecutive CTAs.
+  struct Piece {
+    int u, b, b0, h, n, ka, kb, count;  // b0: the piece's sequence; b: where the search goes on
+  };
+  auto start = [&]() {
+    Piece x{};
+    x.u = even ? 0 : u0;
+    x.b = !even && u0 < u1 ? seq_of(u0) : 0;
+    return x;
+  };
+  auto next = [&](Piece &x) {
+    if (even) {
+      if (x.u > 0) return false;
+      x.u = 1;
+      const int c = blockIdx.x;
+      if (c >= cuts[P.B] * P.Hkv) return false;
+      while (cuts[x.b + 1] * P.Hkv <= c) ++x.b;
+      const int in = c - cuts[x.b] * P.Hkv;
+      x.count = cuts[x.b + 1] - cuts[x.b];
+      x.h = in / x.count;
+      const int i = in - x.h * x.count;
+      x.n = pre[x.b + 1] - pre[x.b] - HEAD_COST;
+      x.ka = (int)((long long)x.n * i / x.count);
+      x.kb = (int)((long long)x.n * (i + 1) / x.count);
+      x.b0 = x.b;
+      return true;
+    }
+    while (x.u < u1) {
+      while (pre[x.b + 1] == pre[x.b]) ++x.b;  // (a unit follows: a non-empty sequence exists)
+      const int cost = pre[x.b + 1] - pre[x.b], head0 = pre[x.b] * P.Hkv;
+      x.h = (x.u - head0) / cost;
+      const int at = head0 + x.h * cost, xa = x.u - at, xb = imin(cost, xa + (u1 - x.u));
+      x.n = cost - HEAD_COST;
+      x.ka = imax(0, xa - HEAD_COST);
+      x.kb = imax(0, xb - HEAD_COST);
+      x.u += xb - xa;
+      x.count = (at + cost - 1) / per - (at + HEAD_COST) / per + 1;
+      x.b0 = x.b;
+      if (x.h == P.Hkv - 1 && xb == cost) ++x.b;
+      if (x.ka < x.kb) return true;
+    }
+    return false;
   };
 
   if (warp >= NCW) {
@@ -228,12 +317,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     uint32_t q = 0, parity = 1;
     int slot = 0;
-    int b = u0 < u1 ? seq_of(u0) : 0;
-    for (int u = u0; u < u1 && ok;) {
-      while (pre[b + 1] == pre[b]) ++b;  // (a unit follows: a non-empty sequence exists)
-      const int n = pre[b + 1] - pre[b];
-      const int in = u - pre[b] * P.Hkv, h = in / n, ka = in - h * n;
-      const int kb = imin(n, ka + (u1 - u));
+    for (Piece x = start(); ok && next(x);) {
+      const int b = x.b0, h = x.h, ka = x.ka, kb = x.kb;
       const Span s = span_of(P, length_of(P, b));
       const int *row = P.table + (long long)b * P.table_stride;
       auto page_at = [&](int k) {
@@ -266,8 +351,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
-      u += kb - ka;
-      if (h == P.Hkv - 1 && kb == n) ++b;
     }
     if (!ok && lane == 0) {  // a wait ran out: no copy may outlive the CTA
       const uint32_t first = q > (uint32_t)NST ? q - NST : 0u;
@@ -302,12 +385,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (!P.by_head && tid == 0) P.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
 
-  int b = u0 < u1 ? seq_of(u0) : 0;
-  for (int u = u0; u < u1;) {
-    while (pre[b + 1] == pre[b]) ++b;
-    const int n = pre[b + 1] - pre[b];
-    const int in = u - pre[b] * P.Hkv, h = in / n, ka = in - h * n;
-    const int kb = imin(n, ka + (u1 - u));
+  for (Piece piece = start(); next(piece);) {
+    const int b = piece.b0, h = piece.h, n = piece.n, ka = piece.ka, kb = piece.kb;
     const Span s = span_of(P, length_of(P, b));
     const int L = s.L, p0 = L - P.M;  // position of row 0
     const int lo = first_seen(P, L);
@@ -592,8 +671,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                           o[2 * c + 1][2 * half + 1] * w);
       }
       named_barrier(1, NCW * 32);
-      for (int x = tid; x < MT * 8 * (D / 4); x += NCW * 32) {
-        const int rr = x / (D / 4), d = (x % (D / 4)) * 4;
+#pragma unroll(MT < 4 ? MT * 2 : 4)
+      for (int x = 0; x < MT * 8 * (D / 4) / (NCW * 32); ++x) {
+        const int rr = (x * NCW * 32 + tid) / (D / 4), d = (tid % (D / 4)) * 4;
         const int r = 16 * (rr >> 3) + 8 * half + (rr & 7);
         if (r >= P.R) continue;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -624,18 +704,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       named_barrier(1, NCW * 32);
     }
-    // the head's first piece names its pieces: CTAs blockIdx.x .. of its last unit
+    // the head's first piece names its pieces
     if (tid == 0 && starts) {
       const int hh = b * P.Hkv + h;
-      const int last = pre[b] * P.Hkv + (h + 1) * n - 1;
-      const int4 d = make_int4(hh, (int)blockIdx.x, ends ? 0 : last / per - (int)blockIdx.x + 1, 0);
+      const int4 d = make_int4(hh, (int)blockIdx.x, ends ? 0 : piece.count, 0);
       if (P.by_head)
         P.desc[hh] = d;
       else if (!ends)
         P.desc[blockIdx.x] = d;
     }
-    u += kb - ka;
-    if (h == P.Hkv - 1 && ends) ++b;
   }
   pdl_launch_dependents();
 }
@@ -831,7 +908,7 @@ sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const int32_t *
   if (!paged::aligned(block_table, 4) || !paged::aligned(kv_lens, 4)) return SV_ERR_INVALID_ARG;
   // positions are 32-bit (with room for a window), and so is the line of units
   const long long cap = (long long)table_width * cache->page_size;
-  if (cap > 0x40000000LL || window > 0x40000000 || cap / paged::CHUNK * imax(B, 1) > 0x7fffffffLL / Hkv)
+  if (cap > 0x40000000LL || window > 0x40000000 || (cap / paged::CHUNK + paged::HEAD_COST) * imax(B, 1) > 0x7fffffffLL / Hkv)
     return SV_ERR_UNSUPPORTED;
   if (B == 0) return SV_OK;
   const int sms = imin(device_sm_count(), paged::MAX_CTAS);
