@@ -21,7 +21,8 @@
 //    5-D copy for K and one for V (page, head, 64-column group, slot, column),
 //    looking pages up 32 chunks ahead.  A chunk never crosses a page.  (A copy
 //    and the wait before it keep a warp for about 250 ns, longer than a chunk's
-//    share of HBM: hence four.)
+//    share of HBM: hence four.  Waiting for several chunks' slots before their
+//    copies costs more than it hides: 119 -> 129 us for 200000 slots of 4 x 256.)
 //  * Each of eight consumer warps takes every (8/MT)-th chunk for one 16-row
 //    tile of query rows and keeps its own running maximum, sum and O in
 //    registers: the scores' accumulator layout is the next product's operand
@@ -53,7 +54,7 @@ constexpr int THREADS = (NCW + NPW) * 32;
 constexpr int REGS_PRODUCER = 72, REGS_CONSUMER = 216;
 constexpr int MAX_B = 4096;
 constexpr int MAX_R = 128;           // query rows per KV head: eight 16-row tiles
-constexpr int MAX_STAGES = 24;
+constexpr int MAX_STAGES = 32;
 constexpr int HEAD_COST = 12;        // chunks' time that a (sequence, head) takes beside its chunks
 constexpr int MAX_EVEN_B = 64;       // sequences up to which heads are cut evenly
 constexpr float RESCALE = 8.f;       // log2 of the largest probability against an old maximum
@@ -136,8 +137,15 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
     mma_bf16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
 }
 
+// Ring slots of n chunks that are taken N at a time.
+template <int N>
+__host__ __device__ constexpr int padded(int n) { return (n + N - 1) / N * N; }
+
 template <int D, bool F8, int MT>
 struct Layout {
+  // Chunks that a consumer warp takes at a time.  Two need twice the ring: one
+  // set in work, one under way.
+  static constexpr int NCH = F8 && MT > 1 ? 2 : 1;
   static constexpr int TILE = CHUNK * D * (F8 ? 1 : 2);  // bytes of a chunk of K (or V)
   static constexpr int STAGE = 2 * TILE;
   static constexpr int QS = 1024;                         // after the barriers
@@ -157,7 +165,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     paged_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                  const Params P) {
   using LY = Layout<D, F8, MT>;
-  constexpr int NL = NCW / MT;  // chunks in flight among the consumer warps
+  constexpr int NL = NCW / MT;  // warps that take turns
+  constexpr int NCH = LY::NCH;
   constexpr int NKS = D / 16;
   constexpr int NT = D / 8;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -328,10 +337,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         return pg;
       };
       int next = page_at(ka + lane);
-      for (int k0 = ka; k0 < kb && ok; k0 += 32) {
+      const int kp = ka + padded<NCH>(kb - ka);  // the slot that fills up a pair gets no copy
+      for (int k0 = ka; k0 < kp && ok; k0 += 32) {
         const int page = next;
         next = page_at(k0 + 32 + lane);
-        const int m = imin(32, kb - k0);
+        const int m = imin(32, kp - k0);
         const int at = (s.chunk(imin(k0 + lane, kb - 1)) % cpp) * CHUNK;
         for (int i = 0; i < m; ++i, ++q) {
           if ((int)(q & 1) == turn) {
@@ -339,10 +349,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], parity, P.err));
             if (!ok) break;
             if (lane == 0) {
-              mbar_arrive_expect_tx(&full[slot], LY::TILE);
-              // a page out of range reads zeros (the copy is clipped to the cache)
-              tma_load_5d(ring + slot * LY::STAGE + (is_v ? LY::TILE : 0), is_v ? &mapV : &mapK, 0, sl, 0, h, pg,
-                          &full[slot], pol);
+              if (k0 + i >= kb) {
+                mbar_arrive(&full[slot]);
+              } else {
+                mbar_arrive_expect_tx(&full[slot], LY::TILE);
+                // a page out of range reads zeros (the copy is clipped to the cache)
+                tma_load_5d(ring + slot * LY::STAGE + (is_v ? LY::TILE : 0), is_v ? &mapV : &mapK, 0, sl, 0, h, pg,
+                            &full[slot], pol);
+              }
             }
           }
           if (++slot == NST) {
@@ -465,85 +479,122 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[nt][j] = 0.f;
 
-    const uint32_t q1 = q0 + (uint32_t)(kb - ka);
-    // this warp's first chunk: the least q >= q0 with q % NL == cl
-    for (uint32_t q = q0 + (uint32_t)((cl - (int)(q0 % NL) + NL) % NL); q < q1; q += NL) {
-      const int slot = (int)(q % (uint32_t)NST);
-      if (ok) ok = mbar_wait(&full[slot], (q / (uint32_t)NST) & 1, P.err);
-      if (!ok) continue;
-      const uint32_t kt = smem_u32(ring + slot * LY::STAGE), vt = kt + LY::TILE;
-      // ---- S = Q K^T, 16 rows x 16 slots ----
-      // (two sums per tile, of the even and the odd steps: a product waits for
-      // the one before it on the same sum)
-      float sa[2][4], sb[2][4];
+    const uint32_t q1 = q0 + (uint32_t)padded<NCH>(kb - ka);
+    auto load_q = [&](int ks, uint32_t (&qf)[4]) {
+      if (QREG) {
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sa[nt][j] = sb[nt][j] = 0.f;
-      auto load_q = [&](int ks, uint32_t (&qf)[4]) {
-        if (QREG) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) qf[t] = qa[QREG ? ks : 0][t];
-        } else {
-          ldmatrix_x4(qf, qtile + swz16(qr, 2 * ks + (lane >> 4)));
-        }
-      };
-      const int kr = 8 * (lane >> 4) + (lane & 7), kc = (lane >> 3) & 1;
-      if (!F8) {
-#pragma unroll
-        for (int ks = 0; ks < NKS; ks += 2) {
-          uint32_t ka[4], kb[4], qf[4], qg[4];
-          ldmatrix_x4(ka, kt + swz16(kr, 2 * ks + kc));
-          ldmatrix_x4(kb, kt + swz16(kr, 2 * ks + 2 + kc));
-          load_q(ks, qf);
-          load_q(ks + 1, qg);
-          mma16<F8>(sa[0], qf, ka[0], ka[1]);
-          mma16<F8>(sa[1], qf, ka[2], ka[3]);
-          mma16<F8>(sb[0], qg, kb[0], kb[1]);
-          mma16<F8>(sb[1], qg, kb[2], kb[3]);
-        }
+        for (int t = 0; t < 4; ++t) qf[t] = qa[QREG ? ks : 0][t];
       } else {
-#pragma unroll
-        for (int kp = 0; kp < NKS / 2; ++kp) {
-          uint32_t kf[4], qf[4], qg[4];
-          ldmatrix_x4(kf, kt + swz16(kr, 2 * kp + kc));
-          load_q(2 * kp, qf);
-          load_q(2 * kp + 1, qg);
-          mma16<F8>(sa[0], qf, e4m3x2_to_f16x2(kf[0]), e4m3x2_to_f16x2_hi(kf[0]));
-          mma16<F8>(sa[1], qf, e4m3x2_to_f16x2(kf[2]), e4m3x2_to_f16x2_hi(kf[2]));
-          mma16<F8>(sb[0], qg, e4m3x2_to_f16x2(kf[1]), e4m3x2_to_f16x2_hi(kf[1]));
-          mma16<F8>(sb[1], qg, e4m3x2_to_f16x2(kf[3]), e4m3x2_to_f16x2_hi(kf[3]));
-        }
+        ldmatrix_x4(qf, qtile + swz16(qr, 2 * ks + (lane >> 4)));
       }
+    };
+    const int kr = 8 * (lane >> 4) + (lane & 7), kc = (lane >> 3) & 1;       // K fragments: slot, group
+    const int vr = 8 * ((lane >> 3) & 1) + (lane & 7), vc = lane >> 4;       // V fragments
+    // this warp's first chunks: the least q >= q0 with q / NCH % NL == cl
+    uint32_t q = q0 + (uint32_t)(NCH * ((cl - (int)(q0 / NCH % NL) + NL) % NL));
+    int at = (int)(q % (uint32_t)NST);  // its ring slot
+    uint32_t parity = (q / (uint32_t)NST) & 1;
+    for (; q < q1; q += NCH * NL) {
+      uint32_t kt[NCH];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sa[nt][j] += sb[nt][j];
-      // ---- scale, mask ----
-      const int pos = CHUNK * s.chunk(ka + (int)(q - q0));
-      // every row sees every slot of the chunk
-      const bool whole = pos + CHUNK - 1 <= p0 && (P.window == 0 || pos >= L - P.window || pos + CHUNK <= P.sinks);
-      // bits 0..n-1 of a chunk's 16 slots
-      auto below = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xFFFFu : (1u << n) - 1u; };
-      uint32_t seen0 = 0xFFFFu, seen1 = 0xFFFFu, any = 0xFFFFu;  // by this thread's rows; by some row
-      if (!whole) {
-        auto seen_by = [&](int p) {
-          return below(imin(p + 1, L) - pos) & (P.window == 0 ? 0xFFFFu : ~below(p - P.window + 1 - pos) | below(P.sinks - pos));
-        };
-        seen0 = seen_by(p0 + i0);
-        seen1 = seen_by(p0 + i1);
-        any = below(L - pos) & (~below(lo - pos) | below(P.sinks - pos));
+      for (int c = 0; c < NCH; ++c) {
+        kt[c] = smem_u32(ring + (at + c) * LY::STAGE);
+        if (ok) ok = mbar_wait(&full[at + c], parity, P.err);
       }
-      float mx0 = -INFINITY, mx1 = -INFINITY;
+      const int now = at;
+      at += NCH * NL;
+      if (at >= NST) {
+        at -= NST;
+        parity ^= 1;
+      }
+      if (!ok) continue;
+      // ---- S = Q K^T, 16 rows x 16 slots (of each of the chunks) ----
+      // one chunk: two sums per tile, of the even and the odd steps (a product
+      // waits for the one before it on the same sum)
+      float sa[NCH][2][4], sb[2][4];
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float v = sa[nt][j] * ((j & 2) ? sc1 : sc0);
-          if (!whole) v = (((j & 2) ? seen1 : seen0) >> (8 * nt + 2 * tq + (j & 1)) & 1u) ? v : -INFINITY;
-          sa[nt][j] = v;
-          if (j & 2) mx1 = fmaxf(mx1, v); else mx0 = fmaxf(mx0, v);
+          sb[nt][j] = 0.f;
+#pragma unroll
+          for (int c = 0; c < NCH; ++c) sa[c][nt][j] = 0.f;
         }
+#pragma unroll
+      for (int kp = 0; kp < NKS / 2; ++kp) {
+        uint32_t ka4[NCH][4], kb4[NCH][4], qf[4], qg[4];
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+          if (!F8) {
+            ldmatrix_x4(ka4[c], kt[c] + swz16(kr, 4 * kp + kc));
+            ldmatrix_x4(kb4[c], kt[c] + swz16(kr, 4 * kp + 2 + kc));
+          } else {
+            uint32_t kf[4];
+            ldmatrix_x4(kf, kt[c] + swz16(kr, 2 * kp + kc));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              ka4[c][2 * t] = e4m3x2_to_f16x2(kf[2 * t]);
+              ka4[c][2 * t + 1] = e4m3x2_to_f16x2_hi(kf[2 * t]);
+              kb4[c][2 * t] = e4m3x2_to_f16x2(kf[2 * t + 1]);
+              kb4[c][2 * t + 1] = e4m3x2_to_f16x2_hi(kf[2 * t + 1]);
+            }
+          }
+        }
+        load_q(2 * kp, qf);
+        load_q(2 * kp + 1, qg);
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) mma16<F8>(sa[c][nt], qf, ka4[c][2 * nt], ka4[c][2 * nt + 1]);
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+            mma16<F8>(NCH == 1 ? sb[nt] : sa[c][nt], qg, kb4[c][2 * nt], kb4[c][2 * nt + 1]);
+      }
+      if (NCH == 1) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sa[0][nt][j] += sb[nt][j];
+      }
+      // ---- scale, mask ----
+      const int k0 = ka + (int)(q - q0);
+      int pos[NCH];
+      bool whole = true;  // every row sees every slot of the chunks
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        pos[c] = CHUNK * s.chunk(k0 + c);
+        whole = whole && k0 + c < kb && pos[c] + CHUNK - 1 <= p0 &&
+                (P.window == 0 || pos[c] >= L - P.window || pos[c] + CHUNK <= P.sinks);
+      }
+      uint32_t any[NCH];  // bit t: some row sees slot t
+      float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        uint32_t seen0 = 0xFFFFu, seen1 = 0xFFFFu;  // by this thread's rows
+        any[c] = 0xFFFFu;
+        if (!whole) {
+          auto below = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xFFFFu : (1u << n) - 1u; };  // bits 0..n-1
+          auto seen_by = [&](int p) {
+            return below(imin(p + 1, L) - pos[c]) &
+                   (P.window == 0 ? 0xFFFFu : ~below(p - P.window + 1 - pos[c]) | below(P.sinks - pos[c]));
+          };
+          const uint32_t real = k0 + c < kb ? 0xFFFFu : 0u;  // not there to fill up a pair
+          seen0 = seen_by(p0 + i0) & real;
+          seen1 = seen_by(p0 + i1) & real;
+          any[c] = below(L - pos[c]) & (~below(lo - pos[c]) | below(P.sinks - pos[c])) & real;
+        }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float v = sa[c][nt][j] * ((j & 2) ? sc1 : sc0);
+            if (!whole) v = (((j & 2) ? seen1 : seen0) >> (8 * nt + 2 * tq + (j & 1)) & 1u) ? v : -INFINITY;
+            sa[c][nt][j] = v;
+            if (j & 2) mx1 = fmaxf(mx1, v); else mx0 = fmaxf(mx0, v);
+          }
+      }
       // ---- running maximum, raised only by a chunk far above it ----
       if (__any_sync(0xffffffffu, mx0 > m0 + RESCALE || mx1 > m1 + RESCALE)) {
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
@@ -566,47 +617,55 @@ __global__ void __launch_bounds__(THREADS, 1)
         m1 = n1;
       }
       const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
-      uint32_t pa[4];
+      uint32_t pa[NCH][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const float x0 = ex2_approx(sa[nt][0] - b0), x1 = ex2_approx(sa[nt][1] - b0);
-        const float y0 = ex2_approx(sa[nt][2] - b1), y1 = ex2_approx(sa[nt][3] - b1);
-        l0 += x0 + x1;
-        l1 += y0 + y1;
-        pa[2 * nt] = F8 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
-        pa[2 * nt + 1] = F8 ? pack_f16x2(y0, y1) : pack_bf16x2(y0, y1);
-      }
+      for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const float x0 = ex2_approx(sa[c][nt][0] - b0), x1 = ex2_approx(sa[c][nt][1] - b0);
+          const float y0 = ex2_approx(sa[c][nt][2] - b1), y1 = ex2_approx(sa[c][nt][3] - b1);
+          l0 += x0 + x1;
+          l1 += y0 + y1;
+          pa[c][2 * nt] = F8 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
+          pa[c][2 * nt + 1] = F8 ? pack_f16x2(y0, y1) : pack_bf16x2(y0, y1);
+        }
       // ---- O += P V; what no row sees may hold anything and counts as zero ----
-      uint32_t vm0 = 0xFFFFFFFFu, vm1 = 0xFFFFFFFFu;
+      uint32_t vm[NCH][2];
       if (!whole) {
-        const uint32_t x = any >> (2 * tq);
-        vm0 = (x & 1u ? 0xFFFFu : 0u) | (x & 2u ? 0xFFFF0000u : 0u);
-        vm1 = (x & 0x100u ? 0xFFFFu : 0u) | (x & 0x200u ? 0xFFFF0000u : 0u);
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+          const uint32_t x = any[c] >> (2 * tq);
+          vm[c][0] = (x & 1u ? 0xFFFFu : 0u) | (x & 2u ? 0xFFFF0000u : 0u);
+          vm[c][1] = (x & 0x100u ? 0xFFFFu : 0u) | (x & 0x200u ? 0xFFFF0000u : 0u);
+        }
       }
 #pragma unroll
       for (int np = 0; np < (F8 ? NT / 4 : NT / 2); ++np) {
-        uint32_t vf[4];
-        ldmatrix_x4_trans(vf, vt + swz16(8 * ((lane >> 3) & 1) + (lane & 7), 2 * np + (lane >> 4)));
-        if (!whole) {
-          vf[0] &= vm0;
-          vf[1] &= vm1;
-          vf[2] &= vm0;
-          vf[3] &= vm1;
-        }
-        if (!F8) {
-          mma16<F8>(o[2 * np], pa, vf[0], vf[1]);
-          mma16<F8>(o[2 * np + 1], pa, vf[2], vf[3]);
-        } else {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {  // 16 columns: the even ones, then the odd ones
-            const uint32_t x = __byte_perm(vf[2 * e], 0u, 0x3120), y = __byte_perm(vf[2 * e + 1], 0u, 0x3120);
-            mma16<F8>(o[4 * np + 2 * e], pa, e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
-            mma16<F8>(o[4 * np + 2 * e + 1], pa, e4m3x2_to_f16x2_hi(x), e4m3x2_to_f16x2_hi(y));
+        for (int c = 0; c < NCH; ++c) {
+          uint32_t vf[4];
+          ldmatrix_x4_trans(vf, kt[c] + LY::TILE + swz16(vr, 2 * np + vc));
+          if (!whole) {
+            vf[0] &= vm[c][0];
+            vf[1] &= vm[c][1];
+            vf[2] &= vm[c][0];
+            vf[3] &= vm[c][1];
+          }
+          if (!F8) {
+            mma16<F8>(o[2 * np], pa[c], vf[0], vf[1]);
+            mma16<F8>(o[2 * np + 1], pa[c], vf[2], vf[3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // 16 columns: the even ones, then the odd ones
+              const uint32_t x = __byte_perm(vf[2 * e], 0u, 0x3120), y = __byte_perm(vf[2 * e + 1], 0u, 0x3120);
+              mma16<F8>(o[4 * np + 2 * e], pa[c], e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
+              mma16<F8>(o[4 * np + 2 * e + 1], pa[c], e4m3x2_to_f16x2_hi(x), e4m3x2_to_f16x2_hi(y));
+            }
           }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[slot]);
+      if (lane < NCH) mbar_arrive(&empty[now + lane]);
     }
     q0 = q1;
 
@@ -847,7 +906,7 @@ static cudaError_t launch_main(const CUtensorMap &mk, const CUtensorMap &mv, Par
   // chunks all fall to the same warps: a warp that came to a slot's next chunk
   // while another's was still on its way would take the barrier's phase of two
   // rounds ago for its own (phases are told apart by parity alone).
-  constexpr int TURNS = NCW / MT;
+  constexpr int TURNS = NCW / MT * LY::NCH;
   P.stages = imin(MAX_STAGES, (int)((SMEM_LIMIT - fixed) / LY::STAGE)) / TURNS * TURNS & ~1;
   return launch_early(paged_kernel<D, F8, MT>, dim3(ctas), dim3(THREADS), fixed + (size_t)P.stages * LY::STAGE, s,
                 mk, mv, P);
