@@ -21,11 +21,10 @@
 //    this one, whose rows two threads share (half of the keys each; they
 //    exchange one maximum a block).  Blocks are 128 keys there too: with 64, S
 //    takes twice the instructions, each as long to issue (about 55 clocks) as
-//    to execute.  A K block comes as two halves of its columns, a V block as
-//    two halves of its keys, 32 KB each.
+//    to execute.
 //  * Only blocks that some row of the CTA's tiles sees are visited.  One warp
-//    streams K and V blocks with TMA into a ring of 32 KB slots, another
-//    fetches the next tiles' queries as soon as the last S product is done.
+//    streams K with TMA, one V, each into a ring of its own; another fetches the
+//    next tiles' queries as soon as the last S product is done.
 //  * The maximum that P refers to is raised only when a block exceeds it by
 //    more than 2^8, so O is rarely rescaled; P is rounded to bf16 (relative
 //    2^-8 at most, as the second product's operand), sums are fp32.
@@ -42,10 +41,9 @@ constexpr int ROWS = 128;           // rows of a tile (TMEM lanes)
 constexpr int BN = 128;             // keys of a block
 constexpr int MAX_B = 4096;
 constexpr float RESCALE = 8.f;      // log2 of the largest P against an old maximum
-constexpr int SLOT = 32768;         // bytes of a ring slot
-// Shared memory: barriers, scan totals (256), halves' exchange (512), prefix
+// Shared memory: barriers, scan totals (320), halves' exchange (512), prefix
 // sums (2560; after the ring if longer), then the query tiles and the ring.
-constexpr int HEADER = 3072, PREFIX = 2560;
+constexpr int HEADER = 3072, PREFIX = 2560, SCAN = 320;
 
 // Two tiles a CTA (D = 128), or one with two S buffers and two threads a row.
 template <int D, int TILES>
@@ -54,12 +52,20 @@ struct Cfg {
   static constexpr int NSB = TILES == 2 ? 1 : 2;  // S buffers per tile
   static constexpr int SOFT = 8;                  // softmax warps
   static constexpr int HALVES = TILES == 2 ? 1 : 2;  // threads that share a row
-  static constexpr int PARTS = D / 128;         // ring slots of a K block (of a V block)
-  static constexpr int VK = BN / PARTS;         // keys of a V slot
+  // Ring slots: at D = 128 a whole block (fewer waits for the issuing warp,
+  // which two tiles keep busy: 376 against 392 us for 8192 rows of 32 heads),
+  // at D = 256 a quarter of one (freed earlier, so that more is on its way:
+  // 537 against 630 us for 8000 rows of 24 heads).
+  static constexpr int SLOT = D == 128 ? 32768 : 16384;
+  static constexpr int PARTS = BN * D * 2 / SLOT;  // slots of a K block (of a V block)
+  static constexpr int KG = D / 64 / PARTS;        // 64-column groups of a K slot
+  static constexpr int VK = BN / PARTS;            // keys of a V slot
   static constexpr int THREADS = (SOFT + 4) * 32;
   static constexpr int QBYTES = ROWS * D * 2;
   static constexpr int RING = HEADER + NT * QBYTES;
-  static_assert(BN * D * 2 == PARTS * SLOT, "block");
+  // slots of the K and the V ring: 160 KB, or 128 beside long prefix sums
+  static constexpr int NK = D == 128 ? 3 : 5, NV = D == 128 ? 2 : 5, LESS = D == 128 ? 2 : 4;
+  static_assert((NK + NV) * SLOT == 160 * 1024 && 2 * LESS * SLOT == 128 * 1024, "ring");
   // tensor memory: O per tile, then the S buffers (P over S)
   static constexpr uint32_t TO = 0, TS = NT * D;
   static_assert(NT * D + NT * NSB * BN <= 512, "tensor memory");
@@ -71,7 +77,8 @@ struct Params {
   unsigned *err;
   int B, Tq, Tk, Hkv, G, PT;  // PT: positions per tile
   float sl2e;
-  int window, sinks, slots;
+  int window, sinks;
+  int few_slots;  // long prefix sums take the place of some
 };
 
 struct Item {
@@ -148,7 +155,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
     window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                   const __grid_constant__ CUtensorMap mapV, const Params P) {
   using C = Cfg<D, TILES>;
-  constexpr int NT = C::NT, NSB = C::NSB, PARTS = C::PARTS, VK = C::VK;
+  constexpr int NT = C::NT, NSB = C::NSB, PARTS = C::PARTS, VK = C::VK, KG = C::KG, SLOT = C::SLOT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw;
   // The swizzled tiles need 1024-byte alignment, which the first dynamic byte
@@ -158,9 +165,9 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
     if (threadIdx.x == 0) atomicOr(P.err, ERR_TIMEOUT);
     return;
   }
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem);  // ring slots (at most 5)
-  uint64_t *empty = full + 5;
-  uint64_t *s_full = empty + 5;    // [2] per S buffer
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem);  // [2][5] slots of the K ring, of the V ring
+  uint64_t *empty = full + 10;     // [2][5]
+  uint64_t *s_full = empty + 10;   // [2] per S buffer
   uint64_t *p_full = s_full + 2;   // [2] per S buffer: P written over it
   uint64_t *o_done = p_full + 2;   // [2] per S buffer: the second product of its P done
   uint64_t *o_free = o_done + 2;   // [NT] O read out
@@ -169,16 +176,16 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
   uint64_t *idle = q_free + 1;
   uint64_t *p_half = idle + 1;     // [2] one S buffer: P of the first half of a block's keys written
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(p_half + 2);
-  int *wsum = reinterpret_cast<int *>(smem + 256);
+  int *wsum = reinterpret_cast<int *>(smem + SCAN);
   float *xchg = reinterpret_cast<float *>(smem + 512);  // [2][2 halves][ROWS] maxima, then sums
   uint8_t *qs = smem + HEADER;
   uint8_t *ring = smem + C::RING;
-  const int NS = P.slots;
-  int *pre = reinterpret_cast<int *>(NS == 5 ? smem + PREFIX : ring + (size_t)NS * SLOT);
+  const int NK = P.few_slots ? C::LESS : C::NK, NV = P.few_slots ? C::LESS : C::NV;
+  int *pre = reinterpret_cast<int *>(P.few_slots ? ring + 2 * C::LESS * SLOT : smem + PREFIX);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < 10; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -243,9 +250,13 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
   if (warp >= C::SOFT) {
     // 384 threads start with 168 registers each: 128*72 + 256*216 is the same total
     setmaxnreg_dec<72>();
-    if (warp == C::SOFT + 1) {
-      // ------------------------------------------- K and V blocks --
+    if (warp == C::SOFT + 1 || warp == C::SOFT + 3) {
+      // -------------------------------- K blocks, in the other V blocks --
       if (lane == 0) {
+        const bool is_v = warp == C::SOFT + 3;
+        uint64_t *landed = full + (is_v ? 5 : 0), *free = empty + (is_v ? 5 : 0);
+        uint8_t *slots = ring + (is_v ? NK * SLOT : 0);
+        const int NS = is_v ? NV : NK;
         bool ok = true;
         uint32_t q = 0, parity = 1;
         int slot = 0;
@@ -256,14 +267,12 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
           for (int j = 0; j < it.n && ok; ++j) {
             const int key = it.k0 + it.block(j) * BN;
 #pragma unroll
-            for (int x = 0; x < 2 * PARTS; ++x) {
-              if (ok) ok = mbar_wait(&empty[slot], parity, P.err);
+            for (int x = 0; x < PARTS; ++x) {
+              if (ok) ok = mbar_wait(&free[slot], parity, P.err);
               if (!ok) break;
-              mbar_arrive_expect_tx(&full[slot], SLOT);
-              if (x < PARTS)
-                tma_load_4d(ring + slot * SLOT, &mapK, 0, key, 2 * x, it.h, &full[slot]);
-              else
-                tma_load_4d(ring + slot * SLOT, &mapV, 0, key + (x - PARTS) * VK, 0, it.h, &full[slot]);
+              mbar_arrive_expect_tx(&landed[slot], SLOT);
+              tma_load_4d(slots + slot * SLOT, is_v ? &mapV : &mapK, 0, is_v ? key + x * VK : key, is_v ? 0 : x * KG, it.h,
+                          &landed[slot]);
               ++q;
               if (++slot == NS) {
                 slot = 0;
@@ -274,7 +283,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
         }
         if (!ok) {  // no copy may outlive the CTA
           const uint32_t first = q > (uint32_t)NS ? q - NS : 0u;
-          for (uint32_t qq = first; qq < q && mbar_wait(&full[qq % NS], (qq / NS) & 1, P.err); ++qq) {
+          for (uint32_t qq = first; qq < q && mbar_wait(&landed[qq % NS], (qq / NS) & 1, P.err); ++qq) {
           }
         }
       }
@@ -308,41 +317,31 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
       constexpr uint32_t IDO = tc::idesc_bf16_f32(ROWS, D, true);
       // descriptors: queries and keys K-major, values with rows along K
       const uint64_t dq = tc::smem_desc_sw128(smem_u32(qs), 16, 1024), dk = tc::smem_desc_sw128(smem_u32(ring), 16, 1024);
-      const uint64_t dv = tc::smem_desc_sw128(smem_u32(ring), VK * 128, 1024);
+      const uint64_t dv = tc::smem_desc_sw128(smem_u32(ring + NK * SLOT), VK * 128, 1024);
       const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32), k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32);
       const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
-      // warp-uniform, so that the products' operands stay in uniform registers
       const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
       const bool leader = tc::elect_one();
+      // After a wait that ran out the warp goes through the rest of the item
+      // without waiting or issuing, so that its lanes stay together.
       bool ok = true;
       auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (ok) ok = spin_wait(bar, parity, P.err);
-        ok = __all_sync(0xffffffffu, ok);
       };
-      // the next K and the next V slot of the ring
-      struct Cursor {
+      struct Cursor {  // a ring's next slot
         int slot;
         uint32_t parity;
-        __device__ __forceinline__ void step(int n, int NS) {
-          slot += n;
-          if (slot >= NS) {
-            slot -= NS;
+        __device__ __forceinline__ void step(int slots) {
+          if (++slot == slots) {
+            slot = 0;
             parity ^= 1;
           }
         }
       };
-      Cursor ck{0, 0}, cv{PARTS, 0};
+      Cursor ck{0, 0}, cv{0, 0};
       uint32_t c = 0;                     // items with work so far
       uint32_t sj[NT] = {}, pj[NT] = {};  // blocks of each tile: S issued, P consumed
       uint32_t oc[NT] = {};               // items of each tile
-      // S of one block for tile t, the leader's part: columns of K part x
-      auto issue_s = [&](int t, uint32_t sb, int x, int slot) {
-        const uint32_t ka = k_lo + slot * (SLOT / 16), d = tb + C::TS + sb * BN;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc::mma_bf16(d, q_lo + (t * C::QBYTES + (2 * x + (ks >> 2)) * ROWS * 128 + (ks & 3) * 32) / 16, q_hi,
-                       ka + ((ks >> 2) * BN * 128 + (ks & 3) * 32) / 16, k_hi, IDS, (x > 0 || ks > 0) ? 1u : 0u);
-      };
       for (int k = 0; k < rounds && ok; ++k) {
         const int id = item_id(k, items);
         if (id < 0) continue;
@@ -350,57 +349,58 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
         const int n = __shfl_sync(0xffffffffu, it.n, 0);
         if (n == 0) continue;
         const int nt = __shfl_sync(0xffffffffu, it.rows > P.PT ? NT : 1, 0);
-        wait(q_full, c & 1);
-        ++c;
-        // S of the first block (two S buffers: also of each next one) for all tiles
-        auto all_s = [&](bool last) {
+        // S of the next block for tiles ta..tb1-1; `release`: they are its last
+        auto issue_s = [&](int ta, int tb1, bool release, bool last) {
+          Cursor at = ck;
 #pragma unroll
           for (int x = 0; x < PARTS; ++x) {
-            wait(&full[ck.slot], ck.parity);
-            if (!ok) return;
+            if (ta == 0) wait(&full[at.slot], at.parity);  // (tile 1 follows tile 0)
             tc::fence_after_sync();
-            if (leader) {
+            if (leader && ok) {
+              const uint32_t ka = k_lo + at.slot * (SLOT / 16);
 #pragma unroll
-              for (int t = 0; t < NT; ++t)
-                if (t < nt) {
-                  const uint32_t sb = NSB == 2 ? (sj[0] & 1) : (uint32_t)t;
-                  issue_s(t, sb, x, ck.slot);
-                  if (x == PARTS - 1) tc::commit(&s_full[sb]);
-                }
-              tc::commit(&empty[ck.slot]);
+              for (int t = 0; t < NT; ++t) {
+                if (t < ta || t >= tb1) continue;
+                const uint32_t sb = NSB == 2 ? (sj[0] & 1) : (uint32_t)t;
+#pragma unroll
+                for (int ks = 0; ks < KG * 4; ++ks)
+                  tc::mma_bf16(tb + C::TS + sb * BN,
+                               q_lo + (t * C::QBYTES + (x * KG + (ks >> 2)) * ROWS * 128 + (ks & 3) * 32) / 16, q_hi,
+                               ka + ((ks >> 2) * BN * 128 + (ks & 3) * 32) / 16, k_hi, IDS,
+                               (x > 0 || ks > 0) ? 1u : 0u);
+                if (x == PARTS - 1) tc::commit(&s_full[sb]);
+              }
+              if (release) tc::commit(&empty[at.slot]);
               if (last && x == PARTS - 1) tc::commit(q_free);
             }
-            ck.step(1, NS);
+            at.step(NK);
           }
-          ck.step(PARTS, NS);
+          if (release) ck = at;
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            if (t < nt) ++sj[t];
+            if (t >= ta && t < tb1) ++sj[t];
         };
-        all_s(n == 1);
-        for (int j = 0; j < n && ok; ++j) {
+        wait(q_full, c & 1);
+        ++c;
+        issue_s(0, nt, true, n == 1);
+        for (int j = 0; j < n; ++j) {
           const bool more = j + 1 < n;
-          if (NSB == 2 && more) all_s(j + 2 == n);  // runs during this block's softmax
+          if (NSB == 2 && more) issue_s(0, 1, true, j + 2 == n);  // runs during this block's softmax
           // rows past the sequence's keys belong to others: they count as zero
           const int past = it.block(j) * BN + BN - it.nk;
-          if (NSB == 1) {  // one slot each for K and V
-            wait(&full[cv.slot], cv.parity);
-            if (more) wait(&full[ck.slot], ck.parity);
-          }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            if (t >= nt || !ok) continue;
+            if (t >= nt) continue;
             const uint32_t sb = NSB == 2 ? (pj[t] & 1) : (uint32_t)t;
             if (j == 0 && oc[t] > 0) wait(&o_free[t], (oc[t] - 1) & 1);
-            wait(NSB == 2 ? &p_full[sb] : &p_half[sb], (NSB == 2 ? pj[t] >> 1 : pj[t]) & 1);
+            if (NSB == 2) wait(&p_full[sb], (pj[t] >> 1) & 1);
+            Cursor at = cv;
 #pragma unroll
             for (int x = 0; x < PARTS; ++x) {
-              if (NSB == 2) wait(&full[cv.slot], cv.parity);
-              if (!ok) break;
-              // keys of this V slot that are past the end
-              const int gone = imin(VK, past - (PARTS - 1 - x) * VK);
+              if (t == 0) wait(&full[5 + at.slot], at.parity);
+              const int gone = imin(VK, past - (PARTS - 1 - x) * VK);  // keys of this slot that are past the end
               if (gone > 0 && t == 0) {
-                uint8_t *vb = ring + cv.slot * SLOT;
+                uint8_t *vb = ring + (NK + at.slot) * SLOT;
                 for (int y = lane; y < gone * (D / 8); y += 32) {
                   const int r = VK - gone + y / (D / 8), z = y % (D / 8);
                   *reinterpret_cast<uint4 *>(vb + (z >> 3) * VK * 128 + r * 128 + (z & 7) * 16) =
@@ -409,45 +409,35 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
                 fence_proxy_async();
                 __syncwarp();
               }
-              tc::fence_after_sync();
-              const uint32_t va = v_lo + cv.slot * (SLOT / 16);
-              auto issue_o = [&](int k0, int k1) {
+              // one S buffer: the first half of the keys while the second's P is made
+              constexpr int STEPS = NSB == 1 ? 2 : 1;
 #pragma unroll
-                for (int ks = k0; ks < k1; ++ks)
-                  tc::mma_bf16_ts(tb + C::TO + t * D, tb + C::TS + sb * BN + (x * (VK / 16) + ks) * 8,
-                                  va + ks * 2048 / 16, v_hi, IDO, (x > 0 || ks > 0) ? 1u : (uint32_t)j);
-              };
-              if (NSB == 1) {  // the first half of the keys while the second's P is made
-                if (leader) issue_o(0, 4);
-                wait(&p_full[sb], pj[t] & 1);
-                if (!ok) break;
+              for (int y = 0; y < STEPS; ++y) {
+                if (NSB == 1) wait(y == 0 ? &p_half[sb] : &p_full[sb], pj[t] & 1);
                 tc::fence_after_sync();
-              }
-              if (leader) {
-                issue_o(NSB == 1 ? 4 : 0, VK / 16);
-                if (x == PARTS - 1) tc::commit(&o_done[sb]);
-                if (t == nt - 1) tc::commit(&empty[cv.slot]);
-                if (NSB == 1 && more) {
-                  issue_s(t, (uint32_t)t, 0, ck.slot);
-                  tc::commit(&s_full[t]);
-                  if (t == nt - 1) {
-                    tc::commit(&empty[ck.slot]);
-                    if (j + 2 == n) tc::commit(q_free);
-                  }
+                if (leader && ok) {
+                  const uint32_t va = v_lo + at.slot * (SLOT / 16);
+#pragma unroll
+                  for (int ks = y * (VK / 16 / STEPS); ks < (y + 1) * (VK / 16 / STEPS); ++ks)
+                    tc::mma_bf16_ts(tb + C::TO + t * D, tb + C::TS + sb * BN + (x * (VK / 16) + ks) * 8,
+                                    va + ks * 2048 / 16, v_hi, IDO, (x > 0 || ks > 0) ? 1u : (uint32_t)j);
                 }
               }
-              if (t == nt - 1) cv.step(1, NS);
+              if (leader && ok) {
+                if (x == PARTS - 1) tc::commit(&o_done[sb]);
+                if (t == nt - 1) tc::commit(&empty[5 + at.slot]);
+              }
+              at.step(NV);
             }
+            if (t == nt - 1) cv = at;
             ++pj[t];
-            if (NSB == 1 && more) ++sj[t];
+            if (NSB == 1 && more) issue_s(t, t + 1, t == nt - 1, t == nt - 1 && j + 2 == n);
           }
-          cv.step(PARTS, NS);
-          if (NSB == 1 && more) ck.step(2, NS);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
           if (t < nt) ++oc[t];
-        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
       }
       if (leader) {  // every product issued above has completed before TMEM is released
         tc::commit(idle);
@@ -700,13 +690,13 @@ static sv_status run(const sv_rows *q, const sv_rows *k, const sv_rows *v, Param
   using C = Cfg<D, TILES>;
   CUtensorMap mq, mk, mv;
   if (!make_map(&mq, q, P.Tq, P.Hkv * P.G, D, true, P.G, P.PT, q->ptr) ||
-      !make_map(&mk, k, P.Tk, P.Hkv, D, false, BN, 2, q->ptr) ||
+      !make_map(&mk, k, P.Tk, P.Hkv, D, false, BN, C::KG, q->ptr) ||
       !make_map(&mv, v, P.Tk, P.Hkv, D, false, C::VK, D / 64, q->ptr))
     return SV_ERR_CUDA;
   const size_t prefix = ((size_t)P.B + 1) * 4;
-  P.slots = prefix <= HEADER - PREFIX ? 5 : 4;
-  const size_t smem = C::RING + (size_t)P.slots * SLOT + (P.slots == 5 ? 0 : prefix);
-  static_assert(C::RING + 5 * SLOT <= 227 * 1024 && C::RING + 4 * SLOT + (MAX_B + 1) * 4 <= 227 * 1024, "shared memory");
+  P.few_slots = prefix <= HEADER - PREFIX ? 0 : 1;
+  const size_t smem = C::RING + (P.few_slots ? 128 * 1024 + prefix : 160 * 1024);
+  static_assert(C::RING + 160 * 1024 <= 227 * 1024 && C::RING + 128 * 1024 + (MAX_B + 1) * 4 <= 227 * 1024, "shared memory");
   // at most one item more per sequence than the rows fill
   const long long items = ((long long)P.Tq / (P.PT * C::NT) + P.B) * P.Hkv;
   const int ctas = (int)lmin(items, sms);
