@@ -52,11 +52,10 @@ struct Cfg {
   static constexpr int NSB = TILES == 2 ? 1 : 2;  // S buffers per tile
   static constexpr int SOFT = 8;                  // softmax warps
   static constexpr int HALVES = TILES == 2 ? 1 : 2;  // threads that share a row
-  // Ring slots: at D = 128 a whole block (fewer waits for the issuing warp,
-  // which two tiles keep busy: 376 against 392 us for 8192 rows of 32 heads),
-  // at D = 256 a quarter of one (freed earlier, so that more is on its way:
-  // 537 against 630 us for 8000 rows of 24 heads).
-  static constexpr int SLOT = D == 128 ? 32768 : 16384;
+  // Ring slots: a whole K or V block at D = 128, at D = 256 half of its columns
+  // (K) or of its keys (V).  (Quarters are freed earlier, but the issuing warp's
+  // waits for them cost more: 526 against 473 us for 8000 rows of 24 heads.)
+  static constexpr int SLOT = 32768;
   static constexpr int PARTS = BN * D * 2 / SLOT;  // slots of a K block (of a V block)
   static constexpr int KG = D / 64 / PARTS;        // 64-column groups of a K slot
   static constexpr int VK = BN / PARTS;            // keys of a V slot
@@ -64,7 +63,7 @@ struct Cfg {
   static constexpr int QBYTES = ROWS * D * 2;
   static constexpr int RING = HEADER + NT * QBYTES;
   // slots of the K and the V ring: 160 KB, or 128 beside long prefix sums
-  static constexpr int NK = D == 128 ? 3 : 5, NV = D == 128 ? 2 : 5, LESS = D == 128 ? 2 : 4;
+  static constexpr int NK = 2, NV = 3, LESS = 2;
   static_assert((NK + NV) * SLOT == 160 * 1024 && 2 * LESS * SLOT == 128 * 1024, "ring");
   // tensor memory: O per tile, then the S buffers (P over S)
   static constexpr uint32_t TO = 0, TS = NT * D;
