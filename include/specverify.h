@@ -288,14 +288,25 @@ SV_API sv_status qk_norm_rope(const sv_rows *q, const sv_rows *k, const sv_rows 
  * value times k_scale[h] (v_scale[h]) is the key (value); scales: device fp32
  * [Hkv], > 0, NULL for 1 (and NULL at bf16).  k, v: device, 16-byte aligned;
  * strides positive multiples of 16 bytes.  page_size a multiple of 16, at
- * most 2^16; 1 <= num_pages < 2^31. */
+ * most 2^16; 1 <= num_pages < 2^31.
+ * maps: host, SV_PAGED_MAPS_BYTES bytes that paged_kv_maps made from these very
+ * fields, or NULL (paged_attn then makes them itself in every call, about
+ * 0.7 us of host time). */
 typedef struct {
   void *k, *v;
   const float *k_scale, *v_scale;
   int64_t page_stride, slot_stride, head_stride;
   int64_t num_pages;
   int32_t page_size, dtype;
+  const void *maps;
 } sv_paged_kv;
+
+/* The copy engine's descriptions of a cache of Hkv heads of D, for its `maps`:
+ * 8-byte aligned host memory.  To be made anew when a field of the cache
+ * changes; its contents (keys, values, scales) may.  Host code only. */
+#define SV_PAGED_MAPS_BYTES 256
+SV_API sv_status paged_kv_maps(const sv_paged_kv *cache, int Hkv, int D, void *maps_out,
+                               size_t maps_bytes);
 
 /* Writes T tokens' keys (normed and rotated on the way, as asked) and values
  * into the cache, and their queries (normed and rotated) to q_out in the same

@@ -111,6 +111,7 @@ def load():
             "rope_phases": (I, [P, I, P]),
             "qk_norm_rope": (I, [P, P, P, P, P, P, I, I, I, I, P]),
             "paged_kv_append": (I, [P, P, P, P, P, P, P, P, I, I, I, I, P]),
+            "paged_kv_maps": (I, [P, I, I, P, Z]),
             "paged_attn_workspace_bytes": (Z, [I, I, I, I, I]),
             "paged_attn": (I, [P, P, P, L, I, P, P, I, I, I, I, I, ctypes.c_float, I, I, P, Z, P]),
             "window_attn_workspace_bytes": (Z, [I, I, I, I]),
@@ -361,7 +362,8 @@ def gdn_verify(state, q, k, v, g, beta, o, tape=None, n_replay=0, stream=None):
 _ROWS = struct.Struct("Pqq")            # sv_rows
 _NORM = struct.Struct("PPff")           # sv_head_norm
 _ROTATION = struct.Struct("PPii")       # sv_rotation
-_PAGED_KV = struct.Struct("PPPPqqqqii")  # sv_paged_kv
+_PAGED_KV = struct.Struct("PPPPqqqqiiP")  # sv_paged_kv
+_PAGED_MAPS_BYTES = 256
 
 
 def _bad(where: str, status: int = SV_ERR_INVALID_ARG):
@@ -385,8 +387,8 @@ def _rows(t, tokens, heads, D, where):
 
 
 def _vector(t, dtype, n, where):
-    """Address of a contiguous CUDA tensor [n]."""
-    if t.dtype is not dtype or t.shape != (n,) or not t.is_cuda or (n > 1 and t.stride(0) != 1):
+    """Address of a contiguous CUDA tensor of n values."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
         _bad(where)
     return t.data_ptr()
 
@@ -419,7 +421,7 @@ def _norm_rotation(q_weight, k_weight, eps, weight_offset, positions, phases, in
     if phases is not None:
         if positions is None:
             _bad(where)
-        half = phases.shape[0]
+        half = phases.numel()
         rot = _ROTATION.pack(_vector(phases, torch.int64, half, where), _vector(positions, torch.int32, T, where),
                              2 * half, 1 if interleaved else 0)
     return norm, rot
@@ -444,7 +446,8 @@ class PagedKV:
     """A paged cache: k and v are CUDA tensors of one shape and one set of
     strides, [pages, slots, heads, D] ("NHD") or [pages, heads, slots, D]
     ("HND"), bf16 or float8_e4m3fn; with the latter, the stored value times
-    k_scale[head] (v_scale[head], fp32 [heads], None for 1) counts."""
+    k_scale[head] (v_scale[head], fp32 [heads], None for 1) counts.  Holds the
+    tensors and what the calls need of them, worked out once."""
 
     def __init__(self, k, v, layout: str = "NHD", k_scale=None, v_scale=None):
         w = "PagedKV"
@@ -457,12 +460,16 @@ class PagedKV:
         slot, head = (1, 2) if layout == "NHD" else (2, 1)
         self.k, self.v, self.k_scale, self.v_scale, self.layout = k, v, k_scale, v_scale, layout
         self.page_size, self.heads, self.D = k.shape[slot], k.shape[head], k.shape[3]
-        self.packed = _PAGED_KV.pack(
-            k.data_ptr(), v.data_ptr(),
-            0 if k_scale is None else _vector(k_scale, torch.float32, self.heads, w),
-            0 if v_scale is None else _vector(v_scale, torch.float32, self.heads, w),
-            k.stride(0), k.stride(slot), k.stride(head), k.shape[0], self.page_size,
-            SV_BF16 if k.dtype is torch.bfloat16 else SV_E4M3)
+        fields = (k.data_ptr(), v.data_ptr(),
+                  0 if k_scale is None else _vector(k_scale, torch.float32, self.heads, w),
+                  0 if v_scale is None else _vector(v_scale, torch.float32, self.heads, w),
+                  k.stride(0), k.stride(slot), k.stride(head), k.shape[0], self.page_size,
+                  SV_BF16 if k.dtype is torch.bfloat16 else SV_E4M3)
+        self.packed = _PAGED_KV.pack(*fields, 0)
+        if self.D in (128, 256):  # what paged_attn reads
+            self._maps = (ctypes.c_uint64 * (_PAGED_MAPS_BYTES // 8))()
+            _check(load().paged_kv_maps(self.packed, self.heads, self.D, self._maps, _PAGED_MAPS_BYTES), w)
+            self.packed = _PAGED_KV.pack(*fields, ctypes.addressof(self._maps))
 
 
 def paged_kv_append(k, v, cache: PagedKV, slots, q=None, q_out=None, positions=None, phases=None,
@@ -497,17 +504,19 @@ def paged_attn(q, cache: PagedKV, block_table, kv_lens, o, M: int, scale: float,
     none; sinks: first positions that stay visible under a window."""
     rows, Hq, D = q.shape
     w = "paged_attn"
-    B = kv_lens.shape[0]
-    if (D != cache.D or rows != B * M or block_table.dtype is not torch.int32 or block_table.dim() != 2
-            or block_table.shape[0] != B or not block_table.is_cuda):
+    B, width = block_table.shape
+    if (D != cache.D or rows != B * M or block_table.dtype is not torch.int32 or not block_table.is_cuda
+            or (workspace is not None and not workspace.is_cuda)):
         _bad(w)
     ts, es = block_table.stride()
-    if es != 1 and block_table.shape[1] != 1:
+    if es != 1 and width != 1:
         _bad(w)
-    _check(load().paged_attn(_rows(q, rows, Hq, D, w), cache.packed, block_table.data_ptr(), ts,
-                             block_table.shape[1], _vector(kv_lens, torch.int32, B, w),
-                             _rows(o, rows, Hq, D, w), B, M, Hq, cache.heads, D, scale, window, sinks,
-                             _ptr(workspace), _nbytes(workspace), _launch_stream(q, stream)), w)
+    status = load().paged_attn(_rows(q, rows, Hq, D, w), cache.packed, block_table.data_ptr(), ts, width,
+                               _vector(kv_lens, torch.int32, B, w), _rows(o, rows, Hq, D, w), B, M, Hq, cache.heads,
+                               D, scale, window, sinks, _ptr(workspace), _nbytes(workspace),
+                               _launch_stream(q, stream))
+    if status:
+        _check(status, w)
 
 
 def window_attn_workspace_bytes(B: int, Hq: int, Hkv: int, D: int) -> int:
@@ -523,7 +532,9 @@ def window_attn(q, k, v, o, cu_q, cu_k, scale: float, window: int = 0, sinks: in
     Tk, Hkv, _ = k.shape
     w = "window_attn"
     n = cu_q.shape[0]
-    _check(load().window_attn(_rows(q, Tq, Hq, D, w), _rows(k, Tk, Hkv, D, w), _rows(v, Tk, Hkv, D, w),
-                              _rows(o, Tq, Hq, D, w), _vector(cu_q, torch.int32, n, w),
-                              _vector(cu_k, torch.int32, n, w), n - 1, Tq, Tk, Hq, Hkv, D, scale, window, sinks,
-                              _ptr(workspace), _nbytes(workspace), _launch_stream(q, stream)), w)
+    status = load().window_attn(_rows(q, Tq, Hq, D, w), _rows(k, Tk, Hkv, D, w), _rows(v, Tk, Hkv, D, w),
+                                _rows(o, Tq, Hq, D, w), _vector(cu_q, torch.int32, n, w),
+                                _vector(cu_k, torch.int32, n, w), n - 1, Tq, Tk, Hq, Hkv, D, scale, window, sinks,
+                                _ptr(workspace), _nbytes(workspace), _launch_stream(q, stream))
+    if status:
+        _check(status, w)

@@ -38,6 +38,8 @@
 // the slots, below the output's own rounding.
 // An e4m3 cache is converted in registers to fp16, which holds every e4m3
 // value exactly; the queries are scaled by a power of two per row to fit fp16.
+#include <cstring>
+
 #include "paged.cuh"
 
 namespace sv {
@@ -949,6 +951,20 @@ size_t paged_attn_workspace_bytes(int B, int M, int Hq, int Hkv, int D) {
   return sms <= 0 ? 0 : paged::ws_bytes_for(sms, M * (Hq / Hkv), D);
 }
 
+sv_status paged_kv_maps(const sv_paged_kv *cache, int Hkv, int D, void *maps_out, size_t maps_bytes) {
+  static_assert(2 * sizeof(CUtensorMap) == SV_PAGED_MAPS_BYTES, "maps");
+  if (Hkv < 1 || D < 1 || !maps_out || maps_bytes < SV_PAGED_MAPS_BYTES || !paged::aligned(maps_out, 8))
+    return SV_ERR_INVALID_ARG;
+  if (D != 128 && D != 256) return SV_ERR_UNSUPPORTED;
+  const sv_status cs = paged::check_cache(cache, D);
+  if (cs != SV_OK) return cs;
+  CUtensorMap m[2];
+  if (!paged::make_map(&m[0], cache->k, cache, D, Hkv) || !paged::make_map(&m[1], cache->v, cache, D, Hkv))
+    return SV_ERR_CUDA;
+  memcpy(maps_out, m, sizeof m);
+  return SV_OK;
+}
+
 sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const int32_t *block_table,
                      int64_t table_stride, int table_width, const int32_t *kv_lens, const sv_rows *o, int B,
                      int M, int Hq, int Hkv, int D, float scale, int window, int sinks, void *workspace,
@@ -976,8 +992,12 @@ sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const int32_t *
   if (!workspace || ws_bytes < paged::ws_bytes_for(sms, R, D)) return SV_ERR_WORKSPACE;
   if (!paged::aligned(workspace, 16)) return SV_ERR_INVALID_ARG;
   CUtensorMap mk, mv;
-  if (!paged::make_map(&mk, cache->k, cache, D, Hkv) || !paged::make_map(&mv, cache->v, cache, D, Hkv))
+  if (cache->maps) {
+    memcpy(&mk, cache->maps, sizeof mk);
+    memcpy(&mv, static_cast<const char *>(cache->maps) + sizeof mk, sizeof mv);
+  } else if (!paged::make_map(&mk, cache->k, cache, D, Hkv) || !paged::make_map(&mv, cache->v, cache, D, Hkv)) {
     return SV_ERR_CUDA;
+  }
   paged::Params P{};
   P.q = *q;
   P.o = *o;

@@ -27,7 +27,7 @@ def rows(sv, ptr=A, ts=1024, hs=128):
 
 
 def cache(sv, k=A, v=A, ks=0, vs=0, page=16 * 4 * 128, slot=4 * 128, head=128, pages=8, size=16, dtype=0):
-    return sv._PAGED_KV.pack(k, v, ks, vs, page, slot, head, pages, size, dtype)
+    return sv._PAGED_KV.pack(k, v, ks, vs, page, slot, head, pages, size, dtype, 0)
 
 
 def norm(sv, q=A, k=A, eps=1e-6, offset=0.0):
@@ -183,3 +183,14 @@ def test_window_attn_refusals(sv):
     assert call(k=rows(sv, ts=0)) == 2 and call(v=rows(sv, hs=0)) == 2   # repeated rows
     assert call(Tk=(1 << 30) + 1) == 2 and call(window=(1 << 30) + 1) == 2
     assert call(B=0) == 0 and call(Tq=0) == 0
+
+
+def test_paged_kv_maps_refusals(sv):
+    f = sv.load().paged_kv_maps
+    out = (ctypes.c_uint64 * 32)()
+    assert f(None, 4, 128, out, 256) == 1
+    assert f(cache(sv), 4, 128, None, 256) == 1 and f(cache(sv), 4, 128, out, 255) == 1
+    assert f(cache(sv), 0, 128, out, 256) == 1
+    assert f(cache(sv, k=A + 8), 4, 128, out, 256) == 1
+    assert f(cache(sv), 4, 64, out, 256) == 2
+    assert sv._PAGED_KV.size == 80
