@@ -14,6 +14,13 @@
  *   verify_attn  -- multi-row decode attention over a bf16 GQA KV cache
  *   spec_accept  -- exact Leviathan-Chen acceptance of the drafts
  *
+ * and what serving many sequences puts around its attention:
+ *
+ *   qk_norm_rope    -- head norms and rotation of projected queries and keys
+ *   paged_kv_append -- the same on the way into a paged bf16 or e4m3 cache
+ *   paged_attn      -- one-token / verify-row attention over that cache
+ *   window_attn     -- causal attention of packed prompts
+ *
  * Conventions shared by every entry point
  *   - Pointers marked "device" are caller-owned device memory on the current
  *     CUDA device; the library never allocates, frees or keeps them.
@@ -365,7 +372,9 @@ SV_API sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const in
  * Keys and values of a sequence hold finite values; rows of others, and rows
  * of no sequence, may hold anything.
  * Supported: D in {128, 256}; Hq % Hkv == 0; Hq/Hkv <= 128; 0 <= B <= 4096;
- *   Tq, Tk <= 2^30; strides of q, k and v above 0; scale > 0 and finite. */
+ *   Tq, Tk <= 2^30; strides of q, k and v above 0; scale > 0 and finite.
+ * One launch.  It needs no workspace at present: the query gives 0, and NULL
+ * with 0 bytes is accepted. */
 SV_API size_t window_attn_workspace_bytes(int B, int Hq, int Hkv, int D);
 SV_API sv_status window_attn(const sv_rows *q, const sv_rows *k, const sv_rows *v, const sv_rows *o,
                              const int32_t *cu_q, const int32_t *cu_k, int B, int Tq, int Tk, int Hq,

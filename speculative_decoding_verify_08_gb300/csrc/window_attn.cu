@@ -22,9 +22,14 @@
 //    exchange one maximum a block).  Blocks are 128 keys there too: with 64, S
 //    takes twice the instructions, each as long to issue (about 55 clocks) as
 //    to execute.
-//  * Only blocks that some row of the CTA's tiles sees are visited.  One warp
-//    streams K with TMA, one V, each into a ring of its own; another fetches the
-//    next tiles' queries as soon as the last S product is done.
+//  * Only blocks that some row of the CTA's tiles sees are visited; behind a
+//    window they begin at the first key seen, and up to 32 always visible first
+//    keys take the place of keys before it in the first block, so that they cost
+//    no block (8192 rows of 32 heads, window 1024, 4 first keys: 129 -> 122 us).
+//    (Blocks cut to whole groups of 32 keys cost every other block more than
+//    they save: 138 us.)
+//  * One warp streams K with TMA, one V, each into a ring of its own; another
+//    fetches the next tiles' queries as soon as the last S product is done.
 //  * The maximum that P refers to is raised only when a block exceeds it by
 //    more than 2^8, so O is rarely rescaled; P is rounded to bf16 (relative
 //    2^-8 at most, as the second product's operand), sums are fp32.
@@ -39,6 +44,7 @@ namespace window {
 
 constexpr int ROWS = 128;           // rows of a tile (TMEM lanes)
 constexpr int BN = 128;             // keys of a block
+constexpr int HEAD = 32;            // first keys that may share a block with others
 constexpr int MAX_B = 4096;
 constexpr float RESCALE = 8.f;      // log2 of the largest P against an old maximum
 // Shared memory: barriers, scan totals (320), halves' exchange (512), prefix
@@ -84,8 +90,11 @@ struct Item {
   int h, q0, k0;     // KV head; first row of the packed queries and keys
   int rows;          // positions of the item
   int p0, nk;        // position of its first row; keys of the sequence
-  int ns, w0, n;     // blocks: 0..ns-1, then w0.. ; n in all
-  __device__ __forceinline__ int block(int j) const { return j < ns ? j : j - ns + w0; }
+  // Blocks: ns over the first keys, then those from key w0 on; n in all.  Up to
+  // HEAD first keys far from the window (ns = 0, w0 > 0, sinks) need no block:
+  // keys 0..HEAD-1 stand in the first block's first rows, for w0..w0+HEAD-1.
+  int ns, skip, n;
+  __device__ __forceinline__ int base(int j) const { return j * BN + (j < ns ? 0 : skip); }
 };
 
 // Rows of sequence b, 0 if its offsets are out of order or out of range.
@@ -114,16 +123,18 @@ __device__ __forceinline__ Item item_at(const Params &P, const int *pre, int id)
   const int nq = P.cu_q[b + 1] - P.cu_q[b];
   it.k0 = P.cu_k[b];
   it.nk = P.cu_k[b + 1] - it.k0;
-  const int first = tile * span;
-  it.q0 = P.cu_q[b] + first;
-  it.rows = imin(span, nq - first);
-  it.p0 = it.nk - nq + first;
-  const int last = it.p0 + it.rows - 1;
-  const int ce = last < 0 ? 0 : last / BN + 1;
-  it.w0 = P.window > 0 ? imax(0, it.p0 - P.window + 1) / BN : 0;
-  it.ns = (imin(P.sinks, imax(0, last + 1)) + BN - 1) / BN;
-  if (it.w0 <= it.ns) it.w0 = it.ns = 0;
-  it.n = it.ns + ce - it.w0;
+  const int row0 = tile * span;
+  it.q0 = P.cu_q[b] + row0;
+  it.rows = imin(span, nq - row0);
+  it.p0 = it.nk - nq + row0;
+  const int end = imax(0, it.p0 + it.rows);  // of the keys that some row sees
+  const int start = P.window > 0 ? imin(end, imax(0, it.p0 - P.window + 1)) : 0;
+  const int first = imin(P.sinks, end);
+  it.ns = first > HEAD ? (first + BN - 1) / BN : 0;
+  int w0 = first > HEAD || first == 0 ? start : imax(0, start - HEAD);
+  if (w0 <= it.ns * BN) w0 = it.ns = 0;
+  it.skip = w0 - it.ns * BN;
+  it.n = it.ns + (end - w0 + BN - 1) / BN;
   return it;
 }
 
@@ -152,7 +163,9 @@ __device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *m
 template <int D, int TILES>
 __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
     window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
-                  const __grid_constant__ CUtensorMap mapV, const Params P) {
+                  const __grid_constant__ CUtensorMap mapV,
+                  const __grid_constant__ CUtensorMap mapK32, const __grid_constant__ CUtensorMap mapV32,
+                  const Params P) {
   using C = Cfg<D, TILES>;
   constexpr int NT = C::NT, NSB = C::NSB, PARTS = C::PARTS, VK = C::VK, KG = C::KG, SLOT = C::SLOT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -264,14 +277,23 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
           if (id < 0) continue;
           const Item it = item_at<NT>(P, pre, id);
           for (int j = 0; j < it.n && ok; ++j) {
-            const int key = it.k0 + it.block(j) * BN;
+            const int key = it.k0 + it.base(j);
+            const bool head = j == 0 && it.ns == 0 && it.skip > 0 && P.sinks > 0;
 #pragma unroll
             for (int x = 0; x < PARTS; ++x) {
               if (ok) ok = mbar_wait(&free[slot], parity, P.err);
               if (!ok) break;
               mbar_arrive_expect_tx(&landed[slot], SLOT);
-              tma_load_4d(slots + slot * SLOT, is_v ? &mapV : &mapK, 0, is_v ? key + x * VK : key, is_v ? 0 : x * KG, it.h,
-                          &landed[slot]);
+              uint8_t *at = slots + slot * SLOT;
+              if (!head) {
+                tma_load_4d(at, is_v ? &mapV : &mapK, 0, is_v ? key + x * VK : key, is_v ? 0 : x * KG, it.h, &landed[slot]);
+              } else {  // HEAD keys and 64 columns at a time
+                const int rows = is_v ? VK : BN, first = is_v ? x * VK : 0, group = is_v ? 0 : x * KG;
+                for (int g = 0; g < SLOT / (rows * 128); ++g)
+                  for (int y = 0; y < rows; y += HEAD)
+                    tma_load_4d(at + (g * rows + y) * 128, is_v ? &mapV32 : &mapK32, 0,
+                                first + y == 0 ? it.k0 : key + first + y, group + g, it.h, &landed[slot]);
+              }
               ++q;
               if (++slot == NS) {
                 slot = 0;
@@ -348,6 +370,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
         const int n = __shfl_sync(0xffffffffu, it.n, 0);
         if (n == 0) continue;
         const int nt = __shfl_sync(0xffffffffu, it.rows > P.PT ? NT : 1, 0);
+        const int beyond = __shfl_sync(0xffffffffu, it.base(it.n - 1) + BN - it.nk, 0);  // the last block's rows past the keys
         // S of the next block for tiles ta..tb1-1; `release`: they are its last
         auto issue_s = [&](int ta, int tb1, bool release, bool last) {
           Cursor at = ck;
@@ -386,7 +409,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
           const bool more = j + 1 < n;
           if (NSB == 2 && more) issue_s(0, 1, true, j + 2 == n);  // runs during this block's softmax
           // rows past the sequence's keys belong to others: they count as zero
-          const int past = it.block(j) * BN + BN - it.nk;
+          const int past = more ? 0 : beyond;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             if (t >= nt) continue;
@@ -452,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
     const int hf = HALVES == 1 ? 0 : warp >> 2;  // half of a block's keys, and of O's columns
     const int r = (warp & 3) * 32 + lane;       // row = TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const int ir = r / P.G, jr = r % P.G;       // position and query head in the tile
+    const int ir = r / P.G;                     // position in the tile
     const float sl2e = P.sl2e;
     const f2 scale2 = pack2(sl2e, sl2e);
     const uint32_t tO = tbase + C::TO + t * D + lane_off;
@@ -507,10 +530,11 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
           for (int c = 0; c < COLS / 32; ++c) tc::ld32(tS + 32 * c, raw[c]);
           tc::wait_ld();
         }
-        const int base = it.block(j) * BN;
+        const int base = it.base(j);
         if (base + BN - 1 > pt || (P.window > 0 && base <= plast - P.window && base + BN > P.sinks)) {
           // key c of the block is seen iff c <= hi and (c > lo or c < sk)
-          const int at = base + hf * COLS, hi = p - at, lo = P.window > 0 ? hi - P.window : -1, sk = P.sinks - at;
+          const int at = base + hf * COLS, hi = p - at, lo = P.window > 0 ? hi - P.window : -1;
+          const int sk = P.sinks - (j == 0 && it.ns == 0 ? hf * COLS : at);
 #pragma unroll
           for (int c = 0; c < COLS / 32; ++c) {
             auto below = [&](int n) {  // bits 0..n-1 of this group of 32
@@ -606,7 +630,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
       constexpr int NG = O0 / 64;
       const float f = l != 0.f ? 1.f / l : 0.f;
       const long long at = (mine && ok) ? (long long)(now.q0 + t * P.PT + ir) * P.o.token_stride +
-                                              (long long)(now.h * P.G + jr) * P.o.head_stride + hf * O0
+                                              (long long)(now.h * P.G + r - ir * P.G) * P.o.head_stride + hf * O0
                                         : -1LL;
       const int tq = lane & 3;
 #pragma unroll 1
@@ -687,10 +711,12 @@ static bool make_map(CUtensorMap *map, const sv_rows *r, int T, int H, int D, bo
 template <int D, int TILES>
 static sv_status run(const sv_rows *q, const sv_rows *k, const sv_rows *v, Params &P, int sms, cudaStream_t s) {
   using C = Cfg<D, TILES>;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mk32, mv32;
   if (!make_map(&mq, q, P.Tq, P.Hkv * P.G, D, true, P.G, P.PT, q->ptr) ||
       !make_map(&mk, k, P.Tk, P.Hkv, D, false, BN, C::KG, q->ptr) ||
-      !make_map(&mv, v, P.Tk, P.Hkv, D, false, C::VK, D / 64, q->ptr))
+      !make_map(&mv, v, P.Tk, P.Hkv, D, false, C::VK, D / 64, q->ptr) ||
+      !make_map(&mk32, k, P.Tk, P.Hkv, D, false, HEAD, 1, q->ptr) ||
+      !make_map(&mv32, v, P.Tk, P.Hkv, D, false, HEAD, 1, q->ptr))
     return SV_ERR_CUDA;
   const size_t prefix = ((size_t)P.B + 1) * 4;
   P.few_slots = prefix <= HEADER - PREFIX ? 0 : 1;
@@ -699,7 +725,8 @@ static sv_status run(const sv_rows *q, const sv_rows *k, const sv_rows *v, Param
   // at most one item more per sequence than the rows fill
   const long long items = ((long long)P.Tq / (P.PT * C::NT) + P.B) * P.Hkv;
   const int ctas = (int)lmin(items, sms);
-  return from_cuda(launch_early(window_kernel<D, TILES>, dim3(ctas), dim3(C::THREADS), smem, s, mq, mk, mv, P));
+  return from_cuda(launch_early(window_kernel<D, TILES>, dim3(ctas), dim3(C::THREADS), smem, s, mq, mk, mv,
+                                mk32, mv32, P));
 }
 
 static sv_status run_any(const sv_rows *q, const sv_rows *k, const sv_rows *v, Params &P, int D, int sms,

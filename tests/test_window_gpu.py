@@ -155,3 +155,17 @@ def test_strided_output_and_no_rows(cuda_lib):
     none = k[:0].to(DEV)   # no keys at all: every row sees nothing
     sv.window_attn(q.to(DEV), none, none, plain_o, cu, torch.zeros(2, dtype=torch.int32, device=DEV), 0.1)
     assert sv.sv_last_device_error() == sv.SV_OK and (plain_o == 0).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (6, 1, 256), (3, 3, 128), (2, 2, 256)])
+@pytest.mark.parametrize("sinks", [1, 31, 32, 33, 64, 129])
+@pytest.mark.parametrize("window", [1, 37, 128, 191])
+def test_first_keys_beside_a_far_window(cuda_lib, Hq, Hkv, D, window, sinks):
+    """First keys that share the window's first block (up to 32 of them), and that have blocks of their own."""
+    check(cuda_lib, [150, 333, 20], [400, 333, 777], Hq, Hkv, D, window, sinks, seed=window + sinks, gap=3)
+
+
+def test_first_keys_beside_a_far_window_sharp(cuda_lib):
+    """The largest scores stand among the first keys, or far from them."""
+    check(cuda_lib, [300, 90], [800, 90], 8, 2, 128, 61, 9, seed=5, gain=12.0)
+    check(cuda_lib, [300, 90], [800, 90], 12, 2, 256, 61, 9, seed=6, gain=12.0)
