@@ -563,7 +563,10 @@ SV_API sv_status sv_last_device_error(sv_stream_t stream);
  *     read activations, queries, logits and workspaces and write outputs only
  *     after the predecessor has completed; the prepacked weights and the KV
  *     cache slots before kv_len-M may be read earlier, so with this flag set
- *     they must not be written by the immediately preceding kernel. */
+ *     they must not be written by the immediately preceding kernel.
+ *     (qk_norm_rope, paged_kv_append, paged_attn and window_attn are launched
+ *     this way whatever the flag says, and read nothing before their
+ *     predecessor has completed.) */
 #define SV_LAUNCH_PDL 1u
 /*   SV_LAUNCH_QMM_CUDA_CORES: a measurement aid, not a faster path.
  *     qmm_small_m at M = 1 and M = 4 (72 KB-stage plans) replaces its

@@ -11,6 +11,17 @@ library raises immediately.
     packed = sv.prepack(codes, scales, biases)          # once per matrix
     ws = sv.workspace(sv.qmm_workspace_bytes(M, N, K))  # zeroed scratch
     sv.qmm_small_m(x, packed, y, M, N, K, ws)           # y = x @ W^T
+
+The calls over a paged cache take their sizes from the tensors' shapes and their
+strides as they are (a slice of a fused projection's rows will do):
+
+    phases = sv.rope_phases(inv_freq)                   # once per model
+    cache = sv.PagedKV(k_pages, v_pages, layout="HND")  # bf16 or e4m3 pages
+    sv.qk_norm_rope(q, k, q_rot, k_rot, positions, phases)           # a prompt
+    sv.window_attn(q_rot, k_rot, v, o, cu_rows, cu_rows, scale, window=1024)
+    sv.paged_kv_append(k, v, cache, slots, q=q, q_out=q_rot,         # new tokens
+                       positions=positions, phases=phases)
+    sv.paged_attn(q_rot, cache, block_table, lens, o, M, scale, workspace=ws)
 """
 from __future__ import annotations
 
