@@ -25,6 +25,9 @@
 //  * The angle is an integer: position times a 64-bit fraction of a turn wraps
 //    at whole turns by itself, so a far position loses nothing and no 64-bit
 //    floating-point arithmetic is needed.
+// Measured: 16381 tokens of 32 + 8 heads of 128: 57 us, 5.9 TB/s of 6.7; 30011
+// tokens' keys and values of 4 heads of 256 into e4m3 pages: 38 us, 4.9 TB/s, held
+// back by instructions (60% of the issue slots); 4 to 61 tokens: 2.3-2.5 us.
 #include <cuda_fp8.h>
 
 #include <cmath>

@@ -29,10 +29,23 @@
 //    (Blocks cut to whole groups of 32 keys cost every other block more than
 //    they save: 138 us.)
 //  * One warp streams K with TMA, one V, each into a ring of its own; another
-//    fetches the next tiles' queries as soon as the last S product is done.
+//    fetches the next tiles' queries as soon as the last S product is done, and
+//    tells the issuing warp the item's size: what that warp does between two
+//    products is on every tile's path (its own look-up: 373 us against 354 for
+//    8192 rows of 32 heads, causal).
+//  * Keys past a sequence's end belong to others.  Scores against them are
+//    masked; their values are not fetched (pieces of 32 keys, the last filled up
+//    with zeros by the issuing warp, older values behind it), as zeroing up to a
+//    whole block there cost the longest item 1 us.
 //  * The maximum that P refers to is raised only when a block exceeds it by
 //    more than 2^8, so O is rarely rescaled; P is rounded to bf16 (relative
 //    2^-8 at most, as the second product's operand), sums are fp32.
+// Measured: 8000 rows of 24/4 heads of 256, causal: 445-466 us, 1.69-1.77 PFLOP/s
+// (bound by the tensor cores); 8192 rows of 32/8 heads of 128, causal: 355 us,
+// 1.55 PFLOP/s, with a window of 1024 and 4 first keys 118 us (the softmax of two
+// tiles, about 1750 clocks a block each, and its hand-overs); seven prompts of 2
+// to 901 rows, 32/8 heads of 128: 20.4 us (three items of 1 to 8 blocks a CTA;
+// start 2600 clocks, end of an item 3200, a block 1850).
 #include "paged.cuh"
 #include "tcgen05.cuh"
 
@@ -44,12 +57,16 @@ namespace window {
 
 constexpr int ROWS = 128;           // rows of a tile (TMEM lanes)
 constexpr int BN = 128;             // keys of a block
-constexpr int HEAD = 32;            // first keys that may share a block with others
+constexpr int PIECE = 32;           // keys of a smaller copy; first keys that may share a block with others
 constexpr int MAX_B = 4096;
 constexpr float RESCALE = 8.f;      // log2 of the largest P against an old maximum
-// Shared memory: barriers, scan totals (320), halves' exchange (512), prefix
-// sums (2560; after the ring if longer), then the query tiles and the ring.
-constexpr int HEADER = 3072, PREFIX = 2560, SCAN = 320;
+// Shared memory: barriers, scan totals (320), the CTA's items (384), the item
+// (448), halves' exchange (512), prefix sums (2560; after the ring if longer), then the query
+// tiles and the ring.
+constexpr int HEADER = 3072, PREFIX = 2560, SCAN = 320, ORDER = 384, INFO = 448;
+// Up to this many sequences and rounds, the items go longest first.
+constexpr int MAX_SORTED = 32, MAX_SORTED_ROUNDS = 12;
+constexpr int SORT_UNIT = 64;       // keys that count as equally long
 
 // Two tiles a CTA (D = 128), or one with two S buffers and two threads a row.
 template <int D, int TILES>
@@ -81,6 +98,7 @@ struct Params {
   const int *cu_q, *cu_k;
   unsigned *err;
   int B, Tq, Tk, Hkv, G, PT;  // PT: positions per tile
+  uint32_t by_span;  // 2^32 over the positions of an item
   float sl2e;
   int window, sinks;
   int few_slots;  // long prefix sums take the place of some
@@ -91,19 +109,20 @@ struct Item {
   int rows;          // positions of the item
   int p0, nk;        // position of its first row; keys of the sequence
   // Blocks: ns over the first keys, then those from key w0 on; n in all.  Up to
-  // HEAD first keys far from the window (ns = 0, w0 > 0, sinks) need no block:
-  // keys 0..HEAD-1 stand in the first block's first rows, for w0..w0+HEAD-1.
+  // PIECE first keys far from the window (ns = 0, w0 > 0, sinks) need no block:
+  // keys 0..PIECE-1 stand in the first block's first rows, for w0..w0+PIECE-1.
   int ns, skip, n;
   __device__ __forceinline__ int base(int j) const { return j * BN + (j < ns ? 0 : skip); }
 };
 
-// Rows of sequence b, 0 if its offsets are out of order or out of range.
-__device__ __forceinline__ int rows_of(const Params &P, int b) {
+// Rows of sequence b (and its keys), 0 if its offsets are out of order or out of range.
+__device__ __forceinline__ int rows_of(const Params &P, int b, int &nk) {
   const int q0 = P.cu_q[b], q1 = P.cu_q[b + 1], k0 = P.cu_k[b], k1 = P.cu_k[b + 1];
   if (q0 < 0 || q1 < q0 || q1 > P.Tq || k0 < 0 || k1 < k0 || k1 > P.Tk) {
     if (blockIdx.x == 0) atomicOr(P.err, ERR_INDEX);
     return 0;
   }
+  nk = k1 - k0;
   return q1 - q0;
 }
 
@@ -130,19 +149,54 @@ __device__ __forceinline__ Item item_at(const Params &P, const int *pre, int id)
   const int end = imax(0, it.p0 + it.rows);  // of the keys that some row sees
   const int start = P.window > 0 ? imin(end, imax(0, it.p0 - P.window + 1)) : 0;
   const int first = imin(P.sinks, end);
-  it.ns = first > HEAD ? (first + BN - 1) / BN : 0;
-  int w0 = first > HEAD || first == 0 ? start : imax(0, start - HEAD);
+  it.ns = first > PIECE ? (first + BN - 1) / BN : 0;
+  int w0 = first > PIECE || first == 0 ? start : imax(0, start - PIECE);
   if (w0 <= it.ns * BN) w0 = it.ns = 0;
   it.skip = w0 - it.ns * BN;
   it.n = it.ns + (end - w0 + BN - 1) / BN;
   return it;
 }
 
-// Item of round k for this CTA (-1: none in this round).  Rounds alternate
-// direction, so that the CTA with a round's longest item gets the next one's shortest.
-__device__ __forceinline__ int item_id(int k, int items) {
-  const int g = (int)gridDim.x, at = (k & 1) ? g - 1 - (int)blockIdx.x : (int)blockIdx.x;
+// Place of this CTA's item of round k on the line of items (-1: none in this
+// round).  Rounds alternate direction, so that the CTA with a round's longest
+// item gets the next one's shortest; of sorted items the last round runs
+// backwards: what it lacks is lacking to the first CTAs, who had the longest.
+__device__ __forceinline__ int place_of(int k, int rounds, int items, bool sorted) {
+  const int g = (int)gridDim.x;
+  const int at = (k & 1) || (sorted && k + 1 == rounds) ? g - 1 - (int)blockIdx.x : (int)blockIdx.x;
   return k * g + at < items ? k * g + at : -1;
+}
+
+// The item at a place of the line that has all items by the position of their
+// last row, in units of SORT_UNIT, the largest first; a warp's work, one lane a
+// sequence (of nt items a KV head, whose first is at position `off`).
+__device__ __forceinline__ void find_sorted(const Params &P, const int *pre, const int2 *where, int place, int *out) {
+  const int lane = threadIdx.x & 31;
+  const bool in = lane < P.B;
+  const int nt = in ? pre[lane + 1] - pre[lane] : 0;
+  const int off = in ? where[lane].x : 0, end = nt > 0 ? where[lane].y : 0;
+  // items of this lane's sequence that end in unit v + 1 or later
+  auto after = [&](int v) {
+    const int e = (v + 1) * SORT_UNIT;
+    // (the quotient may be off by one far out, but never falls as v rises)
+    return end < e ? 0 : nt - imin((int)__umulhi((uint32_t)imax(0, e - off - 1), P.by_span), nt - 1);
+  };
+  const int q = place / P.Hkv, head = place - q * P.Hkv;
+  // v: the unit that the item ends in, the smallest with no more than q after it
+  int lo = 0, hi = __reduce_max_sync(0xffffffffu, end) / SORT_UNIT;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__reduce_add_sync(0xffffffffu, after(mid)) <= q) hi = mid; else lo = mid + 1;
+  }
+  const int later = after(lo), here = (lo > 0 ? after(lo - 1) : nt) - later;
+  int x = here;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  const int r = q - __reduce_add_sync(0xffffffffu, later) - (x - here);
+  if (r >= 0 && r < here) *out = (pre[lane] + later + r) * P.Hkv + head;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -164,7 +218,7 @@ template <int D, int TILES>
 __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
     window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                   const __grid_constant__ CUtensorMap mapV,
-                  const __grid_constant__ CUtensorMap mapK32, const __grid_constant__ CUtensorMap mapV32,
+                  const __grid_constant__ CUtensorMap mapKp, const __grid_constant__ CUtensorMap mapVp,
                   const Params P) {
   using C = Cfg<D, TILES>;
   constexpr int NT = C::NT, NSB = C::NSB, PARTS = C::PARTS, VK = C::VK, KG = C::KG, SLOT = C::SLOT;
@@ -189,7 +243,9 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
   uint64_t *p_half = idle + 1;     // [2] one S buffer: P of the first half of a block's keys written
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(p_half + 2);
   int *wsum = reinterpret_cast<int *>(smem + SCAN);
+  int4 *info = reinterpret_cast<int4 *>(smem + INFO);  // of the item whose queries landed
   float *xchg = reinterpret_cast<float *>(smem + 512);  // [2][2 halves][ROWS] maxima, then sums
+  int2 *where = reinterpret_cast<int2 *>(xchg);         // before: of up to 32 sequences, nk - nq and nk
   uint8_t *qs = smem + HEADER;
   uint8_t *ring = smem + C::RING;
   const int NK = P.few_slots ? C::LESS : C::NK, NV = P.few_slots ? C::LESS : C::NV;
@@ -225,6 +281,10 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
     *reinterpret_cast<uint4 *>(qs + t * C::QBYTES + (c >> 3) * ROWS * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
         make_uint4(0u, 0u, 0u, 0u);
   }
+  // Values of a block's rows past the sequence's end are not fetched: what
+  // stands there meets probabilities of zero and has to be finite.
+  for (int x = tid; x < NV * SLOT / 16; x += C::THREADS)
+    reinterpret_cast<uint4 *>(ring + NK * SLOT)[x] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async();
   pdl_wait();
 
@@ -232,7 +292,9 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
   int total = 0;
   for (int b0 = 0; b0 < P.B; b0 += C::THREADS) {
     const int b = b0 + tid;
-    const int nt = b < P.B ? (rows_of(P, b) + P.PT * NT - 1) / (P.PT * NT) : 0;
+    int nk = 0;
+    const int nq = b < P.B ? rows_of(P, b, nk) : 0;
+    const int nt = (nq + P.PT * NT - 1) / (P.PT * NT);
     int x = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -248,6 +310,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
       all += wsum[w];
     }
     if (b < P.B) pre[b] = total + before + x - nt;
+    if (b < P.B && b < MAX_SORTED) where[b] = make_int2(nk - nq, nk);
     total += all;
     __syncthreads();
   }
@@ -258,6 +321,24 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
   const uint32_t tbase = *tmem_slot;
   const int items = total * P.Hkv;
   const int rounds = (items + (int)gridDim.x - 1) / (int)gridDim.x;
+  // Longest first, if that pays: one sequence is in order already, many rounds
+  // even out by themselves, and finding the order takes 2 us (seven prompts of
+  // 2 to 901 rows: 2.9 items a CTA at D = 128, 22.3 -> 20.4 us; 2.1 at D = 256,
+  // 22.7 -> 23.4; 16 prompts of 69 to 1500 rows, 5.8 items, 68 -> 59).
+  int *order = reinterpret_cast<int *>(smem + ORDER);
+  const bool sorted = P.B > 1 && P.B <= MAX_SORTED && 2 * items >= 5 * (int)gridDim.x && rounds <= MAX_SORTED_ROUNDS;
+  if (sorted) {
+    static_assert(C::THREADS / 32 >= MAX_SORTED_ROUNDS, "a warp a round");
+    if (warp < rounds) {
+      const int place = place_of(warp, rounds, items, true);
+      if (place >= 0)
+        find_sorted(P, pre, where, place, order + warp);
+      else if (lane == 0)
+        order[warp] = -1;
+    }
+    __syncthreads();
+  }
+  auto item_id = [&](int k) { return sorted ? order[k] : place_of(k, rounds, items, false); };
 
   if (warp >= C::SOFT) {
     // 384 threads start with 168 registers each: 128*72 + 256*216 is the same total
@@ -273,26 +354,30 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
         uint32_t q = 0, parity = 1;
         int slot = 0;
         for (int k = 0; k < rounds && ok; ++k) {
-          const int id = item_id(k, items);
+          const int id = item_id(k);
           if (id < 0) continue;
           const Item it = item_at<NT>(P, pre, id);
           for (int j = 0; j < it.n && ok; ++j) {
             const int key = it.k0 + it.base(j);
             const bool head = j == 0 && it.ns == 0 && it.skip > 0 && P.sinks > 0;
+            // keys of the sequence in this block (keys past the end may land: they are masked)
+            const int kept = is_v ? imin(BN, it.nk - it.base(j)) : BN;
 #pragma unroll
             for (int x = 0; x < PARTS; ++x) {
               if (ok) ok = mbar_wait(&free[slot], parity, P.err);
               if (!ok) break;
-              mbar_arrive_expect_tx(&landed[slot], SLOT);
               uint8_t *at = slots + slot * SLOT;
-              if (!head) {
+              if (!head && kept == BN) {
+                mbar_arrive_expect_tx(&landed[slot], SLOT);
                 tma_load_4d(at, is_v ? &mapV : &mapK, 0, is_v ? key + x * VK : key, is_v ? 0 : x * KG, it.h, &landed[slot]);
-              } else {  // HEAD keys and 64 columns at a time
+              } else {  // PIECE keys and 64 columns at a time
                 const int rows = is_v ? VK : BN, first = is_v ? x * VK : 0, group = is_v ? 0 : x * KG;
-                for (int g = 0; g < SLOT / (rows * 128); ++g)
-                  for (int y = 0; y < rows; y += HEAD)
-                    tma_load_4d(at + (g * rows + y) * 128, is_v ? &mapV32 : &mapK32, 0,
-                                first + y == 0 ? it.k0 : key + first + y, group + g, it.h, &landed[slot]);
+                const int groups = SLOT / (rows * 128), some = imin(rows, imax(0, kept - first) + PIECE - 1) / PIECE * PIECE;
+                mbar_arrive_expect_tx(&landed[slot], (uint32_t)(groups * some * 128));
+                for (int g = 0; g < groups; ++g)
+                  for (int y = 0; y < some; y += PIECE)
+                    tma_load_4d(at + (g * rows + y) * 128, is_v ? &mapVp : &mapKp, 0,
+                                head && first + y == 0 ? it.k0 : key + first + y, group + g, it.h, &landed[slot]);
               }
               ++q;
               if (++slot == NS) {
@@ -315,7 +400,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
         bool ok = true;
         uint32_t c = 0;  // items with work so far
         for (int k = 0; k < rounds && ok; ++k) {
-          const int id = item_id(k, items);
+          const int id = item_id(k);
           if (id < 0) continue;
           const Item it = item_at<NT>(P, pre, id);
           if (it.n == 0) continue;
@@ -323,13 +408,20 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
           if (!ok) break;
           ++c;
           const int nt = it.rows > P.PT ? NT : 1;
+          *info = make_int4(it.n, nt, it.base(it.n - 1) + BN - it.nk, 0);
           mbar_arrive_expect_tx(q_full, (uint32_t)(nt * used * D * 2));
           for (int t = 0; t < nt; ++t)
 #pragma unroll
             for (int g = 0; g < D / 64; ++g)
               tma_load_4d(qs + t * C::QBYTES + g * ROWS * 128, &mapQ, 0, it.h * P.G, it.q0 + t * P.PT, g, q_full);
         }
-        if (!ok && c > 0) mbar_wait(q_full, (c - 1) & 1, P.err);
+        if (ok && c > 0) ok = mbar_wait(q_free, (c - 1) & 1, P.err);
+        if (ok) {  // no item is left
+          *info = make_int4(0, 0, 0, 0);
+          mbar_arrive(q_full);
+        } else if (c > 0) {
+          mbar_wait(q_full, (c - 1) & 1, P.err);
+        }
       }
       __syncwarp();
     } else if (warp == C::SOFT) {
@@ -363,14 +455,14 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
       uint32_t c = 0;                     // items with work so far
       uint32_t sj[NT] = {}, pj[NT] = {};  // blocks of each tile: S issued, P consumed
       uint32_t oc[NT] = {};               // items of each tile
-      for (int k = 0; k < rounds && ok; ++k) {
-        const int id = item_id(k, items);
-        if (id < 0) continue;
-        const Item it = item_at<NT>(P, pre, id);
-        const int n = __shfl_sync(0xffffffffu, it.n, 0);
-        if (n == 0) continue;
-        const int nt = __shfl_sync(0xffffffffu, it.rows > P.PT ? NT : 1, 0);
-        const int beyond = __shfl_sync(0xffffffffu, it.base(it.n - 1) + BN - it.nk, 0);  // the last block's rows past the keys
+      while (ok) {
+        wait(q_full, c & 1);
+        if (!ok) break;
+        ++c;
+        // n blocks, nt tiles; the last block's rows past the sequence's keys
+        const int n = __shfl_sync(0xffffffffu, info->x, 0), nt = __shfl_sync(0xffffffffu, info->y, 0);
+        const int beyond = __shfl_sync(0xffffffffu, info->z, 0);
+        if (n == 0) break;
         // S of the next block for tiles ta..tb1-1; `release`: they are its last
         auto issue_s = [&](int ta, int tb1, bool release, bool last) {
           Cursor at = ck;
@@ -402,8 +494,6 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
           for (int t = 0; t < NT; ++t)
             if (t >= ta && t < tb1) ++sj[t];
         };
-        wait(q_full, c & 1);
-        ++c;
         issue_s(0, nt, true, n == 1);
         for (int j = 0; j < n; ++j) {
           const bool more = j + 1 < n;
@@ -420,11 +510,13 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
 #pragma unroll
             for (int x = 0; x < PARTS; ++x) {
               if (t == 0) wait(&full[5 + at.slot], at.parity);
-              const int gone = imin(VK, past - (PARTS - 1 - x) * VK);  // keys of this slot that are past the end
-              if (gone > 0 && t == 0) {
+              // keys of this slot that are the sequence's; the rest of their piece
+              // belongs to others and counts as zero, later rows are old values
+              const int kept = VK - imax(0, past - (PARTS - 1 - x) * VK);
+              if (kept > 0 && kept % PIECE != 0 && t == 0) {
                 uint8_t *vb = ring + (NK + at.slot) * SLOT;
-                for (int y = lane; y < gone * (D / 8); y += 32) {
-                  const int r = VK - gone + y / (D / 8), z = y % (D / 8);
+                for (int y = lane; y < (PIECE - kept % PIECE) * (D / 8); y += 32) {
+                  const int r = kept + y / (D / 8), z = y % (D / 8);
                   *reinterpret_cast<uint4 *>(vb + (z >> 3) * VK * 128 + r * 128 + (z & 7) * 16) =
                       make_uint4(0u, 0u, 0u, 0u);
                 }
@@ -500,13 +592,13 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
       named_barrier(2 + (warp & 3), 64);
       return at[(hf ^ 1) * ROWS + r];
     };
-    int id = rounds > 0 ? item_id(0, items) : -1;
+    int id = rounds > 0 ? item_id(0) : -1;
     Item it{};
     if (id >= 0) it = item_at<NT>(P, pre, id);
     for (int k = 0; k < rounds; ++k) {
       if (id < 0 || (t > 0 && it.rows <= P.PT)) {  // nothing for this tile
         if (k + 1 < rounds) {
-          id = item_id(k + 1, items);
+          id = item_id(k + 1);
           if (id >= 0) it = item_at<NT>(P, pre, id);
         }
         continue;
@@ -615,7 +707,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
       }
       const Item now = it;
       if (k + 1 < rounds) {  // the next item is looked up while the last product runs
-        id = item_id(k + 1, items);
+        id = item_id(k + 1);
         if (id >= 0) it = item_at<NT>(P, pre, id);
       }
       if (now.n > 0) {
@@ -711,14 +803,15 @@ static bool make_map(CUtensorMap *map, const sv_rows *r, int T, int H, int D, bo
 template <int D, int TILES>
 static sv_status run(const sv_rows *q, const sv_rows *k, const sv_rows *v, Params &P, int sms, cudaStream_t s) {
   using C = Cfg<D, TILES>;
-  CUtensorMap mq, mk, mv, mk32, mv32;
+  CUtensorMap mq, mk, mv, mkp, mvp;
   if (!make_map(&mq, q, P.Tq, P.Hkv * P.G, D, true, P.G, P.PT, q->ptr) ||
       !make_map(&mk, k, P.Tk, P.Hkv, D, false, BN, C::KG, q->ptr) ||
       !make_map(&mv, v, P.Tk, P.Hkv, D, false, C::VK, D / 64, q->ptr) ||
-      !make_map(&mk32, k, P.Tk, P.Hkv, D, false, HEAD, 1, q->ptr) ||
-      !make_map(&mv32, v, P.Tk, P.Hkv, D, false, HEAD, 1, q->ptr))
+      !make_map(&mkp, k, P.Tk, P.Hkv, D, false, PIECE, 1, q->ptr) ||
+      !make_map(&mvp, v, P.Tk, P.Hkv, D, false, PIECE, 1, q->ptr))
     return SV_ERR_CUDA;
   const size_t prefix = ((size_t)P.B + 1) * 4;
+  P.by_span = (uint32_t)((0x100000000ull + P.PT * C::NT - 1) / (P.PT * C::NT) - (P.PT * C::NT == 1));
   P.few_slots = prefix <= HEADER - PREFIX ? 0 : 1;
   const size_t smem = C::RING + (P.few_slots ? 128 * 1024 + prefix : 160 * 1024);
   static_assert(C::RING + 160 * 1024 <= 227 * 1024 && C::RING + 128 * 1024 + (MAX_B + 1) * 4 <= 227 * 1024, "shared memory");
@@ -726,7 +819,7 @@ static sv_status run(const sv_rows *q, const sv_rows *k, const sv_rows *v, Param
   const long long items = ((long long)P.Tq / (P.PT * C::NT) + P.B) * P.Hkv;
   const int ctas = (int)lmin(items, sms);
   return from_cuda(launch_early(window_kernel<D, TILES>, dim3(ctas), dim3(C::THREADS), smem, s, mq, mk, mv,
-                                mk32, mv32, P));
+                                mkp, mvp, P));
 }
 
 static sv_status run_any(const sv_rows *q, const sv_rows *k, const sv_rows *v, Params &P, int D, int sms,

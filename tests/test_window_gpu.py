@@ -169,3 +169,12 @@ def test_first_keys_beside_a_far_window_sharp(cuda_lib):
     """The largest scores stand among the first keys, or far from them."""
     check(cuda_lib, [300, 90], [800, 90], 8, 2, 128, 61, 9, seed=5, gain=12.0)
     check(cuda_lib, [300, 90], [800, 90], 12, 2, 256, 61, 9, seed=6, gain=12.0)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 8, 128), (32, 8, 128), (24, 4, 256), (128, 1, 128), (128, 1, 256)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 4)])
+def test_items_longest_first(cuda_lib, Hq, Hkv, D, window, sinks):
+    """Many sequences of very different lengths, pasts and too few keys among them; each row written once."""
+    nq = [1, 700, 2, 0, 35, 333, 64, 1, 128, 129, 90, 1, 1, 5, 260, 17]
+    nk = [1, 700, 500, 3, 20, 333, 65, 0, 128, 400, 90, 1, 7, 5, 900, 16]
+    check(cuda_lib, nq, nk, Hq, Hkv, D, window, sinks, seed=7, gap=1)
