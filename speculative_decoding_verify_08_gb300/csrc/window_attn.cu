@@ -40,11 +40,11 @@
 //  * The maximum that P refers to is raised only when a block exceeds it by
 //    more than 2^8, so O is rarely rescaled; P is rounded to bf16 (relative
 //    2^-8 at most, as the second product's operand), sums are fp32.
-// Measured: 8000 rows of 24/4 heads of 256, causal: 445-466 us, 1.69-1.77 PFLOP/s
-// (bound by the tensor cores); 8192 rows of 32/8 heads of 128, causal: 355 us,
-// 1.55 PFLOP/s, with a window of 1024 and 4 first keys 118 us (the softmax of two
+// Measured: 8000 rows of 24/4 heads of 256, causal: 445-485 us, 1.62-1.77 PFLOP/s
+// (bound by the tensor cores); 8192 rows of 32/8 heads of 128, causal: 357 us,
+// 1.55 PFLOP/s, with a window of 1024 and 4 first keys 116 us (the softmax of two
 // tiles, about 1750 clocks a block each, and its hand-overs); seven prompts of 2
-// to 901 rows, 32/8 heads of 128: 20.4 us (three items of 1 to 8 blocks a CTA;
+// to 901 rows, 32/8 heads of 128: 19.4 us (three items of 1 to 8 blocks a CTA;
 // start 2600 clocks, end of an item 3200, a block 1850).
 #include "paged.cuh"
 #include "tcgen05.cuh"
@@ -323,10 +323,12 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
   const int rounds = (items + (int)gridDim.x - 1) / (int)gridDim.x;
   // Longest first, if that pays: one sequence is in order already, many rounds
   // even out by themselves, and finding the order takes 2 us (seven prompts of
-  // 2 to 901 rows: 2.9 items a CTA at D = 128, 22.3 -> 20.4 us; 2.1 at D = 256,
-  // 22.7 -> 23.4; 16 prompts of 69 to 1500 rows, 5.8 items, 68 -> 59).
+  // 2 to 901 rows: 2.9 items a CTA at D = 128, 22.1 -> 19.4 us; 2.1 at D = 256,
+  // 22.7 -> 23.4; 16 prompts of 69 to 1500 rows, 2.9 pairs, 68 -> 57).  Whether
+  // they are sorted stands behind the list: no role has a register to spare.
   int *order = reinterpret_cast<int *>(smem + ORDER);
   const bool sorted = P.B > 1 && P.B <= MAX_SORTED && 2 * items >= 5 * (int)gridDim.x && rounds <= MAX_SORTED_ROUNDS;
+  if (tid == 0) order[MAX_SORTED_ROUNDS] = sorted;
   if (sorted) {
     static_assert(C::THREADS / 32 >= MAX_SORTED_ROUNDS, "a warp a round");
     if (warp < rounds) {
@@ -336,9 +338,9 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
       else if (lane == 0)
         order[warp] = -1;
     }
-    __syncthreads();
   }
-  auto item_id = [&](int k) { return sorted ? order[k] : place_of(k, rounds, items, false); };
+  __syncthreads();
+  auto item_id = [&](int k) { return order[MAX_SORTED_ROUNDS] ? order[k] : place_of(k, rounds, items, false); };
 
   if (warp >= C::SOFT) {
     // 384 threads start with 168 registers each: 128*72 + 256*216 is the same total
@@ -826,9 +828,9 @@ static sv_status run_any(const sv_rows *q, const sv_rows *k, const sv_rows *v, P
                          cudaStream_t s) {
   if (D == 256) return run<256, 1>(q, k, v, P, sms, s);
   // Two tiles a CTA use the tensor cores best (8192 rows of 32 heads, causal:
-  // 385 us against 458), but their items are twice as long: with fewer than two
+  // 357 us against 425), but their items are twice as long: with fewer than two
   // for every SM single tiles fill the GPU more evenly (seven prompts of 2 to
-  // 901 rows: 24 us against 28).
+  // 901 rows: 20 us against 25; four of 519 to 1200: 35 against 30).
   const long long pairs = ((long long)P.Tq / (P.PT * 2) + P.B) * P.Hkv;
   return pairs >= 2 * sms ? run<128, 2>(q, k, v, P, sms, s) : run<128, 1>(q, k, v, P, sms, s);
 }
