@@ -30,12 +30,16 @@
 //    loop.  The warps' results are joined once per (sequence, head).
 //  * A piece that does not hold all of its (sequence, head) leaves its O,
 //    maximum and sum in the workspace; a second kernel joins them.
-//  * The maximum is raised only when a chunk exceeds it by more than 2^8
-//    (probabilities up to 256 against the old maximum are exact in the same
-//    sense), so the accumulators are rarely rescaled.
-// Probabilities are rounded to the operand type of the second product (bf16;
-// fp16 beside an e4m3 cache): relative 2^-8 or less each, averaging out over
-// the slots, below the output's own rounding.
+//  * The maximum is raised only when a chunk exceeds it by more than 2^8 (2^2
+//    beside an e4m3 cache), so the accumulators are rarely rescaled.
+// Probabilities are rounded to the operand type of the second product, one
+// rounding each.  bf16: relative 2^-8 whatever their size.  fp16 (beside an
+// e4m3 cache, whose values it holds exactly): relative 2^-11 in its normal
+// range only, so they are taken 2^13 times as large, up to 2^15 of 65504, and
+// the sum with them, so that the factor cancels: those down to 2^-27 of the
+// maximum keep 2^-11, smaller ones are off by 2^-38 of the maximum at most
+// (against 1 for the maximum, many small ones beside a large one lost 2^-25
+// each, up to all of their share).
 // An e4m3 cache is converted in registers to fp16, which holds every e4m3
 // value exactly; the queries are scaled by a power of two per row to fit fp16.
 // Measured: 48 sequences of 40 to 16000 slots, 32/8 heads of 128: 96 us, 6.3 TB/s;
@@ -64,7 +68,10 @@ constexpr int MAX_R = 128;           // query rows per KV head: eight 16-row til
 constexpr int MAX_STAGES = 32;
 constexpr int HEAD_COST = 12;        // chunks' time that a (sequence, head) takes beside its chunks
 constexpr int MAX_EVEN_B = 64;       // sequences up to which heads are cut evenly
-constexpr float RESCALE = 8.f;       // log2 of the largest probability against an old maximum
+// log2 of the factor on probabilities and their sum, and of the largest
+// probability, factor included, before the maximum is raised
+__host__ __device__ constexpr float lift(bool f8) { return f8 ? 13.f : 0.f; }
+__host__ __device__ constexpr float largest(bool f8) { return f8 ? 15.f : 8.f; }
 constexpr size_t SMEM_LIMIT = 227 * 1024;
 
 struct Params {
@@ -479,6 +486,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       sc1 *= kscale * qsc[row1];
     }
 
+    // m0, m1: what the exponents refer to, the running maximum less the lift
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float o[NT][4];
 #pragma unroll
@@ -603,12 +611,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
       }
       // ---- running maximum, raised only by a chunk far above it ----
-      if (__any_sync(0xffffffffu, mx0 > m0 + RESCALE || mx1 > m1 + RESCALE)) {
+      if (__any_sync(0xffffffffu, mx0 > m0 + largest(F8) || mx1 > m1 + largest(F8))) {
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+        const float n0 = fmaxf(m0, mx0 - lift(F8)), n1 = fmaxf(m1, mx1 - lift(F8));
         const float a0 = n0 == -INFINITY ? 1.f : ex2_approx(m0 - n0);
         const float a1 = n1 == -INFINITY ? 1.f : ex2_approx(m1 - n1);
         l0 *= a0;
