@@ -983,7 +983,7 @@ sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const int32_t *
                      int M, int Hq, int Hkv, int D, float scale, int window, int sinks, void *workspace,
                      size_t ws_bytes, sv_stream_t stream) {
   if (B < 0 || M < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv != 0) return SV_ERR_INVALID_ARG;
-  if (window < 0 || sinks < 0 || table_width < 1 || table_stride < 0) return SV_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0 || table_width < (B > 0 ? 1 : 0) || table_stride < 0) return SV_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !(scale < INFINITY)) return SV_ERR_INVALID_ARG;
   if (D != 128 && D != 256) return SV_ERR_UNSUPPORTED;
   const int G = Hq / Hkv;

@@ -305,9 +305,9 @@ static bool good_norm(const sv_head_norm *n) {
   return !n || (n->eps >= 0.f && n->eps < INFINITY && std::isfinite(n->weight_offset) &&
                 paged::aligned(n->q_weight, 16) && paged::aligned(n->k_weight, 16));
 }
-static bool good_rotation(const sv_rotation *r, int D) {
+static bool good_rotation(const sv_rotation *r, int T, int D) {
   if (!r || !r->phases) return true;
-  return r->positions && paged::aligned(r->phases, 8) && paged::aligned(r->positions, 4) &&
+  return (r->positions || T == 0) && paged::aligned(r->phases, 8) && paged::aligned(r->positions, 4) &&
          r->rot_dim >= 8 && r->rot_dim % 8 == 0 && r->rot_dim <= D;
 }
 
@@ -373,7 +373,7 @@ sv_status qk_norm_rope(const sv_rows *q, const sv_rows *k, const sv_rows *q_out,
   if (Hq > 4096 || Hkv > 4096 || (long long)T * (Hq + Hkv) > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
   for (const sv_rows *r : {q, k, q_out, k_out})
     if (!paged::good_rows(r, T)) return SV_ERR_INVALID_ARG;
-  if (!rope::good_norm(norm) || !rope::good_rotation(rot, D)) return SV_ERR_INVALID_ARG;
+  if (!rope::good_norm(norm) || !rope::good_rotation(rot, T, D)) return SV_ERR_INVALID_ARG;
   rope::Params P{};
   P.q = rope::rows_of(q);
   P.k = rope::rows_of(k);
@@ -396,7 +396,7 @@ sv_status paged_kv_append(const sv_rows *q, const sv_rows *q_out, const sv_rows 
   const sv_status cs = paged::check_cache(cache, D);
   if (cs != SV_OK) return cs;
   if ((!slots && T > 0) || !paged::aligned(slots, 8)) return SV_ERR_INVALID_ARG;
-  if (!rope::good_norm(norm) || !rope::good_rotation(rot, D)) return SV_ERR_INVALID_ARG;
+  if (!rope::good_norm(norm) || !rope::good_rotation(rot, T, D)) return SV_ERR_INVALID_ARG;
   rope::Params P{};
   if (q) {
     P.q = rope::rows_of(q);

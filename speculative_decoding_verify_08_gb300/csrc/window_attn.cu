@@ -864,6 +864,7 @@ sv_status window_attn(const sv_rows *q, const sv_rows *k, const sv_rows *v, cons
     if (!paged::good_rows(r, Tk)) return SV_ERR_INVALID_ARG;
   if (B > 0 && (!cu_q || !cu_k)) return SV_ERR_INVALID_ARG;
   if (!paged::aligned(cu_q, 4) || !paged::aligned(cu_k, 4)) return SV_ERR_INVALID_ARG;
+  if (B == 0 || Tq == 0) return SV_OK;
   // a tensor map steps by every stride: rows that repeat (stride 0) have none
   if ((Tq > 1 && !q->token_stride) || (Hq > 1 && !q->head_stride)) return SV_ERR_UNSUPPORTED;
   for (const sv_rows *r : {k, v})
@@ -871,7 +872,6 @@ sv_status window_attn(const sv_rows *q, const sv_rows *k, const sv_rows *v, cons
   // the items of all KV heads are counted in 31 bits
   const int pt = window::ROWS / G;
   if (((long long)Tq / pt + B) * Hkv > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
-  if (B == 0 || Tq == 0) return SV_OK;
   const int sms = device_sm_count();
   if (sms <= 0) return SV_ERR_CUDA;
   window::Params P{};
