@@ -13,7 +13,8 @@ library raises immediately.
     sv.qmm_small_m(x, packed, y, M, N, K, ws)           # y = x @ W^T
 
 The calls over a paged cache take their sizes from the tensors' shapes and their
-strides as they are (a slice of a fused projection's rows will do):
+strides as they are (a slice of a fused projection's rows will do); all operands
+live on the current device:
 
     phases = sv.rope_phases(inv_freq)                   # once per model
     cache = sv.PagedKV(k_pages, v_pages, layout="HND")  # bf16 or e4m3 pages
@@ -382,13 +383,22 @@ def _bad(where: str, status: int = SV_ERR_INVALID_ARG):
 
 
 # What a call checks here is what the library cannot see (types, shapes, that
-# memory is the GPU's); one attribute of a tensor costs about 0.1 us.
+# memory is the current GPU's); one attribute of a tensor costs about 0.1 us.
 _BF16 = torch.bfloat16
 
 
-def _rows(t, tokens, heads, D, where):
-    """sv_rows of a CUDA bf16 tensor [tokens, heads, D] (any strides, D contiguous)."""
-    if t.dtype is not _BF16 or t.shape != (tokens, heads, D) or not t.is_cuda:
+def _device(t, where):
+    """The device of a call, that of its first operand.  The library launches on
+    the current one, so it has to be that, and the other operands' too."""
+    d = t.get_device()
+    if d < 0 or d != torch._C._cuda_getDevice():
+        _bad(where)
+    return d
+
+
+def _rows(t, tokens, heads, D, dev, where):
+    """sv_rows of a bf16 tensor [tokens, heads, D] of the call's device (any strides, D contiguous)."""
+    if t.dtype is not _BF16 or t.shape != (tokens, heads, D) or t.get_device() != dev:
         _bad(where)
     ts, hs, ds = t.stride()
     if ds != 1:
@@ -397,17 +407,17 @@ def _rows(t, tokens, heads, D, where):
     return _ROWS.pack(t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0)
 
 
-def _vector(t, dtype, n, where):
-    """Address of a contiguous CUDA tensor of n values."""
-    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+def _vector(t, dtype, n, dev, where):
+    """Address of a contiguous tensor of n values of the call's device."""
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
         _bad(where)
     return t.data_ptr()
 
 
-def _launch_stream(t, stream):
-    """The given stream, or the current one of the tensor's device."""
+def _launch_stream(dev, stream):
+    """The given stream, or the current one of the call's device."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return _stream(stream)
 
 
@@ -423,18 +433,18 @@ def rope_phases(inv_freq, device=None):
     return torch.from_numpy(out.view(np.int64)).to(device if device is not None else torch.device("cuda"))
 
 
-def _norm_rotation(q_weight, k_weight, eps, weight_offset, positions, phases, interleaved, T, D, where):
+def _norm_rotation(q_weight, k_weight, eps, weight_offset, positions, phases, interleaved, T, D, dev, where):
     norm = rot = None
     if q_weight is not None or k_weight is not None:
-        norm = _NORM.pack(0 if q_weight is None else _vector(q_weight, _BF16, D, where),
-                          0 if k_weight is None else _vector(k_weight, _BF16, D, where),
+        norm = _NORM.pack(0 if q_weight is None else _vector(q_weight, _BF16, D, dev, where),
+                          0 if k_weight is None else _vector(k_weight, _BF16, D, dev, where),
                           eps, weight_offset)
     if phases is not None:
         if positions is None:
             _bad(where)
         half = phases.numel()
-        rot = _ROTATION.pack(_vector(phases, torch.int64, half, where), _vector(positions, torch.int32, T, where),
-                             2 * half, 1 if interleaved else 0)
+        rot = _ROTATION.pack(_vector(phases, torch.int64, half, dev, where),
+                             _vector(positions, torch.int32, T, dev, where), 2 * half, 1 if interleaved else 0)
     return norm, rot
 
 
@@ -446,9 +456,11 @@ def qk_norm_rope(q, k, q_out, k_out, positions=None, phases=None, q_weight=None,
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     w = "qk_norm_rope"
-    norm, rot = _norm_rotation(q_weight, k_weight, eps, weight_offset, positions, phases, interleaved, T, D, w)
-    status = load().qk_norm_rope(_rows(q, T, Hq, D, w), _rows(k, T, Hkv, D, w), _rows(q_out, T, Hq, D, w),
-                                 _rows(k_out, T, Hkv, D, w), norm, rot, T, Hq, Hkv, D, _launch_stream(q, stream))
+    dev = _device(q, w)
+    norm, rot = _norm_rotation(q_weight, k_weight, eps, weight_offset, positions, phases, interleaved, T, D, dev, w)
+    status = load().qk_norm_rope(_rows(q, T, Hq, D, dev, w), _rows(k, T, Hkv, D, dev, w),
+                                 _rows(q_out, T, Hq, D, dev, w), _rows(k_out, T, Hkv, D, dev, w), norm, rot, T, Hq,
+                                 Hkv, D, _launch_stream(dev, stream))
     if status:
         _check(status, w)
 
@@ -466,14 +478,15 @@ class PagedKV:
             _bad(w)
         if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype is not k.dtype:
             _bad(w)
-        if not k.is_cuda or v.get_device() != k.get_device() or k.stride(3) != 1:
+        self.device = k.get_device()
+        if self.device < 0 or v.get_device() != self.device or k.stride(3) != 1:
             _bad(w)
         slot, head = (1, 2) if layout == "NHD" else (2, 1)
         self.k, self.v, self.k_scale, self.v_scale, self.layout = k, v, k_scale, v_scale, layout
         self.page_size, self.heads, self.D = k.shape[slot], k.shape[head], k.shape[3]
         fields = (k.data_ptr(), v.data_ptr(),
-                  0 if k_scale is None else _vector(k_scale, torch.float32, self.heads, w),
-                  0 if v_scale is None else _vector(v_scale, torch.float32, self.heads, w),
+                  0 if k_scale is None else _vector(k_scale, torch.float32, self.heads, self.device, w),
+                  0 if v_scale is None else _vector(v_scale, torch.float32, self.heads, self.device, w),
                   k.stride(0), k.stride(slot), k.stride(head), k.shape[0], self.page_size,
                   SV_BF16 if k.dtype is torch.bfloat16 else SV_E4M3)
         self.packed = _PAGED_KV.pack(*fields, 0)
@@ -491,15 +504,17 @@ def paged_kv_append(k, v, cache: PagedKV, slots, q=None, q_out=None, positions=N
     and in the same launch the queries' rows to q_out when q is given."""
     T, Hkv, D = k.shape
     w = "paged_kv_append"
-    if Hkv != cache.heads or D != cache.D or (q is None) != (q_out is None):
+    dev = _device(k, w)
+    if Hkv != cache.heads or D != cache.D or dev != cache.device or (q is None) != (q_out is None):
         _bad(w)
     Hq = 0 if q is None else q.shape[1]
     norm, rot = _norm_rotation(q_weight if q is not None else None, k_weight, eps, weight_offset, positions,
-                               phases, interleaved, T, D, w)
-    status = load().paged_kv_append(None if q is None else _rows(q, T, Hq, D, w),
-                                    None if q is None else _rows(q_out, T, Hq, D, w), _rows(k, T, Hkv, D, w),
-                                    _rows(v, T, Hkv, D, w), cache.packed, _vector(slots, torch.int64, T, w), norm,
-                                    rot, T, Hq, Hkv, D, _launch_stream(k, stream))
+                               phases, interleaved, T, D, dev, w)
+    status = load().paged_kv_append(None if q is None else _rows(q, T, Hq, D, dev, w),
+                                    None if q is None else _rows(q_out, T, Hq, D, dev, w),
+                                    _rows(k, T, Hkv, D, dev, w), _rows(v, T, Hkv, D, dev, w), cache.packed,
+                                    _vector(slots, torch.int64, T, dev, w), norm, rot, T, Hq, Hkv, D,
+                                    _launch_stream(dev, stream))
     if status:
         _check(status, w)
 
@@ -516,16 +531,17 @@ def paged_attn(q, cache: PagedKV, block_table, kv_lens, o, M: int, scale: float,
     rows, Hq, D = q.shape
     w = "paged_attn"
     B, width = block_table.shape
-    if (D != cache.D or rows != B * M or block_table.dtype is not torch.int32 or not block_table.is_cuda
-            or (workspace is not None and not workspace.is_cuda)):
+    dev = _device(q, w)
+    if (D != cache.D or rows != B * M or dev != cache.device or block_table.dtype is not torch.int32
+            or block_table.get_device() != dev or (workspace is not None and workspace.get_device() != dev)):
         _bad(w)
     ts, es = block_table.stride()
     if es != 1 and width != 1:
         _bad(w)
-    status = load().paged_attn(_rows(q, rows, Hq, D, w), cache.packed, block_table.data_ptr(), ts, width,
-                               _vector(kv_lens, torch.int32, B, w), _rows(o, rows, Hq, D, w), B, M, Hq, cache.heads,
-                               D, scale, window, sinks, _ptr(workspace), _nbytes(workspace),
-                               _launch_stream(q, stream))
+    status = load().paged_attn(_rows(q, rows, Hq, D, dev, w), cache.packed, block_table.data_ptr(), ts, width,
+                               _vector(kv_lens, torch.int32, B, dev, w), _rows(o, rows, Hq, D, dev, w), B, M, Hq,
+                               cache.heads, D, scale, window, sinks, _ptr(workspace), _nbytes(workspace),
+                               _launch_stream(dev, stream))
     if status:
         _check(status, w)
 
@@ -543,9 +559,11 @@ def window_attn(q, k, v, o, cu_q, cu_k, scale: float, window: int = 0, sinks: in
     Tk, Hkv, _ = k.shape
     w = "window_attn"
     n = cu_q.shape[0]
-    status = load().window_attn(_rows(q, Tq, Hq, D, w), _rows(k, Tk, Hkv, D, w), _rows(v, Tk, Hkv, D, w),
-                                _rows(o, Tq, Hq, D, w), _vector(cu_q, torch.int32, n, w),
-                                _vector(cu_k, torch.int32, n, w), n - 1, Tq, Tk, Hq, Hkv, D, scale, window, sinks,
-                                _ptr(workspace), _nbytes(workspace), _launch_stream(q, stream))
+    dev = _device(q, w)
+    status = load().window_attn(_rows(q, Tq, Hq, D, dev, w), _rows(k, Tk, Hkv, D, dev, w),
+                                _rows(v, Tk, Hkv, D, dev, w), _rows(o, Tq, Hq, D, dev, w),
+                                _vector(cu_q, torch.int32, n, dev, w), _vector(cu_k, torch.int32, n, dev, w), n - 1,
+                                Tq, Tk, Hq, Hkv, D, scale, window, sinks, _ptr(workspace), _nbytes(workspace),
+                                _launch_stream(dev, stream))
     if status:
         _check(status, w)
