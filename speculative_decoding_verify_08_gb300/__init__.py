@@ -470,7 +470,9 @@ class PagedKV:
     strides, [pages, slots, heads, D] ("NHD") or [pages, heads, slots, D]
     ("HND"), bf16 or float8_e4m3fn; with the latter, the stored value times
     k_scale[head] (v_scale[head], fp32 [heads], None for 1) counts.  Holds the
-    tensors and what the calls need of them, worked out once."""
+    tensors and what the calls need of them, worked out once: its attributes
+    are read-only, and a copy (copy, deepcopy, pickle) is made anew from the
+    copied tensors."""
 
     def __init__(self, k, v, layout: str = "NHD", k_scale=None, v_scale=None):
         w = "PagedKV"
@@ -478,22 +480,32 @@ class PagedKV:
             _bad(w)
         if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype is not k.dtype:
             _bad(w)
-        self.device = k.get_device()
-        if self.device < 0 or v.get_device() != self.device or k.stride(3) != 1:
+        device = k.get_device()
+        if device < 0 or v.get_device() != device or k.stride(3) != 1:
             _bad(w)
         slot, head = (1, 2) if layout == "NHD" else (2, 1)
-        self.k, self.v, self.k_scale, self.v_scale, self.layout = k, v, k_scale, v_scale, layout
-        self.page_size, self.heads, self.D = k.shape[slot], k.shape[head], k.shape[3]
+        page_size, heads, D = k.shape[slot], k.shape[head], k.shape[3]
         fields = (k.data_ptr(), v.data_ptr(),
-                  0 if k_scale is None else _vector(k_scale, torch.float32, self.heads, self.device, w),
-                  0 if v_scale is None else _vector(v_scale, torch.float32, self.heads, self.device, w),
-                  k.stride(0), k.stride(slot), k.stride(head), k.shape[0], self.page_size,
+                  0 if k_scale is None else _vector(k_scale, torch.float32, heads, device, w),
+                  0 if v_scale is None else _vector(v_scale, torch.float32, heads, device, w),
+                  k.stride(0), k.stride(slot), k.stride(head), k.shape[0], page_size,
                   SV_BF16 if k.dtype is torch.bfloat16 else SV_E4M3)
-        self.packed = _PAGED_KV.pack(*fields, 0)
-        if self.D in (128, 256):  # what paged_attn reads
-            self._maps = (ctypes.c_uint64 * (_PAGED_MAPS_BYTES // 8))()
-            _check(load().paged_kv_maps(self.packed, self.heads, self.D, self._maps, _PAGED_MAPS_BYTES), w)
-            self.packed = _PAGED_KV.pack(*fields, ctypes.addressof(self._maps))
+        packed, maps = _PAGED_KV.pack(*fields, 0), None
+        if D in (128, 256):  # what paged_attn reads
+            maps = (ctypes.c_uint64 * (_PAGED_MAPS_BYTES // 8))()
+            _check(load().paged_kv_maps(packed, heads, D, maps, _PAGED_MAPS_BYTES), w)
+            packed = _PAGED_KV.pack(*fields, ctypes.addressof(maps))
+        self.__dict__.update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, layout=layout, device=device,
+                             page_size=page_size, heads=heads, D=D, packed=packed, _maps=maps)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"PagedKV.{name} is read-only: make another PagedKV")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"PagedKV.{name} is read-only")
+
+    def __reduce__(self):  # `packed` and `_maps` hold addresses
+        return type(self), (self.k, self.v, self.layout, self.k_scale, self.v_scale)
 
 
 def paged_kv_append(k, v, cache: PagedKV, slots, q=None, q_out=None, positions=None, phases=None,
