@@ -476,19 +476,23 @@ class PagedKV:
 
     def __init__(self, k, v, layout: str = "NHD", k_scale=None, v_scale=None):
         w = "PagedKV"
-        if layout not in ("NHD", "HND") or k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+        if layout not in ("NHD", "HND") or k.dim() != 4 or k.shape != v.shape:
+            _bad(w)
+        # a dimension of one may carry any stride: here a row's, which is a valid one
+        strides, of_v = ([s if n > 1 else k.shape[3] for n, s in zip(t.shape[:3], t.stride())] for t in (k, v))
+        if strides != of_v:
             _bad(w)
         if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype is not k.dtype:
             _bad(w)
         device = k.get_device()
-        if device < 0 or v.get_device() != device or k.stride(3) != 1:
+        if device < 0 or v.get_device() != device or k.stride(3) != 1 or v.stride(3) != 1:
             _bad(w)
         slot, head = (1, 2) if layout == "NHD" else (2, 1)
         page_size, heads, D = k.shape[slot], k.shape[head], k.shape[3]
         fields = (k.data_ptr(), v.data_ptr(),
                   0 if k_scale is None else _vector(k_scale, torch.float32, heads, device, w),
                   0 if v_scale is None else _vector(v_scale, torch.float32, heads, device, w),
-                  k.stride(0), k.stride(slot), k.stride(head), k.shape[0], page_size,
+                  strides[0], strides[slot], strides[head], k.shape[0], page_size,
                   SV_BF16 if k.dtype is torch.bfloat16 else SV_E4M3)
         packed, maps = _PAGED_KV.pack(*fields, 0), None
         if D in (128, 256):  # what paged_attn reads
