@@ -92,6 +92,7 @@ struct Params {
   int stages;
   int min_units;  // least units per CTA
   int by_head;    // desc is indexed by b * Hkv + h (else by CTA)
+  int stall;      // test aid: the ring's first slot never fills
 };
 
 // Chunks of one sequence that some row sees: the first `ns` chunks, then
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid < NST) {
-    mbar_init(&full[tid], 2);  // K and V
+    mbar_init(&full[tid], 2 + (tid == 0 ? P.stall : 0));  // K and V
     mbar_init(&empty[tid], MT);
     fence_barrier_init();
   }
@@ -516,6 +517,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         kt[c] = smem_u32(ring + (at + c) * LY::STAGE);
         if (ok) ok = mbar_wait(&full[at + c], parity, P.err);
       }
+      // a limit may run out in some lanes while the phase completes for others
+      ok = __all_sync(0xffffffffu, ok);
       const int now = at;
       at += NCH * NL;
       if (at >= NST) {
@@ -1037,6 +1040,7 @@ sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const int32_t *
   P.num_pages = (int)cache->num_pages;
   P.min_units = 8;
   P.by_head = (long long)B * Hkv <= sms ? 1 : 0;
+  P.stall = launch_flags() & SV_LAUNCH_TEST_STALL_COPY ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool f8 = cache->dtype == SV_E4M3;
   return from_cuda(D == 256 ? paged::launch_all<256>(f8, mk, mv, P, sms, s)
