@@ -102,6 +102,7 @@ struct Params {
   float sl2e;
   int window, sinks;
   int few_slots;  // long prefix sums take the place of some
+  int stall;      // test aid: the first slot of the K ring never fills
 };
 
 struct Item {
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < 10; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 1 + (i == 0 ? P.stall : 0));
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -459,6 +460,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
       uint32_t oc[NT] = {};               // items of each tile
       while (ok) {
         wait(q_full, c & 1);
+        // (a limit may run out in some lanes while the phase completes for others)
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++c;
         // n blocks, nt tiles; the last block's rows past the sequence's keys
@@ -889,6 +892,7 @@ sv_status window_attn(const sv_rows *q, const sv_rows *k, const sv_rows *v, cons
   P.sl2e = scale * 1.4426950408889634f;
   P.window = window;
   P.sinks = sinks;
+  P.stall = launch_flags() & SV_LAUNCH_TEST_STALL_COPY ? 1 : 0;
   return window::run_any(q, k, v, P, D, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
