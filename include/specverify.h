@@ -367,12 +367,14 @@ SV_API sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const in
  *   o = softmax_j(scale * <q, k_j>) . v_j, zeros for a row that sees nothing.
  * cu_q, cu_k: device int32 [B+1], 0 <= cu[b] <= cu[b+1] <= Tq (Tk).  A sequence
  *   whose offsets break this is left out and reported by
- *   sv_last_device_error() as SV_ERR_INVALID_ARG.  Rows of o of no sequence
- *   are not written.
+ *   sv_last_device_error() as SV_ERR_INVALID_ARG (all are, where the others
+ *   name rows so often that they hold more than Tq and B of them can).  Rows
+ *   of o of no sequence are not written.
  * Keys and values of a sequence hold finite values; rows of others, and rows
  * of no sequence, may hold anything.
  * Supported: D in {128, 256}; Hq % Hkv == 0; Hq/Hkv <= 128; 0 <= B <= 4096;
- *   Tq, Tk <= 2^30; strides of q, k and v above 0; scale > 0 and finite.
+ *   Tq, Tk <= 2^30; (Tq / (128 / (Hq/Hkv)) + B) * Hkv <= 2^31 - 2^16, divisions
+ *   rounded down; strides of q, k and v above 0; scale > 0 and finite.
  * One launch.  It needs no workspace at present: the query gives 0, and NULL
  * with 0 bytes is accepted. */
 SV_API size_t window_attn_workspace_bytes(int B, int Hq, int Hkv, int D);

@@ -99,6 +99,7 @@ struct Params {
   unsigned *err;
   int B, Tq, Tk, Hkv, G, PT;  // PT: positions per tile
   uint32_t by_span;  // 2^32 over the positions of an item
+  int most;          // items a KV head that sequences without common rows can have
   float sl2e;
   int window, sinks;
   int few_slots;  // long prefix sums take the place of some
@@ -290,6 +291,9 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
   pdl_wait();
 
   // ---- prefix sums of the sequences' items per KV head ----
+  // Offsets that fall and rise again can name the same rows thousands of times:
+  // the sums stay at the top instead of wrapping, and then no item is left.
+  auto sum = [](int a, int b) { return (int)min((unsigned)a + (unsigned)b, 0x7fffffffu); };
   int total = 0;
   for (int b0 = 0; b0 < P.B; b0 += C::THREADS) {
     const int b = b0 + tid;
@@ -300,20 +304,24 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::THREADS, 1)
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      if (lane >= o) x = sum(x, y);
     }
     if (lane == 31) wsum[warp] = x;
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < C::THREADS / 32; ++w) {
-      if (w < warp) before += wsum[w];
-      all += wsum[w];
+      if (w < warp) before = sum(before, wsum[w]);
+      all = sum(all, wsum[w]);
     }
-    if (b < P.B) pre[b] = total + before + x - nt;
+    if (b < P.B) pre[b] = sum(total, sum(before, x)) - nt;
     if (b < P.B && b < MAX_SORTED) where[b] = make_int2(nk - nq, nk);
-    total += all;
+    total = sum(total, all);
     __syncthreads();
+  }
+  if (total > P.most) {
+    if (tid == 0 && blockIdx.x == 0) atomicOr(P.err, ERR_INDEX);
+    total = 0;
   }
   if (tid == 0) pre[P.B] = total;
   tc::fence_before_sync();
@@ -821,7 +829,8 @@ static sv_status run(const sv_rows *q, const sv_rows *k, const sv_rows *v, Param
   const size_t smem = C::RING + (P.few_slots ? 128 * 1024 + prefix : 160 * 1024);
   static_assert(C::RING + 160 * 1024 <= 227 * 1024 && C::RING + 128 * 1024 + (MAX_B + 1) * 4 <= 227 * 1024, "shared memory");
   // at most one item more per sequence than the rows fill
-  const long long items = ((long long)P.Tq / (P.PT * C::NT) + P.B) * P.Hkv;
+  P.most = P.Tq / (P.PT * C::NT) + P.B;
+  const long long items = (long long)P.most * P.Hkv;
   const int ctas = (int)lmin(items, sms);
   return from_cuda(launch_early(window_kernel<D, TILES>, dim3(ctas), dim3(C::THREADS), smem, s, mq, mk, mv,
                                 mkp, mvp, P));
@@ -872,9 +881,9 @@ sv_status window_attn(const sv_rows *q, const sv_rows *k, const sv_rows *v, cons
   if ((Tq > 1 && !q->token_stride) || (Hq > 1 && !q->head_stride)) return SV_ERR_UNSUPPORTED;
   for (const sv_rows *r : {k, v})
     if ((Tk > 1 && !r->token_stride) || (Hkv > 1 && !r->head_stride)) return SV_ERR_UNSUPPORTED;
-  // the items of all KV heads are counted in 31 bits
+  // the items of all KV heads, and the places of a round behind them, are counted in 31 bits
   const int pt = window::ROWS / G;
-  if (((long long)Tq / pt + B) * Hkv > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
+  if (((long long)Tq / pt + B) * Hkv > 0x7fff0000LL) return SV_ERR_UNSUPPORTED;
   const int sms = device_sm_count();
   if (sms <= 0) return SV_ERR_CUDA;
   window::Params P{};
