@@ -348,7 +348,8 @@ SV_API sv_status paged_kv_append(const sv_rows *q, const sv_rows *q_out, const s
  * Slots that no row of the sequence sees may hold anything, NaN included;
  * those that some row sees hold finite values.
  * Supported: D in {128, 256}; Hq % Hkv == 0; M*(Hq/Hkv) <= 128; 0 <= B <= 4096;
- *   table_width*page_size <= 2^30, B*Hkv times that <= 2^35; scale > 0 and finite.
+ *   table_width*page_size <= 2^30; B*Hkv*(table_width*page_size/16 + 12) < 2^31;
+ *   M*Hq*D <= 2^33; window <= 2^30; scale > 0 and finite.
  * Two launches; lengths and tables are read on the device, so a captured call
  * follows their contents. */
 SV_API size_t paged_attn_workspace_bytes(int B, int M, int Hq, int Hkv, int D);
@@ -374,7 +375,8 @@ SV_API sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const in
  * of no sequence, may hold anything.
  * Supported: D in {128, 256}; Hq % Hkv == 0; Hq/Hkv <= 128; 0 <= B <= 4096;
  *   Tq, Tk <= 2^30; (Tq / (128 / (Hq/Hkv)) + B) * Hkv <= 2^31 - 2^16, divisions
- *   rounded down; strides of q, k and v above 0; scale > 0 and finite.
+ *   rounded down; strides of q, k and v above 0; window <= 2^30; scale > 0
+ *   and finite.
  * One launch.  It needs no workspace at present: the query gives 0, and NULL
  * with 0 bytes is accepted. */
 SV_API size_t window_attn_workspace_bytes(int B, int Hq, int Hkv, int D);

@@ -997,6 +997,8 @@ sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const int32_t *
   if (cs != SV_OK) return cs;
   if (B > 0 && (!block_table || !kv_lens)) return SV_ERR_INVALID_ARG;
   if (!paged::aligned(block_table, 4) || !paged::aligned(kv_lens, 4)) return SV_ERR_INVALID_ARG;
+  // the groups of eight of a sequence's rows are counted in 31 bits, with room for a step
+  if ((long long)M * Hq * D > 1LL << 33) return SV_ERR_UNSUPPORTED;
   // positions are 32-bit (with room for a window), and so is the line of units
   const long long cap = (long long)table_width * cache->page_size;
   if (cap > 0x40000000LL || window > 0x40000000 || (cap / paged::CHUNK + paged::HEAD_COST) * imax(B, 1) > 0x7fffffffLL / Hkv)
