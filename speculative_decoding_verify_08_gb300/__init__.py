@@ -387,18 +387,27 @@ def _bad(where: str, status: int = SV_ERR_INVALID_ARG):
 _BF16 = torch.bfloat16
 
 
+# GPUs of this process, once known.  With one, what is a GPU's is on it, and
+# asking every tensor for its device (0.2 us each) is left out.
+_gpus = 0
+
+
 def _device(t, where):
     """The device of a call, that of its first operand.  The library launches on
-    the current one, so it has to be that, and the other operands' too."""
+    the current one, so it has to be that, and the other operands' too.  None:
+    the only one there is."""
+    global _gpus
     d = t.get_device()
     if d < 0 or d != torch._C._cuda_getDevice():
         _bad(where)
-    return d
+    _gpus = _gpus or torch._C._cuda_getDeviceCount()
+    return d if _gpus > 1 else None
 
 
 def _rows(t, tokens, heads, D, dev, where):
     """sv_rows of a bf16 tensor [tokens, heads, D] of the call's device (any strides, D contiguous)."""
-    if t.dtype is not _BF16 or t.shape != (tokens, heads, D) or t.get_device() != dev:
+    if t.dtype is not _BF16 or t.shape != (tokens, heads, D) or not t.is_cuda or (
+            dev is not None and t.get_device() != dev):
         _bad(where)
     ts, hs, ds = t.stride()
     if ds != 1:
@@ -409,7 +418,8 @@ def _rows(t, tokens, heads, D, dev, where):
 
 def _vector(t, dtype, n, dev, where):
     """Address of a contiguous tensor of n values of the call's device."""
-    if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous() or (
+            dev is not None and t.get_device() != dev):
         _bad(where)
     return t.data_ptr()
 
@@ -417,7 +427,7 @@ def _vector(t, dtype, n, dev, where):
 def _launch_stream(dev, stream):
     """The given stream, or the current one of the call's device."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return torch._C._cuda_getCurrentRawStream(dev or 0)
     return _stream(stream)
 
 
@@ -456,7 +466,7 @@ def qk_norm_rope(q, k, q_out, k_out, positions=None, phases=None, q_weight=None,
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     w = "qk_norm_rope"
-    dev = _device(q, w)
+    dev = None if _gpus == 1 else _device(q, w)
     norm, rot = _norm_rotation(q_weight, k_weight, eps, weight_offset, positions, phases, interleaved, T, D, dev, w)
     status = load().qk_norm_rope(_rows(q, T, Hq, D, dev, w), _rows(k, T, Hkv, D, dev, w),
                                  _rows(q_out, T, Hq, D, dev, w), _rows(k_out, T, Hkv, D, dev, w), norm, rot, T, Hq,
@@ -520,8 +530,9 @@ def paged_kv_append(k, v, cache: PagedKV, slots, q=None, q_out=None, positions=N
     and in the same launch the queries' rows to q_out when q is given."""
     T, Hkv, D = k.shape
     w = "paged_kv_append"
-    dev = _device(k, w)
-    if Hkv != cache.heads or D != cache.D or dev != cache.device or (q is None) != (q_out is None):
+    dev = None if _gpus == 1 else _device(k, w)
+    if Hkv != cache.heads or D != cache.D or (q is None) != (q_out is None) or (
+            dev is not None and dev != cache.device):
         _bad(w)
     Hq = 0 if q is None else q.shape[1]
     norm, rot = _norm_rotation(q_weight if q is not None else None, k_weight, eps, weight_offset, positions,
@@ -547,9 +558,12 @@ def paged_attn(q, cache: PagedKV, block_table, kv_lens, o, M: int, scale: float,
     rows, Hq, D = q.shape
     w = "paged_attn"
     B, width = block_table.shape
-    dev = _device(q, w)
-    if (D != cache.D or rows != B * M or dev != cache.device or block_table.dtype is not torch.int32
-            or block_table.get_device() != dev or (workspace is not None and workspace.get_device() != dev)):
+    dev = None if _gpus == 1 else _device(q, w)
+    if (D != cache.D or rows != B * M or block_table.dtype is not torch.int32 or not block_table.is_cuda
+            or (workspace is not None and not workspace.is_cuda)):
+        _bad(w)
+    if dev is not None and (dev != cache.device or block_table.get_device() != dev
+                            or (workspace is not None and workspace.get_device() != dev)):
         _bad(w)
     ts, es = block_table.stride()
     if es != 1 and width != 1:
@@ -575,7 +589,7 @@ def window_attn(q, k, v, o, cu_q, cu_k, scale: float, window: int = 0, sinks: in
     Tk, Hkv, _ = k.shape
     w = "window_attn"
     n = cu_q.shape[0]
-    dev = _device(q, w)
+    dev = None if _gpus == 1 else _device(q, w)
     status = load().window_attn(_rows(q, Tq, Hq, D, dev, w), _rows(k, Tk, Hkv, D, dev, w),
                                 _rows(v, Tk, Hkv, D, dev, w), _rows(o, Tq, Hq, D, dev, w),
                                 _vector(cu_q, torch.int32, n, dev, w), _vector(cu_k, torch.int32, n, dev, w), n - 1,

@@ -15,6 +15,7 @@ def sv(monkeypatch):
     import speculative_decoding_verify_08_gb300 as sv
     sv.load()
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(sv, "_gpus", 2)
     return sv
 
 
@@ -101,3 +102,15 @@ def test_cache_scales(sv):
     refused(sv, lambda: sv.PagedKV(k, v, k_scale=On(0, 2, dtype=torch.float32), v_scale=s))
     refused(sv, lambda: sv.PagedKV(k, v, k_scale=s, v_scale=On(0, 2, dtype=torch.float32)))
     sv.PagedKV(k, v, k_scale=s, v_scale=s)   # a cache may be made while another device is current
+
+
+def test_one_gpu(sv, monkeypatch):
+    """The only GPU is not asked for tensor by tensor; CPU memory is refused all the same."""
+    monkeypatch.setattr(sv, "_gpus", 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDeviceCount", lambda: 1)
+    q, k, cpu = On(0, 0, 8, 64), On(0, 0, 2, 64), torch.empty(0, 2, 64, dtype=torch.bfloat16)
+    sv.qk_norm_rope(q, k, q, k, stream=0)
+    assert sv._gpus == 1
+    sv.qk_norm_rope(q, k, q, k, stream=0)
+    for args in ((q, k, q, cpu), (q, cpu, q, k), (torch.empty(0, 8, 64, dtype=torch.bfloat16), k, q, k)):
+        refused(sv, lambda: sv.qk_norm_rope(*args, stream=0))
