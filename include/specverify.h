@@ -247,7 +247,8 @@ SV_API sv_status verify_attn_noalloc(const void *q, const void *k_cache,
  * given; these calls are what stands before and around verify_attn.) */
 
 /* Rows [token][head][D], D contiguous: strides in elements, non-negative
- * multiples of 8; ptr device, 16-byte aligned (bf16). */
+ * multiples of 8, at most 2^31 (token) and 2^39 (head); ptr device, 16-byte
+ * aligned (bf16). */
 typedef struct {
   void *ptr;
   int64_t token_stride, head_stride;
@@ -293,9 +294,10 @@ SV_API sv_status qk_norm_rope(const sv_rows *q, const sv_rows *k, const sv_rows 
  * element p*page_stride + s*slot_stride + h*head_stride of k and of v (any
  * order of the three; D contiguous).  dtype SV_BF16, or SV_E4M3: the stored
  * value times k_scale[h] (v_scale[h]) is the key (value); scales: device fp32
- * [Hkv], > 0, NULL for 1 (and NULL at bf16).  k, v: device, 16-byte aligned;
- * strides positive multiples of 16 bytes.  page_size a multiple of 16, at
- * most 2^16; 1 <= num_pages < 2^31.
+ * [Hkv], from 2^-100 to 2^100, NULL for 1 (and NULL at bf16).  k, v: device,
+ * 16-byte aligned; strides positive multiples of 16 bytes, at most 2^38 elements.
+ * page_size a multiple of 16, at most 2^16; 1 <= num_pages < 2^31.  (D = 64 is
+ * for readers of the caller's own: paged_attn takes 128 and 256.)
  * maps: host, SV_PAGED_MAPS_BYTES bytes that paged_kv_maps made from these very
  * fields, or NULL (paged_attn then makes them itself in every call, about
  * 0.7 us of host time). */
@@ -347,6 +349,12 @@ SV_API sv_status paged_kv_append(const sv_rows *q, const sv_rows *q_out, const s
  *   SV_ERR_INVALID_ARG.
  * Slots that no row of the sequence sees may hold anything, NaN included;
  * those that some row sees hold finite values.
+ * Arithmetic fp32, with the second product's operands in 16 bits.  bf16 pages:
+ *   each probability is rounded to bf16 (2^-8 relative).  e4m3 pages: to fp16,
+ *   2^-11 relative down to 2^-27 of the row's largest, by 2^-38 of that below;
+ *   and a query row's elements, scaled by a power of two, to fp16 (exact down to
+ *   2^-14 of its largest, by 2^-25 of that below).  Sums take the probabilities
+ *   as they were.
  * Supported: D in {128, 256}; Hq % Hkv == 0; M*(Hq/Hkv) <= 128; 0 <= B <= 4096;
  *   table_width*page_size <= 2^30; B*Hkv*(table_width*page_size/16 + 12) < 2^31;
  *   M*Hq*D <= 2^33; window <= 2^30; scale > 0 and finite.
@@ -373,6 +381,8 @@ SV_API sv_status paged_attn(const sv_rows *q, const sv_paged_kv *cache, const in
  *   of o of no sequence are not written.
  * Keys and values of a sequence hold finite values; rows of others, and rows
  * of no sequence, may hold anything.
+ * Arithmetic fp32, each probability rounded to bf16 (2^-8 relative) for the
+ *   second product; sums take it as it was.
  * Supported: D in {128, 256}; Hq % Hkv == 0; Hq/Hkv <= 128; 0 <= B <= 4096;
  *   Tq, Tk <= 2^30; (Tq / (128 / (Hq/Hkv)) + B) * Hkv <= 2^31 - 2^16, divisions
  *   rounded down; strides of q, k and v above 0; window <= 2^30; scale > 0

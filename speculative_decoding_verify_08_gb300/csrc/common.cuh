@@ -55,7 +55,7 @@ inline sv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV
 // the flags say.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_as(bool early, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                         cudaStream_t stream, Args &&...args) {
+                      cudaStream_t stream, Args &&...args) {
   if (smem > 0) {
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess) return e;

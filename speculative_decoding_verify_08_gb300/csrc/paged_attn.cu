@@ -40,13 +40,15 @@
 // maximum keep 2^-11, smaller ones are off by 2^-38 of the maximum at most
 // (against 1 for the maximum, many small ones beside a large one lost 2^-25
 // each, up to all of their share).
-// An e4m3 cache is converted in registers to fp16, which holds every e4m3
-// value exactly; the queries are scaled by a power of two per row to fit fp16.
-// Measured: 48 sequences of 40 to 16000 slots, 32/8 heads of 128: 96 us, 6.3 TB/s;
-// 64 with a window of 4096 on 16 heads: 305 us, 6.7 TB/s; one of 32768, 4 rows,
-// 24/4 heads of 256: 26.5 us, 5.1 TB/s (start and join of a short stream); one of
-// 777: 8.8 us; 24 of 500 to 32000, 4 rows, e4m3 pages, 24/4 heads of 256: 134 us,
-// 3.8 TB/s, held back by the conversions, which both 16-row tiles' warps make.
+// An e4m3 cache is converted in registers to fp16; the queries are scaled by a
+// power of two per row to fit fp16: exact down to 2^-14 of a row's largest
+// element, off by 2^-25 of that below.
+// Measured, as calls: 48 sequences of 40 to 16000 slots, 32/8 heads of 128: 96 us,
+// 6.2 TB/s; 64 with a window of 4096 on 16 heads: 306 us, 6.7 TB/s; one of 32768, 4
+// rows, 24/4 heads of 256: 28.8 us (27.2 on the GPU), 4.7 TB/s (start and join of
+// a short stream); one of 777: 9.0 us (8.8); over e4m3 pages, 24 of 500 to 32000,
+// 24/4 heads of 256: one row 89 us, 5.7 TB/s; 4 rows 135 us, 3.7 TB/s, held back by
+// the conversions, which both 16-row tiles' warps make.
 #include <cstring>
 
 #include "paged.cuh"
@@ -438,35 +440,35 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
 #pragma unroll
       for (int k = 0; k < QB; ++k) {
-      const int r = (x0 + k * NCW * 32) / (D / 8), c = x0 % (D / 8);
-      const uint4 v = qv[k];
-      uint8_t *tile = qs + (r >> 4) * 16 * D * 2;
-      const int rr = r & 15;
-      if (!F8) {
-        *reinterpret_cast<uint4 *>(tile + swz16(rr, c)) = v;
-      } else {
-        // fp16 rows scaled so that the largest element is in [1, 2); within 16
-        // elements, 4t..4t+3 go where an e4m3 word's elements meet them
-        float f[8] = {bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y),
-                      bf16lo(v.z), bf16hi(v.z), bf16lo(v.w), bf16hi(v.w)};
-        float mx = 0.f;
+        const int r = (x0 + k * NCW * 32) / (D / 8), c = x0 % (D / 8);
+        const uint4 v = qv[k];
+        uint8_t *tile = qs + (r >> 4) * 16 * D * 2;
+        const int rr = r & 15;
+        if (!F8) {
+          *reinterpret_cast<uint4 *>(tile + swz16(rr, c)) = v;
+        } else {
+          // fp16 rows scaled so that the largest element is in [1, 2); within 16
+          // elements, 4t..4t+3 go where an e4m3 word's elements meet them
+          float f[8] = {bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y),
+                        bf16lo(v.z), bf16hi(v.z), bf16lo(v.w), bf16hi(v.w)};
+          float mx = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(f[e]));
+          for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(f[e]));
 #pragma unroll
-        for (int o = D / 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        int ex = (int)(__float_as_uint(mx) >> 23) - 127;
-        if (ex < -126 || ex > 126) ex = ex < 0 ? (mx > 0.f ? -126 : 0) : (ex > 127 ? 0 : 126);
-        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-        if (c == 0) qsc[r] = __uint_as_float((uint32_t)(127 + ex) << 23);
-        uint32_t w[4];
+          for (int o = D / 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          int ex = (int)(__float_as_uint(mx) >> 23) - 127;
+          if (ex < -126 || ex > 126) ex = ex < 0 ? (mx > 0.f ? -126 : 0) : (ex > 127 ? 0 : 126);
+          const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+          if (c == 0) qsc[r] = __uint_as_float((uint32_t)(127 + ex) << 23);
+          uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(f[2 * e] * down, f[2 * e + 1] * down);
-        // chunk c holds elements 8(c&1).. of its group of 16: t = 2(c&1), 2(c&1)+1
-        const int g16 = c & ~1, t = 2 * (c & 1);
-        uint32_t *lo16 = reinterpret_cast<uint32_t *>(tile + swz16(rr, g16));
-        uint32_t *hi16 = reinterpret_cast<uint32_t *>(tile + swz16(rr, g16 + 1));
-        lo16[t] = w[0], hi16[t] = w[1], lo16[t + 1] = w[2], hi16[t + 1] = w[3];
-      }
+          for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(f[2 * e] * down, f[2 * e + 1] * down);
+          // chunk c holds elements 8(c&1).. of its group of 16: t = 2(c&1), 2(c&1)+1
+          const int g16 = c & ~1, t = 2 * (c & 1);
+          uint32_t *lo16 = reinterpret_cast<uint32_t *>(tile + swz16(rr, g16));
+          uint32_t *hi16 = reinterpret_cast<uint32_t *>(tile + swz16(rr, g16 + 1));
+          lo16[t] = w[0], hi16[t] = w[1], lo16[t + 1] = w[2], hi16[t + 1] = w[3];
+        }
       }
     }
     named_barrier(1, NCW * 32);
@@ -812,7 +814,10 @@ __device__ __forceinline__ size_t piece(int c, int i) { return (size_t)(c + i) *
 
 // Few heads, each in many pieces: a block per (head, row); a thread per piece
 // works out the weights, then groups of D/4 threads share the pieces' rows,
-// the first rows' loads being under way meanwhile.
+// the first AHEAD rows of a group under way meanwhile: 40 pieces at D = 256, 80
+// at 128, as many as one sequence of four (two) KV heads has.  (4: 28.5 against
+// 27.5 us for one of 32768, 11.0 against 10.3 for one of 8000; 16: 27.0 and 10.5,
+// but 9.03 against 8.83 for one of 777.)
 template <int D>
 __global__ void __launch_bounds__(JOIN_THREADS) join_few_kernel(const Params P) {
   constexpr int LPG = D / 4, NG = JOIN_THREADS / LPG, AHEAD = 10;

@@ -27,7 +27,8 @@
 //    floating-point arithmetic is needed.
 // Measured: 16381 tokens of 32 + 8 heads of 128: 57 us, 5.9 TB/s of 6.7; 30011
 // tokens' keys and values of 4 heads of 256 into e4m3 pages: 38 us, 4.9 TB/s, held
-// back by instructions (60% of the issue slots); 4 to 61 tokens: 2.3-2.5 us.
+// back by instructions (60% of the issue slots), into bf16 pages: 41 us, 6.0 TB/s; 4
+// to 61 tokens: 2.3-2.5 us.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -64,8 +65,9 @@ struct Params {
 };
 
 // Cosine and sine of position * phase / 2^64 turns.  The product's upper 32
-// bits, as a signed fraction of a turn, are off by 2^-33 turns at most, below
-// the fp32 rounding of the fraction itself.
+// bits, as a signed fraction of a turn, are short by 2^-32 turns at most (and
+// the phase's own rounding, 2^-34 at position 2^31), below the fp32 rounding of
+// the fraction itself (2^-26).
 __device__ __forceinline__ float2 turn(int pos, unsigned long long phase) {
   const unsigned long long f = (unsigned long long)(long long)pos * phase;
   float s, c;

@@ -40,12 +40,14 @@
 //  * The maximum that P refers to is raised only when a block exceeds it by
 //    more than 2^8, so O is rarely rescaled; P is rounded to bf16 (relative
 //    2^-8 at most, as the second product's operand), sums are fp32.
-// Measured: 8000 rows of 24/4 heads of 256, causal: 445-485 us, 1.62-1.77 PFLOP/s
-// (bound by the tensor cores); 8192 rows of 32/8 heads of 128, causal: 357 us,
-// 1.55 PFLOP/s, with a window of 1024 and 4 first keys 116 us (the softmax of two
-// tiles, about 1750 clocks a block each, and its hand-overs); seven prompts of 2
-// to 901 rows, 32/8 heads of 128: 19.4 us (three items of 1 to 8 blocks a CTA;
-// start 2600 clocks, end of an item 3200, a block 1850).
+// Measured, on the GPU: 8000 rows of 24/4 heads of 256, causal: 465-495 us over
+// several GPUs, 1.59-1.69 PFLOP/s (bound by the tensor cores and by power; 515-524
+// us as single calls, 1.50-1.53); 8192 rows of 32/8 heads of 128, causal: 355 us, 1.55
+// PFLOP/s (379 as a call), with a window of 1024 and 4 first keys 117 us (121; the
+// softmax of two tiles, about 1750 clocks a block each, and its hand-overs); 2048
+// rows behind 6144 keys, 32/8 heads of 128: 207 us as a call, 1.16 PFLOP/s (1.7
+// items a CTA); seven prompts of 2 to 901 rows, 32/8 heads of 128: 19.5 us (three
+// items of 1 to 8 blocks a CTA; start 2600 clocks, end of an item 3200, a block 1850).
 #include "paged.cuh"
 #include "tcgen05.cuh"
 
