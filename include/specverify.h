@@ -20,6 +20,8 @@
  *   paged_kv_append -- the same on the way into a paged bf16 or e4m3 cache
  *   paged_attn      -- one-token / verify-row attention over that cache
  *   window_attn     -- causal attention of packed prompts
+ *   gdn_chunk       -- recurrent layers: packed chunks over a pool of states
+ *   gdn_step        -- recurrent layers: one token / verify rows over that pool
  *
  * Conventions shared by every entry point
  *   - Pointers marked "device" are caller-owned device memory on the current
@@ -545,6 +547,70 @@ SV_API sv_status gdn_verify(float *state, const void *tape_k, const void *tape_v
                             const void *q, const void *k, const void *v, const float *g,
                             const float *beta, void *o, sv_dtype o_dtype, int M, int Hk, int Hv,
                             int dk, int dv, sv_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* GatedDeltaNet over a pool of states                                      */
+/* ---------------------------------------------------------------------- */
+/* The recurrent layers of many sequences: their states stand in a pool, the
+ * way their keys and values stand in pages; prompts and chunks of prompts run
+ * through gdn_chunk, the steps behind them through gdn_step.  The rule, the
+ * heads and the gates are gdn_verify's; rows are strided (a slice of a fused
+ * projection's rows will do), gates fp32 [rows][Hv] contiguous. */
+
+/* States fp32 [slot][Hv][dv][dk], the last three contiguous: slot_stride in
+ * elements, a multiple of 4 and at least Hv*dv*dk (any where num_slots is 1);
+ * ptr device, 16-byte aligned; 1 <= num_slots < 2^31. */
+typedef struct {
+  float *ptr;
+  int64_t slot_stride, num_slots;
+} sv_states;
+
+/* M newest rows of each of B sequences, behind what each accepted of its last
+ * round.  For sequence b, with S its state:
+ *   the first n_replay[b] of the tape's rows b*tape_M .. are applied to S;
+ *   the M rows b*M .. run on from there and give o;
+ *   S goes back into the pool as it stood after the tape (commit == 0: the next
+ *   call's tape brings the accepted rows), or after the M rows too (commit != 0:
+ *   plain decoding, prompts of a few tokens).  A state that no token changed is
+ *   not written.
+ * slots: device int32 [B], the sequences' places in the pool; negative: the
+ *   sequence starts from zeros and its state is not kept (rows that fill up a
+ *   captured batch).  Two sequences of a call with one slot >= 0: that state is
+ *   undefined afterwards.
+ * n_replay: device int32 [B], 0..tape_M; NULL: no tape (the tape's arguments are
+ *   not read).  A count outside counts as the nearest of 0 and tape_M, a slot past
+ *   the pool as negative; both are reported by sv_last_device_error() as
+ *   SV_ERR_INVALID_ARG.
+ * tape_k, k, q: bf16 rows [..][Hk][dk]; tape_v, v: bf16 rows [..][Hv][dv]; o: bf16 or
+ *   fp32 rows [B*M][Hv][dv] (o_dtype; strides as for bf16 rows).  M = 0 only commits
+ *   (q, k, v, g, beta, o are not read).
+ * fp32 arithmetic throughout, in the order of the tokens.
+ * Supported: dk in {64, 128, 256}; Hv % Hk == 0, Hv <= 65535; dv <= 65536; M <= 64,
+ *   tape_M <= 64; 0 <= B <= 65535.  One launch; slots and counts are read on the
+ *   device, so a captured call follows their contents. */
+SV_API sv_status gdn_step(const sv_states *states, const int32_t *slots, const sv_rows *tape_k,
+                          const sv_rows *tape_v, const float *tape_g, const float *tape_beta,
+                          const int32_t *n_replay, int tape_M, const sv_rows *q, const sv_rows *k,
+                          const sv_rows *v, const float *g, const float *beta, const sv_rows *o,
+                          sv_dtype o_dtype, int B, int M, int commit, int Hk, int Hv, int dk, int dv,
+                          sv_stream_t stream);
+
+/* Packed chunks of new tokens: sequence b's are rows cu[b]..cu[b+1]-1 of q, k, v,
+ * g, beta and o (bf16).  They run through the rule from the sequence's state,
+ * which is then written back (a new sequence's slot holds zeros).
+ * cu: device int32 [B+1], 0 <= cu[b] <= cu[b+1] <= T.  A sequence whose offsets
+ *   break this is left out and reported by sv_last_device_error() as
+ *   SV_ERR_INVALID_ARG; rows of o of no sequence are not written, nor is the state of
+ *   a sequence without rows.  slots: as gdn_step's.
+ * Supported: dk in {64, 128}; Hv % Hk == 0, Hv <= 65535; dv <= 65536; 0 <= B <= 65535;
+ *   T <= 2^30.
+ * It needs no workspace at present: the query gives 0, and NULL with 0 bytes is
+ * accepted. */
+SV_API size_t gdn_chunk_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv);
+SV_API sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows *q,
+                           const sv_rows *k, const sv_rows *v, const float *g, const float *beta,
+                           const sv_rows *o, const int32_t *cu, int B, int T, int Hk, int Hv, int dk,
+                           int dv, void *workspace, size_t ws_bytes, sv_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* Draft depth                                                              */

@@ -47,6 +47,7 @@ __all__ = [
     "gdn_verify",
     "SV_E4M3", "rope_phases", "qk_norm_rope", "PagedKV", "paged_kv_append",
     "paged_attn_workspace_bytes", "paged_attn", "window_attn_workspace_bytes", "window_attn",
+    "gdn_step", "gdn_chunk_workspace_bytes", "gdn_chunk",
 ]
 
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_CUDA = 0, 1, 2, 3
@@ -127,6 +128,9 @@ def load():
             "paged_attn_workspace_bytes": (Z, [I, I, I, I, I]),
             "paged_attn": (I, [P, P, P, L, I, P, P, I, I, I, I, I, ctypes.c_float, I, I, P, Z, P]),
             "window_attn_workspace_bytes": (Z, [I, I, I, I]),
+            "gdn_step": (I, [P, P, P, P, P, P, P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P]),
+            "gdn_chunk_workspace_bytes": (Z, [I, I, I, I, I, I]),
+            "gdn_chunk": (I, [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, P, Z, P]),
             "window_attn": (I, [P, P, P, P, P, P, I, I, I, I, I, I, ctypes.c_float, I, I, P, Z, P]),
         }
         for name, (res, args) in sig.items():
@@ -375,6 +379,7 @@ _ROWS = struct.Struct("Pqq")            # sv_rows
 _NORM = struct.Struct("PPff")           # sv_head_norm
 _ROTATION = struct.Struct("PPii")       # sv_rotation
 _PAGED_KV = struct.Struct("PPPPqqqqiiP")  # sv_paged_kv
+_STATES = struct.Struct("Pqq")          # sv_states
 _PAGED_MAPS_BYTES = 256
 
 
@@ -595,5 +600,101 @@ def window_attn(q, k, v, o, cu_q, cu_k, scale: float, window: int = 0, sinks: in
                                 _vector(cu_q, torch.int32, n, dev, w), _vector(cu_k, torch.int32, n, dev, w), n - 1,
                                 Tq, Tk, Hq, Hkv, D, scale, window, sinks, _ptr(workspace), _nbytes(workspace),
                                 _launch_stream(dev, stream))
+    if status:
+        _check(status, w)
+
+
+# ----------------------------------------------- recurrent layers over a pool ----
+def _states(t, dev, where):
+    """sv_states of an fp32 tensor [slots, Hv, dv, dk] of the call's device (any slot stride, the rest contiguous)."""
+    if t.dtype is not torch.float32 or t.dim() != 4 or not t.is_cuda or (dev is not None and t.get_device() != dev):
+        _bad(where)
+    n, Hv, dv, dk = t.shape
+    s0, *rest = t.stride()
+    # a dimension of one may carry any stride
+    if any(m > 1 and s != want for m, s, want in zip((Hv, dv, dk), rest, (dv * dk, dk, 1))):
+        _bad(where)
+    return _STATES.pack(t.data_ptr(), s0 if n > 1 else Hv * dv * dk, n)
+
+
+def _out_rows(t, tokens, heads, D, dev, where):
+    """sv_rows of an output of bf16 or fp32, and which."""
+    if t.dtype is not torch.float32:
+        return _rows(t, tokens, heads, D, dev, where), SV_BF16
+    if t.shape != (tokens, heads, D) or not t.is_cuda or (dev is not None and t.get_device() != dev):
+        _bad(where)
+    ts, hs, ds = t.stride()
+    if ds != 1 and D != 1:
+        _bad(where)
+    return _ROWS.pack(t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0), SV_F32
+
+
+def gdn_step(states, slots, q, k, v, g, beta, o, M: int, tape=None, n_replay=None, commit: bool = False, stream=None):
+    """The gated delta rule over M newest rows of each of B sequences: states
+    fp32 [slots, Hv, dv, dk], slots int32 [B] (negative: from zeros, not kept),
+    q and k bf16 [B*M, Hk, dk], v and o [B*M, Hv, dv] (o bf16 or fp32), g (log
+    decay) and beta fp32 [B*M, Hv].  tape: (k, v, g, beta) of the last round,
+    the same number of rows for each sequence, of which the first n_replay[b]
+    (int32 [B]) go into the state first.  commit: the M rows go into it too.
+    M = 0 only commits the tape; q, k, v, g, beta and o may be None then."""
+    w = "gdn_step"
+    dev = None if _gpus == 1 else _device(states, w)
+    B = slots.numel()
+    n, Hv, dv, dk = states.shape if states.dim() == 4 else _bad(w)
+    if (tape is None) != (n_replay is None):
+        _bad(w)
+    Hk = (tape[0] if M == 0 and tape is not None else k).shape[1] if M or tape is not None else 1
+    t = [None] * 4
+    tape_M = 0
+    if tape is not None:
+        tape_M, rest = divmod(tape[0].shape[0], B) if B else (0, 0)
+        if rest or len(tape) != 4:
+            _bad(w)
+        rows = B * tape_M
+        t = [_rows(tape[0], rows, Hk, dk, dev, w), _rows(tape[1], rows, Hv, dv, dev, w),
+             _gates(tape[2], rows, Hv, dev, w), _gates(tape[3], rows, Hv, dev, w)]
+    own, odt = [None] * 6, SV_BF16
+    if M:
+        rows = B * M
+        out, odt = _out_rows(o, rows, Hv, dv, dev, w)
+        own = [_rows(q, rows, Hk, dk, dev, w), _rows(k, rows, Hk, dk, dev, w), _rows(v, rows, Hv, dv, dev, w),
+               _gates(g, rows, Hv, dev, w), _gates(beta, rows, Hv, dev, w), out]
+    status = load().gdn_step(_states(states, dev, w), _vector(slots, torch.int32, B, dev, w), *t,
+                             None if n_replay is None else _vector(n_replay, torch.int32, B, dev, w), tape_M, *own,
+                             odt, B, M, 1 if commit else 0, Hk, Hv, dk, dv, _launch_stream(dev, stream))
+    if status:
+        _check(status, w)
+
+
+def _gates(t, rows, Hv, dev, where):
+    """Address of gates fp32 [rows, Hv], contiguous."""
+    if t.shape != (rows, Hv):
+        _bad(where)
+    return _vector(t, torch.float32, rows * Hv, dev, where)
+
+
+def gdn_chunk_workspace_bytes(B: int, T: int, Hk: int, Hv: int, dk: int, dv: int) -> int:
+    return load().gdn_chunk_workspace_bytes(B, T, Hk, Hv, dk, dv)
+
+
+def gdn_chunk(states, slots, q, k, v, g, beta, o, cu, workspace=None, stream=None):
+    """The gated delta rule over packed chunks of new tokens: sequence b is rows
+    cu[b]..cu[b+1] (int32 [B+1]) of q and k bf16 [T, Hk, dk], v and o bf16
+    [T, Hv, dv], g (log decay) and beta fp32 [T, Hv]; it starts from, and goes
+    back into, place slots[b] (int32 [B]; negative: from zeros, not kept) of
+    the states fp32 [slots, Hv, dv, dk]."""
+    w = "gdn_chunk"
+    T, Hk, dk = q.shape
+    dev = None if _gpus == 1 else _device(q, w)
+    n, Hv, dv, dk_ = states.shape if states.dim() == 4 else _bad(w)
+    B = slots.numel()
+    if dk_ != dk or (workspace is not None and (not workspace.is_cuda or (
+            dev is not None and workspace.get_device() != dev))):
+        _bad(w)
+    status = load().gdn_chunk(_states(states, dev, w), _vector(slots, torch.int32, B, dev, w),
+                              _rows(q, T, Hk, dk, dev, w), _rows(k, T, Hk, dk, dev, w), _rows(v, T, Hv, dv, dev, w),
+                              _gates(g, T, Hv, dev, w), _gates(beta, T, Hv, dev, w), _rows(o, T, Hv, dv, dev, w),
+                              _vector(cu, torch.int32, B + 1, dev, w), B, T, Hk, Hv, dk, dv, _ptr(workspace),
+                              _nbytes(workspace), _launch_stream(dev, stream))
     if status:
         _check(status, w)

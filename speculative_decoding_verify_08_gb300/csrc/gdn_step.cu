@@ -1,0 +1,215 @@
+// gdn_step.cu -- the gated delta rule token by token, for many sequences over
+// a pool of states: one new token each, or the rows of a verify step behind
+// what each accepted of its last one.
+//
+// Per value head (key head h / (Hv/Hk)) the state S is dv x dk, and a token
+// makes   S <- a S + u k^T,  u = b (v - a S k),  a = exp(g),  and reads o = S q.
+//
+// What bounds it: a state is read once and written once (8 * dk * dv bytes a
+// value head) and meets few tokens, so HBM; for one sequence the chain of a
+// token's two dot products.  Rows of S are independent under the rule: eight
+// lanes hold one in registers for the whole call (lane `sub` columns
+// 4*sub + 32*j .. +3, so that the eight read whole 128-byte lines and their
+// shared reads of a key meet no bank twice), a dot product ends in three
+// shuffles, and a block is a few rows of one head.  The state's loads are
+// issued before the tokens are staged (fp32, in shared memory), so both wait
+// for memory together.
+#include "gdn_pool.cuh"
+
+namespace sv {
+namespace gdn {
+namespace {
+
+constexpr int LPR = 8;         // lanes per state row
+constexpr int MAX_STAGE = 32;  // tokens staged at a time
+
+// Sum over the eight lanes of a row.
+__device__ __forceinline__ float over_row(float v) {
+#pragma unroll
+  for (int off = LPR / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+template <int NJ>
+__device__ __forceinline__ float dot_row(const f2 (&row)[2 * NJ], const float *x) {
+  f2 s[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(x + 32 * j);
+    s[0] = fma2(row[2 * j], y.x, s[0]);
+    s[1] = fma2(row[2 * j + 1], y.y, s[1]);
+  }
+  const float2 z = unpack2(add2(s[0], s[1]));
+  return over_row(z.x + z.y);
+}
+
+// Stages n bf16 rows of DK (head `h`, from row `r0` on) as fp32.
+template <int DK>
+__device__ __forceinline__ void stage_rows(float *dst, const sv_rows &src, long long r0, int h, int n) {
+  const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(src.ptr) + (long long)h * src.head_stride;
+  for (int e = threadIdx.x; e < n * (DK / 8); e += blockDim.x) {
+    const int t = e / (DK / 8), c = e % (DK / 8);
+    const uint4 w = *reinterpret_cast<const uint4 *>(p + (r0 + t) * src.token_stride + c * 8);
+    float4 *d = reinterpret_cast<float4 *>(dst + (size_t)e * 8);
+    d[0] = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+    d[1] = make_float4(bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w));
+  }
+}
+
+template <int DK>
+__global__ void __launch_bounds__(256) tokens_kernel(const PoolParams P) {
+  constexpr int NJ = DK / 32;
+  extern __shared__ __align__(16) float sm[];
+  const int rows = blockDim.x / LPR;
+  const int i0 = blockIdx.x * rows, h = blockIdx.y, b = blockIdx.z;
+  const int hk = h / (P.Hv / P.Hk);
+  const int tid = threadIdx.x, r = tid / LPR, sub = tid % LPR, i = i0 + r;
+  const bool live = i < P.dv, report = blockIdx.x == 0 && h == 0 && tid == 0;
+  float *sk = sm, *sq = sk + P.stage * DK, *sv_ = sq + P.stage * DK, *sab = sv_ + P.stage * rows;
+  pdl_wait();
+  const int slot = slot_of(P, b, report);
+  const int2 own = rows_of(P, b, report);
+  int replay = 0;
+  if (P.n_replay) {
+    replay = P.n_replay[b];
+    if (replay < 0 || replay > P.tape_M) {
+      if (report) atomicOr(P.err, ERR_INDEX);
+      replay = imin(imax(replay, 0), P.tape_M);
+    }
+  }
+  const bool kept = slot >= 0 && live;
+  float *srow = P.states.ptr + (slot >= 0 ? slot : 0) * P.states.slot_stride + ((long long)h * P.dv + (live ? i : 0)) * DK + sub * 4;
+  f2 row[2 * NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    ulonglong2 x = make_ulonglong2(0, 0);
+    if (kept) x = *reinterpret_cast<const ulonglong2 *>(srow + 32 * j);
+    row[2 * j] = x.x, row[2 * j + 1] = x.y;
+  }
+  auto keep = [&]() {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (kept) *reinterpret_cast<ulonglong2 *>(srow + 32 * j) = make_ulonglong2(row[2 * j], row[2 * j + 1]);
+  };
+  // the tape's tokens, then the sequence's own
+  for (int part = 0; part < 2; ++part) {
+    const bool mine = part == 1;
+    const int n = mine ? own.y : replay;
+    const long long r0 = mine ? own.x : (long long)b * P.tape_M;
+    const sv_rows &K = mine ? P.k : P.tk, &V = mine ? P.v : P.tv;
+    const float *G = mine ? P.g : P.tg, *Bt = mine ? P.b : P.tb;
+    for (int t0 = 0; t0 < n; t0 += P.stage) {
+      const int m = imin(P.stage, n - t0);
+      if (part + t0 > 0) __syncthreads();  // what was staged has been read
+      stage_rows<DK>(sk, K, r0 + t0, hk, m);
+      if (mine) stage_rows<DK>(sq, P.q, r0 + t0, hk, m);
+      for (int e = tid; e < m * rows; e += blockDim.x) {
+        const int t = e / rows, x = e % rows;
+        sv_[e] = i0 + x < P.dv ? __bfloat162float(static_cast<const __nv_bfloat16 *>(
+                                     V.ptr)[(r0 + t0 + t) * V.token_stride + h * V.head_stride + i0 + x])
+                               : 0.f;
+      }
+      for (int t = tid; t < m; t += blockDim.x) {
+        sab[2 * t] = expf(G[(r0 + t0 + t) * P.Hv + h]);
+        sab[2 * t + 1] = Bt[(r0 + t0 + t) * P.Hv + h];
+      }
+      __syncthreads();
+      for (int t = 0; t < m; ++t) {
+        const float *kk = sk + t * DK + sub * 4;
+        const float a = sab[2 * t];
+        const float u = sab[2 * t + 1] * (sv_[t * rows + r] - a * dot_row<NJ>(row, kk));
+        const f2 a2 = pack2(a, a), u2 = pack2(u, u);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(kk + 32 * j);
+          row[2 * j] = fma2(a2, row[2 * j], mul2(u2, y.x));
+          row[2 * j + 1] = fma2(a2, row[2 * j + 1], mul2(u2, y.y));
+        }
+        if (mine) {
+          const float ov = dot_row<NJ>(row, sq + t * DK + sub * 4);
+          if (sub == 0 && live) {
+            const long long at = (r0 + t0 + t) * P.o.token_stride + h * P.o.head_stride + i;
+            if (P.o_f32)
+              static_cast<float *>(P.o.ptr)[at] = ov;
+            else
+              static_cast<__nv_bfloat16 *>(P.o.ptr)[at] = __float2bfloat16_rn(ov);
+          }
+        }
+      }
+    }
+    // (a state that no token has changed is not written)
+    if (mine ? P.commit && own.y + replay > 0 : !P.commit && replay > 0) keep();
+  }
+}
+
+template <int DK>
+sv_status run_tokens(PoolParams &P, cudaStream_t s) {
+  // Blocks of eight rows while that leaves each SM few of them (one sequence of
+  // 48 heads: 768), of 32 beyond, where what a block stages is shared by more rows.
+  const long long small = (long long)P.B * P.Hv * ((P.dv + 7) / 8);
+  const int sms = device_sm_count();
+  if (sms <= 0) return SV_ERR_CUDA;
+  const int threads = small > 16LL * sms ? 256 : 64, rows = threads / LPR;
+  const size_t smem = (size_t)P.stage * (2 * DK + rows + 2) * 4;
+  return from_cuda(launch_early(tokens_kernel<DK>, dim3((P.dv + rows - 1) / rows, P.Hv, P.B), dim3(threads), smem, s, P));
+}
+
+}  // namespace
+
+sv_status launch_tokens(PoolParams &P, int dk, cudaStream_t s) {
+  const int most = P.cu ? P.T : imax(P.M, P.tape_M);
+  P.stage = imax(1, imin(most, MAX_STAGE));
+  switch (dk) {
+    case 64: return run_tokens<64>(P, s);
+    case 128: return run_tokens<128>(P, s);
+    default: return run_tokens<256>(P, s);
+  }
+}
+
+}  // namespace gdn
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+sv_status gdn_step(const sv_states *states, const int32_t *slots, const sv_rows *tape_k, const sv_rows *tape_v,
+                   const float *tape_g, const float *tape_beta, const int32_t *n_replay, int tape_M, const sv_rows *q,
+                   const sv_rows *k, const sv_rows *v, const float *g, const float *beta, const sv_rows *o,
+                   sv_dtype o_dtype, int B, int M, int commit, int Hk, int Hv, int dk, int dv, sv_stream_t stream) {
+  if (B < 0 || M < 0 || tape_M < 0 || Hk < 1 || Hv < 1 || Hv % Hk != 0 || dk < 1 || dv < 1) return SV_ERR_INVALID_ARG;
+  if (o_dtype != SV_BF16 && o_dtype != SV_F32) return SV_ERR_INVALID_ARG;
+  if (dk != 64 && dk != 128 && dk != 256) return SV_ERR_UNSUPPORTED;
+  if (M > 64 || tape_M > 64 || Hv > 65535 || B > gdn::MAX_POOL_B || dv > 65536) return SV_ERR_UNSUPPORTED;
+  if (sv_status e = gdn::check_states(states, Hv, dk, dv)) return e;
+  const bool tape = n_replay != nullptr && tape_M > 0, rows = M > 0;
+  if (B > 0 && (!slots || !paged::aligned(slots, 4) || !paged::aligned(n_replay, 4))) return SV_ERR_INVALID_ARG;
+  if (rows) {
+    for (const sv_rows *r : {q, k, v, o})
+      if (!paged::good_rows(r, (long long)B * M)) return SV_ERR_INVALID_ARG;
+    if (B > 0 && (!g || !beta || !paged::aligned(g, 4) || !paged::aligned(beta, 4))) return SV_ERR_INVALID_ARG;
+  }
+  if (tape) {
+    for (const sv_rows *r : {tape_k, tape_v})
+      if (!paged::good_rows(r, (long long)B * tape_M)) return SV_ERR_INVALID_ARG;
+    if (B > 0 && (!tape_g || !tape_beta || !paged::aligned(tape_g, 4) || !paged::aligned(tape_beta, 4)))
+      return SV_ERR_INVALID_ARG;
+  }
+  if (B == 0 || (!rows && !tape)) return SV_OK;
+  gdn::PoolParams P{};
+  P.states = *states;
+  P.slots = slots;
+  if (tape) {
+    P.tk = *tape_k, P.tv = *tape_v, P.tg = tape_g, P.tb = tape_beta;
+    P.n_replay = n_replay, P.tape_M = tape_M;
+  }
+  if (rows) P.q = *q, P.k = *k, P.v = *v, P.o = *o, P.g = g, P.b = beta;
+  P.err = device_error_word();
+  if (!P.err) return SV_ERR_CUDA;
+  P.B = B, P.M = M, P.T = B * M, P.Hk = Hk, P.Hv = Hv, P.dv = dv;
+  P.commit = commit ? 1 : 0;
+  P.o_f32 = o_dtype == SV_F32 ? 1 : 0;
+  return gdn::launch_tokens(P, dk, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
