@@ -10,19 +10,21 @@
 // With T = (I + A)^-1 these are products, all of them on the tensor cores.
 //
 // What bounds it: blocks of one sequence follow one another, and in each a chain
-// of three products and the register work between them; sequences, heads and 128
-// rows of a state each have a CTA.
-//  * Everything is held transposed, a row of the state (and of U, O) per lane of
-//    tensor memory: X = S K^T, then R = b (v - e^G X) becomes U = R T^T, U becomes
-//    S' = U~ K, and each result is read by the threads that hold its rows and written
-//    back as the next product's first operand, in tensor memory.  Two threads share
-//    a row; S itself stays in their registers, in fp32.
-//  * Eight warps run that chain; four prepare the next block meanwhile: keys and
-//    queries to fp16, K K^T and Q K^T on the tensor cores, decays, the inverse T.
+// of three products and the register work between them.  Hence two kernels:
+//  * prepare_kernel does what no state enters, for all blocks side by side: keys and
+//    queries to fp16, K K^T and Q K^T (once for the value heads of a key head),
+//    decays, T and P, laid out in the workspace the way the chain's copies take them.
+//  * chain_kernel walks the blocks of one sequence, value head and 128 rows of the
+//    state.  Everything is held transposed, a row of the state (and of U, O) per lane
+//    of tensor memory: X = S K^T, R = b (v - e^G X), U = R T^T, S' = U~ K; each result is
+//    read by the threads that hold its rows and written back over itself as the
+//    next product's first operand.  Four threads share a row; S stays in their
+//    registers, in fp32.  One warp issues the products, one the copies (three
+//    blocks ahead at most).
 //  * Products take fp16 operands and fp32 sums.  S, R, U and T are fp32 values held
-//    as two fp16 parts (x = hi + lo, 2^-22 of x), so that a state stays an fp32 one; what only an
-//    output sees (S and U there, P and the decayed queries) is one part, 2^-11 beside
-//    the output's own 2^-8.  (bf16 parts would need three for that, half as many
+//    as two fp16 parts (x = hi + lo, 2^-22 of x), so that a state stays an fp32 one; what
+//    only an output sees (S and U there, and P) is one part, 2^-11 beside the
+//    output's own 2^-8.  (bf16 parts would need three for that, half as many
 //    products again.)
 //  * fp16 reaches from 2^-24 to 2^16, so everything is scaled by powers of two, exactly:
 //    a key to a largest element in [2^-4, 2^-3) (k = 2^e k': b' = 4^e b, v' = 2^-e v,
@@ -33,58 +35,42 @@
 //    below 2^16, and the parts are off by 2^-27 of the larger of the two at most.
 //  * The inverse: four 16 x 16 blocks by forward substitution, then joined twice by
 //    -T22 (A21 T11), in fp32 on the CUDA cores, which is as stable as the substitution.
-//  * G is summed in 64 bits and its differences are taken of two fp32 parts: a gate that
-//    closes (g = -1000) leaves the decays behind it exact.
+//  * G is summed in two fp32 parts and so are its differences: a gate that closes
+//    (g = -1000) leaves the decays behind it exact.
 #include "gdn_pool.cuh"
 #include "tcgen05.cuh"
 
 namespace sv {
+namespace attn {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // attn.cu
+}
 namespace gdn {
 namespace {
 
 constexpr int C = 64;        // tokens of a block
 constexpr int ROWS = 128;    // rows of the state a CTA holds (TMEM lanes)
-constexpr int CHAIN = 256, PREP = 128, THREADS = CHAIN + PREP;
-constexpr int AS = 68;       // row stride of the inverse's fp32 matrices
+constexpr int AS = 68;       // row stride of the inverse's fp32 matrix
 constexpr int MAX_SORTED = 128;
 constexpr float G_LEAST = -10000.f;  // e^g is 0 long before
-constexpr float Q_GAIN = 1024.f;     // queries and P are taken so much larger: e^G down to 2^-24 keeps its bits
+constexpr float P_GAIN = 1024.f;     // P is taken so much larger: decays down to 2^-24 keep their bits
 
-// One block's scalars.
+// A block's scalars for one value head.
 struct Scalars {
-  float bv[C], bx[C], en[C], os[C];  // of v in R, of X in R, of U in U~, of the output
-  float gc;                          // decay over the block
-  float pad[3];
+  float bv[C], bx[C], en[C], os1[C], os2[C];  // of v and of X (negative) in R, of U in U~, of the output's two products
+  float gc;                                   // decay over the block
+  float pad[63];
 };
-
+constexpr int PART = C * 128;  // bytes of one part of T, and of P
+constexpr int HEAD_BYTES = 3 * PART + (int)sizeof(Scalars);  // T (hi, lo), P, scalars
+static_assert(sizeof(Scalars) == 1536 && HEAD_BYTES % 1024 == 512, "copies");
 template <int DK>
-struct L {
-  static constexpr int G = DK / 64;                  // 64-column groups
-  static constexpr int KQ_BYTES = G * 128 * 128;     // K' in rows 0..63, Q' in 64..127
-  static constexpr int RAW_BYTES = 128 * DK * 2;
-  static constexpr int V_BYTES = C * ROWS * 2;
-  static constexpr int T_BYTES = C * 128;            // one part; P too
-  static constexpr int KQ = 1024;                    // [2]
-  static constexpr int T = KQ + 2 * KQ_BYTES;        // [2][hi, lo]
-  static constexpr int P = T + 4 * T_BYTES;          // [2]
-  static constexpr int V = P + 2 * T_BYTES;          // [3]
-  static constexpr int RAW = V + 3 * V_BYTES;
-  static constexpr int A = RAW + RAW_BYTES;          // fp32 [64][AS], inverted in place
-  static constexpr int SC = A + C * AS * 4;          // Scalars[2]
-  static constexpr int GH = SC + 2 * (int)sizeof(Scalars);  // G in units of log 2, two parts [2][64]
-  static constexpr int EXP = GH + 2 * C * 4;         // exponent of a key's or query's scale [128]
-  static constexpr int XCHG = EXP + 128 * 4;         // [2][2][ROWS]
-  static constexpr int BYTES = XCHG + 4 * ROWS * 4;
-  static_assert(BYTES <= 227 * 1024, "shared memory");
-  // tensor memory: S in two parts; X, then U beside it, then S' over both; R in two
-  // parts, then U~ in two and U in one; O; K K^T over Q K^T
-  static constexpr uint32_t SH = 0, SL = DK / 2, X = 128, U = 192, D = 128, R = 256, O = 352, KK = 416;
-};
+__host__ __device__ constexpr int key_bytes() { return C * DK * 2; }  // a block's keys (and queries) of one key head
 
 struct ChunkParams {
   PoolParams p;
-  int blocks;  // of ROWS rows a head
-  int stall;   // test aid: the first block's keys never arrive
+  uint8_t *keys, *heads;  // [blocks][Hk][2][key_bytes], [blocks][Hv][HEAD_BYTES]
+  int row_blocks;         // of ROWS rows a value head
+  int stall;              // test aid: the first block never arrives
 };
 
 __device__ __forceinline__ uint32_t swz(int row, int c16) {  // 16-byte piece c16 of a 128-byte row
@@ -101,52 +87,380 @@ __device__ __forceinline__ void split2(f2 x, uint32_t &hi, uint32_t &lo) {
 
 __device__ __forceinline__ float pow2_field(int e) { return __int_as_float(e << 23); }  // 2^(e - 127)
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+// Place of a sequence's first block in the workspace: sequences do not share
+// places, and none is past T / C + B.
+__device__ __forceinline__ int first_block(const PoolParams &P, int b, int row0) { return row0 / C + b; }
+
+// x + y of two-part values, the first part the value rounded.
+__device__ __forceinline__ float2 add_parts(float2 x, float2 y) {
+  const float s = x.x + y.x, t = s - x.x;
+  const float e = ((x.x - (s - t)) + (y.x - t)) + (x.y + y.y);
+  const float h = s + e;
+  return make_float2(h, e - (h - s));
+}
+
+// ------------------------------------------------------------------ prepare --
+template <int DK>
+struct PL {
+  static constexpr int KQ = 0;                        // [DK/64][128 rows][128 B]: keys in rows 0..63, queries behind
+  static constexpr int A = KQ + 128 * DK * 2;         // fp32 [64][AS], inverted in place
+  static constexpr int GH = A + C * AS * 4;           // G in units of log 2, two parts [2][64]
+  static constexpr int EX = GH + 2 * C * 4;           // exponents of the largest elements [128]
+  static constexpr int BAR = EX + 128 * 4;
+  static constexpr int BYTES = BAR + 64;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(128, 4) prepare_kernel(const __grid_constant__ ChunkParams CP) {
+  using Y = PL<DK>;
+  const PoolParams &P = CP.p;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(P.err, ERR_TIMEOUT);
+    return;
+  }
+  float *A = reinterpret_cast<float *>(smem + Y::A);
+  float *gh = reinterpret_cast<float *>(smem + Y::GH), *gl = gh + C;
+  int *ex = reinterpret_cast<int *>(smem + Y::EX);
+  uint64_t *done = reinterpret_cast<uint64_t *>(smem + Y::BAR);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  const int pt = threadIdx.x, pw = pt >> 5, lane = pt & 31;
+  pdl_wait();
+  // ---- the block: sequence and first row ----
+  const int w = blockIdx.x, hk = blockIdx.y;
+  int lo = 0, hi = P.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first_block(P, mid, P.cu[mid]) <= w) lo = mid; else hi = mid - 1;
+  }
+  const int2 own = rows_of(P, lo, false);
+  const int c = w - first_block(P, lo, own.x);
+  if (c < 0 || c * C >= own.y) return;
+  const long long r0 = own.x + (long long)c * C;
+  const int m = imin(C, own.y - c * C);
+  if (pt == 0) {
+    mbar_init(done, 1);
+    fence_barrier_init();
+  }
+  if (pw == 0) {
+    tc::tmem_alloc(tmem_slot, 64u);
+    tc::tmem_relinquish();
+  }
+  // ---- keys and queries to fp16: eight threads a row ----
+  {
+    constexpr int PR = DK / 64;  // 16-byte pieces a thread
+    const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(P.k.ptr) + (long long)hk * P.k.head_stride;
+    const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(P.q.ptr) + (long long)hk * P.q.head_stride;
+    uint8_t *image = CP.keys + ((size_t)w * P.Hk + hk) * 2 * key_bytes<DK>();
+    const int s8 = pt & 7, t0 = pt >> 3;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const __nv_bfloat16 *src = half ? qp : kp;
+      const long long stride = half ? P.q.token_stride : P.k.token_stride;
+      uint4 v[4][PR];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int t = t0 + 16 * y;
+#pragma unroll
+        for (int z = 0; z < PR; ++z)
+          v[y][z] = t < m ? *reinterpret_cast<const uint4 *>(src + (r0 + t) * stride + (s8 + 8 * z) * 8) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int t = t0 + 16 * y;
+        uint32_t mx = 0;
+#pragma unroll
+        for (int z = 0; z < PR; ++z)  // (of finite values the larger has the larger bits)
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[y][z].x & 0x7fff7fffu, v[y][z].y & 0x7fff7fffu),
+                                     __vmaxu2(v[y][z].z & 0x7fff7fffu, v[y][z].w & 0x7fff7fffu)));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const int E = (int)(max(mx & 0xffffu, mx >> 16) >> 7);
+        const float f = pow2_field(imax(250 - E, 1));
+        const f2 f2x = pack2(f, f);
+        auto two = [&](uint32_t x) {
+          const float2 p = unpack2(mul2(pack2(bf16lo(x), bf16hi(x)), f2x));
+          return pack_f16x2(p.x, p.y);
+        };
+#pragma unroll
+        for (int z = 0; z < PR; ++z) {
+          const uint4 d = make_uint4(two(v[y][z].x), two(v[y][z].y), two(v[y][z].z), two(v[y][z].w));
+          *reinterpret_cast<uint4 *>(smem + Y::KQ + z * 128 * 128 + swz(half * C + t, s8)) = d;
+          *reinterpret_cast<uint4 *>(image + half * key_bytes<DK>() + z * C * 128 + swz(t, s8)) = d;
+        }
+        if (s8 == 0) ex[half * C + t] = E;
+      }
+    }
+  }
+  fence_proxy_async();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tb = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  // ---- K K^T over Q K^T ----
+  if (pw == 0 && tc::elect_one()) {
+    const uint64_t da = tc::smem_desc_sw128(smem_u32(smem + Y::KQ), 16, 1024);
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      const uint64_t d = da + ((ks >> 2) * 128 * 128 + (ks & 3) * 32) / 16;
+      tc::mma_bf16(tb, d, d, tc::idesc_f16_f32(128, C, false), ks > 0);
+    }
+    tc::commit(done);
+  }
+  __syncwarp();
+  bool ok = mbar_wait(done, 0, P.err);
+  ok = __all_sync(0xffffffffu, ok);
+  tc::fence_after_sync();
+  uint32_t raw[2][32];
+  if (ok) {
+    tc::ld32(tb + ((uint32_t)(pw * 32) << 16), raw[0]);
+    tc::ld32(tb + 32 + ((uint32_t)(pw * 32) << 16), raw[1]);
+    tc::wait_ld();
+  }
+  const bool isP = pw >= 2;
+  const int i = (pw & 1) * 32 + lane;  // this thread's row of A, or of P
+  const float e_i = pow2_field(imin(ex[i] + 4, 254));  // 2^e of its key
+  const int group = P.Hv / P.Hk;
+  for (int e = 0; e < group; ++e) {
+    const int h = hk * group + e;
+    uint8_t *out = CP.heads + ((size_t)w * P.Hv + h) * HEAD_BYTES;
+    float be = 0.f;
+    if (i < m) be = P.b[(r0 + i) * P.Hv + h];
+    if (e > 0) __syncthreads();  // A and G of the head before have been read
+    if (pw == 0) {  // running sums of the gates, in units of log 2, two tokens a lane
+      auto gate = [&](int t) {
+        float g = t < m ? P.g[(r0 + t) * P.Hv + h] : 0.f;
+        g = g < G_LEAST ? G_LEAST : g;
+        // log2(e) in two parts
+        const float x = g * 1.44269502f;
+        return make_float2(x, fmaf(g, 1.44269502f, -x) + g * 1.92596303e-8f);
+      };
+      const float2 g0 = gate(2 * lane), g1 = gate(2 * lane + 1);
+      const float2 pair = add_parts(g0, g1);
+      float2 x = pair;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float2 y = make_float2(__shfl_up_sync(0xffffffffu, x.x, o), __shfl_up_sync(0xffffffffu, x.y, o));
+        if (lane >= o) x = add_parts(x, y);
+      }
+      const float2 before = make_float2(__shfl_up_sync(0xffffffffu, x.x, 1), __shfl_up_sync(0xffffffffu, x.y, 1));
+      const float2 x0 = lane > 0 ? add_parts(before, g0) : g0;
+      *reinterpret_cast<float2 *>(gh + 2 * lane) = make_float2(x0.x, x.x);
+      *reinterpret_cast<float2 *>(gl + 2 * lane) = make_float2(x0.y, x.y);
+    }
+    __syncthreads();
+    Scalars *S = reinterpret_cast<Scalars *>(out + 3 * PART);
+    const float hi_i = gh[i], lo_i = gl[i], ga = ex2_approx(hi_i + lo_i);
+    if (!isP) {
+      const float bs = be * e_i;
+      S->bv[i] = bs;
+      S->bx[i] = -(bs * e_i * ga);
+      S->en[i] = ex2_approx((gh[C - 1] - hi_i) + (gl[C - 1] - lo_i));
+    } else {
+      const float os = pow2_field(imin(ex[C + i] + 4, 254));
+      S->os1[i] = os * ga;
+      S->os2[i] = os * (1.f / P_GAIN);
+      if (i == C - 1) S->gc = ga;
+    }
+    // ---- A (rows of the first two warps) and P ----
+    {
+      const float rf = isP ? P_GAIN : be * e_i * e_i;
+      const f2 rowf = pack2(rf, rf), hi2 = pack2(hi_i, hi_i), lo2 = pack2(lo_i, lo_i), neg = pack2(-1.f, -1.f);
+      const int last = isP ? i : i - 1;  // columns up to it count
+#pragma unroll
+      for (int c0 = 0; c0 < 2; ++c0) {
+        const bool any = c0 == 0 || (pw & 1);  // columns 32.. of rows 0..31 are zero
+#pragma unroll
+        for (int x = 0; x < 32; x += 8) {
+          const int j = c0 * 32 + x;
+          f2 y[4] = {0, 0, 0, 0};
+          if (any) {
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const f2 hj = *reinterpret_cast<const f2 *>(gh + j + 2 * z), lj = *reinterpret_cast<const f2 *>(gl + j + 2 * z);
+              const float2 d = unpack2(add2(fma2(hj, neg, hi2), fma2(lj, neg, lo2)));
+              const f2 kk = pack2(__uint_as_float(raw[c0][x + 2 * z]), __uint_as_float(raw[c0][x + 2 * z + 1]));
+              const float2 t = unpack2(mul2(mul2(kk, rowf), pack2(ex2_approx(d.x), ex2_approx(d.y))));
+              y[z] = pack2(j + 2 * z <= last ? t.x : 0.f, j + 2 * z + 1 <= last ? t.y : 0.f);
+            }
+          }
+          if (isP) {
+            auto h2 = [](f2 v) {
+              const float2 p = unpack2(v);
+              return pack_f16x2(p.x, p.y);
+            };
+            *reinterpret_cast<uint4 *>(out + 2 * PART + swz(i, j >> 3)) = make_uint4(h2(y[0]), h2(y[1]), h2(y[2]), h2(y[3]));
+          } else {
+            *reinterpret_cast<ulonglong2 *>(A + i * AS + j) = make_ulonglong2(y[0], y[1]);
+            *reinterpret_cast<ulonglong2 *>(A + i * AS + j + 4) = make_ulonglong2(y[2], y[3]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    // ---- T = (I + A)^-1 in place: a 16 x 16 block a warp, a column a lane ----
+    {
+      const int o = pw * 16;
+      float x[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        float s0 = r == lane ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < r; j += 4) {
+          const float4 a = *reinterpret_cast<const float4 *>(A + (o + r) * AS + o + j);
+          s0 = fmaf(-a.x, x[j], s0);
+          if (j + 1 < r) s1 = fmaf(-a.y, x[j + 1], s1);
+          if (j + 2 < r) s0 = fmaf(-a.z, x[j + 2], s0);
+          if (j + 3 < r) s1 = fmaf(-a.w, x[j + 3], s1);
+        }
+        x[r] = s0 + s1;
+      }
+      __syncwarp();
+      if (lane < 16) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) A[(o + r) * AS + o + lane] = x[r];
+      }
+    }
+    __syncthreads();
+    // joined: T21 = -T22 (A21 T11), 16 rows and columns of two pairs, then 32 of one
+    {
+      // one row, four columns a thread: pair pt / 64
+      const int o = (pt >> 6) * 32, r = o + 16 + ((pt & 63) >> 2), j = o + (pt & 3) * 4;
+#pragma unroll
+      for (int pass = 0; pass < 2; ++pass) {
+        f2 w0 = 0, w1 = 0;
+        const int k0 = o + 16 * pass;
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+          const float4 a = *reinterpret_cast<const float4 *>(A + r * AS + k0 + k);
+          const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const ulonglong2 t = *reinterpret_cast<const ulonglong2 *>(A + (k0 + k + z) * AS + j);
+            const float x = pass ? -av[z] : av[z];
+            w0 = fma2(pack2(x, x), t.x, w0), w1 = fma2(pack2(x, x), t.y, w1);
+          }
+        }
+        __syncthreads();
+        *reinterpret_cast<ulonglong2 *>(A + r * AS + j) = make_ulonglong2(w0, w1);
+        __syncthreads();
+      }
+    }
+    {
+      const int r = 32 + (pt >> 3) * 2, j = (pt & 7) * 4;  // two rows, four columns
+#pragma unroll
+      for (int pass = 0; pass < 2; ++pass) {
+        f2 s[2][2] = {{0, 0}, {0, 0}};
+        const int k0 = 32 * pass;
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          const float4 a = *reinterpret_cast<const float4 *>(A + r * AS + k0 + k), d = *reinterpret_cast<const float4 *>(A + (r + 1) * AS + k0 + k);
+          const float av[4] = {a.x, a.y, a.z, a.w}, dv_[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const ulonglong2 t = *reinterpret_cast<const ulonglong2 *>(A + (k0 + k + z) * AS + j);
+            const float p = pass ? -av[z] : av[z], q = pass ? -dv_[z] : dv_[z];
+            s[0][0] = fma2(pack2(p, p), t.x, s[0][0]), s[0][1] = fma2(pack2(p, p), t.y, s[0][1]);
+            s[1][0] = fma2(pack2(q, q), t.x, s[1][0]), s[1][1] = fma2(pack2(q, q), t.y, s[1][1]);
+          }
+        }
+        __syncthreads();
+        *reinterpret_cast<ulonglong2 *>(A + r * AS + j) = make_ulonglong2(s[0][0], s[0][1]);
+        *reinterpret_cast<ulonglong2 *>(A + (r + 1) * AS + j) = make_ulonglong2(s[1][0], s[1][1]);
+        __syncthreads();
+      }
+    }
+    // ---- T in two parts: pieces of eight, a row's eight pieces side by side ----
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int r = (pt >> 3) + 16 * x, p = pt & 7;
+      const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(A + r * AS + p * 8), d = *reinterpret_cast<const ulonglong2 *>(A + r * AS + p * 8 + 4);
+      uint4 th, tl;
+      split2(a.x, th.x, tl.x);
+      split2(a.y, th.y, tl.y);
+      split2(d.x, th.z, tl.z);
+      split2(d.y, th.w, tl.w);
+      *reinterpret_cast<uint4 *>(out + swz(r, p)) = th;
+      *reinterpret_cast<uint4 *>(out + PART + swz(r, p)) = tl;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (pw == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tb, 64u);
+  }
+}
+
+// -------------------------------------------------------------------- chain --
+constexpr int CHAIN_WARPS = 16, CHAIN_THREADS = (CHAIN_WARPS + 4) * 32, STAGES = 3;
+
+template <int DK>
+struct CL {
+  static constexpr int K = 0, Q = key_bytes<DK>(), T = 2 * key_bytes<DK>(), P = T + 2 * PART, V = P + PART;
+  static constexpr int S = V + C * ROWS * 2;            // scalars
+  static constexpr int STAGE = S + 2048;                // (stages 1024-byte aligned)
+  static constexpr int XCHG = 1024;                     // [2][4][ROWS]
+  static constexpr int RING = XCHG + 8 * ROWS * 4;
+  static constexpr int BYTES = RING + STAGES * STAGE - 512;
+  static_assert(RING % 1024 == 0 && STAGE % 1024 == 0 && BYTES <= 227 * 1024, "shared memory");
+  // tensor memory: S in two parts; X, then R over it (16 columns a k-step: hi, lo), then U
+  // in one part; U, then U~ over it; S'; S Q^T; P U
+  static constexpr uint32_t SH = 0, SL = DK / 2, X = 128, U = 192, D = 256, O1 = 384, O2 = 448;
+};
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tensor_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
 }
 
 template <int DK>
-__global__ void __launch_bounds__(THREADS, 1) chunk_kernel(const ChunkParams CP) {
-  using Y = L<DK>;
+__global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_constant__ CUtensorMap mapV, const __grid_constant__ ChunkParams CP) {
+  using Y = CL<DK>;
   const PoolParams &P = CP.p;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // swizzled tiles need it; so it is in a kernel without static shared memory
     if (threadIdx.x == 0) atomicOr(P.err, ERR_TIMEOUT);
     return;
   }
-  uint64_t *kq_full = reinterpret_cast<uint64_t *>(smem);  // [2] keys, queries and values of a block
-  uint64_t *tp_full = kq_full + 2;                         // [2] T, P, decayed queries, scalars
-  uint64_t *free_ = tp_full + 2;                           // [2] all of a block's read
-  uint64_t *x_done = free_ + 2, *u_done = x_done + 1, *d_done = u_done + 1, *o_done = d_done + 1;
-  uint64_t *k_done = o_done + 1, *idle = k_done + 1;       // idle [2]
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(idle + 2);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem);     // [STAGES]
+  uint64_t *empty = full + STAGES;                         // [STAGES]
+  uint64_t *s_ready = empty + STAGES;                      // [2] even and odd k-steps of S in place
+  uint64_t *x_done = s_ready + 2, *r_ready = x_done + 1, *u_done = r_ready + 1, *ut_ready = u_done + 1;
+  uint64_t *d_done = ut_ready + 1, *o_done = d_done + 1, *o_free = o_done + 1, *idle = o_free + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(idle + 1);
   int *pick = reinterpret_cast<int *>(tmem_slot + 1);
-  Scalars *sc_all = reinterpret_cast<Scalars *>(smem + Y::SC);
+  uint8_t *ring = smem + Y::RING;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&kq_full[i], 4 + (i == 0 ? CP.stall : 0));
-      mbar_init(&tp_full[i], 4);
-      mbar_init(&free_[i], 9);
-      mbar_init(&idle[i], 1);
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&full[i], 1 + (i == 0 ? CP.stall : 0));
+      mbar_init(&empty[i], CHAIN_WARPS + 1);
     }
-    for (uint64_t *b : {x_done, u_done, d_done, o_done, k_done}) mbar_init(b, 1);
+    for (uint64_t *b : {s_ready, s_ready + 1, r_ready, ut_ready, o_free}) mbar_init(b, CHAIN_WARPS);
+    for (uint64_t *b : {x_done, u_done, d_done, o_done, idle}) mbar_init(b, 1);
     fence_barrier_init();
     *pick = 0;
   }
-  if (warp == 8) {
+  if (warp == CHAIN_WARPS) {
     tc::tmem_alloc(tmem_slot, 512u);
     tc::tmem_relinquish();
   }
   pdl_wait();
   // ---- the item: longest sequences first ----
-  const int per = P.Hv * CP.blocks;
+  const int per = P.Hv * CP.row_blocks;
   int b = blockIdx.x / per;
-  const int rest = blockIdx.x - b * per, h = rest / CP.blocks, i0 = (rest - h * CP.blocks) * ROWS;
-  __syncthreads();
+  const int rest = blockIdx.x - b * per, h = rest / CP.row_blocks, i0 = (rest - h * CP.row_blocks) * ROWS;
   if (P.B > 1 && P.B <= MAX_SORTED) {
-    int *len = reinterpret_cast<int *>(smem + Y::GH);  // (GH and EXP are 256 ints)
+    int *len = reinterpret_cast<int *>(smem + Y::XCHG);
     if (tid < P.B) len[tid] = rows_of(P, tid, false).y;
     __syncthreads();
     if (tid < P.B) {
@@ -166,329 +480,131 @@ __global__ void __launch_bounds__(THREADS, 1) chunk_kernel(const ChunkParams CP)
   const int2 own = rows_of(P, b, report);
   const int slot = slot_of(P, b, report);
   const int n = (own.y + C - 1) / C;  // blocks
-  const int hk = h / (P.Hv / P.Hk);
+  bool ok = true;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (ok) ok = spin_wait(bar, parity, P.err);
+    ok = __all_sync(0xffffffffu, ok);
+  };
 
-  if (warp >= 8) {
-    // ------------------------------------------------ the next block --
-    // 384 threads start with 168 registers each: 256 * 184 + 128 * 136 is the same total
-    setmaxnreg_dec<136>();
-    const int pt = tid - CHAIN, pw = warp - 8;
-    const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(P.k.ptr) + (long long)hk * P.k.head_stride;
-    const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(P.q.ptr) + (long long)hk * P.q.head_stride;
-    const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(P.v.ptr) + (long long)h * P.v.head_stride + i0;
-    const int live = imin(ROWS, P.dv - i0);  // rows of the state that exist
-    float *A = reinterpret_cast<float *>(smem + Y::A);
-    float *gh = reinterpret_cast<float *>(smem + Y::GH), *gl = gh + C;
-    int *ex = reinterpret_cast<int *>(smem + Y::EXP);
-    const bool issuer = pw == 0 && tc::elect_one();
-    const uint32_t lane_off = (uint32_t)(pw * 32) << 16;
-    auto bar = [&]() { named_barrier(1, PREP); };
-    // Copies of block c: keys and queries as they are, values to their place.
-    auto fetch = [&](int c) {
-      const int m = imin(C, own.y - c * C);
-      const long long r0 = own.x + (long long)c * C;
-      const uint32_t raw = smem_u32(smem + Y::RAW), vs = smem_u32(smem + Y::V + (c % 3) * Y::V_BYTES);
-      constexpr int PC = DK / 8;
-#pragma unroll 4
-      for (int e = pt; e < 128 * PC; e += PREP) {
-        const int r = e / PC, x = e % PC, t = r & 63;
-        const bool in = t < m;
-        const __nv_bfloat16 *src = r < C ? kp + (r0 + (in ? t : 0)) * P.k.token_stride : qp + (r0 + (in ? t : 0)) * P.q.token_stride;
-        cp_async16(raw + r * DK * 2 + ((x ^ (r & 7)) << 4), src + x * 8, in);
-      }
-#pragma unroll 4
-      for (int e = pt; e < C * (ROWS / 8); e += PREP) {
-        const int t = e / (ROWS / 8), x = e % (ROWS / 8);
-        const __nv_bfloat16 *src = vp + (r0 + (t < m ? t : 0)) * P.v.token_stride;
-        const uint32_t at = vs + t * ROWS * 2 + x * 16;
-        if (x * 8 + 8 <= live || x * 8 >= live || t >= m) {
-          const bool in = t < m && x * 8 < live;
-          cp_async16(at, in ? src + x * 8 : src, in);
-        } else {  // the last columns, fewer than eight: nothing behind them is read
-          __nv_bfloat16 *d = reinterpret_cast<__nv_bfloat16 *>(smem + Y::V + (c % 3) * Y::V_BYTES) + t * ROWS + x * 8;
-          for (int y = 0; y < 8; ++y) d[y] = x * 8 + y < live ? src[x * 8 + y] : __float2bfloat16_rn(0.f);
+  if (warp >= CHAIN_WARPS) {
+    // 640 threads start with 96 registers each: 512 * 112 + 128 * 32 is the same total
+    setmaxnreg_dec<32>();
+    if (warp == CHAIN_WARPS) {
+      // ---------------------------------------------------------- copies --
+      if (lane == 0) {
+        const int hk = h / (P.Hv / P.Hk), w0 = first_block(P, b, own.x);
+        int c = 0;
+        for (; c < n && ok; ++c) {
+          const int st = c % STAGES;
+          if (c >= STAGES) ok = mbar_wait(&empty[st], (c / STAGES - 1) & 1, P.err);
+          if (!ok) break;
+          uint8_t *at = ring + st * Y::STAGE;
+          mbar_arrive_expect_tx(&full[st], 2 * key_bytes<DK>() + HEAD_BYTES + C * ROWS * 2);
+          bulk_load(at + Y::K, CP.keys + ((size_t)(w0 + c) * P.Hk + hk) * 2 * key_bytes<DK>(), 2 * key_bytes<DK>(), &full[st]);
+          const uint8_t *src = CP.heads + ((size_t)(w0 + c) * P.Hv + h) * HEAD_BYTES;
+          bulk_load(at + Y::T, src, 3 * PART, &full[st]);
+          bulk_load(at + Y::S, src + 3 * PART, sizeof(Scalars), &full[st]);
+          tensor_load_3d(at + Y::V, &mapV, i0, h, own.x + c * C, &full[st]);
         }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    bool ok = true;
-    if (n > 0) fetch(0);
-    for (int c = 0; c < n; ++c) {
-      const int st = c & 1, m = imin(C, own.y - c * C);
-      Scalars &S = sc_all[st];
-      // gates of two tokens a lane (first warp)
-      float g0 = 0.f, g1 = 0.f, be = 0.f;
-      const long long r0 = own.x + (long long)c * C;
-      if (pw == 0) {
-        if (2 * lane < m) g0 = P.g[(r0 + 2 * lane) * P.Hv + h];
-        if (2 * lane + 1 < m) g1 = P.g[(r0 + 2 * lane + 1) * P.Hv + h];
-      }
-      if (pt < m && pt < C) be = P.b[(r0 + pt) * P.Hv + h];
-      if (c >= 2 && ok) ok = mbar_wait(&free_[st], ((c >> 1) - 1) & 1, P.err);
-      cp_async_wait_all();
-      fence_proxy_async();
-      bar();
-      uint8_t *kq = smem + Y::KQ + st * Y::KQ_BYTES;
-      // keys and queries to fp16: eight threads a row, DK/8 elements each
-      constexpr int PR = DK / 64;  // 16-byte pieces a thread
-#pragma unroll 2
-      for (int r = pt >> 3; r < 128; r += PREP / 8) {
-        const int s8 = pt & 7;
-        uint4 w[PR];
-        uint32_t mx = 0;
-#pragma unroll
-        for (int y = 0; y < PR; ++y) {
-          const int x = s8 + 8 * y;
-          w[y] = *reinterpret_cast<const uint4 *>(smem + Y::RAW + r * DK * 2 + ((x ^ (r & 7)) << 4));
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {  // (of finite values the larger has the larger bits)
-            const uint32_t v = (&w[y].x)[z];
-            mx = max(mx, max(v & 0x7fffu, (v >> 16) & 0x7fffu));
+        if (!ok)  // no copy may outlive the CTA
+          for (int k = imax(0, c - STAGES); k < c && mbar_wait(&full[k % STAGES], (k / STAGES) & 1, P.err); ++k) {
           }
-        }
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const int E = (int)(mx >> 7);
-        const float f = pow2_field(imax(250 - E, 1));
-        const f2 f2x = pack2(f, f);
-#pragma unroll
-        for (int y = 0; y < PR; ++y) {
-          const int x = s8 + 8 * y;
-          uint4 d;
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const uint32_t v = (&w[y].x)[z];
-            const float2 p = unpack2(mul2(pack2(bf16lo(v), bf16hi(v)), f2x));
-            (&d.x)[z] = pack_f16x2(p.x, p.y);
-          }
-          *reinterpret_cast<uint4 *>(kq + (x >> 3) * 128 * 128 + swz(r, x & 7)) = d;
-        }
-        if (s8 == 0) ex[r] = E;
-      }
-      if (pw == 0) {  // running sums of the gates, in units of log 2
-        double a0 = (double)(g0 < G_LEAST ? G_LEAST : g0), a1 = a0 + (double)(g1 < G_LEAST ? G_LEAST : g1);
-        double x = a1;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        const double k2 = 1.4426950408889634074;
-        const double s1 = x * k2, s0 = (x - a1 + a0) * k2;
-        gh[2 * lane] = (float)s0, gl[2 * lane] = (float)(s0 - (double)(float)s0);
-        gh[2 * lane + 1] = (float)s1, gl[2 * lane + 1] = (float)(s1 - (double)(float)s1);
-      }
-      fence_proxy_async();
-      bar();
-      if (issuer && ok) {
-        const uint64_t da = tc::smem_desc_sw128(smem_u32(kq), 16, 1024);
-#pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks) {
-          const uint64_t d = da + ((ks >> 2) * 128 * 128 + (ks & 3) * 32) / 16;
-          tc::mma_bf16(tb + Y::KK, d, d, tc::idesc_f16_f32(128, C, false), ks > 0);
-        }
-        tc::commit(k_done);
       }
       __syncwarp();
-      if (pt < C) {
-        const float gt = gh[pt] + gl[pt];
-        const float e1 = pow2_field(imin(ex[pt] + 4, 254));  // 2^e
-        const float ga = ex2_approx(gt), bs = be * e1;
-        S.bv[pt] = bs;
-        S.bx[pt] = bs * e1 * ga;
-        S.en[pt] = ex2_approx((gh[C - 1] - gh[pt]) + (gl[C - 1] - gl[pt]));
-        S.os[pt] = pow2_field(imin(ex[C + pt] + 4, 254)) * (1.f / Q_GAIN);
-        if (pt == C - 1) S.gc = ga;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&kq_full[st]);
-      if (c + 1 < n) fetch(c + 1);
-      if (ok) ok = mbar_wait(k_done, c & 1, P.err);
-      ok = __all_sync(0xffffffffu, ok);
-      tc::fence_after_sync();
-      // ---- A (rows 0..63) and P (64..127) ----
-      {
-        const int i = (pw & 1) * 32 + lane;
-        const bool isP = pw >= 2;
-        const float hi_i = gh[i], lo_i = gl[i];
-        const float f = isP ? Q_GAIN : pow2_field(imin(ex[i] + 4, 254));
-        // b' of this row (b is with the thread of the token)
-        float bi = 1.f;
-        if (!isP) bi = be * f * f;  // pt == i here
-        const f2 rowf = pack2(isP ? Q_GAIN : bi, isP ? Q_GAIN : bi), hi2 = pack2(hi_i, hi_i), lo2 = pack2(lo_i, lo_i);
-        const f2 neg = pack2(-1.f, -1.f);
-        uint8_t *pp = smem + Y::P + st * Y::T_BYTES;
+    } else if (warp == CHAIN_WARPS + 1) {
+      // -------------------------------------------------------- products --
+      const bool leader = tc::elect_one();
+      constexpr uint32_t IDN = tc::idesc_f16_f32(128, C, false), IDD = tc::idesc_f16_f32(128, DK, true);
+      const uint64_t d_row = tc::smem_desc_sw128(smem_u32(ring), 16, 1024), d_col = tc::smem_desc_sw128(smem_u32(ring), C * 128, 1024);
+      const uint32_t row_hi = (uint32_t)(d_row >> 32), col_hi = (uint32_t)(d_col >> 32);
+      for (int c = 0; c < n; ++c) {
+        const int st = c % STAGES;
+        const uint32_t par = c & 1, lo = (uint32_t)d_row + st * (Y::STAGE / 16), lot = (uint32_t)d_col + st * (Y::STAGE / 16);
+        wait(&full[st], (c / STAGES) & 1);
+        // X = S K^T, as the parts of S come
 #pragma unroll
-        for (int c0 = 0; c0 < 2; ++c0) {
-          uint32_t raw[32];
-          const bool any = c0 == 0 || (pw & 1);  // columns 32.. of rows 0..31 are zero
-          if (any && ok) {
-            tc::ld32(tb + Y::KK + c0 * 32 + lane_off, raw);
-            tc::wait_ld();
+        for (int x = 0; x < 2; ++x) {
+          wait(&s_ready[x], par);
+          tc::fence_after_sync();
+          if (leader && ok) {
+#pragma unroll
+            for (int ks = x; ks < DK / 16; ks += 2)
+#pragma unroll
+              for (int p = 0; p < 2; ++p)
+                tc::mma_bf16_ts(tb + Y::X, tb + (p ? Y::SL : Y::SH) + ks * 8, lo + (Y::K + (ks >> 2) * C * 128 + (ks & 3) * 32) / 16, row_hi,
+                                IDN, x > 0 || ks > 0 || p > 0);
+            if (x == 1) tc::commit(x_done);
           }
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float y[8];
-#pragma unroll
-            for (int z = 0; z < 8; z += 4) {
-              const int j = c0 * 32 + e + z;
-              const ulonglong2 hj = *reinterpret_cast<const ulonglong2 *>(gh + j), lj = *reinterpret_cast<const ulonglong2 *>(gl + j);
-#pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                const f2 dh = fma2(w ? hj.y : hj.x, neg, hi2), dl = fma2(w ? lj.y : lj.x, neg, lo2);
-                const float2 d = unpack2(add2(dh, dl));
-                const f2 kk = pack2(__uint_as_float(raw[e + z + 2 * w]), __uint_as_float(raw[e + z + 2 * w + 1]));
-                const float2 t = unpack2(mul2(mul2(kk, rowf), pack2(ex2_approx(d.x), ex2_approx(d.y))));
-                const int jj = j + 2 * w;
-                y[z + 2 * w] = any && (isP ? jj <= i : jj < i) ? t.x : 0.f;
-                y[z + 2 * w + 1] = any && (isP ? jj + 1 <= i : jj + 1 < i) ? t.y : 0.f;
-              }
-            }
-            const int j = c0 * 32 + e;
-            if (isP) {
-              *reinterpret_cast<uint4 *>(pp + swz(i, j >> 3)) = make_uint4(pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3]),
-                                                                          pack_f16x2(y[4], y[5]), pack_f16x2(y[6], y[7]));
-            } else {
-              *reinterpret_cast<float4 *>(A + i * AS + j) = make_float4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<float4 *>(A + i * AS + j + 4) = make_float4(y[4], y[5], y[6], y[7]);
-            }
-          }
+          __syncwarp();
         }
-      }
-      tc::fence_before_sync();
-      bar();
-      // ---- decayed queries (their product with the keys is done) ----
-#pragma unroll 2
-      for (int r = C + (pt >> 3); r < 128; r += PREP / 8) {
-        const __half2 ga = __float2half2_rn(ex2_approx(gh[r - C] + gl[r - C]) * Q_GAIN);
+        // U = R T^T
+        wait(r_ready, par);
+        tc::fence_after_sync();
+        if (leader && ok) {
 #pragma unroll
-        for (int y = 0; y < PR; ++y) {
-          uint4 *p = reinterpret_cast<uint4 *>(kq + y * 128 * 128 + swz(r, pt & 7));
-          uint4 d = *p;
+          for (int ks = 0; ks < C / 16; ++ks)
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            __half2 v = *reinterpret_cast<__half2 *>(&(&d.x)[z]);
-            v = __hmul2(v, ga);
-            (&d.x)[z] = *reinterpret_cast<uint32_t *>(&v);
-          }
-          *p = d;
-        }
-      }
-      // ---- T = (I + A)^-1 in place: a 16 x 16 block a warp, a column a lane ----
-      {
-        const int o = pw * 16;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
-#pragma unroll
-          for (int j = 0; j < i; ++j) {
-            const float a = A[(o + i) * AS + o + j];
-            if (j & 1) s1 = fmaf(-a, x[j], s1); else s0 = fmaf(-a, x[j], s0);
-          }
-          x[i] = s0 + s1;
+            for (int p = 0; p < 3; ++p)  // hi hi, lo hi, hi lo
+              tc::mma_bf16_ts(tb + Y::U, tb + Y::X + ks * 16 + (p == 1 ? 8 : 0), lo + (Y::T + (p == 2 ? PART : 0) + ks * 32) / 16, row_hi, IDN,
+                              ks > 0 || p > 0);
+          tc::commit(u_done);
         }
         __syncwarp();
-        if (lane < 16) {
+        // S Q^T
+        if (c > 0) wait(o_free, par ^ 1);
+        tc::fence_after_sync();
+        if (leader && ok) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) A[(o + i) * AS + o + lane] = x[i];
+          for (int ks = 0; ks < DK / 16; ++ks)
+            tc::mma_bf16_ts(tb + Y::O1, tb + Y::SH + ks * 8, lo + (Y::Q + (ks >> 2) * C * 128 + (ks & 3) * 32) / 16, row_hi, IDN, ks > 0);
         }
-      }
-      bar();
-      // joined: T21 = -T22 (A21 T11), 16 rows and columns of two pairs, then 32 of one
-      {
-        // one row, four columns a thread: pair pt / 64
-        const int o = (pt >> 6) * 32, i = o + 16 + ((pt & 63) >> 2), j = o + (pt & 3) * 4;
+        __syncwarp();
+        // S' = U~ K, then P U
+        wait(ut_ready, par);
+        tc::fence_after_sync();
+        if (leader && ok) {
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-          f2 w0 = 0, w1 = 0;
-          const int k0 = o + 16 * pass;
+          for (int ks = 0; ks < C / 16; ++ks)
 #pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(A + i * AS + k0 + k);
+            for (int p = 0; p < 2; ++p)
+              tc::mma_bf16_ts(tb + Y::D, tb + Y::U + ks * 16 + p * 8, lot + (Y::K + ks * 2048) / 16, col_hi, IDD, ks > 0 || p > 0);
+          tc::commit(d_done);
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              const ulonglong2 t = *reinterpret_cast<const ulonglong2 *>(A + (k0 + k + z) * AS + j);
-              const float av = pass ? -(&a.x)[z] : (&a.x)[z];
-              w0 = fma2(pack2(av, av), t.x, w0), w1 = fma2(pack2(av, av), t.y, w1);
-            }
-          }
-          bar();
-          *reinterpret_cast<ulonglong2 *>(A + i * AS + j) = make_ulonglong2(w0, w1);
-          bar();
+          for (int ks = 0; ks < C / 16; ++ks)
+            tc::mma_bf16_ts(tb + Y::O2, tb + Y::X + ks * 16, lo + (Y::P + ks * 32) / 16, row_hi, IDN, ks > 0);
+          tc::commit(o_done);
+          tc::commit(&empty[st]);
         }
+        __syncwarp();
       }
-      {
-        const int i = 32 + (pt >> 3) * 2, j = (pt & 7) * 4;  // two rows, four columns
-#pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-          f2 w[2][2] = {{0, 0}, {0, 0}};
-          const int k0 = 32 * pass;
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(A + i * AS + k0 + k);
-            const float4 a1 = *reinterpret_cast<const float4 *>(A + (i + 1) * AS + k0 + k);
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              const ulonglong2 t = *reinterpret_cast<const ulonglong2 *>(A + (k0 + k + z) * AS + j);
-              const float p = pass ? -(&a.x)[z] : (&a.x)[z], q = pass ? -(&a1.x)[z] : (&a1.x)[z];
-              w[0][0] = fma2(pack2(p, p), t.x, w[0][0]), w[0][1] = fma2(pack2(p, p), t.y, w[0][1]);
-              w[1][0] = fma2(pack2(q, q), t.x, w[1][0]), w[1][1] = fma2(pack2(q, q), t.y, w[1][1]);
-            }
-          }
-          bar();
-          *reinterpret_cast<ulonglong2 *>(A + i * AS + j) = make_ulonglong2(w[0][0], w[0][1]);
-          *reinterpret_cast<ulonglong2 *>(A + (i + 1) * AS + j) = make_ulonglong2(w[1][0], w[1][1]);
-          bar();
-        }
+      if (leader) {  // every product issued has completed before tensor memory is released
+        tc::commit(idle);
+        spin_wait(idle, 0, P.err);
       }
-      // ---- T in two parts: half a row a thread ----
-      {
-        const int i = pt >> 1, j0 = (pt & 1) * 32;
-        uint8_t *th = smem + Y::T + st * 2 * Y::T_BYTES, *tl = th + Y::T_BYTES;
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint4 hi, lo;
-          const int j = j0 + e;
-          const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(A + i * AS + j), d = *reinterpret_cast<const ulonglong2 *>(A + i * AS + j + 4);
-          split2(a.x, hi.x, lo.x);
-          split2(a.y, hi.y, lo.y);
-          split2(d.x, hi.z, lo.z);
-          split2(d.y, hi.w, lo.w);
-          *reinterpret_cast<uint4 *>(th + swz(i, j >> 3)) = hi;
-          *reinterpret_cast<uint4 *>(tl + swz(i, j >> 3)) = lo;
-        }
-      }
-      fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tp_full[st]);
     }
-    cp_async_wait_all();
-    if (issuer) {
-      tc::commit(&idle[0]);
-      spin_wait(&idle[0], 0, P.err);
-    }
-    __syncwarp();
   } else {
-    // ---------------------------------------------------- the chain --
-    setmaxnreg_inc<184>();
-    constexpr int SC = DK / 2;  // columns of S that are this thread's
-    const int hf = warp >> 2, r = (warp & 3) * 32 + lane, i = i0 + r;
+    // ------------------------------------------------------- rows of S --
+    setmaxnreg_inc<112>();
+    constexpr int SC = DK / 4;  // columns of S that are this thread's
+    const int q = warp >> 2, r = (warp & 3) * 32 + lane, i = i0 + r;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const bool live = i < P.dv;
-    const bool issuer = warp == 0 && tc::elect_one();
-    auto bar = [&]() { named_barrier(2, CHAIN); };
     float *xchg = reinterpret_cast<float *>(smem + Y::XCHG);
     uint32_t trades = 0;
-    // the larger of a value that both threads of a row have
-    auto both = [&](float x) {
-      float *at = xchg + (trades & 1) * 2 * ROWS;
+    // the largest of a value that the four threads of a row have
+    auto among = [&](float x) {
+      float *at = xchg + (trades & 1) * 4 * ROWS + r;
       ++trades;
-      at[hf * ROWS + r] = x;
-      named_barrier(3 + (warp & 3), 64);
-      return fmaxf(x, at[(hf ^ 1) * ROWS + r]);
+      at[q * ROWS] = x;
+      named_barrier(1 + (warp & 3), 128);
+      return fmaxf(fmaxf(at[0], at[ROWS]), fmaxf(at[2 * ROWS], at[3 * ROWS]));
     };
-    float *srow = P.states.ptr + (slot >= 0 ? slot : 0) * P.states.slot_stride + ((long long)h * P.dv + (live ? i : 0)) * DK + hf * SC;
+    auto arrive = [&](uint64_t *bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    float *srow = P.states.ptr + (slot >= 0 ? slot : 0) * P.states.slot_stride + ((long long)h * P.dv + (live ? i : 0)) * DK + q * SC;
     const bool kept = slot >= 0 && live && n > 0;
     f2 S[SC / 2];
 #pragma unroll
@@ -506,207 +622,169 @@ __global__ void __launch_bounds__(THREADS, 1) chunk_kernel(const ChunkParams CP)
       }
       return fmaxf(m0, m1);
     };
-    // largest |b' v'| of this thread's half of block c
+    auto scalars = [&](int c) { return reinterpret_cast<const Scalars *>(ring + (c % STAGES) * Y::STAGE + Y::S); };
+    auto values = [&](int c) { return reinterpret_cast<const uint16_t *>(ring + (c % STAGES) * Y::STAGE + Y::V) + q * 16 * ROWS + r; };
+    // values of this thread's tokens 2t, 2t + 1 (zeros past the sequence's end)
+    auto pair = [&](const uint16_t *v, int t, int some) {
+      const uint32_t x = 2 * t < some ? v[2 * t * ROWS] : 0u, y = 2 * t + 1 < some ? v[(2 * t + 1) * ROWS] : 0u;
+      return x | y << 16;
+    };
+    // largest |b' v'| of them
     auto v_max = [&](int c) {
-      const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(smem + Y::V + (c % 3) * Y::V_BYTES) + hf * 32 * ROWS + r;
-      const float *bv = &sc_all[c & 1].bv[hf * 32];
-      float m0 = 0.f, m1 = 0.f;
+      const uint16_t *v = values(c);
+      const Scalars *Z = scalars(c);
+      const int some = own.y - c * C - q * 16;
+      float m = 0.f;
 #pragma unroll
-      for (int t = 0; t < 32; t += 4) {
-        const float4 b4 = *reinterpret_cast<const float4 *>(bv + t);
-        m0 = fmaxf(m0, fmaxf(fabsf(b4.x * __bfloat162float(v[t * ROWS])), fabsf(b4.y * __bfloat162float(v[(t + 1) * ROWS]))));
-        m1 = fmaxf(m1, fmaxf(fabsf(b4.z * __bfloat162float(v[(t + 2) * ROWS])), fabsf(b4.w * __bfloat162float(v[(t + 3) * ROWS]))));
+      for (int t = 0; t < 8; ++t) {
+        const uint32_t x = pair(v, t, some);
+        const float2 b2 = *reinterpret_cast<const float2 *>(&Z->bv[q * 16 + 2 * t]);
+        m = fmaxf(m, fmaxf(fabsf(bf16lo(x) * b2.x), fabsf(bf16hi(x) * b2.y)));
       }
-      return fmaxf(m0, m1);
+      return m;
     };
     // scale of a row: 2^-k with at most 1 behind it
     auto scale_of = [&](float most) { return pow2_field(253 - imin(imax(__float_as_int(most) >> 23, 27), 226)); };
+    // S as the next product's operand, 16 columns (a k-step) at a time
     auto put_state = [&](float sc) {
       const f2 sc2 = pack2(sc, sc);
+      constexpr int STEPS = SC / 16;
 #pragma unroll
-      for (int g = 0; g < SC / 32; ++g) {
-        uint32_t hi[16], lo[16];
+      for (int g = 0; g < STEPS; ++g) {
+        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) split2(mul2(S[16 * g + e], sc2), hi[e], lo[e]);
-        tc::st16(tb + Y::SH + hf * (SC / 2) + 16 * g + lane_off, hi);
-        tc::st16(tb + Y::SL + hf * (SC / 2) + 16 * g + lane_off, lo);
-      }
-      tc::wait_st();
-      tc::fence_before_sync();
-    };
-    bool ok = true;
-    auto wait = [&](uint64_t *bar_, uint32_t parity) {
-      if (ok) ok = spin_wait(bar_, parity, P.err);
-      ok = __all_sync(0xffffffffu, ok);
-    };
-    float m = row_max();
-    float sc = 1.f, isc_before = 1.f;
-    if (n > 0) {
-      wait(&kq_full[0], 0);
-      sc = scale_of(both(fmaxf(m * 0.015625f, 0.125f * v_max(0))));
-      put_state(sc);
-      bar();
-    }
-    // O of block c
-    auto put_out = [&](int c, float isc) {
-      wait(o_done, c & 1);
-      tc::fence_after_sync();
-      const Scalars &Z = sc_all[c & 1];
-      uint32_t raw[32];
-      if (ok) {
-        tc::ld32(tb + Y::O + hf * 32 + lane_off, raw);
-        tc::wait_ld();
-      }
-      const int t0 = c * C + hf * 32, mt = imin(32, own.y - t0);
-      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.o.ptr) + (own.x + (long long)t0) * P.o.token_stride + (long long)h * P.o.head_stride + i;
-#pragma unroll
-      for (int t = 0; t < 32; ++t) {
-        const float x = __uint_as_float(raw[t]) * isc * Z.os[hf * 32 + t];
-        if (live && ok && t < mt) out[(long long)t * P.o.token_stride] = __float2bfloat16_rn(x);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&free_[c & 1]);
-    };
-    constexpr uint32_t IDN = tc::idesc_f16_f32(128, C, false), IDD = tc::idesc_f16_f32(128, DK, true);
-    for (int c = 0; c < n; ++c) {
-      const int st = c & 1;
-      const uint32_t par = c & 1;
-      const Scalars &Z = sc_all[st];
-      const uint64_t dk = tc::smem_desc_sw128(smem_u32(smem + Y::KQ + st * Y::KQ_BYTES), 16, 1024);
-      const uint64_t dkt = tc::smem_desc_sw128(smem_u32(smem + Y::KQ + st * Y::KQ_BYTES), 128 * 128, 1024);
-      const uint64_t dt = tc::smem_desc_sw128(smem_u32(smem + Y::T + st * 2 * Y::T_BYTES), 16, 1024);
-      const uint64_t dp = tc::smem_desc_sw128(smem_u32(smem + Y::P + st * Y::T_BYTES), 16, 1024);
-      auto k_step = [](int ks) { return (uint64_t)(((ks >> 2) * 128 * 128 + (ks & 3) * 32) / 16); };
-      // X = S K^T
-      if (issuer && ok) {
-        tc::fence_after_sync();
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int ks = 0; ks < DK / 16; ++ks)
-            tc::mma_bf16_ts(tb + Y::X, tb + (p ? Y::SL : Y::SH) + ks * 8, dk + k_step(ks), IDN, p > 0 || ks > 0);
-        tc::commit(x_done);
-      }
-      __syncwarp();
-      if (c > 0) put_out(c - 1, isc_before);
-      wait(&tp_full[st], (c >> 1) & 1);
-      // R = b (v - e^G X)
-      {
-        const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(smem + Y::V + (c % 3) * Y::V_BYTES) + hf * 32 * ROWS + r;
-        f2 vv[16];
-        const f2 sc2 = pack2(sc, sc);
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          const f2 bv = *reinterpret_cast<const f2 *>(&Z.bv[hf * 32 + 2 * t]);
-          vv[t] = mul2(mul2(pack2(__bfloat162float(v[2 * t * ROWS]), __bfloat162float(v[(2 * t + 1) * ROWS])), sc2), bv);
-        }
-        wait(x_done, par);
-        tc::fence_after_sync();
-        uint32_t raw[32];
-        if (ok) {
-          tc::ld32(tb + Y::X + hf * 32 + lane_off, raw);
-          tc::wait_ld();
-        }
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          const f2 bx = mul2(*reinterpret_cast<const f2 *>(&Z.bx[hf * 32 + 2 * t]), pack2(-1.f, -1.f));
-          split2(fma2(bx, pack2(__uint_as_float(raw[2 * t]), __uint_as_float(raw[2 * t + 1])), vv[t]), hi[t], lo[t]);
-        }
-        tc::st16(tb + Y::R + hf * 16 + lane_off, hi);
-        tc::st16(tb + Y::R + 32 + hf * 16 + lane_off, lo);
+        for (int e = 0; e < 8; ++e) split2(mul2(S[8 * g + e], sc2), hi[e], lo[e]);
+        tc::st8(tb + Y::SH + q * (SC / 2) + 8 * g + lane_off, hi);
+        tc::st8(tb + Y::SL + q * (SC / 2) + 8 * g + lane_off, lo);
         tc::wait_st();
         tc::fence_before_sync();
-        bar();
+        if (STEPS == 2) arrive(&s_ready[g]);
       }
-      // U = R T^T, and O = S Q^T
-      if (issuer && ok) {
-        tc::fence_after_sync();
-#pragma unroll
-        for (int p = 0; p < 3; ++p)  // hi hi, lo hi, hi lo
-#pragma unroll
-          for (int ks = 0; ks < C / 16; ++ks)
-            tc::mma_bf16_ts(tb + Y::U, tb + Y::R + (p == 1 ? 32 : 0) + ks * 8, dt + (uint64_t)(((p == 2 ? Y::T_BYTES : 0) + ks * 32) / 16),
-                            IDN, p > 0 || ks > 0);
-        tc::commit(u_done);
-#pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks)
-          tc::mma_bf16_ts(tb + Y::O, tb + Y::SH + ks * 8, dk + k_step(ks) + 64 * 128 / 16, IDN, ks > 0);
+      if (STEPS == 1) {  // (one k-step a thread: all are there at once)
+        arrive(&s_ready[0]);
+        arrive(&s_ready[1]);
       }
-      __syncwarp();
-      float um = 0.f;
-      {
-        f2 en[16];
-#pragma unroll
-        for (int t = 0; t < 16; ++t) en[t] = *reinterpret_cast<const f2 *>(&Z.en[hf * 32 + 2 * t]);
-        wait(u_done, par);
-        tc::fence_after_sync();
-        uint32_t raw[32];
+    };
+    float m = row_max(), sc = 1.f;
+    if (n > 0) {
+      wait(&full[0], 0);
+      sc = scale_of(among(fmaxf(m * 0.015625f, 0.125f * v_max(0))));
+      put_state(sc);
+    }
+    // O of block c, whose rows were scaled by 1 / isc
+    auto put_out = [&](int c, float isc) {
+      const Scalars *Z = scalars(c);
+      wait(o_done, c & 1);
+      tc::fence_after_sync();
+      const int t0 = c * C + q * 16, some = live && ok ? own.y - t0 : 0;
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.o.ptr) + (own.x + (long long)t0) * P.o.token_stride + (long long)h * P.o.head_stride + i;
+      const long long step = P.o.token_stride;
+#pragma unroll 1
+      for (int t = 0; t < 16; t += 4) {  // (four at a time: registers)
+        uint32_t a[4], d[4];
         if (ok) {
-          tc::ld32(tb + Y::U + hf * 32 + lane_off, raw);
+          tc::ld4(tb + Y::O1 + q * 16 + t + lane_off, a);
+          tc::ld4(tb + Y::O2 + q * 16 + t + lane_off, d);
           tc::wait_ld();
         }
-        uint32_t hi[16], lo[16], u[16];
+        const float4 s1 = *reinterpret_cast<const float4 *>(&Z->os1[q * 16 + t]), s2 = *reinterpret_cast<const float4 *>(&Z->os2[q * 16 + t]);
+        const float x[4] = {__uint_as_float(a[0]) * s1.x + __uint_as_float(d[0]) * s2.x, __uint_as_float(a[1]) * s1.y + __uint_as_float(d[1]) * s2.y,
+                            __uint_as_float(a[2]) * s1.z + __uint_as_float(d[2]) * s2.z, __uint_as_float(a[3]) * s1.w + __uint_as_float(d[3]) * s2.w};
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
+        for (int z = 0; z < 4; ++z) {
+          if (t + z < some) *out = __float2bfloat16_rn(x[z] * isc);
+          out += step;
+        }
+      }
+      tc::fence_before_sync();
+      arrive(o_free);
+      arrive(&empty[c % STAGES]);
+    };
+    float isc_before = 1.f;
+    for (int c = 0; c < n; ++c) {
+      const uint32_t par = c & 1;
+      const Scalars *Z = scalars(c);
+      const f2 sc2 = pack2(sc, sc);
+      if (c > 0) put_out(c - 1, isc_before);
+      // R = b (v - e^G X)
+      {
+        const int some = own.y - c * C - q * 16;
+        const uint16_t *v = values(c);
+        uint32_t vb[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) vb[t] = pair(v, t, some);
+        wait(x_done, par);
+        tc::fence_after_sync();
+        uint32_t raw[16], hi[8], lo[8];
+        if (ok) {
+          tc::ld16(tb + Y::X + q * 16 + lane_off, raw);
+          tc::wait_ld();
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const f2 bx = *reinterpret_cast<const f2 *>(&Z->bx[q * 16 + 2 * t]), bv = *reinterpret_cast<const f2 *>(&Z->bv[q * 16 + 2 * t]);
+          const f2 w = mul2(mul2(pack2(bf16lo(vb[t]), bf16hi(vb[t])), sc2), bv);
+          split2(fma2(bx, pack2(__uint_as_float(raw[2 * t]), __uint_as_float(raw[2 * t + 1])), w), hi[t], lo[t]);
+        }
+        tc::st8(tb + Y::X + q * 16 + lane_off, hi);
+        tc::st8(tb + Y::X + q * 16 + 8 + lane_off, lo);
+        tc::wait_st();
+        tc::fence_before_sync();
+        arrive(r_ready);
+      }
+      float um = 0.f;
+      {
+        wait(u_done, par);
+        tc::fence_after_sync();
+        uint32_t raw[16], hi[8], lo[8], u[8];
+        if (ok) {
+          tc::ld16(tb + Y::U + q * 16 + lane_off, raw);
+          tc::wait_ld();
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
           const float a = __uint_as_float(raw[2 * t]), d = __uint_as_float(raw[2 * t + 1]);
           u[t] = pack_f16x2(a, d);
-          const f2 x = mul2(pack2(a, d), en[t]);
+          const f2 x = mul2(pack2(a, d), *reinterpret_cast<const f2 *>(&Z->en[q * 16 + 2 * t]));
           const float2 y = unpack2(x);
           um = fmaxf(um, fmaxf(fabsf(y.x), fabsf(y.y)));
           split2(x, hi[t], lo[t]);
         }
-        tc::st16(tb + Y::R + hf * 16 + lane_off, hi);
-        tc::st16(tb + Y::R + 32 + hf * 16 + lane_off, lo);
-        tc::st16(tb + Y::R + 64 + hf * 16 + lane_off, u);
+        tc::st8(tb + Y::U + q * 16 + lane_off, hi);
+        tc::st8(tb + Y::U + q * 16 + 8 + lane_off, lo);
+        tc::st8(tb + Y::X + q * 16 + lane_off, u);
         tc::wait_st();
         tc::fence_before_sync();
-        bar();
+        arrive(ut_ready);
       }
-      // S' = U~ K, then O += P U
-      if (issuer && ok) {
-        tc::fence_after_sync();
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int ks = 0; ks < C / 16; ++ks)
-            tc::mma_bf16_ts(tb + Y::D, tb + Y::R + p * 32 + ks * 8, dkt + (uint64_t)(ks * 2048 / 16), IDD, p > 0 || ks > 0);
-        tc::commit(d_done);
-#pragma unroll
-        for (int ks = 0; ks < C / 16; ++ks)
-          tc::mma_bf16_ts(tb + Y::O, tb + Y::R + 64 + ks * 8, dp + (uint64_t)(ks * 32 / 16), IDN, true);
-        tc::commit(o_done);
-        tc::commit(&free_[st]);
-      }
-      __syncwarp();
-      const float gc = Z.gc, isc = 1.f / sc;  // (exact)
+      const float gc = Z->gc, isc = 1.f / sc;  // (exact)
       float sc_next = sc;
       if (c + 1 < n) {
-        wait(&kq_full[st ^ 1], ((c + 1) >> 1) & 1);
-        // elements of k' are below 2^-3, 64 tokens: |S'| <= 8 |U~|; twice for the other half's
-        sc_next = scale_of(both(fmaxf((gc * m + 8.f * um * isc) * 0.03125f, 0.125f * v_max(c + 1))));
+        wait(&full[(c + 1) % STAGES], ((c + 1) / STAGES) & 1);
+        // elements of k' are below 2^-3, 64 tokens: |S'| <= 8 |U~|; twice, as the largest of
+        // the sums' terms may be different threads'
+        sc_next = scale_of(among(fmaxf((gc * m + 8.f * um * isc) * 0.03125f, 0.125f * v_max(c + 1))));
       }
-      {
-        const f2 gc2 = pack2(gc, gc), isc2 = pack2(isc, isc);
+      const f2 gc2 = pack2(gc, gc), isc2 = pack2(isc, isc);
 #pragma unroll
-        for (int e = 0; e < SC / 2; ++e) S[e] = mul2(S[e], gc2);
-        wait(d_done, par);
-        tc::fence_after_sync();
+      for (int e = 0; e < SC / 2; ++e) S[e] = mul2(S[e], gc2);
+      wait(d_done, par);
+      tc::fence_after_sync();
 #pragma unroll
-        for (int g = 0; g < SC / 32; ++g) {
-          uint32_t raw[32];
-          if (ok) {
-            tc::ld32(tb + Y::D + hf * SC + 32 * g + lane_off, raw);
-            tc::wait_ld();
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            S[16 * g + e] = fma2(pack2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), isc2, S[16 * g + e]);
+      for (int g = 0; g < SC / 16; ++g) {
+        uint32_t raw[16];
+        if (ok) {
+          tc::ld16(tb + Y::D + q * SC + 16 * g + lane_off, raw);
+          tc::wait_ld();
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          S[8 * g + e] = fma2(pack2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), isc2, S[8 * g + e]);
       }
-      put_state(sc_next);
-      bar();
-      m = row_max();
+      if (c + 1 < n) {
+        put_state(sc_next);
+        m = row_max();
+      }
       isc_before = isc;
       sc = sc_next;
     }
@@ -715,25 +793,37 @@ __global__ void __launch_bounds__(THREADS, 1) chunk_kernel(const ChunkParams CP)
 #pragma unroll
       for (int e = 0; e < SC / 2; e += 2) *reinterpret_cast<ulonglong2 *>(srow + 2 * e) = make_ulonglong2(S[e], S[e + 1]);
     }
-    if (issuer) {
-      tc::commit(&idle[1]);
-      spin_wait(&idle[1], 0, P.err);
-    }
-    __syncwarp();
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == CHAIN_WARPS) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tb, 512u);
   }
 }
 
+// Blocks that the workspace has places for.
+inline long long places(int B, int T) { return (long long)T / C + B; }
+
 template <int DK>
 sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
-  const long long items = (long long)CP.p.B * CP.p.Hv * CP.blocks;
+  const PoolParams &P = CP.p;
+  const long long items = (long long)P.B * P.Hv * CP.row_blocks, blocks = places(P.B, P.T);
   if (items > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
-  return from_cuda(launch_early(chunk_kernel<DK>, dim3((unsigned)items), dim3(THREADS), (size_t)L<DK>::BYTES, s, CP));
+  // values (column, head, token) in boxes of 128 x 1 x 64, zeros past the last column
+  auto fn = attn::encode_fn();
+  if (!fn) return SV_ERR_CUDA;
+  CUtensorMap mv;
+  // the stride of a dimension of one is never used, but has to be a valid one
+  cuuint64_t dims[3] = {(cuuint64_t)P.dv, (cuuint64_t)P.Hv, (cuuint64_t)P.T};
+  cuuint64_t strides[2] = {P.Hv > 1 ? (cuuint64_t)P.v.head_stride * 2 : 16, P.T > 1 ? (cuuint64_t)P.v.token_stride * 2 : 16};
+  cuuint32_t box[3] = {ROWS, 1, C}, estr[3] = {1, 1, 1};
+  if (fn(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, P.v.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return SV_ERR_CUDA;
+  cudaError_t e = launch_early(prepare_kernel<DK>, dim3((unsigned)blocks, P.Hk), dim3(128), (size_t)PL<DK>::BYTES, s, CP);
+  if (e != cudaSuccess) return SV_ERR_CUDA;
+  return from_cuda(launch_early(chain_kernel<DK>, dim3((unsigned)items), dim3(CHAIN_THREADS), (size_t)CL<DK>::BYTES, s, mv, CP));
 }
 
 }  // namespace
@@ -745,14 +835,15 @@ using namespace sv;
 extern "C" {
 
 size_t gdn_chunk_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv) {
-  (void)B, (void)T, (void)Hk, (void)Hv, (void)dk, (void)dv;
-  return 0;
+  (void)dv;
+  if (B < 1 || T < 1 || Hk < 1 || Hv < 1 || (dk != 64 && dk != 128)) return 0;
+  const size_t per = (size_t)Hk * 4 * gdn::C * dk + (size_t)Hv * gdn::HEAD_BYTES;
+  return (size_t)gdn::places(B, T) * per;
 }
 
 sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows *q, const sv_rows *k,
                     const sv_rows *v, const float *g, const float *beta, const sv_rows *o, const int32_t *cu, int B,
                     int T, int Hk, int Hv, int dk, int dv, void *workspace, size_t ws_bytes, sv_stream_t stream) {
-  (void)workspace, (void)ws_bytes;
   if (B < 0 || T < 0 || Hk < 1 || Hv < 1 || Hv % Hk != 0 || dk < 1 || dv < 1) return SV_ERR_INVALID_ARG;
   if (dk != 64 && dk != 128) return SV_ERR_UNSUPPORTED;
   if (Hv > 65535 || B > gdn::MAX_POOL_B || T > 0x40000000 || dv > 65536) return SV_ERR_UNSUPPORTED;
@@ -762,7 +853,12 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   if (T > 0 && (!g || !beta || !paged::aligned(g, 4) || !paged::aligned(beta, 4))) return SV_ERR_INVALID_ARG;
   if (B > 0 && (!slots || !cu || !paged::aligned(slots, 4) || !paged::aligned(cu, 4))) return SV_ERR_INVALID_ARG;
   if (B == 0 || T == 0) return SV_OK;
-  gdn::PoolParams P{};
+  // a tensor map steps by every stride: values that repeat (stride 0) have none
+  if ((T > 1 && !v->token_stride) || (Hv > 1 && !v->head_stride)) return SV_ERR_UNSUPPORTED;
+  if (!workspace || ws_bytes < gdn_chunk_workspace_bytes(B, T, Hk, Hv, dk, dv)) return SV_ERR_WORKSPACE;
+  if (!paged::aligned(workspace, 16)) return SV_ERR_INVALID_ARG;
+  gdn::ChunkParams CP{};
+  gdn::PoolParams &P = CP.p;
   P.states = *states;
   P.slots = slots;
   P.q = *q, P.k = *k, P.v = *v, P.o = *o, P.g = g, P.b = beta;
@@ -771,9 +867,9 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   if (!P.err) return SV_ERR_CUDA;
   P.B = B, P.T = T, P.Hk = Hk, P.Hv = Hv, P.dv = dv;
   P.commit = 1;
-  gdn::ChunkParams CP{};
-  CP.p = P;
-  CP.blocks = (dv + gdn::ROWS - 1) / gdn::ROWS;
+  CP.keys = static_cast<uint8_t *>(workspace);
+  CP.heads = CP.keys + (size_t)gdn::places(B, T) * Hk * 4 * gdn::C * dk;
+  CP.row_blocks = (dv + gdn::ROWS - 1) / gdn::ROWS;
   CP.stall = launch_flags() & SV_LAUNCH_TEST_STALL_COPY ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return dk == 64 ? gdn::run_chunks<64>(CP, s) : gdn::run_chunks<128>(CP, s);

@@ -57,7 +57,7 @@ __device__ __forceinline__ void stage_rows(float *dst, const sv_rows &src, long 
 }
 
 template <int DK>
-__global__ void __launch_bounds__(256) tokens_kernel(const PoolParams P) {
+__global__ void __launch_bounds__(256) tokens_kernel(const __grid_constant__ PoolParams P) {
   constexpr int NJ = DK / 32;
   extern __shared__ __align__(16) float sm[];
   const int rows = blockDim.x / LPR;

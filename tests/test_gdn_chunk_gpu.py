@@ -18,6 +18,13 @@ BF16 = 2.0 ** -8
 STATE, OUT = 2.0 ** -14, 2.0 ** -8
 
 
+def chunk(sv, states, slots, r, o, cu):
+    """The call with a workspace of its own."""
+    (T, Hk, dk), (_, Hv, dv) = r[0].shape, r[2].shape
+    ws = sv.workspace(sv.gdn_chunk_workspace_bytes(len(slots), T, Hk, Hv, dk, dv))
+    sv.gdn_chunk(states, slots, *r, o, cu, workspace=ws)
+
+
 def case(sv, lens, Hk, Hv, dk, dv, seed, slots=None, extra=0, **how):
     B, T = len(lens), sum(lens)
     gen = torch.Generator().manual_seed(seed)
@@ -30,8 +37,7 @@ def case(sv, lens, Hk, Hv, dk, dv, seed, slots=None, extra=0, **how):
     q, k, v = fused.split([Hk * dk, Hk * dk, Hv * dv], 1)
     q, k, v = q.unflatten(1, (Hk, dk)), k.unflatten(1, (Hk, dk)), v.unflatten(1, (Hv, dv))
     states, o = pool.cuda(), torch.full((T + extra, Hv, dv), 99.0, device="cuda", dtype=torch.bfloat16)
-    ws = sv.workspace(sv.gdn_chunk_workspace_bytes(B, T + extra, Hk, Hv, dk, dv))
-    sv.gdn_chunk(states, slots.cuda(), q, k, v, g, beta, o, cu.cuda(), workspace=ws)
+    chunk(sv, states, slots.cuda(), (q, k, v, g, beta), o, cu.cuda())
     assert sv.sv_last_device_error() == sv.SV_OK
     want, out = pool.double().clone(), []
     for b in range(B):
@@ -92,7 +98,7 @@ def test_chunks_continue_one_another(cuda_lib):
     outs = []
     for lo, hi in ((0, 100), (100, 101), (101, 230), (230, 296)):
         o = torch.empty(hi - lo, Hv, dv, device="cuda", dtype=torch.bfloat16)
-        sv.gdn_chunk(a, one, *(x[lo:hi] for x in plain.on(r)), o, torch.tensor([0, hi - lo], dtype=torch.int32, device="cuda"))
+        chunk(sv, a, one, [x[lo:hi] for x in plain.on(r)], o, torch.tensor([0, hi - lo], dtype=torch.int32, device="cuda"))
         outs.append(o)
     o = torch.empty(4, Hv, dv, device="cuda", dtype=torch.bfloat16)
     sv.gdn_step(a, one, *(x[296:] for x in plain.on(r)), o, 4, commit=True)
@@ -112,8 +118,8 @@ def test_sizes_of_keys_values_and_states(cuda_lib):
         r["beta"] = r["beta"] / ks ** 2
         pool = torch.randn(1, Hv, dv, dk, generator=torch.Generator().manual_seed(1)) * (vs / ks)
         states, o = pool.cuda(), torch.empty(T, Hv, dv, device="cuda", dtype=torch.bfloat16)
-        sv.gdn_chunk(states, torch.zeros(1, dtype=torch.int32, device="cuda"), *plain.on(r), o,
-                     torch.tensor([0, T], dtype=torch.int32, device="cuda"))
+        chunk(sv, states, torch.zeros(1, dtype=torch.int32, device="cuda"), plain.on(r), o,
+              torch.tensor([0, T], dtype=torch.int32, device="cuda"))
         assert sv.sv_last_device_error() == sv.SV_OK
         S, want = plain.run(pool[0], r, 0, T)
         plain.close(o, want, OUT, BF16, f"o {ks} {vs} {qs}")
@@ -129,7 +135,7 @@ def test_offsets_out_of_order(cuda_lib):
     slots = torch.arange(3, dtype=torch.int32, device="cuda")
     for cu, bad in (([0, 40, 30, 100], 1), ([0, 40, 90, 101], 2), ([-1, 40, 90, 100], 0)):
         states, o = pool.cuda(), torch.full((T, Hv, dv), 99.0, device="cuda", dtype=torch.bfloat16)
-        sv.gdn_chunk(states, slots, *plain.on(r), o, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        chunk(sv, states, slots, plain.on(r), o, torch.tensor(cu, dtype=torch.int32, device="cuda"))
         assert sv.sv_last_device_error() == sv.SV_ERR_INVALID_ARG
         for b in range(3):
             if b == bad:
