@@ -18,9 +18,9 @@
 //    state.  Everything is held transposed, a row of the state (and of U, O) per lane
 //    of tensor memory: X = S K^T, R = b (v - e^G X), U = R T^T, S' = U~ K; each result is
 //    read by the threads that hold its rows and written back over itself as the
-//    next product's first operand.  Four threads share a row; S stays in their
-//    registers, in fp32.  One warp issues the products, one the copies (three
-//    blocks ahead at most).
+//    next product's first operand.  Two threads share a row; S stays in their
+//    registers, in fp32.  Four warps write the output meanwhile, one issues the
+//    products, one the copies (up to three blocks ahead).
 //  * Products take fp16 operands and fp32 sums.  S, R, U and T are fp32 values held
 //    as two fp16 parts (x = hi + lo, 2^-22 of x), so that a state stays an fp32 one; what
 //    only an output sees (S and U there, and P) is one part, 2^-11 beside the
@@ -69,6 +69,7 @@ __host__ __device__ constexpr int key_bytes() { return C * DK * 2; }  // a block
 struct ChunkParams {
   PoolParams p;
   uint8_t *keys, *heads;  // [blocks][Hk][2][key_bytes], [blocks][Hv][HEAD_BYTES]
+  float *most;            // [blocks][Hv][row_blocks][ROWS]: of each row, the largest |b' v'|
   int row_blocks;         // of ROWS rows a value head
   int stall;              // test aid: the first block never arrives
 };
@@ -106,7 +107,9 @@ struct PL {
   static constexpr int A = KQ + 128 * DK * 2;         // fp32 [64][AS], inverted in place
   static constexpr int GH = A + C * AS * 4;           // G in units of log 2, two parts [2][64]
   static constexpr int EX = GH + 2 * C * 4;           // exponents of the largest elements [128]
-  static constexpr int BAR = EX + 128 * 4;
+  static constexpr int BV = EX + 128 * 4;             // b' v' / v in bf16, twice a word [64]
+  static constexpr int RED = BV + C * 4;              // [4 warps][128] bf16
+  static constexpr int BAR = RED + 4 * 128 * 2;
   static constexpr int BYTES = BAR + 64;
 };
 
@@ -251,8 +254,10 @@ __global__ void __launch_bounds__(128, 4) prepare_kernel(const __grid_constant__
     __syncthreads();
     Scalars *S = reinterpret_cast<Scalars *>(out + 3 * PART);
     const float hi_i = gh[i], lo_i = gl[i], ga = ex2_approx(hi_i + lo_i);
+    uint32_t *bv16 = reinterpret_cast<uint32_t *>(smem + Y::BV);
     if (!isP) {
       const float bs = be * e_i;
+      bv16[i] = pack_bf16x2(fabsf(bs), fabsf(bs));
       S->bv[i] = bs;
       S->bx[i] = -(bs * e_i * ga);
       S->en[i] = ex2_approx((gh[C - 1] - hi_i) + (gl[C - 1] - lo_i));
@@ -298,6 +303,47 @@ __global__ void __launch_bounds__(128, 4) prepare_kernel(const __grid_constant__
       }
     }
     __syncthreads();
+    // ---- largest |b' v'| of each row of the state: eight tokens, eight columns a thread ----
+    for (int rb = 0; rb < CP.row_blocks; ++rb) {
+      const int col = rb * ROWS + (pt & 15) * 8, t0 = (pt >> 4) * 8, have = P.dv - col;
+      const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(P.v.ptr) + (r0 + t0) * P.v.token_stride + (long long)h * P.v.head_stride + col;
+      __nv_bfloat162 mx[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) mx[z] = __float2bfloat162_rn(0.f);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        uint32_t x[4] = {0u, 0u, 0u, 0u};
+        if (t0 + t < m && have >= 8) {
+          const uint4 y = *reinterpret_cast<const uint4 *>(src + t * P.v.token_stride);
+          x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+        } else if (t0 + t < m) {  // the last columns: nothing behind them is read
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            if (z < have) x[z >> 1] |= (uint32_t)__bfloat16_as_ushort(src[t * P.v.token_stride + z]) << (16 * (z & 1));
+        }
+        const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(bv16 + t0 + t);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const uint32_t y = x[z] & 0x7fff7fffu;
+          mx[z] = __hmax2(mx[z], __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), f));
+        }
+      }
+      uint32_t *red = reinterpret_cast<uint32_t *>(smem + Y::RED);
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        uint32_t y = *reinterpret_cast<uint32_t *>(&mx[z]);
+        const uint32_t w2 = __shfl_xor_sync(0xffffffffu, y, 16);
+        mx[z] = __hmax2(mx[z], *reinterpret_cast<const __nv_bfloat162 *>(&w2));
+        if (lane < 16) red[pw * 64 + lane * 4 + z] = *reinterpret_cast<uint32_t *>(&mx[z]);
+      }
+      __syncthreads();
+      const __nv_bfloat16 *r16 = reinterpret_cast<const __nv_bfloat16 *>(red) + pt;
+      float most = 0.f;
+#pragma unroll
+      for (int z = 0; z < 4; ++z) most = fmaxf(most, __bfloat162float(r16[z * 128]));
+      CP.most[(((size_t)w * P.Hv + h) * CP.row_blocks + rb) * ROWS + pt] = most;
+      __syncthreads();
+    }
     // ---- T = (I + A)^-1 in place: a 16 x 16 block a warp, a column a lane ----
     {
       const int o = pw * 16;
@@ -393,20 +439,26 @@ __global__ void __launch_bounds__(128, 4) prepare_kernel(const __grid_constant__
 }
 
 // -------------------------------------------------------------------- chain --
-constexpr int CHAIN_WARPS = 16, CHAIN_THREADS = (CHAIN_WARPS + 4) * 32, STAGES = 3;
+// Eight warps hold the rows of S, two threads a row; four write the output; one
+// fetches, one issues the products.
+constexpr int ROW_WARPS = 8, OUT_WARPS = 4, FETCH = ROW_WARPS + OUT_WARPS, ISSUE = FETCH + 1;
+constexpr int CHAIN_THREADS = (ROW_WARPS + OUT_WARPS + 4) * 32, STAGES = 3;
 
 template <int DK>
 struct CL {
   static constexpr int K = 0, Q = key_bytes<DK>(), T = 2 * key_bytes<DK>(), P = T + 2 * PART, V = P + PART;
-  static constexpr int S = V + C * ROWS * 2;            // scalars
-  static constexpr int STAGE = S + 2048;                // (stages 1024-byte aligned)
-  static constexpr int XCHG = 1024;                     // [2][4][ROWS]
-  static constexpr int RING = XCHG + 8 * ROWS * 4;
-  static constexpr int BYTES = RING + STAGES * STAGE - 512;
+  static constexpr int S = V + C * ROWS * 2;            // scalars, then the rows' largest |b' v'|
+  static constexpr int MOST = S + (int)sizeof(Scalars);
+  static constexpr int STAGE = MOST + ROWS * 4;         // (1024-byte aligned)
+  static constexpr int XCHG = 1024;                     // [2][2][ROWS]
+  static constexpr int SCALE = XCHG + 4 * ROWS * 4;     // [2][ROWS] what the rows' output is multiplied by
+  static constexpr int RING = SCALE + 2 * ROWS * 4;
+  static constexpr int BYTES = RING + STAGES * STAGE;
   static_assert(RING % 1024 == 0 && STAGE % 1024 == 0 && BYTES <= 227 * 1024, "shared memory");
   // tensor memory: S in two parts; X, then R over it (16 columns a k-step: hi, lo), then U
   // in one part; U, then U~ over it; S'; S Q^T; P U
   static constexpr uint32_t SH = 0, SL = DK / 2, X = 128, U = 192, D = 256, O1 = 384, O2 = 448;
+  static constexpr int STEPS = DK / 32;  // k-steps of S that are one thread's
 };
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -433,24 +485,26 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
   }
   uint64_t *full = reinterpret_cast<uint64_t *>(smem);     // [STAGES]
   uint64_t *empty = full + STAGES;                         // [STAGES]
-  uint64_t *s_ready = empty + STAGES;                      // [2] even and odd k-steps of S in place
+  uint64_t *s_ready = empty + STAGES;                      // [2] first and second half of each thread's k-steps of S
   uint64_t *x_done = s_ready + 2, *r_ready = x_done + 1, *u_done = r_ready + 1, *ut_ready = u_done + 1;
   uint64_t *d_done = ut_ready + 1, *o_done = d_done + 1, *o_free = o_done + 1, *idle = o_free + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(idle + 1);
   int *pick = reinterpret_cast<int *>(tmem_slot + 1);
+  float *scale = reinterpret_cast<float *>(smem + Y::SCALE);
   uint8_t *ring = smem + Y::RING;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&full[i], 1 + (i == 0 ? CP.stall : 0));
-      mbar_init(&empty[i], CHAIN_WARPS + 1);
+      mbar_init(&empty[i], ROW_WARPS + OUT_WARPS + 1);
     }
-    for (uint64_t *b : {s_ready, s_ready + 1, r_ready, ut_ready, o_free}) mbar_init(b, CHAIN_WARPS);
+    for (uint64_t *b : {s_ready, s_ready + 1, r_ready, ut_ready}) mbar_init(b, ROW_WARPS);
+    mbar_init(o_free, OUT_WARPS);
     for (uint64_t *b : {x_done, u_done, d_done, o_done, idle}) mbar_init(b, 1);
     fence_barrier_init();
     *pick = 0;
   }
-  if (warp == CHAIN_WARPS) {
+  if (warp == FETCH) {
     tc::tmem_alloc(tmem_slot, 512u);
     tc::tmem_relinquish();
   }
@@ -480,16 +534,24 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
   const int2 own = rows_of(P, b, report);
   const int slot = slot_of(P, b, report);
   const int n = (own.y + C - 1) / C;  // blocks
+  const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+  const int r = (warp & 3) * 32 + lane;  // row, of those that hold one
   bool ok = true;
+  // After a wait that ran out a warp goes on without waiting, reading or issuing.
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (ok) ok = spin_wait(bar, parity, P.err);
     ok = __all_sync(0xffffffffu, ok);
   };
+  auto arrive = [&](uint64_t *bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  auto scalars = [&](int st) { return reinterpret_cast<const Scalars *>(ring + st * Y::STAGE + Y::S); };
 
-  if (warp >= CHAIN_WARPS) {
-    // 640 threads start with 96 registers each: 512 * 112 + 128 * 32 is the same total
-    setmaxnreg_dec<32>();
-    if (warp == CHAIN_WARPS) {
+  // 512 threads start with 128 registers each: 256 * 184 + 256 * 72 is the same total
+  if (warp >= FETCH) {
+    setmaxnreg_dec<72>();
+    if (warp == FETCH) {
       // ---------------------------------------------------------- copies --
       if (lane == 0) {
         const int hk = h / (P.Hv / P.Hk), w0 = first_block(P, b, own.x);
@@ -499,11 +561,12 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
           if (c >= STAGES) ok = mbar_wait(&empty[st], (c / STAGES - 1) & 1, P.err);
           if (!ok) break;
           uint8_t *at = ring + st * Y::STAGE;
-          mbar_arrive_expect_tx(&full[st], 2 * key_bytes<DK>() + HEAD_BYTES + C * ROWS * 2);
+          mbar_arrive_expect_tx(&full[st], 2 * key_bytes<DK>() + HEAD_BYTES + ROWS * 4 + C * ROWS * 2);
+          const size_t place = (size_t)(w0 + c) * P.Hv + h;
           bulk_load(at + Y::K, CP.keys + ((size_t)(w0 + c) * P.Hk + hk) * 2 * key_bytes<DK>(), 2 * key_bytes<DK>(), &full[st]);
-          const uint8_t *src = CP.heads + ((size_t)(w0 + c) * P.Hv + h) * HEAD_BYTES;
-          bulk_load(at + Y::T, src, 3 * PART, &full[st]);
-          bulk_load(at + Y::S, src + 3 * PART, sizeof(Scalars), &full[st]);
+          bulk_load(at + Y::T, CP.heads + place * HEAD_BYTES, 3 * PART, &full[st]);
+          bulk_load(at + Y::S, CP.heads + place * HEAD_BYTES + 3 * PART, sizeof(Scalars), &full[st]);
+          bulk_load(at + Y::MOST, CP.most + place * CP.row_blocks * ROWS + i0, ROWS * 4, &full[st]);
           tensor_load_3d(at + Y::V, &mapV, i0, h, own.x + c * C, &full[st]);
         }
         if (!ok)  // no copy may outlive the CTA
@@ -511,7 +574,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
           }
       }
       __syncwarp();
-    } else if (warp == CHAIN_WARPS + 1) {
+    } else if (warp == ISSUE) {
       // -------------------------------------------------------- products --
       const bool leader = tc::elect_one();
       constexpr uint32_t IDN = tc::idesc_f16_f32(128, C, false), IDD = tc::idesc_f16_f32(128, DK, true);
@@ -528,11 +591,13 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
           tc::fence_after_sync();
           if (leader && ok) {
 #pragma unroll
-            for (int ks = x; ks < DK / 16; ks += 2)
+            for (int y = 0; y < Y::STEPS; ++y) {
+              const int ks = (y / (Y::STEPS / 2)) * Y::STEPS + x * (Y::STEPS / 2) + y % (Y::STEPS / 2);
 #pragma unroll
               for (int p = 0; p < 2; ++p)
                 tc::mma_bf16_ts(tb + Y::X, tb + (p ? Y::SL : Y::SH) + ks * 8, lo + (Y::K + (ks >> 2) * C * 128 + (ks & 3) * 32) / 16, row_hi,
-                                IDN, x > 0 || ks > 0 || p > 0);
+                                IDN, x > 0 || y > 0 || p > 0);
+            }
             if (x == 1) tc::commit(x_done);
           }
           __syncwarp();
@@ -583,151 +648,145 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       }
       __syncwarp();
     }
+  } else if (warp >= ROW_WARPS) {
+    // ---------------------------------------------------------- output --
+    setmaxnreg_dec<72>();
+    const long long step = P.o.token_stride;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.o.ptr) + own.x * step + (long long)h * P.o.head_stride + i0 + r;
+    for (int c = 0; c < n; ++c) {
+      const int st = c % STAGES;
+      const Scalars *Z = scalars(st);
+      // (o_done alone cannot run ahead of this warp; the rows' scale was written before the
+      // products that it reports were let go)
+      wait(o_done, c & 1);
+      tc::fence_after_sync();
+      const float f = scale[(c & 1) * ROWS + r];
+      const int some = i0 + r < P.dv && ok ? own.y - c * C : 0;
+#pragma unroll 1
+      for (int t = 0; t < C; t += 8) {
+        uint32_t a[8], d[8];
+        if (ok) {
+          tc::ld8(tb + Y::O1 + t + lane_off, a);
+          tc::ld8(tb + Y::O2 + t + lane_off, d);
+          tc::wait_ld();
+        }
+        if (t == C - 8) {
+          tc::fence_before_sync();
+          arrive(o_free);
+        }
+        float s1[8], s2[8];
+#pragma unroll
+        for (int z = 0; z < 8; z += 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(&Z->os1[t + z]), y = *reinterpret_cast<const float4 *>(&Z->os2[t + z]);
+          s1[z] = x.x, s1[z + 1] = x.y, s1[z + 2] = x.z, s1[z + 3] = x.w;
+          s2[z] = y.x, s2[z + 1] = y.y, s2[z + 2] = y.z, s2[z + 3] = y.w;
+        }
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          const float x = __uint_as_float(a[z]) * s1[z] + __uint_as_float(d[z]) * s2[z];
+          if (t + z < some) *out = __float2bfloat16_rn(x * f);
+          out += step;
+        }
+      }
+      arrive(&empty[st]);
+    }
   } else {
     // ------------------------------------------------------- rows of S --
-    setmaxnreg_inc<112>();
-    constexpr int SC = DK / 4;  // columns of S that are this thread's
-    const int q = warp >> 2, r = (warp & 3) * 32 + lane, i = i0 + r;
-    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const bool live = i < P.dv;
+    setmaxnreg_inc<184>();
+    constexpr int SC = DK / 2;  // columns of S that are this thread's
+    const int hf = warp >> 2;
+    const bool live = i0 + r < P.dv;
     float *xchg = reinterpret_cast<float *>(smem + Y::XCHG);
     uint32_t trades = 0;
-    // the largest of a value that the four threads of a row have
-    auto among = [&](float x) {
-      float *at = xchg + (trades & 1) * 4 * ROWS + r;
+    // the larger of a value that both threads of a row have
+    auto both = [&](float x) {
+      float *at = xchg + (trades & 1) * 2 * ROWS + r;
       ++trades;
-      at[q * ROWS] = x;
-      named_barrier(1 + (warp & 3), 128);
-      return fmaxf(fmaxf(at[0], at[ROWS]), fmaxf(at[2 * ROWS], at[3 * ROWS]));
+      at[hf * ROWS] = x;
+      named_barrier(1 + (warp & 3), 64);
+      return fmaxf(x, at[(hf ^ 1) * ROWS]);
     };
-    auto arrive = [&](uint64_t *bar) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    };
-    float *srow = P.states.ptr + (slot >= 0 ? slot : 0) * P.states.slot_stride + ((long long)h * P.dv + (live ? i : 0)) * DK + q * SC;
+    float *srow = P.states.ptr + (slot >= 0 ? slot : 0) * P.states.slot_stride + ((long long)h * P.dv + (live ? i0 + r : 0)) * DK + hf * SC;
     const bool kept = slot >= 0 && live && n > 0;
     f2 S[SC / 2];
+    float m = 0.f, sc = 1.f;
 #pragma unroll
     for (int e = 0; e < SC / 2; e += 2) {
       ulonglong2 x = make_ulonglong2(0, 0);
       if (kept) x = *reinterpret_cast<const ulonglong2 *>(srow + 2 * e);
       S[e] = x.x, S[e + 1] = x.y;
+      const float2 y = unpack2(x.x), z = unpack2(x.y);
+      m = fmaxf(m, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(z.x), fabsf(z.y))));
     }
-    auto row_max = [&]() {
+    // scale of a row: 2^-k with at most 1 behind it
+    auto scale_of = [&](float most) { return pow2_field(253 - imin(imax(__float_as_int(most) >> 23, 27), 226)); };
+    auto most_of = [&](int st) { return reinterpret_cast<const float *>(ring + st * Y::STAGE + Y::MOST)[r]; };
+    // S as the next product's operand, a k-step at a time; the largest |S|
+    auto put_state = [&](float by) {
+      const f2 by2 = pack2(by, by);
       float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-      for (int e = 0; e < SC / 2; ++e) {
-        const float2 x = unpack2(S[e]);
-        m0 = fmaxf(m0, fabsf(x.x)), m1 = fmaxf(m1, fabsf(x.y));
+      for (int g = 0; g < Y::STEPS; ++g) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          split2(mul2(S[8 * g + e], by2), hi[e], lo[e]);
+          const float2 x = unpack2(S[8 * g + e]);
+          m0 = fmaxf(m0, fabsf(x.x)), m1 = fmaxf(m1, fabsf(x.y));
+        }
+        tc::st8(tb + Y::SH + hf * (SC / 2) + 8 * g + lane_off, hi);
+        tc::st8(tb + Y::SL + hf * (SC / 2) + 8 * g + lane_off, lo);
+        if ((g + 1) % (Y::STEPS / 2) == 0) {
+          tc::wait_st();
+          tc::fence_before_sync();
+          arrive(&s_ready[g / (Y::STEPS / 2)]);
+        }
       }
       return fmaxf(m0, m1);
     };
-    auto scalars = [&](int c) { return reinterpret_cast<const Scalars *>(ring + (c % STAGES) * Y::STAGE + Y::S); };
-    auto values = [&](int c) { return reinterpret_cast<const uint16_t *>(ring + (c % STAGES) * Y::STAGE + Y::V) + q * 16 * ROWS + r; };
-    // values of this thread's tokens 2t, 2t + 1 (zeros past the sequence's end)
-    auto pair = [&](const uint16_t *v, int t, int some) {
-      const uint32_t x = 2 * t < some ? v[2 * t * ROWS] : 0u, y = 2 * t + 1 < some ? v[(2 * t + 1) * ROWS] : 0u;
-      return x | y << 16;
-    };
-    // largest |b' v'| of them
-    auto v_max = [&](int c) {
-      const uint16_t *v = values(c);
-      const Scalars *Z = scalars(c);
-      const int some = own.y - c * C - q * 16;
-      float m = 0.f;
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const uint32_t x = pair(v, t, some);
-        const float2 b2 = *reinterpret_cast<const float2 *>(&Z->bv[q * 16 + 2 * t]);
-        m = fmaxf(m, fmaxf(fabsf(bf16lo(x) * b2.x), fabsf(bf16hi(x) * b2.y)));
-      }
-      return m;
-    };
-    // scale of a row: 2^-k with at most 1 behind it
-    auto scale_of = [&](float most) { return pow2_field(253 - imin(imax(__float_as_int(most) >> 23, 27), 226)); };
-    // S as the next product's operand, 16 columns (a k-step) at a time
-    auto put_state = [&](float sc) {
-      const f2 sc2 = pack2(sc, sc);
-      constexpr int STEPS = SC / 16;
-#pragma unroll
-      for (int g = 0; g < STEPS; ++g) {
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) split2(mul2(S[8 * g + e], sc2), hi[e], lo[e]);
-        tc::st8(tb + Y::SH + q * (SC / 2) + 8 * g + lane_off, hi);
-        tc::st8(tb + Y::SL + q * (SC / 2) + 8 * g + lane_off, lo);
-        tc::wait_st();
-        tc::fence_before_sync();
-        if (STEPS == 2) arrive(&s_ready[g]);
-      }
-      if (STEPS == 1) {  // (one k-step a thread: all are there at once)
-        arrive(&s_ready[0]);
-        arrive(&s_ready[1]);
-      }
-    };
-    float m = row_max(), sc = 1.f;
     if (n > 0) {
       wait(&full[0], 0);
-      sc = scale_of(among(fmaxf(m * 0.015625f, 0.125f * v_max(0))));
+      sc = scale_of(both(fmaxf(m * 0.015625f, 0.125f * most_of(0))));
       put_state(sc);
     }
-    // O of block c, whose rows were scaled by 1 / isc
-    auto put_out = [&](int c, float isc) {
-      const Scalars *Z = scalars(c);
-      wait(o_done, c & 1);
-      tc::fence_after_sync();
-      const int t0 = c * C + q * 16, some = live && ok ? own.y - t0 : 0;
-      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.o.ptr) + (own.x + (long long)t0) * P.o.token_stride + (long long)h * P.o.head_stride + i;
-      const long long step = P.o.token_stride;
-#pragma unroll 1
-      for (int t = 0; t < 16; t += 4) {  // (four at a time: registers)
-        uint32_t a[4], d[4];
-        if (ok) {
-          tc::ld4(tb + Y::O1 + q * 16 + t + lane_off, a);
-          tc::ld4(tb + Y::O2 + q * 16 + t + lane_off, d);
-          tc::wait_ld();
-        }
-        const float4 s1 = *reinterpret_cast<const float4 *>(&Z->os1[q * 16 + t]), s2 = *reinterpret_cast<const float4 *>(&Z->os2[q * 16 + t]);
-        const float x[4] = {__uint_as_float(a[0]) * s1.x + __uint_as_float(d[0]) * s2.x, __uint_as_float(a[1]) * s1.y + __uint_as_float(d[1]) * s2.y,
-                            __uint_as_float(a[2]) * s1.z + __uint_as_float(d[2]) * s2.z, __uint_as_float(a[3]) * s1.w + __uint_as_float(d[3]) * s2.w};
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          if (t + z < some) *out = __float2bfloat16_rn(x[z] * isc);
-          out += step;
-        }
-      }
-      tc::fence_before_sync();
-      arrive(o_free);
-      arrive(&empty[c % STAGES]);
-    };
-    float isc_before = 1.f;
+    int st = 0;
+    uint32_t phase = 0;  // of the stage after this one
     for (int c = 0; c < n; ++c) {
       const uint32_t par = c & 1;
-      const Scalars *Z = scalars(c);
-      const f2 sc2 = pack2(sc, sc);
-      if (c > 0) put_out(c - 1, isc_before);
-      // R = b (v - e^G X)
+      const Scalars *Z = scalars(st);
+      const float isc = 1.f / sc;  // (exact)
+      if (hf == 0) scale[par * ROWS + r] = isc;
+      // R = b (v - e^G X), a k-step (16 tokens) at a time
       {
-        const int some = own.y - c * C - q * 16;
-        const uint16_t *v = values(c);
-        uint32_t vb[8];
+        const int some = own.y - c * C - hf * 32;
+        const uint16_t *v = reinterpret_cast<const uint16_t *>(ring + st * Y::STAGE + Y::V) + hf * 32 * ROWS + r;
+        const f2 sc2 = pack2(sc, sc);
+        uint32_t vb[16];  // values of two tokens each, zeros past the sequence's end
 #pragma unroll
-        for (int t = 0; t < 8; ++t) vb[t] = pair(v, t, some);
+        for (int t = 0; t < 16; ++t) vb[t] = v[2 * t * ROWS] | (uint32_t)v[(2 * t + 1) * ROWS] << 16;
+        if (some < 32) {
+#pragma unroll
+          for (int t = 0; t < 16; ++t) vb[t] = 2 * t + 1 < some ? vb[t] : 2 * t < some ? vb[t] & 0xffffu : 0u;
+        }
         wait(x_done, par);
         tc::fence_after_sync();
-        uint32_t raw[16], hi[8], lo[8];
-        if (ok) {
-          tc::ld16(tb + Y::X + q * 16 + lane_off, raw);
-          tc::wait_ld();
-        }
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const f2 bx = *reinterpret_cast<const f2 *>(&Z->bx[q * 16 + 2 * t]), bv = *reinterpret_cast<const f2 *>(&Z->bv[q * 16 + 2 * t]);
-          const f2 w = mul2(mul2(pack2(bf16lo(vb[t]), bf16hi(vb[t])), sc2), bv);
-          split2(fma2(bx, pack2(__uint_as_float(raw[2 * t]), __uint_as_float(raw[2 * t + 1])), w), hi[t], lo[t]);
+        for (int g = 0; g < 2; ++g) {
+          uint32_t raw[16], hi[8], lo[8];
+          if (ok) {
+            tc::ld16(tb + Y::X + hf * 32 + 16 * g + lane_off, raw);
+            tc::wait_ld();
+          }
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const int at = hf * 32 + 16 * g + 2 * t;
+            const f2 bx = *reinterpret_cast<const f2 *>(&Z->bx[at]), bv = *reinterpret_cast<const f2 *>(&Z->bv[at]);
+            const f2 w = mul2(mul2(pack2(bf16lo(vb[8 * g + t]), bf16hi(vb[8 * g + t])), sc2), bv);
+            split2(fma2(bx, pack2(__uint_as_float(raw[2 * t]), __uint_as_float(raw[2 * t + 1])), w), hi[t], lo[t]);
+          }
+          tc::st8(tb + Y::X + hf * 32 + 16 * g + lane_off, hi);
+          tc::st8(tb + Y::X + hf * 32 + 16 * g + 8 + lane_off, lo);
         }
-        tc::st8(tb + Y::X + q * 16 + lane_off, hi);
-        tc::st8(tb + Y::X + q * 16 + 8 + lane_off, lo);
         tc::wait_st();
         tc::fence_before_sync();
         arrive(r_ready);
@@ -736,34 +795,40 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       {
         wait(u_done, par);
         tc::fence_after_sync();
-        uint32_t raw[16], hi[8], lo[8], u[8];
-        if (ok) {
-          tc::ld16(tb + Y::U + q * 16 + lane_off, raw);
-          tc::wait_ld();
-        }
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const float a = __uint_as_float(raw[2 * t]), d = __uint_as_float(raw[2 * t + 1]);
-          u[t] = pack_f16x2(a, d);
-          const f2 x = mul2(pack2(a, d), *reinterpret_cast<const f2 *>(&Z->en[q * 16 + 2 * t]));
-          const float2 y = unpack2(x);
-          um = fmaxf(um, fmaxf(fabsf(y.x), fabsf(y.y)));
-          split2(x, hi[t], lo[t]);
+        for (int g = 0; g < 2; ++g) {
+          uint32_t raw[16], hi[8], lo[8], u[8];
+          if (ok) {
+            tc::ld16(tb + Y::U + hf * 32 + 16 * g + lane_off, raw);
+            tc::wait_ld();
+          }
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const float a = __uint_as_float(raw[2 * t]), d = __uint_as_float(raw[2 * t + 1]);
+            u[t] = pack_f16x2(a, d);
+            const f2 x = mul2(pack2(a, d), *reinterpret_cast<const f2 *>(&Z->en[hf * 32 + 16 * g + 2 * t]));
+            const float2 y = unpack2(x);
+            um = fmaxf(um, fmaxf(fabsf(y.x), fabsf(y.y)));
+            split2(x, hi[t], lo[t]);
+          }
+          tc::st8(tb + Y::U + hf * 32 + 16 * g + lane_off, hi);
+          tc::st8(tb + Y::U + hf * 32 + 16 * g + 8 + lane_off, lo);
+          tc::st8(tb + Y::X + hf * 32 + 16 * g + lane_off, u);
         }
-        tc::st8(tb + Y::U + q * 16 + lane_off, hi);
-        tc::st8(tb + Y::U + q * 16 + 8 + lane_off, lo);
-        tc::st8(tb + Y::X + q * 16 + lane_off, u);
         tc::wait_st();
         tc::fence_before_sync();
         arrive(ut_ready);
       }
-      const float gc = Z->gc, isc = 1.f / sc;  // (exact)
+      const float gc = Z->gc;
+      arrive(&empty[st]);
+      st = st + 1 == STAGES ? 0 : st + 1;
+      phase ^= st == 0;
       float sc_next = sc;
       if (c + 1 < n) {
-        wait(&full[(c + 1) % STAGES], ((c + 1) / STAGES) & 1);
+        wait(&full[st], phase);
         // elements of k' are below 2^-3, 64 tokens: |S'| <= 8 |U~|; twice, as the largest of
-        // the sums' terms may be different threads'
-        sc_next = scale_of(among(fmaxf((gc * m + 8.f * um * isc) * 0.03125f, 0.125f * v_max(c + 1))));
+        // the sum's terms may be different threads'
+        sc_next = scale_of(both(fmaxf((gc * m + 8.f * um * isc) * 0.03125f, 0.125f * most_of(st))));
       }
       const f2 gc2 = pack2(gc, gc), isc2 = pack2(isc, isc);
 #pragma unroll
@@ -774,21 +839,16 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       for (int g = 0; g < SC / 16; ++g) {
         uint32_t raw[16];
         if (ok) {
-          tc::ld16(tb + Y::D + q * SC + 16 * g + lane_off, raw);
+          tc::ld16(tb + Y::D + hf * SC + 16 * g + lane_off, raw);
           tc::wait_ld();
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           S[8 * g + e] = fma2(pack2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), isc2, S[8 * g + e]);
       }
-      if (c + 1 < n) {
-        put_state(sc_next);
-        m = row_max();
-      }
-      isc_before = isc;
+      if (c + 1 < n) m = put_state(sc_next);
       sc = sc_next;
     }
-    if (n > 0) put_out(n - 1, isc_before);
     if (kept && ok) {
 #pragma unroll
       for (int e = 0; e < SC / 2; e += 2) *reinterpret_cast<ulonglong2 *>(srow + 2 * e) = make_ulonglong2(S[e], S[e + 1]);
@@ -796,7 +856,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == CHAIN_WARPS) {
+  if (warp == FETCH) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tb, 512u);
   }
@@ -804,6 +864,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
 
 // Blocks that the workspace has places for.
 inline long long places(int B, int T) { return (long long)T / C + B; }
+inline size_t padded(int dv) { return ((size_t)dv + ROWS - 1) / ROWS * ROWS; }
 
 template <int DK>
 sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
@@ -835,9 +896,8 @@ using namespace sv;
 extern "C" {
 
 size_t gdn_chunk_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv) {
-  (void)dv;
-  if (B < 1 || T < 1 || Hk < 1 || Hv < 1 || (dk != 64 && dk != 128)) return 0;
-  const size_t per = (size_t)Hk * 4 * gdn::C * dk + (size_t)Hv * gdn::HEAD_BYTES;
+  if (B < 1 || T < 1 || Hk < 1 || Hv < 1 || dv < 1 || (dk != 64 && dk != 128)) return 0;
+  const size_t per = (size_t)Hk * 4 * gdn::C * dk + (size_t)Hv * (gdn::HEAD_BYTES + gdn::padded(dv) * 4);
   return (size_t)gdn::places(B, T) * per;
 }
 
@@ -869,7 +929,8 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   P.commit = 1;
   CP.keys = static_cast<uint8_t *>(workspace);
   CP.heads = CP.keys + (size_t)gdn::places(B, T) * Hk * 4 * gdn::C * dk;
-  CP.row_blocks = (dv + gdn::ROWS - 1) / gdn::ROWS;
+  CP.most = reinterpret_cast<float *>(CP.heads + (size_t)gdn::places(B, T) * Hv * gdn::HEAD_BYTES);
+  CP.row_blocks = (int)(gdn::padded(dv) / gdn::ROWS);
   CP.stall = launch_flags() & SV_LAUNCH_TEST_STALL_COPY ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return dk == 64 ? gdn::run_chunks<64>(CP, s) : gdn::run_chunks<128>(CP, s);
