@@ -310,22 +310,27 @@ __global__ void __launch_bounds__(128, 4) prepare_kernel(const __grid_constant__
       __nv_bfloat162 mx[4];
 #pragma unroll
       for (int z = 0; z < 4; ++z) mx[z] = __float2bfloat162_rn(0.f);
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        uint32_t x[4] = {0u, 0u, 0u, 0u};
-        if (t0 + t < m && have >= 8) {
-          const uint4 y = *reinterpret_cast<const uint4 *>(src + t * P.v.token_stride);
-          x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
-        } else if (t0 + t < m) {  // the last columns: nothing behind them is read
-#pragma unroll
-          for (int z = 0; z < 8; ++z)
-            if (z < have) x[z >> 1] |= (uint32_t)__bfloat16_as_ushort(src[t * P.v.token_stride + z]) << (16 * (z & 1));
-        }
+      auto take = [&](int t, uint4 y) {
         const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(bv16 + t0 + t);
+        const uint32_t x[4] = {y.x & 0x7fff7fffu, y.y & 0x7fff7fffu, y.z & 0x7fff7fffu, y.w & 0x7fff7fffu};
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const uint32_t y = x[z] & 0x7fff7fffu;
-          mx[z] = __hmax2(mx[z], __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), f));
+        for (int z = 0; z < 4; ++z) mx[z] = __hmax2(mx[z], __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x[z]), f));
+      };
+      if (have >= 8) {
+        uint4 y[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          y[t] = t0 + t < m ? *reinterpret_cast<const uint4 *>(src + t * P.v.token_stride) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) take(t, y[t]);
+      } else if (have > 0) {  // the last columns: nothing behind them is read
+#pragma unroll 1
+        for (int t = 0; t < 8 && t0 + t < m; ++t) {
+          uint32_t x[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int z = 0; z < 7; ++z)
+            if (z < have) x[z >> 1] |= (uint32_t)__bfloat16_as_ushort(src[t * P.v.token_stride + z]) << (16 * (z & 1));
+          take(t, make_uint4(x[0], x[1], x[2], x[3]));
         }
       }
       uint32_t *red = reinterpret_cast<uint32_t *>(smem + Y::RED);
@@ -537,7 +542,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const int r = (warp & 3) * 32 + lane;  // row, of those that hold one
   bool ok = true;
-  // After a wait that ran out a warp goes on without waiting, reading or issuing.
+  // After a wait that ran out a warp goes on without waiting, issuing or storing (what it
+  // reads of tensor memory then has no meaning; loads under a condition cost registers).
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (ok) ok = spin_wait(bar, parity, P.err);
     ok = __all_sync(0xffffffffu, ok);
@@ -770,13 +776,14 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
         }
         wait(x_done, par);
         tc::fence_after_sync();
+        uint32_t raw2[2][16];
+        tc::ld16(tb + Y::X + hf * 32 + lane_off, raw2[0]);
+        tc::ld16(tb + Y::X + hf * 32 + 16 + lane_off, raw2[1]);
+        tc::wait_ld();
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          uint32_t raw[16], hi[8], lo[8];
-          if (ok) {
-            tc::ld16(tb + Y::X + hf * 32 + 16 * g + lane_off, raw);
-            tc::wait_ld();
-          }
+          uint32_t hi[8], lo[8];
+          const uint32_t (&raw)[16] = raw2[g];
 #pragma unroll
           for (int t = 0; t < 8; ++t) {
             const int at = hf * 32 + 16 * g + 2 * t;
@@ -795,13 +802,14 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       {
         wait(u_done, par);
         tc::fence_after_sync();
+        uint32_t raw2[2][16];
+        tc::ld16(tb + Y::U + hf * 32 + lane_off, raw2[0]);
+        tc::ld16(tb + Y::U + hf * 32 + 16 + lane_off, raw2[1]);
+        tc::wait_ld();
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          uint32_t raw[16], hi[8], lo[8], u[8];
-          if (ok) {
-            tc::ld16(tb + Y::U + hf * 32 + 16 * g + lane_off, raw);
-            tc::wait_ld();
-          }
+          uint32_t hi[8], lo[8], u[8];
+          const uint32_t (&raw)[16] = raw2[g];
 #pragma unroll
           for (int t = 0; t < 8; ++t) {
             const float a = __uint_as_float(raw[2 * t]), d = __uint_as_float(raw[2 * t + 1]);
@@ -835,17 +843,15 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       for (int e = 0; e < SC / 2; ++e) S[e] = mul2(S[e], gc2);
       wait(d_done, par);
       tc::fence_after_sync();
+      uint32_t raw[SC / 16][16];
 #pragma unroll
-      for (int g = 0; g < SC / 16; ++g) {
-        uint32_t raw[16];
-        if (ok) {
-          tc::ld16(tb + Y::D + hf * SC + 16 * g + lane_off, raw);
-          tc::wait_ld();
-        }
+      for (int g = 0; g < SC / 16; ++g) tc::ld16(tb + Y::D + hf * SC + 16 * g + lane_off, raw[g]);
+      tc::wait_ld();
+#pragma unroll
+      for (int g = 0; g < SC / 16; ++g)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          S[8 * g + e] = fma2(pack2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), isc2, S[8 * g + e]);
-      }
+          S[8 * g + e] = fma2(pack2(__uint_as_float(raw[g][2 * e]), __uint_as_float(raw[g][2 * e + 1])), isc2, S[8 * g + e]);
       if (c + 1 < n) m = put_state(sc_next);
       sc = sc_next;
     }
