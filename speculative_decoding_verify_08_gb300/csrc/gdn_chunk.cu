@@ -33,8 +33,8 @@
 //    at most |b' v'| |k'| to a row's norm, and |k'| is from 2^-4 to sqrt(2), so that u' <=
 //    32 |S| + |b' v'|: |S| <= 2^6 and |b' v'| <= 2^3 at a block's start keep all of it
 //    below 2^16, and the parts are off by 2^-27 of the larger of the two at most.
-//  * The inverse: four 16 x 16 blocks by forward substitution, then joined twice by
-//    -T22 (A21 T11), in fp32 on the CUDA cores, which is as stable as the substitution.
+//  * The inverse: four 16 x 16 blocks by forward substitution in fp32, then joined twice
+//    by -T22 (A21 T11), which is as stable as the substitution.
 //  * G is summed in two fp32 parts and so are its differences: a gate that closes
 //    (g = -1000) leaves the decays behind it exact.
 #include "gdn_pool.cuh"
@@ -104,8 +104,9 @@ __device__ __forceinline__ float2 add_parts(float2 x, float2 y) {
 template <int DK>
 struct PL {
   static constexpr int KQ = 0;                        // [DK/64][128 rows][128 B]: keys in rows 0..63, queries behind
-  static constexpr int A = KQ + 128 * DK * 2;         // fp32 [64][AS], inverted in place
-  static constexpr int GH = A + C * AS * 4;           // G in units of log 2, two parts [2][64]
+  static constexpr int A = KQ;                        // then: fp32 [64][AS], inverted in place
+  static constexpr int FIRST = 128 * DK * 2 > C * AS * 4 ? 128 * DK * 2 : (C * AS * 4 + 1023) / 1024 * 1024;
+  static constexpr int GH = FIRST;                    // G in units of log 2, two parts [2][64]
   static constexpr int EX = GH + 2 * C * 4;           // exponents of the largest elements [128]
   static constexpr int BV = EX + 128 * 4;             // b' v' / v in bf16, twice a word [64]
   static constexpr int RED = BV + C * 4;              // [4 warps][128] bf16
@@ -113,8 +114,36 @@ struct PL {
   static constexpr int BYTES = BAR + 64;
 };
 
+// Operands of a warp's 16 x 8 x 16 product out of fp32 matrices of row stride AS, in two parts.
+template <int N>
+struct Parts {
+  uint32_t hi[N], lo[N];
+};
+__device__ __forceinline__ void left_operand(Parts<4> &p, const float *a, int lane) {
+#pragma unroll
+  for (int z = 0; z < 4; ++z)
+    split2(*reinterpret_cast<const f2 *>(a + ((lane >> 2) + 8 * (z & 1)) * AS + 2 * (lane & 3) + 8 * (z >> 1)), p.hi[z], p.lo[z]);
+}
+__device__ __forceinline__ void right_operand(Parts<2> &p, const float *a, int lane) {
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    const float *x = a + (2 * (lane & 3) + 8 * z) * AS + (lane >> 2);
+    split2(pack2(x[0], x[AS]), p.hi[z], p.lo[z]);
+  }
+}
+__device__ __forceinline__ void multiply(float (&d)[4], const Parts<4> &l, const Parts<2> &r) {
+  mma_f16_16816(d, l.lo[0], l.lo[1], l.lo[2], l.lo[3], r.hi[0], r.hi[1]);
+  mma_f16_16816(d, l.hi[0], l.hi[1], l.hi[2], l.hi[3], r.lo[0], r.lo[1]);
+  mma_f16_16816(d, l.hi[0], l.hi[1], l.hi[2], l.hi[3], r.hi[0], r.hi[1]);
+}
+__device__ __forceinline__ void put_tile(float *a, const float (&d)[4], bool minus, int lane) {
+  float *x = a + (lane >> 2) * AS + 2 * (lane & 3);
+  *reinterpret_cast<float2 *>(x) = minus ? make_float2(-d[0], -d[1]) : make_float2(d[0], d[1]);
+  *reinterpret_cast<float2 *>(x + 8 * AS) = minus ? make_float2(-d[2], -d[3]) : make_float2(d[2], d[3]);
+}
+
 template <int DK>
-__global__ void __launch_bounds__(128, 4) prepare_kernel(const __grid_constant__ ChunkParams CP) {
+__global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__ ChunkParams CP) {
   using Y = PL<DK>;
   const PoolParams &P = CP.p;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -130,7 +159,7 @@ __global__ void __launch_bounds__(128, 4) prepare_kernel(const __grid_constant__
   const int pt = threadIdx.x, pw = pt >> 5, lane = pt & 31;
   pdl_wait();
   // ---- the block: sequence and first row ----
-  const int w = blockIdx.x, hk = blockIdx.y;
+  const int w = blockIdx.x / P.Hk, hk = blockIdx.x - w * P.Hk;  // (key heads of the same tokens side by side)
   int lo = 0, hi = P.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -141,6 +170,15 @@ __global__ void __launch_bounds__(128, 4) prepare_kernel(const __grid_constant__
   if (c < 0 || c * C >= own.y) return;
   const long long r0 = own.x + (long long)c * C;
   const int m = imin(C, own.y - c * C);
+  const int group = P.Hv / P.Hk;
+  {  // the values of its heads are read below: on their way to L2 from now on
+    const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(P.v.ptr) + (long long)hk * group * P.v.head_stride;
+    const int lines = (P.dv * 2 + 127) / 128;
+    for (int e = pt; e < m * group * lines; e += 128) {
+      const int t = e % m, x = e / m, hh = x / lines;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(vp + (r0 + t) * P.v.token_stride + (long long)hh * P.v.head_stride + (x - hh * lines) * 64));
+    }
+  }
   if (pt == 0) {
     mbar_init(done, 1);
     fence_barrier_init();
@@ -211,25 +249,18 @@ __global__ void __launch_bounds__(128, 4) prepare_kernel(const __grid_constant__
     tc::commit(done);
   }
   __syncwarp();
-  bool ok = mbar_wait(done, 0, P.err);
-  ok = __all_sync(0xffffffffu, ok);
+  mbar_wait(done, 0, P.err);
+  __syncwarp();
   tc::fence_after_sync();
-  uint32_t raw[2][32];
-  if (ok) {
-    tc::ld32(tb + ((uint32_t)(pw * 32) << 16), raw[0]);
-    tc::ld32(tb + 32 + ((uint32_t)(pw * 32) << 16), raw[1]);
-    tc::wait_ld();
-  }
   const bool isP = pw >= 2;
   const int i = (pw & 1) * 32 + lane;  // this thread's row of A, or of P
   const float e_i = pow2_field(imin(ex[i] + 4, 254));  // 2^e of its key
-  const int group = P.Hv / P.Hk;
   for (int e = 0; e < group; ++e) {
     const int h = hk * group + e;
     uint8_t *out = CP.heads + ((size_t)w * P.Hv + h) * HEAD_BYTES;
     float be = 0.f;
     if (i < m) be = P.b[(r0 + i) * P.Hv + h];
-    if (e > 0) __syncthreads();  // A and G of the head before have been read
+    __syncthreads();  // A and G of the head before (the products' operands) have been read
     if (pw == 0) {  // running sums of the gates, in units of log 2, two tokens a lane
       auto gate = [&](int t) {
         float g = t < m ? P.g[(r0 + t) * P.Hv + h] : 0.f;
@@ -275,6 +306,9 @@ __global__ void __launch_bounds__(128, 4) prepare_kernel(const __grid_constant__
 #pragma unroll
       for (int c0 = 0; c0 < 2; ++c0) {
         const bool any = c0 == 0 || (pw & 1);  // columns 32.. of rows 0..31 are zero
+        uint32_t raw[32];  // (from tensor memory for every head: kept, they cost two blocks an SM)
+        tc::ld32(tb + c0 * 32 + ((uint32_t)(pw * 32) << 16), raw);
+        tc::wait_ld();
 #pragma unroll
         for (int x = 0; x < 32; x += 8) {
           const int j = c0 * 32 + x;
@@ -284,7 +318,7 @@ __global__ void __launch_bounds__(128, 4) prepare_kernel(const __grid_constant__
             for (int z = 0; z < 4; ++z) {
               const f2 hj = *reinterpret_cast<const f2 *>(gh + j + 2 * z), lj = *reinterpret_cast<const f2 *>(gl + j + 2 * z);
               const float2 d = unpack2(add2(fma2(hj, neg, hi2), fma2(lj, neg, lo2)));
-              const f2 kk = pack2(__uint_as_float(raw[c0][x + 2 * z]), __uint_as_float(raw[c0][x + 2 * z + 1]));
+              const f2 kk = pack2(__uint_as_float(raw[x + 2 * z]), __uint_as_float(raw[x + 2 * z + 1]));
               const float2 t = unpack2(mul2(mul2(kk, rowf), pack2(ex2_approx(d.x), ex2_approx(d.y))));
               y[z] = pack2(j + 2 * z <= last ? t.x : 0.f, j + 2 * z + 1 <= last ? t.y : 0.f);
             }
@@ -373,51 +407,44 @@ __global__ void __launch_bounds__(128, 4) prepare_kernel(const __grid_constant__
       }
     }
     __syncthreads();
-    // joined: T21 = -T22 (A21 T11), 16 rows and columns of two pairs, then 32 of one
+    // joined: T21 = -T22 (A21 T11), 16 rows and columns of two pairs, then 32 of one; the
+    // products in two fp16 parts too (on the CUDA cores their operands' way through shared
+    // memory took longer than all else here)
     {
-      // one row, four columns a thread: pair pt / 64
-      const int o = (pt >> 6) * 32, r = o + 16 + ((pt & 63) >> 2), j = o + (pt & 3) * 4;
+      const int o = (pw >> 1) * 32, n0 = o + (pw & 1) * 8;  // pair, eight columns
 #pragma unroll
       for (int pass = 0; pass < 2; ++pass) {
-        f2 w0 = 0, w1 = 0;
-        const int k0 = o + 16 * pass;
-#pragma unroll
-        for (int k = 0; k < 16; k += 4) {
-          const float4 a = *reinterpret_cast<const float4 *>(A + r * AS + k0 + k);
-          const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const ulonglong2 t = *reinterpret_cast<const ulonglong2 *>(A + (k0 + k + z) * AS + j);
-            const float x = pass ? -av[z] : av[z];
-            w0 = fma2(pack2(x, x), t.x, w0), w1 = fma2(pack2(x, x), t.y, w1);
-          }
-        }
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        const float *left = A + (o + 16) * AS + o + 16 * pass, *right = A + (o + 16 * pass) * AS + n0;
+        Parts<4> l;
+        Parts<2> r;
+        left_operand(l, left, lane);
+        right_operand(r, right, lane);
+        multiply(d, l, r);
         __syncthreads();
-        *reinterpret_cast<ulonglong2 *>(A + r * AS + j) = make_ulonglong2(w0, w1);
+        put_tile(A + (o + 16) * AS + n0, d, pass, lane);
         __syncthreads();
       }
     }
     {
-      const int r = 32 + (pt >> 3) * 2, j = (pt & 7) * 4;  // two rows, four columns
+      const int m0 = 32 + (pw & 1) * 16, n0 = (pw >> 1) * 16;  // 16 rows, 16 columns
 #pragma unroll
       for (int pass = 0; pass < 2; ++pass) {
-        f2 s[2][2] = {{0, 0}, {0, 0}};
-        const int k0 = 32 * pass;
+        float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          const float4 a = *reinterpret_cast<const float4 *>(A + r * AS + k0 + k), d = *reinterpret_cast<const float4 *>(A + (r + 1) * AS + k0 + k);
-          const float av[4] = {a.x, a.y, a.z, a.w}, dv_[4] = {d.x, d.y, d.z, d.w};
+        for (int k = 32 * pass; k < 32 * pass + 32; k += 16) {
+          Parts<4> l;
+          left_operand(l, A + m0 * AS + k, lane);
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const ulonglong2 t = *reinterpret_cast<const ulonglong2 *>(A + (k0 + k + z) * AS + j);
-            const float p = pass ? -av[z] : av[z], q = pass ? -dv_[z] : dv_[z];
-            s[0][0] = fma2(pack2(p, p), t.x, s[0][0]), s[0][1] = fma2(pack2(p, p), t.y, s[0][1]);
-            s[1][0] = fma2(pack2(q, q), t.x, s[1][0]), s[1][1] = fma2(pack2(q, q), t.y, s[1][1]);
+          for (int z = 0; z < 2; ++z) {
+            Parts<2> r;
+            right_operand(r, A + k * AS + n0 + 8 * z, lane);
+            multiply(d[z], l, r);
           }
         }
         __syncthreads();
-        *reinterpret_cast<ulonglong2 *>(A + r * AS + j) = make_ulonglong2(s[0][0], s[0][1]);
-        *reinterpret_cast<ulonglong2 *>(A + (r + 1) * AS + j) = make_ulonglong2(s[1][0], s[1][1]);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) put_tile(A + m0 * AS + n0 + 8 * z, d[z], pass, lane);
         __syncthreads();
       }
     }
@@ -668,30 +695,38 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       tc::fence_after_sync();
       const float f = scale[(c & 1) * ROWS + r];
       const int some = i0 + r < P.dv && ok ? own.y - c * C : 0;
-#pragma unroll 1
+      // all of it is read before any is stored: the next block's products wait for it
+      uint32_t y[C / 2];
+#pragma unroll
       for (int t = 0; t < C; t += 8) {
         uint32_t a[8], d[8];
-        if (ok) {
-          tc::ld8(tb + Y::O1 + t + lane_off, a);
-          tc::ld8(tb + Y::O2 + t + lane_off, d);
-          tc::wait_ld();
-        }
-        if (t == C - 8) {
-          tc::fence_before_sync();
-          arrive(o_free);
-        }
-        float s1[8], s2[8];
+        tc::ld8(tb + Y::O1 + t + lane_off, a);
+        tc::ld8(tb + Y::O2 + t + lane_off, d);
+        tc::wait_ld();
 #pragma unroll
-        for (int z = 0; z < 8; z += 4) {
-          const float4 x = *reinterpret_cast<const float4 *>(&Z->os1[t + z]), y = *reinterpret_cast<const float4 *>(&Z->os2[t + z]);
-          s1[z] = x.x, s1[z + 1] = x.y, s1[z + 2] = x.z, s1[z + 3] = x.w;
-          s2[z] = y.x, s2[z + 1] = y.y, s2[z + 2] = y.z, s2[z + 3] = y.w;
+        for (int z = 0; z < 8; z += 2) {
+          const f2 s1 = *reinterpret_cast<const f2 *>(&Z->os1[t + z]), s2 = *reinterpret_cast<const f2 *>(&Z->os2[t + z]);
+          const f2 x = fma2(pack2(__uint_as_float(a[z]), __uint_as_float(a[z + 1])), s1,
+                            mul2(pack2(__uint_as_float(d[z]), __uint_as_float(d[z + 1])), s2));
+          const float2 v = unpack2(mul2(x, pack2(f, f)));
+          y[(t + z) / 2] = pack_bf16x2(v.x, v.y);
         }
+      }
+      tc::fence_before_sync();
+      arrive(o_free);
+      if (some >= C) {
 #pragma unroll
-        for (int z = 0; z < 8; ++z) {
-          const float x = __uint_as_float(a[z]) * s1[z] + __uint_as_float(d[z]) * s2[z];
-          if (t + z < some) *out = __float2bfloat16_rn(x * f);
-          out += step;
+        for (int t = 0; t < C / 2; ++t) {
+          *reinterpret_cast<uint16_t *>(out) = (uint16_t)y[t];
+          *reinterpret_cast<uint16_t *>(out + step) = (uint16_t)(y[t] >> 16);
+          out += 2 * step;
+        }
+      } else {  // the last block: nothing behind the sequence is written
+#pragma unroll
+        for (int t = 0; t < C / 2; ++t) {
+          if (2 * t < some) *reinterpret_cast<uint16_t *>(out) = (uint16_t)y[t];
+          if (2 * t + 1 < some) *reinterpret_cast<uint16_t *>(out + step) = (uint16_t)(y[t] >> 16);
+          out += 2 * step;
         }
       }
       arrive(&empty[st]);
@@ -727,18 +762,16 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
     // scale of a row: 2^-k with at most 1 behind it
     auto scale_of = [&](float most) { return pow2_field(253 - imin(imax(__float_as_int(most) >> 23, 27), 226)); };
     auto most_of = [&](int st) { return reinterpret_cast<const float *>(ring + st * Y::STAGE + Y::MOST)[r]; };
-    // S as the next product's operand, a k-step at a time; the largest |S|
-    auto put_state = [&](float by) {
-      const f2 by2 = pack2(by, by);
-      float m0 = 0.f, m1 = 0.f;
+    // S (held scaled) as the next product's operand, a k-step at a time; the largest |S| of it
+    auto put_state = [&]() {
+      __half2 most = __float2half2_rn(0.f);
 #pragma unroll
       for (int g = 0; g < Y::STEPS; ++g) {
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          split2(mul2(S[8 * g + e], by2), hi[e], lo[e]);
-          const float2 x = unpack2(S[8 * g + e]);
-          m0 = fmaxf(m0, fabsf(x.x)), m1 = fmaxf(m1, fabsf(x.y));
+          split2(S[8 * g + e], hi[e], lo[e]);
+          most = __hmax2(most, __habs2(*reinterpret_cast<__half2 *>(&hi[e])));
         }
         tc::st8(tb + Y::SH + hf * (SC / 2) + 8 * g + lane_off, hi);
         tc::st8(tb + Y::SL + hf * (SC / 2) + 8 * g + lane_off, lo);
@@ -748,31 +781,33 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
           arrive(&s_ready[g / (Y::STEPS / 2)]);
         }
       }
-      return fmaxf(m0, m1);
+      return fmaxf(__low2float(most), __high2float(most));
     };
     if (n > 0) {
       wait(&full[0], 0);
       sc = scale_of(both(fmaxf(m * 0.015625f, 0.125f * most_of(0))));
-      put_state(sc);
+      const f2 sc2 = pack2(sc, sc);
+#pragma unroll
+      for (int e = 0; e < SC / 2; ++e) S[e] = mul2(S[e], sc2);
+      m = put_state();
     }
     int st = 0;
     uint32_t phase = 0;  // of the stage after this one
     for (int c = 0; c < n; ++c) {
       const uint32_t par = c & 1;
       const Scalars *Z = scalars(st);
-      const float isc = 1.f / sc;  // (exact)
-      if (hf == 0) scale[par * ROWS + r] = isc;
+      if (hf == 0) scale[par * ROWS + r] = 1.f / sc;  // (exact)
       // R = b (v - e^G X), a k-step (16 tokens) at a time
       {
         const int some = own.y - c * C - hf * 32;
         const uint16_t *v = reinterpret_cast<const uint16_t *>(ring + st * Y::STAGE + Y::V) + hf * 32 * ROWS + r;
         const f2 sc2 = pack2(sc, sc);
-        uint32_t vb[16];  // values of two tokens each, zeros past the sequence's end
+        f2 w[16];  // b' v' of two tokens each, zeros past the sequence's end
 #pragma unroll
-        for (int t = 0; t < 16; ++t) vb[t] = v[2 * t * ROWS] | (uint32_t)v[(2 * t + 1) * ROWS] << 16;
-        if (some < 32) {
-#pragma unroll
-          for (int t = 0; t < 16; ++t) vb[t] = 2 * t + 1 < some ? vb[t] : 2 * t < some ? vb[t] & 0xffffu : 0u;
+        for (int t = 0; t < 16; ++t) {
+          uint32_t x = (uint32_t)v[2 * t * ROWS] << 16, y = (uint32_t)v[(2 * t + 1) * ROWS] << 16;
+          if (some < 32) x = 2 * t < some ? x : 0u, y = 2 * t + 1 < some ? y : 0u;
+          w[t] = mul2(mul2(pack2(__uint_as_float(x), __uint_as_float(y)), sc2), *reinterpret_cast<const f2 *>(&Z->bv[hf * 32 + 2 * t]));
         }
         wait(x_done, par);
         tc::fence_after_sync();
@@ -787,9 +822,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
 #pragma unroll
           for (int t = 0; t < 8; ++t) {
             const int at = hf * 32 + 16 * g + 2 * t;
-            const f2 bx = *reinterpret_cast<const f2 *>(&Z->bx[at]), bv = *reinterpret_cast<const f2 *>(&Z->bv[at]);
-            const f2 w = mul2(mul2(pack2(bf16lo(vb[8 * g + t]), bf16hi(vb[8 * g + t])), sc2), bv);
-            split2(fma2(bx, pack2(__uint_as_float(raw[2 * t]), __uint_as_float(raw[2 * t + 1])), w), hi[t], lo[t]);
+            const f2 bx = *reinterpret_cast<const f2 *>(&Z->bx[at]);
+            split2(fma2(bx, pack2(__uint_as_float(raw[2 * t]), __uint_as_float(raw[2 * t + 1])), w[8 * g + t]), hi[t], lo[t]);
           }
           tc::st8(tb + Y::X + hf * 32 + 16 * g + lane_off, hi);
           tc::st8(tb + Y::X + hf * 32 + 16 * g + 8 + lane_off, lo);
@@ -798,7 +832,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
         tc::fence_before_sync();
         arrive(r_ready);
       }
-      float um = 0.f;
+      __half2 um = __float2half2_rn(0.f);
       {
         wait(u_done, par);
         tc::fence_after_sync();
@@ -814,10 +848,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
           for (int t = 0; t < 8; ++t) {
             const float a = __uint_as_float(raw[2 * t]), d = __uint_as_float(raw[2 * t + 1]);
             u[t] = pack_f16x2(a, d);
-            const f2 x = mul2(pack2(a, d), *reinterpret_cast<const f2 *>(&Z->en[hf * 32 + 16 * g + 2 * t]));
-            const float2 y = unpack2(x);
-            um = fmaxf(um, fmaxf(fabsf(y.x), fabsf(y.y)));
-            split2(x, hi[t], lo[t]);
+            split2(mul2(pack2(a, d), *reinterpret_cast<const f2 *>(&Z->en[hf * 32 + 16 * g + 2 * t])), hi[t], lo[t]);
+            um = __hmax2(um, __habs2(*reinterpret_cast<__half2 *>(&hi[t])));
           }
           tc::st8(tb + Y::U + hf * 32 + 16 * g + lane_off, hi);
           tc::st8(tb + Y::U + hf * 32 + 16 * g + 8 + lane_off, lo);
@@ -831,16 +863,20 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       arrive(&empty[st]);
       st = st + 1 == STAGES ? 0 : st + 1;
       phase ^= st == 0;
-      float sc_next = sc;
+      float ratio = 1.f;  // of the next block's scale to this one's
       if (c + 1 < n) {
         wait(&full[st], phase);
         // elements of k' are below 2^-3, 64 tokens: |S'| <= 8 |U~|; twice, as the largest of
         // the sum's terms may be different threads'
-        sc_next = scale_of(both(fmaxf((gc * m + 8.f * um * isc) * 0.03125f, 0.125f * most_of(st))));
+        const float most = (gc * m + 8.f * fmaxf(__low2float(um), __high2float(um))) * 0.03125f;
+        const float next = scale_of(both(fmaxf(most / sc, 0.125f * most_of(st))));
+        ratio = next / sc;  // (exact)
+        sc = next;
       }
-      const f2 gc2 = pack2(gc, gc), isc2 = pack2(isc, isc);
+      const float keep = gc * ratio;
+      const f2 keep2 = pack2(keep, keep), ratio2 = pack2(ratio, ratio);
 #pragma unroll
-      for (int e = 0; e < SC / 2; ++e) S[e] = mul2(S[e], gc2);
+      for (int e = 0; e < SC / 2; ++e) S[e] = mul2(S[e], keep2);
       wait(d_done, par);
       tc::fence_after_sync();
       uint32_t raw[SC / 16][16];
@@ -851,13 +887,14 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       for (int g = 0; g < SC / 16; ++g)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          S[8 * g + e] = fma2(pack2(__uint_as_float(raw[g][2 * e]), __uint_as_float(raw[g][2 * e + 1])), isc2, S[8 * g + e]);
-      if (c + 1 < n) m = put_state(sc_next);
-      sc = sc_next;
+          S[8 * g + e] = fma2(pack2(__uint_as_float(raw[g][2 * e]), __uint_as_float(raw[g][2 * e + 1])), ratio2, S[8 * g + e]);
+      if (c + 1 < n) m = put_state();
     }
     if (kept && ok) {
+      const f2 isc2 = pack2(1.f / sc, 1.f / sc);
 #pragma unroll
-      for (int e = 0; e < SC / 2; e += 2) *reinterpret_cast<ulonglong2 *>(srow + 2 * e) = make_ulonglong2(S[e], S[e + 1]);
+      for (int e = 0; e < SC / 2; e += 2)
+        *reinterpret_cast<ulonglong2 *>(srow + 2 * e) = make_ulonglong2(mul2(S[e], isc2), mul2(S[e + 1], isc2));
     }
   }
   tc::fence_before_sync();
@@ -876,7 +913,7 @@ template <int DK>
 sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
   const PoolParams &P = CP.p;
   const long long items = (long long)P.B * P.Hv * CP.row_blocks, blocks = places(P.B, P.T);
-  if (items > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
+  if (items > 0x7fffffffLL || blocks * P.Hk > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
   // values (column, head, token) in boxes of 128 x 1 x 64, zeros past the last column
   auto fn = attn::encode_fn();
   if (!fn) return SV_ERR_CUDA;
@@ -888,7 +925,7 @@ sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
   if (fn(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, P.v.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return SV_ERR_CUDA;
-  cudaError_t e = launch_early(prepare_kernel<DK>, dim3((unsigned)blocks, P.Hk), dim3(128), (size_t)PL<DK>::BYTES, s, CP);
+  cudaError_t e = launch_early(prepare_kernel<DK>, dim3((unsigned)(blocks * P.Hk)), dim3(128), (size_t)PL<DK>::BYTES, s, CP);
   if (e != cudaSuccess) return SV_ERR_CUDA;
   return from_cuda(launch_early(chain_kernel<DK>, dim3((unsigned)items), dim3(CHAIN_THREADS), (size_t)CL<DK>::BYTES, s, mv, CP));
 }
