@@ -20,6 +20,7 @@
  *   paged_kv_append -- the same on the way into a paged bf16 or e4m3 cache
  *   paged_attn      -- one-token / verify-row attention over that cache
  *   window_attn     -- causal attention of packed prompts
+ *   paged_chunk_attn -- chunks of new tokens over the paged cache
  *   gdn_chunk       -- recurrent layers: packed chunks over a pool of states
  *   gdn_step        -- recurrent layers: one token / verify rows over that pool
  *
@@ -396,6 +397,36 @@ SV_API sv_status window_attn(const sv_rows *q, const sv_rows *k, const sv_rows *
                              const int32_t *cu_q, const int32_t *cu_k, int B, int Tq, int Tk, int Hq,
                              int Hkv, int D, float scale, int window, int sinks, void *workspace,
                              size_t ws_bytes, sv_stream_t stream);
+
+/* Attention of chunks of new tokens over a paged cache that already holds them:
+ * sequence b's queries are rows cu_q[b]..cu_q[b+1]-1 of q and o, nq of them, and its
+ * positions 0..kv_lens[b]-1 stand in the pages of row b of block_table.  Row i
+ * stands at position p = kv_lens[b] - nq + i and sees position j >= 0 iff j <= p and
+ * (window == 0, or j > p - window, or j < sinks):
+ *   o = softmax_j(scale * <q, k_j>) . v_j, zeros for a row that sees nothing.
+ * Prompts and chunks of prompts of any length, and single tokens among them, in one
+ * call (window_attn is the form for keys in packed rows, paged_attn for calls of few rows
+ * each).
+ * cu_q: device int32 [B+1], 0 <= cu_q[b] <= cu_q[b+1] <= Tq.  A sequence whose
+ *   offsets break this is left out and reported by sv_last_device_error() as
+ *   SV_ERR_INVALID_ARG (all are, where the others name rows so often that they hold
+ *   more than Tq and B of them can).  Rows of o of no sequence are not written.
+ * block_table, kv_lens, cache: as paged_attn's, with its rules for lengths, entries
+ *   and pages out of range, and for slots that no row sees.
+ * Arithmetic as paged_attn's: fp32, with the second product's operands in 16 bits.
+ * Supported: D in {128, 256}; Hq % Hkv == 0; Hq/Hkv <= 128; 0 <= B <= 4096;
+ *   Tq <= 2^30; table_width*page_size <= 2^30; (Tq / (128 / (Hq/Hkv)) + B) * Hkv *
+ *   (table_width*page_size/128 + 4) < 2^31, divisions rounded down; strides of q above
+ *   0; window <= 2^30; scale > 0 and finite.
+ * workspace: device, 16-byte aligned; nothing in it has to be zero.
+ * Two launches; offsets, lengths and tables are read on the device, so a captured
+ * call follows their contents. */
+SV_API size_t paged_chunk_attn_workspace_bytes(int B, int Tq, int Hq, int Hkv, int D);
+SV_API sv_status paged_chunk_attn(const sv_rows *q, const sv_paged_kv *cache, const int32_t *block_table,
+                                  int64_t table_stride, int table_width, const int32_t *kv_lens,
+                                  const sv_rows *o, const int32_t *cu_q, int B, int Tq, int Hq, int Hkv, int D,
+                                  float scale, int window, int sinks, void *workspace, size_t ws_bytes,
+                                  sv_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* Exact acceptance                                                         */

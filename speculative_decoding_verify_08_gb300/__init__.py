@@ -47,7 +47,7 @@ __all__ = [
     "gdn_verify",
     "SV_E4M3", "rope_phases", "qk_norm_rope", "PagedKV", "paged_kv_append",
     "paged_attn_workspace_bytes", "paged_attn", "window_attn_workspace_bytes", "window_attn",
-    "gdn_step", "gdn_chunk_workspace_bytes", "gdn_chunk",
+    "paged_chunk_attn_workspace_bytes", "paged_chunk_attn", "gdn_step", "gdn_chunk_workspace_bytes", "gdn_chunk",
 ]
 
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_CUDA = 0, 1, 2, 3
@@ -128,6 +128,8 @@ def load():
             "paged_attn_workspace_bytes": (Z, [I, I, I, I, I]),
             "paged_attn": (I, [P, P, P, L, I, P, P, I, I, I, I, I, ctypes.c_float, I, I, P, Z, P]),
             "window_attn_workspace_bytes": (Z, [I, I, I, I]),
+            "paged_chunk_attn_workspace_bytes": (Z, [I, I, I, I, I]),
+            "paged_chunk_attn": (I, [P, P, P, L, I, P, P, P, I, I, I, I, I, ctypes.c_float, I, I, P, Z, P]),
             "gdn_step": (I, [P, P, P, P, P, P, P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P]),
             "gdn_chunk_workspace_bytes": (Z, [I, I, I, I, I, I]),
             "gdn_chunk": (I, [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, P, Z, P]),
@@ -600,6 +602,38 @@ def window_attn(q, k, v, o, cu_q, cu_k, scale: float, window: int = 0, sinks: in
                                 _vector(cu_q, torch.int32, n, dev, w), _vector(cu_k, torch.int32, n, dev, w), n - 1,
                                 Tq, Tk, Hq, Hkv, D, scale, window, sinks, _ptr(workspace), _nbytes(workspace),
                                 _launch_stream(dev, stream))
+    if status:
+        _check(status, w)
+
+
+def paged_chunk_attn_workspace_bytes(B: int, Tq: int, Hq: int, Hkv: int, D: int) -> int:
+    return load().paged_chunk_attn_workspace_bytes(B, Tq, Hq, Hkv, D)
+
+
+def paged_chunk_attn(q, cache: PagedKV, block_table, kv_lens, o, cu_q, scale: float, window: int = 0,
+                     sinks: int = 0, workspace=None, stream=None):
+    """Attention of ragged chunks of new tokens over the cache that already
+    holds them: q and o [Tq, Hq, D], sequence b rows cu_q[b]..cu_q[b+1] (int32
+    [B+1]), its last row at position kv_lens[b] - 1 (int32 [B]); block_table
+    int32 [B, width]; window 0: none; sinks: first positions that stay visible
+    under a window."""
+    Tq, Hq, D = q.shape
+    w = "paged_chunk_attn"
+    B, width = block_table.shape
+    dev = None if _gpus == 1 else _device(q, w)
+    if (D != cache.D or block_table.dtype is not torch.int32 or not block_table.is_cuda
+            or (workspace is not None and not workspace.is_cuda)):
+        _bad(w)
+    if dev is not None and (dev != cache.device or block_table.get_device() != dev
+                            or (workspace is not None and workspace.get_device() != dev)):
+        _bad(w)
+    ts, es = block_table.stride()
+    if es != 1 and width != 1:
+        _bad(w)
+    status = load().paged_chunk_attn(_rows(q, Tq, Hq, D, dev, w), cache.packed, block_table.data_ptr(), ts, width,
+                                     _vector(kv_lens, torch.int32, B, dev, w), _rows(o, Tq, Hq, D, dev, w),
+                                     _vector(cu_q, torch.int32, B + 1, dev, w), B, Tq, Hq, cache.heads, D, scale,
+                                     window, sinks, _ptr(workspace), _nbytes(workspace), _launch_stream(dev, stream))
     if status:
         _check(status, w)
 
