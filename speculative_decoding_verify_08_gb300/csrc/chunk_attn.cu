@@ -182,8 +182,15 @@ __device__ __forceinline__ bool heads(const Params &P, const Item &it, int j) {
 __device__ __forceinline__ int position(const Params &P, const Item &it, int j, int r) {
   return r < PIECE && heads(P, it, j) ? r : it.base(j) + r;
 }
-__device__ __forceinline__ bool seen(const Params &P, const Item &it, int pos) {
-  return pos < it.len && (pos < P.sinks || pos >= it.from);
+// Rows of block j that no row of the sequence sees (or none of the item): a..b-1, and those from c on.
+struct Blind {
+  int a, b, c;
+  __device__ __forceinline__ bool operator()(int r) const { return (r >= a && r < b) || r >= c; }
+};
+__device__ __forceinline__ Blind blind(const Params &P, const Item &it, int j) {
+  const int base = it.base(j);
+  const bool h = heads(P, it, j);
+  return Blind{h ? P.sinks : imax(0, P.sinks - base), h ? imax(PIECE, it.from - base) : it.from - base, it.len - base};
 }
 // Page of a piece of R slots at pos: out of the cache where its entry is (which reads as
 // zeros), -1 where no row sees any slot of it.
@@ -418,9 +425,6 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       int slot = 0;
       // One slot's copies: rows first.. of block j, column groups `group`.. (kv: K or V)
       auto fetch = [&](const Item &it, int j, int x, bool v) {
-        if (ok && lane == 0) ok = mbar_wait(&free[slot], parity, P.err);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) return;
         const int rows = v ? VK : BN, first = v ? x * VK : 0, pieces = rows / P.R;
         int p, g, place;  // piece, column group, where in the slot
         if (F8) {
@@ -434,7 +438,10 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
           p = lane / KG, g = x * KG + lane % KG, place = ((lane % KG) * BN + p * P.R) * 128;
         }
         const int pos = position(P, it, j, first + p * P.R);
-        const int page = p < pieces ? page_of(P, it, pos) : -1;
+        const int page = p < pieces ? page_of(P, it, pos) : -1;  // (looked up while the slot is still taken)
+        if (lane == 0 && ok) ok = mbar_wait(&free[slot], parity, P.err);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) return;
         const uint32_t bytes = (uint32_t)P.R * 128 * (!F8 && v ? D / 64 : 1);
         const uint32_t n = __popc(__ballot_sync(0xffffffffu, page >= 0));
         if (lane == 0) mbar_arrive_expect_tx(&landed[slot], n * bytes);
@@ -511,14 +518,13 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
           const uint8_t *raw = raws + rs * C::RAW;
           uint8_t *out = ring + (v ? NK + vs : ks) * SLOT;
           const int rows = v ? VK : BN;
-          const int base = it.base(j) + (v ? x * VK : 0);
-          // slots of this block that no row sees
-          const bool some = v && (heads(P, it, j) || base + VK > it.len || (base < it.from && base + VK > P.sinks));
+          const Blind none = blind(P, it, j);
+          const int row0 = x * VK;
 #pragma unroll 4
           for (int y = 0; y < C::RAW / 16 / 128; ++y) {
             const int e = i + 128 * y, g = e / (rows * 8), r = (e >> 3) % rows, c = e & 7;
             uint4 w = *reinterpret_cast<const uint4 *>(raw + e * 16);
-            if (some && !seen(P, it, position(P, it, j, x * VK + r))) w = make_uint4(0u, 0u, 0u, 0u);
+            if (v && none(row0 + r)) w = make_uint4(0u, 0u, 0u, 0u);
             const uint32_t z[4] = {w.x, w.y, w.z, w.w};
             uint32_t f[8];
 #pragma unroll
@@ -632,9 +638,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         for (int j = j0; j < j1; ++j) {
           const bool more = j + 1 < j1;
           if (NSB == 2 && more) issue_s(0, 1, true, j + 2 == j1);  // runs during this block's softmax
-          const int base = it.base(j);
-          // slots of this block that no row sees (e4m3: zeros already)
-          const bool some = !F8 && (heads(P, it, j) || base + BN > it.len || (base < it.from && base + BN > P.sinks));
+          const Blind none = blind(P, it, j);  // (e4m3: zeros already)
+          const int upto = F8 ? 0 : (none.c + P.R - 1) & -P.R;  // (pieces behind hold older values)
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             if (t >= nt) continue;
@@ -645,14 +650,18 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
 #pragma unroll
             for (int x = 0; x < PARTS; ++x) {
               if (t == 0) wait(&full[5 + at.slot], at.parity);
-              if (some && t == 0) {
+              if (!F8 && t == 0 && (none.a < none.b || none.c < BN)) {
                 uint8_t *vb = ring + (NK + at.slot) * SLOT;
-                for (int r = 0; r < VK; ++r) {
-                  if (seen(P, it, position(P, it, j, x * VK + r))) continue;
-                  for (int y = lane; y < D / 8; y += 32)
+                auto clear = [&](int r0, int r1) {  // rows of the block, those of this slot
+                  r0 = imax(r0 - x * VK, 0), r1 = imin(r1 - x * VK, VK);
+                  for (int e = lane; e < (r1 - r0) * (D / 8); e += 32) {
+                    const int r = r0 + e / (D / 8), y = e % (D / 8);
                     *reinterpret_cast<uint4 *>(vb + (r / P.R) * P.R * 128 * (D / 64) + (y >> 3) * P.R * 128 + (r % P.R) * 128 + (y & 7) * 16) =
                         make_uint4(0u, 0u, 0u, 0u);
-                }
+                  }
+                };
+                clear(none.a, imin(none.b, BN));
+                clear(none.c, imin(upto, BN));
                 fence_proxy_async();
                 __syncwarp();
               }
