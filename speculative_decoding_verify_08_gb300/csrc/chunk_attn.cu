@@ -20,11 +20,14 @@
 //    (fp32), maximum and sum in the workspace, and a second kernel joins them.
 //  * Slots that no row of the sequence sees may hold anything: their scores are
 //    masked, and their values are overwritten with zeros before the product.
-//  * e4m3 pages: four more warps turn the copies into fp16 tiles (each value exactly),
+//  * e4m3 pages: copies land in the second halves of their slots, and four more warps spread them out
+//    to fp16 tiles there (each value exactly);
 //    queries are scaled by a power of two per row and turned to fp16 in place
 //    (exact down to 2^-14 of a row's largest element, off by 2^-25 of that below), and
 //    probabilities are taken 2^13 times as large, and their sum with them, so that
 //    those down to 2^-27 of the maximum keep 2^-11 (smaller ones are off by 2^-38 of it).
+#include <type_traits>
+
 #include "paged.cuh"
 #include "tcgen05.cuh"
 
@@ -39,7 +42,7 @@ constexpr int BN = 128;             // keys of a block
 constexpr int PIECE = 32;           // first keys that may share a block with others
 constexpr int MAX_B = 4096;
 constexpr int HEAD_COST = 2;        // blocks' time that an item takes beside its blocks
-// Shared memory: barriers, the CTA's cuts (256), more barriers (336), the item
+// Shared memory: barriers, the CTA's cuts (256), more barriers (280), the item
 // (400), halves' exchange (512), prefix sums (2560; after the ring if longer), then the query
 // tiles and the ring.
 constexpr int HEADER = 3072, PREFIX = 2560, CUTS = 256, INFO = 400;
@@ -53,36 +56,34 @@ struct Cfg {
   static constexpr int HALVES = TILES == 2 ? 1 : 2;  // threads that share a row
   // Ring slots: a whole K or V block at D = 128, at D = 256 half of its columns
   // (K) or of its keys (V).
-  static constexpr int SLOT = 32768, RAW = SLOT / 2;
+  static constexpr int SLOT = 32768, RAW = SLOT / 2;  // (e4m3: where a copy lands)
   static constexpr int PARTS = BN * D * 2 / SLOT;  // slots of a K block (of a V block)
   static constexpr int KG = D / 64 / PARTS;        // 64-column groups of a K slot
   static constexpr int VK = BN / PARTS;            // keys of a V slot
   static constexpr int THREADS = (SOFT + (F8 ? 8 : 4)) * 32;
   static constexpr int QBYTES = ROWS * D * 2;
   static constexpr int RING = HEADER + NT * QBYTES;
-  // slots of the K and the V ring, 160 KB; one fewer beside long prefix sums; e4m3: two
-  // each, and two (one) of half the size for what the copies bring
-  static constexpr int NK = 2, NV = F8 ? 2 : 3, LESS = 2, NR = 2;
-  static constexpr int PREFIX_AT = RING + (F8 ? (NK + NV) * SLOT + RAW : 2 * LESS * SLOT);
-  static_assert((NK + NV) * SLOT + (F8 ? NR * RAW : 0) == 160 * 1024, "ring");
+  // slots of the K and the V ring: 160 KB, or 128 beside long prefix sums and e4m3's scales
+  static constexpr int NK = 2, NV = 3, LESS = 2;
+  static_assert((NK + NV) * SLOT == 160 * 1024 && 2 * LESS * SLOT == 128 * 1024, "ring");
+  static constexpr int BEHIND = RING + 128 * 1024;  // prefix sums
+  static constexpr int SCALES = BEHIND + ((MAX_B + 1) * 4 + 15) / 16 * 16;  // [2][ROWS] of e4m3's queries
   // tensor memory: O per tile, then the S buffers (P over S)
   static constexpr uint32_t TO = 0, TS = NT * D;
   static_assert(NT * D + NT * NSB * BN <= 512, "tensor memory");
   // registers: as many as the threads start with
-  static constexpr int SOFT_REGS = F8 ? 200 : 216, OTHER_REGS = F8 ? 56 : 72;
+  static constexpr int SOFT_REGS = F8 ? 184 : 216, OTHER_REGS = 72;
   static_assert(256 * SOFT_REGS + (THREADS - 256) * OTHER_REGS <= (65536 / THREADS / 8 * 8) * THREADS, "registers");
   // log2 of the factor on probabilities and their sum, and of the largest P against an
   // old maximum, factor included
   static constexpr float LIFT = F8 ? 13.f : 0.f, RESCALE = F8 ? 2.f : 8.f;
 };
 
-// What the join needs of a CTA's pieces of cut items.
+// Item that a CTA begins and does not end: its pieces are this CTA's second and the first of
+// each of the pieces - 1 CTAs behind it (0: none).
 struct Cut {
-  int h, q0, rows, begins;  // item whose first piece this CTA had last (begins != 0)
-  int state;                // of its first piece: NEW_ITEM, GOES_ON, ENDS (of the item before), NONE (no piece at all)
-  int pad[3];
+  int h, q0, rows, pieces;
 };
-enum { NEW_ITEM = 0, GOES_ON = 1, ENDS = 2, NONE = 3 };
 
 struct Params {
   sv_rows o;
@@ -99,8 +100,9 @@ struct Params {
   float sl2e;
   int window, sinks;
   int few_slots;  // long prefix sums take the place of some
-  int stall;      // test aid: the first slot of the K ring (what the copies bring) never fills
+  int stall;      // test aid: the first slot of the K ring never fills
 };
+constexpr int MAX_KEPT = 31;  // sequences whose offsets and lengths are kept in shared memory (int4 each)
 
 struct Item {
   int b, h, q0;      // sequence, KV head, first row
@@ -137,22 +139,30 @@ __device__ __forceinline__ int length_of(const Params &P, int b, bool report) {
   return l;
 }
 
-// Tile `c` of the line (pre: tiles before a sequence), for KV head h.
+// Tile `c` of the line (pre: tiles before a sequence, or, of few sequences, those, the first
+// row, the rows and the length), for KV head h.
 template <int NT>
 __device__ __forceinline__ Item tile_at(const Params &P, const int *pre, int c, int h) {
+  const bool kept = P.B <= MAX_KEPT;
+  const int each = kept ? 4 : 1;
   int lo = 0, hi = P.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= c) lo = mid; else hi = mid - 1;
+    if (pre[mid * each] <= c) lo = mid; else hi = mid - 1;
   }
   const int b = lo, span = P.PT * NT;
   Item it;
   it.b = b;
   it.h = h;
   // a sequence's last tiles first: they see the most
-  const int row0 = (pre[b + 1] - 1 - c) * span;
-  const int q0 = P.cu_q[b], nq = P.cu_q[b + 1] - q0;
-  it.len = length_of(P, b, false);
+  const int row0 = (pre[(b + 1) * each] - 1 - c) * span;
+  int q0, nq;
+  if (kept) {
+    const int4 x = reinterpret_cast<const int4 *>(pre)[b];
+    q0 = x.y, nq = x.z, it.len = x.w;
+  } else {
+    q0 = P.cu_q[b], nq = P.cu_q[b + 1] - q0, it.len = length_of(P, b, false);
+  }
   it.q0 = q0 + row0;
   it.rows = imin(span, nq - row0);
   it.p0 = it.len - nq + row0;
@@ -192,18 +202,6 @@ __device__ __forceinline__ Blind blind(const Params &P, const Item &it, int j) {
   const bool h = heads(P, it, j);
   return Blind{h ? P.sinks : imax(0, P.sinks - base), h ? imax(PIECE, it.from - base) : it.from - base, it.len - base};
 }
-// Page of a piece of R slots at pos: out of the cache where its entry is (which reads as
-// zeros), -1 where no row sees any slot of it.
-__device__ __forceinline__ int page_of(const Params &P, const Item &it, int pos) {
-  if (pos >= it.len || (pos >= P.sinks && pos + P.R <= it.from)) return -1;
-  const int e = P.table[it.b * P.table_stride + pos / P.page_size];
-  if (e < 0 || e >= P.num_pages) {
-    atomicOr(P.err, ERR_INDEX);
-    return P.num_pages;
-  }
-  return e;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -259,26 +257,27 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   uint64_t *o_free = o_done + 2;   // [2] O read out
   uint64_t *q_full = o_free + 2;   // queries of the item landed
   uint64_t *q_free = q_full + 1;   // last S product of the item done
-  // (32 barriers, 256 bytes; the rest stands behind the halves' exchange)
-  uint64_t *more = reinterpret_cast<uint64_t *>(smem + 336);
+  // (30 barriers, 240 bytes; the rest stands behind the cuts)
+  uint64_t *more = reinterpret_cast<uint64_t *>(smem + 280);
   uint64_t *idle = more, *p_half = more + 1;  // p_half [2] one S buffer: P of the first half of a block's keys written
-  uint64_t *raw_full = more + 3, *raw_empty = more + 5, *q_ready = more + 7;  // e4m3
+  uint64_t *q_ready = more + 3, *copied = more + 4;  // e4m3: queries turned, [2][5] copies landed
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + CUTS + 16);
   int2 *cut = reinterpret_cast<int2 *>(smem + CUTS);  // [2] item and block where this CTA begins, and the next one
   Item *info_it = reinterpret_cast<Item *>(smem + INFO);  // of the item whose queries landed
   int *info = reinterpret_cast<int *>(smem + INFO + 48);  // its first block, its end, its tiles
   float *xchg = reinterpret_cast<float *>(smem + 512);  // [2][2 halves][ROWS] maxima, then sums
+  float *rowscale = reinterpret_cast<float *>(smem + C::SCALES);  // e4m3: [2][ROWS] what the rows' scores are multiplied by
   uint8_t *qs = smem + HEADER;
   uint8_t *ring = smem + C::RING;
-  const int NK = C::NK, NV = !F8 && P.few_slots ? C::LESS : C::NV, NR = F8 && P.few_slots ? 1 : C::NR;
-  uint8_t *raws = ring + (C::NK + C::NV) * SLOT;
-  int *pre = reinterpret_cast<int *>(smem + (P.few_slots ? C::PREFIX_AT : PREFIX));
+  const int NK = C::NK, NV = P.few_slots ? C::LESS : C::NV;
+  int *pre = reinterpret_cast<int *>(smem + (P.few_slots ? C::BEHIND : PREFIX));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < 10; ++i) {
       mbar_init(&full[i], (F8 ? 4 : 1) + (i == 0 && !F8 ? P.stall : 0));
       mbar_init(&empty[i], 1);
+      if (F8) mbar_init(&copied[i], 1 + (i == 0 ? P.stall : 0));
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -286,12 +285,10 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       mbar_init(&o_done[i], 1);
       mbar_init(&p_half[i], 4);
       mbar_init(&o_free[i], 4 * C::HALVES);
-      mbar_init(&raw_full[i], 1 + (i == 0 ? P.stall : 0));
-      mbar_init(&raw_empty[i], 4);
     }
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
-    mbar_init(q_ready, C::SOFT);
+    mbar_init(q_ready, 4);
     mbar_init(idle, 1);
     fence_barrier_init();
   }
@@ -310,8 +307,6 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   // Values of slots that are not copied meet probabilities of zero and have to be finite.
   for (int x = tid; x < NV * SLOT / 16; x += C::THREADS)
     reinterpret_cast<uint4 *>(ring + NK * SLOT)[x] = make_uint4(0u, 0u, 0u, 0u);
-  if (F8)
-    for (int x = tid; x < NR * C::RAW / 16; x += C::THREADS) reinterpret_cast<uint4 *>(raws)[x] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async();
   pdl_wait();
 
@@ -344,18 +339,23 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   for (int b0 = 0; b0 < P.B; b0 += C::THREADS) {
     const int b = b0 + tid;
     const int nq = b < P.B ? rows_of(P, b, report) : 0;
-    if (b < P.B) length_of(P, b, report);
+    const int len = b < P.B ? length_of(P, b, report) : 0;
     const int nt = (nq + P.PT * NT - 1) / (P.PT * NT);
     int all;
     const int x = scan(nt, all);
-    if (b < P.B) pre[b] = sum(tiles, x) - nt;
+    if (b < P.B) {
+      if (P.B <= MAX_KEPT)
+        reinterpret_cast<int4 *>(pre)[b] = make_int4(sum(tiles, x) - nt, P.cu_q[b], nq, len);
+      else
+        pre[b] = sum(tiles, x) - nt;
+    }
     tiles = sum(tiles, all);
   }
   if (tiles > P.most) {
     if (tid == 0 && blockIdx.x == 0) atomicOr(P.err, ERR_INDEX);
     tiles = 0;
   }
-  if (tid == 0) pre[P.B] = tiles;
+  if (tid == 0) pre[P.B <= MAX_KEPT ? 4 * P.B : P.B] = tiles;
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -370,101 +370,132 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       scan(mine, all);
       per_head += all;  // (in 31 bits with the heads: checked on the host)
     }
-    const long long W = (long long)per_head * P.Hkv, ctas = gridDim.x;
-    const long long at[2] = {W * blockIdx.x / ctas, W * (blockIdx.x + 1) / ctas};
+    // (no CTA takes less than four blocks' time, so that no two cuts coincide)
+    const int W = per_head * P.Hkv, ctas = imin(gridDim.x, imax(1, W / 4));
+    auto line = [&](int x) { return (int)((long long)W * imin(x, ctas) / ctas); };
+    const int at[2] = {line(blockIdx.x), line(blockIdx.x + 1)};
     // A cut this near to an item's beginning or end moves there: what cutting costs (both
     // pieces' O through the workspace) is a block or two.
-    const int near = imax(3, (int)(W / ctas / 16));
+    const int near = imax(3, W / ctas / 16);
     if (tid < 2) cut[tid] = make_int2(tiles * P.Hkv, 0);
+    if (tid == 0) P.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     int before = 0;
     for (int c0 = 0; c0 < tiles; c0 += C::THREADS) {
       const int c = c0 + tid, w = tiles > C::THREADS ? weight(c) : mine;
       const int x = before + scan(w, all) - w;  // tiles' weight before this one
       before += all;
-#pragma unroll
+#pragma unroll 1
       for (int e = 0; e < 2; ++e) {
-        const long long y = at[e] - (long long)x * P.Hkv;
-        if (y < 0 || y >= (long long)w * P.Hkv) continue;
-        const int h = (int)y / w, j = (int)y - h * w - HEAD_COST, n = w - HEAD_COST, id = c * P.Hkv + h;
+        const int y = at[e] - x * P.Hkv;
+        if (y < 0 || y >= w * P.Hkv) continue;
+        const int h = y / w, j = y - h * w - HEAD_COST, n = w - HEAD_COST, id = c * P.Hkv + h;
         cut[e] = j < near ? make_int2(id, 0) : n - j < near ? make_int2(id + 1, 0) : make_int2(id, j);
+        if (e == 1 && j >= near && n - j >= near && at[0] - HEAD_COST - near < at[1] - j - HEAD_COST) {
+          // cut at its end, and not in the same item at its beginning: the item begins here; every
+          // CTA up to the last cut in it has a piece
+          const int last_cut = at[1] - j + n - near;  // of the line, the last place to cut it
+          int more_ctas = 1;
+          while (line(blockIdx.x + 1 + more_ctas) <= last_cut && (int)blockIdx.x + 1 + more_ctas < ctas) ++more_ctas;
+          const Item it = tile_at<NT>(P, pre, c, h);
+          P.cuts[blockIdx.x] = Cut{it.h, it.q0, it.rows, 1 + more_ctas};
+        }
       }
     }
     __syncthreads();
   }
-  const int2 from = cut[0], to = cut[1];
-  const int parts = to.x - from.x + (to.y > 0 ? 1 : 0);
-  // this CTA's k-th part
+  const int parts = cut[1].x - cut[0].x + (cut[1].y > 0 ? 1 : 0);
+  // this CTA's k-th part (its cuts out of shared memory each time: no role has a register to spare)
+  const uint32_t cut_at = smem_u32(cut);
+  auto id_of = [&](int k) { return (int)lds64(cut_at).x + k; };
   auto part_of = [&](int k, const Item &it) {
-    const int id = from.x + k;
-    return Part{id, k == 0 ? from.y : 0, id == to.x ? to.y : it.n};
+    const uint2 a = lds64(cut_at), z = lds64(cut_at + 8);
+    return Part{(int)a.x + k, k == 0 ? (int)a.y : 0, (int)a.x + k == (int)z.x ? (int)z.y : it.n};
   };
-  if (tid == 0) {
-    Cut c{};
-    c.state = parts <= 0 ? NONE : NEW_ITEM;
-    if (parts > 0 && from.y > 0) c.state = from.x == to.x ? GOES_ON : ENDS;
-    if (parts > 0 && to.y > 0 && !(from.x == to.x && from.y > 0)) {
-      const Item it = item_at<NT>(P, pre, to.x);
-      c.h = it.h, c.q0 = it.q0, c.rows = it.rows, c.begins = 1;
-    }
-    P.cuts[blockIdx.x] = c;
-  }
 
   if (warp >= C::SOFT) {
     setmaxnreg_dec<C::OTHER_REGS>();
-    if (F8 ? warp == C::SOFT + 1 : (warp == C::SOFT + 1 || warp == C::SOFT + 3)) {
-      // ------------------------------------------------------- copies --
-      // bf16: K blocks by one warp, V blocks by the other.  e4m3: both by one, in the order that the
-      // products take them.  A lane a piece (of a column group).
+    if (warp == C::SOFT + 1 || warp == C::SOFT + 3) {
+      // -------------------- copies: K blocks by one warp, V blocks by the other --
       const bool is_v = warp == C::SOFT + 3;
-      uint64_t *landed = F8 ? raw_full : full + (is_v ? 5 : 0), *free = F8 ? raw_empty : empty + (is_v ? 5 : 0);
-      uint8_t *slots = F8 ? raws : ring + (is_v ? NK * SLOT : 0);
-      const int NS = F8 ? NR : is_v ? NV : NK;
+      uint64_t *landed = (F8 ? copied : full) + (is_v ? 5 : 0), *free = empty + (is_v ? 5 : 0);
+      uint8_t *slots = ring + (is_v ? NK * SLOT : 0);
+      const int NS = is_v ? NV : NK;
+      // A lane a piece of R rows (of a column group), all pieces of a slot at once.
+      int first, gap, group, place;  // its first row in slot 0 of a block, from slot to slot, column group, where in the slot
+      int step = 0;                  // of the column group from slot to slot
+      if (F8) {
+        const int groups = is_v ? D / 128 : 1, p = lane / groups;  // of 128 columns
+        first = p * P.R, gap = is_v ? VK : 0;
+        group = is_v ? lane - p * groups : 0, step = is_v ? 0 : 1;
+        place = C::RAW + (is_v ? group * VK * 128 : 0) + p * P.R * 128;
+      } else if (is_v) {
+        first = lane * P.R, gap = VK, group = 0, place = lane * P.R * 128 * (D / 64);
+      } else {
+        first = lane / KG * P.R, gap = 0, group = lane % KG, step = KG, place = ((lane % KG) * BN + first) * 128;
+      }
+      const bool here = first < (is_v ? VK : BN);
+      const uint32_t bytes = (uint32_t)P.R * 128 * (!F8 && is_v ? D / 64 : 1);
+      // A piece's page and its slot there: page -1 where no row sees any slot of it, past the cache
+      // where its entry is (which reads as zeros).
+      struct Place {
+        int page, slot;
+      };
+      auto look = [&](const Item &it, int j, int x) {
+        const int pos = position(P, it, j, first + x * gap);
+        if (!here || pos >= it.len || (pos >= P.sinks && pos + P.R <= it.from)) return Place{-1, 0};
+        const int e = pos / P.page_size;
+        const int page = P.table[it.b * P.table_stride + e];
+        return Place{page, page == -1 ? ~(pos - e * P.page_size) : pos - e * P.page_size};
+      };
       bool ok = true;
       uint32_t q = 0, parity = 1;
       int slot = 0;
-      // One slot's copies: rows first.. of block j, column groups `group`.. (kv: K or V)
-      auto fetch = [&](const Item &it, int j, int x, bool v) {
-        const int rows = v ? VK : BN, first = v ? x * VK : 0, pieces = rows / P.R;
-        int p, g, place;  // piece, column group, where in the slot
-        if (F8) {
-          constexpr int GROUPS = D / 128;  // of 128 columns
-          const int groups = v ? GROUPS : 1;
-          p = lane / groups, g = v ? lane - p * groups : x;
-          place = (v ? g * VK * 128 : 0) + p * P.R * 128;
-        } else if (v) {
-          p = lane, g = 0, place = p * P.R * 128 * (D / 64);
-        } else {
-          p = lane / KG, g = x * KG + lane % KG, place = ((lane % KG) * BN + p * P.R) * 128;
+      Item it{};
+      Part pt{0, 0, 0};
+      int k = -1;
+      auto next_part = [&]() {  // the next one with blocks
+        do {
+          if (++k >= parts) return false;
+          it = item_at<NT>(P, pre, id_of(k));
+          pt = part_of(k, it);
+        } while (pt.j0 == pt.j1);
+        return true;
+      };
+      bool more_parts = next_part();
+      int j = pt.j0, x = 0, h = it.h;
+      Place at = more_parts ? look(it, j, x) : Place{-1, 0};
+      while (more_parts) {
+        // the one after it is looked up before this one's slot is waited for
+        const int now_x = x;
+        h = it.h;
+        if (++x == PARTS) x = 0, ++j;
+        if (j == pt.j1) {
+          more_parts = next_part();
+          j = pt.j0;
         }
-        const int pos = position(P, it, j, first + p * P.R);
-        const int page = p < pieces ? page_of(P, it, pos) : -1;  // (looked up while the slot is still taken)
-        if (lane == 0 && ok) ok = mbar_wait(&free[slot], parity, P.err);
+        const Place next = more_parts ? look(it, j, x) : Place{-1, 0};
+        if (ok && lane == 0) ok = mbar_wait(&free[slot], parity, P.err);
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) return;
-        const uint32_t bytes = (uint32_t)P.R * 128 * (!F8 && v ? D / 64 : 1);
-        const uint32_t n = __popc(__ballot_sync(0xffffffffu, page >= 0));
+        if (!ok) break;
+        bool live = at.page != -1;
+        // (an entry of -1 that is needed counts as a page past the cache: told apart by the slot)
+        if (at.slot < 0) live = true, at.slot = ~at.slot;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, live));
         if (lane == 0) mbar_arrive_expect_tx(&landed[slot], n * bytes);
         __syncwarp();
-        if (page >= 0)
-          page_load(slots + slot * (F8 ? C::RAW : SLOT) + place, v ? &mapV : &mapK, pos % P.page_size, g, it.h, page, &landed[slot]);
+        if (live) {
+          if (at.page < 0 || at.page >= P.num_pages) {
+            atomicOr(P.err, ERR_INDEX);
+            at.page = P.num_pages;
+          }
+          page_load(slots + slot * SLOT + place, is_v ? &mapV : &mapK, at.slot, group + now_x * step, h, at.page, &landed[slot]);
+        }
+        at = next;
         ++q;
         if (++slot == NS) {
           slot = 0;
           parity ^= 1;
-        }
-      };
-      for (int k = 0; k < parts && ok; ++k) {
-        const Item it = item_at<NT>(P, pre, from.x + k);
-        const Part pt = part_of(k, it);
-        if (F8) {
-          for (int j = pt.j0; j <= pt.j1 && ok; ++j) {
-            for (int x = 0; x < PARTS && j < pt.j1; ++x) fetch(it, j, x, false);
-            for (int x = 0; x < PARTS && j > pt.j0; ++x) fetch(it, j - 1, x, true);
-          }
-        } else {
-          for (int j = pt.j0; j < pt.j1 && ok; ++j)
-            for (int x = 0; x < PARTS; ++x) fetch(it, j, x, is_v);
         }
       }
       if (!ok && lane == 0) {  // no copy may outlive the CTA
@@ -479,7 +510,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         bool ok = true;
         uint32_t c = 0;  // parts with work so far
         for (int k = 0; k < parts && ok; ++k) {
-          const Item it = item_at<NT>(P, pre, from.x + k);
+          const Item it = item_at<NT>(P, pre, id_of(k));
           const Part pt = part_of(k, it);
           if (pt.j0 == pt.j1) continue;
           if (c > 0) ok = mbar_wait(q_free, (c - 1) & 1, P.err);
@@ -504,55 +535,89 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       }
       __syncwarp();
     } else if (F8 && warp >= C::SOFT + 4) {
-      // ------------------------------------------ e4m3 copies to fp16 --
+      // --------------------------------------- queries and e4m3 copies to fp16 --
       const int i = tid - (C::SOFT + 4) * 32;
       bool ok = true;
-      int rs = 0, ks = 0, vs = 0;
-      uint32_t rp = 0, kp = 1, vp = 1;
-      auto turn = [&](const Item &it, int j, int x, bool v) {
-        uint64_t *to_full = v ? &full[5 + vs] : &full[ks], *to_empty = v ? &empty[5 + vs] : &empty[ks];
-        if (ok) ok = mbar_wait(to_empty, v ? vp : kp, P.err);
-        if (ok) ok = mbar_wait(&raw_full[rs], rp, P.err);
+      int ks = 0, vs = 0;
+      uint32_t kp = 0, vp = 0, worked = 0;
+      // One slot: its copy stands in the second half; each thread reads 16 bytes of rows 16 apart, and
+      // when all have, writes them as two pieces of fp16 each.
+      auto turn = [&](auto is_v, const Item &it, int j, int x) {
+        constexpr bool v = decltype(is_v)::value;
+        constexpr int rows = v ? VK : BN, N = C::RAW / 16 / 128;
+        const int at_slot = v ? vs : ks;
+        if (ok) ok = spin_wait(&copied[(v ? 5 : 0) + at_slot], v ? vp : kp, P.err);
         ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          const uint8_t *raw = raws + rs * C::RAW;
-          uint8_t *out = ring + (v ? NK + vs : ks) * SLOT;
-          const int rows = v ? VK : BN;
-          const Blind none = blind(P, it, j);
-          const int row0 = x * VK;
-#pragma unroll 4
-          for (int y = 0; y < C::RAW / 16 / 128; ++y) {
-            const int e = i + 128 * y, g = e / (rows * 8), r = (e >> 3) % rows, c = e & 7;
-            uint4 w = *reinterpret_cast<const uint4 *>(raw + e * 16);
-            if (v && none(row0 + r)) w = make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t z[4] = {w.x, w.y, w.z, w.w};
-            uint32_t f[8];
+        const int r0 = i >> 3, c = i & 7;
+        uint8_t *base = ring + (v ? NK + at_slot : at_slot) * SLOT;
+        uint4 w[N];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) f[2 * u] = e4m3x2_to_f16x2(z[u]), f[2 * u + 1] = e4m3x2_to_f16x2_hi(z[u]);
-            uint8_t *at = out + (2 * g + (c >> 2)) * rows * 128 + r * 128;
-            *reinterpret_cast<uint4 *>(at + (((2 * (c & 3)) ^ (r & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<uint4 *>(at + (((2 * (c & 3) + 1) ^ (r & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(to_full);
-            mbar_arrive(&raw_empty[rs]);
-          }
+        for (int y = 0; y < N; ++y) w[y] = *reinterpret_cast<const uint4 *>(base + C::RAW + i * 16 + y * 2048);
+        if (v && (j <= it.ns || j + 1 == it.n)) {  // slots that no row sees count as zeros
+          const Blind none = blind(P, it, j);
+#pragma unroll
+          for (int y = 0; y < N; ++y)
+            if (none(x * VK + (r0 + 16 * y) % rows)) w[y] = make_uint4(0u, 0u, 0u, 0u);
         }
-        if (++rs == NR) rs = 0, rp ^= 1;
+        named_barrier(6, 128);
+        uint8_t *out = base + (c >> 2) * rows * 128 + r0 * 128;
+        const uint32_t a0 = ((2 * (c & 3)) ^ (r0 & 7)) << 4, a1 = ((2 * (c & 3) + 1) ^ (r0 & 7)) << 4;
+#pragma unroll
+        for (int y = 0; y < N; ++y) {
+          // (16 * y rows on: another pair of column groups behind every `rows`)
+          uint8_t *at = out + (16 * y / rows) * 2 * rows * 128 + (16 * y % rows) * 128;
+          *reinterpret_cast<uint4 *>(at + a0) =
+              make_uint4(e4m3x2_to_f16x2(w[y].x), e4m3x2_to_f16x2_hi(w[y].x), e4m3x2_to_f16x2(w[y].y), e4m3x2_to_f16x2_hi(w[y].y));
+          *reinterpret_cast<uint4 *>(at + a1) =
+              make_uint4(e4m3x2_to_f16x2(w[y].z), e4m3x2_to_f16x2_hi(w[y].z), e4m3x2_to_f16x2(w[y].w), e4m3x2_to_f16x2_hi(w[y].w));
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[(v ? 5 : 0) + at_slot]);
         if (v) {
           if (++vs == NV) vs = 0, vp ^= 1;
         } else if (++ks == NK) {
           ks = 0, kp ^= 1;
         }
       };
-      for (int k = 0; k < parts && ok; ++k) {
-        const Item it = item_at<NT>(P, pre, from.x + k);
+      for (int k = 0; k < parts; ++k) {
+        const Item it = item_at<NT>(P, pre, id_of(k));
         const Part pt = part_of(k, it);
-        for (int j = pt.j0; j <= pt.j1 && ok; ++j) {
-          for (int x = 0; x < PARTS && j < pt.j1; ++x) turn(it, j, x, false);
-          for (int x = 0; x < PARTS && j > pt.j0; ++x) turn(it, j - 1, x, true);
+        if (pt.j0 == pt.j1) continue;
+        // This thread's row of the queries, scaled by a power of two: largest element in [2^14, 2^15).
+        if (ok) ok = spin_wait(q_full, worked & 1, P.err);
+        ok = __all_sync(0xffffffffu, ok);
+        {
+          uint8_t *row = qs + i * 128;
+          auto place = [&](int x) { return reinterpret_cast<uint4 *>(row + (x >> 3) * ROWS * 128 + (((x & 7) ^ (i & 7)) << 4)); };
+          uint32_t mx = 0;  // (of finite values the larger has the larger bits)
+#pragma unroll 8
+          for (int x = 0; x < D / 8; ++x) {
+            const uint4 w = *place(x);
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+          }
+          const int E = imin(imax((int)(max(mx & 0xffffu, mx >> 16) >> 7), 16), 254);
+          const float up = __int_as_float(imin(268 - E, 254) << 23);  // 2^(14 - (E - 127)), 2^127 at most
+          rowscale[(worked & 1) * ROWS + i] = 1.f / up;
+          const f2 up2 = pack2(up, up);
+#pragma unroll 8
+          for (int x = 0; x < D / 8; ++x) {
+            uint4 w = *place(x);
+            auto two = [&](uint32_t y) {
+              const float2 z = unpack2(mul2(pack2(bf16lo(y), bf16hi(y)), up2));
+              return pack_f16x2(z.x, z.y);
+            };
+            w = make_uint4(two(w.x), two(w.y), two(w.z), two(w.w));
+            *place(x) = w;
+          }
+        }
+        ++worked;
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready);
+        for (int j = pt.j0; j <= pt.j1; ++j) {
+          for (int x = 0; x < PARTS && j < pt.j1; ++x) turn(std::false_type{}, it, j, x);
+          for (int x = 0; x < PARTS && j > pt.j0; ++x) turn(std::true_type{}, it, j - 1, x);
         }
       }
       __syncwarp();
@@ -602,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         const int j0 = __shfl_sync(0xffffffffu, info[0], 0), j1 = __shfl_sync(0xffffffffu, info[1], 0);
         const int nt = __shfl_sync(0xffffffffu, info[2], 0);
         if (j1 == 0) break;
-        const Item it = *info_it;
+        const Item it = *info_it;  // (the next part's may stand there before this one's last product)
         // S of the next block for tiles ta..tb1-1; `release`: they are its last
         auto issue_s = [&](int ta, int tb1, bool release, bool last) {
           Cursor at = ck;
@@ -638,8 +703,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         for (int j = j0; j < j1; ++j) {
           const bool more = j + 1 < j1;
           if (NSB == 2 && more) issue_s(0, 1, true, j + 2 == j1);  // runs during this block's softmax
-          const Blind none = blind(P, it, j);  // (e4m3: zeros already)
-          const int upto = F8 ? 0 : (none.c + P.R - 1) & -P.R;  // (pieces behind hold older values)
+          // blocks with slots that no row sees: those up to a window's first, and the last
+          const bool some = !F8 && (j <= it.ns || j + 1 == it.n);  // (e4m3: zeros already)
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             if (t >= nt) continue;
@@ -650,7 +715,9 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
 #pragma unroll
             for (int x = 0; x < PARTS; ++x) {
               if (t == 0) wait(&full[5 + at.slot], at.parity);
-              if (!F8 && t == 0 && (none.a < none.b || none.c < BN)) {
+              if (some && t == 0) {
+                const Blind none = blind(P, it, j);
+                const int upto = (none.c + P.R - 1) & -P.R;  // (pieces behind hold older values)
                 uint8_t *vb = ring + (NK + at.slot) * SLOT;
                 auto clear = [&](int r0, int r1) {  // rows of the block, those of this slot
                   r0 = imax(r0 - x * VK, 0), r1 = imin(r1 - x * VK, VK);
@@ -738,63 +805,18 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       return at[(hf ^ 1) * ROWS + r];
     };
     Item it{};
-    if (parts > 0) it = item_at<NT>(P, pre, from.x);
+    if (parts > 0) it = item_at<NT>(P, pre, id_of(0));
     for (int k = 0; k < parts; ++k) {
       const Part part = part_of(k, it);
       const bool work = part.j1 > part.j0;
       if (t > 0 && it.rows <= P.PT) {  // nothing for this tile
-        if (F8 && work) {  // (one arrival a part from every warp)
-          if (ok) ok = spin_wait(q_full, worked & 1, P.err);
-          ok = __all_sync(0xffffffffu, ok);
-          if (lane == 0) mbar_arrive(q_ready);
-        }
-        worked += work;
-        if (k + 1 < parts) it = item_at<NT>(P, pre, from.x + k + 1);
+        if (k + 1 < parts) it = item_at<NT>(P, pre, id_of(k + 1));
         continue;
       }
       const bool mine = ir < P.PT && t * P.PT + ir < it.rows;  // a row of the prompt
       const int pt = it.p0 + t * P.PT, p = pt + ir;            // position of the tile's first row, of this one
       const int plast = it.p0 + imin(it.rows, (t + 1) * P.PT) - 1;
       float m = -INFINITY, l = 0.f;
-      if (F8 && work) {
-        // This row's queries to fp16, scaled by a power of two (the two halves of a row a half
-        // each): largest element in [2^14, 2^15).
-        if (ok) ok = spin_wait(q_full, worked & 1, P.err);
-        ok = __all_sync(0xffffffffu, ok);
-        constexpr int PC = D / 8 / HALVES;
-        uint8_t *row = qs + t * C::QBYTES + r * 128;
-        auto place = [&](int c) {
-          const int x = hf * PC + c;
-          return reinterpret_cast<uint4 *>(row + (x >> 3) * ROWS * 128 + (((x & 7) ^ (r & 7)) << 4));
-        };
-        uint32_t mx = 0;  // (of finite values the larger has the larger bits)
-#pragma unroll 4
-        for (int c = 0; c < PC; ++c) {
-          const uint4 w = *place(c);
-          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-        }
-        float big = __uint_as_float(max(mx & 0xffffu, mx >> 16) << 16);
-        if (HALVES == 2) big = fmaxf(big, trade(big));
-        const int E = imin(imax(__float_as_int(big) >> 23, 16), 254);
-        const float up = __int_as_float((268 - E < 254 ? 268 - E : 254) << 23);  // 2^(14 - (E - 127)), 2^127 at most
-        sl2e = P.sl2e * (P.ks ? P.ks[it.h] : 1.f) / up;
-        scale2 = pack2(sl2e, sl2e);
-        const f2 up2 = pack2(up, up);
-#pragma unroll 4
-        for (int c = 0; c < PC; ++c) {
-          uint4 w = *place(c);
-          auto two = [&](uint32_t x) {
-            const float2 y = unpack2(mul2(pack2(bf16lo(x), bf16hi(x)), up2));
-            return pack_f16x2(y.x, y.y);
-          };
-          w = make_uint4(two(w.x), two(w.y), two(w.z), two(w.w));
-          *place(c) = w;
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_ready);
-      }
-      worked += work;
       // Both halves of a row take part in every trade whatever `ok` says (the
       // barriers have no time limit); after a wait that ran out only the work
       // is skipped.
@@ -804,6 +826,10 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         if (ok) ok = spin_wait(&s_full[sb], (NSB == 2 ? cnt >> 1 : cnt) & 1, P.err);
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after_sync();
+        if (F8 && j == part.j0) {  // the scale of this row's queries (S is there: so are they, and it)
+          sl2e = P.sl2e * (P.ks ? P.ks[it.h] : 1.f) * rowscale[(worked & 1) * ROWS + r];
+          scale2 = pack2(sl2e, sl2e);
+        }
         uint32_t raw[COLS / 32][32];
         // (after a wait that ran out what stands there has no meaning, and nothing is stored;
         // loads under a condition cost registers)
@@ -893,9 +919,10 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[sb]);
       }
+      worked += work;
       const Item now = it;
       // the next item is looked up while the last product runs
-      if (k + 1 < parts) it = item_at<NT>(P, pre, from.x + k + 1);
+      if (k + 1 < parts) it = item_at<NT>(P, pre, id_of(k + 1));
       if (work) {
         wait_product();
         tc::fence_after_sync();
@@ -908,7 +935,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       constexpr int NG = O0 / 64;
       if (part.j0 > 0 || part.j1 < now.n) {  // a piece of an item: O as it is, maximum and sum
         const size_t at = ((size_t)(2 * blockIdx.x + (part.j0 > 0 ? 0 : 1)) * NT + t) * ROWS + r;
-        if (hf == 0 && ok) P.ml[at] = make_float2(m, l);
+        if (hf == 0 && mine && ok) P.ml[at] = make_float2(m, l);
         float4 *out = reinterpret_cast<float4 *>(P.opart + at * D + hf * O0);
 #pragma unroll 1
         for (int c = 0; c < O0 / 32; ++c) {
@@ -920,7 +947,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_free[t]);
           }
-          if (ok) {
+          if (mine && ok) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               out[8 * c + e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
@@ -988,49 +1015,59 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
 }
 
 
-// Joins the pieces of the item that CTA blockIdx.x begins and does not end: two rows a warp.
+// Joins the pieces of the item that CTA blockIdx.x begins and does not end, a row a warp.
+constexpr int JOIN_BLOCKS = 8;
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params P, int rows, int ctas) {
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params P, int rows) {
   pdl_wait();
   const Cut c = P.cuts[blockIdx.x];
-  if (!c.begins) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pt = ROWS / P.G;
+  if (!c.pieces) return;
+  const int lane = threadIdx.x & 31, pt = ROWS / P.G, n = c.pieces;
   const float vs = P.vs ? P.vs[c.h] : 1.f;
+  // rows of a piece; this CTA's second, then the others' first
+  auto piece = [&](int x) { return (size_t)(2 * (blockIdx.x + x) + (x == 0 ? 1 : 0)) * rows; };
 #pragma unroll 1
-  for (int z = 0; z < 2; ++z) {
-    const int row = blockIdx.y * 16 + warp * 2 + z;
+  for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < rows; row += JOIN_BLOCKS * 8) {
     const int t = row / ROWS, r = row - t * ROWS, ir = r / P.G;
     if (ir >= pt || t * pt + ir >= c.rows) continue;
     float m = -INFINITY, l = 0.f;
     float4 o[D / 128];
 #pragma unroll
     for (int e = 0; e < D / 128; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    int x = blockIdx.x;
-    bool go = true;
-    for (size_t piece = 2 * (size_t)x + 1; go;) {
-      const size_t at = piece * rows + row;
-      const float2 s = P.ml[at];
-      float4 v[D / 128];
+#pragma unroll 1
+    for (int x0 = 0; x0 < n; x0 += 32) {
+      const float2 s = x0 + lane < n ? P.ml[piece(x0 + lane) + row] : make_float2(-INFINITY, 0.f);
+      float top = s.x;
 #pragma unroll
-      for (int e = 0; e < D / 128; ++e) v[e] = *reinterpret_cast<const float4 *>(P.opart + at * D + e * 128 + lane * 4);
-      if (s.x != -INFINITY) {  // (a piece that the row sees nothing of holds anything)
-        const float top = fmaxf(m, s.x), a = m == -INFINITY ? 0.f : ex2_approx(m - top), b = ex2_approx(s.x - top);
-        m = top;
-        l = l * a + s.y * b;
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      top = fmaxf(top, m);
+      const float a = m == -INFINITY ? 0.f : ex2_approx(m - top), w = s.x == -INFINITY ? 0.f : ex2_approx(s.x - top);
+      m = top;
+      l = l * a + s.y * w;
 #pragma unroll
-        for (int e = 0; e < D / 128; ++e)
-          o[e] = make_float4(o[e].x * a + v[e].x * b, o[e].y * a + v[e].y * b, o[e].z * a + v[e].z * b, o[e].w * a + v[e].w * b);
-      }
-      // the next CTA that has a piece
-      int state = ENDS;
-      if (x == blockIdx.x || P.cuts[x].state != ENDS)
-        while (++x < ctas && (state = P.cuts[x].state) == NONE) {
+      for (int e = 0; e < D / 128; ++e) o[e] = make_float4(o[e].x * a, o[e].y * a, o[e].z * a, o[e].w * a);
+      const int some = imin(32, n - x0);
+#pragma unroll 1
+      for (int x = 0; x < some; x += 4) {
+        float4 v[4][D / 128];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float *src = P.opart + (piece(x0 + imin(x + u, some - 1)) + row) * D + lane * 4;
+#pragma unroll
+          for (int e = 0; e < D / 128; ++e) v[u][e] = *reinterpret_cast<const float4 *>(src + e * 128);
         }
-      else
-        x = ctas;
-      go = x < ctas && (state == GOES_ON || state == ENDS);
-      piece = 2 * (size_t)x;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float b = x + u < some ? __shfl_sync(0xffffffffu, w, x + u) : 0.f;
+          if (b == 0.f) continue;  // (a piece that the row sees nothing of holds anything)
+#pragma unroll
+          for (int e = 0; e < D / 128; ++e)
+            o[e] = make_float4(fmaf(v[u][e].x, b, o[e].x), fmaf(v[u][e].y, b, o[e].y), fmaf(v[u][e].z, b, o[e].z), fmaf(v[u][e].w, b, o[e].w));
+        }
+      }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     const float f = l != 0.f ? vs / l : 0.f;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.o.ptr) + (long long)(c.q0 + t * pt + ir) * P.o.token_stride +
                          (long long)(c.h * P.G + r - ir * P.G) * P.o.head_stride;
@@ -1078,9 +1115,10 @@ static sv_status run(const sv_rows *q, const sv_paged_kv *cache, Params &P, int 
       !page_map(&mv, cache->v, cache, D, P.Hkv, P.R, F8 ? 1 : D / 64))
     return SV_ERR_CUDA;
   const size_t prefix = ((size_t)P.B + 1) * 4;
-  P.few_slots = prefix <= HEADER - PREFIX ? 0 : 1;
-  const size_t smem = P.few_slots ? C::PREFIX_AT + prefix : C::RING + 160 * 1024;
-  static_assert(C::RING + 160 * 1024 <= 227 * 1024 && C::PREFIX_AT + (MAX_B + 1) * 4 <= 227 * 1024 + 16, "shared memory");
+  P.few_slots = !F8 && prefix <= HEADER - PREFIX ? 0 : 1;
+  const size_t smem = F8 ? C::SCALES + 2 * ROWS * 4 : P.few_slots ? C::BEHIND + prefix : C::RING + 160 * 1024;
+  static_assert((MAX_KEPT + 1) * 16 <= HEADER - PREFIX, "sequences kept");
+  static_assert(C::RING + 160 * 1024 <= 227 * 1024 && C::SCALES + 2 * ROWS * 4 <= 227 * 1024, "shared memory");
   // at most one tile more per sequence than the rows fill, and no more CTAs than blocks
   P.most = P.Tq / (P.PT * C::NT) + P.B;
   const long long blocks = ((long long)P.width * P.page_size + BN - 1) / BN + 1;
@@ -1089,7 +1127,7 @@ static sv_status run(const sv_rows *q, const sv_paged_kv *cache, Params &P, int 
   cudaError_t e = launch_early(chunk_attn_kernel<D, TILES, F8>, dim3(ctas), dim3(C::THREADS), smem, s, mq, mk, mv, P);
   if (e != cudaSuccess) return SV_ERR_CUDA;
   if (ctas == 1) return SV_OK;
-  return from_cuda(launch_early(join_kernel<D>, dim3(ctas - 1, C::NT * ROWS / 16), dim3(256), 0, s, P, C::NT * ROWS, ctas));
+  return from_cuda(launch_early(join_kernel<D>, dim3(ctas - 1, JOIN_BLOCKS), dim3(256), 0, s, P, C::NT * ROWS));
 }
 
 template <bool F8>
