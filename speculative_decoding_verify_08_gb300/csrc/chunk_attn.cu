@@ -10,7 +10,7 @@
 // tensor cores; for few rows the stream of the cache.  The products, the softmax
 // between them and the tiles are window_attn's (128 query rows of one KV head a tile,
 // S and P in tensor memory, O accumulated there); what differs:
-//  * Keys and values come from pages: a copy is R = 16 or 32 slots (a divisor of the
+//  * Keys and values come from pages: a copy is R = 16, 32 or 64 slots (a divisor of the
 //    page size), one lane of the copying warp a copy, each looking its page up a
 //    block ahead.  Blocks of a window begin at a multiple of R.
 //  * The work is a line of all items (tiles of all KV heads), each as long as its
@@ -24,8 +24,9 @@
 //    to fp16 tiles there (each value exactly);
 //    queries are scaled by a power of two per row and turned to fp16 in place
 //    (exact down to 2^-14 of a row's largest element, off by 2^-25 of that below), and
-//    probabilities are taken 2^13 times as large, and their sum with them, so that
-//    those down to 2^-27 of the maximum keep 2^-11 (smaller ones are off by 2^-38 of it).
+//    probabilities are taken 2^10 times as large, and their sum with them, so that
+//    those down to 2^-24 of the maximum keep 2^-11 (smaller ones are off by 2^-35 of it; the
+//    maximum that they refer to is raised when a block exceeds it by more than 2^5).
 #include <type_traits>
 
 #include "paged.cuh"
@@ -39,7 +40,6 @@ namespace chunk {
 
 constexpr int ROWS = 128;           // rows of a tile (TMEM lanes)
 constexpr int BN = 128;             // keys of a block
-constexpr int PIECE = 32;           // first keys that may share a block with others
 constexpr int MAX_B = 4096;
 constexpr int HEAD_COST = 2;        // blocks' time that an item takes beside its blocks
 // Shared memory: barriers, the CTA's cuts (256), more barriers (280), the item
@@ -64,7 +64,8 @@ struct Cfg {
   static constexpr int QBYTES = ROWS * D * 2;
   static constexpr int RING = HEADER + NT * QBYTES;
   // slots of the K and the V ring: 160 KB, or 128 beside long prefix sums and e4m3's scales
-  static constexpr int NK = 2, NV = 3, LESS = 2;
+  // (At D = 256 a block takes two slots of each, and the next block's keys are needed first.)
+  static constexpr int NK = D == 256 ? 3 : 2, NV = 5 - NK, LESS = 2;
   static_assert((NK + NV) * SLOT == 160 * 1024 && 2 * LESS * SLOT == 128 * 1024, "ring");
   static constexpr int BEHIND = RING + 128 * 1024;  // prefix sums
   static constexpr int SCALES = BEHIND + ((MAX_B + 1) * 4 + 15) / 16 * 16;  // [2][ROWS] of e4m3's queries
@@ -76,7 +77,7 @@ struct Cfg {
   static_assert(256 * SOFT_REGS + (THREADS - 256) * OTHER_REGS <= (65536 / THREADS / 8 * 8) * THREADS, "registers");
   // log2 of the factor on probabilities and their sum, and of the largest P against an
   // old maximum, factor included
-  static constexpr float LIFT = F8 ? 13.f : 0.f, RESCALE = F8 ? 2.f : 8.f;
+  static constexpr float LIFT = F8 ? 10.f : 0.f, RESCALE = F8 ? 5.f : 8.f;
 };
 
 // Item that a CTA begins and does not end: its pieces are this CTA's second and the first of
@@ -89,7 +90,8 @@ struct Params {
   sv_rows o;
   const int *cu_q, *lens, *table;
   long long table_stride;
-  int width, page_size, num_pages, R;  // R: slots of a copy
+  int width, page_size, num_pages;
+  int R, piece;  // slots of a copy; first keys that may share a block with others (whole copies)
   const float *ks, *vs;
   float *opart;  // [2 * ctas][NT * ROWS][D] unnormalised O
   float2 *ml;    // [2 * ctas][NT * ROWS] maximum (log2 domain) and sum
@@ -110,8 +112,8 @@ struct Item {
   int p0, len;       // position of its first row; slots of the sequence
   int from;          // positions before it that are not among the first `sinks` are seen by no row of the sequence
   // Blocks: ns over the first keys, then those from key w0 on; n in all.  Up to
-  // PIECE first keys far from the window (ns = 0, w0 > 0, sinks) need no block:
-  // keys 0..PIECE-1 stand in the first block's first rows, for w0..w0+PIECE-1.
+  // `piece` first keys far from the window (ns = 0, w0 > 0, sinks) need no block:
+  // keys 0..piece-1 stand in the first block's first rows, for w0..w0+piece-1.
   int ns, skip, n;
   __device__ __forceinline__ int base(int j) const { return j * BN + (j < ns ? 0 : skip); }
 };
@@ -170,8 +172,8 @@ __device__ __forceinline__ Item tile_at(const Params &P, const int *pre, int c, 
   const int end = imax(0, it.p0 + it.rows);  // of the keys that some row sees
   const int start = P.window > 0 ? imin(end, imax(0, it.p0 - P.window + 1)) : 0;
   const int first = imin(P.sinks, end);
-  it.ns = first > PIECE ? (first + BN - 1) / BN : 0;
-  int w0 = first > PIECE || first == 0 ? start : imax(0, start - PIECE);
+  it.ns = first > P.piece ? (first + BN - 1) / BN : 0;
+  int w0 = first > P.piece || first == 0 ? start : imax(0, start - P.piece);
   w0 &= -P.R;
   if (w0 <= it.ns * BN) w0 = it.ns = 0;
   it.skip = w0 - it.ns * BN;
@@ -190,7 +192,7 @@ __device__ __forceinline__ bool heads(const Params &P, const Item &it, int j) {
 }
 // Position of row r of block j.
 __device__ __forceinline__ int position(const Params &P, const Item &it, int j, int r) {
-  return r < PIECE && heads(P, it, j) ? r : it.base(j) + r;
+  return r < P.piece && heads(P, it, j) ? r : it.base(j) + r;
 }
 // Rows of block j that no row of the sequence sees (or none of the item): a..b-1, and those from c on.
 struct Blind {
@@ -200,7 +202,7 @@ struct Blind {
 __device__ __forceinline__ Blind blind(const Params &P, const Item &it, int j) {
   const int base = it.base(j);
   const bool h = heads(P, it, j);
-  return Blind{h ? P.sinks : imax(0, P.sinks - base), h ? imax(PIECE, it.from - base) : it.from - base, it.len - base};
+  return Blind{h ? P.sinks : imax(0, P.sinks - base), h ? imax(P.piece, it.from - base) : it.from - base, it.len - base};
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   float *rowscale = reinterpret_cast<float *>(smem + C::SCALES);  // e4m3: [2][ROWS] what the rows' scores are multiplied by
   uint8_t *qs = smem + HEADER;
   uint8_t *ring = smem + C::RING;
-  const int NK = C::NK, NV = P.few_slots ? C::LESS : C::NV;
+  const int NK = P.few_slots ? C::LESS : C::NK, NV = P.few_slots ? C::LESS : C::NV;
   int *pre = reinterpret_cast<int *>(smem + (P.few_slots ? C::BEHIND : PREFIX));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -633,7 +635,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32), k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32);
       const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
       // of 16 keys' step ks in a slot of values: piece by piece, all column groups of one together
-      const int lg = F8 ? 31 : P.R == 32 ? 1 : 0;  // log2 of steps a piece
+      const int lg = F8 ? 4 : P.R == 64 ? 2 : P.R == 32 ? 1 : 0, steps = (1 << lg) - 1;  // log2 of steps a piece
       const uint32_t piece = (uint32_t)VR * 128 * (D / 64) / 16;
       const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
       const bool leader = tc::elect_one();
@@ -742,7 +744,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
                   const uint32_t va = v_lo + at.slot * (SLOT / 16);
 #pragma unroll
                   for (int ks = y * (VK / 16 / STEPS); ks < (y + 1) * (VK / 16 / STEPS); ++ks) {
-                    const uint32_t vo = F8 ? ks * (2048 / 16) : (uint32_t)(ks >> lg) * piece + (uint32_t)(ks & lg) * (2048 / 16);
+                    const uint32_t vo = (uint32_t)(ks >> lg) * piece + (uint32_t)(ks & steps) * (2048 / 16);
                     tc::mma_bf16_ts(tb + C::TO + t * D, tb + C::TS + sb * BN + (x * (VK / 16) + ks) * 8,
                                     va + vo, v_hi, IDO, (x > 0 || ks > 0) ? 1u : (uint32_t)(j > j0));
                   }
@@ -1110,7 +1112,8 @@ template <int D, int TILES, bool F8>
 static sv_status run(const sv_rows *q, const sv_paged_kv *cache, Params &P, int sms, cudaStream_t s) {
   using C = Cfg<D, TILES, F8>;
   CUtensorMap mq, mk, mv;
-  P.R = P.page_size % 32 == 0 ? 32 : 16;
+  P.R = P.page_size % 64 == 0 ? 64 : P.page_size % 32 == 0 ? 32 : 16;
+  P.piece = imax(P.R, 32);
   if (!query_map(&mq, q, P.Tq, P.Hkv * P.G, D, P.G, P.PT) || !page_map(&mk, cache->k, cache, D, P.Hkv, P.R, 1) ||
       !page_map(&mv, cache->v, cache, D, P.Hkv, P.R, F8 ? 1 : D / 64))
     return SV_ERR_CUDA;
