@@ -68,12 +68,12 @@ struct Cfg {
   static constexpr int NK = D == 256 ? 3 : 2, NV = 5 - NK, LESS = 2;
   static_assert((NK + NV) * SLOT == 160 * 1024 && 2 * LESS * SLOT == 128 * 1024, "ring");
   static constexpr int BEHIND = RING + 128 * 1024;  // prefix sums
-  static constexpr int SCALES = BEHIND + ((MAX_B + 1) * 4 + 15) / 16 * 16;  // [2][ROWS] of e4m3's queries
+  static constexpr int SCALES = BEHIND + ((MAX_B + 1) * 4 + 15) / 16 * 16;  // [2][NT][ROWS] of e4m3's queries
   // tensor memory: O per tile, then the S buffers (P over S)
   static constexpr uint32_t TO = 0, TS = NT * D;
   static_assert(NT * D + NT * NSB * BN <= 512, "tensor memory");
   // registers: as many as the threads start with
-  static constexpr int SOFT_REGS = F8 ? 184 : 216, OTHER_REGS = 72;
+  static constexpr int SOFT_REGS = F8 ? (NT == 2 ? 208 : 184) : 216, OTHER_REGS = F8 && NT == 2 ? 48 : 72;
   static_assert(256 * SOFT_REGS + (THREADS - 256) * OTHER_REGS <= (65536 / THREADS / 8 * 8) * THREADS, "registers");
   // log2 of the factor on probabilities and their sum, and of the largest P against an
   // old maximum, factor included
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   Item *info_it = reinterpret_cast<Item *>(smem + INFO);  // of the item whose queries landed
   int *info = reinterpret_cast<int *>(smem + INFO + 48);  // its first block, its end, its tiles
   float *xchg = reinterpret_cast<float *>(smem + 512);  // [2][2 halves][ROWS] maxima, then sums
-  float *rowscale = reinterpret_cast<float *>(smem + C::SCALES);  // e4m3: [2][ROWS] what the rows' scores are multiplied by
+  float *rowscale = reinterpret_cast<float *>(smem + C::SCALES);  // e4m3: [2][NT][ROWS] what the rows' scores are multiplied by
   uint8_t *qs = smem + HEADER;
   uint8_t *ring = smem + C::RING;
   const int NK = P.few_slots ? C::LESS : C::NK, NV = P.few_slots ? C::LESS : C::NV;
@@ -542,36 +542,40 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       bool ok = true;
       int ks = 0, vs = 0;
       uint32_t kp = 0, vp = 0, worked = 0;
-      // One slot: its copy stands in the second half; each thread reads 16 bytes of rows 16 apart, and
-      // when all have, writes them as two pieces of fp16 each.
+      // One slot: its copy stands in the second half.  The half of the columns whose fp16 tiles lie in the
+      // first half comes first, then, once all have read them, the rest.
       auto turn = [&](auto is_v, const Item &it, int j, int x) {
         constexpr bool v = decltype(is_v)::value;
-        constexpr int rows = v ? VK : BN, N = C::RAW / 16 / 128;
+        constexpr bool whole = (v ? VK : BN) == 64;  // a half of the copy: all pieces of 64 rows, or half of those of 128
+        constexpr int gap = whole ? 16 : 32;         // rows between a thread's pieces
         const int at_slot = v ? vs : ks;
         if (ok) ok = spin_wait(&copied[(v ? 5 : 0) + at_slot], v ? vp : kp, P.err);
         ok = __all_sync(0xffffffffu, ok);
-        const int r0 = i >> 3, c = i & 7;
         uint8_t *base = ring + (v ? NK + at_slot : at_slot) * SLOT;
-        uint4 w[N];
+        const int r0 = whole ? i >> 3 : i >> 2, c = whole ? i & 7 : i & 3;
+        Blind none{0, 0, BN};
+        if (v && (j <= it.ns || j + 1 == it.n)) none = blind(P, it, j);
 #pragma unroll
-        for (int y = 0; y < N; ++y) w[y] = *reinterpret_cast<const uint4 *>(base + C::RAW + i * 16 + y * 2048);
-        if (v && (j <= it.ns || j + 1 == it.n)) {  // slots that no row sees count as zeros
-          const Blind none = blind(P, it, j);
+        for (int half = 0; half < 2; ++half) {
+          const uint8_t *raw = base + C::RAW + (whole ? half * 8192 + r0 * 128 + c * 16 : r0 * 128 + (4 * half + c) * 16);
+          uint4 w[4];
 #pragma unroll
-          for (int y = 0; y < N; ++y)
-            if (none(x * VK + (r0 + 16 * y) % rows)) w[y] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        named_barrier(6, 128);
-        uint8_t *out = base + (c >> 2) * rows * 128 + r0 * 128;
-        const uint32_t a0 = ((2 * (c & 3)) ^ (r0 & 7)) << 4, a1 = ((2 * (c & 3) + 1) ^ (r0 & 7)) << 4;
+          for (int y = 0; y < 4; ++y) w[y] = *reinterpret_cast<const uint4 *>(raw + y * gap * 128);
+          if (v && (none.a < none.b || none.c < BN)) {  // slots that no row sees count as zeros
 #pragma unroll
-        for (int y = 0; y < N; ++y) {
-          // (16 * y rows on: another pair of column groups behind every `rows`)
-          uint8_t *at = out + (16 * y / rows) * 2 * rows * 128 + (16 * y % rows) * 128;
-          *reinterpret_cast<uint4 *>(at + a0) =
-              make_uint4(e4m3x2_to_f16x2(w[y].x), e4m3x2_to_f16x2_hi(w[y].x), e4m3x2_to_f16x2(w[y].y), e4m3x2_to_f16x2_hi(w[y].y));
-          *reinterpret_cast<uint4 *>(at + a1) =
-              make_uint4(e4m3x2_to_f16x2(w[y].z), e4m3x2_to_f16x2_hi(w[y].z), e4m3x2_to_f16x2(w[y].w), e4m3x2_to_f16x2_hi(w[y].w));
+            for (int y = 0; y < 4; ++y)
+              if (none(x * VK + r0 + gap * y)) w[y] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          if (half == 1) named_barrier(6, 128);
+          uint8_t *out = base + half * C::RAW + (whole ? (c >> 2) * 8192 : 0) + r0 * 128;
+          const uint32_t a0 = ((2 * (c & 3)) ^ (r0 & 7)) << 4, a1 = ((2 * (c & 3) + 1) ^ (r0 & 7)) << 4;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            *reinterpret_cast<uint4 *>(out + y * gap * 128 + a0) =
+                make_uint4(e4m3x2_to_f16x2(w[y].x), e4m3x2_to_f16x2_hi(w[y].x), e4m3x2_to_f16x2(w[y].y), e4m3x2_to_f16x2_hi(w[y].y));
+            *reinterpret_cast<uint4 *>(out + y * gap * 128 + a1) =
+                make_uint4(e4m3x2_to_f16x2(w[y].z), e4m3x2_to_f16x2_hi(w[y].z), e4m3x2_to_f16x2(w[y].w), e4m3x2_to_f16x2_hi(w[y].w));
+          }
         }
         fence_proxy_async();
         __syncwarp();
@@ -589,8 +593,9 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         // This thread's row of the queries, scaled by a power of two: largest element in [2^14, 2^15).
         if (ok) ok = spin_wait(q_full, worked & 1, P.err);
         ok = __all_sync(0xffffffffu, ok);
-        {
-          uint8_t *row = qs + i * 128;
+#pragma unroll 1
+        for (int t = 0; t < NT; ++t) {
+          uint8_t *row = qs + t * C::QBYTES + i * 128;
           auto place = [&](int x) { return reinterpret_cast<uint4 *>(row + (x >> 3) * ROWS * 128 + (((x & 7) ^ (i & 7)) << 4)); };
           uint32_t mx = 0;  // (of finite values the larger has the larger bits)
 #pragma unroll 8
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
           }
           const int E = imin(imax((int)(max(mx & 0xffffu, mx >> 16) >> 7), 16), 254);
           const float up = __int_as_float(imin(268 - E, 254) << 23);  // 2^(14 - (E - 127)), 2^127 at most
-          rowscale[(worked & 1) * ROWS + i] = 1.f / up;
+          rowscale[((worked & 1) * NT + t) * ROWS + i] = 1.f / up;
           const f2 up2 = pack2(up, up);
 #pragma unroll 8
           for (int x = 0; x < D / 8; ++x) {
@@ -812,6 +817,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       const Part part = part_of(k, it);
       const bool work = part.j1 > part.j0;
       if (t > 0 && it.rows <= P.PT) {  // nothing for this tile
+        worked += work;
         if (k + 1 < parts) it = item_at<NT>(P, pre, id_of(k + 1));
         continue;
       }
@@ -829,7 +835,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after_sync();
         if (F8 && j == part.j0) {  // the scale of this row's queries (S is there: so are they, and it)
-          sl2e = P.sl2e * (P.ks ? P.ks[it.h] : 1.f) * rowscale[(worked & 1) * ROWS + r];
+          sl2e = P.sl2e * (P.ks ? P.ks[it.h] : 1.f) * rowscale[((worked & 1) * NT + t) * ROWS + r];
           scale2 = pack2(sl2e, sl2e);
         }
         uint32_t raw[COLS / 32][32];
@@ -1119,9 +1125,9 @@ static sv_status run(const sv_rows *q, const sv_paged_kv *cache, Params &P, int 
     return SV_ERR_CUDA;
   const size_t prefix = ((size_t)P.B + 1) * 4;
   P.few_slots = !F8 && prefix <= HEADER - PREFIX ? 0 : 1;
-  const size_t smem = F8 ? C::SCALES + 2 * ROWS * 4 : P.few_slots ? C::BEHIND + prefix : C::RING + 160 * 1024;
+  const size_t smem = F8 ? C::SCALES + 2 * C::NT * ROWS * 4 : P.few_slots ? C::BEHIND + prefix : C::RING + 160 * 1024;
   static_assert((MAX_KEPT + 1) * 16 <= HEADER - PREFIX, "sequences kept");
-  static_assert(C::RING + 160 * 1024 <= 227 * 1024 && C::SCALES + 2 * ROWS * 4 <= 227 * 1024, "shared memory");
+  static_assert(C::RING + 160 * 1024 <= 227 * 1024 && C::SCALES + 2 * C::NT * ROWS * 4 <= 227 * 1024, "shared memory");
   // at most one tile more per sequence than the rows fill, and no more CTAs than blocks
   P.most = P.Tq / (P.PT * C::NT) + P.B;
   const long long blocks = ((long long)P.width * P.page_size + BN - 1) / BN + 1;
@@ -1137,10 +1143,8 @@ template <bool F8>
 static sv_status run_any(const sv_rows *q, const sv_paged_kv *cache, Params &P, int D, int sms, cudaStream_t s) {
   if (D == 256) return run<256, 1, F8>(q, cache, P, sms, s);
   // Two tiles a CTA share each block of keys; they pay where most sequences fill more than
-  // one.  (Beside the conversions of e4m3 their softmax, a row a thread, has too few registers.)
-  if constexpr (!F8)
-    if (P.Tq > (long long)P.B * P.PT) return run<128, 2, false>(q, cache, P, sms, s);
-  return run<128, 1, F8>(q, cache, P, sms, s);
+  // one.
+  return P.Tq > (long long)P.B * P.PT ? run<128, 2, F8>(q, cache, P, sms, s) : run<128, 1, F8>(q, cache, P, sms, s);
 }
 
 // Pieces of cut items: two a CTA.
