@@ -57,7 +57,7 @@ __device__ __forceinline__ void stage_rows(float *dst, const sv_rows &src, long 
 }
 
 template <int DK>
-__global__ void __launch_bounds__(256) tokens_kernel(const __grid_constant__ PoolParams P) {
+__global__ void __launch_bounds__(256, DK <= 128 ? 6 : 4) tokens_kernel(const __grid_constant__ PoolParams P) {
   constexpr int NJ = DK / 32;
   extern __shared__ __align__(16) float sm[];
   const int rows = blockDim.x / LPR;
@@ -142,13 +142,225 @@ __global__ void __launch_bounds__(256) tokens_kernel(const __grid_constant__ Poo
   }
 }
 
+// ---- many states: a stream of tiles of 32 rows through shared memory ----
+constexpr int TILE = 32, TOKENS = 16;  // rows of a tile; tokens of a sequence (tape and own) at most
+constexpr int WORK_WARPS = TILE * LPR / 32, STREAM_THREADS = (WORK_WARPS + 2) * 32;
+
+template <int DK>
+struct SL {
+  static constexpr int STATE = TILE * DK * 4;
+  // of a stage: the rows of S, the tokens' gates (a, b), what the tile is, the tokens
+  static constexpr int GATES = STATE, META = GATES + TOKENS * 8, TOKEN = META + 16;
+  static constexpr int EACH = 4 * DK + 2 * TILE;  // bytes of a token: key, query, values
+  __host__ __device__ static int stage(int tokens) { return (TOKEN + tokens * EACH + 127) / 128 * 128; }
+};
+
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// The same rule on the same lanes.  What differs: a block walks over tiles (sequence, head, 32
+// rows), one warp asking for the next ones' states, keys, queries and values by bulk copies, one
+// writing the states back; as many bytes are on their way as the ring holds, whatever the
+// tiles' own latency (61 sequences of 48 heads: 80 us with a block a tile, STREAM_US this way).
+template <int DK>
+__global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_constant__ PoolParams P, int stages, int tiles, int row_tiles) {
+  using Y = SL<DK>;
+  constexpr int NJ = DK / 32;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[16], done[16], empty[16];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tape = P.tape_M, tokens = tape + P.M, size = Y::stage(tokens);
+  if (tid == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&done[i], WORK_WARPS);
+      mbar_init(&empty[i], 1);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  const int mine = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  // sequence, head and first row of this block's k-th tile
+  struct Where {
+    int b, h, i0;
+  };
+  auto where = [&](int k) {
+    const int t = blockIdx.x + k * gridDim.x, x = t / row_tiles, b = x / P.Hv;
+    return Where{b, x - b * P.Hv, (t - x * row_tiles) * TILE};
+  };
+  bool ok = true;
+  if (warp == WORK_WARPS) {
+    // ------------------------------------------------------------ copies in --
+    struct Ask {  // of a tile, asked for one tile ahead
+      Where w;
+      int slot, replay;
+      float g, b;  // of token `lane`
+    };
+    auto ask = [&](int k) {
+      Ask a{};
+      a.w = where(k);
+      a.slot = P.slots[a.w.b];
+      a.replay = P.n_replay ? P.n_replay[a.w.b] : 0;
+      if (lane < tokens) {
+        const bool own = lane >= tape;
+        const long long at = (own ? (long long)a.w.b * P.M + lane - tape : (long long)a.w.b * tape + lane) * P.Hv + a.w.h;
+        a.g = own ? P.g[at] : P.tg[at];
+        a.b = own ? P.b[at] : P.tb[at];
+      }
+      return a;
+    };
+    Ask next{};
+    if (mine > 0) next = ask(0);
+    for (int k = 0; k < mine && ok; ++k) {
+      Ask a = next;
+      if (k + 1 < mine) next = ask(k + 1);
+      const int st = k % stages;
+      if (k >= stages && lane == 0) ok = mbar_wait(&empty[st], (k / stages - 1) & 1, P.err);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      uint8_t *at = ring + st * size;
+      if (a.slot >= P.states.num_slots || a.replay < 0 || a.replay > tape) {
+        if (lane == 0) atomicOr(P.err, ERR_INDEX);
+        a.slot = a.slot >= P.states.num_slots ? -1 : a.slot;
+        a.replay = imin(imax(a.replay, 0), tape);
+      }
+      if (lane < tokens) *reinterpret_cast<float2 *>(at + Y::GATES + lane * 8) = make_float2(expf(a.g), a.b);
+      if (lane == 0) *reinterpret_cast<int2 *>(at + Y::META) = make_int2(a.slot, a.replay);
+      __syncwarp();
+      const int rows = imin(TILE, P.dv - a.w.i0);
+      const uint32_t state = a.slot >= 0 ? rows * DK * 4 : 0, values = rows * 2;
+      if (lane == 0)
+        mbar_arrive_expect_tx(&full[st], state + a.replay * (DK * 2 + values) + P.M * (DK * 4 + values));
+      __syncwarp();
+      const int hk = a.w.h / (P.Hv / P.Hk);
+      if (lane == 31 && state)
+        bulk_load(at, P.states.ptr + a.slot * P.states.slot_stride + ((long long)a.w.h * P.dv + a.w.i0) * DK, state, &full[st]);
+      if (lane < tape ? lane < a.replay : lane < tokens) {
+        const bool own = lane >= tape;
+        const long long t = own ? (long long)a.w.b * P.M + lane - tape : (long long)a.w.b * tape + lane;
+        const sv_rows &K = own ? P.k : P.tk, &V = own ? P.v : P.tv;
+        uint8_t *to = at + Y::TOKEN + lane * Y::EACH;
+        bulk_load(to, static_cast<const __nv_bfloat16 *>(K.ptr) + t * K.token_stride + hk * K.head_stride, DK * 2, &full[st]);
+        if (own) bulk_load(to + DK * 2, static_cast<const __nv_bfloat16 *>(P.q.ptr) + t * P.q.token_stride + hk * P.q.head_stride, DK * 2, &full[st]);
+        bulk_load(to + DK * 4, static_cast<const __nv_bfloat16 *>(V.ptr) + t * V.token_stride + a.w.h * V.head_stride + a.w.i0, values, &full[st]);
+      }
+      __syncwarp();
+    }
+  } else if (warp == WORK_WARPS + 1) {
+    // ----------------------------------------------------------- states out --
+    if (lane == 0) {
+      int k = 0;
+      for (; k < mine; ++k) {
+        const int st = k % stages;
+        if (!mbar_wait(&done[st], (k / stages) & 1, P.err)) break;
+        uint8_t *at = ring + st * size;
+        const int2 meta = *reinterpret_cast<const int2 *>(at + Y::META);
+        if (meta.x >= 0 && (meta.y > 0 || (P.commit && P.M > 0))) {
+          const Where w = where(k);
+          bulk_store(P.states.ptr + meta.x * P.states.slot_stride + ((long long)w.h * P.dv + w.i0) * DK, at, imin(TILE, P.dv - w.i0) * DK * 4);
+        }
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        // the tile before this one has been read out
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        if (k > 0) mbar_arrive(&empty[(k - 1) % stages]);
+      }
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      if (k == mine && k > 0) mbar_arrive(&empty[(k - 1) % stages]);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- rows --
+    const int r = tid / LPR, sub = tid % LPR;
+    for (int k = 0; k < mine; ++k) {
+      const int st = k % stages;
+      if (ok) ok = mbar_wait(&full[st], (k / stages) & 1, P.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      uint8_t *at = ring + st * size;
+      const Where w = where(k);
+      const bool live = w.i0 + r < P.dv;
+      const int2 meta = *reinterpret_cast<const int2 *>(at + Y::META);
+      float *srow = reinterpret_cast<float *>(at) + r * DK + sub * 4;
+      f2 row[2 * NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const ulonglong2 x = meta.x >= 0 && live ? *reinterpret_cast<const ulonglong2 *>(srow + 32 * j) : make_ulonglong2(0, 0);
+        row[2 * j] = x.x, row[2 * j + 1] = x.y;
+      }
+      auto keep = [&]() {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          if (live) *reinterpret_cast<ulonglong2 *>(srow + 32 * j) = make_ulonglong2(row[2 * j], row[2 * j + 1]);
+      };
+      auto dot = [&](const uint8_t *x) {  // with a row of bf16
+        f2 s[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const uint2 y = *reinterpret_cast<const uint2 *>(x + sub * 8 + 64 * j);
+          s[0] = fma2(row[2 * j], pack2(bf16lo(y.x), bf16hi(y.x)), s[0]);
+          s[1] = fma2(row[2 * j + 1], pack2(bf16lo(y.y), bf16hi(y.y)), s[1]);
+        }
+        const float2 z = unpack2(add2(s[0], s[1]));
+        return over_row(z.x + z.y);
+      };
+      auto token = [&](int n) {
+        const uint8_t *x = at + Y::TOKEN + n * Y::EACH;
+        const float2 ab = *reinterpret_cast<const float2 *>(at + Y::GATES + n * 8);
+        const float v = live ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(x + DK * 4)[r]) : 0.f;
+        const float u = ab.y * (v - ab.x * dot(x));
+        const f2 a2 = pack2(ab.x, ab.x), u2 = pack2(u, u);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const uint2 y = *reinterpret_cast<const uint2 *>(x + sub * 8 + 64 * j);
+          row[2 * j] = fma2(a2, row[2 * j], mul2(u2, pack2(bf16lo(y.x), bf16hi(y.x))));
+          row[2 * j + 1] = fma2(a2, row[2 * j + 1], mul2(u2, pack2(bf16lo(y.y), bf16hi(y.y))));
+        }
+      };
+#pragma unroll 1
+      for (int n = 0; n < meta.y; ++n) token(n);
+      if (!P.commit && meta.y > 0) keep();
+#pragma unroll 1
+      for (int n = 0; n < P.M; ++n) {
+        token(tape + n);
+        const float ov = dot(at + Y::TOKEN + (tape + n) * Y::EACH + DK * 2);
+        if (sub == 0 && live) {
+          const long long o = ((long long)w.b * P.M + n) * P.o.token_stride + w.h * P.o.head_stride + w.i0 + r;
+          if (P.o_f32)
+            static_cast<float *>(P.o.ptr)[o] = ov;
+          else
+            static_cast<__nv_bfloat16 *>(P.o.ptr)[o] = __float2bfloat16_rn(ov);
+        }
+      }
+      if (P.commit) keep();
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&done[st]);
+    }
+  }
+}
+
 template <int DK>
 sv_status run_tokens(PoolParams &P, cudaStream_t s) {
-  // Blocks of eight rows while that leaves each SM few of them (one sequence of
-  // 48 heads: 768), of 32 beyond, where what a block stages is shared by more rows.
   const long long small = (long long)P.B * P.Hv * ((P.dv + 7) / 8);
   const int sms = device_sm_count();
   if (sms <= 0) return SV_ERR_CUDA;
+  // Few tokens of many states are streamed (values in whole 16 bytes); it pays from some
+  // tiles a block on.
+  const int row_tiles = (P.dv + TILE - 1) / TILE;
+  const long long tiles = (long long)P.B * P.Hv * row_tiles;
+  if (!P.cu && P.tape_M + P.M <= TOKENS && P.dv % 8 == 0 && tiles >= 8LL * sms && tiles <= 0x7fffffffLL) {
+    const int size = SL<DK>::stage(P.tape_M + P.M), stages = imin(16, 110 * 1024 / size);
+    return from_cuda(launch_early(stream_kernel<DK>, dim3(2 * sms), dim3(STREAM_THREADS), (size_t)stages * size, s, P, stages, (int)tiles, row_tiles));
+  }
+  // Otherwise a block a few rows: eight while that leaves each SM few of them (one sequence of
+  // 48 heads: 768), 32 beyond, where what a block stages is shared by more rows.
   const int threads = small > 16LL * sms ? 256 : 64, rows = threads / LPR;
   const size_t smem = (size_t)P.stage * (2 * DK + rows + 2) * 4;
   return from_cuda(launch_early(tokens_kernel<DK>, dim3((P.dv + rows - 1) / rows, P.Hv, P.B), dim3(threads), smem, s, P));
