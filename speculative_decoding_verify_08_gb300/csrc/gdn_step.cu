@@ -142,12 +142,14 @@ __global__ void __launch_bounds__(256, DK <= 128 ? 6 : 4) tokens_kernel(const __
   }
 }
 
-// ---- many states: a stream of tiles of 32 rows through shared memory ----
-constexpr int TILE = 32, TOKENS = 16;  // rows of a tile; tokens of a sequence (tape and own) at most
-constexpr int WORK_WARPS = TILE * LPR / 32, STREAM_THREADS = (WORK_WARPS + 2) * 32;
+// ---- many states: a stream of tiles through shared memory ----
+constexpr int TOKENS = 16;  // tokens of a sequence (tape and own) at most
+constexpr int WORK_WARPS = 8, STREAM_THREADS = (WORK_WARPS + 2) * 32;
 
 template <int DK>
 struct SL {
+  // Rows of a thread: two share its reads of a key.  Rows of a tile.
+  static constexpr int RP = DK <= 128 ? 2 : 1, TILE = RP * WORK_WARPS * 32 / LPR;
   static constexpr int STATE = TILE * DK * 4;
   // of a stage: the rows of S, the tokens' gates (a, b), what the tile is, the tokens
   static constexpr int GATES = STATE, META = GATES + TOKENS * 8, TOKEN = META + 16;
@@ -164,14 +166,14 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                : "memory");
 }
 
-// The same rule on the same lanes.  What differs: a block walks over tiles (sequence, head, 32
-// rows), one warp asking for the next ones' states, keys, queries and values by bulk copies, one
+// The same rule on the same lanes.  What differs: a block walks over tiles (sequence, head, 64
+// or 32 rows), one warp asking for the next ones' states, keys, queries and values by bulk copies, one
 // writing the states back; as many bytes are on their way as the ring holds, whatever the
 // tiles' own latency (61 sequences of 48 heads: 80 us with a block a tile, STREAM_US this way).
 template <int DK>
 __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_constant__ PoolParams P, int stages, int tiles, int row_tiles) {
   using Y = SL<DK>;
-  constexpr int NJ = DK / 32;
+  constexpr int NJ = DK / 32, RP = Y::RP, TILE = Y::TILE;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[16], done[16], empty[16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -285,42 +287,61 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_
       if (!ok) break;
       uint8_t *at = ring + st * size;
       const Where w = where(k);
-      const bool live = w.i0 + r < P.dv;
       const int2 meta = *reinterpret_cast<const int2 *>(at + Y::META);
-      float *srow = reinterpret_cast<float *>(at) + r * DK + sub * 4;
-      f2 row[2 * NJ];
+      float *srow = reinterpret_cast<float *>(at) + r * DK + sub * 4;  // (rows of a thread: 32 apart)
+      f2 row[RP][2 * NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const ulonglong2 x = meta.x >= 0 && live ? *reinterpret_cast<const ulonglong2 *>(srow + 32 * j) : make_ulonglong2(0, 0);
-        row[2 * j] = x.x, row[2 * j + 1] = x.y;
-      }
-      auto keep = [&]() {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          if (live) *reinterpret_cast<ulonglong2 *>(srow + 32 * j) = make_ulonglong2(row[2 * j], row[2 * j + 1]);
-      };
-      auto dot = [&](const uint8_t *x) {  // with a row of bf16
-        f2 s[2] = {0, 0};
+      for (int p = 0; p < RP; ++p)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          const uint2 y = *reinterpret_cast<const uint2 *>(x + sub * 8 + 64 * j);
-          s[0] = fma2(row[2 * j], pack2(bf16lo(y.x), bf16hi(y.x)), s[0]);
-          s[1] = fma2(row[2 * j + 1], pack2(bf16lo(y.y), bf16hi(y.y)), s[1]);
+          const bool live = w.i0 + r + 32 * p < P.dv;
+          const ulonglong2 x = meta.x >= 0 && live ? *reinterpret_cast<const ulonglong2 *>(srow + 32 * p * DK + 32 * j) : make_ulonglong2(0, 0);
+          row[p][2 * j] = x.x, row[p][2 * j + 1] = x.y;
         }
-        const float2 z = unpack2(add2(s[0], s[1]));
-        return over_row(z.x + z.y);
+      auto keep = [&]() {
+#pragma unroll
+        for (int p = 0; p < RP; ++p)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            *reinterpret_cast<ulonglong2 *>(srow + 32 * p * DK + 32 * j) = make_ulonglong2(row[p][2 * j], row[p][2 * j + 1]);
+      };
+      // this lane's pieces of a row of bf16
+      auto pieces = [&](const uint8_t *x, f2 (&y)[2 * NJ]) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const uint2 z = *reinterpret_cast<const uint2 *>(x + sub * 8 + 64 * j);
+          y[2 * j] = pack2(bf16lo(z.x), bf16hi(z.x)), y[2 * j + 1] = pack2(bf16lo(z.y), bf16hi(z.y));
+        }
+      };
+      auto dots = [&](const f2 (&x)[2 * NJ], float (&out)[RP]) {
+#pragma unroll
+        for (int p = 0; p < RP; ++p) {
+          f2 s[2] = {0, 0};
+#pragma unroll
+          for (int j = 0; j < 2 * NJ; ++j) s[j & 1] = fma2(row[p][j], x[j], s[j & 1]);
+          const float2 z = unpack2(add2(s[0], s[1]));
+          out[p] = z.x + z.y;
+        }
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1)
+#pragma unroll
+          for (int p = 0; p < RP; ++p) out[p] += __shfl_xor_sync(0xffffffffu, out[p], off);
       };
       auto token = [&](int n) {
         const uint8_t *x = at + Y::TOKEN + n * Y::EACH;
         const float2 ab = *reinterpret_cast<const float2 *>(at + Y::GATES + n * 8);
-        const float v = live ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(x + DK * 4)[r]) : 0.f;
-        const float u = ab.y * (v - ab.x * dot(x));
-        const f2 a2 = pack2(ab.x, ab.x), u2 = pack2(u, u);
+        f2 key[2 * NJ];
+        float d[RP];
+        pieces(x, key);
+        dots(key, d);
+        const f2 a2 = pack2(ab.x, ab.x);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const uint2 y = *reinterpret_cast<const uint2 *>(x + sub * 8 + 64 * j);
-          row[2 * j] = fma2(a2, row[2 * j], mul2(u2, pack2(bf16lo(y.x), bf16hi(y.x))));
-          row[2 * j + 1] = fma2(a2, row[2 * j + 1], mul2(u2, pack2(bf16lo(y.y), bf16hi(y.y))));
+        for (int p = 0; p < RP; ++p) {
+          const float v = w.i0 + r + 32 * p < P.dv ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(x + DK * 4)[r + 32 * p]) : 0.f;
+          const float u = ab.y * (v - ab.x * d[p]);
+          const f2 u2 = pack2(u, u);
+#pragma unroll
+          for (int j = 0; j < 2 * NJ; ++j) row[p][j] = fma2(a2, row[p][j], mul2(u2, key[j]));
         }
       };
 #pragma unroll 1
@@ -329,14 +350,19 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_
 #pragma unroll 1
       for (int n = 0; n < P.M; ++n) {
         token(tape + n);
-        const float ov = dot(at + Y::TOKEN + (tape + n) * Y::EACH + DK * 2);
-        if (sub == 0 && live) {
-          const long long o = ((long long)w.b * P.M + n) * P.o.token_stride + w.h * P.o.head_stride + w.i0 + r;
-          if (P.o_f32)
-            static_cast<float *>(P.o.ptr)[o] = ov;
-          else
-            static_cast<__nv_bfloat16 *>(P.o.ptr)[o] = __float2bfloat16_rn(ov);
-        }
+        f2 query[2 * NJ];
+        float d[RP];
+        pieces(at + Y::TOKEN + (tape + n) * Y::EACH + DK * 2, query);
+        dots(query, d);
+        const long long o = ((long long)w.b * P.M + n) * P.o.token_stride + w.h * P.o.head_stride + w.i0 + r;
+#pragma unroll
+        for (int p = 0; p < RP; ++p)
+          if (sub == p && w.i0 + r + 32 * p < P.dv) {
+            if (P.o_f32)
+              static_cast<float *>(P.o.ptr)[o + 32 * p] = d[p];
+            else
+              static_cast<__nv_bfloat16 *>(P.o.ptr)[o + 32 * p] = __float2bfloat16_rn(d[p]);
+          }
       }
       if (P.commit) keep();
       fence_proxy_async();
@@ -353,9 +379,9 @@ sv_status run_tokens(PoolParams &P, cudaStream_t s) {
   if (sms <= 0) return SV_ERR_CUDA;
   // Few tokens of many states are streamed (values in whole 16 bytes); it pays from some
   // tiles a block on.
-  const int row_tiles = (P.dv + TILE - 1) / TILE;
+  const int row_tiles = (P.dv + SL<DK>::TILE - 1) / SL<DK>::TILE;
   const long long tiles = (long long)P.B * P.Hv * row_tiles;
-  if (!P.cu && P.tape_M + P.M <= TOKENS && P.dv % 8 == 0 && tiles >= 8LL * sms && tiles <= 0x7fffffffLL) {
+  if (!P.cu && P.tape_M + P.M <= TOKENS && P.dv % 8 == 0 && tiles >= 4LL * sms && tiles <= 0x7fffffffLL) {
     const int size = SL<DK>::stage(P.tape_M + P.M), stages = imin(16, 110 * 1024 / size);
     return from_cuda(launch_early(stream_kernel<DK>, dim3(2 * sms), dim3(STREAM_THREADS), (size_t)stages * size, s, P, stages, (int)tiles, row_tiles));
   }

@@ -32,20 +32,24 @@ def case(sv, B, M, tape_M, Hk, Hv, dk, dv, commit, seed, o_dtype=torch.bfloat16,
     states.copy_(pool)
     o = torch.full((B * M, Hv, dv), 99.0, device="cuda", dtype=o_dtype)
     tape = plain.on(old)[1:] if tape_M else None
+    if M == 0:
+        o = None
     n = torch.tensor(replay, dtype=torch.int32, device="cuda") if tape_M else None
-    sv.gdn_step(states, slots.cuda(), *plain.on(now), o, M, tape=tape, n_replay=n, commit=commit)
+    args = [None] * 5 if M == 0 else plain.on(now)
+    sv.gdn_step(states, slots.cuda(), *args, o, M, tape=tape, n_replay=n, commit=commit)
     assert sv.sv_last_device_error() == sv.SV_OK
     want, out = pool.double().clone(), []
     for b in range(B):
         at = int(slots[b])
         S = pool[at].double() if at >= 0 else torch.zeros(Hv, dv, dk, dtype=torch.float64)
         S, _ = plain.run(S, old, b * tape_M, b * tape_M + (replay[b] if tape_M else 0), False)
-        after, got = plain.run(S, now, b * M, (b + 1) * M)
+        after, got = plain.run(S, now, b * M, (b + 1) * M) if M else (S, None)
         out.append(got)
         if at >= 0:
             want[at] = after if commit else S
     tol = bound(M + tape_M, dk)
-    plain.close(o, torch.cat(out), tol, BF16 if o_dtype is torch.bfloat16 else 0.0, "o")
+    if M:
+        plain.close(o, torch.cat(out), tol, BF16 if o_dtype is torch.bfloat16 else 0.0, "o")
     plain.close(states, want, tol, 0.0, "states")
     touched = {int(s) for b, s in enumerate(slots) if s >= 0 and (commit or (tape_M and replay[b]))}
     for s in set(range(N)) - touched:  # equal bits where nothing was to be written
@@ -63,6 +67,18 @@ def test_shapes(cuda_lib, dk, dv, commit):
 @pytest.mark.parametrize("B,M,tape_M", [(1, 1, 0), (61, 1, 0), (1, 64, 0), (2, 33, 64), (9, 1, 1), (70, 4, 4)])
 def test_counts(cuda_lib, B, M, tape_M):
     case(cuda_lib, B, M, tape_M, 4, 8, 128, 64, True, seed=B + M)
+
+
+@pytest.mark.parametrize("B,M,tape_M,Hv,dk,dv", [(200, 1, 0, 8, 128, 64), (90, 4, 4, 8, 128, 72), (170, 2, 3, 8, 64, 136),
+                                                (110, 3, 0, 8, 256, 40), (160, 1, 2, 8, 128, 8), (160, 0, 5, 8, 128, 64)])
+@pytest.mark.parametrize("commit", [False, True])
+def test_many_states(cuda_lib, B, M, tape_M, Hv, dk, dv, commit):
+    """Enough tiles for every SM to walk over several, some of a few rows only, slots of -1 among them."""
+    if M == 0:
+        commit = False
+    slots = [(b * 7) % B if b % 11 else -1 for b in range(B)]
+    slots = [s if s < 0 or s not in slots[:b] else -1 for b, s in enumerate(slots)]
+    case(cuda_lib, B, M, tape_M, 4, Hv, dk, dv, commit, seed=B + dk, slots=slots)
 
 
 def test_fp32_outputs_and_slot_strides(cuda_lib):
