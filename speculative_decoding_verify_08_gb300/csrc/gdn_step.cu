@@ -148,8 +148,9 @@ constexpr int WORK_WARPS = 8, STREAM_THREADS = (WORK_WARPS + 2) * 32;
 
 template <int DK>
 struct SL {
-  // Rows of a thread: two share its reads of a key.  Rows of a tile.
-  static constexpr int RP = DK <= 128 ? 2 : 1, TILE = RP * WORK_WARPS * 32 / LPR;
+  // Rows of a thread: two of 64 columns, so that a tile is 16 KB as it is at 128 (one token of 61
+  // sequences of 48 heads of 64: 52 us with one; at 128 64 with two, 60 with one).
+  static constexpr int RP = DK == 64 ? 2 : 1, TILE = RP * WORK_WARPS * 32 / LPR;
   static constexpr int STATE = TILE * DK * 4;
   // of a stage: the rows of S, the tokens' gates (a, b), what the tile is, the tokens
   static constexpr int GATES = STATE, META = GATES + TOKENS * 8, TOKEN = META + 16;
@@ -169,7 +170,9 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 // The same rule on the same lanes.  What differs: a block walks over tiles (sequence, head, 64
 // or 32 rows), one warp asking for the next ones' states, keys, queries and values by bulk copies, one
 // writing the states back; as many bytes are on their way as the ring holds, whatever the
-// tiles' own latency (61 sequences of 48 heads: 80 us with a block a tile, STREAM_US this way).
+// tiles' own latency (one token of 61 sequences of 48 heads of 128 x
+// 128: 80 us with a block a tile, 60 this way, 6.4 TB/s; of 24 sequences of 4 rows behind 2 replayed on
+// average: 47, the rows' instructions).
 template <int DK>
 __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_constant__ PoolParams P, int stages, int tiles, int row_tiles) {
   using Y = SL<DK>;
