@@ -28,11 +28,11 @@
 //    products again.)
 //  * fp16 reaches from 2^-24 to 2^16, so everything is scaled by powers of two, exactly:
 //    a key to a largest element in [2^-4, 2^-3) (k = 2^e k': b' = 4^e b, v' = 2^-e v,
-//    u' = 2^e u is the same rule), a query likewise, and a row of S, R and U by one
-//    factor a block, from bounds of what it can reach: with b |k|^2 <= 2 a token adds
-//    at most |b' v'| |k'| to a row's norm, and |k'| is from 2^-4 to sqrt(2), so that u' <=
-//    32 |S| + |b' v'|: |S| <= 2^6 and |b' v'| <= 2^3 at a block's start keep all of it
-//    below 2^16, and the parts are off by 2^-27 of the larger of the two at most.
+//    u' = 2^e u is the same rule), a query likewise, and each row of S, and of R and U, by
+//    factors of a block of their own, from bounds of what they can reach: S by its largest
+//    element before and sum |U~| |k'|; U by its own: with b |k|^2 <= 2 a token adds at most
+//    |b' v'| |k'| to a row's norm, so that |u'| <= |b' v'| + b' |k'| (|S| + 64 |b' v'| |k'|).  The parts are
+//    off by 2^-22 of themselves, or 2^-40 of that bound.
 //  * The inverse: four 16 x 16 blocks by forward substitution in fp32, then joined twice
 //    by -T22 (A21 T11), which is as stable as the substitution.
 //  * G is summed in two fp32 parts and so are its differences: a gate that closes
@@ -58,18 +58,18 @@ constexpr float P_GAIN = 1024.f;     // P is taken so much larger: decays down t
 struct Scalars {
   float bv[C], bx[C], en[C], os1[C], os2[C];  // of v and of X (negative) in R, of U in U~, of the output's two products
   float gc;                                   // decay over the block
-  float pad[63];
+  float bk[2];                                // largest b' |k'|, of the first and of the last tokens
+  float pad[61];
 };
 constexpr int PART = C * 128;  // bytes of one part of T, and of P
 constexpr int HEAD_BYTES = 3 * PART + (int)sizeof(Scalars);  // T (hi, lo), P, scalars
-static_assert(sizeof(Scalars) == 1536 && HEAD_BYTES % 1024 == 512, "copies");
+static_assert(sizeof(Scalars) == 1536 && HEAD_BYTES % 512 == 0, "copies");
 template <int DK>
 __host__ __device__ constexpr int key_bytes() { return C * DK * 2; }  // a block's keys (and queries) of one key head
 
 struct ChunkParams {
   PoolParams p;
   uint8_t *keys, *heads;  // [blocks][Hk][2][key_bytes], [blocks][Hv][HEAD_BYTES]
-  float *most;            // [blocks][Hv][row_blocks][ROWS]: of each row, the largest |b' v'|
   int row_blocks;         // of ROWS rows a value head
   int stall;              // test aid: the first block never arrives
 };
@@ -87,6 +87,7 @@ __device__ __forceinline__ void split2(f2 x, uint32_t &hi, uint32_t &lo) {
 }
 
 __device__ __forceinline__ float pow2_field(int e) { return __int_as_float(e << 23); }  // 2^(e - 127)
+__device__ __forceinline__ float pow2_inverse(float x) { return __int_as_float((254 << 23) - __float_as_int(x)); }  // of a power of two
 
 // Place of a sequence's first block in the workspace: sequences do not share
 // places, and none is past T / C + B.
@@ -108,9 +109,7 @@ struct PL {
   static constexpr int FIRST = 128 * DK * 2 > C * AS * 4 ? 128 * DK * 2 : (C * AS * 4 + 1023) / 1024 * 1024;
   static constexpr int GH = FIRST;                    // G in units of log 2, two parts [2][64]
   static constexpr int EX = GH + 2 * C * 4;           // exponents of the largest elements [128]
-  static constexpr int BV = EX + 128 * 4;             // b' v' / v in bf16, twice a word [64]
-  static constexpr int RED = BV + C * 4;              // [4 warps][128] bf16
-  static constexpr int BAR = RED + 4 * 128 * 2;
+  static constexpr int BAR = EX + 128 * 4;
   static constexpr int BYTES = BAR + 64;
 };
 
@@ -171,14 +170,6 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
   const long long r0 = own.x + (long long)c * C;
   const int m = imin(C, own.y - c * C);
   const int group = P.Hv / P.Hk;
-  {  // the values of its heads are read below: on their way to L2 from now on
-    const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(P.v.ptr) + (long long)hk * group * P.v.head_stride;
-    const int lines = (P.dv * 2 + 127) / 128;
-    for (int e = pt; e < m * group * lines; e += 128) {
-      const int t = e % m, x = e / m, hh = x / lines;
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(vp + (r0 + t) * P.v.token_stride + (long long)hh * P.v.head_stride + (x - hh * lines) * 64));
-    }
-  }
   if (pt == 0) {
     mbar_init(done, 1);
     fence_barrier_init();
@@ -285,10 +276,8 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
     __syncthreads();
     Scalars *S = reinterpret_cast<Scalars *>(out + 3 * PART);
     const float hi_i = gh[i], lo_i = gl[i], ga = ex2_approx(hi_i + lo_i);
-    uint32_t *bv16 = reinterpret_cast<uint32_t *>(smem + Y::BV);
     if (!isP) {
       const float bs = be * e_i;
-      bv16[i] = pack_bf16x2(fabsf(bs), fabsf(bs));
       S->bv[i] = bs;
       S->bx[i] = -(bs * e_i * ga);
       S->en[i] = ex2_approx((gh[C - 1] - hi_i) + (gl[C - 1] - lo_i));
@@ -309,6 +298,14 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
         uint32_t raw[32];  // (from tensor memory for every head: kept, they cost two blocks an SM)
         tc::ld32(tb + c0 * 32 + ((uint32_t)(pw * 32) << 16), raw);
         tc::wait_ld();
+        if (!isP && c0 == (pw & 1)) {  // |k'|^2 of this row's key stands on the diagonal
+          float kk = 0.f;
+#pragma unroll
+          for (int x = 0; x < 32; ++x) kk = x == lane ? __uint_as_float(raw[x]) : kk;
+          // (of values that are not negative the larger has the larger bits)
+          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(rf) * sqrtf(kk)));
+          if (lane == 0) S->bk[pw] = __uint_as_float(top);
+        }
 #pragma unroll
         for (int x = 0; x < 32; x += 8) {
           const int j = c0 * 32 + x;
@@ -337,52 +334,6 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
       }
     }
     __syncthreads();
-    // ---- largest |b' v'| of each row of the state: eight tokens, eight columns a thread ----
-    for (int rb = 0; rb < CP.row_blocks; ++rb) {
-      const int col = rb * ROWS + (pt & 15) * 8, t0 = (pt >> 4) * 8, have = P.dv - col;
-      const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(P.v.ptr) + (r0 + t0) * P.v.token_stride + (long long)h * P.v.head_stride + col;
-      __nv_bfloat162 mx[4];
-#pragma unroll
-      for (int z = 0; z < 4; ++z) mx[z] = __float2bfloat162_rn(0.f);
-      auto take = [&](int t, uint4 y) {
-        const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(bv16 + t0 + t);
-        const uint32_t x[4] = {y.x & 0x7fff7fffu, y.y & 0x7fff7fffu, y.z & 0x7fff7fffu, y.w & 0x7fff7fffu};
-#pragma unroll
-        for (int z = 0; z < 4; ++z) mx[z] = __hmax2(mx[z], __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x[z]), f));
-      };
-      if (have >= 8) {
-        uint4 y[8];
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-          y[t] = t0 + t < m ? *reinterpret_cast<const uint4 *>(src + t * P.v.token_stride) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) take(t, y[t]);
-      } else if (have > 0) {  // the last columns: nothing behind them is read
-#pragma unroll 1
-        for (int t = 0; t < 8 && t0 + t < m; ++t) {
-          uint32_t x[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-          for (int z = 0; z < 7; ++z)
-            if (z < have) x[z >> 1] |= (uint32_t)__bfloat16_as_ushort(src[t * P.v.token_stride + z]) << (16 * (z & 1));
-          take(t, make_uint4(x[0], x[1], x[2], x[3]));
-        }
-      }
-      uint32_t *red = reinterpret_cast<uint32_t *>(smem + Y::RED);
-#pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        uint32_t y = *reinterpret_cast<uint32_t *>(&mx[z]);
-        const uint32_t w2 = __shfl_xor_sync(0xffffffffu, y, 16);
-        mx[z] = __hmax2(mx[z], *reinterpret_cast<const __nv_bfloat162 *>(&w2));
-        if (lane < 16) red[pw * 64 + lane * 4 + z] = *reinterpret_cast<uint32_t *>(&mx[z]);
-      }
-      __syncthreads();
-      const __nv_bfloat16 *r16 = reinterpret_cast<const __nv_bfloat16 *>(red) + pt;
-      float most = 0.f;
-#pragma unroll
-      for (int z = 0; z < 4; ++z) most = fmaxf(most, __bfloat162float(r16[z * 128]));
-      CP.most[(((size_t)w * P.Hv + h) * CP.row_blocks + rb) * ROWS + pt] = most;
-      __syncthreads();
-    }
     // ---- T = (I + A)^-1 in place: a 16 x 16 block a warp, a column a lane ----
     {
       const int o = pw * 16;
@@ -479,12 +430,11 @@ constexpr int CHAIN_THREADS = (ROW_WARPS + OUT_WARPS + 4) * 32, STAGES = 3;
 template <int DK>
 struct CL {
   static constexpr int K = 0, Q = key_bytes<DK>(), T = 2 * key_bytes<DK>(), P = T + 2 * PART, V = P + PART;
-  static constexpr int S = V + C * ROWS * 2;            // scalars, then the rows' largest |b' v'|
-  static constexpr int MOST = S + (int)sizeof(Scalars);
-  static constexpr int STAGE = MOST + ROWS * 4;         // (1024-byte aligned)
-  static constexpr int XCHG = 1024;                     // [2][2][ROWS]
-  static constexpr int SCALE = XCHG + 4 * ROWS * 4;     // [2][ROWS] what the rows' output is multiplied by
-  static constexpr int RING = SCALE + 2 * ROWS * 4;
+  static constexpr int S = V + C * ROWS * 2;            // scalars
+  static constexpr int STAGE = S + 2048;                // (1024-byte aligned)
+  static constexpr int SCALE = 1024;                    // [2][ROWS] bf16x2: what the rows' two outputs are multiplied by
+  static constexpr int XCHG = SCALE + 2 * ROWS * 4;     // [2][2][ROWS]
+  static constexpr int RING = XCHG + 4 * ROWS * 4;
   static constexpr int BYTES = RING + STAGES * STAGE;
   static_assert(RING % 1024 == 0 && STAGE % 1024 == 0 && BYTES <= 227 * 1024, "shared memory");
   // tensor memory: S in two parts; X, then R over it (16 columns a k-step: hi, lo), then U
@@ -522,7 +472,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
   uint64_t *d_done = ut_ready + 1, *o_done = d_done + 1, *o_free = o_done + 1, *idle = o_free + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(idle + 1);
   int *pick = reinterpret_cast<int *>(tmem_slot + 1);
-  float *scale = reinterpret_cast<float *>(smem + Y::SCALE);
+  uint32_t *scale = reinterpret_cast<uint32_t *>(smem + Y::SCALE);
   uint8_t *ring = smem + Y::RING;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -594,12 +544,11 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
           if (c >= STAGES) ok = mbar_wait(&empty[st], (c / STAGES - 1) & 1, P.err);
           if (!ok) break;
           uint8_t *at = ring + st * Y::STAGE;
-          mbar_arrive_expect_tx(&full[st], 2 * key_bytes<DK>() + HEAD_BYTES + ROWS * 4 + C * ROWS * 2);
+          mbar_arrive_expect_tx(&full[st], 2 * key_bytes<DK>() + HEAD_BYTES + C * ROWS * 2);
           const size_t place = (size_t)(w0 + c) * P.Hv + h;
           bulk_load(at + Y::K, CP.keys + ((size_t)(w0 + c) * P.Hk + hk) * 2 * key_bytes<DK>(), 2 * key_bytes<DK>(), &full[st]);
           bulk_load(at + Y::T, CP.heads + place * HEAD_BYTES, 3 * PART, &full[st]);
           bulk_load(at + Y::S, CP.heads + place * HEAD_BYTES + 3 * PART, sizeof(Scalars), &full[st]);
-          bulk_load(at + Y::MOST, CP.most + place * CP.row_blocks * ROWS + i0, ROWS * 4, &full[st]);
           tensor_load_3d(at + Y::V, &mapV, i0, h, own.x + c * C, &full[st]);
         }
         if (!ok)  // no copy may outlive the CTA
@@ -693,7 +642,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       // products that it reports were let go)
       wait(o_done, c & 1);
       tc::fence_after_sync();
-      const float f = scale[(c & 1) * ROWS + r];
+      const uint32_t scales = scale[(c & 1) * ROWS + r];
+      const f2 f1 = pack2(bf16lo(scales), bf16lo(scales)), f2_ = pack2(bf16hi(scales), bf16hi(scales));
       const int some = i0 + r < P.dv && ok ? own.y - c * C : 0;
       // all of it is read before any is stored: the next block's products wait for it
       uint32_t y[C / 2];
@@ -706,9 +656,9 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
 #pragma unroll
         for (int z = 0; z < 8; z += 2) {
           const f2 s1 = *reinterpret_cast<const f2 *>(&Z->os1[t + z]), s2 = *reinterpret_cast<const f2 *>(&Z->os2[t + z]);
-          const f2 x = fma2(pack2(__uint_as_float(a[z]), __uint_as_float(a[z + 1])), s1,
-                            mul2(pack2(__uint_as_float(d[z]), __uint_as_float(d[z + 1])), s2));
-          const float2 v = unpack2(mul2(x, pack2(f, f)));
+          const f2 x = fma2(pack2(__uint_as_float(a[z]), __uint_as_float(a[z + 1])), mul2(s1, f1),
+                            mul2(pack2(__uint_as_float(d[z]), __uint_as_float(d[z + 1])), mul2(s2, f2_)));
+          const float2 v = unpack2(x);
           y[(t + z) / 2] = pack_bf16x2(v.x, v.y);
         }
       }
@@ -761,7 +711,6 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
     }
     // scale of a row: 2^-k with at most 1 behind it
     auto scale_of = [&](float most) { return pow2_field(253 - imin(imax(__float_as_int(most) >> 23, 27), 226)); };
-    auto most_of = [&](int st) { return reinterpret_cast<const float *>(ring + st * Y::STAGE + Y::MOST)[r]; };
     // S (held scaled) as the next product's operand, a k-step at a time; the largest |S| of it
     auto put_state = [&]() {
       __half2 most = __float2half2_rn(0.f);
@@ -784,31 +733,42 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       return fmaxf(__low2float(most), __high2float(most));
     };
     if (n > 0) {
-      wait(&full[0], 0);
-      sc = scale_of(both(fmaxf(m * 0.015625f, 0.125f * most_of(0))));
+      sc = scale_of(both(m * 0.015625f));
       const f2 sc2 = pack2(sc, sc);
 #pragma unroll
       for (int e = 0; e < SC / 2; ++e) S[e] = mul2(S[e], sc2);
       m = put_state();
     }
     int st = 0;
-    uint32_t phase = 0;  // of the stage after this one
+    uint32_t phase = 0;
     for (int c = 0; c < n; ++c) {
       const uint32_t par = c & 1;
       const Scalars *Z = scalars(st);
-      if (hf == 0) scale[par * ROWS + r] = 1.f / sc;  // (exact)
+      float scr;  // the scale of R, U and what comes of them
       // R = b (v - e^G X), a k-step (16 tokens) at a time
       {
         const int some = own.y - c * C - hf * 32;
         const uint16_t *v = reinterpret_cast<const uint16_t *>(ring + st * Y::STAGE + Y::V) + hf * 32 * ROWS + r;
-        const f2 sc2 = pack2(sc, sc);
+        wait(&full[st], phase);
         f2 w[16];  // b' v' of two tokens each, zeros past the sequence's end
+        float wm = 0.f;
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
           uint32_t x = (uint32_t)v[2 * t * ROWS] << 16, y = (uint32_t)v[(2 * t + 1) * ROWS] << 16;
           if (some < 32) x = 2 * t < some ? x : 0u, y = 2 * t + 1 < some ? y : 0u;
-          w[t] = mul2(mul2(pack2(__uint_as_float(x), __uint_as_float(y)), sc2), *reinterpret_cast<const f2 *>(&Z->bv[hf * 32 + 2 * t]));
+          w[t] = mul2(pack2(__uint_as_float(x), __uint_as_float(y)), *reinterpret_cast<const f2 *>(&Z->bv[hf * 32 + 2 * t]));
+          const float2 z = unpack2(w[t]);
+          wm = fmaxf(wm, fmaxf(fabsf(z.x), fabsf(z.y)));
         }
+        // what U can reach, twice as the two halves of a row have terms of their own
+        const float bk = fmaxf(Z->bk[0], Z->bk[1]), isc = pow2_inverse(sc);
+        scr = scale_of(both(fmaf(bk, 12.f * m * isc + 91.f * wm, wm) * 0x1p-14f));
+        if (hf == 0) scale[par * ROWS + r] = pack_bf16x2(isc, pow2_inverse(scr));  // (powers of two)
+        const f2 scr2 = pack2(scr, scr);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) w[t] = mul2(w[t], scr2);
+        const float rise = scr * isc;
+        const f2 rise2 = pack2(rise, rise);
         wait(x_done, par);
         tc::fence_after_sync();
         uint32_t raw2[2][16];
@@ -822,7 +782,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
 #pragma unroll
           for (int t = 0; t < 8; ++t) {
             const int at = hf * 32 + 16 * g + 2 * t;
-            const f2 bx = *reinterpret_cast<const f2 *>(&Z->bx[at]);
+            const f2 bx = mul2(*reinterpret_cast<const f2 *>(&Z->bx[at]), rise2);
             split2(fma2(bx, pack2(__uint_as_float(raw[2 * t]), __uint_as_float(raw[2 * t + 1])), w[8 * g + t]), hi[t], lo[t]);
           }
           tc::st8(tb + Y::X + hf * 32 + 16 * g + lane_off, hi);
@@ -863,18 +823,15 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       arrive(&empty[st]);
       st = st + 1 == STAGES ? 0 : st + 1;
       phase ^= st == 0;
-      float ratio = 1.f;  // of the next block's scale to this one's
+      const float isc = pow2_inverse(sc), iscr = pow2_inverse(scr);
+      float next = sc;
       if (c + 1 < n) {
-        wait(&full[st], phase);
-        // elements of k' are below 2^-3, 64 tokens: |S'| <= 8 |U~|; twice, as the largest of
-        // the sum's terms may be different threads'
-        const float most = (gc * m + 8.f * fmaxf(__low2float(um), __high2float(um))) * 0.03125f;
-        const float next = scale_of(both(fmaxf(most / sc, 0.125f * most_of(st))));
-        ratio = next / sc;  // (exact)
-        sc = next;
+        // elements of k' are below 2^-3, 64 tokens: |S'| <= 8 |U~|; twice, as above
+        next = scale_of(both((gc * m * isc + 8.f * fmaxf(__low2float(um), __high2float(um)) * iscr) * 0.03125f));
       }
-      const float keep = gc * ratio;
-      const f2 keep2 = pack2(keep, keep), ratio2 = pack2(ratio, ratio);
+      const float keep = gc * (next * isc), add = next * iscr;
+      sc = next;
+      const f2 keep2 = pack2(keep, keep), add_2 = pack2(add, add);
 #pragma unroll
       for (int e = 0; e < SC / 2; ++e) S[e] = mul2(S[e], keep2);
       wait(d_done, par);
@@ -887,11 +844,11 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       for (int g = 0; g < SC / 16; ++g)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          S[8 * g + e] = fma2(pack2(__uint_as_float(raw[g][2 * e]), __uint_as_float(raw[g][2 * e + 1])), ratio2, S[8 * g + e]);
+          S[8 * g + e] = fma2(pack2(__uint_as_float(raw[g][2 * e]), __uint_as_float(raw[g][2 * e + 1])), add_2, S[8 * g + e]);
       if (c + 1 < n) m = put_state();
     }
     if (kept && ok) {
-      const f2 isc2 = pack2(1.f / sc, 1.f / sc);
+      const f2 isc2 = pack2(pow2_inverse(sc), pow2_inverse(sc));
 #pragma unroll
       for (int e = 0; e < SC / 2; e += 2)
         *reinterpret_cast<ulonglong2 *>(srow + 2 * e) = make_ulonglong2(mul2(S[e], isc2), mul2(S[e + 1], isc2));
@@ -940,7 +897,7 @@ extern "C" {
 
 size_t gdn_chunk_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv) {
   if (B < 1 || T < 1 || Hk < 1 || Hv < 1 || dv < 1 || (dk != 64 && dk != 128)) return 0;
-  const size_t per = (size_t)Hk * 4 * gdn::C * dk + (size_t)Hv * (gdn::HEAD_BYTES + gdn::padded(dv) * 4);
+  const size_t per = (size_t)Hk * 4 * gdn::C * dk + (size_t)Hv * gdn::HEAD_BYTES;
   return (size_t)gdn::places(B, T) * per;
 }
 
@@ -972,7 +929,6 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   P.commit = 1;
   CP.keys = static_cast<uint8_t *>(workspace);
   CP.heads = CP.keys + (size_t)gdn::places(B, T) * Hk * 4 * gdn::C * dk;
-  CP.most = reinterpret_cast<float *>(CP.heads + (size_t)gdn::places(B, T) * Hv * gdn::HEAD_BYTES);
   CP.row_blocks = (int)(gdn::padded(dv) / gdn::ROWS);
   CP.stall = launch_flags() & SV_LAUNCH_TEST_STALL_COPY ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
