@@ -739,8 +739,17 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       for (int e = 0; e < SC / 2; ++e) S[e] = mul2(S[e], sc2);
       m = put_state();
     }
+    // values of this thread's tokens, two a register, when they are there
+    uint32_t vb[16];
+    auto load_values = [&](int stage, uint32_t parity) {
+      wait(&full[stage], parity);
+      const uint16_t *v = reinterpret_cast<const uint16_t *>(ring + stage * Y::STAGE + Y::V) + hf * 32 * ROWS + r;
+#pragma unroll
+      for (int t = 0; t < 16; ++t) vb[t] = v[2 * t * ROWS] | (uint32_t)v[(2 * t + 1) * ROWS] << 16;
+    };
     int st = 0;
     uint32_t phase = 0;
+    if (n > 0) load_values(0, 0);
     for (int c = 0; c < n; ++c) {
       const uint32_t par = c & 1;
       const Scalars *Z = scalars(st);
@@ -748,13 +757,11 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       // R = b (v - e^G X), a k-step (16 tokens) at a time
       {
         const int some = own.y - c * C - hf * 32;
-        const uint16_t *v = reinterpret_cast<const uint16_t *>(ring + st * Y::STAGE + Y::V) + hf * 32 * ROWS + r;
-        wait(&full[st], phase);
         f2 w[16];  // b' v' of two tokens each, zeros past the sequence's end
         float wm = 0.f;
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
-          uint32_t x = (uint32_t)v[2 * t * ROWS] << 16, y = (uint32_t)v[(2 * t + 1) * ROWS] << 16;
+          uint32_t x = vb[t] << 16, y = vb[t] & 0xffff0000u;
           if (some < 32) x = 2 * t < some ? x : 0u, y = 2 * t + 1 < some ? y : 0u;
           w[t] = mul2(pack2(__uint_as_float(x), __uint_as_float(y)), *reinterpret_cast<const f2 *>(&Z->bv[hf * 32 + 2 * t]));
           const float2 z = unpack2(w[t]);
@@ -829,6 +836,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
         // elements of k' are below 2^-3, 64 tokens: |S'| <= 8 |U~|; twice, as above
         next = scale_of(both((gc * m * isc + 8.f * fmaxf(__low2float(um), __high2float(um)) * iscr) * 0.03125f));
       }
+      if (c + 1 < n) load_values(st, phase);
       const float keep = gc * (next * isc), add = next * iscr;
       sc = next;
       const f2 keep2 = pack2(keep, keep), add_2 = pack2(add, add);
