@@ -87,6 +87,19 @@ __device__ __forceinline__ void split2(f2 x, uint32_t &hi, uint32_t &lo) {
 }
 
 __device__ __forceinline__ float pow2_field(int e) { return __int_as_float(e << 23); }  // 2^(e - 127)
+// Whether `ok` holds for all threads of the rows' warps, which all come by.
+__device__ __forceinline__ bool all_rows(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.red.and.pred q, 5, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ float pow2_inverse(float x) { return __int_as_float((254 << 23) - __float_as_int(x)); }  // of a power of two
 
 // Place of a sequence's first block in the workspace: sequences do not share
@@ -456,8 +469,24 @@ __device__ __forceinline__ void tensor_load_3d(void *dst, const CUtensorMap *map
       : "memory");
 }
 
+// A block of rows of one head's state: (32 columns, row, column group, head, slot).
+__device__ __forceinline__ void state_load(void *dst, const CUtensorMap *map, int row, int head, int slot, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(0), "r"(row), "r"(0), "r"(head), "r"(slot), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void state_store(const CUtensorMap *map, const void *src, int row, int head, int slot) {
+  asm volatile("cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4, %5}], [%6];" ::"l"(map), "r"(0),
+               "r"(row), "r"(0), "r"(head), "r"(slot), "r"(smem_u32(src))
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 template <int DK>
-__global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_constant__ CUtensorMap mapV, const __grid_constant__ ChunkParams CP) {
+__global__ void __launch_bounds__(CHAIN_THREADS, 1)
+    chain_kernel(const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapS, const __grid_constant__ ChunkParams CP) {
   using Y = CL<DK>;
   const PoolParams &P = CP.p;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -470,7 +499,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
   uint64_t *s_ready = empty + STAGES;                      // [2] first and second half of each thread's k-steps of S
   uint64_t *x_done = s_ready + 2, *r_ready = x_done + 1, *u_done = r_ready + 1, *ut_ready = u_done + 1;
   uint64_t *d_done = ut_ready + 1, *o_done = d_done + 1, *o_free = o_done + 1, *idle = o_free + 1;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(idle + 1);
+  uint64_t *s_here = idle + 1, *s_read = s_here + 1;       // the state in the last stage, and read
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_read + 1);
   int *pick = reinterpret_cast<int *>(tmem_slot + 1);
   uint32_t *scale = reinterpret_cast<uint32_t *>(smem + Y::SCALE);
   uint8_t *ring = smem + Y::RING;
@@ -480,9 +510,9 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       mbar_init(&full[i], 1 + (i == 0 ? CP.stall : 0));
       mbar_init(&empty[i], ROW_WARPS + OUT_WARPS + 1);
     }
-    for (uint64_t *b : {s_ready, s_ready + 1, r_ready, ut_ready}) mbar_init(b, ROW_WARPS);
+    for (uint64_t *b : {s_ready, s_ready + 1, r_ready, ut_ready, s_read}) mbar_init(b, ROW_WARPS);
     mbar_init(o_free, OUT_WARPS);
-    for (uint64_t *b : {x_done, u_done, d_done, o_done, idle}) mbar_init(b, 1);
+    for (uint64_t *b : {x_done, u_done, d_done, o_done, idle, s_here}) mbar_init(b, 1);
     fence_barrier_init();
     *pick = 0;
   }
@@ -539,9 +569,14 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       if (lane == 0) {
         const int hk = h / (P.Hv / P.Hk), w0 = first_block(P, b, own.x);
         int c = 0;
+        if (n > 0 && slot >= 0) {
+          mbar_arrive_expect_tx(s_here, ROWS * DK * 4);
+          state_load(ring + (STAGES - 1) * Y::STAGE, &mapS, i0, h, slot, s_here);
+        }
         for (; c < n && ok; ++c) {
           const int st = c % STAGES;
           if (c >= STAGES) ok = mbar_wait(&empty[st], (c / STAGES - 1) & 1, P.err);
+          if (c == STAGES - 1 && slot >= 0) ok = mbar_wait(s_read, 0, P.err);
           if (!ok) break;
           uint8_t *at = ring + st * Y::STAGE;
           mbar_arrive_expect_tx(&full[st], 2 * key_bytes<DK>() + HEAD_BYTES + C * ROWS * 2);
@@ -551,7 +586,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
           bulk_load(at + Y::S, CP.heads + place * HEAD_BYTES + 3 * PART, sizeof(Scalars), &full[st]);
           tensor_load_3d(at + Y::V, &mapV, i0, h, own.x + c * C, &full[st]);
         }
-        if (!ok)  // no copy may outlive the CTA
+        if (n > 0 && slot >= 0) mbar_wait(s_here, 0, P.err);  // no copy may outlive the CTA
+        if (!ok)
           for (int k = imax(0, c - STAGES); k < c && mbar_wait(&full[k % STAGES], (k / STAGES) & 1, P.err); ++k) {
           }
       }
@@ -686,7 +722,6 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
     setmaxnreg_inc<184>();
     constexpr int SC = DK / 2;  // columns of S that are this thread's
     const int hf = warp >> 2;
-    const bool live = i0 + r < P.dv;
     float *xchg = reinterpret_cast<float *>(smem + Y::XCHG);
     uint32_t trades = 0;
     // the larger of a value that both threads of a row have
@@ -697,18 +732,23 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
       named_barrier(1 + (warp & 3), 64);
       return fmaxf(x, at[(hf ^ 1) * ROWS]);
     };
-    float *srow = P.states.ptr + (slot >= 0 ? slot : 0) * P.states.slot_stride + ((long long)h * P.dv + (live ? i0 + r : 0)) * DK + hf * SC;
-    const bool kept = slot >= 0 && live && n > 0;
+    // 16 bytes of this row's state in a stage (32 columns a group, pieces swizzled as the copies do)
+    auto piece = [&](int stage, int e) {
+      const int x = hf * SC / 4 + e;
+      return reinterpret_cast<ulonglong2 *>(ring + stage * Y::STAGE + (x >> 3) * ROWS * 128 + r * 128 + (((x & 7) ^ (r & 7)) << 4));
+    };
+    const bool kept = slot >= 0 && n > 0;
     f2 S[SC / 2];
     float m = 0.f, sc = 1.f;
+    if (kept) wait(s_here, 0);
 #pragma unroll
-    for (int e = 0; e < SC / 2; e += 2) {
-      ulonglong2 x = make_ulonglong2(0, 0);
-      if (kept) x = *reinterpret_cast<const ulonglong2 *>(srow + 2 * e);
-      S[e] = x.x, S[e + 1] = x.y;
+    for (int e = 0; e < SC / 4; ++e) {  // (rows past the head's come as zeros)
+      const ulonglong2 x = kept ? *piece(STAGES - 1, e) : make_ulonglong2(0, 0);
+      S[2 * e] = x.x, S[2 * e + 1] = x.y;
       const float2 y = unpack2(x.x), z = unpack2(x.y);
       m = fmaxf(m, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(z.x), fabsf(z.y))));
     }
+    if (kept) arrive(s_read);
     // scale of a row: 2^-k with at most 1 behind it
     auto scale_of = [&](float most) { return pow2_field(253 - imin(imax(__float_as_int(most) >> 23, 27), 226)); };
     // S (held scaled) as the next product's operand, a k-step at a time; the largest |S| of it
@@ -855,11 +895,17 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) chain_kernel(const __grid_co
           S[8 * g + e] = fma2(pack2(__uint_as_float(raw[g][2 * e]), __uint_as_float(raw[g][2 * e + 1])), add_2, S[8 * g + e]);
       if (c + 1 < n) m = put_state();
     }
-    if (kept && ok) {
+    if (kept) {
+      // through the stage behind the last block's: nothing reads it any more
       const f2 isc2 = pack2(pow2_inverse(sc), pow2_inverse(sc));
+      const int stage = n % STAGES;
 #pragma unroll
-      for (int e = 0; e < SC / 2; e += 2)
-        *reinterpret_cast<ulonglong2 *>(srow + 2 * e) = make_ulonglong2(mul2(S[e], isc2), mul2(S[e + 1], isc2));
+      for (int e = 0; e < SC / 4; ++e) *piece(stage, e) = make_ulonglong2(mul2(S[2 * e], isc2), mul2(S[2 * e + 1], isc2));
+      fence_proxy_async();
+      // (all of the rows' warps are there, whatever ran out; nothing is stored if anything did)
+      const bool all = all_rows(ok);
+      if (all && tid == 0) state_store(&mapS, ring + stage * Y::STAGE, i0, h, slot);
+      __syncwarp();
     }
   }
   tc::fence_before_sync();
@@ -890,9 +936,19 @@ sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
   if (fn(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, P.v.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return SV_ERR_CUDA;
+  // states (32 columns, row of the head, column group, head, slot) in boxes of 32 x 128 x all, 128-byte
+  // swizzle: rows past the head's are read as zeros and not written
+  CUtensorMap ms;
+  cuuint64_t sdims[5] = {32, (cuuint64_t)P.dv, DK / 32, (cuuint64_t)P.Hv, (cuuint64_t)P.states.num_slots};
+  cuuint64_t sstr[4] = {DK * 4, 128, (cuuint64_t)P.dv * DK * 4,
+                        P.states.num_slots > 1 ? (cuuint64_t)P.states.slot_stride * 4 : 16};
+  cuuint32_t sbox[5] = {32, ROWS, DK / 32, 1, 1}, sest[5] = {1, 1, 1, 1, 1};
+  if (fn(&ms, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 5, P.states.ptr, sdims, sstr, sbox, sest, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return SV_ERR_CUDA;
   cudaError_t e = launch_early(prepare_kernel<DK>, dim3((unsigned)(blocks * P.Hk)), dim3(128), (size_t)PL<DK>::BYTES, s, CP);
   if (e != cudaSuccess) return SV_ERR_CUDA;
-  return from_cuda(launch_early(chain_kernel<DK>, dim3((unsigned)items), dim3(CHAIN_THREADS), (size_t)CL<DK>::BYTES, s, mv, CP));
+  return from_cuda(launch_early(chain_kernel<DK>, dim3((unsigned)items), dim3(CHAIN_THREADS), (size_t)CL<DK>::BYTES, s, mv, ms, CP));
 }
 
 }  // namespace
@@ -916,6 +972,7 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   if (dk != 64 && dk != 128) return SV_ERR_UNSUPPORTED;
   if (Hv > 65535 || B > gdn::MAX_POOL_B || T > 0x40000000 || dv > 65536) return SV_ERR_UNSUPPORTED;
   if (sv_status e = gdn::check_states(states, Hv, dk, dv)) return e;
+  if (states->slot_stride > ((int64_t)1 << 37)) return SV_ERR_UNSUPPORTED;  // (a tensor map's bound is 2^40 bytes)
   for (const sv_rows *r : {q, k, v, o})
     if (!paged::good_rows(r, T)) return SV_ERR_INVALID_ARG;
   if (T > 0 && (!g || !beta || !paged::aligned(g, 4) || !paged::aligned(beta, 4))) return SV_ERR_INVALID_ARG;
@@ -940,6 +997,10 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   CP.row_blocks = (int)(gdn::padded(dv) / gdn::ROWS);
   CP.stall = launch_flags() & SV_LAUNCH_TEST_STALL_COPY ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // A block costs as much with one token as with 64, and an item several times that; token by token
+  // is faster up to some eight tokens a sequence (48 heads of 128 x 128: one sequence of 16 tokens 12 us
+  // against 20, of 32 21 both; eight of 8 27 against 37, of 16 46 against 37; 64 of 8 178 against 215).
+  if (T <= 24 || T <= 8LL * B) return gdn::launch_tokens(P, dk, s);
   return dk == 64 ? gdn::run_chunks<64>(CP, s) : gdn::run_chunks<128>(CP, s);
 }
 
