@@ -610,7 +610,7 @@ typedef struct {
  *   sequence starts from zeros and its state is not kept (rows that fill up a
  *   captured batch).  Two sequences of a call with one slot >= 0: that state is
  *   undefined afterwards.
- * n_replay: device int32 [B], 0..tape_M; NULL: no tape (the tape's arguments are
+ * n_replay: device int32 [B], 0..tape_M; NULL, or tape_M 0: no tape (its arguments are
  *   not read).  A count outside counts as the nearest of 0 and tape_M, a slot past
  *   the pool as negative; both are reported by sv_last_device_error() as
  *   SV_ERR_INVALID_ARG.
@@ -635,10 +635,21 @@ SV_API sv_status gdn_step(const sv_states *states, const int32_t *slots, const s
  *   break this is left out and reported by sv_last_device_error() as
  *   SV_ERR_INVALID_ARG; rows of o of no sequence are not written, nor is the state of
  *   a sequence without rows.  slots: as gdn_step's.
+ * Domain: 0 <= beta and beta * |k|^2 <= 2 (a token then lengthens no state; unit keys with
+ *   gates from a sigmoid, or twice one, do) and g <= 0; finite values.
+ * Arithmetic: blocks of 64 tokens, fp32 sums of products whose operands are fp32 values held as
+ *   two fp16 parts (off by 2^-22 of themselves, or by 2^-40 of a bound of their row); what only o
+ *   sees, the state and the updates in its products, is one part (2^-11).  Elements of a key or
+ *   query are exact down to 2^-13 of its largest and off by 2^-21 of that below.  A call of T <= 24 or
+ *   T <= 8*B runs token by token, as gdn_step does.
+ * Offsets that fall, so that sequences name the same rows: o of those rows, and the states of all
+ *   sequences of the call, are undefined.
  * Supported: dk in {64, 128}; Hv % Hk == 0, Hv <= 65535; dv <= 65536; 0 <= B <= 65535;
- *   T <= 2^30.
- * It needs no workspace at present: the query gives 0, and NULL with 0 bytes is
- * accepted. */
+ *   T <= 2^30; slot_stride <= 2^37; B*Hv*((dv+127)/128) and (T/64 + B)*Hk < 2^31, divisions
+ *   rounded down; strides of v above 0.
+ * workspace: device, 16-byte aligned, of the query's size; nothing in it has to be zero.
+ * Two launches (one token by token); offsets and slots are read on the device, so a captured call
+ * follows their contents. */
 SV_API size_t gdn_chunk_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv);
 SV_API sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows *q,
                            const sv_rows *k, const sv_rows *v, const float *g, const float *beta,
@@ -677,9 +688,10 @@ SV_API sv_status sv_last_device_error(sv_stream_t stream);
  *     after the predecessor has completed; the prepacked weights and the KV
  *     cache slots before kv_len-M may be read earlier, so with this flag set
  *     they must not be written by the immediately preceding kernel.
- *     (qk_norm_rope, paged_kv_append, paged_attn and window_attn are launched
- *     this way whatever the flag says, and read nothing before their
- *     predecessor has completed.) */
+ *     (qk_norm_rope, paged_kv_append, paged_attn, window_attn,
+ *     paged_chunk_attn, gdn_chunk and gdn_step are launched this way whatever
+ *     the flag says, and read nothing before their predecessor has
+ *     completed.) */
 #define SV_LAUNCH_PDL 1u
 /*   SV_LAUNCH_QMM_CUDA_CORES: a measurement aid, not a faster path.
  *     qmm_small_m at M = 1 and M = 4 (72 KB-stage plans) replaces its
@@ -702,7 +714,9 @@ SV_API sv_status sv_last_device_error(sv_stream_t stream);
  *     issuing it, and the quantised matmul (qmm_small_m, qmm8_small_m; not
  *     under its thread-block cluster plan) its first weight stage, so their
  *     waits run out after about 1.5 s of SM clocks; in paged_attn and
- *     window_attn the first slot of the (K) ring never counts as filled.  The
+ *     window_attn the first slot of the (K) ring never counts as filled, in
+ *     paged_chunk_attn the first copy of the ring and in gdn_chunk (beyond its
+ *     token-by-token form) the first block are never issued.  The
  *     call completes with an undefined output and sv_last_device_error()
  *     reports SV_ERR_TIMEOUT.  Workspaces stay usable for the next call.  No
  *     other kernel reads it. */

@@ -923,8 +923,7 @@ inline size_t padded(int dv) { return ((size_t)dv + ROWS - 1) / ROWS * ROWS; }
 template <int DK>
 sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
   const PoolParams &P = CP.p;
-  const long long items = (long long)P.B * P.Hv * CP.row_blocks, blocks = places(P.B, P.T);
-  if (items > 0x7fffffffLL || blocks * P.Hk > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
+  const long long items = (long long)P.B * P.Hv * CP.row_blocks, blocks = places(P.B, P.T);  // (checked: 31 bits)
   // values (column, head, token) in boxes of 128 x 1 x 64, zeros past the last column
   auto fn = attn::encode_fn();
   if (!fn) return SV_ERR_CUDA;
@@ -980,6 +979,8 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   if (B == 0 || T == 0) return SV_OK;
   // a tensor map steps by every stride: values that repeat (stride 0) have none
   if ((T > 1 && !v->token_stride) || (Hv > 1 && !v->head_stride)) return SV_ERR_UNSUPPORTED;
+  const int row_blocks = (int)(gdn::padded(dv) / gdn::ROWS);
+  if ((long long)B * Hv * row_blocks > 0x7fffffffLL || gdn::places(B, T) * Hk > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
   if (!workspace || ws_bytes < gdn_chunk_workspace_bytes(B, T, Hk, Hv, dk, dv)) return SV_ERR_WORKSPACE;
   if (!paged::aligned(workspace, 16)) return SV_ERR_INVALID_ARG;
   gdn::ChunkParams CP{};
@@ -994,7 +995,7 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   P.commit = 1;
   CP.keys = static_cast<uint8_t *>(workspace);
   CP.heads = CP.keys + (size_t)gdn::places(B, T) * Hk * 4 * gdn::C * dk;
-  CP.row_blocks = (int)(gdn::padded(dv) / gdn::ROWS);
+  CP.row_blocks = row_blocks;
   CP.stall = launch_flags() & SV_LAUNCH_TEST_STALL_COPY ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // A block costs as much with one token as with 64, and an item several times that; token by token
