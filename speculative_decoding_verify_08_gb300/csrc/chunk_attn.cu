@@ -58,15 +58,18 @@ struct Cfg {
   // (K) or of its keys (V).
   static constexpr int SLOT = 32768, RAW = SLOT / 2;  // (e4m3: where a copy lands)
   static constexpr int PARTS = BN * D * 2 / SLOT;  // slots of a K block (of a V block)
-  static constexpr int KG = D / 64 / PARTS;        // 64-column groups of a K slot
+  // e4m3 keys are operands as they land: a slot a block
+  static constexpr int KSLOT = F8 ? BN * D : SLOT, KPARTS = F8 ? 1 : PARTS;
+  static constexpr int KG = D / 64 / PARTS;        // 64-column groups of a K slot (bf16)
   static constexpr int VK = BN / PARTS;            // keys of a V slot
   static constexpr int THREADS = (SOFT + (F8 ? 8 : 4)) * 32;
   static constexpr int QBYTES = ROWS * D * 2;
   static constexpr int RING = HEADER + NT * QBYTES;
   // slots of the K and the V ring: 160 KB, or 128 beside long prefix sums and e4m3's scales
   // (At D = 256 a block takes two slots of each, and the next block's keys are needed first.)
-  static constexpr int NK = D == 256 ? 3 : 2, NV = 5 - NK, LESS = 2;
-  static_assert((NK + NV) * SLOT == 160 * 1024 && 2 * LESS * SLOT == 128 * 1024, "ring");
+  static constexpr int NK = F8 ? 2 : D == 256 ? 3 : 2, NV = F8 ? (D == 256 ? 2 : 3) : 5 - NK;
+  static constexpr int LESS_K = 2, LESS_V = F8 ? NV : 2;
+  static_assert(NK * KSLOT + NV * SLOT == (F8 ? 128 : 160) * 1024 && LESS_K * KSLOT + LESS_V * SLOT == 128 * 1024, "ring");
   static constexpr int BEHIND = RING + 128 * 1024;  // prefix sums
   static constexpr int SCALES = BEHIND + ((MAX_B + 1) * 4 + 15) / 16 * 16;  // [2][NT][ROWS] of e4m3's queries
   // tensor memory: O per tile, then the S buffers (P over S)
@@ -220,6 +223,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2_hi(uint32_t v) {  // high 16
   return d;
 }
 
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(f2 v) {  // to the nearest, in the low 16 bits
+  const float2 x = unpack2(v);
+  uint32_t d;
+  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tmov.b32 %0, {t, 0};\n\t}\n" : "=r"(d) : "f"(x.x), "f"(x.y));
+  return d;
+}
+
 __device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *map, int c0, int c1, int c2,
                                             int c3, uint64_t *bar) {
   asm volatile(
@@ -242,7 +252,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                       const __grid_constant__ CUtensorMap mapV, const __grid_constant__ Params P) {
   using C = Cfg<D, TILES, F8>;
-  constexpr int NT = C::NT, NSB = C::NSB, PARTS = C::PARTS, VK = C::VK, KG = C::KG, SLOT = C::SLOT;
+  constexpr int NT = C::NT, NSB = C::NSB, PARTS = C::PARTS, VK = C::VK, KG = C::KG, SLOT = C::SLOT, KSLOT = C::KSLOT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw;
   // The swizzled tiles need 1024-byte alignment, which the first dynamic byte
@@ -262,7 +272,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   // (30 barriers, 240 bytes; the rest stands behind the cuts)
   uint64_t *more = reinterpret_cast<uint64_t *>(smem + 280);
   uint64_t *idle = more, *p_half = more + 1;  // p_half [2] one S buffer: P of the first half of a block's keys written
-  uint64_t *q_ready = more + 3, *copied = more + 4;  // e4m3: queries turned, [2][5] copies landed
+  uint64_t *q_ready = more + 3, *copied = more + 4;  // e4m3: queries turned, [5] copies of values landed
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + CUTS + 16);
   int2 *cut = reinterpret_cast<int2 *>(smem + CUTS);  // [2] item and block where this CTA begins, and the next one
   Item *info_it = reinterpret_cast<Item *>(smem + INFO);  // of the item whose queries landed
@@ -271,15 +281,15 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   float *rowscale = reinterpret_cast<float *>(smem + C::SCALES);  // e4m3: [2][NT][ROWS] what the rows' scores are multiplied by
   uint8_t *qs = smem + HEADER;
   uint8_t *ring = smem + C::RING;
-  const int NK = P.few_slots ? C::LESS : C::NK, NV = P.few_slots ? C::LESS : C::NV;
+  const int NK = P.few_slots ? C::LESS_K : C::NK, NV = P.few_slots ? C::LESS_V : C::NV;
   int *pre = reinterpret_cast<int *>(smem + (P.few_slots ? C::BEHIND : PREFIX));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < 10; ++i) {
-      mbar_init(&full[i], (F8 ? 4 : 1) + (i == 0 && !F8 ? P.stall : 0));
+      mbar_init(&full[i], (F8 && i >= 5 ? 4 : 1) + (i == 0 ? P.stall : 0));
       mbar_init(&empty[i], 1);
-      if (F8) mbar_init(&copied[i], 1 + (i == 0 ? P.stall : 0));
+      if (F8 && i < 5) mbar_init(&copied[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -308,7 +318,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   }
   // Values of slots that are not copied meet probabilities of zero and have to be finite.
   for (int x = tid; x < NV * SLOT / 16; x += C::THREADS)
-    reinterpret_cast<uint4 *>(ring + NK * SLOT)[x] = make_uint4(0u, 0u, 0u, 0u);
+    reinterpret_cast<uint4 *>(ring + NK * KSLOT)[x] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async();
   pdl_wait();
 
@@ -420,17 +430,17 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
     if (warp == C::SOFT + 1 || warp == C::SOFT + 3) {
       // -------------------- copies: K blocks by one warp, V blocks by the other --
       const bool is_v = warp == C::SOFT + 3;
-      uint64_t *landed = (F8 ? copied : full) + (is_v ? 5 : 0), *free = empty + (is_v ? 5 : 0);
-      uint8_t *slots = ring + (is_v ? NK * SLOT : 0);
-      const int NS = is_v ? NV : NK;
+      uint64_t *landed = is_v ? (F8 ? copied : full + 5) : full, *free = empty + (is_v ? 5 : 0);
+      uint8_t *slots = ring + (is_v ? NK * KSLOT : 0);
+      const int NS = is_v ? NV : NK, size = is_v ? SLOT : KSLOT, per_block = is_v ? PARTS : C::KPARTS;
       // A lane a piece of R rows (of a column group), all pieces of a slot at once.
       int first, gap, group, place;  // its first row in slot 0 of a block, from slot to slot, column group, where in the slot
       int step = 0;                  // of the column group from slot to slot
       if (F8) {
-        const int groups = is_v ? D / 128 : 1, p = lane / groups;  // of 128 columns
-        first = p * P.R, gap = is_v ? VK : 0;
-        group = is_v ? lane - p * groups : 0, step = is_v ? 0 : 1;
-        place = C::RAW + (is_v ? group * VK * 128 : 0) + p * P.R * 128;
+        constexpr int groups = D / 128;  // of 128 columns
+        const int p = lane / groups;
+        first = p * P.R, gap = is_v ? VK : 0, group = lane % groups;
+        place = (is_v ? C::RAW : 0) + group * (is_v ? VK : BN) * 128 + p * P.R * 128;
       } else if (is_v) {
         first = lane * P.R, gap = VK, group = 0, place = lane * P.R * 128 * (D / 64);
       } else {
@@ -471,7 +481,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         // the one after it is looked up before this one's slot is waited for
         const int now_x = x;
         h = it.h;
-        if (++x == PARTS) x = 0, ++j;
+        if (++x == per_block) x = 0, ++j;
         if (j == pt.j1) {
           more_parts = next_part();
           j = pt.j0;
@@ -491,7 +501,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
             atomicOr(P.err, ERR_INDEX);
             at.page = P.num_pages;
           }
-          page_load(slots + slot * SLOT + place, is_v ? &mapV : &mapK, at.slot, group + now_x * step, h, at.page, &landed[slot]);
+          page_load(slots + slot * size + place, is_v ? &mapV : &mapK, at.slot, group + now_x * step, h, at.page, &landed[slot]);
         }
         at = next;
         ++q;
@@ -537,31 +547,29 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       }
       __syncwarp();
     } else if (F8 && warp >= C::SOFT + 4) {
-      // --------------------------------------- queries and e4m3 copies to fp16 --
+      // --------------------------------------- queries to two e4m3 parts, values to fp16 --
       const int i = tid - (C::SOFT + 4) * 32;
       bool ok = true;
-      int ks = 0, vs = 0;
-      uint32_t kp = 0, vp = 0, worked = 0;
+      int at_slot = 0;
+      uint32_t phase = 0, worked = 0;
       // One slot: its copy stands in the second half.  The half of the columns whose fp16 tiles lie in the
       // first half comes first, then, once all have read them, the rest.
-      auto turn = [&](auto is_v, const Item &it, int j, int x) {
-        constexpr bool v = decltype(is_v)::value;
-        constexpr bool whole = (v ? VK : BN) == 64;  // a half of the copy: all pieces of 64 rows, or half of those of 128
+      auto turn = [&](const Item &it, int j, int x) {
+        constexpr bool whole = VK == 64;             // a half of the copy: all pieces of 64 rows, or half of those of 128
         constexpr int gap = whole ? 16 : 32;         // rows between a thread's pieces
-        const int at_slot = v ? vs : ks;
-        if (ok) ok = spin_wait(&copied[(v ? 5 : 0) + at_slot], v ? vp : kp, P.err);
+        if (ok) ok = spin_wait(&copied[at_slot], phase, P.err);
         ok = __all_sync(0xffffffffu, ok);
-        uint8_t *base = ring + (v ? NK + at_slot : at_slot) * SLOT;
+        uint8_t *base = ring + NK * KSLOT + at_slot * SLOT;
         const int r0 = whole ? i >> 3 : i >> 2, c = whole ? i & 7 : i & 3;
         Blind none{0, 0, BN};
-        if (v && (j <= it.ns || j + 1 == it.n)) none = blind(P, it, j);
+        if (j <= it.ns || j + 1 == it.n) none = blind(P, it, j);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const uint8_t *raw = base + C::RAW + (whole ? half * 8192 + r0 * 128 + c * 16 : r0 * 128 + (4 * half + c) * 16);
           uint4 w[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) w[y] = *reinterpret_cast<const uint4 *>(raw + y * gap * 128);
-          if (v && (none.a < none.b || none.c < BN)) {  // slots that no row sees count as zeros
+          if (none.a < none.b || none.c < BN) {  // slots that no row sees count as zeros
 #pragma unroll
             for (int y = 0; y < 4; ++y)
               if (none(x * VK + r0 + gap * y)) w[y] = make_uint4(0u, 0u, 0u, 0u);
@@ -579,18 +587,15 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         }
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[(v ? 5 : 0) + at_slot]);
-        if (v) {
-          if (++vs == NV) vs = 0, vp ^= 1;
-        } else if (++ks == NK) {
-          ks = 0, kp ^= 1;
-        }
+        if (lane == 0) mbar_arrive(&full[5 + at_slot]);
+        if (++at_slot == NV) at_slot = 0, phase ^= 1;
       };
       for (int k = 0; k < parts; ++k) {
         const Item it = item_at<NT>(P, pre, id_of(k));
         const Part pt = part_of(k, it);
         if (pt.j0 == pt.j1) continue;
-        // This thread's row of the queries, scaled by a power of two: largest element in [2^14, 2^15).
+        // This thread's row of the queries, scaled by a power of two: largest element in [2^7, 2^8).
+        // 32 elements at a time, in place: their first parts, then what those leave.
         if (ok) ok = spin_wait(q_full, worked & 1, P.err);
         ok = __all_sync(0xffffffffu, ok);
 #pragma unroll 1
@@ -603,40 +608,55 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
             const uint4 w = *place(x);
             mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
           }
-          const int E = imin(imax((int)(max(mx & 0xffffu, mx >> 16) >> 7), 16), 254);
-          const float up = __int_as_float(imin(268 - E, 254) << 23);  // 2^(14 - (E - 127)), 2^127 at most
-          rowscale[((worked & 1) * NT + t) * ROWS + i] = 1.f / up;
+          const int e = (int)(max(mx & 0xffffu, mx >> 16) >> 7), E = imin(imax(e, 16), 254);
+          const float up = __int_as_float((261 - E) << 23);  // 2^(7 - (E - 127))
+          // (an element that is not finite makes the row's scores NaN: e4m3 has no infinity)
+          rowscale[((worked & 1) * NT + t) * ROWS + i] = e == 255 ? __int_as_float(0x7fffffff) : 1.f / up;
           const f2 up2 = pack2(up, up);
-#pragma unroll 8
-          for (int x = 0; x < D / 8; ++x) {
-            uint4 w = *place(x);
-            auto two = [&](uint32_t y) {
-              const float2 z = unpack2(mul2(pack2(bf16lo(y), bf16hi(y)), up2));
-              return pack_f16x2(z.x, z.y);
+#pragma unroll 1
+          for (int x = 0; x < D / 8; x += 4) {
+            uint4 hi[2], lo[2];
+            auto two = [&](uint32_t y, uint32_t &l) {  // two elements
+              const f2 v = mul2(pack2(bf16lo(y), bf16hi(y)), up2);
+              const uint32_t h = f32x2_to_e4m3x2(v), b = e4m3x2_to_f16x2(h);
+              l = f32x2_to_e4m3x2(fma2(pack2(f16lo(b), f16hi(b)), pack2(-1.f, -1.f), v));
+              return h;
             };
-            w = make_uint4(two(w.x), two(w.y), two(w.z), two(w.w));
-            *place(x) = w;
+            auto four = [&](uint32_t y, uint32_t z, uint32_t &h, uint32_t &l) {
+              uint32_t l0, l1;
+              const uint32_t h0 = two(y, l0), h1 = two(z, l1);
+              h = h0 | h1 << 16, l = l0 | l1 << 16;
+            };
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint4 w = *place(x + 2 * z), w2 = *place(x + 2 * z + 1);
+              four(w.x, w.y, hi[z].x, lo[z].x);
+              four(w.z, w.w, hi[z].y, lo[z].y);
+              four(w2.x, w2.y, hi[z].z, lo[z].z);
+              four(w2.z, w2.w, hi[z].w, lo[z].w);
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z) *place(x + z) = hi[z], *place(x + 2 + z) = lo[z];
           }
         }
         ++worked;
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready);
-        for (int j = pt.j0; j <= pt.j1; ++j) {
-          for (int x = 0; x < PARTS && j < pt.j1; ++x) turn(std::false_type{}, it, j, x);
-          for (int x = 0; x < PARTS && j > pt.j0; ++x) turn(std::true_type{}, it, j - 1, x);
-        }
+        for (int j = pt.j0; j < pt.j1; ++j)
+#pragma unroll 1
+          for (int x = 0; x < PARTS; ++x) turn(it, j, x);
       }
       __syncwarp();
     } else if (warp == C::SOFT) {
       // ------------------------------------------------- MMA issuer --
-      constexpr uint32_t IDS = F8 ? tc::idesc_f16_f32(ROWS, BN, false) : tc::idesc_bf16_f32(ROWS, BN, false);
+      constexpr uint32_t IDS = F8 ? tc::idesc_e4m3_f32(ROWS, BN) : tc::idesc_bf16_f32(ROWS, BN, false);
       constexpr uint32_t IDO = F8 ? tc::idesc_f16_f32(ROWS, D, true) : tc::idesc_bf16_f32(ROWS, D, true);
       // rows of a piece of values: a copy's (bf16), or all of a slot
       const int VR = F8 ? VK : P.R;
       // descriptors: queries and keys K-major, values with rows along K
       const uint64_t dq = tc::smem_desc_sw128(smem_u32(qs), 16, 1024), dk = tc::smem_desc_sw128(smem_u32(ring), 16, 1024);
-      const uint64_t dv = tc::smem_desc_sw128(smem_u32(ring + NK * SLOT), VR * 128, 1024);
+      const uint64_t dv = tc::smem_desc_sw128(smem_u32(ring + NK * KSLOT), VR * 128, 1024);
       const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32), k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32);
       const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
       // of 16 keys' step ks in a slot of values: piece by piece, all column groups of one together
@@ -679,25 +699,32 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         auto issue_s = [&](int ta, int tb1, bool release, bool last) {
           Cursor at = ck;
 #pragma unroll
-          for (int x = 0; x < PARTS; ++x) {
+          for (int x = 0; x < C::KPARTS; ++x) {
             if (ta == 0) wait(&full[at.slot], at.parity);  // (tile 1 follows tile 0)
             tc::fence_after_sync();
             if (leader && ok) {
-              const uint32_t ka = k_lo + at.slot * (SLOT / 16);
+              const uint32_t ka = k_lo + at.slot * (KSLOT / 16);
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
                 if (t < ta || t >= tb1) continue;
                 const uint32_t sb = NSB == 2 ? (sj[0] & 1) : (uint32_t)t;
+                if constexpr (F8) {  // 32 columns a step, both parts of the queries
 #pragma unroll
-                for (int ks = 0; ks < KG * 4; ++ks)
-                  tc::mma_bf16(tb + C::TS + sb * BN,
-                               q_lo + (t * C::QBYTES + (x * KG + (ks >> 2)) * ROWS * 128 + (ks & 3) * 32) / 16, q_hi,
-                               ka + ((ks >> 2) * BN * 128 + (ks & 3) * 32) / 16, k_hi, IDS,
-                               (x > 0 || ks > 0) ? 1u : 0u);
-                if (x == PARTS - 1) tc::commit(&s_full[sb]);
+                  for (int ks = 0; ks < D / 16; ++ks)
+                    tc::mma_e4m3(tb + C::TS + sb * BN, q_lo + (t * C::QBYTES + (ks >> 2) * ROWS * 128 + (ks & 3) * 32) / 16, q_hi,
+                                 ka + ((ks >> 3) * BN * 128 + ((ks >> 1) & 3) * 32) / 16, k_hi, IDS, ks > 0 ? 1u : 0u);
+                } else {
+#pragma unroll
+                  for (int ks = 0; ks < KG * 4; ++ks)
+                    tc::mma_bf16(tb + C::TS + sb * BN,
+                                 q_lo + (t * C::QBYTES + (x * KG + (ks >> 2)) * ROWS * 128 + (ks & 3) * 32) / 16, q_hi,
+                                 ka + ((ks >> 2) * BN * 128 + (ks & 3) * 32) / 16, k_hi, IDS,
+                                 (x > 0 || ks > 0) ? 1u : 0u);
+                }
+                if (x == C::KPARTS - 1) tc::commit(&s_full[sb]);
               }
               if (release) tc::commit(&empty[at.slot]);
-              if (last && x == PARTS - 1) tc::commit(q_free);
+              if (last && x == C::KPARTS - 1) tc::commit(q_free);
             }
             at.step(NK);
           }
@@ -725,7 +752,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
               if (some && t == 0) {
                 const Blind none = blind(P, it, j);
                 const int upto = (none.c + P.R - 1) & -P.R;  // (pieces behind hold older values)
-                uint8_t *vb = ring + (NK + at.slot) * SLOT;
+                uint8_t *vb = ring + NK * KSLOT + at.slot * SLOT;
                 auto clear = [&](int r0, int r1) {  // rows of the block, those of this slot
                   r0 = imax(r0 - x * VK, 0), r1 = imin(r1 - x * VK, VK);
                   for (int e = lane; e < (r1 - r0) * (D / 8); e += 32) {
@@ -1101,7 +1128,7 @@ static bool query_map(CUtensorMap *map, const sv_rows *r, int T, int H, int D, i
 
 // 5-D map of a cache (128 bytes of columns, slot, column group, head, page) in boxes of R
 // slots and `groups` groups; zeros past the last page.
-static bool page_map(CUtensorMap *map, void *base, const sv_paged_kv *c, int D, int Hkv, int R, int groups) {
+static bool page_map(CUtensorMap *map, void *base, const sv_paged_kv *c, int D, int Hkv, int R, int groups, bool swizzle) {
   auto fn = attn::encode_fn();
   if (!fn) return false;
   const int es = c->dtype == SV_E4M3 ? 1 : 2;
@@ -1110,7 +1137,7 @@ static bool page_map(CUtensorMap *map, void *base, const sv_paged_kv *c, int D, 
   cuuint64_t strides[4] = {(cuuint64_t)c->slot_stride * es, 128, (cuuint64_t)c->head_stride * es, (cuuint64_t)c->page_stride * es};
   cuuint32_t box[5] = {cols, (cuuint32_t)R, (cuuint32_t)groups, 1, 1}, estr[5] = {1, 1, 1, 1, 1};
   return fn(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, es == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1120,8 +1147,8 @@ static sv_status run(const sv_rows *q, const sv_paged_kv *cache, Params &P, int 
   CUtensorMap mq, mk, mv;
   P.R = P.page_size % 64 == 0 ? 64 : P.page_size % 32 == 0 ? 32 : 16;
   P.piece = imax(P.R, 32);
-  if (!query_map(&mq, q, P.Tq, P.Hkv * P.G, D, P.G, P.PT) || !page_map(&mk, cache->k, cache, D, P.Hkv, P.R, 1) ||
-      !page_map(&mv, cache->v, cache, D, P.Hkv, P.R, F8 ? 1 : D / 64))
+  if (!query_map(&mq, q, P.Tq, P.Hkv * P.G, D, P.G, P.PT) || !page_map(&mk, cache->k, cache, D, P.Hkv, P.R, 1, true) ||
+      !page_map(&mv, cache->v, cache, D, P.Hkv, P.R, F8 ? 1 : D / 64, !F8))
     return SV_ERR_CUDA;
   const size_t prefix = ((size_t)P.B + 1) * 4;
   P.few_slots = !F8 && prefix <= HEADER - PREFIX ? 0 : 1;
