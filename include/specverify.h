@@ -640,12 +640,12 @@ SV_API sv_status gdn_step(const sv_states *states, const int32_t *slots, const s
  * Arithmetic: blocks of 64 tokens, fp32 sums of products whose operands are fp32 values held as
  *   two fp16 parts (off by 2^-22 of themselves, or by 2^-40 of a bound of their row); what only o
  *   sees, the state and the updates in its products, is one part (2^-11).  Elements of a key or
- *   query are exact down to 2^-13 of its largest and off by 2^-21 of that below.  A call of T <= 24 or
+ *   query are exact down to 2^-13 of its largest and off by 2^-21 of that below.  A call of T <= 20 or
  *   T <= 8*B runs token by token, as gdn_step does.
  * Offsets that fall, so that sequences name the same rows: o of those rows, and the states of all
  *   sequences of the call, are undefined.
  * Supported: dk in {64, 128}; Hv % Hk == 0, Hv <= 65535; dv <= 65536; 0 <= B <= 65535;
- *   T <= 2^30; slot_stride <= 2^37; B*Hv*((dv+127)/128) and (T/64 + B)*Hk < 2^31, divisions
+ *   T <= 2^30; slot_stride <= 2^37; B*Hv*((dv+127)/128) and (T/64 + B)*Hv < 2^31, divisions
  *   rounded down; strides of v above 0.
  * workspace: device, 16-byte aligned, of the query's size; nothing in it has to be zero.
  * Two launches (one token by token); offsets and slots are read on the device, so a captured call

@@ -609,9 +609,9 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
             mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
           }
           const int e = (int)(max(mx & 0xffffu, mx >> 16) >> 7), E = imin(imax(e, 16), 254);
-          const float up = __int_as_float((261 - E) << 23);  // 2^(7 - (E - 127))
-          // (an element that is not finite makes the row's scores NaN: e4m3 has no infinity)
-          rowscale[((worked & 1) * NT + t) * ROWS + i] = e == 255 ? __int_as_float(0x7fffffff) : 1.f / up;
+          float up = __int_as_float((261 - E) << 23);  // 2^(7 - (E - 127))
+          rowscale[((worked & 1) * NT + t) * ROWS + i] = 1.f / up;
+          if (e == 255) up = __int_as_float(0x7fffffff);  // e4m3 has no infinity: the row's scores are NaN
           const f2 up2 = pack2(up, up);
 #pragma unroll 1
           for (int x = 0; x < D / 8; x += 4) {

@@ -12,8 +12,8 @@
 // What bounds it: blocks of one sequence follow one another, and in each a chain
 // of three products and the register work between them.  Hence two kernels:
 //  * prepare_kernel does what no state enters, for all blocks side by side: keys and
-//    queries to fp16, K K^T and Q K^T (once for the value heads of a key head),
-//    decays, T and P, laid out in the workspace the way the chain's copies take them.
+//    queries to fp16, K K^T and Q K^T (once for the value heads of a key head, where there
+//    are many), decays, T and P, laid out in the workspace the way the chain's copies take them.
 //  * chain_kernel walks the blocks of one sequence, value head and 128 rows of the
 //    state.  Everything is held transposed, a row of the state (and of U, O) per lane
 //    of tensor memory: X = S K^T, R = b (v - e^G X), U = R T^T, S' = U~ K; each result is
@@ -21,6 +21,9 @@
 //    next product's first operand.  Two threads share a row; S stays in their
 //    registers, in fp32.  Four warps write the output meanwhile, one issues the
 //    products, one the copies (up to three blocks ahead).
+//    A block takes it 2.5 us, 0.7 of them products; the rest is their results' way through
+//    registers, four times a block.
+//  * both_kernel is the chains with the preparation of later blocks on the SMs that they leave.
 //  * Products take fp16 operands and fp32 sums.  S, R, U and T are fp32 values held
 //    as two fp16 parts (x = hi + lo, 2^-22 of x), so that a state stays an fp32 one; what
 //    only an output sees (S and U there, and P) is one part, 2^-11 beside the
@@ -70,6 +73,10 @@ __host__ __device__ constexpr int key_bytes() { return C * DK * 2; }  // a block
 struct ChunkParams {
   PoolParams p;
   uint8_t *keys, *heads;  // [blocks][Hk][2][key_bytes], [blocks][Hv][HEAD_BYTES]
+  int split;              // prepare_kernel: a CTA a value head, not a key head
+  int first;              // only a sequence's first blocks are prepared before the chains start (0: all)
+  unsigned *made;         // [blocks][Hv]: a later block prepared, beside the chains
+  int makers;             // CTAs that do
   int row_blocks;         // of ROWS rows a value head
   int stall;              // test aid: the first block never arrives
 };
@@ -154,43 +161,19 @@ __device__ __forceinline__ void put_tile(float *a, const float (&d)[4], bool min
   *reinterpret_cast<float2 *>(x + 8 * AS) = minus ? make_float2(-d[2], -d[3]) : make_float2(d[2], d[3]);
 }
 
+// Prepares rows r0..r0+m-1, block w of the workspace, for value heads e0..e1-1 of key head hk: 128
+// threads (pt), `smem` and 64 columns of tensor memory of their own.
 template <int DK>
-__global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__ ChunkParams CP) {
+__device__ __forceinline__ void prepare(const ChunkParams &CP, uint8_t *smem, uint32_t tb, uint64_t *done, uint32_t parity,
+                                        int barrier, int pt, int hk, int e0, int e1, int w, long long r0,
+                                        int m) {
   using Y = PL<DK>;
   const PoolParams &P = CP.p;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  if (smem_u32(smem) & 1023u) {
-    if (threadIdx.x == 0) atomicOr(P.err, ERR_TIMEOUT);
-    return;
-  }
   float *A = reinterpret_cast<float *>(smem + Y::A);
   float *gh = reinterpret_cast<float *>(smem + Y::GH), *gl = gh + C;
   int *ex = reinterpret_cast<int *>(smem + Y::EX);
-  uint64_t *done = reinterpret_cast<uint64_t *>(smem + Y::BAR);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
-  const int pt = threadIdx.x, pw = pt >> 5, lane = pt & 31;
-  pdl_wait();
-  // ---- the block: sequence and first row ----
-  const int w = blockIdx.x / P.Hk, hk = blockIdx.x - w * P.Hk;  // (key heads of the same tokens side by side)
-  int lo = 0, hi = P.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first_block(P, mid, P.cu[mid]) <= w) lo = mid; else hi = mid - 1;
-  }
-  const int2 own = rows_of(P, lo, false);
-  const int c = w - first_block(P, lo, own.x);
-  if (c < 0 || c * C >= own.y) return;
-  const long long r0 = own.x + (long long)c * C;
-  const int m = imin(C, own.y - c * C);
-  const int group = P.Hv / P.Hk;
-  if (pt == 0) {
-    mbar_init(done, 1);
-    fence_barrier_init();
-  }
-  if (pw == 0) {
-    tc::tmem_alloc(tmem_slot, 64u);
-    tc::tmem_relinquish();
-  }
+  const int pw = pt >> 5, lane = pt & 31, group = P.Hv / P.Hk;
+  auto sync = [&]() { named_barrier(barrier, 128); };
   // ---- keys and queries to fp16: eight threads a row ----
   {
     constexpr int PR = DK / 64;  // 16-byte pieces a thread
@@ -231,7 +214,7 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
         for (int z = 0; z < PR; ++z) {
           const uint4 d = make_uint4(two(v[y][z].x), two(v[y][z].y), two(v[y][z].z), two(v[y][z].w));
           *reinterpret_cast<uint4 *>(smem + Y::KQ + z * 128 * 128 + swz(half * C + t, s8)) = d;
-          *reinterpret_cast<uint4 *>(image + half * key_bytes<DK>() + z * C * 128 + swz(t, s8)) = d;
+          if (e0 == 0) *reinterpret_cast<uint4 *>(image + half * key_bytes<DK>() + z * C * 128 + swz(t, s8)) = d;
         }
         if (s8 == 0) ex[half * C + t] = E;
       }
@@ -239,9 +222,8 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
   }
   fence_proxy_async();
   tc::fence_before_sync();
-  __syncthreads();
+  sync();
   tc::fence_after_sync();
-  const uint32_t tb = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   // ---- K K^T over Q K^T ----
   if (pw == 0 && tc::elect_one()) {
     const uint64_t da = tc::smem_desc_sw128(smem_u32(smem + Y::KQ), 16, 1024);
@@ -253,18 +235,18 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
     tc::commit(done);
   }
   __syncwarp();
-  mbar_wait(done, 0, P.err);
+  mbar_wait(done, parity, P.err);
   __syncwarp();
   tc::fence_after_sync();
   const bool isP = pw >= 2;
   const int i = (pw & 1) * 32 + lane;  // this thread's row of A, or of P
   const float e_i = pow2_field(imin(ex[i] + 4, 254));  // 2^e of its key
-  for (int e = 0; e < group; ++e) {
+  for (int e = e0; e < e1; ++e) {
     const int h = hk * group + e;
     uint8_t *out = CP.heads + ((size_t)w * P.Hv + h) * HEAD_BYTES;
     float be = 0.f;
     if (i < m) be = P.b[(r0 + i) * P.Hv + h];
-    __syncthreads();  // A and G of the head before (the products' operands) have been read
+    sync();  // A and G of the head before (the products' operands) have been read
     if (pw == 0) {  // running sums of the gates, in units of log 2, two tokens a lane
       auto gate = [&](int t) {
         float g = t < m ? P.g[(r0 + t) * P.Hv + h] : 0.f;
@@ -286,7 +268,7 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
       *reinterpret_cast<float2 *>(gh + 2 * lane) = make_float2(x0.x, x.x);
       *reinterpret_cast<float2 *>(gl + 2 * lane) = make_float2(x0.y, x.y);
     }
-    __syncthreads();
+    sync();
     Scalars *S = reinterpret_cast<Scalars *>(out + 3 * PART);
     const float hi_i = gh[i], lo_i = gl[i], ga = ex2_approx(hi_i + lo_i);
     if (!isP) {
@@ -346,7 +328,7 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
         }
       }
     }
-    __syncthreads();
+    sync();
     // ---- T = (I + A)^-1 in place: a 16 x 16 block a warp, a column a lane ----
     {
       const int o = pw * 16;
@@ -370,7 +352,7 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
         for (int r = 0; r < 16; ++r) A[(o + r) * AS + o + lane] = x[r];
       }
     }
-    __syncthreads();
+    sync();
     // joined: T21 = -T22 (A21 T11), 16 rows and columns of two pairs, then 32 of one; the
     // products in two fp16 parts too (on the CUDA cores their operands' way through shared
     // memory took longer than all else here)
@@ -385,9 +367,9 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
         left_operand(l, left, lane);
         right_operand(r, right, lane);
         multiply(d, l, r);
-        __syncthreads();
+        sync();
         put_tile(A + (o + 16) * AS + n0, d, pass, lane);
-        __syncthreads();
+        sync();
       }
     }
     {
@@ -406,10 +388,10 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
             multiply(d[z], l, r);
           }
         }
-        __syncthreads();
+        sync();
 #pragma unroll
         for (int z = 0; z < 2; ++z) put_tile(A + m0 * AS + n0 + 8 * z, d[z], pass, lane);
-        __syncthreads();
+        sync();
       }
     }
     // ---- T in two parts: pieces of eight, a row's eight pieces side by side ----
@@ -426,9 +408,60 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
       *reinterpret_cast<uint4 *>(out + PART + swz(r, p)) = tl;
     }
   }
+}
+
+template <int DK>
+__global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__ ChunkParams CP) {
+  using Y = PL<DK>;
+  const PoolParams &P = CP.p;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(P.err, ERR_TIMEOUT);
+    return;
+  }
+  uint64_t *done = reinterpret_cast<uint64_t *>(smem + Y::BAR);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  const int pt = threadIdx.x;
+  pdl_wait();
+  // ---- the block: sequence and first row ----
+  const int group = P.Hv / P.Hk, heads = CP.split ? P.Hv : P.Hk;
+  int w = blockIdx.x / heads, b, c;  // (heads of the same tokens side by side)
+  const int head = blockIdx.x - w * heads, hk = CP.split ? head / group : head;
+  const int e0 = CP.split ? head - hk * group : 0, e1 = CP.split ? e0 + 1 : group;
+  int2 own;
+  if (CP.first) {
+    const unsigned flags = (unsigned)(P.T / C + P.B) * P.Hv;
+    for (unsigned x = blockIdx.x * 128 + pt; x < flags; x += gridDim.x * 128) CP.made[x] = 0;
+    b = w / CP.first, c = w - b * CP.first;
+    own = rows_of(P, b, false);
+    w = first_block(P, b, own.x) + c;
+  } else {
+    int lo = 0, hi = P.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first_block(P, mid, P.cu[mid]) <= w) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    own = rows_of(P, b, false);
+    c = w - first_block(P, b, own.x);
+  }
+  if (c < 0 || c * C >= own.y) return;
+  if (pt == 0) {
+    mbar_init(done, 1);
+    fence_barrier_init();
+  }
+  if (pt < 32) {
+    tc::tmem_alloc(tmem_slot, 64u);
+    tc::tmem_relinquish();
+  }
   tc::fence_before_sync();
   __syncthreads();
-  if (pw == 0) {
+  tc::fence_after_sync();
+  const uint32_t tb = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  prepare<DK>(CP, smem, tb, done, 0, 0, pt, hk, e0, e1, w, own.x + (long long)c * C, imin(C, own.y - c * C));
+  tc::fence_before_sync();
+  __syncthreads();
+  if (pt < 32) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tb, 64u);
   }
@@ -439,6 +472,7 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
 // fetches, one issues the products.
 constexpr int ROW_WARPS = 8, OUT_WARPS = 4, FETCH = ROW_WARPS + OUT_WARPS, ISSUE = FETCH + 1;
 constexpr int CHAIN_THREADS = (ROW_WARPS + OUT_WARPS + 4) * 32, STAGES = 3;
+constexpr int FIRST = 8;  // blocks of a sequence that are prepared before the chains, where later ones are beside them
 
 template <int DK>
 struct CL {
@@ -484,16 +518,26 @@ __device__ __forceinline__ void state_store(const CUtensorMap *map, const void *
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// Whether another CTA's flag is up, sooner or later.
+__device__ __forceinline__ bool wait_flag(const unsigned *flag, unsigned *err) {
+  unsigned x;
+  const long long t0 = clock64();
+  while (true) {
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(flag) : "memory");
+    if (x) return true;
+    if (clock64() - t0 > WAIT_LIMIT_CYCLES) {
+      atomicOr(err, ERR_TIMEOUT);
+      return false;
+    }
+    __nanosleep(100);
+  }
+}
+
+// Item `id` of the chains.  `beside`: other CTAs of the launch prepare the blocks meanwhile.
 template <int DK>
-__global__ void __launch_bounds__(CHAIN_THREADS, 1)
-    chain_kernel(const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapS, const __grid_constant__ ChunkParams CP) {
+__device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap &mapS, const ChunkParams &CP, uint8_t *smem, int id, bool beside) {
   using Y = CL<DK>;
   const PoolParams &P = CP.p;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  if (smem_u32(smem) & 1023u) {  // swizzled tiles need it; so it is in a kernel without static shared memory
-    if (threadIdx.x == 0) atomicOr(P.err, ERR_TIMEOUT);
-    return;
-  }
   uint64_t *full = reinterpret_cast<uint64_t *>(smem);     // [STAGES]
   uint64_t *empty = full + STAGES;                         // [STAGES]
   uint64_t *s_ready = empty + STAGES;                      // [2] first and second half of each thread's k-steps of S
@@ -523,8 +567,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
   pdl_wait();
   // ---- the item: longest sequences first ----
   const int per = P.Hv * CP.row_blocks;
-  int b = blockIdx.x / per;
-  const int rest = blockIdx.x - b * per, h = rest / CP.row_blocks, i0 = (rest - h * CP.row_blocks) * ROWS;
+  int b = id / per;
+  const int rest = id - b * per, h = rest / CP.row_blocks, i0 = (rest - h * CP.row_blocks) * ROWS;
   if (P.B > 1 && P.B <= MAX_SORTED) {
     int *len = reinterpret_cast<int *>(smem + Y::XCHG);
     if (tid < P.B) len[tid] = rows_of(P, tid, false).y;
@@ -577,6 +621,11 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
           const int st = c % STAGES;
           if (c >= STAGES) ok = mbar_wait(&empty[st], (c / STAGES - 1) & 1, P.err);
           if (c == STAGES - 1 && slot >= 0) ok = mbar_wait(s_read, 0, P.err);
+          if (beside && ok && c >= CP.first) {
+            const unsigned *made = CP.made + (size_t)(w0 + c) * P.Hv;  // (keys come with the first of their value heads)
+            ok = wait_flag(made + hk * (P.Hv / P.Hk), P.err) && wait_flag(made + h, P.err);
+            fence_proxy_async();  // what was stored there is read by copies
+          }
           if (!ok) break;
           uint8_t *at = ring + st * Y::STAGE;
           mbar_arrive_expect_tx(&full[st], 2 * key_bytes<DK>() + HEAD_BYTES + C * ROWS * 2);
@@ -917,6 +966,83 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
 }
 
 // Blocks that the workspace has places for.
+template <int DK>
+__global__ void __launch_bounds__(CHAIN_THREADS, 1)
+    chain_kernel(const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapS, const __grid_constant__ ChunkParams CP) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // swizzled tiles need it; so it is in a kernel without static shared memory
+    if (threadIdx.x == 0) atomicOr(CP.p.err, ERR_TIMEOUT);
+    return;
+  }
+  chain<DK>(mapV, mapS, CP, smem, blockIdx.x, false);
+}
+
+// The chains, and the preparation of all but a sequence's first blocks beside them: few
+// items (one sequence: a chain a value head) leave most SMs idle.  The launch's first CTAs prepare, block
+// by block in the order in which the chains take them, and put up a flag for each; the chains
+// wait for the flags.  The preparing CTAs wait for nobody and start first, so every wait ends.
+constexpr int MAKER_GROUPS = CHAIN_THREADS / 128;
+template <int DK>
+__global__ void __launch_bounds__(CHAIN_THREADS, 1)
+    both_kernel(const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapS, const __grid_constant__ ChunkParams CP) {
+  using Y = PL<DK>;
+  constexpr int OWN = (Y::BYTES + 1023) / 1024 * 1024;
+  static_assert(MAKER_GROUPS * OWN <= CL<DK>::BYTES && MAKER_GROUPS * 64 <= 512, "a group's shared and tensor memory");
+  const PoolParams &P = CP.p;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(P.err, ERR_TIMEOUT);
+    return;
+  }
+  if ((int)blockIdx.x >= CP.makers) {
+    chain<DK>(mapV, mapS, CP, smem, blockIdx.x - CP.makers, true);
+    return;
+  }
+  const int g = threadIdx.x >> 7, pt = threadIdx.x & 127;
+  uint8_t *own = smem + g * OWN;
+  uint64_t *done = reinterpret_cast<uint64_t *>(own + Y::BAR);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Y::BAR + 8);
+  if (pt == 0) {
+    mbar_init(done, 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x < 32) {
+    tc::tmem_alloc(tmem_slot, MAKER_GROUPS * 64u);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tb = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  pdl_wait();
+  const int group = P.Hv / P.Hk;
+  int most = 0;  // blocks of the longest sequence
+  for (int b = threadIdx.x & 31; b < P.B; b += 32) most = imax(most, (rows_of(P, b, false).y + C - 1) / C);
+  most = __reduce_max_sync(0xffffffffu, most);
+  const long long tasks = (long long)imax(0, most - CP.first) * P.B * P.Hv;
+  uint32_t parity = 0;
+  for (long long x = blockIdx.x + (long long)g * CP.makers; x < tasks; x += (long long)MAKER_GROUPS * CP.makers) {
+    const long long y = x / P.Hv;
+    const int h = (int)(x - y * P.Hv), later = (int)(y / P.B), b = (int)(y - (long long)later * P.B), c = later + CP.first;
+    const int2 rows = rows_of(P, b, false);
+    if (c * C >= rows.y) continue;
+    const int w = first_block(P, b, rows.x) + c;
+    prepare<DK>(CP, own, tb + 64 * g, done, parity, 1 + g, pt, h / group, h % group, h % group + 1, w, rows.x + (long long)c * C, imin(C, rows.y - c * C));
+    parity ^= 1;
+    __threadfence();
+    fence_proxy_async();
+    named_barrier(1 + g, 128);
+    if (pt == 0)
+      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&CP.made[(size_t)w * P.Hv + h]), "r"(1u) : "memory");
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tb, MAKER_GROUPS * 64u);
+  }
+}
+
 inline long long places(int B, int T) { return (long long)T / C + B; }
 inline size_t padded(int dv) { return ((size_t)dv + ROWS - 1) / ROWS * ROWS; }
 
@@ -945,9 +1071,22 @@ sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
   if (fn(&ms, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 5, P.states.ptr, sdims, sstr, sbox, sest, CU_TENSOR_MAP_INTERLEAVE_NONE,
          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return SV_ERR_CUDA;
-  cudaError_t e = launch_early(prepare_kernel<DK>, dim3((unsigned)(blocks * P.Hk)), dim3(128), (size_t)PL<DK>::BYTES, s, CP);
+  const int sms = device_sm_count();
+  if (sms <= 0) return SV_ERR_CUDA;
+  // Few items: all but the first blocks are prepared while the chains run (one sequence of 8192
+  // tokens, 48 heads of 128 x 128: 338 us against 401; 2000 tokens 101 against 111; 1000 not faster).
+  CP.first = items <= sms / 2 && P.T > 2LL * FIRST * C * P.B ? FIRST : 0;
+  const long long before = CP.first ? (long long)P.B * FIRST : blocks;
+  // A value head a CTA while all of them are on the SMs at once, its key head's products made anew for
+  // each (77 tokens: 18 us against 24; but eleven prompts of 1 to 3001 tokens 225 us against 199).
+  CP.split = before * P.Hv <= 6LL * sms;
+  const long long grid = before * (CP.split ? P.Hv : P.Hk);
+  cudaError_t e = launch_early(prepare_kernel<DK>, dim3((unsigned)grid), dim3(128), (size_t)PL<DK>::BYTES, s, CP);
   if (e != cudaSuccess) return SV_ERR_CUDA;
-  return from_cuda(launch_early(chain_kernel<DK>, dim3((unsigned)items), dim3(CHAIN_THREADS), (size_t)CL<DK>::BYTES, s, mv, ms, CP));
+  const size_t smem = CL<DK>::BYTES;
+  if (!CP.first) return from_cuda(launch_early(chain_kernel<DK>, dim3((unsigned)items), dim3(CHAIN_THREADS), smem, s, mv, ms, CP));
+  CP.makers = sms - (int)items;
+  return from_cuda(launch_early(both_kernel<DK>, dim3(sms), dim3(CHAIN_THREADS), smem, s, mv, ms, CP));
 }
 
 }  // namespace
@@ -960,7 +1099,7 @@ extern "C" {
 
 size_t gdn_chunk_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv) {
   if (B < 1 || T < 1 || Hk < 1 || Hv < 1 || dv < 1 || (dk != 64 && dk != 128)) return 0;
-  const size_t per = (size_t)Hk * 4 * gdn::C * dk + (size_t)Hv * gdn::HEAD_BYTES;
+  const size_t per = (size_t)Hk * 4 * gdn::C * dk + (size_t)Hv * (gdn::HEAD_BYTES + 4);
   return (size_t)gdn::places(B, T) * per;
 }
 
@@ -980,7 +1119,7 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   // a tensor map steps by every stride: values that repeat (stride 0) have none
   if ((T > 1 && !v->token_stride) || (Hv > 1 && !v->head_stride)) return SV_ERR_UNSUPPORTED;
   const int row_blocks = (int)(gdn::padded(dv) / gdn::ROWS);
-  if ((long long)B * Hv * row_blocks > 0x7fffffffLL || gdn::places(B, T) * Hk > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
+  if ((long long)B * Hv * row_blocks > 0x7fffffffLL || gdn::places(B, T) * Hv > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
   if (!workspace || ws_bytes < gdn_chunk_workspace_bytes(B, T, Hk, Hv, dk, dv)) return SV_ERR_WORKSPACE;
   if (!paged::aligned(workspace, 16)) return SV_ERR_INVALID_ARG;
   gdn::ChunkParams CP{};
@@ -995,13 +1134,15 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   P.commit = 1;
   CP.keys = static_cast<uint8_t *>(workspace);
   CP.heads = CP.keys + (size_t)gdn::places(B, T) * Hk * 4 * gdn::C * dk;
+  CP.made = reinterpret_cast<unsigned *>(CP.heads + (size_t)gdn::places(B, T) * Hv * gdn::HEAD_BYTES);
   CP.row_blocks = row_blocks;
   CP.stall = launch_flags() & SV_LAUNCH_TEST_STALL_COPY ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // A block costs as much with one token as with 64, and an item several times that; token by token
-  // is faster up to some eight tokens a sequence (48 heads of 128 x 128: one sequence of 16 tokens 12 us
-  // against 20, of 32 21 both; eight of 8 27 against 37, of 16 46 against 37; 64 of 8 178 against 215).
-  if (T <= 24 || T <= 8LL * B) return gdn::launch_tokens(P, dk, s);
+  // A block costs as much with one token as with 64; token by token is faster up to some eight tokens a
+  // sequence (48 heads of 128 x 128: one sequence of 16 tokens 13 us against 15.5, of 24 17.6 against 15.1;
+  // two of 8 12 against 16, of 12 20 against 16; eight of 8 25 against 34, of 12 34 both; 64 of 8 169
+  // against 218, of 12 231 against 219; a long sequence among short ones takes 0.55 us a token).
+  if (T <= 20 || T <= 8LL * B) return gdn::launch_tokens(P, dk, s);
   return dk == 64 ? gdn::run_chunks<64>(CP, s) : gdn::run_chunks<128>(CP, s);
 }
 

@@ -157,7 +157,7 @@ def test_scores_far_apart(cuda_lib, e4m3):
 
 
 def test_queries_of_any_size(cuda_lib):
-    """e4m3 pages turn queries to fp16 behind a power of two a row."""
+    """Beside e4m3 pages queries are two e4m3 parts behind a power of two a row."""
     c = Call(cuda_lib, [(60, 200)], 4, 2, 128, 16, e4m3=True, seed=9, dirty=False)
     for size in (1e-30, 1e-3, 1e4, 1e30):
         c.q = (torch.randn(60, 8, 128, generator=torch.Generator().manual_seed(1)) * size).bfloat16()
@@ -167,6 +167,26 @@ def test_queries_of_any_size(cuda_lib):
         c.want = [attend(c.q[:, :4], K, V, 140, c.scale, 0, 0)]
         if 1e-35 < c.scale < 1e35:
             c.check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_queries_that_are_not_finite(cuda_lib, e4m3):
+    """They reach their own rows only, and none that sees nothing."""
+    sv = cuda_lib
+    c = Call(sv, [(5, 2), (9, 40)], 4, 2, 128, 16, e4m3=e4m3, seed=13, dirty=False)
+    t = c.tensors()
+    good = c.run(t).clone()
+    t[0][0] = float("nan")             # rows 0..2 stand before position 0
+    t[0][1, :, 3] = float("inf")
+    t[0][8, 1, 100] = float("nan")
+    t[0][9, 2, 5] = float("inf")
+    o = c.run(t)
+    assert sv.sv_last_device_error() == sv.SV_OK
+    assert bool((o[:3] == 0).all())
+    assert bool(o[8, 1].isnan().all())
+    good[8, 1] = good[9, 2] = 0
+    o[8, 1] = o[9, 2] = 0
+    assert torch.equal(o, good)
 
 
 def test_pages_lengths_and_offsets_out_of_range(cuda_lib):

@@ -43,8 +43,8 @@ def test_chunk_attention(cuda_lib, seqs, Hq, Hkv, D, e4m3):
     c.check()
 
 
-# one chain of several blocks; more CTAs than fit at once
-@pytest.mark.parametrize("lens,Hv,dk,dv", [([400], 2, 128, 128), ([70, 3, 90], 4, 64, 200), ([40] * 90, 4, 128, 64)])
+# one chain of several blocks; more CTAs than fit at once; blocks prepared beside the chains
+@pytest.mark.parametrize("lens,Hv,dk,dv", [([400], 2, 128, 128), ([70, 3, 90], 4, 64, 200), ([40] * 90, 4, 128, 64), ([2600], 2, 128, 128)])
 def test_chunked_rule(cuda_lib, lens, Hv, dk, dv):
     sv, B, T = cuda_lib, len(lens), sum(lens)
     r = gdn_plain.rows(T, 2, Hv, dk, dv, 3)

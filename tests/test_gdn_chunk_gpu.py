@@ -65,6 +65,17 @@ def test_shapes(cuda_lib, dk, dv):
     case(cuda_lib, [70, 5, 130], 2, 4, dk, dv, seed=dk + dv)
 
 
+@pytest.mark.parametrize("lens,Hk,Hv,dk,dv", [
+    ([1100], 1, 2, 128, 128), ([3000, 1, 200], 2, 2, 128, 64), ([0, 2100], 1, 3, 64, 200), ([513, 512, 1200, 1900], 1, 1, 64, 8)])
+def test_long_sequences_of_few_heads(cuda_lib, lens, Hk, Hv, dk, dv):
+    """Later blocks are prepared beside the chains that take them."""
+    case(cuda_lib, lens, Hk, Hv, dk, dv, seed=len(lens) + dk, extra=3)
+
+
+def test_many_value_heads_of_a_key_head(cuda_lib):
+    case(cuda_lib, [1030, 20], 1, 12, 64, 16, seed=21)
+
+
 def test_ragged_with_empty_sequences_and_rows_behind(cuda_lib):
     case(cuda_lib, [0, 3, 0, 190, 64, 1, 0, 77], 2, 6, 128, 64, seed=4, extra=9)
 
@@ -146,13 +157,34 @@ def test_offsets_out_of_order(cuda_lib):
     assert sv.sv_last_device_error() == sv.SV_OK
 
 
-def test_bits_repeat_and_a_captured_call_follows_its_inputs(cuda_lib):
+def test_offsets_that_fall_far(cuda_lib):
+    """Sequences that share rows: nothing waits for what never comes, and the next call is right."""
     sv = cuda_lib
-    lens, Hk, Hv, dk, dv = [130, 7, 260], 2, 4, 128, 128
+    T, Hk, Hv, dk, dv = 3200, 1, 2, 64, 64
+    r = plain.on(plain.rows(T, Hk, Hv, dk, dv, 15))
+    slots = torch.arange(3, dtype=torch.int32, device="cuda")
+    states, o = torch.zeros(3, Hv, dv, dk, device="cuda"), torch.zeros(T, Hv, dv, device="cuda", dtype=torch.bfloat16)
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    good = [states.clone(), o.clone()]
+    chunk(sv, good[0], slots, r, good[1], ints(0, 3000, 3100, 3200))
+    assert sv.sv_last_device_error() == sv.SV_OK
+    for cu in ((0, 3000, 100, 3200), (100, 3200, 0, 3100), (0, 3201, 0, 3200)):
+        chunk(sv, states, slots, r, o, ints(*cu))
+        assert sv.sv_last_device_error() == sv.SV_ERR_INVALID_ARG
+    states.zero_()
+    chunk(sv, states, slots, r, o, ints(0, 3000, 3100, 3200))
+    assert sv.sv_last_device_error() == sv.SV_OK
+    assert torch.equal(states, good[0]) and torch.equal(o, good[1])
+
+
+@pytest.mark.parametrize("lens", [[130, 7, 260], [1500, 7, 1700]])
+def test_bits_repeat_and_a_captured_call_follows_its_inputs(cuda_lib, lens):
+    sv = cuda_lib
+    Hk, Hv, dk, dv = 2, 4, 128, 128
     T = sum(lens)
     q, k, v, g, beta = plain.on(plain.rows(T, Hk, Hv, dk, dv, 14))
     pool = torch.randn(5, Hv, dv, dk, generator=torch.Generator().manual_seed(2)).cuda()
-    slots, cu = torch.tensor([3, 0, 4], dtype=torch.int32, device="cuda"), torch.tensor([0, 130, 137, T], dtype=torch.int32, device="cuda")
+    slots, cu = torch.tensor([3, 0, 4], dtype=torch.int32, device="cuda"), torch.tensor([0, lens[0], lens[0] + 7, T], dtype=torch.int32, device="cuda")
     ws = sv.workspace(sv.gdn_chunk_workspace_bytes(3, T, Hk, Hv, dk, dv))
 
     def once(st, o):
