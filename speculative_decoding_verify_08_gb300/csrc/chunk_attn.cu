@@ -96,7 +96,7 @@ struct Params {
   int width, page_size, num_pages;
   int R, piece;  // slots of a copy; first keys that may share a block with others (whole copies)
   const float *ks, *vs;
-  float *opart;  // [2 * ctas][NT * ROWS][D] unnormalised O
+  float *opart;  // [2 * ctas][NT][D / 4][ROWS][4] unnormalised O
   float2 *ml;    // [2 * ctas][NT * ROWS] maximum (log2 domain) and sum
   Cut *cuts;     // [ctas]
   unsigned *err;
@@ -376,26 +376,28 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   // ---- this CTA's piece of the line ----
   {
     auto weight = [&](int c) { return c < tiles ? tile_at<NT>(P, pre, c, 0).n + HEAD_COST : 0; };
-    int per_head = 0, all = 0, mine = 0;
+    int per_head = 0, all = 0, mine = 0, upto = 0;
     for (int c0 = 0; c0 < tiles; c0 += C::THREADS) {
       mine = weight(c0 + tid);
-      scan(mine, all);
+      upto = scan(mine, all);
       per_head += all;  // (in 31 bits with the heads: checked on the host)
     }
     // (no CTA takes less than four blocks' time, so that no two cuts coincide)
     const int W = per_head * P.Hkv, ctas = imin(gridDim.x, imax(1, W / 4));
-    auto line = [&](int x) { return (int)((long long)W * imin(x, ctas) / ctas); };
+    const int share = W / ctas, rest = W - share * ctas;
+    auto line = [&](int x) { return x = imin(x, ctas), share * x + rest * x / ctas; };  // W * x / ctas
     const int at[2] = {line(blockIdx.x), line(blockIdx.x + 1)};
     // A cut this near to an item's beginning or end moves there: what cutting costs (both
     // pieces' O through the workspace) is a block or two.
-    const int near = imax(3, W / ctas / 16);
+    const int near = imax(3, share / 16);
     if (tid < 2) cut[tid] = make_int2(tiles * P.Hkv, 0);
     if (tid == 0) P.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     int before = 0;
     for (int c0 = 0; c0 < tiles; c0 += C::THREADS) {
-      const int c = c0 + tid, w = tiles > C::THREADS ? weight(c) : mine;
-      const int x = before + scan(w, all) - w;  // tiles' weight before this one
+      const bool again = tiles > C::THREADS;
+      const int c = c0 + tid, w = again ? weight(c) : mine;
+      const int x = before + (again ? scan(w, all) : upto) - w;  // tiles' weight before this one
       before += all;
 #pragma unroll 1
       for (int e = 0; e < 2; ++e) {
@@ -407,10 +409,9 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
           // cut at its end, and not in the same item at its beginning: the item begins here; every
           // CTA up to the last cut in it has a piece
           const int last_cut = at[1] - j + n - near;  // of the line, the last place to cut it
-          int more_ctas = 1;
-          while (line(blockIdx.x + 1 + more_ctas) <= last_cut && (int)blockIdx.x + 1 + more_ctas < ctas) ++more_ctas;
+          const int last = (int)lmin(ctas - 1, (((long long)last_cut + 1) * ctas - 1) / W);  // the last x with line(x) <= last_cut
           const Item it = tile_at<NT>(P, pre, c, h);
-          P.cuts[blockIdx.x] = Cut{it.h, it.q0, it.rows, 1 + more_ctas};
+          P.cuts[blockIdx.x] = Cut{it.h, it.q0, it.rows, 1 + imax(1, last - (int)blockIdx.x)};
         }
       }
     }
@@ -612,15 +613,17 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
           float up = __int_as_float((261 - E) << 23);  // 2^(7 - (E - 127))
           rowscale[((worked & 1) * NT + t) * ROWS + i] = 1.f / up;
           if (e == 255) up = __int_as_float(0x7fffffff);  // e4m3 has no infinity: the row's scores are NaN
-          const f2 up2 = pack2(up, up);
-#pragma unroll 1
+          const f2 up2 = pack2(up, up), minus = pack2(-1.f, -1.f);
+#pragma unroll(NT == 1 ? 2 : 1)
           for (int x = 0; x < D / 8; x += 4) {
             uint4 hi[2], lo[2];
             auto two = [&](uint32_t y, uint32_t &l) {  // two elements
               const f2 v = mul2(pack2(bf16lo(y), bf16hi(y)), up2);
-              const uint32_t h = f32x2_to_e4m3x2(v), b = e4m3x2_to_f16x2(h);
-              l = f32x2_to_e4m3x2(fma2(pack2(f16lo(b), f16hi(b)), pack2(-1.f, -1.f), v));
-              return h;
+              // to four bits in fp32 (c - (c - v), Veltkamp): what e4m3 rounds to above 2^-6
+              const f2 c = mul2(v, pack2(0x1p20f + 1.f, 0x1p20f + 1.f)), d = fma2(v, minus, c);
+              const f2 h = fma2(d, minus, c);
+              l = f32x2_to_e4m3x2(fma2(h, minus, v));
+              return f32x2_to_e4m3x2(h);
             };
             auto four = [&](uint32_t y, uint32_t z, uint32_t &h, uint32_t &l) {
               uint32_t l0, l1;
@@ -971,7 +974,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       if (part.j0 > 0 || part.j1 < now.n) {  // a piece of an item: O as it is, maximum and sum
         const size_t at = ((size_t)(2 * blockIdx.x + (part.j0 > 0 ? 0 : 1)) * NT + t) * ROWS + r;
         if (hf == 0 && mine && ok) P.ml[at] = make_float2(m, l);
-        float4 *out = reinterpret_cast<float4 *>(P.opart + at * D + hf * O0);
+        // four columns of all rows side by side: a warp's store is 512 bytes in one piece
+        float4 *out = reinterpret_cast<float4 *>(P.opart + (at - r) * D) + (size_t)(hf * O0 / 4) * ROWS + r;
 #pragma unroll 1
         for (int c = 0; c < O0 / 32; ++c) {
           uint32_t o[32];
@@ -985,7 +989,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
           if (mine && ok) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              out[8 * c + e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+              out[(8 * c + e) * ROWS] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
           }
         }
         continue;
@@ -1049,67 +1053,62 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   }
 }
 
-
-// Joins the pieces of the item that CTA blockIdx.x begins and does not end, a row a warp.
+// Joins the pieces of the item that CTA blockIdx.x begins and does not end: a warp takes 8 rows of
+// 64 columns, a lane 16 columns of a row.
 constexpr int JOIN_BLOCKS = 8;
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params P, int rows) {
   pdl_wait();
   const Cut c = P.cuts[blockIdx.x];
   if (!c.pieces) return;
-  const int lane = threadIdx.x & 31, pt = ROWS / P.G, n = c.pieces;
+  const int lane = threadIdx.x & 31, n = c.pieces;
   const float vs = P.vs ? P.vs[c.h] : 1.f;
-  // rows of a piece; this CTA's second, then the others' first
+  // rows before a piece; this CTA's second, then the others' first
   auto piece = [&](int x) { return (size_t)(2 * (blockIdx.x + x) + (x == 0 ? 1 : 0)) * rows; };
 #pragma unroll 1
-  for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < rows; row += JOIN_BLOCKS * 8) {
+  for (int x8 = blockIdx.y * 8 + (threadIdx.x >> 5); x8 < rows / 8 * (D / 64); x8 += JOIN_BLOCKS * 8) {
+    const int row = x8 / (D / 64) * 8 + (lane & 7), c16 = x8 % (D / 64) * 16 + (lane >> 3) * 4;  // first four columns' place
     const int t = row / ROWS, r = row - t * ROWS, ir = r / P.G;
-    if (ir >= pt || t * pt + ir >= c.rows) continue;
+    if (ir >= P.PT || t * P.PT + ir >= c.rows) continue;
+    const float4 *src = reinterpret_cast<const float4 *>(P.opart) + (size_t)t * ROWS * (D / 4) + c16 * ROWS + r;
     float m = -INFINITY, l = 0.f;
-    float4 o[D / 128];
+#pragma unroll 8
+    for (int x = 0; x < n; ++x) m = fmaxf(m, P.ml[piece(x) + row].x);
+    float4 o[4];
 #pragma unroll
-    for (int e = 0; e < D / 128; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int e = 0; e < 4; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int x0 = 0; x0 < n; x0 += 32) {
-      const float2 s = x0 + lane < n ? P.ml[piece(x0 + lane) + row] : make_float2(-INFINITY, 0.f);
-      float top = s.x;
+    for (int x = 0; x < n; x += 4) {
+      float2 s[4];
+      float4 v[4][4];
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      top = fmaxf(top, m);
-      const float a = m == -INFINITY ? 0.f : ex2_approx(m - top), w = s.x == -INFINITY ? 0.f : ex2_approx(s.x - top);
-      m = top;
-      l = l * a + s.y * w;
+      for (int u = 0; u < 4; ++u) {
+        const size_t at = piece(imin(x + u, n - 1));
+        s[u] = x + u < n ? P.ml[at + row] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int e = 0; e < D / 128; ++e) o[e] = make_float4(o[e].x * a, o[e].y * a, o[e].z * a, o[e].w * a);
-      const int some = imin(32, n - x0);
-#pragma unroll 1
-      for (int x = 0; x < some; x += 4) {
-        float4 v[4][D / 128];
+        for (int e = 0; e < 4; ++e) v[u][e] = src[at * (D / 4) + e * ROWS];
+      }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float *src = P.opart + (piece(x0 + imin(x + u, some - 1)) + row) * D + lane * 4;
+      for (int u = 0; u < 4; ++u) {
+        const float w = s[u].x == -INFINITY ? 0.f : ex2_approx(s[u].x - m);
+        l = fmaf(s[u].y, w, l);
+        if (w == 0.f) continue;  // (a piece that the row sees nothing of holds anything)
 #pragma unroll
-          for (int e = 0; e < D / 128; ++e) v[u][e] = *reinterpret_cast<const float4 *>(src + e * 128);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float b = x + u < some ? __shfl_sync(0xffffffffu, w, x + u) : 0.f;
-          if (b == 0.f) continue;  // (a piece that the row sees nothing of holds anything)
-#pragma unroll
-          for (int e = 0; e < D / 128; ++e)
-            o[e] = make_float4(fmaf(v[u][e].x, b, o[e].x), fmaf(v[u][e].y, b, o[e].y), fmaf(v[u][e].z, b, o[e].z), fmaf(v[u][e].w, b, o[e].w));
-        }
+        for (int e = 0; e < 4; ++e)
+          o[e] = make_float4(fmaf(v[u][e].x, w, o[e].x), fmaf(v[u][e].y, w, o[e].y), fmaf(v[u][e].z, w, o[e].z), fmaf(v[u][e].w, w, o[e].w));
       }
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     const float f = l != 0.f ? vs / l : 0.f;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.o.ptr) + (long long)(c.q0 + t * pt + ir) * P.o.token_stride +
-                         (long long)(c.h * P.G + r - ir * P.G) * P.o.head_stride;
+    uint32_t y[8];
 #pragma unroll
-    for (int e = 0; e < D / 128; ++e)
-      *reinterpret_cast<uint2 *>(out + e * 128 + lane * 4) =
-          f != 0.f ? make_uint2(pack_bf16x2(o[e].x * f, o[e].y * f), pack_bf16x2(o[e].z * f, o[e].w * f)) : make_uint2(0u, 0u);
+    for (int e = 0; e < 4; ++e) {
+      y[2 * e] = f != 0.f ? pack_bf16x2(o[e].x * f, o[e].y * f) : 0u;
+      y[2 * e + 1] = f != 0.f ? pack_bf16x2(o[e].z * f, o[e].w * f) : 0u;
+    }
+    uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(P.o.ptr) + (long long)(c.q0 + t * P.PT + ir) * P.o.token_stride +
+                                           (long long)(c.h * P.G + r - ir * P.G) * P.o.head_stride + c16 * 4);
+    out[0] = make_uint4(y[0], y[1], y[2], y[3]);
+    out[1] = make_uint4(y[4], y[5], y[6], y[7]);
   }
 }
 
