@@ -76,7 +76,7 @@ struct Cfg {
   static constexpr uint32_t TO = 0, TS = NT * D;
   static_assert(NT * D + NT * NSB * BN <= 512, "tensor memory");
   // registers: as many as the threads start with
-  static constexpr int SOFT_REGS = F8 ? (NT == 2 ? 208 : 184) : 216, OTHER_REGS = F8 && NT == 2 ? 48 : 72;
+  static constexpr int SOFT_REGS = F8 ? (NT == 2 ? 216 : 184) : 216, OTHER_REGS = F8 && NT == 2 ? 40 : 72;
   static_assert(256 * SOFT_REGS + (THREADS - 256) * OTHER_REGS <= (65536 / THREADS / 8 * 8) * THREADS, "registers");
   // log2 of the factor on probabilities and their sum, and of the largest P against an
   // old maximum, factor included
@@ -285,23 +285,14 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   int *pre = reinterpret_cast<int *>(smem + (P.few_slots ? C::BEHIND : PREFIX));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int i = 0; i < 10; ++i) {
-      mbar_init(&full[i], (F8 && i >= 5 ? 4 : 1) + (i == 0 ? P.stall : 0));
-      mbar_init(&empty[i], 1);
-      if (F8 && i < 5) mbar_init(&copied[i], 1);
+  if (warp == 0) {  // a barrier a lane, in the order above
+    if (lane < 30) {
+      const int of_values = F8 && lane >= 5 && lane < 10 ? 4 : 1, softmax = 4 * C::HALVES;
+      const int n = lane < 10 ? of_values + (lane == 0 ? P.stall : 0)
+                              : (lane == 22 || lane == 23 || lane == 26 || lane == 27) ? softmax : 1;
+      mbar_init(&full[lane], n);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4 * C::HALVES);
-      mbar_init(&o_done[i], 1);
-      mbar_init(&p_half[i], 4);
-      mbar_init(&o_free[i], 4 * C::HALVES);
-    }
-    mbar_init(q_full, 1);
-    mbar_init(q_free, 1);
-    mbar_init(q_ready, 4);
-    mbar_init(idle, 1);
+    if (lane < 9) mbar_init(&more[lane], lane == 1 || lane == 2 || lane == 3 ? 4 : 1);
     fence_barrier_init();
   }
   if (warp == C::SOFT) {
@@ -348,20 +339,28 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   };
   const bool report = blockIdx.x == 0;
   int tiles = 0;
-  for (int b0 = 0; b0 < P.B; b0 += C::THREADS) {
-    const int b = b0 + tid;
-    const int nq = b < P.B ? rows_of(P, b, report) : 0;
-    const int len = b < P.B ? length_of(P, b, report) : 0;
-    const int nt = (nq + P.PT * NT - 1) / (P.PT * NT);
-    int all;
-    const int x = scan(nt, all);
-    if (b < P.B) {
-      if (P.B <= MAX_KEPT)
-        reinterpret_cast<int4 *>(pre)[b] = make_int4(sum(tiles, x) - nt, P.cu_q[b], nq, len);
-      else
-        pre[b] = sum(tiles, x) - nt;
+  if (P.B <= MAX_KEPT) {  // a sequence a lane, in every warp
+    const int q0 = lane < P.B ? P.cu_q[lane] : 0, nq = lane < P.B ? rows_of(P, lane, report) : 0;
+    const int len = lane < P.B ? length_of(P, lane, report) : 0, nt = (nq + P.PT * NT - 1) / (P.PT * NT);
+    int x = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = sum(x, y);
     }
-    tiles = sum(tiles, all);
+    if (warp == 0 && lane < P.B) reinterpret_cast<int4 *>(pre)[lane] = make_int4(x - nt, q0, nq, len);
+    tiles = __shfl_sync(0xffffffffu, x, 31);
+  } else {
+    for (int b0 = 0; b0 < P.B; b0 += C::THREADS) {
+      const int b = b0 + tid;
+      const int nq = b < P.B ? rows_of(P, b, report) : 0;
+      if (b < P.B) length_of(P, b, report);
+      const int nt = (nq + P.PT * NT - 1) / (P.PT * NT);
+      int all;
+      const int x = scan(nt, all);
+      if (b < P.B) pre[b] = sum(tiles, x) - nt;
+      tiles = sum(tiles, all);
+    }
   }
   if (tiles > P.most) {
     if (tid == 0 && blockIdx.x == 0) atomicOr(P.err, ERR_INDEX);
