@@ -71,7 +71,6 @@ struct Cfg {
   static constexpr int LESS_K = 2, LESS_V = F8 ? NV : 2;
   static_assert(NK * KSLOT + NV * SLOT == (F8 ? 128 : 160) * 1024 && LESS_K * KSLOT + LESS_V * SLOT == 128 * 1024, "ring");
   static constexpr int BEHIND = RING + 128 * 1024;  // prefix sums
-  static constexpr int SCALES = BEHIND + ((MAX_B + 1) * 4 + 15) / 16 * 16;  // [2][NT][ROWS] of e4m3's queries
   // tensor memory: O per tile, then the S buffers (P over S)
   static constexpr uint32_t TO = 0, TS = NT * D;
   static_assert(NT * D + NT * NSB * BN <= 512, "tensor memory");
@@ -267,18 +266,17 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
   uint64_t *p_full = s_full + 2;   // [2] per S buffer: P written over it
   uint64_t *o_done = p_full + 2;   // [2] per S buffer: the second product of its P done
   uint64_t *o_free = o_done + 2;   // [2] O read out
-  uint64_t *q_full = o_free + 2;   // queries of the item landed
-  uint64_t *q_free = q_full + 1;   // last S product of the item done
-  // (30 barriers, 240 bytes; the rest stands behind the cuts)
+  uint64_t *q_full = o_free + 2;   // [2] queries of a tile of the item landed
+  uint64_t *q_free = q_full + 2;   // last S product of the item done
+  // (31 barriers, 248 bytes; the rest stands behind the cuts)
   uint64_t *more = reinterpret_cast<uint64_t *>(smem + 280);
   uint64_t *idle = more, *p_half = more + 1;  // p_half [2] one S buffer: P of the first half of a block's keys written
-  uint64_t *q_ready = more + 3, *copied = more + 4;  // e4m3: queries turned, [5] copies of values landed
+  uint64_t *q_ready = more + 3, *copied = more + 5;  // e4m3: [2] queries of a tile turned, [5] copies of values landed
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + CUTS + 16);
   int2 *cut = reinterpret_cast<int2 *>(smem + CUTS);  // [2] item and block where this CTA begins, and the next one
   Item *info_it = reinterpret_cast<Item *>(smem + INFO);  // of the item whose queries landed
   int *info = reinterpret_cast<int *>(smem + INFO + 48);  // its first block, its end, its tiles
   float *xchg = reinterpret_cast<float *>(smem + 512);  // [2][2 halves][ROWS] maxima, then sums
-  float *rowscale = reinterpret_cast<float *>(smem + C::SCALES);  // e4m3: [2][NT][ROWS] what the rows' scores are multiplied by
   uint8_t *qs = smem + HEADER;
   uint8_t *ring = smem + C::RING;
   const int NK = P.few_slots ? C::LESS_K : C::NK, NV = P.few_slots ? C::LESS_V : C::NV;
@@ -286,13 +284,13 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 0) {  // a barrier a lane, in the order above
-    if (lane < 30) {
+    if (lane < 31) {
       const int of_values = F8 && lane >= 5 && lane < 10 ? 4 : 1, softmax = 4 * C::HALVES;
       const int n = lane < 10 ? of_values + (lane == 0 ? P.stall : 0)
                               : (lane == 22 || lane == 23 || lane == 26 || lane == 27) ? softmax : 1;
       mbar_init(&full[lane], n);
     }
-    if (lane < 9) mbar_init(&more[lane], lane == 1 || lane == 2 || lane == 3 ? 4 : 1);
+    if (lane < 10) mbar_init(&more[lane], lane == 1 || lane == 2 ? 4 : lane == 3 || lane == 4 ? 4 * C::HALVES : 1);
     fence_barrier_init();
   }
   if (warp == C::SOFT) {
@@ -520,7 +518,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       // --------------------------------------------------- queries --
       if (lane == 0) {
         bool ok = true;
-        uint32_t c = 0;  // parts with work so far
+        uint32_t c = 0, c1 = 0;  // parts with work so far, those with a second tile
         for (int k = 0; k < parts && ok; ++k) {
           const Item it = item_at<NT>(P, pre, id_of(k));
           const Part pt = part_of(k, it);
@@ -529,29 +527,32 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
           if (!ok) break;
           ++c;
           const int nt = it.rows > P.PT ? NT : 1;
+          c1 += nt - 1;
           *info_it = it;
           info[0] = pt.j0, info[1] = pt.j1, info[2] = nt;
-          mbar_arrive_expect_tx(q_full, (uint32_t)(nt * used * D * 2));
-          for (int t = 0; t < nt; ++t)
+          for (int t = 0; t < nt; ++t) {
+            mbar_arrive_expect_tx(&q_full[t], (uint32_t)(used * D * 2));
 #pragma unroll
             for (int g = 0; g < D / 64; ++g)
-              tma_load_4d(qs + t * C::QBYTES + g * ROWS * 128, &mapQ, 0, it.h * P.G, it.q0 + t * P.PT, g, q_full);
+              tma_load_4d(qs + t * C::QBYTES + g * ROWS * 128, &mapQ, 0, it.h * P.G, it.q0 + t * P.PT, g, &q_full[t]);
+          }
         }
         if (ok && c > 0) ok = mbar_wait(q_free, (c - 1) & 1, P.err);
         if (ok) {  // no part is left
           info[0] = info[1] = 0;
           mbar_arrive(q_full);
-        } else if (c > 0) {
-          mbar_wait(q_full, (c - 1) & 1, P.err);
+        } else {
+          if (c > 0) mbar_wait(q_full, (c - 1) & 1, P.err);
+          if (c1 > 0) mbar_wait(q_full + 1, (c1 - 1) & 1, P.err);
         }
       }
       __syncwarp();
     } else if (F8 && warp >= C::SOFT + 4) {
-      // --------------------------------------- queries to two e4m3 parts, values to fp16 --
+      // ------------------------------------------------ e4m3 values to fp16 --
       const int i = tid - (C::SOFT + 4) * 32;
       bool ok = true;
       int at_slot = 0;
-      uint32_t phase = 0, worked = 0;
+      uint32_t phase = 0;
       // One slot: its copy stands in the second half.  The half of the columns whose fp16 tiles lie in the
       // first half comes first, then, once all have read them, the rest.
       auto turn = [&](const Item &it, int j, int x) {
@@ -594,57 +595,6 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         const Item it = item_at<NT>(P, pre, id_of(k));
         const Part pt = part_of(k, it);
         if (pt.j0 == pt.j1) continue;
-        // This thread's row of the queries, scaled by a power of two: largest element in [2^7, 2^8).
-        // 32 elements at a time, in place: their first parts, then what those leave.
-        if (ok) ok = spin_wait(q_full, worked & 1, P.err);
-        ok = __all_sync(0xffffffffu, ok);
-#pragma unroll 1
-        for (int t = 0; t < NT; ++t) {
-          uint8_t *row = qs + t * C::QBYTES + i * 128;
-          auto place = [&](int x) { return reinterpret_cast<uint4 *>(row + (x >> 3) * ROWS * 128 + (((x & 7) ^ (i & 7)) << 4)); };
-          uint32_t mx = 0;  // (of finite values the larger has the larger bits)
-#pragma unroll 8
-          for (int x = 0; x < D / 8; ++x) {
-            const uint4 w = *place(x);
-            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-          }
-          const int e = (int)(max(mx & 0xffffu, mx >> 16) >> 7), E = imin(imax(e, 16), 254);
-          float up = __int_as_float((261 - E) << 23);  // 2^(7 - (E - 127))
-          rowscale[((worked & 1) * NT + t) * ROWS + i] = 1.f / up;
-          if (e == 255) up = __int_as_float(0x7fffffff);  // e4m3 has no infinity: the row's scores are NaN
-          const f2 up2 = pack2(up, up), minus = pack2(-1.f, -1.f);
-#pragma unroll(NT == 1 ? 2 : 1)
-          for (int x = 0; x < D / 8; x += 4) {
-            uint4 hi[2], lo[2];
-            auto two = [&](uint32_t y, uint32_t &l) {  // two elements
-              const f2 v = mul2(pack2(bf16lo(y), bf16hi(y)), up2);
-              // to four bits in fp32 (c - (c - v), Veltkamp): what e4m3 rounds to above 2^-6
-              const f2 c = mul2(v, pack2(0x1p20f + 1.f, 0x1p20f + 1.f)), d = fma2(v, minus, c);
-              const f2 h = fma2(d, minus, c);
-              l = f32x2_to_e4m3x2(fma2(h, minus, v));
-              return f32x2_to_e4m3x2(h);
-            };
-            auto four = [&](uint32_t y, uint32_t z, uint32_t &h, uint32_t &l) {
-              uint32_t l0, l1;
-              const uint32_t h0 = two(y, l0), h1 = two(z, l1);
-              h = h0 | h1 << 16, l = l0 | l1 << 16;
-            };
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint4 w = *place(x + 2 * z), w2 = *place(x + 2 * z + 1);
-              four(w.x, w.y, hi[z].x, lo[z].x);
-              four(w.z, w.w, hi[z].y, lo[z].y);
-              four(w2.x, w2.y, hi[z].z, lo[z].z);
-              four(w2.z, w2.w, hi[z].w, lo[z].w);
-            }
-#pragma unroll
-            for (int z = 0; z < 2; ++z) *place(x + z) = hi[z], *place(x + 2 + z) = lo[z];
-          }
-        }
-        ++worked;
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_ready);
         for (int j = pt.j0; j < pt.j1; ++j)
 #pragma unroll 1
           for (int x = 0; x < PARTS; ++x) turn(it, j, x);
@@ -688,7 +638,6 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       uint32_t oc[NT] = {};               // parts of each tile
       while (ok) {
         wait(q_full, c & 1);
-        if (F8 && info[1] > 0) wait(q_ready, c & 1);
         // (a limit may run out in some lanes while the phase completes for others)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -697,6 +646,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         const int nt = __shfl_sync(0xffffffffu, info[2], 0);
         if (j1 == 0) break;
         const Item it = *info_it;  // (the next part's may stand there before this one's last product)
+        if (!F8 && nt == 2) wait(q_full + 1, oc[NT - 1] & 1);
         // S of the next block for tiles ta..tb1-1; `release`: they are its last
         auto issue_s = [&](int ta, int tb1, bool release, bool last) {
           Cursor at = ck;
@@ -735,7 +685,16 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
           for (int t = 0; t < NT; ++t)
             if (t >= ta && t < tb1) ++sj[t];
         };
-        issue_s(0, nt, true, j1 - j0 == 1);
+        if (F8) {  // a tile as soon as its queries are turned
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (t >= nt) continue;
+            wait(q_ready + t, oc[t] & 1);
+            issue_s(t, t + 1, t == nt - 1, t == nt - 1 && j1 - j0 == 1);
+          }
+        } else {
+          issue_s(0, nt, true, j1 - j0 == 1);
+        }
         for (int j = j0; j < j1; ++j) {
           const bool more = j + 1 < j1;
           if (NSB == 2 && more) issue_s(0, 1, true, j + 2 == j1);  // runs during this block's softmax
@@ -817,7 +776,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
     const int ir = r / P.G;                     // position in the tile
     float sl2e = P.sl2e;
     f2 scale2 = pack2(sl2e, sl2e);
-    uint32_t worked = 0;  // parts with work so far
+    uint32_t turned = 0;  // parts of this tile so far (e4m3)
     const uint32_t tO = tbase + C::TO + t * D + lane_off;
     constexpr int O0 = D / HALVES;
     bool ok = true;
@@ -846,7 +805,6 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       const Part part = part_of(k, it);
       const bool work = part.j1 > part.j0;
       if (t > 0 && it.rows <= P.PT) {  // nothing for this tile
-        worked += work;
         if (k + 1 < parts) it = item_at<NT>(P, pre, id_of(k + 1));
         continue;
       }
@@ -854,6 +812,61 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       const int pt = it.p0 + t * P.PT, p = pt + ir;            // position of the tile's first row, of this one
       const int plast = it.p0 + imin(it.rows, (t + 1) * P.PT) - 1;
       float m = -INFINITY, l = 0.f;
+      if constexpr (F8) {
+        if (work) {
+          // This row of the queries (this thread's columns of it), scaled by a power of two: largest element
+          // in [2^7, 2^8).  32 elements at a time, in place: their first e4m3 parts, then what those leave.
+          if (ok) ok = spin_wait(&q_full[t], turned++ & 1, P.err);
+          ok = __all_sync(0xffffffffu, ok);
+          constexpr int PC = D / HALVES / 8;
+          uint8_t *row = qs + t * C::QBYTES + r * 128;
+          auto place = [&](int x) {
+            x += hf * PC;
+            return reinterpret_cast<uint4 *>(row + (x >> 3) * ROWS * 128 + (((x & 7) ^ (r & 7)) << 4));
+          };
+          uint4 w[PC];
+          uint32_t mx = 0;  // (of finite values the larger has the larger bits)
+#pragma unroll
+          for (int x = 0; x < PC; ++x) {
+            w[x] = *place(x);
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w[x].x & 0x7fff7fffu, w[x].y & 0x7fff7fffu), __vmaxu2(w[x].z & 0x7fff7fffu, w[x].w & 0x7fff7fffu)));
+          }
+          mx = max(mx & 0xffffu, mx >> 16);
+          if (HALVES == 2) mx = max(mx, __float_as_uint(trade(__uint_as_float(mx))));
+          const int e = (int)(mx >> 7), E = imin(imax(e, 16), 254);
+          float up = __int_as_float((261 - E) << 23);  // 2^(7 - (E - 127))
+          sl2e = P.sl2e * (P.ks ? P.ks[it.h] : 1.f) * __int_as_float((E - 7) << 23);
+          scale2 = pack2(sl2e, sl2e);
+          if (e == 255) up = __int_as_float(0x7fffffff);  // e4m3 has no infinity: the row's scores are NaN
+          const f2 up2 = pack2(up, up), minus = pack2(-1.f, -1.f);
+          auto two = [&](uint32_t y, uint32_t &l) {  // two elements
+            const f2 v = mul2(pack2(bf16lo(y), bf16hi(y)), up2);
+            // to four bits in fp32 (c - (c - v), Veltkamp): what e4m3 rounds to above 2^-6
+            const f2 c = mul2(v, pack2(0x1p20f + 1.f, 0x1p20f + 1.f)), d = fma2(v, minus, c);
+            const f2 h = fma2(d, minus, c);
+            l = f32x2_to_e4m3x2(fma2(h, minus, v));
+            return f32x2_to_e4m3x2(h);
+          };
+          auto four = [&](uint32_t y, uint32_t z, uint32_t &h, uint32_t &l) {
+            uint32_t l0, l1;
+            const uint32_t h0 = two(y, l0), h1 = two(z, l1);
+            h = h0 | h1 << 16, l = l0 | l1 << 16;
+          };
+#pragma unroll
+          for (int x = 0; x < PC; x += 2) {
+            uint4 hi, lo;
+            four(w[x].x, w[x].y, hi.x, lo.x);
+            four(w[x].z, w[x].w, hi.y, lo.y);
+            four(w[x + 1].x, w[x + 1].y, hi.z, lo.z);
+            four(w[x + 1].z, w[x + 1].w, hi.w, lo.w);
+            const int at = (x & ~3) + ((x >> 1) & 1);
+            *place(at) = hi, *place(at + 2) = lo;
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_ready[t]);
+        }
+      }
       // Both halves of a row take part in every trade whatever `ok` says (the
       // barriers have no time limit); after a wait that ran out only the work
       // is skipped.
@@ -863,10 +876,6 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         if (ok) ok = spin_wait(&s_full[sb], (NSB == 2 ? cnt >> 1 : cnt) & 1, P.err);
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after_sync();
-        if (F8 && j == part.j0) {  // the scale of this row's queries (S is there: so are they, and it)
-          sl2e = P.sl2e * (P.ks ? P.ks[it.h] : 1.f) * rowscale[((worked & 1) * NT + t) * ROWS + r];
-          scale2 = pack2(sl2e, sl2e);
-        }
         uint32_t raw[COLS / 32][32];
         // (after a wait that ran out what stands there has no meaning, and nothing is stored;
         // loads under a condition cost registers)
@@ -956,7 +965,6 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[sb]);
       }
-      worked += work;
       const Item now = it;
       // the next item is looked up while the last product runs
       if (k + 1 < parts) it = item_at<NT>(P, pre, id_of(k + 1));
@@ -1150,9 +1158,9 @@ static sv_status run(const sv_rows *q, const sv_paged_kv *cache, Params &P, int 
     return SV_ERR_CUDA;
   const size_t prefix = ((size_t)P.B + 1) * 4;
   P.few_slots = !F8 && prefix <= HEADER - PREFIX ? 0 : 1;
-  const size_t smem = F8 ? C::SCALES + 2 * C::NT * ROWS * 4 : P.few_slots ? C::BEHIND + prefix : C::RING + 160 * 1024;
+  const size_t smem = P.few_slots ? C::BEHIND + imax((int)prefix, HEADER - PREFIX) : C::RING + 160 * 1024;
   static_assert((MAX_KEPT + 1) * 16 <= HEADER - PREFIX, "sequences kept");
-  static_assert(C::RING + 160 * 1024 <= 227 * 1024 && C::SCALES + 2 * C::NT * ROWS * 4 <= 227 * 1024, "shared memory");
+  static_assert(C::RING + 160 * 1024 <= 227 * 1024 && C::BEHIND + (MAX_B + 1) * 4 <= 227 * 1024, "shared memory");
   // at most one tile more per sequence than the rows fill, and no more CTAs than blocks
   P.most = P.Tq / (P.PT * C::NT) + P.B;
   const long long blocks = ((long long)P.width * P.page_size + BN - 1) / BN + 1;
