@@ -222,10 +222,9 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2_hi(uint32_t v) {  // high 16
   return d;
 }
 
-__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(f2 v) {  // to the nearest, in the low 16 bits
-  const float2 x = unpack2(v);
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t v) {  // to the nearest, in the low 16 bits
   uint32_t d;
-  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tmov.b32 %0, {t, 0};\n\t}\n" : "=r"(d) : "f"(x.x), "f"(x.y));
+  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f16x2 t, %1;\n\tmov.b32 %0, {t, 0};\n\t}\n" : "=r"(d) : "r"(v));
   return d;
 }
 
@@ -824,43 +823,47 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
             x += hf * PC;
             return reinterpret_cast<uint4 *>(row + (x >> 3) * ROWS * 128 + (((x & 7) ^ (r & 7)) << 4));
           };
-          uint4 w[PC];
           uint32_t mx = 0;  // (of finite values the larger has the larger bits)
-#pragma unroll
+#pragma unroll 8
           for (int x = 0; x < PC; ++x) {
-            w[x] = *place(x);
-            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w[x].x & 0x7fff7fffu, w[x].y & 0x7fff7fffu), __vmaxu2(w[x].z & 0x7fff7fffu, w[x].w & 0x7fff7fffu)));
+            const uint4 w = *place(x);
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
           }
           mx = max(mx & 0xffffu, mx >> 16);
           if (HALVES == 2) mx = max(mx, __float_as_uint(trade(__uint_as_float(mx))));
           const int e = (int)(mx >> 7), E = imin(imax(e, 16), 254);
-          float up = __int_as_float((261 - E) << 23);  // 2^(7 - (E - 127))
           sl2e = P.sl2e * (P.ks ? P.ks[it.h] : 1.f) * __int_as_float((E - 7) << 23);
           scale2 = pack2(sl2e, sl2e);
+          float up = __int_as_float((261 - E) << 23);  // 2^(7 - (E - 127))
           if (e == 255) up = __int_as_float(0x7fffffff);  // e4m3 has no infinity: the row's scores are NaN
-          const f2 up2 = pack2(up, up), minus = pack2(-1.f, -1.f);
-          auto two = [&](uint32_t y, uint32_t &l) {  // two elements
-            const f2 v = mul2(pack2(bf16lo(y), bf16hi(y)), up2);
-            // to four bits in fp32 (c - (c - v), Veltkamp): what e4m3 rounds to above 2^-6
-            const f2 c = mul2(v, pack2(0x1p20f + 1.f, 0x1p20f + 1.f)), d = fma2(v, minus, c);
-            const f2 h = fma2(d, minus, c);
-            l = f32x2_to_e4m3x2(fma2(h, minus, v));
-            return f32x2_to_e4m3x2(h);
+          const f2 up2 = pack2(up, up);
+          auto two = [&](uint32_t y, uint32_t &l) {  // two elements; what the first part leaves is exact in fp16
+            const float2 z = unpack2(mul2(pack2(bf16lo(y), bf16hi(y)), up2));
+            const uint32_t v = pack_f16x2(z.x, z.y), h = f16x2_to_e4m3x2(v), b = e4m3x2_to_f16x2(h);
+            const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&b));
+            l = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t *>(&d));
+            return h;
           };
           auto four = [&](uint32_t y, uint32_t z, uint32_t &h, uint32_t &l) {
             uint32_t l0, l1;
             const uint32_t h0 = two(y, l0), h1 = two(z, l1);
             h = h0 | h1 << 16, l = l0 | l1 << 16;
           };
+          // (a loop: all of it unrolled, it waits for its instructions)
+#pragma unroll 1
+          for (int x = 0; x < PC; x += 4) {
+            uint4 w[4], hi[2], lo[2];
 #pragma unroll
-          for (int x = 0; x < PC; x += 2) {
-            uint4 hi, lo;
-            four(w[x].x, w[x].y, hi.x, lo.x);
-            four(w[x].z, w[x].w, hi.y, lo.y);
-            four(w[x + 1].x, w[x + 1].y, hi.z, lo.z);
-            four(w[x + 1].z, w[x + 1].w, hi.w, lo.w);
-            const int at = (x & ~3) + ((x >> 1) & 1);
-            *place(at) = hi, *place(at + 2) = lo;
+            for (int y = 0; y < 4; ++y) w[y] = *place(x + y);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              four(w[2 * y].x, w[2 * y].y, hi[y].x, lo[y].x);
+              four(w[2 * y].z, w[2 * y].w, hi[y].y, lo[y].y);
+              four(w[2 * y + 1].x, w[2 * y + 1].y, hi[y].z, lo[y].z);
+              four(w[2 * y + 1].z, w[2 * y + 1].w, hi[y].w, lo[y].w);
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) *place(x + y) = hi[y], *place(x + 2 + y) = lo[y];
           }
           fence_proxy_async();
           __syncwarp();
