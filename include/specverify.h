@@ -415,7 +415,8 @@ SV_API sv_status window_attn(const sv_rows *q, const sv_rows *k, const sv_rows *
  *   and pages out of range, and for slots that no row sees.
  * Arithmetic as paged_attn's: fp32, with the second product's operands in 16 bits
  *   (e4m3 pages: probabilities keep 2^-11 down to 2^-24 of the row's largest, and are
- *   off by 2^-35 of that below).
+ *   off by 2^-35 of that below; a query row's elements are exact down to 2^-9 of its
+ *   largest, and off by 2^-17 of that below).
  * Supported: D in {128, 256}; Hq % Hkv == 0; Hq/Hkv <= 128; 0 <= B <= 4096;
  *   Tq <= 2^30; table_width*page_size <= 2^30; (Tq / (128 / (Hq/Hkv)) + B) * Hkv *
  *   (table_width*page_size/128 + 4) < 2^31, divisions rounded down; strides of q above

@@ -20,13 +20,20 @@
 //    (fp32), maximum and sum in the workspace, and a second kernel joins them.
 //  * Slots that no row of the sequence sees may hold anything: their scores are
 //    masked, and their values are overwritten with zeros before the product.
-//  * e4m3 pages: copies land in the second halves of their slots, and four more warps spread them out
-//    to fp16 tiles there (each value exactly);
-//    queries are scaled by a power of two per row and turned to fp16 in place
-//    (exact down to 2^-14 of a row's largest element, off by 2^-25 of that below), and
-//    probabilities are taken 2^10 times as large, and their sum with them, so that
+//  * e4m3 pages: keys are operands as they land, against queries in two e4m3 parts behind a power of two
+//    per row (what the first part leaves is the second: exact down to 2^-9 of a row's largest element, off
+//    by 2^-17 of that below).  Values meet probabilities, which take more than e4m3 parts: their copies
+//    land in the second halves of their slots, and four more warps spread them out to fp16 tiles there
+//    (each value exactly).  Probabilities are taken 2^10 times as large, and their sum with them, so that
 //    those down to 2^-24 of the maximum keep 2^-11 (smaller ones are off by 2^-35 of it; the
 //    maximum that they refer to is raised when a block exceeds it by more than 2^5).
+//
+// Measured (GB300, whole calls; the products' time at 1893 TFLOP/s): 2048 rows behind 30000
+// positions, 24 heads of 256 over 4, 1.03-1.14 ms (0.83); 13 chunks of 1 to 777 rows behind 5000, 32 heads
+// of 128 over 8, 116-120 us (67); 2 x 4001 rows under a window of 1024 over e4m3 pages 155 us (71; over bf16
+// pages 129); 61 rows behind 16000 over e4m3 pages 38-42 us, of which 9 pass before the first product and 5
+// behind the last.  A block of two tiles takes 2900 clocks, of which 2050 are products: each tile's chain of
+// scores, softmax and second product; an item costs 6000 more, 9000 with queries to turn.
 #include <type_traits>
 
 #include "paged.cuh"
@@ -56,7 +63,7 @@ struct Cfg {
   static constexpr int HALVES = TILES == 2 ? 1 : 2;  // threads that share a row
   // Ring slots: a whole K or V block at D = 128, at D = 256 half of its columns
   // (K) or of its keys (V).
-  static constexpr int SLOT = 32768, RAW = SLOT / 2;  // (e4m3: where a copy lands)
+  static constexpr int SLOT = 32768, RAW = SLOT / 2;  // (e4m3: where a copy of values lands)
   static constexpr int PARTS = BN * D * 2 / SLOT;  // slots of a K block (of a V block)
   // e4m3 keys are operands as they land: a slot a block
   static constexpr int KSLOT = F8 ? BN * D : SLOT, KPARTS = F8 ? 1 : PARTS;
@@ -65,7 +72,7 @@ struct Cfg {
   static constexpr int THREADS = (SOFT + (F8 ? 8 : 4)) * 32;
   static constexpr int QBYTES = ROWS * D * 2;
   static constexpr int RING = HEADER + NT * QBYTES;
-  // slots of the K and the V ring: 160 KB, or 128 beside long prefix sums and e4m3's scales
+  // slots of the K and the V ring: 160 KB, or 128 beside long prefix sums and with e4m3 pages
   // (At D = 256 a block takes two slots of each, and the next block's keys are needed first.)
   static constexpr int NK = F8 ? 2 : D == 256 ? 3 : 2, NV = F8 ? (D == 256 ? 2 : 3) : 5 - NK;
   static constexpr int LESS_K = 2, LESS_V = F8 ? NV : 2;
