@@ -23,6 +23,10 @@ live on the current device:
     sv.paged_kv_append(k, v, cache, slots, q=q, q_out=q_rot,         # new tokens
                        positions=positions, phases=phases)
     sv.paged_attn(q_rot, cache, block_table, lens, o, M, scale, workspace=ws)
+    sv.paged_chunk_attn(q, cache, block_table, lens, o, cu_rows, scale,     # prompts in chunks
+                        workspace=ws)
+    sv.gdn_chunk(states, places, q, k, v, g, beta, o, cu_rows, workspace=ws)   # recurrent layers
+    sv.gdn_step(states, places, q, k, v, g, beta, o, M, tape=last_round, n_replay=accepted)
 """
 from __future__ import annotations
 

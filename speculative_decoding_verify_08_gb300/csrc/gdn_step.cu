@@ -144,16 +144,17 @@ __global__ void __launch_bounds__(256, DK <= 128 ? 6 : 4) tokens_kernel(const __
 
 // ---- many states: a stream of tiles through shared memory ----
 constexpr int TOKENS = 16;  // tokens of a sequence (tape and own) at most
+// Shared memory a block: two share an SM's 228 KB, of which a block takes 1 KB itself.
+constexpr int STREAM_BYTES = 115200;
 constexpr int WORK_WARPS = 8, STREAM_THREADS = (WORK_WARPS + 2) * 32;
 
-template <int DK>
+// RP: rows of a thread.
+template <int DK, int RP>
 struct SL {
-  // Rows of a thread: two of 64 columns, so that a tile is 16 KB as it is at 128 (one token of 61
-  // sequences of 48 heads of 64: 52 us with one; at 128 64 with two, 60 with one).
-  static constexpr int RP = DK == 64 ? 2 : 1, TILE = RP * WORK_WARPS * 32 / LPR;
+  static constexpr int TILE = RP * WORK_WARPS * 32 / LPR;
   static constexpr int STATE = TILE * DK * 4;
   // of a stage: the rows of S, the tokens' gates (a, b), what the tile is, the tokens
-  static constexpr int GATES = STATE, META = GATES + TOKENS * 8, TOKEN = META + 16;
+  static constexpr int GATES = STATE, META = GATES + TOKENS * 8, TOKEN = META + 32;
   static constexpr int EACH = 4 * DK + 2 * TILE;  // bytes of a token: key, query, values
   __host__ __device__ static int stage(int tokens) { return (TOKEN + tokens * EACH + 127) / 128 * 128; }
 };
@@ -167,16 +168,15 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                : "memory");
 }
 
-// The same rule on the same lanes.  What differs: a block walks over tiles (sequence, head, 64
-// or 32 rows), one warp asking for the next ones' states, keys, queries and values by bulk copies, one
+// The same rule on the same lanes.  What differs: a block walks over tiles (sequence, head, 32 or
+// 64 rows), one warp asking for the next ones' states, keys, queries and values by bulk copies, one
 // writing the states back; as many bytes are on their way as the ring holds, whatever the
-// tiles' own latency (one token of 61 sequences of 48 heads of 128 x
-// 128: 80 us with a block a tile, 60 this way, 6.4 TB/s; of 24 sequences of 4 rows behind 2 replayed on
-// average: 47, the rows' instructions).
-template <int DK>
+// tiles' own latency (48 heads of 128 x 128: one token of 61 sequences 80 us with a block a tile, 60 this
+// way, 6.4 TB/s; 24 sequences of 4 rows behind 2 replayed on average 36.5, the rows' instructions).
+template <int DK, int RP>
 __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_constant__ PoolParams P, int stages, int tiles, int row_tiles) {
-  using Y = SL<DK>;
-  constexpr int NJ = DK / 32, RP = Y::RP, TILE = Y::TILE;
+  using Y = SL<DK, RP>;
+  constexpr int NJ = DK / 32, TILE = Y::TILE;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[16], done[16], empty[16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -237,7 +237,10 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_
         a.replay = imin(imax(a.replay, 0), tape);
       }
       if (lane < tokens) *reinterpret_cast<float2 *>(at + Y::GATES + lane * 8) = make_float2(expf(a.g), a.b);
-      if (lane == 0) *reinterpret_cast<int2 *>(at + Y::META) = make_int2(a.slot, a.replay);
+      if (lane == 0) {
+        *reinterpret_cast<int4 *>(at + Y::META) = make_int4(a.slot, a.replay, a.w.b, a.w.h);
+        *reinterpret_cast<int *>(at + Y::META + 16) = a.w.i0;
+      }
       __syncwarp();
       const int rows = imin(TILE, P.dv - a.w.i0);
       const uint32_t state = a.slot >= 0 ? rows * DK * 4 : 0, values = rows * 2;
@@ -266,11 +269,10 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_
         const int st = k % stages;
         if (!mbar_wait(&done[st], (k / stages) & 1, P.err)) break;
         uint8_t *at = ring + st * size;
-        const int2 meta = *reinterpret_cast<const int2 *>(at + Y::META);
-        if (meta.x >= 0 && (meta.y > 0 || (P.commit && P.M > 0))) {
-          const Where w = where(k);
-          bulk_store(P.states.ptr + meta.x * P.states.slot_stride + ((long long)w.h * P.dv + w.i0) * DK, at, imin(TILE, P.dv - w.i0) * DK * 4);
-        }
+        const int4 meta = *reinterpret_cast<const int4 *>(at + Y::META);
+        const int i0 = *reinterpret_cast<const int *>(at + Y::META + 16);
+        if (meta.x >= 0 && (meta.y > 0 || (P.commit && P.M > 0)))
+          bulk_store(P.states.ptr + meta.x * P.states.slot_stride + ((long long)meta.w * P.dv + i0) * DK, at, imin(TILE, P.dv - i0) * DK * 4);
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         // the tile before this one has been read out
         asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
@@ -289,8 +291,8 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       uint8_t *at = ring + st * size;
-      const Where w = where(k);
-      const int2 meta = *reinterpret_cast<const int2 *>(at + Y::META);
+      const int4 meta = *reinterpret_cast<const int4 *>(at + Y::META);
+      const Where w{meta.z, meta.w, *reinterpret_cast<const int *>(at + Y::META + 16)};
       float *srow = reinterpret_cast<float *>(at) + r * DK + sub * 4;  // (rows of a thread: 32 apart)
       f2 row[RP][2 * NJ];
 #pragma unroll
@@ -375,6 +377,15 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_
   }
 }
 
+template <int DK, int RP>
+sv_status run_stream(const PoolParams &P, int sms, cudaStream_t s) {
+  using Y = SL<DK, RP>;
+  const int row_tiles = (P.dv + Y::TILE - 1) / Y::TILE;
+  const int size = Y::stage(P.tape_M + P.M), stages = imin(16, STREAM_BYTES / size);
+  return from_cuda(launch_early(stream_kernel<DK, RP>, dim3(2 * sms), dim3(STREAM_THREADS), (size_t)stages * size, s, P, stages,
+                                (int)((long long)P.B * P.Hv * row_tiles), row_tiles));
+}
+
 template <int DK>
 sv_status run_tokens(PoolParams &P, cudaStream_t s) {
   const long long small = (long long)P.B * P.Hv * ((P.dv + 7) / 8);
@@ -382,11 +393,14 @@ sv_status run_tokens(PoolParams &P, cudaStream_t s) {
   if (sms <= 0) return SV_ERR_CUDA;
   // Few tokens of many states are streamed (values in whole 16 bytes); it pays from some
   // tiles a block on.
-  const int row_tiles = (P.dv + SL<DK>::TILE - 1) / SL<DK>::TILE;
-  const long long tiles = (long long)P.B * P.Hv * row_tiles;
+  // Two rows a thread share what it reads of keys and queries: at 64 columns always (tiles of 16 KB), at 128
+  // from two tokens on (32 KB; 24 sequences of 48 heads, 4 + 4 tokens 36.5 us against 48, 4 tokens 29 against
+  // 43, but one token of 61 sequences 64 against 60).
+  constexpr int ONE = DK == 64 ? 2 : 1;
+  const long long tiles = (long long)P.B * P.Hv * ((P.dv + SL<DK, ONE>::TILE - 1) / SL<DK, ONE>::TILE);
   if (!P.cu && P.tape_M + P.M <= TOKENS && P.dv % 8 == 0 && tiles >= 4LL * sms && tiles <= 0x7fffffffLL) {
-    const int size = SL<DK>::stage(P.tape_M + P.M), stages = imin(16, 110 * 1024 / size);
-    return from_cuda(launch_early(stream_kernel<DK>, dim3(2 * sms), dim3(STREAM_THREADS), (size_t)stages * size, s, P, stages, (int)tiles, row_tiles));
+    if (DK == 128 && P.tape_M + P.M >= 2) return run_stream<DK, DK == 128 ? 2 : ONE>(P, sms, s);
+    return run_stream<DK, ONE>(P, sms, s);
   }
   // Otherwise a block a few rows: eight while that leaves each SM few of them (one sequence of
   // 48 heads: 768), 32 beyond, where what a block stages is shared by more rows.
