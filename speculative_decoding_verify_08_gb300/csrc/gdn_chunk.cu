@@ -21,7 +21,7 @@
 //    next product's first operand.  Two threads share a row; S stays in their
 //    registers, in fp32.  Four warps write the output meanwhile, one issues the
 //    products, one the copies (up to three blocks ahead).
-//    A block takes it 2.5 us, 0.7 of them products; the rest is their results' way through
+//    A block takes it 2.3 us, 0.7 of them products; the rest is their results' way through
 //    registers, four times a block.
 //  * both_kernel is the chains with the preparation of later blocks on the SMs that they leave.
 //  * Products take fp16 operands and fp32 sums.  S, R, U and T are fp32 values held
@@ -472,7 +472,9 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
 // fetches, one issues the products.
 constexpr int ROW_WARPS = 8, OUT_WARPS = 4, FETCH = ROW_WARPS + OUT_WARPS, ISSUE = FETCH + 1;
 constexpr int CHAIN_THREADS = (ROW_WARPS + OUT_WARPS + 4) * 32, STAGES = 3;
-constexpr int FIRST = 8;  // blocks of a sequence that are prepared before the chains, where later ones are beside them
+// Blocks of a sequence that are prepared before the chains where later ones are beside them, and how
+// many of those a value head at a time (sooner there; 8192 tokens 356 us with none, 342 with 16 or more).
+constexpr int FIRST = 8, SOON = 16;
 
 template <int DK>
 struct CL {
@@ -541,7 +543,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
   uint64_t *full = reinterpret_cast<uint64_t *>(smem);     // [STAGES]
   uint64_t *empty = full + STAGES;                         // [STAGES]
   uint64_t *s_ready = empty + STAGES;                      // [2] first and second half of each thread's k-steps of S
-  uint64_t *x_done = s_ready + 2, *r_ready = x_done + 1, *u_done = r_ready + 1, *ut_ready = u_done + 1;
+  uint64_t *x_done = s_ready + 2, *r_ready = x_done + 1, *u_done = r_ready + 2, *ut_ready = u_done + 1;  // (r_ready [2], as s_ready)
   uint64_t *d_done = ut_ready + 1, *o_done = d_done + 1, *o_free = o_done + 1, *idle = o_free + 1;
   uint64_t *s_here = idle + 1, *s_read = s_here + 1;       // the state in the last stage, and read
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_read + 1);
@@ -554,7 +556,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
       mbar_init(&full[i], 1 + (i == 0 ? CP.stall : 0));
       mbar_init(&empty[i], ROW_WARPS + OUT_WARPS + 1);
     }
-    for (uint64_t *b : {s_ready, s_ready + 1, r_ready, ut_ready, s_read}) mbar_init(b, ROW_WARPS);
+    for (uint64_t *b : {s_ready, s_ready + 1, r_ready, r_ready + 1, ut_ready, s_read}) mbar_init(b, ROW_WARPS);
     mbar_init(o_free, OUT_WARPS);
     for (uint64_t *b : {x_done, u_done, d_done, o_done, idle, s_here}) mbar_init(b, 1);
     fence_barrier_init();
@@ -669,19 +671,22 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
           }
           __syncwarp();
         }
-        // U = R T^T
-        wait(r_ready, par);
-        tc::fence_after_sync();
-        if (leader && ok) {
+        // U = R T^T, the first 16 tokens of each thread, then the rest
 #pragma unroll
-          for (int ks = 0; ks < C / 16; ++ks)
+        for (int x = 0; x < 2; ++x) {
+          wait(&r_ready[x], par);
+          tc::fence_after_sync();
+          if (leader && ok) {
 #pragma unroll
-            for (int p = 0; p < 3; ++p)  // hi hi, lo hi, hi lo
-              tc::mma_bf16_ts(tb + Y::U, tb + Y::X + ks * 16 + (p == 1 ? 8 : 0), lo + (Y::T + (p == 2 ? PART : 0) + ks * 32) / 16, row_hi, IDN,
-                              ks > 0 || p > 0);
-          tc::commit(u_done);
+            for (int ks = x; ks < C / 16; ks += 2)
+#pragma unroll
+              for (int p = 0; p < 3; ++p)  // hi hi, lo hi, hi lo
+                tc::mma_bf16_ts(tb + Y::U, tb + Y::X + ks * 16 + (p == 1 ? 8 : 0), lo + (Y::T + (p == 2 ? PART : 0) + ks * 32) / 16, row_hi, IDN,
+                                x > 0 || ks > 0 || p > 0);
+            if (x == 1) tc::commit(u_done);
+          }
+          __syncwarp();
         }
-        __syncwarp();
         // S Q^T
         if (c > 0) wait(o_free, par ^ 1);
         tc::fence_after_sync();
@@ -883,10 +888,10 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
           }
           tc::st8(tb + Y::X + hf * 32 + 16 * g + lane_off, hi);
           tc::st8(tb + Y::X + hf * 32 + 16 * g + 8 + lane_off, lo);
+          tc::wait_st();
+          tc::fence_before_sync();
+          arrive(&r_ready[g]);
         }
-        tc::wait_st();
-        tc::fence_before_sync();
-        arrive(r_ready);
       }
       __half2 um = __float2half2_rn(0.f);
       {
@@ -1019,21 +1024,28 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
   int most = 0;  // blocks of the longest sequence
   for (int b = threadIdx.x & 31; b < P.B; b += 32) most = imax(most, (rows_of(P, b, false).y + C - 1) / C);
   most = __reduce_max_sync(0xffffffffu, most);
-  const long long tasks = (long long)imax(0, most - CP.first) * P.B * P.Hv;
+  // the next blocks a value head at a time, those behind them a key head
+  const int later = imax(0, most - CP.first), soon = imin(later, SOON);
+  const long long single = (long long)soon * P.B * P.Hv, tasks = single + (long long)(later - soon) * P.B * P.Hk;
   uint32_t parity = 0;
   for (long long x = blockIdx.x + (long long)g * CP.makers; x < tasks; x += (long long)MAKER_GROUPS * CP.makers) {
-    const long long y = x / P.Hv;
-    const int h = (int)(x - y * P.Hv), later = (int)(y / P.B), b = (int)(y - (long long)later * P.B), c = later + CP.first;
+    const bool one = x < single;
+    const long long z = one ? x : x - single;
+    const int heads = one ? P.Hv : P.Hk;
+    const long long y = z / heads;
+    const int head = (int)(z - y * heads), n = (int)(y / P.B), b = (int)(y - (long long)n * P.B);
+    const int c = CP.first + (one ? n : soon + n), hk = one ? head / group : head;
+    const int e0 = one ? head - hk * group : 0, e1 = one ? e0 + 1 : group;
     const int2 rows = rows_of(P, b, false);
     if (c * C >= rows.y) continue;
     const int w = first_block(P, b, rows.x) + c;
-    prepare<DK>(CP, own, tb + 64 * g, done, parity, 1 + g, pt, h / group, h % group, h % group + 1, w, rows.x + (long long)c * C, imin(C, rows.y - c * C));
+    prepare<DK>(CP, own, tb + 64 * g, done, parity, 1 + g, pt, hk, e0, e1, w, rows.x + (long long)c * C, imin(C, rows.y - c * C));
     parity ^= 1;
     __threadfence();
     fence_proxy_async();
     named_barrier(1 + g, 128);
-    if (pt == 0)
-      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&CP.made[(size_t)w * P.Hv + h]), "r"(1u) : "memory");
+    for (int e = e0 + pt; e < e1; e += 128)
+      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&CP.made[(size_t)w * P.Hv + hk * group + e]), "r"(1u) : "memory");
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -1074,7 +1086,7 @@ sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
   const int sms = device_sm_count();
   if (sms <= 0) return SV_ERR_CUDA;
   // Few items: all but the first blocks are prepared while the chains run (one sequence of 8192
-  // tokens, 48 heads of 128 x 128: 338 us against 401; 2000 tokens 101 against 111; 1000 not faster).
+  // tokens, 48 heads of 128 x 128: 325 us against 390; 2000 tokens 99 against 107; 1000 not faster).
   CP.first = items <= sms / 2 && P.T > 2LL * FIRST * C * P.B ? FIRST : 0;
   const long long before = CP.first ? (long long)P.B * FIRST : blocks;
   // A value head a CTA while all of them are on the SMs at once, its key head's products made anew for
@@ -1085,8 +1097,10 @@ sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
   if (e != cudaSuccess) return SV_ERR_CUDA;
   const size_t smem = CL<DK>::BYTES;
   if (!CP.first) return from_cuda(launch_early(chain_kernel<DK>, dim3((unsigned)items), dim3(CHAIN_THREADS), smem, s, mv, ms, CP));
-  CP.makers = sms - (int)items;
-  return from_cuda(launch_early(both_kernel<DK>, dim3(sms), dim3(CHAIN_THREADS), smem, s, mv, ms, CP));
+  // Three to two chains keep up with them, and more slow the chains down: 8192 tokens, 48 chains, 327 us
+  // with 70, 331 with 88, 342 with 104, 339 with 52.  Beside few chains as many as leave each SM pair one CTA.
+  CP.makers = imin(sms - (int)items, imax(3 * (int)items / 2, sms / 2 - (int)items));
+  return from_cuda(launch_early(both_kernel<DK>, dim3((unsigned)(CP.makers + items)), dim3(CHAIN_THREADS), smem, s, mv, ms, CP));
 }
 
 }  // namespace
