@@ -52,7 +52,7 @@ constexpr int HEAD_COST = 2;        // blocks' time that an item takes beside it
 // Shared memory: barriers, the CTA's cuts (256), more barriers (280), the item
 // (400), halves' exchange (512), prefix sums (2560; after the ring if longer), then the query
 // tiles and the ring.
-constexpr int HEADER = 3072, PREFIX = 2560, CUTS = 256, INFO = 400;
+constexpr int HEADER = 3 * 1024, PREFIX = 2560, CUTS = 256, INFO = 400;
 
 // Two tiles a CTA (D = 128), or one with two S buffers and two threads a row.
 template <int D, int TILES, bool F8>
