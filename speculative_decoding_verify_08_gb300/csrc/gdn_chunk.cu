@@ -24,6 +24,8 @@
 //    A block takes it 2.3 us, 0.7 of them products; the rest is their results' way through
 //    registers, four times a block.
 //  * both_kernel is the chains with the preparation of later blocks on the SMs that they leave.
+//    Measured (48 heads of 128 x 128 over 16): one sequence of 8192 tokens 325 us, of 77 17; eleven of 1 to
+//    3001 tokens 196, of which preparation takes 75.
 //  * Products take fp16 operands and fp32 sums.  S, R, U and T are fp32 values held
 //    as two fp16 parts (x = hi + lo, 2^-22 of x), so that a state stays an fp32 one; what
 //    only an output sees (S and U there, and P) is one part, 2^-11 beside the

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_
           y[2 * j] = pack2(bf16lo(z.x), bf16hi(z.x)), y[2 * j + 1] = pack2(bf16lo(z.y), bf16hi(z.y));
         }
       };
-      auto dots = [&](const f2 (&x)[2 * NJ], float (&out)[RP]) {
+      auto parts = [&](const f2 (&x)[2 * NJ], float (&out)[RP]) {
 #pragma unroll
         for (int p = 0; p < RP; ++p) {
           f2 s[2] = {0, 0};
@@ -327,6 +327,9 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_
           const float2 z = unpack2(add2(s[0], s[1]));
           out[p] = z.x + z.y;
         }
+      };
+      auto dots = [&](const f2 (&x)[2 * NJ], float (&out)[RP]) {
+        parts(x, out);
 #pragma unroll
         for (int off = LPR / 2; off > 0; off >>= 1)
 #pragma unroll
@@ -342,7 +345,8 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_
         const f2 a2 = pack2(ab.x, ab.x);
 #pragma unroll
         for (int p = 0; p < RP; ++p) {
-          const float v = w.i0 + r + 32 * p < P.dv ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(x + DK * 4)[r + 32 * p]) : 0.f;
+          // (rows past the head's last are not stored, whatever stands there)
+          const float v = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(x + DK * 4)[r + 32 * p]);
           const float u = ab.y * (v - ab.x * d[p]);
           const f2 u2 = pack2(u, u);
 #pragma unroll
@@ -352,22 +356,30 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_
 #pragma unroll 1
       for (int n = 0; n < meta.y; ++n) token(n);
       if (!P.commit && meta.y > 0) keep();
+      // the row that this lane writes outputs of: of two, the second half of the lanes' second
+      const int mine = w.i0 + r + (RP == 2 ? sub / (LPR / 2) * 32 : 0);
+      const bool writes = sub % (LPR / RP) == 0 && mine < P.dv;
+      long long o = (long long)w.b * P.M * P.o.token_stride + w.h * P.o.head_stride + mine;
 #pragma unroll 1
-      for (int n = 0; n < P.M; ++n) {
+      for (int n = 0; n < P.M; ++n, o += P.o.token_stride) {
         token(tape + n);
         f2 query[2 * NJ];
         float d[RP];
         pieces(at + Y::TOKEN + (tape + n) * Y::EACH + DK * 2, query);
-        dots(query, d);
-        const long long o = ((long long)w.b * P.M + n) * P.o.token_stride + w.h * P.o.head_stride + w.i0 + r;
+        parts(query, d);
+        float x = d[0];
+        if (RP == 2) {  // each half of the lanes goes on with one row
+          const bool second = sub >= LPR / 2;
+          x = (second ? d[RP - 1] : d[0]) + __shfl_xor_sync(0xffffffffu, second ? d[0] : d[RP - 1], LPR / 2);
+        }
 #pragma unroll
-        for (int p = 0; p < RP; ++p)
-          if (sub == p && w.i0 + r + 32 * p < P.dv) {
-            if (P.o_f32)
-              static_cast<float *>(P.o.ptr)[o + 32 * p] = d[p];
-            else
-              static_cast<__nv_bfloat16 *>(P.o.ptr)[o + 32 * p] = __float2bfloat16_rn(d[p]);
-          }
+        for (int off = LPR / 2 / RP; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        if (writes) {
+          if (P.o_f32)
+            static_cast<float *>(P.o.ptr)[o] = x;
+          else
+            static_cast<__nv_bfloat16 *>(P.o.ptr)[o] = __float2bfloat16_rn(x);
+        }
       }
       if (P.commit) keep();
       fence_proxy_async();
