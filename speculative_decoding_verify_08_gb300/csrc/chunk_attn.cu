@@ -34,8 +34,6 @@
 // pages 129); 61 rows behind 16000 over e4m3 pages 38-42 us, of which 9 pass before the first product and 5
 // behind the last.  A block of two tiles takes 2900 clocks, of which 2050 are products: each tile's chain of
 // scores, softmax and second product; an item costs 6000 more, 9000 with queries to turn.
-#include <type_traits>
-
 #include "paged.cuh"
 #include "tcgen05.cuh"
 
