@@ -644,15 +644,16 @@ def paged_chunk_attn(q, cache: PagedKV, block_table, kv_lens, o, cu_q, scale: fl
 
 # ----------------------------------------------- recurrent layers over a pool ----
 def _states(t, dev, where):
-    """sv_states of an fp32 tensor [slots, Hv, dv, dk] of the call's device (any slot stride, the rest contiguous)."""
+    """sv_states of an fp32 tensor [slots, Hv, dv, dk] of the call's device (any
+    slot stride, the rest contiguous), and its Hv, dv and dk."""
     if t.dtype is not torch.float32 or t.dim() != 4 or not t.is_cuda or (dev is not None and t.get_device() != dev):
         _bad(where)
     n, Hv, dv, dk = t.shape
-    s0, *rest = t.stride()
+    s0, s1, s2, s3 = t.stride()
     # a dimension of one may carry any stride
-    if any(m > 1 and s != want for m, s, want in zip((Hv, dv, dk), rest, (dv * dk, dk, 1))):
+    if (s3 != 1 and dk > 1) or (s2 != dk and dv > 1) or (s1 != dv * dk and Hv > 1):
         _bad(where)
-    return _STATES.pack(t.data_ptr(), s0 if n > 1 else Hv * dv * dk, n)
+    return _STATES.pack(t.data_ptr(), s0 if n > 1 else Hv * dv * dk, n), Hv, dv, dk
 
 
 def _out_rows(t, tokens, heads, D, dev, where):
@@ -678,7 +679,7 @@ def gdn_step(states, slots, q, k, v, g, beta, o, M: int, tape=None, n_replay=Non
     w = "gdn_step"
     dev = None if _gpus == 1 else _device(states, w)
     B = slots.numel()
-    n, Hv, dv, dk = states.shape if states.dim() == 4 else _bad(w)
+    pool, Hv, dv, dk = _states(states, dev, w)
     if (tape is None) != (n_replay is None):
         _bad(w)
     Hk = (tape[0] if M == 0 and tape is not None else k).shape[1] if M or tape is not None else 1
@@ -697,7 +698,7 @@ def gdn_step(states, slots, q, k, v, g, beta, o, M: int, tape=None, n_replay=Non
         out, odt = _out_rows(o, rows, Hv, dv, dev, w)
         own = [_rows(q, rows, Hk, dk, dev, w), _rows(k, rows, Hk, dk, dev, w), _rows(v, rows, Hv, dv, dev, w),
                _gates(g, rows, Hv, dev, w), _gates(beta, rows, Hv, dev, w), out]
-    status = load().gdn_step(_states(states, dev, w), _vector(slots, torch.int32, B, dev, w), *t,
+    status = load().gdn_step(pool, _vector(slots, torch.int32, B, dev, w), *t,
                              None if n_replay is None else _vector(n_replay, torch.int32, B, dev, w), tape_M, *own,
                              odt, B, M, 1 if commit else 0, Hk, Hv, dk, dv, _launch_stream(dev, stream))
     if status:
@@ -706,9 +707,10 @@ def gdn_step(states, slots, q, k, v, g, beta, o, M: int, tape=None, n_replay=Non
 
 def _gates(t, rows, Hv, dev, where):
     """Address of gates fp32 [rows, Hv], contiguous."""
-    if t.shape != (rows, Hv):
+    if t.dtype is not torch.float32 or t.shape != (rows, Hv) or not t.is_cuda or not t.is_contiguous() or (
+            dev is not None and t.get_device() != dev):
         _bad(where)
-    return _vector(t, torch.float32, rows * Hv, dev, where)
+    return t.data_ptr()
 
 
 def gdn_chunk_workspace_bytes(B: int, T: int, Hk: int, Hv: int, dk: int, dv: int) -> int:
@@ -724,12 +726,12 @@ def gdn_chunk(states, slots, q, k, v, g, beta, o, cu, workspace=None, stream=Non
     w = "gdn_chunk"
     T, Hk, dk = q.shape
     dev = None if _gpus == 1 else _device(q, w)
-    n, Hv, dv, dk_ = states.shape if states.dim() == 4 else _bad(w)
+    pool, Hv, dv, dk_ = _states(states, dev, w)
     B = slots.numel()
     if dk_ != dk or (workspace is not None and (not workspace.is_cuda or (
             dev is not None and workspace.get_device() != dev))):
         _bad(w)
-    status = load().gdn_chunk(_states(states, dev, w), _vector(slots, torch.int32, B, dev, w),
+    status = load().gdn_chunk(pool, _vector(slots, torch.int32, B, dev, w),
                               _rows(q, T, Hk, dk, dev, w), _rows(k, T, Hk, dk, dev, w), _rows(v, T, Hv, dv, dev, w),
                               _gates(g, T, Hv, dev, w), _gates(beta, T, Hv, dev, w), _rows(o, T, Hv, dv, dev, w),
                               _vector(cu, torch.int32, B + 1, dev, w), B, T, Hk, Hv, dk, dv, _ptr(workspace),
