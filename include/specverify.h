@@ -641,7 +641,7 @@ SV_API sv_status gdn_step(const sv_states *states, const int32_t *slots, const s
  * Arithmetic: blocks of 64 tokens, fp32 sums of products whose operands are fp32 values held as
  *   two fp16 parts (off by 2^-22 of themselves, or by 2^-40 of a bound of their row); what only o
  *   sees, the state and the updates in its products, is one part (2^-11).  Elements of a key or
- *   query are exact down to 2^-13 of its largest and off by 2^-21 of that below.  A call of T <= 20 or
+ *   query are exact down to 2^-13 of its largest and off by 2^-21 of that below.  A call of T <= 16 or
  *   T <= 8*B runs token by token, as gdn_step does.
  * Offsets that fall, so that sequences name the same rows: o of those rows, and the states of all
  *   sequences of the call, are undefined.

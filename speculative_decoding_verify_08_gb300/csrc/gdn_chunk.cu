@@ -24,7 +24,7 @@
 //    A block takes it 2.3 us, 0.7 of them products; the rest is their results' way through
 //    registers, four times a block.
 //  * both_kernel is the chains with the preparation of later blocks on the SMs that they leave.
-//    Measured (48 heads of 128 x 128 over 16): one sequence of 8192 tokens 325 us, of 77 17; eleven of 1 to
+//    Measured (48 heads of 128 x 128 over 16): one sequence of 8192 tokens 325 us, of 77 16; eleven of 1 to
 //    3001 tokens 196, of which preparation takes 75.
 //  * Products take fp16 operands and fp32 sums.  S, R, U and T are fp32 values held
 //    as two fp16 parts (x = hi + lo, 2^-22 of x), so that a state stays an fp32 one; what
@@ -76,6 +76,7 @@ struct ChunkParams {
   PoolParams p;
   uint8_t *keys, *heads;  // [blocks][Hk][2][key_bytes], [blocks][Hv][HEAD_BYTES]
   int split;              // prepare_kernel: a CTA a value head, not a key head
+  int early;              // the chains may start beside it
   int first;              // only a sequence's first blocks are prepared before the chains start (0: all)
   unsigned *made;         // [blocks][Hv]: a later block prepared, beside the chains
   int makers;             // CTAs that do
@@ -460,6 +461,9 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tb = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  // The chains may start: what ran before this kernel is over, and every block of it that is still to
+  // finish has its place and its tensor memory.
+  if (CP.early) pdl_launch_dependents();
   prepare<DK>(CP, smem, tb, done, 0, 0, pt, hk, e0, e1, w, own.x + (long long)c * C, imin(C, own.y - c * C));
   tc::fence_before_sync();
   __syncthreads();
@@ -568,7 +572,8 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
     tc::tmem_alloc(tmem_slot, 512u);
     tc::tmem_relinquish();
   }
-  pdl_wait();
+  // (what the sequences are and their states: from before the kernel that prepares, which has waited
+  // for it before it let this one start)
   // ---- the item: longest sequences first ----
   const int per = P.Hv * CP.row_blocks;
   int b = id / per;
@@ -621,6 +626,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
           mbar_arrive_expect_tx(s_here, ROWS * DK * 4);
           state_load(ring + (STAGES - 1) * Y::STAGE, &mapS, i0, h, slot, s_here);
         }
+        pdl_wait();  // for what has been prepared
         for (; c < n && ok; ++c) {
           const int st = c % STAGES;
           if (c >= STAGES) ok = mbar_wait(&empty[st], (c / STAGES - 1) & 1, P.err);
@@ -1095,6 +1101,9 @@ sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
   // each (77 tokens: 18 us against 24; but eleven prompts of 1 to 3001 tokens 225 us against 199).
   CP.split = before * P.Hv <= 6LL * sms;
   const long long grid = before * (CP.split ? P.Hv : P.Hk);
+  // Chains that find SMs of their own fetch their states meanwhile (77 tokens 16.1 us against 17.6); others would
+  // only take places early (eleven prompts 212 us against 196, 8192 tokens 342 against 325).
+  CP.early = !CP.first && grid + items <= sms;
   cudaError_t e = launch_early(prepare_kernel<DK>, dim3((unsigned)grid), dim3(128), (size_t)PL<DK>::BYTES, s, CP);
   if (e != cudaSuccess) return SV_ERR_CUDA;
   const size_t smem = CL<DK>::BYTES;
@@ -1155,10 +1164,10 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   CP.stall = launch_flags() & SV_LAUNCH_TEST_STALL_COPY ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // A block costs as much with one token as with 64; token by token is faster up to some eight tokens a
-  // sequence (48 heads of 128 x 128: one sequence of 16 tokens 13 us against 15.5, of 24 17.6 against 15.1;
+  // sequence (48 heads of 128 x 128: one sequence of 16 tokens 13 us against 14, of 24 17.6 against 14;
   // two of 8 12 against 16, of 12 20 against 16; eight of 8 25 against 34, of 12 34 both; 64 of 8 169
   // against 218, of 12 231 against 219; a long sequence among short ones takes 0.55 us a token).
-  if (T <= 20 || T <= 8LL * B) return gdn::launch_tokens(P, dk, s);
+  if (T <= 16 || T <= 8LL * B) return gdn::launch_tokens(P, dk, s);
   return dk == 64 ? gdn::run_chunks<64>(CP, s) : gdn::run_chunks<128>(CP, s);
 }
 
