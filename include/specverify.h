@@ -643,13 +643,13 @@ SV_API sv_status gdn_step(const sv_states *states, const int32_t *slots, const s
  *   sees, the state and the updates in its products, is one part (2^-11).  Elements of a key or
  *   query are exact down to 2^-13 of its largest and off by 2^-21 of that below.  A call of T <= 16 or
  *   T <= 8*B runs token by token, as gdn_step does.
- * Offsets that fall, so that sequences name the same rows: o of those rows, and the states of all
- *   sequences of the call, are undefined.
+ * Offsets that fall, so that sequences name the same rows: o of those rows is undefined.  Where they
+ *   name rows so often that they hold more blocks of 64 than T and B of them can, all are left out.
  * Supported: dk in {64, 128}; Hv % Hk == 0, Hv <= 65535; dv <= 65536; 0 <= B <= 65535;
  *   T <= 2^30; slot_stride <= 2^37; B*Hv*((dv+127)/128) and (T/64 + B)*Hv < 2^31, divisions
  *   rounded down; strides of v above 0.
  * workspace: device, 16-byte aligned, of the query's size; nothing in it has to be zero.
- * Two launches (one token by token); offsets and slots are read on the device, so a captured call
+ * Two launches (one token by token; three from 129 sequences on); offsets and slots are read on the device, so a captured call
  * follows their contents. */
 SV_API size_t gdn_chunk_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv);
 SV_API sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows *q,

@@ -55,7 +55,7 @@ namespace {
 constexpr int C = 64;        // tokens of a block
 constexpr int ROWS = 128;    // rows of the state a CTA holds (TMEM lanes)
 constexpr int AS = 68;       // row stride of the inverse's fp32 matrix
-constexpr int MAX_SORTED = 128;
+constexpr int MAX_KEPT = 128;  // sequences whose lengths and places a CTA looks at itself
 constexpr float G_LEAST = -10000.f;  // e^g is 0 long before
 constexpr float P_GAIN = 1024.f;     // P is taken so much larger: decays down to 2^-24 keep their bits
 
@@ -79,6 +79,7 @@ struct ChunkParams {
   int early;              // the chains may start beside it
   int first;              // only a sequence's first blocks are prepared before the chains start (0: all)
   unsigned *made;         // [blocks][Hv]: a later block prepared, beside the chains
+  unsigned *before;       // [B + 1]: blocks of the sequences before one, and of all (more than MAX_KEPT sequences)
   int makers;             // CTAs that do
   int row_blocks;         // of ROWS rows a value head
   int stall;              // test aid: the first block never arrives
@@ -112,9 +113,67 @@ __device__ __forceinline__ bool all_rows(bool ok) {
 }
 __device__ __forceinline__ float pow2_inverse(float x) { return __int_as_float((254 << 23) - __float_as_int(x)); }  // of a power of two
 
-// Place of a sequence's first block in the workspace: sequences do not share
-// places, and none is past T / C + B.
-__device__ __forceinline__ int first_block(const PoolParams &P, int b, int row0) { return row0 / C + b; }
+// Blocks that the workspace has places for: as many as sequences without common rows can have.
+__host__ __device__ inline long long places(int B, int T) { return (long long)T / C + B; }
+
+// A sequence's blocks stand behind those of all sequences before it that are not left out.  Sequences that
+// share rows (their offsets fall) may have more blocks than there are places: all are left out then.
+__device__ __forceinline__ unsigned blocks_of(const PoolParams &P, int b) { return ((unsigned)rows_of(P, b, false).y + C - 1) / C; }
+// Places of up to MAX_KEPT sequences, four a lane of the warp (128 sequences of 2^24 blocks stay within 32 bits).
+struct Places {
+  unsigned before[4], all;
+  // (b: the same in all lanes)
+  __device__ __forceinline__ int first(int b) const {
+    const int x = b & 3;
+    return (int)__shfl_sync(0xffffffffu, x == 0 ? before[0] : x == 1 ? before[1] : x == 2 ? before[2] : before[3], b >> 2);
+  }
+};
+__device__ __forceinline__ Places places_of(const PoolParams &P, int lane) {
+  Places p;
+  unsigned n[4], x = 0;
+#pragma unroll
+  for (int y = 0; y < 4; ++y) x += n[y] = 4 * lane + y < P.B ? blocks_of(P, 4 * lane + y) : 0u;
+  const unsigned mine = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  p.all = __shfl_sync(0xffffffffu, x, 31);
+  p.before[0] = x - mine;
+#pragma unroll
+  for (int y = 1; y < 4; ++y) p.before[y] = p.before[y - 1] + n[y - 1];
+  return p;
+}
+// Of more sequences: once a call, by one CTA.
+__global__ void __launch_bounds__(1024) places_kernel(const __grid_constant__ ChunkParams CP) {
+  const PoolParams &P = CP.p;
+  __shared__ unsigned sums[32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  pdl_wait();
+  const unsigned most = (unsigned)places(P.B, P.T) + 1;  // (below 2^25; sums stay at it)
+  unsigned all = 0;
+  for (int b0 = 0; b0 < P.B; b0 += 1024) {
+    const unsigned n = b0 + tid < P.B ? blocks_of(P, b0 + tid) : 0u;
+    unsigned x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = min(x + y, most);
+    }
+    __syncthreads();  // (sums of the sequences before have been read)
+    if (lane == 31) sums[tid >> 5] = x;
+    __syncthreads();
+    unsigned front = 0, round = 0;
+    for (int w = 0; w < 32; ++w) {
+      if (w < (tid >> 5)) front = min(front + sums[w], most);
+      round = min(round + sums[w], most);
+    }
+    if (b0 + tid < P.B) CP.before[b0 + tid] = min(min(all + front, most) + x, most) - n;
+    all = min(all + round, most);
+  }
+  if (tid == 0) CP.before[P.B] = all;
+}
 
 // x + y of two-part values, the first part the value rounded.
 __device__ __forceinline__ float2 add_parts(float2 x, float2 y) {
@@ -431,24 +490,32 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
   int w = blockIdx.x / heads, b, c;  // (heads of the same tokens side by side)
   const int head = blockIdx.x - w * heads, hk = CP.split ? head / group : head;
   const int e0 = CP.split ? head - hk * group : 0, e1 = CP.split ? e0 + 1 : group;
-  int2 own;
+  unsigned all;
   if (CP.first) {
-    const unsigned flags = (unsigned)(P.T / C + P.B) * P.Hv;
+    const unsigned flags = (unsigned)places(P.B, P.T) * P.Hv;
     for (unsigned x = blockIdx.x * 128 + pt; x < flags; x += gridDim.x * 128) CP.made[x] = 0;
     b = w / CP.first, c = w - b * CP.first;
-    own = rows_of(P, b, false);
-    w = first_block(P, b, own.x) + c;
+    const Places at = places_of(P, pt & 31);
+    w = at.first(b) + c, all = at.all;
+  } else if (P.B <= MAX_KEPT) {
+    const Places at = places_of(P, pt & 31);
+    // the last sequence that begins at or before it: the last of a lane's four, of the last such lane
+    int mine = -1, from = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      if (4 * (pt & 31) + y < P.B && (int)at.before[y] <= w) mine = 4 * (pt & 31) + y, from = (int)at.before[y];
+    const int lane = 31 - __clz(__ballot_sync(0xffffffffu, mine >= 0));  // (the first sequence begins at 0)
+    b = __shfl_sync(0xffffffffu, mine, lane), c = w - __shfl_sync(0xffffffffu, from, lane), all = at.all;
   } else {
     int lo = 0, hi = P.B - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (first_block(P, mid, P.cu[mid]) <= w) lo = mid; else hi = mid - 1;
+      if (CP.before[mid] <= (unsigned)w) lo = mid; else hi = mid - 1;
     }
-    b = lo;
-    own = rows_of(P, b, false);
-    c = w - first_block(P, b, own.x);
+    b = lo, c = w - (int)CP.before[b], all = CP.before[P.B];
   }
-  if (c < 0 || c * C >= own.y) return;
+  const int2 own = rows_of(P, b, false);
+  if ((long long)c * C >= own.y || all > (unsigned)places(P.B, P.T)) return;
   if (pt == 0) {
     mbar_init(done, 1);
     fence_barrier_init();
@@ -578,7 +645,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
   const int per = P.Hv * CP.row_blocks;
   int b = id / per;
   const int rest = id - b * per, h = rest / CP.row_blocks, i0 = (rest - h * CP.row_blocks) * ROWS;
-  if (P.B > 1 && P.B <= MAX_SORTED) {
+  if (P.B > 1 && P.B <= MAX_KEPT) {
     int *len = reinterpret_cast<int *>(smem + Y::XCHG);
     if (tid < P.B) len[tid] = rows_of(P, tid, false).y;
     __syncthreads();
@@ -598,7 +665,18 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
   const bool report = rest == 0 && tid == 0;
   const int2 own = rows_of(P, b, report);
   const int slot = slot_of(P, b, report);
-  const int n = (own.y + C - 1) / C;  // blocks
+  int w0 = 0;                   // place of its first block
+  int n = (own.y + C - 1) / C;  // blocks
+  if (P.B > 1) {
+    unsigned all;
+    if (P.B <= MAX_KEPT) {
+      const Places at = places_of(P, lane);
+      w0 = at.first(b), all = at.all;
+    } else {
+      w0 = (int)CP.before[b], all = CP.before[P.B];
+    }
+    if (all > (unsigned)places(P.B, P.T)) n = 0;
+  }
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const int r = (warp & 3) * 32 + lane;  // row, of those that hold one
   bool ok = true;
@@ -620,7 +698,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
     if (warp == FETCH) {
       // ---------------------------------------------------------- copies --
       if (lane == 0) {
-        const int hk = h / (P.Hv / P.Hk), w0 = first_block(P, b, own.x);
+        const int hk = h / (P.Hv / P.Hk);
         int c = 0;
         if (n > 0 && slot >= 0) {
           mbar_arrive_expect_tx(s_here, ROWS * DK * 4);
@@ -978,7 +1056,6 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
   }
 }
 
-// Blocks that the workspace has places for.
 template <int DK>
 __global__ void __launch_bounds__(CHAIN_THREADS, 1)
     chain_kernel(const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapS, const __grid_constant__ ChunkParams CP) {
@@ -1029,9 +1106,10 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
   const uint32_t tb = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_wait();
   const int group = P.Hv / P.Hk;
+  const Places at = places_of(P, threadIdx.x & 31);  // (few items, so few sequences)
   int most = 0;  // blocks of the longest sequence
   for (int b = threadIdx.x & 31; b < P.B; b += 32) most = imax(most, (rows_of(P, b, false).y + C - 1) / C);
-  most = __reduce_max_sync(0xffffffffu, most);
+  most = at.all > (unsigned)places(P.B, P.T) ? 0 : __reduce_max_sync(0xffffffffu, most);
   // the next blocks a value head at a time, those behind them a key head
   const int later = imax(0, most - CP.first), soon = imin(later, SOON);
   const long long single = (long long)soon * P.B * P.Hv, tasks = single + (long long)(later - soon) * P.B * P.Hk;
@@ -1046,7 +1124,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
     const int e0 = one ? head - hk * group : 0, e1 = one ? e0 + 1 : group;
     const int2 rows = rows_of(P, b, false);
     if (c * C >= rows.y) continue;
-    const int w = first_block(P, b, rows.x) + c;
+    const int w = at.first(b) + c;
     prepare<DK>(CP, own, tb + 64 * g, done, parity, 1 + g, pt, hk, e0, e1, w, rows.x + (long long)c * C, imin(C, rows.y - c * C));
     parity ^= 1;
     __threadfence();
@@ -1063,7 +1141,6 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1)
   }
 }
 
-inline long long places(int B, int T) { return (long long)T / C + B; }
 inline size_t padded(int dv) { return ((size_t)dv + ROWS - 1) / ROWS * ROWS; }
 
 template <int DK>
@@ -1095,7 +1172,7 @@ sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
   if (sms <= 0) return SV_ERR_CUDA;
   // Few items: all but the first blocks are prepared while the chains run (one sequence of 8192
   // tokens, 48 heads of 128 x 128: 325 us against 390; 2000 tokens 99 against 107; 1000 not faster).
-  CP.first = items <= sms / 2 && P.T > 2LL * FIRST * C * P.B ? FIRST : 0;
+  CP.first = items <= sms / 2 && P.B <= MAX_KEPT && P.T > 2LL * FIRST * C * P.B ? FIRST : 0;
   const long long before = CP.first ? (long long)P.B * FIRST : blocks;
   // A value head a CTA while all of them are on the SMs at once, its key head's products made anew for
   // each (77 tokens: 18 us against 24; but eleven prompts of 1 to 3001 tokens 225 us against 199).
@@ -1104,6 +1181,7 @@ sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
   // Chains that find SMs of their own fetch their states meanwhile (77 tokens 16.1 us against 17.6); others would
   // only take places early (eleven prompts 212 us against 196, 8192 tokens 342 against 325).
   CP.early = !CP.first && grid + items <= sms;
+  if (P.B > MAX_KEPT && launch_early(places_kernel, dim3(1), dim3(1024), 0, s, CP) != cudaSuccess) return SV_ERR_CUDA;
   cudaError_t e = launch_early(prepare_kernel<DK>, dim3((unsigned)grid), dim3(128), (size_t)PL<DK>::BYTES, s, CP);
   if (e != cudaSuccess) return SV_ERR_CUDA;
   const size_t smem = CL<DK>::BYTES;
@@ -1125,7 +1203,7 @@ extern "C" {
 size_t gdn_chunk_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv) {
   if (B < 1 || T < 1 || Hk < 1 || Hv < 1 || dv < 1 || (dk != 64 && dk != 128)) return 0;
   const size_t per = (size_t)Hk * 4 * gdn::C * dk + (size_t)Hv * (gdn::HEAD_BYTES + 4);
-  return (size_t)gdn::places(B, T) * per;
+  return (size_t)gdn::places(B, T) * per + ((size_t)B + 1) * 4;
 }
 
 sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows *q, const sv_rows *k,
@@ -1160,6 +1238,7 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   CP.keys = static_cast<uint8_t *>(workspace);
   CP.heads = CP.keys + (size_t)gdn::places(B, T) * Hk * 4 * gdn::C * dk;
   CP.made = reinterpret_cast<unsigned *>(CP.heads + (size_t)gdn::places(B, T) * Hv * gdn::HEAD_BYTES);
+  CP.before = CP.made + (size_t)gdn::places(B, T) * Hv;
   CP.row_blocks = row_blocks;
   CP.stall = launch_flags() & SV_LAUNCH_TEST_STALL_COPY ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
