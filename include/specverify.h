@@ -638,11 +638,11 @@ SV_API sv_status gdn_step(const sv_states *states, const int32_t *slots, const s
  *   a sequence without rows.  slots: as gdn_step's.
  * Domain: 0 <= beta and beta * |k|^2 <= 2 (a token then lengthens no state; unit keys with
  *   gates from a sigmoid, or twice one, do) and g <= 0; finite values.
- * Arithmetic: blocks of 64 tokens, fp32 sums of products whose operands are fp32 values held as
- *   two fp16 parts (off by 2^-22 of themselves, or by 2^-40 of a bound of their row); what only o
- *   sees, the state and the updates in its products, is one part (2^-11).  Elements of a key or
- *   query are exact down to 2^-13 of its largest and off by 2^-21 of that below.  A call of T <= 16 or
- *   T <= 8*B runs token by token, as gdn_step does.
+ * Arithmetic: blocks of 64 tokens, fp32 sums of products whose operands are fp32 values held as two
+ *   fp16 parts (off by 2^-22 of themselves, or by 2^-39 of a bound of their row in the block; entries of
+ *   the blocks' inverse, 1 on its diagonal, by 2^-34); what only o sees, the state and the updates in its
+ *   products, is one part (2^-11).  Elements of a key or query are exact down to 2^-13 of its largest
+ *   and off by 2^-21 of that below.  A call of T <= 16 or T <= 8*B runs token by token, as gdn_step does.
  * Offsets that fall, so that sequences name the same rows: o of those rows is undefined.  Where they
  *   name rows so often that they hold more blocks of 64 than T and B of them can, all are left out.
  * Supported: dk in {64, 128}; Hv % Hk == 0, Hv <= 65535; dv <= 65536; 0 <= B <= 65535;

@@ -36,10 +36,13 @@
 //    u' = 2^e u is the same rule), a query likewise, and each row of S, and of R and U, by
 //    factors of a block of their own, from bounds of what they can reach: S by its largest
 //    element before and sum |U~| |k'|; U by its own: with b |k|^2 <= 2 a token adds at most
-//    |b' v'| |k'| to a row's norm, so that |u'| <= |b' v'| + b' |k'| (|S| + 64 |b' v'| |k'|).  The parts are
-//    off by 2^-22 of themselves, or 2^-40 of that bound.
+//    |b' v'| |k'| to a row's norm, so that |u'| <= |b' v'| + b' |k'| (|S| + 64 |b' v'| |k'|).  Both stand
+//    below 2^15, so that the parts are off by 2^-22 of themselves, or 2^-39 of that bound.
 //  * The inverse: four 16 x 16 blocks by forward substitution in fp32, then joined twice
-//    by -T22 (A21 T11), which is as stable as the substitution.
+//    by -T22 (A21 T11), which is as stable as the substitution.  Its entries are at most 45 (b' |k'|^2 <= 2,
+//    and no |k'| is over 23 times another); they are held T_GAIN times as large, which fp16 still reaches,
+//    so that small ones (a token seen through many decays) are off by 2^-34 only: a state that decays by e^-6.4 in
+//    a block keeps 2^-22 of itself, and 2^-16 without that.
 //  * G is summed in two fp32 parts and so are its differences: a gate that closes
 //    (g = -1000) leaves the decays behind it exact.
 #include "gdn_pool.cuh"
@@ -58,10 +61,11 @@ constexpr int AS = 68;       // row stride of the inverse's fp32 matrix
 constexpr int MAX_KEPT = 128;  // sequences whose lengths and places a CTA looks at itself
 constexpr float G_LEAST = -10000.f;  // e^g is 0 long before
 constexpr float P_GAIN = 1024.f;     // P is taken so much larger: decays down to 2^-24 keep their bits
+constexpr float T_GAIN = 512.f;      // and A and T
 
 // A block's scalars for one value head.
 struct Scalars {
-  float bv[C], bx[C], en[C], os1[C], os2[C];  // of v and of X (negative) in R, of U in U~, of the output's two products
+  float bv[C], bx[C], en[C], os1[C], os2[C];  // of v and of X (negative) in R, of T_GAIN U in U~, of the output's two products
   float gc;                                   // decay over the block
   float bk[2];                                // largest b' |k'|, of the first and of the last tokens
   float pad[61];
@@ -217,10 +221,12 @@ __device__ __forceinline__ void multiply(float (&d)[4], const Parts<4> &l, const
   mma_f16_16816(d, l.hi[0], l.hi[1], l.hi[2], l.hi[3], r.lo[0], r.lo[1]);
   mma_f16_16816(d, l.hi[0], l.hi[1], l.hi[2], l.hi[3], r.hi[0], r.hi[1]);
 }
+// A product of two matrices that are held T_GAIN times as large, as such a matrix.
 __device__ __forceinline__ void put_tile(float *a, const float (&d)[4], bool minus, int lane) {
   float *x = a + (lane >> 2) * AS + 2 * (lane & 3);
-  *reinterpret_cast<float2 *>(x) = minus ? make_float2(-d[0], -d[1]) : make_float2(d[0], d[1]);
-  *reinterpret_cast<float2 *>(x + 8 * AS) = minus ? make_float2(-d[2], -d[3]) : make_float2(d[2], d[3]);
+  const float f = minus ? -1.f / T_GAIN : 1.f / T_GAIN;
+  *reinterpret_cast<float2 *>(x) = make_float2(f * d[0], f * d[1]);
+  *reinterpret_cast<float2 *>(x + 8 * AS) = make_float2(f * d[2], f * d[3]);
 }
 
 // Prepares rows r0..r0+m-1, block w of the workspace, for value heads e0..e1-1 of key head hk: 128
@@ -337,7 +343,7 @@ __device__ __forceinline__ void prepare(const ChunkParams &CP, uint8_t *smem, ui
       const float bs = be * e_i;
       S->bv[i] = bs;
       S->bx[i] = -(bs * e_i * ga);
-      S->en[i] = ex2_approx((gh[C - 1] - hi_i) + (gl[C - 1] - lo_i));
+      S->en[i] = ex2_approx((gh[C - 1] - hi_i) + (gl[C - 1] - lo_i)) * (1.f / T_GAIN);
     } else {
       const float os = pow2_field(imin(ex[C + i] + 4, 254));
       S->os1[i] = os * ga;
@@ -346,7 +352,7 @@ __device__ __forceinline__ void prepare(const ChunkParams &CP, uint8_t *smem, ui
     }
     // ---- A (rows of the first two warps) and P ----
     {
-      const float rf = isP ? P_GAIN : be * e_i * e_i;
+      const float rf = isP ? P_GAIN : be * e_i * e_i * T_GAIN;
       const f2 rowf = pack2(rf, rf), hi2 = pack2(hi_i, hi_i), lo2 = pack2(lo_i, lo_i), neg = pack2(-1.f, -1.f);
       const int last = isP ? i : i - 1;  // columns up to it count
 #pragma unroll
@@ -360,7 +366,7 @@ __device__ __forceinline__ void prepare(const ChunkParams &CP, uint8_t *smem, ui
 #pragma unroll
           for (int x = 0; x < 32; ++x) kk = x == lane ? __uint_as_float(raw[x]) : kk;
           // (of values that are not negative the larger has the larger bits)
-          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(rf) * sqrtf(kk)));
+          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(rf) * (1.f / T_GAIN) * sqrtf(kk)));
           if (lane == 0) S->bk[pw] = __uint_as_float(top);
         }
 #pragma unroll
@@ -397,7 +403,7 @@ __device__ __forceinline__ void prepare(const ChunkParams &CP, uint8_t *smem, ui
       float x[16];
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        float s0 = r == lane ? 1.f : 0.f, s1 = 0.f;
+        float s0 = r == lane ? T_GAIN : 0.f, s1 = 0.f;
 #pragma unroll
         for (int j = 0; j < r; j += 4) {
           const float4 a = *reinterpret_cast<const float4 *>(A + (o + r) * AS + o + j);
@@ -406,12 +412,12 @@ __device__ __forceinline__ void prepare(const ChunkParams &CP, uint8_t *smem, ui
           if (j + 2 < r) s0 = fmaf(-a.z, x[j + 2], s0);
           if (j + 3 < r) s1 = fmaf(-a.w, x[j + 3], s1);
         }
-        x[r] = s0 + s1;
+        x[r] = (s0 + s1) * (1.f / T_GAIN);
       }
       __syncwarp();
       if (lane < 16) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) A[(o + r) * AS + o + lane] = x[r];
+        for (int r = 0; r < 16; ++r) A[(o + r) * AS + o + lane] = x[r] * T_GAIN;
       }
     }
     sync();
@@ -913,7 +919,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
       return fmaxf(__low2float(most), __high2float(most));
     };
     if (n > 0) {
-      sc = scale_of(both(m * 0.015625f));
+      sc = scale_of(both(m * 0x1p-15f));
       const f2 sc2 = pack2(sc, sc);
 #pragma unroll
       for (int e = 0; e < SC / 2; ++e) S[e] = mul2(S[e], sc2);
@@ -993,9 +999,10 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
           const uint32_t (&raw)[16] = raw2[g];
 #pragma unroll
           for (int t = 0; t < 8; ++t) {
-            const float a = __uint_as_float(raw[2 * t]), d = __uint_as_float(raw[2 * t + 1]);
-            u[t] = pack_f16x2(a, d);
-            split2(mul2(pack2(a, d), *reinterpret_cast<const f2 *>(&Z->en[hf * 32 + 16 * g + 2 * t])), hi[t], lo[t]);
+            const f2 ad = pack2(__uint_as_float(raw[2 * t]), __uint_as_float(raw[2 * t + 1]));
+            const float2 one = unpack2(mul2(ad, pack2(1.f / T_GAIN, 1.f / T_GAIN)));
+            u[t] = pack_f16x2(one.x, one.y);
+            split2(mul2(ad, *reinterpret_cast<const f2 *>(&Z->en[hf * 32 + 16 * g + 2 * t])), hi[t], lo[t]);
             um = __hmax2(um, __habs2(*reinterpret_cast<__half2 *>(&hi[t])));
           }
           tc::st8(tb + Y::U + hf * 32 + 16 * g + lane_off, hi);
@@ -1014,7 +1021,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
       float next = sc;
       if (c + 1 < n) {
         // elements of k' are below 2^-3, 64 tokens: |S'| <= 8 |U~|; twice, as above
-        next = scale_of(both((gc * m * isc + 8.f * fmaxf(__low2float(um), __high2float(um)) * iscr) * 0.03125f));
+        next = scale_of(both((gc * m * isc + 8.f * fmaxf(__low2float(um), __high2float(um)) * iscr) * 0x1p-14f));
       }
       if (c + 1 < n) load_values(st, phase);
       const float keep = gc * (next * isc), add = next * iscr;
