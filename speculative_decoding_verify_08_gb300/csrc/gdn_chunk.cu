@@ -896,7 +896,9 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
     }
     if (kept) arrive(s_read);
     // scale of a row: 2^-k with at most 1 behind it
-    auto scale_of = [&](float most) { return pow2_field(253 - imin(imax(__float_as_int(most) >> 23, 27), 226)); };
+    auto scale_of = [&](float most) { return pow2_field(253 - imin(imax(__float_as_int(most) >> 23, 1), 250)); };
+    // the smallest of what fp16 parts show; smaller elements are 0 in them
+    constexpr float LEAST = 0x1p-24f;
     // S (held scaled) as the next product's operand, a k-step at a time; the largest |S| of it
     auto put_state = [&]() {
       __half2 most = __float2half2_rn(0.f);
@@ -953,9 +955,10 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
           const float2 z = unpack2(w[t]);
           wm = fmaxf(wm, fmaxf(fabsf(z.x), fabsf(z.y)));
         }
-        // what U can reach, twice as the two halves of a row have terms of their own
-        const float bk = fmaxf(Z->bk[0], Z->bk[1]), isc = pow2_inverse(sc);
-        scr = scale_of(both(fmaf(bk, 12.f * m * isc + 91.f * wm, wm) * 0x1p-14f));
+        // what U can reach, twice as the two halves of a row have terms of their own; and not so little beside
+        // the state that the step from its scale to this one leaves fp32 (nothing at all where beta is 0)
+        const float bk = fmaxf(Z->bk[0], Z->bk[1]), isc = pow2_inverse(sc), wl = wm * 0x1p-14f;
+        scr = scale_of(both(fmaf(bk, 12.f * m * (isc * 0x1p-14f) + 91.f * wl, wl) + isc * 0x1p-94f));
         if (hf == 0) scale[par * ROWS + r] = pack_bf16x2(isc, pow2_inverse(scr));  // (powers of two)
         const f2 scr2 = pack2(scr, scr);
 #pragma unroll
@@ -1018,13 +1021,14 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
       st = st + 1 == STAGES ? 0 : st + 1;
       phase ^= st == 0;
       const float isc = pow2_inverse(sc), iscr = pow2_inverse(scr);
-      float next = sc;
-      if (c + 1 < n) {
-        // elements of k' are below 2^-3, 64 tokens: |S'| <= 8 |U~|; twice, as above
-        next = scale_of(both((gc * m * isc + 8.f * fmaxf(__low2float(um), __high2float(um)) * iscr) * 0x1p-14f));
-      }
+      // elements of k' are below 2^-3, 64 tokens: |S'| <= 8 |U~|; twice, as above (with LEAST neither step
+      // from an old scale to the new one passes 2^40, whatever a gate has cleared; behind the last block too,
+      // where what was added may be far larger than the state was)
+      const float u = fmaxf(fmaxf(__low2float(um), __high2float(um)), LEAST);
+      const float next = scale_of(both(gc * fmaxf(m, LEAST) * (isc * 0x1p-14f) + 8.f * u * (iscr * 0x1p-14f)));
       if (c + 1 < n) load_values(st, phase);
-      const float keep = gc * (next * isc), add = next * iscr;
+      const float step = next * isc, add = next * iscr;
+      const float keep = step <= 0x1p126f ? gc * step : gc * isc * next;  // (a large one: gc is small)
       sc = next;
       const f2 keep2 = pack2(keep, keep), add_2 = pack2(add, add);
 #pragma unroll
