@@ -271,8 +271,10 @@ __device__ __forceinline__ void prepare(const ChunkParams &CP, uint8_t *smem, ui
                                      __vmaxu2(v[y][z].z & 0x7fff7fffu, v[y][z].w & 0x7fff7fffu)));
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const int E = (int)(max(mx & 0xffffu, mx >> 16) >> 7);
-        const float f = pow2_field(imax(250 - E, 1));
+        // (2^(250 - E) and its inverse both have to be normal: beyond, queries are left larger, still within
+        // fp16, and keys are zeros, as beta can only be 0 there)
+        const int top = (int)(max(mx & 0xffffu, mx >> 16) >> 7), E = imin(top, 249);
+        const float f = top > 249 && half == 0 ? 0.f : pow2_field(250 - E);
         const f2 f2x = pack2(f, f);
         auto two = [&](uint32_t x) {
           const float2 p = unpack2(mul2(pack2(bf16lo(x), bf16hi(x)), f2x));
@@ -308,7 +310,7 @@ __device__ __forceinline__ void prepare(const ChunkParams &CP, uint8_t *smem, ui
   tc::fence_after_sync();
   const bool isP = pw >= 2;
   const int i = (pw & 1) * 32 + lane;  // this thread's row of A, or of P
-  const float e_i = pow2_field(imin(ex[i] + 4, 254));  // 2^e of its key
+  const float e_i = pow2_field(ex[i] + 4);  // 2^e of its key
   for (int e = e0; e < e1; ++e) {
     const int h = hk * group + e;
     uint8_t *out = CP.heads + ((size_t)w * P.Hv + h) * HEAD_BYTES;
@@ -345,7 +347,7 @@ __device__ __forceinline__ void prepare(const ChunkParams &CP, uint8_t *smem, ui
       S->bx[i] = -(bs * e_i * ga);
       S->en[i] = ex2_approx((gh[C - 1] - hi_i) + (gl[C - 1] - lo_i)) * (1.f / T_GAIN);
     } else {
-      const float os = pow2_field(imin(ex[C + i] + 4, 254));
+      const float os = pow2_field(ex[C + i] + 4);
       S->os1[i] = os * ga;
       S->os2[i] = os * (1.f / P_GAIN);
       if (i == C - 1) S->gc = ga;

@@ -73,3 +73,28 @@ def test_from_an_empty_state(cuda_lib, dk, size, T):
     """A new sequence's state is zeros: nothing about it says how large the values are."""
     Hk, Hv, dv = 1, 2, 40
     compare(cuda_lib, some_rows(T, Hk, Hv, dk, dv, 79, values=size), torch.zeros(1, Hv, dv, dk), T)
+
+
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("size", [1e-30, 1e30, 1e38])
+def test_queries_of_any_size(cuda_lib, dk, size):
+    """Up to the largest bf16 holds, beside states that keep the outputs in range."""
+    T, Hk, Hv, dv = 150, 1, 2, 40
+    small = 1e-30 if size > 1 else 1.0
+    r = some_rows(T, Hk, Hv, dk, dv, 77, values=small, queries=size)
+    assert bool(torch.isfinite(r["q"].float()).all())
+    compare(cuda_lib, r, some_states(Hv, dv, dk, 78, small), T)
+
+
+@pytest.mark.parametrize("dk", [64, 128])
+def test_keys_of_any_size(cuda_lib, dk):
+    """From 1e-30 to the largest bf16 holds, each with a strength to match (none where fp32 has none)."""
+    T, Hk, Hv, dv = 150, 1, 2, 40
+    r = some_rows(T, Hk, Hv, dk, dv, 80)
+    # values go with the keys, so that every token moves the state as much
+    size = torch.tensor([1.0, 1e-15, 1e15, 1e38, 1e-30, 1.0, 3e17])[torch.arange(T) % 7]
+    r["k"] = (r["k"].float() * size[:, None, None]).bfloat16()
+    r["v"] = (r["v"].float() * size[:, None, None]).clamp(-3e38, 3e38).bfloat16()  # finite, as the contract wants them
+    assert bool(torch.isfinite(r["k"].float()).all()) and bool(torch.isfinite(r["v"].float()).all())
+    r["beta"] = torch.where(size[:, None] > 1e30, torch.zeros(()), (r["beta"].double() / size[:, None].double() ** 2).clamp(max=1e30).float())
+    compare(cuda_lib, r, some_states(Hv, dv, dk, 81, 1.0), T)
