@@ -837,7 +837,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
           mx = max(mx & 0xffffu, mx >> 16);
           if (HALVES == 2) mx = max(mx, __float_as_uint(trade(__uint_as_float(mx))));
           const int e = (int)(mx >> 7), E = imin(imax(e, 16), 254);
-          sl2e = P.sl2e * (P.ks ? P.ks[it.h] : 1.f) * __int_as_float((E - 7) << 23);
+          // (never 0, which would make a masked score's -inf NaN: scores this small are all 0 to their exponential)
+          sl2e = fmaxf(P.sl2e * (P.ks ? P.ks[it.h] : 1.f) * __int_as_float((E - 7) << 23), 0x1p-126f);
           scale2 = pack2(sl2e, sl2e);
           float up = __int_as_float((261 - E) << 23);  // 2^(7 - (E - 127))
           if (e == 255) up = __int_as_float(0x7fffffff);  // e4m3 has no infinity: the row's scores are NaN
