@@ -451,16 +451,18 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
       const bool here = first < (is_v ? VK : BN);
       const uint32_t bytes = (uint32_t)P.R * 128 * (!F8 && is_v ? D / 64 : 1);
       // A piece's page and its slot there: page -1 where no row sees any slot of it, past the cache
-      // where its entry is (which reads as zeros).
+      // where its entry is (which reads as zeros).  Values behind the sequence's end are read as the page
+      // behind the last, as zeros: their place holds what another item left, which may be anything.
       struct Place {
         int page, slot;
       };
       auto look = [&](const Item &it, int j, int x) {
         const int pos = position(P, it, j, first + x * gap);
+        if (!F8 && is_v && here && pos >= it.len) return Place{P.num_pages, 0};
         if (!here || pos >= it.len || (pos >= P.sinks && pos + P.R <= it.from)) return Place{-1, 0};
         const int e = pos / P.page_size;
         const int page = P.table[it.b * P.table_stride + e];
-        return Place{page, page == -1 ? ~(pos - e * P.page_size) : pos - e * P.page_size};
+        return Place{page == P.num_pages ? -2 : page, page == -1 ? ~(pos - e * P.page_size) : pos - e * P.page_size};
       };
       bool ok = true;
       uint32_t q = 0, parity = 1;
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
         if (lane == 0) mbar_arrive_expect_tx(&landed[slot], n * bytes);
         __syncwarp();
         if (live) {
-          if (at.page < 0 || at.page >= P.num_pages) {
+          if (at.page < 0 || at.page > P.num_pages) {
             atomicOr(P.err, ERR_INDEX);
             at.page = P.num_pages;
           }
@@ -716,7 +718,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, F8>::THREADS, 1)
               if (t == 0) wait(&full[5 + at.slot], at.parity);
               if (some && t == 0) {
                 const Blind none = blind(P, it, j);
-                const int upto = (none.c + P.R - 1) & -P.R;  // (pieces behind hold older values)
+                const int upto = (none.c + P.R - 1) & -P.R;  // (pieces behind are zeros)
                 uint8_t *vb = ring + NK * KSLOT + at.slot * SLOT;
                 auto clear = [&](int r0, int r1) {  // rows of the block, those of this slot
                   r0 = imax(r0 - x * VK, 0), r1 = imin(r1 - x * VK, VK);
