@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_
   }
   __syncthreads();
   pdl_wait();
-  const int mine = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  // (tiles may be next to 2^31)
+  const int mine = tiles > (int)blockIdx.x ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
   // sequence, head and first row of this block's k-th tile
   struct Where {
     int b, h, i0;
