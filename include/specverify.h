@@ -413,10 +413,13 @@ SV_API sv_status window_attn(const sv_rows *q, const sv_rows *k, const sv_rows *
  *   more than Tq and B of them can).  Rows of o of no sequence are not written.
  * block_table, kv_lens, cache: as paged_attn's, with its rules for lengths, entries
  *   and pages out of range, and for slots that no row sees.
- * Arithmetic as paged_attn's: fp32, with the second product's operands in 16 bits
- *   (e4m3 pages: probabilities keep 2^-11 down to 2^-24 of the row's largest, and are
- *   off by 2^-35 of that below; a query row's elements are exact down to 2^-9 of its
- *   largest, and off by 2^-17 of that below).
+ * Arithmetic fp32, with the second product's operands in 16 bits.  bf16 pages: as
+ *   paged_attn's.  e4m3 pages: fewer bits than paged_attn's: probabilities in fp16, 2^-11
+ *   relative down to 2^-24 of the row's largest, by 2^-35 of that below; a query row's
+ *   elements in two e4m3 parts, exact down to 2^-9 of its largest (of rows whose largest is
+ *   2^-111 or more), by 2^-17 of that below.  Sums take the probabilities as they were.
+ *   Visible values that are not finite reach their own sequence's rows only, and queries
+ *   that are not their own row.
  * Supported: D in {128, 256}; Hq % Hkv == 0; Hq/Hkv <= 128; 0 <= B <= 4096;
  *   Tq <= 2^30; table_width*page_size <= 2^30; (Tq / (128 / (Hq/Hkv)) + B) * Hkv *
  *   (table_width*page_size/128 + 4) < 2^31, divisions rounded down; strides of q above

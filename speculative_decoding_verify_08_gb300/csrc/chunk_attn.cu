@@ -29,11 +29,12 @@
 //    maximum that they refer to is raised when a block exceeds it by more than 2^5).
 //
 // Measured (GB300, whole calls; the products' time at 1893 TFLOP/s): 2048 rows behind 30000
-// positions, 24 heads of 256 over 4, 1.03-1.14 ms (0.83); 13 chunks of 1 to 777 rows behind 5000, 32 heads
-// of 128 over 8, 116-120 us (67); 2 x 4001 rows under a window of 1024 over e4m3 pages 155 us (71; over bf16
-// pages 129); 61 rows behind 16000 over e4m3 pages 38-42 us, of which 9 pass before the first product and 5
-// behind the last.  A block of two tiles takes 2900 clocks, of which 2050 are products: each tile's chain of
-// scores, softmax and second product; an item costs 6000 more, 9000 with queries to turn.
+// positions, 24 heads of 256 over 4, 1.05 ms at 2.07 GHz and 1.16 at the 1.67 GHz that power leaves it (0.83); 13
+// chunks of 1 to 777 rows behind 5000, 32 heads of 128 over 8, 116-120 us (67); 2 x 4001 rows under a window of
+// 1024 over e4m3 pages 155 us (71; over bf16 pages 129); 61 rows behind 16000 over e4m3 pages 38-42 us, of which 9
+// pass before the first product and 5 behind the last.  A block of two tiles takes 2900 clocks, of which 2050 are
+// products: each tile's chain of scores, softmax and second product; an item costs 6000 more, 9000 with queries
+// to turn.
 #include "paged.cuh"
 #include "tcgen05.cuh"
 

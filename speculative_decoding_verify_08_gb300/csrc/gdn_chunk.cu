@@ -21,11 +21,11 @@
 //    next product's first operand.  Two threads share a row; S stays in their
 //    registers, in fp32.  Four warps write the output meanwhile, one issues the
 //    products, one the copies (up to three blocks ahead).
-//    A block takes it 2.3 us, 0.7 of them products; the rest is their results' way through
+//    A block takes it 2.5 us, 0.7 of them products; the rest is their results' way through
 //    registers, four times a block.
 //  * both_kernel is the chains with the preparation of later blocks on the SMs that they leave.
-//    Measured (48 heads of 128 x 128 over 16): one sequence of 8192 tokens 325 us, of 77 16; eleven of 1 to
-//    3001 tokens 196, of which preparation takes 75.
+//    Measured (48 heads of 128 x 128 over 16): one sequence of 8192 tokens 331 us, of 77 15.7; eleven of 1 to
+//    3001 tokens 198, of which preparation takes 78.
 //  * Products take fp16 operands and fp32 sums.  S, R, U and T are fp32 values held
 //    as two fp16 parts (x = hi + lo, 2^-22 of x), so that a state stays an fp32 one; what
 //    only an output sees (S and U there, and P) is one part, 2^-11 beside the
@@ -553,8 +553,9 @@ __global__ void __launch_bounds__(128, 6) prepare_kernel(const __grid_constant__
 // fetches, one issues the products.
 constexpr int ROW_WARPS = 8, OUT_WARPS = 4, FETCH = ROW_WARPS + OUT_WARPS, ISSUE = FETCH + 1;
 constexpr int CHAIN_THREADS = (ROW_WARPS + OUT_WARPS + 4) * 32, STAGES = 3;
-// Blocks of a sequence that are prepared before the chains where later ones are beside them, and how
-// many of those a value head at a time (sooner there; 8192 tokens 356 us with none, 342 with 16 or more).
+// Blocks of a sequence that are prepared before the chains where later ones are beside them (8192 tokens 332 us
+// with 8, 338 with 4), and how many of those a value head at a time (sooner there; 346 us with none, 339 with 8,
+// 331 with 16, 32 or 64).
 constexpr int FIRST = 8, SOON = 16;
 
 template <int DK>
@@ -1184,23 +1185,25 @@ sv_status run_chunks(ChunkParams &CP, cudaStream_t s) {
   const int sms = device_sm_count();
   if (sms <= 0) return SV_ERR_CUDA;
   // Few items: all but the first blocks are prepared while the chains run (one sequence of 8192
-  // tokens, 48 heads of 128 x 128: 325 us against 390; 2000 tokens 99 against 107; 1000 not faster).
+  // tokens, 48 heads of 128 x 128: 332 us against 392; 2000 tokens 103 against 110; 1000 would be 61 against 64).
   CP.first = items <= sms / 2 && P.B <= MAX_KEPT && P.T > 2LL * FIRST * C * P.B ? FIRST : 0;
   const long long before = CP.first ? (long long)P.B * FIRST : blocks;
   // A value head a CTA while all of them are on the SMs at once, its key head's products made anew for
-  // each (77 tokens: 18 us against 24; but eleven prompts of 1 to 3001 tokens 225 us against 199).
+  // each (77 tokens: 15.6 us against 21.8; but eleven prompts of 1 to 3001 tokens 225 us against 198).
   CP.split = before * P.Hv <= 6LL * sms;
   const long long grid = before * (CP.split ? P.Hv : P.Hk);
-  // Chains that find SMs of their own fetch their states meanwhile (77 tokens 16.1 us against 17.6); others would
-  // only take places early (eleven prompts 212 us against 196, 8192 tokens 342 against 325).
+  // Chains that find SMs of their own fetch their states meanwhile (77 tokens 15.6 us against 17.1); others would
+  // only take places early (eleven prompts 211 us against 198).
   CP.early = !CP.first && grid + items <= sms;
   if (P.B > MAX_KEPT && launch_early(places_kernel, dim3(1), dim3(1024), 0, s, CP) != cudaSuccess) return SV_ERR_CUDA;
   cudaError_t e = launch_early(prepare_kernel<DK>, dim3((unsigned)grid), dim3(128), (size_t)PL<DK>::BYTES, s, CP);
   if (e != cudaSuccess) return SV_ERR_CUDA;
   const size_t smem = CL<DK>::BYTES;
   if (!CP.first) return from_cuda(launch_early(chain_kernel<DK>, dim3((unsigned)items), dim3(CHAIN_THREADS), smem, s, mv, ms, CP));
-  // Three to two chains keep up with them, and more slow the chains down: 8192 tokens, 48 chains, 327 us
-  // with 70, 331 with 88, 342 with 104, 339 with 52.  Beside few chains as many as leave each SM pair one CTA.
+  // Three to two chains keep up with them, and more slow the chains down: 8192 tokens, 48 chains, 332 us
+  // with 72, 334 with 88, 351 with 104, 342 with 60, 360 with 40; 32 chains 328 with 48 to 96, 347 with 120, 344 with
+  // 32.  Beside few chains as many as leave each SM pair one CTA (8 chains 320 to 323 with any from 16 to 140, 2 chains
+  // 314 to 317).
   CP.makers = imin(sms - (int)items, imax(3 * (int)items / 2, sms / 2 - (int)items));
   return from_cuda(launch_early(both_kernel<DK>, dim3((unsigned)(CP.makers + items)), dim3(CHAIN_THREADS), smem, s, mv, ms, CP));
 }
@@ -1256,9 +1259,10 @@ sv_status gdn_chunk(const sv_states *states, const int32_t *slots, const sv_rows
   CP.stall = launch_flags() & SV_LAUNCH_TEST_STALL_COPY ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // A block costs as much with one token as with 64; token by token is faster up to some eight tokens a
-  // sequence (48 heads of 128 x 128: one sequence of 16 tokens 13 us against 14, of 24 17.6 against 14;
-  // two of 8 12 against 16, of 12 20 against 16; eight of 8 25 against 34, of 12 34 both; 64 of 8 169
-  // against 218, of 12 231 against 219; a long sequence among short ones takes 0.55 us a token).
+  // sequence (48 heads of 128 x 128: one sequence of 16 tokens 12 us against 13, of 24 17 against 13;
+  // two of 8 10 against 16, of 12 19 against 16; eight of 8 26 against 40, of 12 35 against 40; 64 of 8 168
+  // against 222, of 12 231 against 225).  The rule is the whole call's: a long sequence among many short ones
+  // takes 0.55 us a token, and short ones beside a long one a block each.
   if (T <= 16 || T <= 8LL * B) return gdn::launch_tokens(P, dk, s);
   return dk == 64 ? gdn::run_chunks<64>(CP, s) : gdn::run_chunks<128>(CP, s);
 }

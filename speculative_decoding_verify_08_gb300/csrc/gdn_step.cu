@@ -171,8 +171,8 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 // The same rule on the same lanes.  What differs: a block walks over tiles (sequence, head, 32 or
 // 64 rows), one warp asking for the next ones' states, keys, queries and values by bulk copies, one
 // writing the states back; as many bytes are on their way as the ring holds, whatever the
-// tiles' own latency (48 heads of 128 x 128: one token of 61 sequences 80 us with a block a tile, 60 this
-// way, 6.4 TB/s; 24 sequences of 4 rows behind 2 replayed on average 36.5, the rows' instructions).
+// tiles' own latency (48 heads of 128 x 128: one token of 61 sequences 79 us with a block a tile, 60 this
+// way, 6.5 TB/s; 24 sequences of 4 rows behind 2 replayed on average 53 and 36, the rows' instructions).
 template <int DK, int RP>
 __global__ void __launch_bounds__(STREAM_THREADS, 2) stream_kernel(const __grid_constant__ PoolParams P, int stages, int tiles, int row_tiles) {
   using Y = SL<DK, RP>;
@@ -407,8 +407,8 @@ sv_status run_tokens(PoolParams &P, cudaStream_t s) {
   // Few tokens of many states are streamed (values in whole 16 bytes); it pays from some
   // tiles a block on.
   // Two rows a thread share what it reads of keys and queries: at 64 columns always (tiles of 16 KB), at 128
-  // from two tokens on (32 KB; 24 sequences of 48 heads, 4 + 4 tokens 36.5 us against 48, 4 tokens 29 against
-  // 43, but one token of 61 sequences 64 against 60).
+  // from two tokens on (32 KB; 24 sequences of 48 heads, 4 + 4 tokens 35 us against 43, 4 tokens 29 against
+  // 37, two tokens of 61 sequences 43 against 63, but one token of them 64 against 60).
   constexpr int ONE = DK == 64 ? 2 : 1;
   const long long tiles = (long long)P.B * P.Hv * ((P.dv + SL<DK, ONE>::TILE - 1) / SL<DK, ONE>::TILE);
   if (!P.cu && P.tape_M + P.M <= TOKENS && P.dv % 8 == 0 && tiles >= 4LL * sms && tiles <= 0x7fffffffLL) {
