@@ -900,8 +900,6 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
     if (kept) arrive(s_read);
     // scale of a row: 2^-k with at most 1 behind it
     auto scale_of = [&](float most) { return pow2_field(253 - imin(imax(__float_as_int(most) >> 23, 1), 250)); };
-    // the smallest of what fp16 parts show; smaller elements are 0 in them
-    constexpr float LEAST = 0x1p-24f;
     // S (held scaled) as the next product's operand, a k-step at a time; the largest |S| of it
     auto put_state = [&]() {
       __half2 most = __float2half2_rn(0.f);
@@ -1024,14 +1022,15 @@ __device__ __forceinline__ void chain(const CUtensorMap &mapV, const CUtensorMap
       st = st + 1 == STAGES ? 0 : st + 1;
       phase ^= st == 0;
       const float isc = pow2_inverse(sc), iscr = pow2_inverse(scr);
-      // elements of k' are below 2^-3, 64 tokens: |S'| <= 8 |U~|; twice, as above (with LEAST neither step
-      // from an old scale to the new one passes 2^40, whatever a gate has cleared; behind the last block too,
+      // elements of k' are below 2^-3, 64 tokens: |S'| <= 8 |U~|; twice, as above (behind the last block too,
       // where what was added may be far larger than the state was)
-      const float u = fmaxf(fmaxf(__low2float(um), __high2float(um)), LEAST);
-      const float next = scale_of(both(gc * fmaxf(m, LEAST) * (isc * 0x1p-14f) + 8.f * u * (iscr * 0x1p-14f)));
+      const float next = scale_of(both(gc * m * (isc * 0x1p-14f) + 8.f * fmaxf(__low2float(um), __high2float(um)) * (iscr * 0x1p-14f)));
       if (c + 1 < n) load_values(st, phase);
-      const float step = next * isc, add = next * iscr;
-      const float keep = step <= 0x1p126f ? gc * step : gc * isc * next;  // (a large one: gc is small)
+      // Parts end at 2^-25.  Where a row shows anything of S, the step to the new scale is below 2^38, and where it
+      // does not, a larger step finds S below 2^-40 of its bound: it counts as 0.  Likewise an update that
+      // shows nothing is 0, whatever multiplies it.
+      const float step = next * isc, keep_all = step <= 0x1p126f ? gc * step : gc * isc * next;  // (a large one: gc is small)
+      const float keep = keep_all <= 0x1p40f ? keep_all : 0.f, add = fminf(next * iscr, 0x1p126f);
       sc = next;
       const f2 keep2 = pack2(keep, keep), add_2 = pack2(add, add);
 #pragma unroll

@@ -98,3 +98,23 @@ def test_keys_of_any_size(cuda_lib, dk):
     assert bool(torch.isfinite(r["k"].float()).all()) and bool(torch.isfinite(r["v"].float()).all())
     r["beta"] = torch.where(size[:, None] > 1e30, torch.zeros(()), (r["beta"].double() / size[:, None].double() ** 2).clamp(max=1e30).float())
     compare(cuda_lib, r, some_states(Hv, dv, dk, 81, 1.0), T)
+
+
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("size", [1e6, 1e20, 1e36])
+@pytest.mark.parametrize("at", [63, 127])
+def test_small_values_behind_a_large_state_that_a_gate_clears(cuda_lib, dk, size, at):
+    """At the end of a block of 64, so that no bound of a block holds both: what follows is seen at once."""
+    sv, T, Hk, Hv, dv = cuda_lib, 400, 1, 2, 40
+    r = some_rows(T, Hk, Hv, dk, dv, 82)
+    r["g"][at], r["beta"][at] = -1000.0, 0.0
+    pool = some_states(Hv, dv, dk, 83, size)
+    states, o = pool.cuda(), torch.empty(T, Hv, dv, device="cuda", dtype=torch.bfloat16)
+    sv.gdn_chunk(states, torch.zeros(1, dtype=torch.int32, device="cuda"), *plain.on(r), o,
+                 torch.tensor([0, T], dtype=torch.int32, device="cuda"),
+                 workspace=sv.workspace(sv.gdn_chunk_workspace_bytes(1, T, Hk, Hv, dk, dv)))
+    assert sv.sv_last_device_error() == sv.SV_OK
+    S, want = plain.run(pool[0], r, 0, T)
+    plain.close(o[:at], want[:at], OUT, BF16, "o before")
+    plain.close(o[at:], want[at:], OUT, BF16, "o behind")
+    plain.close(states[0], S, STATE, 0.0, "state")
