@@ -29,6 +29,8 @@ def spoiled(B, each, at, value):
     (2600, spoiled(200, 13, 100, 1 << 30)),
     (2600, spoiled(200, 13, 7, -7)),
     (2600, spoiled(200, 13, 200, 2601)),
+    (22500, spoiled(2500, 9, 1500, -1)),
+    (22500, spoiled(2500, 9, 1024, 1 << 30)),
 ], ids=lambda x: str(len(x) - 1) if isinstance(x, list) else None)
 def test_sequences_beside_bad_offsets(cuda_lib, T, cu):
     sv, B, Hk, Hv, dk, dv = cuda_lib, len(cu) - 1, 1, 2, 64, 64
@@ -74,3 +76,27 @@ def test_rows_that_too_many_sequences_name(cuda_lib):
         plain.close(states, want, STATE, 0.0, "states")
         if not kept:
             assert bool((o == 99.0).all())
+
+
+def test_rows_that_very_many_sequences_name(cuda_lib):
+    """The count of their blocks passes every limit; nothing is written, and the next call is right."""
+    sv, T, B, Hk, Hv, dk, dv = cuda_lib, 13000, 1500, 1, 1, 64, 16
+    r = plain.rows(T, Hk, Hv, dk, dv, 66)
+    pool = torch.randn(B, Hv, dv, dk, generator=torch.Generator().manual_seed(67)) * 0.3
+    slots = torch.arange(B, dtype=torch.int32, device="cuda")
+    states, o = pool.cuda(), torch.full((T, Hv, dv), 99.0, device="cuda", dtype=torch.bfloat16)
+    ws = sv.workspace(sv.gdn_chunk_workspace_bytes(B, T, Hk, Hv, dk, dv))
+    ws.fill_(255)
+    cu = torch.tensor([0, T] * (B // 2) + [0], dtype=torch.int32, device="cuda")
+    sv.gdn_chunk(states, slots, *plain.on(r), o, cu, workspace=ws)
+    assert sv.sv_last_device_error() == sv.SV_ERR_INVALID_ARG
+    assert torch.equal(states.cpu(), pool) and bool((o == 99.0).all())
+    cu = torch.tensor([0] * (B - 2) + [3000, T - 1, T], dtype=torch.int32, device="cuda")
+    sv.gdn_chunk(states, slots, *plain.on(r), o, cu, workspace=ws)
+    assert sv.sv_last_device_error() == sv.SV_OK
+    want, out = pool.double().clone(), []
+    for b, lo, hi in ((B - 3, 0, 3000), (B - 2, 3000, T - 1), (B - 1, T - 1, T)):
+        want[b], got = plain.run(pool[b], r, lo, hi)
+        out.append(got)
+    plain.close(states, want, STATE, 0.0, "states")
+    plain.close(o, torch.cat(out), OUT, BF16, "o")
